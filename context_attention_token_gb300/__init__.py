@@ -14,7 +14,7 @@ __all__ = ["cpt", "synth", "build"]
 
 
 def __getattr__(name):
-    if name.startswith("cpt_") or name.startswith("CPT_") or name in ("Plan", "Epoch", "CptError"):
+    if name.startswith("cpt_") or name.startswith("CPT_") or name in ("Plan", "Epoch", "Rotary", "CptError"):
         from . import cpt as _cpt
 
         return getattr(_cpt, name)

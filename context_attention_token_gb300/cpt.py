@@ -62,6 +62,12 @@ CPT_KERNEL_BULK = 2
 CPT_CALL_ROW_GATHER = 0
 CPT_CALL_GRAD_RETURN = 1
 CPT_CALL_SLOT_REDUCE = 2
+CPT_ROTARY_HALF = 0
+CPT_ROTARY_INTERLEAVED = 1
+CPT_ROTARY_MAX_AXES = 8
+CPT_ORDER_GLOBAL = 0
+CPT_ORDER_LOCAL = 1
+CPT_ATTENTION_MAX_HEADS = 1024
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
@@ -115,6 +121,15 @@ _sig("cpt_test_stall_bulk_waits", ctypes.c_int, _i32)
 _sig("cpt_kernel_path_of", ctypes.c_int, _i32, _i32, _i32, _i32, _i32, _i64, _i64, ctypes.POINTER(_i32))
 _sig("cpt_slot_reduce", ctypes.c_int, _vp, _i32, _i64, ctypes.c_int, ctypes.c_int, _vp, _vp, _vp)
 _sig("cpt_stream_ceiling", ctypes.c_int, _vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp)
+_sig("cpt_rotary_create", ctypes.c_int, _i32, _i32, _vp, _vp, _i32, ctypes.c_int, ctypes.POINTER(_vp))
+_sig("cpt_rotary_destroy", ctypes.c_int, _vp)
+_sig("cpt_rotary_apply", ctypes.c_int, _vp, _vp, _i32, _vp, _vp, _vp, ctypes.c_int, _vp, ctypes.c_int,
+     ctypes.c_int, _i32, _vp)
+_sig("cpt_attention", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i32, ctypes.c_int,
+     ctypes.c_float, _i64, _i32, _vp)
+_sig("cpt_attention_backward_workspace_bytes", _sz, _vp, _i32, _i32, _i32)
+_sig("cpt_attention_backward", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
+     _i32, ctypes.c_int, ctypes.c_float, _i64, _i32, _vp, _sz, _vp)
 _sig("cpt_bounds_checked", _i32)
 _sig("cpt_bounds_violations", ctypes.c_int, ctypes.POINTER(ctypes.c_uint32), _i32)
 
@@ -568,6 +583,126 @@ def cpt_slot_reduce(slots, dst: torch.Tensor, status: torch.Tensor | int | None 
         _need(status, 4, "status", torch.int32)
     _check(_lib.cpt_slot_reduce(sl.array(), n, numel, sl.code(), _dtype_code(dst), _ptr(dst),
                                 _ptr(status), _stream(stream)))
+
+
+# ------------------------------------------------------------------ attention layer
+
+class Rotary:
+    """Host handle of a rotation's frequencies and axes."""
+
+    def __init__(self, handle: int, head_dim: int, n_axes: int):
+        self.handle = handle
+        self.head_dim = head_dim
+        self.n_axes = n_axes
+
+    def __del__(self):
+        h, self.handle = getattr(self, "handle", None), None
+        if h:
+            _lib.cpt_rotary_destroy(h)
+
+
+def cpt_rotary_create(head_dim: int, inv_freq, axis_of_pair, n_axes: int,
+                      pairing: int = CPT_ROTARY_HALF) -> Rotary:
+    """Pair i of a head turns by pos[axis_of_pair[i]] * inv_freq[i]."""
+    freq = [float(f) for f in inv_freq]
+    axis = [int(a) for a in axis_of_pair]
+    if len(freq) != len(axis):
+        raise ValueError("inv_freq and axis_of_pair differ in length")
+    n = len(freq)
+    h = _vp()
+    _check(_lib.cpt_rotary_create(head_dim, n, (ctypes.c_double * n)(*freq), (_i32 * n)(*axis), n_axes,
+                                  pairing, ctypes.byref(h)))
+    return Rotary(h.value, head_dim, n_axes)
+
+
+def cpt_rotary_destroy(rotary: Rotary) -> None:
+    h, rotary.handle = rotary.handle, None
+    if h:
+        _check(_lib.cpt_rotary_destroy(h))
+
+
+def cpt_rotary_apply(rotary: Rotary, plan: Plan, srcs, dsts, positions: torch.Tensor,
+                     src_order: int = CPT_ORDER_GLOBAL, dst_order: int = CPT_ORDER_LOCAL,
+                     inverse: bool = False, stream=None):
+    """dsts[t] = srcs[t] rotated by its tokens' positions ([n_axes, T] int32),
+    moved from src_order to dst_order. Tensors are [T, heads, head_dim] in
+    global and [P, T_pad/P, heads, head_dim] in local order."""
+    srcs, dsts = list(srcs), list(dsts)
+    if len(srcs) != len(dsts):
+        raise ValueError("srcs and dsts differ in length")
+    if not srcs:
+        raise ValueError("no tensors")
+    rows = {CPT_ORDER_GLOBAL: plan.total_tokens, CPT_ORDER_LOCAL: plan.padded_tokens}
+    if src_order not in rows or dst_order not in rows:
+        raise ValueError("unknown order")
+    heads = []
+    for i, (a, b) in enumerate(zip(srcs, dsts)):
+        if a.dtype != srcs[0].dtype or b.dtype != srcs[0].dtype:
+            raise ValueError("srcs and dsts must share one dtype")
+        for t, what in ((a, "srcs"), (b, "dsts")):
+            if t.dim() < 2 or t.shape[-1] != rotary.head_dim:
+                raise ValueError(f"{what}[{i}] has no heads of {rotary.head_dim} elements")
+        if a.shape[-2] != b.shape[-2]:
+            raise ValueError(f"srcs[{i}] and dsts[{i}] differ in heads")
+        heads.append(int(a.shape[-2]))
+        row = heads[-1] * rotary.head_dim * a.element_size()
+        _need(a, rows[src_order] * row, f"srcs[{i}]")
+        _need(b, rows[dst_order] * row, f"dsts[{i}]")
+    _need(positions, 4 * rotary.n_axes * plan.total_tokens, "positions", torch.int32)
+    _check(_lib.cpt_rotary_apply(rotary.handle, plan.handle, len(srcs), _ptr_array(srcs), _ptr_array(dsts),
+                                 (_i32 * len(heads))(*heads), _dtype_code(srcs[0]), _ptr(positions),
+                                 src_order, dst_order, 1 if inverse else 0, _stream(stream)))
+
+
+def _attention_shape(plan: Plan, q, k, same_as_q, same_as_k, lse):
+    """(q_heads, kv_heads, head_dim, dtype code), every buffer large enough."""
+    if q.dim() < 2 or k.dim() < 2 or q.shape[-1] != k.shape[-1]:
+        raise ValueError("q and k must end in [heads, head_dim] with one head_dim")
+    hq, hk, d = int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1])
+    for group, like, rows, heads in ((same_as_q, q, plan.padded_tokens, hq), (same_as_k, k, plan.total_tokens, hk)):
+        for t, what in group:
+            if t.dtype != q.dtype or t.dim() < 2 or t.shape[-2:] != like.shape[-2:]:
+                raise ValueError(f"{what} differs in dtype, heads or head_dim")
+            _need(t, rows * heads * d * t.element_size(), what)
+    _need(lse, 4 * hq * plan.padded_tokens, "lse", torch.float32)
+    return hq, hk, d, _dtype_code(q)
+
+
+def cpt_attention(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
+                  lse: torch.Tensor, scale: float, window: int, sinks: int = 0, stream=None):
+    """out ([P, T_pad/P, Hq, D], like q) and lse ([Hq, T_pad]) = causal attention
+    of rank-local queries over the packed documents' keys and values ([T, Hkv,
+    D], global order) with a sliding window and `sinks` first tokens."""
+    hq, hk, d, code = _attention_shape(plan, q, k, ((q, "q"), (out, "out")), ((k, "k"), (v, "v")), lse)
+    _check(_lib.cpt_attention(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), hq, hk, d, code,
+                              scale, window, sinks, _stream(stream)))
+
+
+def cpt_attention_backward_workspace_bytes(plan: Plan, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib.cpt_attention_backward_workspace_bytes(plan.handle, q_heads, kv_heads, head_dim))
+
+
+def cpt_attention_backward(plan: Plan, q, k, v, out, lse, dout, dq, dk_writers, dv_writers, scale: float,
+                           window: int, sinks: int = 0, workspace: torch.Tensor | None = None, stream=None):
+    """dq (like q) and every writer's dk and dv ([P, T_pad, Hkv, D] or lists of P
+    tensors) of cpt_attention. Without a workspace the binding allocates one
+    from torch on the current stream."""
+    hq, hk, d, code = _attention_shape(plan, q, k, ((q, "q"), (out, "out"), (dout, "dout"), (dq, "dq")),
+                                       ((k, "k"), (v, "v")), lse)
+    P = plan.cp_size
+    dkw, dvw = _Parts(dk_writers, P), _Parts(dv_writers, P)
+    for parts, what in ((dkw, "dk_writers"), (dvw, "dv_writers")):
+        if parts.dtype != q.dtype:
+            raise ValueError(f"{what} must have the dtype of q")
+        _need_parts(parts, plan.padded_tokens, hk * d, what)
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("give a workspace with a stream: torch allocates on its current stream only")
+        need = cpt_attention_backward_workspace_bytes(plan, hq, hk, d)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    _check(_lib.cpt_attention_backward(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
+                                       _ptr(dq), dkw.array(), dvw.array(), hq, hk, d, code, scale, window, sinks,
+                                       _ptr(workspace), _nbytes(workspace), _stream(stream)))
 
 
 # ------------------------------------------------------------------ epochs

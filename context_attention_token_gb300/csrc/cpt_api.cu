@@ -16,6 +16,7 @@
 #include <cuda.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -250,6 +251,13 @@ struct cpt_plan {
     int32_t *cu, *cup, *cu_local, *num_segs, *first, *offs, *l2g, *g2l, *l2r, *r2l;
     std::vector<int32_t> h_cu;   // host copy of cu_seqlens (the source of its device copy)
     std::vector<int32_t> h_cup;  // host copy of the padded boundaries
+};
+
+struct cpt_rotary {
+    int32_t head_dim, pairs, axes;
+    bool interleaved;
+    uint64_t turn[kRotaryMaxPairs];   // inverse frequency / 2 pi, in 2^-64 of a turn
+    uint8_t axis[kRotaryMaxPairs];
 };
 
 struct cpt_epoch {
@@ -1105,12 +1113,15 @@ cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset)
         return fail(CPT_ERR_UNSUPPORTED, "this library was built without CPT_CHECK_BOUNDS");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int a = 0, b = 0, c = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
     cudaError_t e = read_index_map_bounds_violations(&a, reset != 0);
     if (e == cudaSuccess) e = read_gather_bounds_violations(&b, reset != 0);
     if (e == cudaSuccess) e = read_grad_return_bounds_violations(&c, reset != 0);
+    if (e == cudaSuccess) e = read_rotary_bounds_violations(&d, reset != 0);
+    if (e == cudaSuccess) e = read_attention_bounds_violations(&f, reset != 0);
+    if (e == cudaSuccess) e = read_attention_backward_bounds_violations(&g, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "bounds counter read");
-    *count = a + b + c;
+    *count = a + b + c + d + f + g;
     return CPT_OK;
 }
 
@@ -1146,6 +1157,309 @@ cpt_status cpt_stream_ceiling(const void *const *srcs, int32_t n_src, void *dst,
     cudaError_t e = launch_stream_ceiling(s8, n_src, static_cast<uint8_t *>(dst), bytes, block_bytes,
                                           stages, ctas_per_sm, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CPT_OK : cuda_fail(e, "stream ceiling launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- rotary
+//
+// The attention layer around the reorder and the gradient return: rotary
+// positions, windowed attention, its gradient.
+
+namespace {
+
+// f / 2 pi modulo one turn, as a 64-bit fixed-point fraction. The quotient is
+// carried in two doubles, so the fraction is right to its last bits and a
+// position of 2^31 still has its angle to 2^-30 of a turn.
+uint64_t turn_of(double f)
+{
+    const double two_pi_hi = 6.283185307179586477, two_pi_lo = 2.449293598294706414e-16;
+    const double t0 = f / two_pi_hi;
+    const double rest = std::fma(-t0, two_pi_hi, f) - t0 * two_pi_lo;
+    const double t1 = rest / two_pi_hi;
+    const double frac = t0 - std::floor(t0);                   // exact
+    const double hi = std::floor(std::ldexp(frac, 32));        // top 32 bits, exact
+    const double lo = std::ldexp(frac, 64) - std::ldexp(hi, 32) + std::ldexp(t1, 64);
+    return (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(static_cast<int64_t>(std::nearbyint(lo)));
+}
+
+bool order_ok(cpt_order o) { return o == CPT_ORDER_GLOBAL || o == CPT_ORDER_LOCAL; }
+
+}  // namespace
+
+extern "C" {
+
+cpt_status cpt_rotary_create(int32_t head_dim, int32_t n_pairs, const double *inv_freq,
+                             const int32_t *axis_of_pair, int32_t n_axes, cpt_rotary_pairing pairing,
+                             cpt_rotary **out)
+{
+    if (out == nullptr) return fail(CPT_ERR_INVALID_ARG, "out is NULL");
+    *out = nullptr;
+    if (inv_freq == nullptr || axis_of_pair == nullptr)
+        return fail(CPT_ERR_INVALID_ARG, "inv_freq or axis_of_pair is NULL");
+    if (head_dim < 2 || head_dim > 2 * kRotaryMaxPairs || head_dim % 2 != 0)
+        return fail(CPT_ERR_UNSUPPORTED, "head_dim %d is not an even number in 2..%d", head_dim,
+                    2 * kRotaryMaxPairs);
+    if (n_pairs < 1 || n_pairs > head_dim / 2)
+        return fail(CPT_ERR_INVALID_ARG, "n_pairs %d outside 1..head_dim / 2 = %d", n_pairs, head_dim / 2);
+    if (n_axes < 1 || n_axes > CPT_ROTARY_MAX_AXES)
+        return fail(CPT_ERR_INVALID_ARG, "n_axes %d outside 1..%d", n_axes, CPT_ROTARY_MAX_AXES);
+    if (pairing != CPT_ROTARY_HALF && pairing != CPT_ROTARY_INTERLEAVED)
+        return fail(CPT_ERR_INVALID_ARG, "unknown pairing %d", (int)pairing);
+    for (int i = 0; i < n_pairs; ++i) {
+        if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1048576.0)
+            return fail(CPT_ERR_INVALID_ARG, "inv_freq[%d] is not a finite number of at most 2^20", i);
+        if (axis_of_pair[i] < 0 || axis_of_pair[i] >= n_axes)
+            return fail(CPT_ERR_INVALID_ARG, "axis_of_pair[%d] = %d outside 0..%d", i, axis_of_pair[i],
+                        n_axes - 1);
+    }
+    cpt_rotary *r = new (std::nothrow) cpt_rotary;
+    if (r == nullptr) return fail(CPT_ERR_INVALID_ARG, "out of host memory");
+    r->head_dim = head_dim;
+    r->pairs = n_pairs;
+    r->axes = n_axes;
+    r->interleaved = pairing == CPT_ROTARY_INTERLEAVED;
+    for (int i = 0; i < n_pairs; ++i) {
+        r->turn[i] = turn_of(inv_freq[i]);
+        r->axis[i] = static_cast<uint8_t>(axis_of_pair[i]);
+    }
+    *out = r;
+    return CPT_OK;
+}
+
+cpt_status cpt_rotary_destroy(cpt_rotary *rotary)
+{
+    delete rotary;
+    return CPT_OK;
+}
+
+cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *plan, int32_t n_tensors,
+                            const void *const *src, void *const *dst, const int32_t *heads,
+                            cpt_dtype dtype, const int32_t *positions, cpt_order src_order,
+                            cpt_order dst_order, int32_t inverse, void *stream)
+{
+    Trace trace("cpt_rotary_apply");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    if (rotary == nullptr) return fail(CPT_ERR_INVALID_ARG, "rotary is NULL");
+    if (n_tensors < 1 || n_tensors > kMaxTensors)
+        return fail(CPT_ERR_INVALID_ARG, "n_tensors %d outside 1..3", n_tensors);
+    if (src == nullptr || dst == nullptr || heads == nullptr)
+        return fail(CPT_ERR_INVALID_ARG, "src, dst or heads is NULL");
+    if (!dtype_ok(dtype)) return fail(CPT_ERR_INVALID_ARG, "unknown dtype");
+    if (!order_ok(src_order) || !order_ok(dst_order)) return fail(CPT_ERR_INVALID_ARG, "unknown order");
+    const bool from_local = src_order == CPT_ORDER_LOCAL, to_local = dst_order == CPT_ORDER_LOCAL;
+    RotaryParams p;
+    memset(&p, 0, sizeof p);
+    p.rows = to_local ? plan->Tpad : plan->T;
+    p.src_rows = from_local ? plan->Tpad : plan->T;
+    int64_t heads_total = 0;
+    for (int t = 0; t < n_tensors; ++t) {
+        if (heads[t] < 1) return fail(CPT_ERR_INVALID_ARG, "heads[%d] = %d < 1", t, heads[t]);
+        int64_t units = 0;
+        if ((st = check_row((int64_t)heads[t] * rotary->head_dim, dtype, dtype, &units))) return st;
+        p.row_bytes[t] = units * 16;
+        p.heads[t] = heads[t];
+        heads_total += heads[t];
+    }
+    // a CTA counts the heads of its tokens in 32 bits
+    if (heads_total > 0x7FFFFFFF / kRotaryMaxTile)
+        return fail(CPT_ERR_INVALID_ARG, "%lld heads are too many", (long long)heads_total);
+    p.heads_total = (int32_t)heads_total;
+    if (plan->T == 0) return CPT_OK;
+    std::vector<Range> r;
+    add_range(r, plan->ws, plan->ws_bytes, false, "workspace");
+    if ((st = check_ptr(positions, dev, 4, "positions"))) return st;
+    add_range(r, positions, sizeof(int32_t) * (size_t)rotary->axes * (size_t)plan->T, false, "positions");
+    for (int t = 0; t < n_tensors; ++t) {
+        if ((st = check_ptr(src[t], dev, 16, "src", t))) return st;
+        if ((st = check_ptr(dst[t], dev, 16, "dst", t))) return st;
+        add_range(r, src[t], (size_t)(p.src_rows * p.row_bytes[t]), false, "src", t);
+        add_range(r, dst[t], (size_t)(p.rows * p.row_bytes[t]), true, "dst", t);
+        p.src[t] = static_cast<const uint8_t *>(src[t]);
+        p.dst[t] = static_cast<uint8_t *>(dst[t]);
+    }
+    if ((st = check_overlaps(r))) return st;
+    // packed-contiguous local order is the global order: no map is read
+    if (plan->layout != CPT_LAYOUT_PACKED_CONTIGUOUS) {
+        const bool pad = is_padded(plan->layout);
+        const int32_t *l2r = pad ? plan->l2r : plan->l2g;
+        if (to_local) p.token_map = l2r;
+        if (to_local && !from_local) p.row_map = l2r;
+        if (to_local && from_local && pad) p.pad_map = l2r;
+        if (!to_local && from_local) p.row_map = pad ? plan->r2l : plan->g2l;
+    }
+    p.positions = positions;
+    p.T = plan->T;
+    p.head_bytes = (int32_t)(rotary->head_dim * (int64_t)dtype_size(dtype));
+    p.pairs = rotary->pairs;
+    p.inverse = inverse != 0;
+    memcpy(p.turn, rotary->turn, sizeof p.turn);
+    memcpy(p.axis, rotary->axis, sizeof p.axis);
+    cudaError_t e = launch_rotary(p, dtype, rotary->interleaved, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "rotary launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- attention
+
+namespace {
+
+// The checks that do not look at a device: shapes, types, the mask.
+cpt_status check_attention(int32_t q_heads, int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
+                           int64_t window, int32_t sinks)
+{
+    if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
+        return fail(CPT_ERR_INVALID_ARG, "q_heads %d is not a positive multiple of kv_heads %d", q_heads,
+                    kv_heads);
+    if (q_heads > CPT_ATTENTION_MAX_HEADS)
+        return fail(CPT_ERR_UNSUPPORTED, "q_heads %d is over %d", q_heads, CPT_ATTENTION_MAX_HEADS);
+    if (!dtype_ok(dtype)) return fail(CPT_ERR_INVALID_ARG, "unknown dtype");
+    if (dtype != CPT_BF16) return fail(CPT_ERR_UNSUPPORTED, "attention takes bf16 tensors only");
+    if (head_dim < 8 || head_dim > kAttnMaxHeadDim || head_dim % 8 != 0)
+        return fail(CPT_ERR_UNSUPPORTED, "head_dim %d is not a multiple of 8 in 8..%d", head_dim,
+                    kAttnMaxHeadDim);
+    if (!std::isfinite(scale) || !(scale > 0.0f))
+        return fail(CPT_ERR_INVALID_ARG, "scale is not a finite positive number");
+    if (window < 0) return fail(CPT_ERR_INVALID_ARG, "window %lld < 0", (long long)window);
+    if (sinks < 0) return fail(CPT_ERR_INVALID_ARG, "sinks %d < 0", sinks);
+    return CPT_OK;
+}
+
+void fill_attention(AttentionParams &p, const cpt_plan *plan, const void *q, const void *k, const void *v,
+                    void *out, float *lse, int32_t q_heads, int32_t kv_heads, int32_t head_dim, float scale,
+                    int64_t window, int32_t sinks)
+{
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.out = out;
+    p.lse = lse;
+    p.l2r = is_padded(plan->layout) ? plan->l2r : plan->l2g;
+    p.cu = plan->cu;
+    p.T = plan->T;
+    p.Tpad = plan->Tpad;
+    p.Tp = plan->Tp;
+    p.P = plan->P;
+    p.n_docs = plan->n;
+    p.Hq = q_heads;
+    p.Hkv = kv_heads;
+    p.D = head_dim;
+    // no document is longer than 2^31 - 1 tokens
+    p.window = static_cast<int32_t>(window > 0x7FFFFFFF ? 0x7FFFFFFF : window);
+    p.sinks = sinks;
+    p.scale = scale;
+}
+
+size_t backward_workspace(const cpt_plan *plan, int32_t q_heads)
+{
+    return align256(sizeof(float) * (size_t)q_heads * (size_t)plan->Tpad);
+}
+
+}  // namespace
+
+extern "C" {
+
+cpt_status cpt_attention(const cpt_plan *plan, const void *q, const void *k, const void *v, void *out,
+                         float *lse, int32_t q_heads, int32_t kv_heads, int32_t head_dim, cpt_dtype dtype,
+                         float scale, int64_t window, int32_t sinks, void *stream)
+{
+    Trace trace("cpt_attention");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    if ((st = check_attention(q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
+    if (plan->Tpad == 0) return CPT_OK;
+    const size_t qb = (size_t)plan->Tpad * q_heads * head_dim * 2, kb = (size_t)plan->T * kv_heads * head_dim * 2;
+    std::vector<Range> r;
+    add_range(r, plan->ws, plan->ws_bytes, false, "workspace");
+    if ((st = check_ptr(q, dev, 16, "q"))) return st;
+    if ((st = check_ptr(k, dev, 16, "k"))) return st;
+    if ((st = check_ptr(v, dev, 16, "v"))) return st;
+    if ((st = check_ptr(out, dev, 16, "out"))) return st;
+    if ((st = check_ptr(lse, dev, 16, "lse"))) return st;
+    add_range(r, q, qb, false, "q");
+    add_range(r, k, kb, false, "k");
+    add_range(r, v, kb, false, "v");
+    add_range(r, out, qb, true, "out");
+    add_range(r, lse, sizeof(float) * (size_t)q_heads * (size_t)plan->Tpad, true, "lse");
+    if ((st = check_overlaps(r))) return st;
+    AttentionParams p;
+    memset(&p, 0, sizeof p);
+    fill_attention(p, plan, q, k, v, out, lse, q_heads, kv_heads, head_dim, scale, window, sinks);
+    cudaError_t e = launch_attention(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "attention launch");
+}
+
+size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int32_t q_heads, int32_t kv_heads,
+                                              int32_t head_dim)
+{
+    if (plan == nullptr) {
+        fail(CPT_ERR_INVALID_ARG, "plan is NULL");
+        return 0;
+    }
+    if (check_attention(q_heads, kv_heads, head_dim, CPT_BF16, 1.0f, 0, 0) != CPT_OK) return 0;
+    return backward_workspace(plan, q_heads);
+}
+
+cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,
+                                  const void *out, const float *lse, const void *dout, void *dq,
+                                  void *const *dk_writers, void *const *dv_writers, int32_t q_heads,
+                                  int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
+                                  int64_t window, int32_t sinks, void *workspace, size_t workspace_bytes,
+                                  void *stream)
+{
+    Trace trace("cpt_attention_backward");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    if ((st = check_attention(q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
+    if (dk_writers == nullptr || dv_writers == nullptr)
+        return fail(CPT_ERR_INVALID_ARG, "dk_writers or dv_writers is NULL");
+    if (plan->Tpad == 0) return CPT_OK;
+    const size_t need = backward_workspace(plan, q_heads);
+    if (workspace == nullptr) return fail(CPT_ERR_WORKSPACE, "workspace is NULL");
+    if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+        return fail(CPT_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+    if (workspace_bytes < need)
+        return fail(CPT_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    if ((st = check_ptr(workspace, dev, 256, "workspace"))) return st;
+    const size_t qb = (size_t)plan->Tpad * q_heads * head_dim * 2, kb = (size_t)plan->T * kv_heads * head_dim * 2;
+    const size_t wb = (size_t)plan->Tpad * kv_heads * head_dim * 2;
+    const size_t lb = sizeof(float) * (size_t)q_heads * (size_t)plan->Tpad;
+    struct { const void *p; size_t bytes; bool output; const char *what; } bufs[] = {
+        {q, qb, false, "q"},     {k, kb, false, "k"},       {v, kb, false, "v"},  {out, qb, false, "out"},
+        {lse, lb, false, "lse"}, {dout, qb, false, "dout"}, {dq, qb, true, "dq"},
+    };
+    std::vector<Range> r;
+    add_range(r, plan->ws, plan->ws_bytes, false, "plan workspace");
+    add_range(r, workspace, need, true, "workspace");
+    for (const auto &b : bufs) {
+        if ((st = check_ptr(b.p, dev, 16, b.what))) return st;
+        add_range(r, b.p, b.bytes, b.output, b.what);
+    }
+    AttentionBackwardParams p;
+    memset(&p, 0, sizeof p);
+    for (int w = 0; w < plan->P; ++w) {
+        if ((st = check_ptr(dk_writers[w], dev, 16, "dk_writers", w))) return st;
+        if ((st = check_ptr(dv_writers[w], dev, 16, "dv_writers", w))) return st;
+        add_range(r, dk_writers[w], wb, true, "dk_writers", w);
+        add_range(r, dv_writers[w], wb, true, "dv_writers", w);
+        p.dk[w] = dk_writers[w];
+        p.dv[w] = dv_writers[w];
+    }
+    if ((st = check_overlaps(r))) return st;
+    fill_attention(p.a, plan, q, k, v, const_cast<void *>(out), const_cast<float *>(lse), q_heads, kv_heads,
+                   head_dim, scale, window, sinks);
+    p.dout = dout;
+    p.dq = dq;
+    p.g2l = plan->g2l;
+    p.cup = plan->cup;
+    p.delta = static_cast<float *>(workspace);
+    cudaError_t e = launch_attention_backward(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "attention backward launch");
 }
 
 }  // extern "C"

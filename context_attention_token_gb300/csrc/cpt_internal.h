@@ -111,6 +111,60 @@ struct SlotReduceParams {
 cudaError_t launch_slot_reduce(const SlotReduceParams &p, int n_slots, int in_dtype,
                                int out_dtype, cudaStream_t stream);
 
+// Rotary positions applied while rows move: dst[t][d] = turn(src[t][s(d)]).
+constexpr int kRotaryMaxPairs = 128;
+constexpr int kRotaryMaxTile = 64;   // tokens of one CTA
+struct RotaryParams {
+    const uint8_t *src[kMaxTensors];
+    uint8_t *dst[kMaxTensors];
+    const int32_t *row_map;      // source row of every destination row (nullptr: the same row)
+    const int32_t *token_map;    // raw token of every destination row (nullptr: the row itself)
+    const int32_t *pad_map;      // negative: a destination row of padding, written as zeros (nullptr: none)
+    const int32_t *positions;    // [axes][T]
+    int64_t rows;                // destination rows
+    int64_t src_rows;            // source rows (bounds checks)
+    int64_t T;                   // raw tokens
+    int64_t row_bytes[kMaxTensors];
+    int32_t heads[kMaxTensors];
+    int32_t heads_total;
+    int32_t head_bytes;
+    int32_t pairs;
+    int32_t inverse;
+    int32_t rot_units, copy_units, tile;   // filled in by the launcher
+    uint64_t turn[kRotaryMaxPairs];        // turns per position, of 2^64
+    uint8_t axis[kRotaryMaxPairs];
+};
+cudaError_t launch_rotary(RotaryParams p, int dtype, bool interleaved, cudaStream_t stream);
+
+// Causal attention over packed documents with a sliding window and sinks:
+// queries in rank-local order, keys and values in raw global order.
+constexpr int kAttnMaxHeadDim = 128;
+struct AttentionParams {
+    const void *q, *k, *v;         // bf16 [Tpad][Hq][D], [T][Hkv][D] twice
+    void *out;                     // bf16 [Tpad][Hq][D]
+    float *lse;                    // [Hq][Tpad]
+    const int32_t *l2r;            // raw token of every local row (-1: padding)
+    const int32_t *cu;             // raw document boundaries [n_docs + 1]
+    int64_t T, Tpad, Tp;
+    int32_t P, n_docs;
+    int32_t Hq, Hkv, D;
+    int32_t window;                // rows see the last `window` tokens up to their own,
+    int32_t sinks;                 // and the first `sinks` of their document
+    float scale;
+};
+cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream);
+
+struct AttentionBackwardParams {
+    AttentionParams a;             // out and lse are inputs here
+    const void *dout;              // bf16 [Tpad][Hq][D]
+    void *dq;                      // bf16 [Tpad][Hq][D]
+    void *dk[kMaxCp], *dv[kMaxCp]; // writer r's bf16 [Tpad][Hkv][D]
+    const int32_t *g2l;            // local row of every (padded) global position
+    const int32_t *cup;            // padded document boundaries [n_docs + 1]
+    float *delta;                  // workspace [Hq][Tpad]
+};
+cudaError_t launch_attention_backward(const AttentionBackwardParams &p, cudaStream_t stream);
+
 // Streaming ceiling: dst = copy of srcs[0], srcs[1..n_src) read and
 // discarded, through the bulk-copy engine in blocks of block_bytes and a ring
 // of `stages` stages per CTA, at most ctas_per_sm CTAs per SM.
@@ -124,6 +178,9 @@ cudaError_t read_ceiling_wait_timeouts(unsigned int *count, bool reset);
 cudaError_t read_index_map_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_gather_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_grad_return_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_rotary_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_attention_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset);
 
 // Bounded epoch check: one warp polls flags_row[0..P) with acquire loads until
 // every (int32)(flag - epoch) >= 0, for at most timeout_ns, then writes 0 or

@@ -10,7 +10,9 @@
  *   - the fused owner-gradient return (P writers' global dK/dV summed into
  *     the owners' local gradients in binary32, writer order 0..P-1),
  *   - the staged alternative (scatter, epoch publish, bounded epoch wait,
- *     slot reduce), and the ordered one-shot sum of P slot buffers.
+ *     slot reduce), and the ordered one-shot sum of P slot buffers,
+ *   - the attention layer between the reorder and the return: rotary
+ *     positions, attention with a sliding window and sinks, its gradient.
  *
  * Sources, by page title:
  *   [TE-3221] "[PyTorch] Add experimental packed-contiguous THD all-gather
@@ -51,8 +53,9 @@
  *   Threads     Calls are thread-safe; the error string is per thread.
  *   Graphs      cpt_index_map, cpt_thd_metadata, cpt_thd_real_lengths,
  *               cpt_partition, cpt_restore, cpt_grad_return(_accumulate),
- *               cpt_grad_scatter and cpt_slot_reduce only enqueue kernels, so
- *               they can be recorded into a CUDA graph (build the plan
+ *               cpt_grad_scatter, cpt_slot_reduce, cpt_rotary_apply,
+ *               cpt_attention and cpt_attention_backward only enqueue kernels,
+ *               so they can be recorded into a CUDA graph (build the plan
  *               first). cpt_plan_create, cpt_grad_return_noalloc and the
  *               epoch publish/wait calls act on host state at call time and
  *               return CPT_ERR_UNSUPPORTED inside stream capture (as the
@@ -651,6 +654,134 @@ CPT_API cpt_status cpt_test_stall_bulk_waits(int32_t on);
 CPT_API cpt_status cpt_slot_reduce(const void *const *slots, int32_t n_slots, int64_t n_elems,
                            cpt_dtype in, cpt_dtype out, void *dst, const int32_t *status,
                            void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Rotary positions                                                    */
+/* ------------------------------------------------------------------ */
+
+/* The attention layer that the reorder and the gradient return belong to
+ * (the pages leave it to the caller): rotary positions, attention with a
+ * sliding window and sinks, and its gradient. A step runs
+ *   cpt_rotary_apply (Q to rank-local order, K in global order),
+ *   cpt_attention, cpt_attention_backward (dQ in rank-local order, each
+ *   rank's dK and dV in its writer slot), cpt_grad_return, and
+ *   cpt_rotary_apply with `inverse` on dQ and the owners' dK. */
+
+/* How the elements of a head form pairs: element i with i + n_pairs, or 2i
+ * with 2i + 1. */
+typedef enum cpt_rotary_pairing { CPT_ROTARY_HALF = 0, CPT_ROTARY_INTERLEAVED = 1 } cpt_rotary_pairing;
+
+/* Row order of a token tensor: GLOBAL is [T][row], the raw packed order;
+ * LOCAL is the plan's rank-major [P][T_pad/P][row]. */
+typedef enum cpt_order { CPT_ORDER_GLOBAL = 0, CPT_ORDER_LOCAL = 1 } cpt_order;
+
+typedef struct cpt_rotary cpt_rotary; /* opaque: pairs, frequencies and axes */
+
+/* Most position axes of one rotation. */
+#define CPT_ROTARY_MAX_AXES 8
+
+/* Frequencies and axes of a rotation with several position axes (time,
+ * height, width). Pair i turns by pos[axis_of_pair[i]] * inv_freq[i] radians.
+ *  head_dim      elements of a head: even, 2..256. Elements from 2 * n_pairs on
+ *                are copied.
+ *  n_pairs       1..head_dim/2.
+ *  inv_freq      host double[n_pairs], finite, |f| <= 2^20.
+ *  axis_of_pair  host int32[n_pairs], each in 0..n_axes-1 (sections of
+ *                neighbouring pairs or any other assignment).
+ *  n_axes        1..CPT_ROTARY_MAX_AXES.
+ *  out           receives a host-side handle, valid on every device; free it
+ *                with cpt_rotary_destroy.
+ *  Host only. Errors: CPT_ERR_INVALID_ARG; CPT_ERR_UNSUPPORTED (head_dim). */
+CPT_API cpt_status cpt_rotary_create(int32_t head_dim, int32_t n_pairs, const double *inv_freq,
+                                     const int32_t *axis_of_pair, int32_t n_axes,
+                                     cpt_rotary_pairing pairing, cpt_rotary **out);
+
+/* Free the handle (NULL is accepted). Work already enqueued is not affected. */
+CPT_API cpt_status cpt_rotary_destroy(cpt_rotary *rotary);
+
+/* Rotate up to three token tensors while moving them between row orders, in
+ * one launch: dst[t][d] = R(pos of d's token) src[t][row of d's token]. With
+ * GLOBAL to LOCAL this is cpt_partition with the rotation in it; LOCAL to
+ * GLOBAL is cpt_restore with it; with equal orders every row keeps its place.
+ *  src, dst   host arrays of n_tensors (1..3) device pointers: [rows][heads[t]]
+ *             [head_dim], rows T for GLOBAL and T_pad for LOCAL. A dst must not
+ *             overlap any other buffer of the call.
+ *  heads      host int32[n_tensors]; heads[t] * head_dim elements must be a
+ *             multiple of 16 bytes.
+ *  positions  device int32[n_axes][T], of the raw tokens in global order; any
+ *             values. Angles are exact to 2^-31 of a turn at any position.
+ *  inverse    non-zero: turn back. This is the gradient of the forward call
+ *             with the two orders exchanged.
+ *  Arithmetic is binary32, with one rounding to bf16 at the end. Padding rows of
+ *  a LOCAL dst are written as zeros; those of a LOCAL src are not read.
+ *  Errors: as cpt_partition. */
+CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *plan, int32_t n_tensors,
+                                    const void *const *src, void *const *dst, const int32_t *heads,
+                                    cpt_dtype dtype, const int32_t *positions, cpt_order src_order,
+                                    cpt_order dst_order, int32_t inverse, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Attention with a sliding window and sinks                           */
+/* ------------------------------------------------------------------ */
+
+/* Most query heads of one call. */
+#define CPT_ATTENTION_MAX_HEADS 1024
+
+/* Causal attention over the plan's packed documents, every rank's queries in
+ * one launch. The token at position u of its document sees position j of the
+ * same document when j <= u and (u - j < window or j < sinks):
+ *   out = softmax(scale q . K) V over the keys it sees, lse = the natural
+ *   logarithm of the sum of exp(scale q . k) over them.
+ * A token that sees nothing (window 0, no sinks) has out = 0 and lse = -inf, as
+ * has every padding row.
+ *  q, out     device bf16 [P][T_pad/P][q_heads][head_dim], rank-local order.
+ *  k, v       device bf16 [T][kv_heads][head_dim], raw global order (what
+ *             cpt_restore gives back from the all-gathered ranks).
+ *  lse        device float32 [q_heads][T_pad], local rows.
+ *  q_heads    a multiple of kv_heads, at most CPT_ATTENTION_MAX_HEADS; query
+ *             head h reads kv head h / (q_heads / kv_heads).
+ *  head_dim   a multiple of 8 in 8..128.
+ *  dtype      CPT_BF16.
+ *  scale      finite, positive.
+ *  window     >= 0; a window of the longest document or more is the whole
+ *             causal triangle.
+ *  sinks      >= 0, first tokens of every document that stay visible.
+ *  Scores, softmax statistics and sums are binary32. Infinities and NaN reach
+ *  the rows that see them and no others.
+ *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (dtype, head_dim, too many
+ *  heads), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
+ *  another buffer), CPT_ERR_CUDA. */
+CPT_API cpt_status cpt_attention(const cpt_plan *plan, const void *q, const void *k, const void *v, void *out,
+                                 float *lse, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                 cpt_dtype dtype, float scale, int64_t window, int32_t sinks, void *stream);
+
+/* Device workspace bytes of cpt_attention_backward, or 0 for a NULL plan or
+ * head counts and a head_dim that it refuses. Host only. */
+CPT_API size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int32_t q_heads, int32_t kv_heads,
+                                                      int32_t head_dim);
+
+/* Gradient of cpt_attention, every rank's in one call.
+ *  q, k, v, out, lse  the arguments and results of cpt_attention, with the same
+ *             heads, scale, window and sinks.
+ *  dout       device bf16, like out: the gradient with respect to it.
+ *  dq         device bf16, like q: overwritten; zeros in padding rows.
+ *  dk_writers, dv_writers  host arrays of P device pointers: writer r's bf16
+ *             [T_pad][kv_heads][head_dim] in (padded) global order, the input of
+ *             cpt_grad_return. Every element is written: the sum over rank r's
+ *             queries alone, zeros where none of them sees the key and in
+ *             padding.
+ *  workspace  device, 256-byte aligned, >= cpt_attention_backward_workspace_bytes;
+ *             needed until the stream has passed the call. Calls that may run
+ *             at the same time (two streams, two graphs) need one each.
+ *  Sums are binary32 in a fixed order: a repeated call gives the same bits.
+ *  Padding rows of q, out, lse and dout are not used. Other arguments and errors:
+ *  as cpt_attention, and CPT_ERR_WORKSPACE. */
+CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,
+                                          const void *out, const float *lse, const void *dout, void *dq,
+                                          void *const *dk_writers, void *const *dv_writers, int32_t q_heads,
+                                          int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
+                                          int64_t window, int32_t sinks, void *workspace,
+                                          size_t workspace_bytes, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Measurement                                                         */

@@ -1,0 +1,403 @@
+"""Windowed attention with sinks and its gradient on the GPU, against dense
+64-bit forms. The bounds of every error are derived in attention_ref."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import attention_ref as ref
+from gpu_helpers import Guarded
+
+pytestmark = pytest.mark.gpu
+
+
+class Batch:
+    """Inputs of one call in guarded buffers, and its outputs."""
+
+    def __init__(self, cpt, layout, P, lens, Hq, Hk, D, window, sinks, seed=0, scale=None):
+        self.cpt, self.P, self.window, self.sinks = cpt, P, window, sinks
+        self.l2r, self.l2g, self.cu, self.cup = ref.local_rows(layout, P, lens)
+        self.T, self.Tpad = int(self.cu[-1]), len(self.l2r)
+        self.Hq, self.Hk, self.D = Hq, Hk, D
+        self.scale = scale or D ** -0.5
+        self.plan = cpt.cpt_plan_create(layout, P, self.cu.tolist(), self.T)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        rnd = lambda *s: torch.randn(s, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+        self.q, self.dout = rnd(self.Tpad, Hq, D), rnd(self.Tpad, Hq, D)
+        self.k, self.v = rnd(self.T, Hk, D), rnd(self.T, Hk, D)
+        self.out = Guarded((self.Tpad, Hq, D), torch.bfloat16)
+        self.lse = Guarded((Hq, self.Tpad), torch.float32)
+        self.dq = Guarded((self.Tpad, Hq, D), torch.bfloat16)
+        self.dk = [Guarded((self.Tpad, Hk, D), torch.bfloat16) for _ in range(P)]
+        self.dv = [Guarded((self.Tpad, Hk, D), torch.bfloat16) for _ in range(P)]
+        self.see = ref.visible(self.l2r, self.cu, self.T, window, sinks, "cuda")
+        self.pad = torch.from_numpy(self.l2r < 0).cuda()
+
+    def forward(self, stream=None):
+        self.cpt.cpt_attention(self.plan, self.q, self.k, self.v, self.out.t, self.lse.t, self.scale, self.window,
+                               self.sinks, stream=stream)
+
+    def backward(self, workspace=None, stream=None):
+        self.cpt.cpt_attention_backward(self.plan, self.q, self.k, self.v, self.out.t, self.lse.t, self.dout,
+                                        self.dq.t, [x.t for x in self.dk], [x.t for x in self.dv], self.scale,
+                                        self.window, self.sinks, workspace=workspace, stream=stream)
+
+    def workspace(self, extra=0):
+        need = self.cpt.cpt_attention_backward_workspace_bytes(self.plan, self.Hq, self.Hk, self.D)
+        return Guarded((need,), torch.uint8)
+
+    def check_forward(self, q=None):
+        assert self.out.bands_intact() and self.lse.bands_intact()
+        out, lse, tol = ref.attention64(self.q if q is None else q, self.k, self.v, self.see, self.scale)
+        got = self.out.t.double()
+        assert torch.isfinite(got).all()
+        assert ((got - out).abs() <= tol).all(), float(((got - out).abs() - tol).max())
+        empty = lse == -math.inf
+        assert torch.equal(self.lse.t == -math.inf, empty)
+        diff = torch.where(empty, 0.0, (self.lse.t.double() - lse).abs())
+        assert (diff <= ref.E32 + 2.0 ** -22 * lse.abs()).logical_or(empty).all(), float(diff.max())
+        assert (got[empty.all(0)] == 0).all()
+
+    def check_backward(self, q=None, dout=None, out=None):
+        for x in [self.dq] + self.dk + self.dv:
+            assert x.bands_intact()
+        dq, tol, writers = ref.backward64(self.q if q is None else q, self.k, self.v,
+                                          self.out.t if out is None else out,
+                                          self.dout if dout is None else dout, self.see, self.scale, self.P)
+        got = self.dq.t.double()
+        assert torch.isfinite(got).all()
+        assert ((got - dq).abs() <= tol).all(), float(((got - dq).abs() - tol).max())
+        for r, pair in enumerate(writers):
+            for name, buf, (want, tol) in zip(("dk", "dv"), (self.dk[r], self.dv[r]), pair):
+                want, tol = (ref.to_padded(x, self.cu, self.cup, self.Tpad) for x in (want, tol))
+                diff = (buf.t.double() - want).abs()
+                assert torch.isfinite(diff).all(), (name, r)
+                assert (diff <= tol).all(), (name, r, float((diff - tol).max()))
+
+
+def both(cpt, *a, **kw):
+    b = Batch(cpt, *a, **kw)
+    b.forward()
+    ws = b.workspace()
+    b.backward(ws.t)
+    torch.cuda.synchronize()
+    assert ws.bands_intact()
+    b.check_forward()
+    b.check_backward()
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+    return b
+
+
+ODD = [1, 127, 128, 129, 0, 5, 300, 2, 0, 77]
+EVEN = {P: [2 * P * m for m in (1, 17, 0, 40, 3)] for P in (1, 2, 3, 4, 8)}
+
+
+@pytest.mark.parametrize("layout,P,lens", [
+    (0, 4, [512]), (0, 2, EVEN[2]), (0, 8, EVEN[8]), (0, 1, [640]), (0, 3, EVEN[3]),
+    (1, 1, ODD), (1, 4, ODD + [3]), (1, 3, [768]),
+    (3, 1, ODD), (3, 4, ODD), (3, 8, [1, 1, 1, 3]), (3, 2, [701])])
+@pytest.mark.parametrize("window,sinks", [(64, 4), (1 << 40, 0)])
+def test_layouts(cpt, cuda_device, layout, P, lens, window, sinks):
+    both(cpt, layout, P, lens, 2, 1, 64, window, sinks)
+
+
+@pytest.mark.parametrize("window", [0, 1, 2, 127, 128, 129, 255, 400])
+@pytest.mark.parametrize("sinks", [0, 1, 7, 128, 200])
+def test_windows_and_sinks(cpt, cuda_device, window, sinks):
+    both(cpt, 3, 2, [1, 390, 140, 260], 2, 2, 32, window, sinks, seed=window + sinks)
+
+
+@pytest.mark.parametrize("Hq,Hk", [(1, 1), (3, 1), (4, 2), (6, 2), (5, 5), (8, 1)])
+@pytest.mark.parametrize("D", [8, 64, 72, 128])
+def test_heads(cpt, cuda_device, Hq, Hk, D):
+    both(cpt, 3, 4, [150, 33, 301], Hq, Hk, D, 100, 3, seed=D + Hq)
+
+
+@pytest.mark.parametrize("D", [16, 24, 32, 40, 48, 56, 80, 88, 96, 104, 112, 120])
+def test_head_dims(cpt, cuda_device, D):
+    both(cpt, 1, 2, [150, 34], 2, 1, D, 1000, 0, seed=D)
+
+
+@pytest.mark.parametrize("layout,P,lens", [(3, 1, [1]), (3, 8, [1]), (1, 1, [0, 1, 0]), (3, 2, [0, 1, 1, 0]), (1, 8, [8])])
+def test_shortest_batches(cpt, cuda_device, layout, P, lens):
+    both(cpt, layout, P, lens, 2, 1, 64, 4, 1)
+
+
+def test_empty_batch(cpt, cuda_device):
+    plan = cpt.cpt_plan_create(1, 2, [0, 0], 0)
+    z = torch.empty(0, 2, 64, device="cuda", dtype=torch.bfloat16)
+    lse = torch.empty(2, 0, device="cuda")
+    cpt.cpt_attention(plan, z, z, z, z, lse, 1.0, 4, 0)
+    cpt.cpt_attention_backward(plan, z, z, z, z, lse, z, z, [z, z], [z, z], 1.0, 4, 0)
+    torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("window,sinks", [(300, 16), (4096, 0)])
+def test_longer_documents(cpt, cuda_device, window, sinks):
+    both(cpt, 0, 4, [2048, 1024], 2, 1, 128, window, sinks)
+    both(cpt, 3, 3, [1999, 601, 450], 2, 2, 64, window, sinks)
+
+
+def test_many_short_documents(cpt, cuda_device):
+    rng = np.random.default_rng(5)
+    lens = [int(x) for x in rng.integers(0, 40, 90)]
+    both(cpt, 3, 4, lens, 2, 1, 64, 16, 2)
+    lens[-1] += -sum(lens) % 4
+    both(cpt, 1, 4, lens, 2, 1, 64, 1 << 31, 0)
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 4.0])
+def test_scales(cpt, cuda_device, scale):
+    # scores of up to some 100 * scale: the binary32 slack of a weight grows with them
+    b = Batch(cpt, 0, 2, [256], 2, 1, 64, 100, 2, scale=scale)
+    b.forward()
+    b.backward()
+    slack = max(1.0, 8 * scale)   # |s| grows by scale * sqrt(D) = 8 scale over unit scores
+    e, ref.E32 = ref.E32, ref.E32 * slack
+    try:
+        b.check_forward()
+        b.check_backward()
+    finally:
+        ref.E32 = e
+
+
+def test_first_row_of_every_document_copies_v(cpt, cuda_device):
+    """A row that sees one key alone has out = v, bit for bit."""
+    b = Batch(cpt, 3, 4, [1, 50, 129, 3], 2, 1, 64, 1, 0)
+    b.forward()
+    real = ~b.pad
+    want = b.v[torch.from_numpy(b.l2r).cuda()[real]].repeat_interleave(2, 1)
+    assert torch.equal(b.out.t[real], want)
+
+
+def test_gradients_against_differences(cpt, cuda_device):
+    """Directional derivatives of sum(out * dout) by central differences of the
+    64-bit form agree with the kernels' gradients."""
+    b = both(cpt, 3, 2, [60, 33, 140], 4, 2, 64, 50, 2)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    dk = sum(ref_raw(b, x.t.double()) for x in b.dk)
+    dv = sum(ref_raw(b, x.t.double()) for x in b.dv)
+    do = torch.where(b.pad[:, None, None], 0.0, b.dout.double())
+    for name, grad in (("q", b.dq.t.double()), ("k", dk), ("v", dv)):
+        x = getattr(b, name).double()
+        d = torch.randn(x.shape, device="cuda", generator=g, dtype=torch.float64)
+        h = 1e-4
+        f = []
+        for sgn in (1, -1):
+            args = {n: getattr(b, n).double() for n in "qkv"}
+            args[name] = x + sgn * h * d
+            out, _, _ = ref.attention64(args["q"], args["k"], args["v"], b.see, b.scale)
+            f.append((out * do).sum())
+        want = (f[0] - f[1]) / (2 * h)
+        got = (grad * d).sum()
+        # every element of the gradient is off by a few roundings (independent signs); the
+        # difference's own error is of order h^2
+        assert abs(want - got) <= 8 * ref.U * (grad * d).square().sum().sqrt() + 1e-4 * abs(want) + 1e-2, name
+
+
+def ref_raw(b, x):
+    """Padded global rows back in raw order."""
+    at = np.arange(b.T) + np.repeat(b.cup[:-1] - b.cu[:-1], np.diff(b.cu))
+    return x[torch.from_numpy(at).cuda()]
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("D", [64, 128])
+def test_infinities_and_nan_stay_where_they_are_seen(cpt, cuda_device, bad, D):
+    """K and V rows of one document, a key past its window and the last key
+    of a document hold NaN or infinities: rows that do not see them are as if
+    they were finite, in both directions."""
+    lens, W, S = [100, 90, 260], 70, 2
+    b = Batch(cpt, 3, 2, lens, 2, 1, D, W, S)
+    spoiled = [99, 120, 190 + 40]          # raw tokens: last of document 0, inside 1, past sinks of 2
+    k, v = b.k, b.v
+    b.k, b.v = k.clone(), v.clone()
+    b.k[spoiled] = bad
+    b.v[spoiled] = bad
+    hit = b.see[:, spoiled].any(1)
+    assert hit.any() and (~hit).any()
+    b.forward()
+    want, lse, tol = ref.attention64(b.q, k, v, b.see, b.scale)
+    real = ~hit & ~b.pad
+    assert ((b.out.t.double() - want).abs() <= tol)[~hit].all()
+    assert ((b.lse.t.double() - lse).abs()[:, real] <= ref.E32 + 2.0 ** -22 * lse.abs()[:, real]).all()
+    # the gradient: rows that saw none of it, and keys that no such row sees
+    b.out.t.copy_(want)
+    b.lse.t.copy_(lse)
+    b.backward()
+    dq, tol, writers = ref.backward64(b.q, k, v, b.out.t, b.dout, b.see, b.scale, 2)
+    assert ((b.dq.t.double() - dq).abs() <= tol)[~hit].all()
+    free = ~b.see[hit].any(0)
+    free[spoiled] = False
+    assert free.any()
+    for r, pair in enumerate(writers):
+        for buf, (want, tol) in zip((b.dk[r], b.dv[r]), pair):
+            assert ((ref_raw(b, buf.t.double()) - want).abs() <= tol)[free].all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_garbage_in_padding_rows_is_not_used(cpt, cuda_device, D):
+    b = Batch(cpt, 3, 4, [3, 1, 150, 47, 9], 4, 2, D, 60, 2)
+    q, dout = b.q.clone(), b.dout.clone()
+    q[b.pad] = 0
+    dout[b.pad] = 0
+    b.q[b.pad] = float("nan")
+    b.dout[b.pad] = float("inf")
+    b.forward()
+    b.check_forward(q=q)
+    assert (b.out.t[b.pad] == 0).all() and (b.lse.t[:, b.pad] == -math.inf).all()
+    out = b.out.t.clone()
+    b.out.t[b.pad] = float("nan")
+    b.lse.t[:, b.pad] = float("nan")
+    b.backward()
+    b.check_backward(q=q, dout=dout, out=out)
+    assert (b.dq.t[b.pad] == 0).all()
+
+
+def test_repeated_calls_give_the_same_bits(cpt, cuda_device):
+    b = Batch(cpt, 3, 4, [700, 33, 900, 1], 4, 2, 128, 500, 5)
+    b.forward()
+    b.backward()
+    first = [x.t.clone() for x in [b.out, b.lse, b.dq] + b.dk + b.dv]
+    for _ in range(3):
+        for x in [b.out, b.lse, b.dq] + b.dk + b.dv:
+            x.t.fill_(7.0)
+        b.forward()
+        b.backward()
+        for x, y in zip([b.out, b.lse, b.dq] + b.dk + b.dv, first):
+            assert torch.equal(x.t, y)
+
+
+def test_streams_and_graphs(cpt, cuda_device):
+    """On another stream, captured and replayed, two graphs at once with a
+    workspace each."""
+    batches = [Batch(cpt, 3, 4, [300, 33, 129], 4, 2, 64, 100, 3, seed=s) for s in (1, 2)]
+    wants = []
+    for b in batches:
+        b.forward()
+        b.backward()
+        wants.append([x.t.clone() for x in [b.out, b.lse, b.dq] + b.dk + b.dv])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in batches]
+    spaces = [b.workspace() for b in batches]
+
+    def clear():
+        for b in batches:
+            for x in [b.out, b.lse, b.dq] + b.dk + b.dv:
+                x.t.zero_()
+        torch.cuda.synchronize()
+
+    def check():
+        torch.cuda.synchronize()
+        for b, want in zip(batches, wants):
+            for x, y in zip([b.out, b.lse, b.dq] + b.dk + b.dv, want):
+                assert torch.equal(x.t, y)
+
+    clear()
+    for b, s, w in zip(batches, streams, spaces):
+        b.forward(stream=s)
+        b.backward(w.t, stream=s)
+    check()
+    graphs = []
+    for b, w in zip(batches, spaces):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            b.forward()
+            b.backward(w.t)
+        graphs.append(graph)
+    for _ in range(2):
+        clear()
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+        check()
+
+
+def test_refusals_on_the_device(cpt, cuda_device):
+    b = Batch(cpt, 0, 2, [64], 2, 1, 64, 16, 0)
+    ok = dict(q=b.q, k=b.k, v=b.v, out=b.out.t, lse=b.lse.t, scale=1.0, window=4, sinks=0)
+
+    def status(**kw):
+        with pytest.raises(cpt.CptError) as e:
+            cpt.cpt_attention(b.plan, **{**ok, **kw})
+        return e.value.status
+
+    f = lambda t: t.float()  # noqa: E731
+    assert status(q=f(b.q), k=f(b.k), v=f(b.v), out=f(b.out.t)) == cpt.CPT_ERR_UNSUPPORTED
+    assert status(scale=0.0) == cpt.CPT_ERR_INVALID_ARG
+    assert status(scale=-1.0) == cpt.CPT_ERR_INVALID_ARG
+    assert status(scale=float("nan")) == cpt.CPT_ERR_INVALID_ARG
+    assert status(window=-1) == cpt.CPT_ERR_INVALID_ARG
+    assert status(sinks=-1) == cpt.CPT_ERR_INVALID_ARG
+    assert status(out=b.q) == cpt.CPT_ERR_ALIAS
+    assert status(k=b.k.cpu()) == cpt.CPT_ERR_DEVICE
+    ws = b.workspace().t
+
+    def back(**kw):
+        a = dict(q=b.q, k=b.k, v=b.v, out=b.out.t, lse=b.lse.t, dout=b.dout, dq=b.dq.t,
+                 dk_writers=[x.t for x in b.dk], dv_writers=[x.t for x in b.dv], scale=1.0, window=4, sinks=0,
+                 workspace=ws)
+        with pytest.raises(cpt.CptError) as e:
+            cpt.cpt_attention_backward(b.plan, **{**a, **kw})
+        return e.value.status
+
+    assert back(workspace=ws[:-1]) == cpt.CPT_ERR_WORKSPACE
+    assert back(workspace=ws[16:]) == cpt.CPT_ERR_WORKSPACE
+    assert back(dq=b.q) == cpt.CPT_ERR_ALIAS
+    assert back(dv_writers=[b.dv[0].t, b.dk[1].t]) == cpt.CPT_ERR_ALIAS
+    assert back(window=-1) == cpt.CPT_ERR_INVALID_ARG
+    torch.cuda.synchronize()
+
+
+def test_a_whole_step(cpt, cuda_device):
+    """Rotate, attend, differentiate, return and turn back, as a step uses the
+    calls, against autograd in 64 bits over the whole documents."""
+    lens, P, Hq, Hk, D, W, S = [130, 0, 57, 300], 4, 4, 2, 64, 90, 3
+    b = Batch(cpt, 3, P, lens, Hq, Hk, D, W, S)
+    T, Tpad = b.T, b.Tpad
+    g = torch.Generator(device="cuda").manual_seed(4)
+    freq, axis = [10000.0 ** (-i / 32) for i in range(32)], [i * 3 // 32 for i in range(32)]
+    pos = torch.randint(0, 5000, (3, T), dtype=torch.int32, device="cuda", generator=g)
+    q0, k0 = (torch.randn(T, h, D, device="cuda", generator=g).to(torch.bfloat16) for h in (Hq, Hk))
+    rot = cpt.cpt_rotary_create(D, freq, axis, 3)
+    kr = torch.empty_like(k0)
+    cpt.cpt_rotary_apply(rot, b.plan, [q0], [b.q], pos)
+    cpt.cpt_rotary_apply(rot, b.plan, [k0], [kr], pos, cpt.CPT_ORDER_GLOBAL, cpt.CPT_ORDER_GLOBAL)
+    b.k = kr
+    b.forward()
+    b.check_forward()
+    b.backward()
+    b.check_backward()
+    own = [[torch.empty(Tpad // P, Hk, D, device="cuda", dtype=torch.bfloat16) for _ in range(P)] for _ in range(2)]
+    cpt.cpt_grad_return(b.plan, [x.t for x in b.dk], [x.t for x in b.dv], own[0], own[1])
+    gq, gk = torch.empty_like(q0), torch.empty_like(k0)
+    gv = torch.empty_like(k0)
+    dko, dvo = torch.cat(own[0]), torch.cat(own[1])
+    L, G = cpt.CPT_ORDER_LOCAL, cpt.CPT_ORDER_GLOBAL
+    cpt.cpt_rotary_apply(rot, b.plan, [b.dq.t, dko], [gq, gk], pos, L, G, True)
+    cpt.cpt_restore(b.plan, [dvo], [gv])
+
+    x = [t.double().cpu().requires_grad_() for t in (q0, k0, b.v)]
+    theta = torch.stack([pos[a].double().cpu() * f for a, f in zip(axis, freq)], 1)[:, None, :]
+    turn = torch.polar(torch.ones_like(theta), theta)
+
+    def rotate(t):
+        z = torch.complex(t[..., :32], t[..., 32:]) * turn
+        return torch.cat([z.real, z.imag], -1)
+
+    see = ref.visible(np.arange(T), b.cu, T, W, S, "cpu")
+    s = torch.einsum("ihd,jhd->hij", rotate(x[0]), rotate(x[1]).repeat_interleave(Hq // Hk, 1)) * b.scale
+    p = torch.softmax(s.masked_fill(~see, -math.inf), -1)
+    out = torch.einsum("hij,jhd->ihd", p, x[2].repeat_interleave(Hq // Hk, 1))
+    real = torch.from_numpy(b.l2r[b.l2r >= 0])
+    do = torch.zeros(T, Hq, D, dtype=torch.float64)
+    do[real] = b.dout.double().cpu()[torch.from_numpy(b.l2r >= 0)]
+    (out * do).sum().backward()
+    got_out = torch.empty(T, Hq, D, dtype=torch.float64)
+    got_out[real] = b.out.t.double().cpu()[torch.from_numpy(b.l2r >= 0)]
+    # by norms: rotated q and k, p or ds, the output, the sum and the rotation back are rounded
+    # to bf16 once each, at most U of their values
+    for got, want in ((got_out, out.detach()), (gq, x[0].grad), (gk, x[1].grad), (gv, x[2].grad)):
+        rel = (got.double().cpu() - want).norm() / want.norm()
+        assert rel <= 6 * ref.U, float(rel)
