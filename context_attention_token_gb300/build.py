@@ -23,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 
 SOURCES = ["cpt_api.cu", "index_map.cu", "gather.cu", "grad_return.cu", "slot_reduce.cu", "ceiling.cu",
            "rotary.cu", "attention.cu", "attention_backward.cu"]
-HEADERS = ["cpt_internal.h", "cpt_device.cuh", "attention_common.cuh"]
+HEADERS = ["cpt_internal.h", "cpt_device.cuh", "attention_common.cuh", "tcgen05.cuh"]
 
 # The two builds of the library: the product, and the same sources with
 # every device index checked before use (CPT_CHECK_BOUNDS), for debugging and

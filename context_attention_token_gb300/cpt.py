@@ -68,6 +68,7 @@ CPT_ROTARY_MAX_AXES = 8
 CPT_ORDER_GLOBAL = 0
 CPT_ORDER_LOCAL = 1
 CPT_ATTENTION_MAX_HEADS = 1024
+CPT_ATTENTION_MAX_TOKENS = 2147482624
 
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32

@@ -4,14 +4,23 @@
 //   out = sum exp(s_j - m) v_j / l, lse = m + log l.
 // A row that sees nothing has out = 0 and lse = -inf.
 #include "attention_common.cuh"
+#include "tcgen05.cuh"
+
+#include <atomic>
 
 namespace cpt {
 
 namespace {
 
-// One warp computes one row of one head: lanes hold four elements each, keys
-// come one at a time, the softmax keeps its running maximum and sum.
-__device__ void row_forward(const AttentionParams &p, int64_t row, int head)
+// Waits that ran out (see cpt_kernel_wait_timeouts).
+__device__ unsigned int g_wait_timeouts;
+
+// One warp computes one row of one head from the definition: lanes hold four
+// elements each, keys come one at a time, the softmax keeps its running
+// maximum and sum. The tiled kernel multiplies hidden keys by a weight of zero,
+// which an infinity or NaN in their V turns into NaN: it gives such rows to
+// this function, which never touches a hidden key.
+__device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, int head)
 {
     const int lane = threadIdx.x & 31, at = lane * 4, D = p.D;
     const int kvh = head / (p.Hq / p.Hkv);
@@ -43,30 +52,546 @@ __device__ void row_forward(const AttentionParams &p, int64_t row, int head)
     if (lane == 0) p.lse[head * p.Tpad + row] = m + logf(l);
 }
 
-constexpr int kWarps = 8;
+// ----------------------------------------------------------------- tiled kernel
+//
+// A CTA works on items of two tiles of 128 query rows against one kv head: the
+// same rows of two heads that share it, or neighbouring rows of one head. It
+// is persistent (one per SM) and split into roles that hand tiles on through
+// barriers, so that loads, matrix instructions and softmax of different tiles
+// run at the same time, across items too:
+//   rows     (2 warps)  which keys every row of the next item sees;
+//   loader   (1 warp)   the item's list of key tiles, its Q, K and V by TMA;
+//   issuer   (1 thread) the matrix instructions: S = Q K^T into tensor memory,
+//                       then O += P V with P read from tensor memory;
+//   softmax  (2 x 4 warps, one warpgroup per query tile, one thread per row)
+//            scores to weights in place, statistics, the final division.
+// Tensor memory: S of both tiles (P over it), O of both tiles: 4 x 128 columns.
+//
+// Key tiles start anywhere: the next one starts at the first key at or behind
+// the last one's end that any row of the item sees. This covers windows,
+// sinks, jumps between a rank's chunks and short documents in one rule, with
+// at most one partly used tile per contiguous span.
 
-__global__ void __launch_bounds__(32 * kWarps) attention_rows_kernel(const __grid_constant__ AttentionParams p)
+constexpr int kRing = 8;       // key-tile announcements in flight
+constexpr uint32_t kNeed = 1, kFull = 4, kFirst = 16, kLast = 32, kStop = 64;   // kNeed, kFull: << query tile
+
+template <int DP>
+struct Shape {
+    static constexpr int kSlabs = DP / 64;
+    static constexpr uint32_t kTileBytes = kSlabs * kSlab;
+    static constexpr int kStages = DP == 128 ? 4 : 8;      // K and V tiles
+    static constexpr uint32_t kSmem = 1024 + (2 + kStages) * kTileBytes;
+};
+
+struct Shared {
+    uint64_t q_full, q_empty;
+    uint64_t kv_full[8], kv_empty[8];
+    uint64_t info_full[kRing], info_empty[kRing];
+    uint64_t rows_full[2], rows_empty[2];
+    uint64_t s_ready[2], p_ready[2], pv_done[2], drained;
+    int2 info[kRing];                  // first key, flags
+    int4 rows[2][2][kTile];            // two visible spans of every row of an item
+    uint32_t tmem;
+    uint32_t stop;
+};
+
+struct Maps {
+    CUtensorMap q, k, v;
+};
+
+// Where an item lies.
+struct Item {
+    int rank, head;
+    int64_t row0;        // first row, of the rank's
+    bool pair;           // two heads, not two row tiles
+};
+
+__device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int64_t row_tiles, bool pair)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (i >= p.Tpad * p.Hq) return;
-    row_forward(p, i % p.Tpad, static_cast<int>(i / p.Tpad));
+    // heads slowest, so that neighbouring CTAs share keys in L2; within a head the
+    // later rows first, which see the most keys when the window is long
+    Item t;
+    t.pair = pair;
+    const int64_t per_head = row_tiles * p.P;
+    const int64_t h = i / per_head, j = i - h * per_head;
+    t.head = static_cast<int>(pair ? 2 * h : h);
+    t.rank = static_cast<int>(j % p.P);
+    t.row0 = (row_tiles - 1 - j / p.P) * (pair ? kTile : 2 * kTile);
+    return t;
+}
+
+// First key >= x of two spans; the largest int when there is none.
+__device__ __forceinline__ int next_key(int4 r, int x)
+{
+    return x < r.y ? max(x, r.x) : (x < r.w ? max(x, r.z) : 0x7FFFFFFF);
+}
+
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
+                     int64_t row_tiles, bool pair)
+{
+    typedef Shape<DP> Sh;
+    extern __shared__ uint8_t raw[];
+    __shared__ Shared sh;
+    const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
+    const uint32_t q_at = base, kv_at = base + 2 * Sh::kTileBytes;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        for (int i = 0; i < Sh::kStages; ++i) {
+            mbar_init(&sh.kv_full[i], 1);
+            mbar_init(&sh.kv_empty[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh.info_full[i], 1);
+            mbar_init(&sh.info_empty[i], 9);     // issuer, 8 softmax warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.rows_full[i], 64);
+            mbar_init(&sh.rows_empty[i], 9);     // loader, 8 softmax warps
+            mbar_init(&sh.s_ready[i], 1);
+            mbar_init(&sh.p_ready[i], kTile);
+            mbar_init(&sh.pv_done[i], 1);
+        }
+        mbar_init(&sh.drained, 1);
+        sh.stop = 0;
+        mbar_init_fence();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t *stop = &sh.stop;
+    const int group = p.Hq / p.Hkv;
+    const int steps = (p.D + 15) / 16;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------- loader
+        uint32_t n = 0, c = 0, k = 0;   // announcements, ring loads, items
+        bool ok = true;
+        auto announce = [&](int key, uint32_t flags) {
+            const uint32_t s = n % kRing;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_empty[s], (n / kRing & 1) ^ 1, stop));
+            if (ok && lane == 0) {
+                sh.info[s] = make_int2(key, static_cast<int>(flags));
+                mbar_arrive(&sh.info_full[s]);
+            }
+            ++n;
+            return ok;
+        };
+        auto load = [&](const CUtensorMap *map, int head, int key) {
+            const uint32_t s = c % Sh::kStages;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.kv_empty[s], (c / Sh::kStages & 1) ^ 1, stop));
+            if (!ok) return false;
+            if (lane == 0) {
+                mbar_expect_tx(&sh.kv_full[s], Sh::kTileBytes);
+                for (int i = 0; i < Sh::kSlabs; ++i)
+                    tma_slab(kv_at + s * Sh::kTileBytes + i * kSlab, map, 64 * i, head, key, &sh.kv_full[s]);
+            }
+            ++c;
+            return true;
+        };
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++k) {
+            const Item t = item_at(p, it, row_tiles, pair);
+            const int b = k & 1;
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.rows_full[b], k / 2 & 1, stop));
+            if (!ok) break;
+            int4 r[2][4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) r[x][i] = sh.rows[b][pair ? 0 : x][lane + 32 * i];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop));
+            if (!ok) break;
+            if (lane == 0) {
+                mbar_expect_tx(&sh.q_full, 2 * Sh::kTileBytes);
+                for (int x = 0; x < 2; ++x)
+                    for (int i = 0; i < Sh::kSlabs; ++i)
+                        tma_slab(q_at + x * Sh::kTileBytes + i * kSlab, &maps.q, 64 * i, t.head + (pair ? x : 0),
+                                 static_cast<int>(t.rank * p.Tp + t.row0 + (pair ? 0 : x * kTile)), &sh.q_full);
+            }
+            auto next = [&](int x) {
+                int m = 0x7FFFFFFF;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) m = min(m, min(next_key(r[0][i], x), next_key(r[1][i], x)));
+                return __reduce_min_sync(0xFFFFFFFFu, m);
+            };
+            const int kvh = t.head / group;
+            int key = next(0);
+            uint32_t first = kFirst;
+            if (key == 0x7FFFFFFF) announce(0, kFirst | kLast);
+            while (ok && key != 0x7FFFFFFF) {
+                const int end = key + kTile;   // below 2^31: a tile starts at a token
+                bool need[2] = {false, false}, full[2] = {true, true};
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int4 v = r[x][i];
+                        const bool any = (v.x < end && v.y > key) || (v.z < end && v.w > key);
+                        const bool all = (v.x <= key && v.y >= end) || (v.z <= key && v.w >= end);
+                        need[x] |= any;
+                        full[x] &= all || (v.y == 0 && v.w == 0);
+                    }
+                uint32_t flags = first;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (__any_sync(0xFFFFFFFFu, need[x])) flags |= kNeed << x;
+                    if (__all_sync(0xFFFFFFFFu, full[x])) flags |= kFull << x;
+                }
+                const int nk = next(end);
+                if (nk == 0x7FFFFFFF) flags |= kLast;
+                if (!announce(key, flags) || !load(&maps.k, kvh, key) || !load(&maps.v, kvh, key)) break;
+                key = nk;
+                first = 0;
+            }
+        }
+        if (ok) announce(0, kStop);
+        if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
+            for (uint32_t i = c > Sh::kStages ? c - Sh::kStages : 0; i < c; ++i)
+                mbar_wait_bounded(&sh.kv_full[i % Sh::kStages], i / Sh::kStages & 1);
+            if (k > 0) mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
+            mbar_wait_bounded(&sh.q_full, k & 1);
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------- issuer
+        if (lane == 0) {
+            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+            uint32_t c = 0, items_seen = 0, ps[2] = {0, 0};
+            uint32_t prev = 0, v_stage = 0;   // flags of the last key tile, the stage of its V
+            bool started[2] = {false, false};
+            bool ok = true;
+            for (uint32_t n = 0; ok; ++n) {
+                const uint32_t s = n % kRing;
+                if (!(ok = mbar_wait_or_stop(&sh.info_full[s], n / kRing & 1, stop))) break;
+                const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
+                mbar_arrive(&sh.info_empty[s]);
+                const bool tile = (e & (3 * kNeed)) != 0;
+                const uint32_t k_stage = c % Sh::kStages, k_parity = c / Sh::kStages & 1;
+                if ((e & kFirst) && !(ok = mbar_wait_or_stop(&sh.q_full, items_seen & 1, stop))) break;
+                if (prev & (3 * kNeed)) {
+                    // its V was loaded right after its K
+                    const uint32_t vc = v_stage;
+                    if (!(ok = mbar_wait_or_stop(&sh.kv_full[vc % Sh::kStages], vc / Sh::kStages & 1, stop))) break;
+                }
+                if (tile && !(ok = mbar_wait_or_stop(&sh.kv_full[k_stage], k_parity, stop))) break;
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    if (prev & (kNeed << x)) {
+                        if (!(ok = mbar_wait_or_stop(&sh.p_ready[x], ps[x] & 1, stop))) break;
+                        ++ps[x];
+                        tmem_fence_after();
+                        const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
+                        for (int k = 0; k < kTile / 16; ++k)
+                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape,
+                                     started[x] || k > 0);
+                        started[x] = true;
+                        mma_commit(&sh.pv_done[x]);
+                    }
+                    if (e & kFirst) started[x] = false;
+                    if (e & (kNeed << x)) {
+                        mma_scores(tmem + 128 * x, q_at + x * Sh::kTileBytes, kv_at + k_stage * Sh::kTileBytes, s_shape,
+                                   steps);
+                        mma_commit(&sh.s_ready[x]);
+                    }
+                }
+                if (!ok) break;
+                if (prev & (3 * kNeed)) mma_commit(&sh.kv_empty[v_stage % Sh::kStages]);
+                if (tile) {
+                    mma_commit(&sh.kv_empty[k_stage]);
+                    v_stage = c + 1;
+                    c += 2;
+                }
+                if (e & kLast) {
+                    mma_commit(&sh.q_empty);
+                    ++items_seen;
+                }
+                prev = e;
+                if (e & kStop) break;
+            }
+            mma_commit(&sh.drained);
+            mbar_wait_bounded(&sh.drained, 0);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------- rows
+        uint32_t k = 0;
+        for (int64_t it = blockIdx.x; it < items; it += gridDim.x, ++k) {
+            const Item t = item_at(p, it, row_tiles, pair);
+            const int b = k & 1;
+            if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
+            for (int i = threadIdx.x - 64; i < (pair ? kTile : 2 * kTile); i += 64) {
+                int4 r = make_int4(0, 0, 0, 0);
+                const int64_t row = t.row0 + i;
+                const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;
+                if (g >= 0) {
+                    const RowKeys w = keys_of_token(p, g);
+                    if (w.ns > 0) r.x = w.kb, r.y = w.kb + w.ns;
+                    if (w.lo <= g) r.z = w.lo, r.w = g + 1;
+                    if (r.y == r.z && r.w != 0 && r.y != 0) {   // one span
+                        r.z = r.x;
+                        r.x = r.y = 0;
+                    }
+                }
+                sh.rows[b][i / kTile][i % kTile] = r;
+            }
+            mbar_arrive(&sh.rows_full[b]);
+        }
+    } else {
+        // ------------------------------------------------------------- softmax
+        const int x = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
+        const uint32_t s_at = tmem + lanes + 128 * x, o_at = tmem + lanes + 256 + 128 * x;
+        const float c = p.scale * 1.4426950408889634f;
+        uint32_t k = 0, ns = 0;
+        int4 r = make_int4(0, 0, 0, 0);
+        float m = -INFINITY, l = 0.0f;
+        bool used = false, spoiled = false, done = false;
+        int64_t it = blockIdx.x;
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_full[slot], n / kRing & 1, stop))) break;
+            const int2 e = sh.info[slot];
+            const uint32_t flags = static_cast<uint32_t>(e.y);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+            if (flags & kStop) {
+                done = true;
+                break;
+            }
+            if (flags & kFirst) {
+                const int b = k & 1;
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.rows_full[b], k / 2 & 1, stop))) break;
+                r = sh.rows[b][pair ? 0 : x][t];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
+                m = -INFINITY;
+                l = 0.0f;
+                used = false;
+            }
+            if (flags & (kNeed << x)) {
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.s_ready[x], ns & 1, stop))) break;
+                tmem_fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_load32(s_at + 32 * i, s[i]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) tmem_wait_loads(s[i]);
+                if (!(flags & (kFull << x))) {
+                    const int a0 = r.x - e.x, a1 = r.y - e.x, b0 = r.z - e.x, b1 = r.w - e.x;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t bits = span_bits(a0, a1, i) | span_bits(b0, b1, i);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
+                    }
+                }
+                float mx = __uint_as_float(s[0][0]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[i][j]));
+                mx = fmaxf(m, mx);
+                // The maximum in use may lag behind by a factor of 2^8 in the weights: binary32 sums
+                // have the room, and O is rarely read back to be scaled.
+                bool late = false;
+                if (m == -INFINITY) m = mx;
+                else late = (mx - m) * c > 8.0f;
+                if (__any_sync(0xFFFFFFFFu, late)) {
+                    const float f = late ? exp2_fast((m - mx) * c) : 1.0f;
+                    l *= f;
+                    if (late) m = mx;
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.pv_done[x], (ns - 1) & 1, stop))) break;
+                    tmem_fence_after();
+                    for (int i = 0; i < steps; ++i) {
+                        uint32_t o[16];
+                        tmem_load16(o_at + 16 * i, o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_store16(o_at + 16 * i, o);
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.0f : m * c;
+                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const float a = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j]), c, -mc));
+                        const float b = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j + 1]), c, -mc));
+                        sum[j & 1] += a;
+                        sum[2 + (j & 1)] += b;
+                        // weights are rounded to bf16 for the matrix instruction; their sum is not
+                        w[j] = pack_bf16x2(a, b);
+                    }
+                    tmem_store16(s_at + 16 * i, w);
+                }
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                tmem_wait_stores();
+                tmem_fence_before();
+                mbar_arrive(&sh.p_ready[x]);
+                ++ns;
+                used = true;
+            }
+            if (flags & kLast) {
+                const Item d = item_at(p, it, row_tiles, pair);
+                const int head = d.head + (pair ? x : 0);
+                const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t;
+                const int64_t row = d.rank * p.Tp + in_rank;
+                const bool valid = in_rank < p.Tp, sees_any = r.y != 0 || r.w != 0;
+                const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
+                float bad = 0.0f;
+                if (used) {
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.pv_done[x], (ns - 1) & 1, stop))) break;
+                    tmem_fence_after();
+                }
+                uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
+                for (int i = 0; i < steps; ++i) {
+                    uint32_t o[16] = {};
+                    if (used) tmem_load16(o_at + 16 * i, o);
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float a = sees_any ? __uint_as_float(o[2 * j]) * inv : 0.0f;
+                        const float b = sees_any ? __uint_as_float(o[2 * j + 1]) * inv : 0.0f;
+                        bad = __fmaf_rn(a, 0.0f, __fmaf_rn(b, 0.0f, bad));
+                        w[j] = pack_bf16x2(a, b);
+                    }
+                    if (valid) {
+                        *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (16 * i + 8 < p.D)
+                            *reinterpret_cast<uint4 *>(out + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+                    }
+                }
+                if (valid)
+                    p.lse[head * p.Tpad + row] =
+                        sees_any && l != 0.0f ? (m * c + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                spoiled |= valid && bad != 0.0f;   // NaN
+                it += gridDim.x;
+                ++k;
+            }
+        }
+        // Rows with an infinity or NaN once more, one at a time, when no other role waits.
+        if (done && __any_sync(0xFFFFFFFFu, spoiled)) {
+            for (it = blockIdx.x; it < items; it += gridDim.x) {
+                const Item d = item_at(p, it, row_tiles, pair);
+                const int head = d.head + (pair ? x : 0);
+                const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t, row = d.rank * p.Tp + in_rank;
+                bool bad = false;
+                if (in_rank < p.Tp) {
+                    const uint16_t *out = row_of(p.out, row, p.Hq, head, p.D);
+                    for (int i = 0; i < p.D; ++i) bad |= (out[i] & 0x7F80) == 0x7F80;
+                }
+                unsigned todo = __ballot_sync(0xFFFFFFFFu, bad);
+                while (todo) {
+                    const int from = __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    row_forward(p, __shfl_sync(0xFFFFFFFFu, row, from), head);
+                }
+            }
+        }
+    }
+    __syncthreads();
+    if (warp == 2) tmem_free(tmem);
+    if (threadIdx.x == 0 && sh.stop != 0) atomicAdd(&g_wait_timeouts, 1u);
+}
+
+// ----------------------------------------------------------------- launch
+
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                             const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                             CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeFn encode_fn()
+{
+    static std::atomic<void *> fn{nullptr};
+    void *f = fn.load(std::memory_order_acquire);
+    if (f == nullptr) {
+        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            return nullptr;
+        }
+        fn.store(f, std::memory_order_release);
+    }
+    return reinterpret_cast<EncodeFn>(f);
+}
+
+}  // namespace
+
+cudaError_t make_slab_map(CUtensorMap *map, const void *base, int D, int heads, int64_t rows)
+{
+    const EncodeFn encode = encode_fn();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)D * 2 * (cuuint64_t)heads};
+    const cuuint32_t box[3] = {64, 1, (cuuint32_t)kTile}, ones[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void *>(base), dims, strides, box,
+                              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+namespace {
+
+template <int DP>
+cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_t stream)
+{
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> attr_set[64];
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(attention_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
+    }
+    // two heads of one kv head see the same keys and share every K and V tile
+    const bool pair = p.Hq / p.Hkv % 2 == 0;
+    const int64_t rows = pair ? kTile : 2 * kTile;
+    const int64_t row_tiles = (p.Tp + rows - 1) / rows;
+    const int64_t items = row_tiles * p.P * (pair ? p.Hq / 2 : p.Hq);
+    const int64_t sms = sm_count(dev);
+    attention_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), 384, Shape<DP>::kSmem, stream>>>(
+        p, maps, items, row_tiles, pair);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream)
 {
-    const int64_t rows = p.Tpad * p.Hq;
-    if (rows == 0) return cudaSuccess;
-    const int64_t grid = (rows + kWarps - 1) / kWarps;
-    if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    attention_rows_kernel<<<static_cast<unsigned>(grid), 32 * kWarps, 0, stream>>>(p);
-    return cudaGetLastError();
+    if (p.Tpad == 0) return cudaSuccess;
+    Maps maps;
+    cudaError_t e = make_slab_map(&maps.q, p.q, p.D, p.Hq, p.Tpad);
+    if (e == cudaSuccess) e = make_slab_map(&maps.k, p.k, p.D, p.Hkv, p.T);
+    if (e == cudaSuccess) e = make_slab_map(&maps.v, p.v, p.D, p.Hkv, p.T);
+    if (e != cudaSuccess) return e;
+    return p.D <= 64 ? launch_tiled<64>(p, maps, stream) : launch_tiled<128>(p, maps, stream);
 }
 
 cudaError_t read_attention_bounds_violations(unsigned int *count, bool reset)
 {
     return read_bounds_counter(count, reset);
+}
+
+cudaError_t read_attention_wait_timeouts(unsigned int *count, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned int));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 }  // namespace cpt

@@ -1086,13 +1086,14 @@ cpt_status cpt_kernel_wait_timeouts(uint32_t *count, int32_t reset)
     if (count == nullptr) return fail(CPT_ERR_INVALID_ARG, "NULL argument");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int v = 0, w = 0, x = 0, y = 0;
+    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0;
     cudaError_t e = read_wait_timeouts(&v, reset != 0);
     if (e == cudaSuccess) e = read_slot_reduce_wait_timeouts(&w, reset != 0);
     if (e == cudaSuccess) e = read_gather_wait_timeouts(&x, reset != 0);
     if (e == cudaSuccess) e = read_ceiling_wait_timeouts(&y, reset != 0);
+    if (e == cudaSuccess) e = read_attention_wait_timeouts(&z, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "wait-timeout counter read");
-    *count = v + w + x + y;
+    *count = v + w + x + y + z;
     return CPT_OK;
 }
 
@@ -1307,10 +1308,14 @@ cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *plan, int3
 
 namespace {
 
-// The checks that do not look at a device: shapes, types, the mask.
-cpt_status check_attention(int32_t q_heads, int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
+// The checks that do not look at a device: lengths, shapes, types, the mask.
+cpt_status check_attention(const cpt_plan *plan, int32_t q_heads, int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
                            int64_t window, int32_t sinks)
 {
+    // tiles reach past the last token, in 32-bit positions
+    if (plan->Tpad > CPT_ATTENTION_MAX_TOKENS)
+        return fail(CPT_ERR_UNSUPPORTED, "%lld tokens are over %d", (long long)plan->Tpad,
+                    CPT_ATTENTION_MAX_TOKENS);
     if (q_heads < 1 || kv_heads < 1 || q_heads % kv_heads != 0)
         return fail(CPT_ERR_INVALID_ARG, "q_heads %d is not a positive multiple of kv_heads %d", q_heads,
                     kv_heads);
@@ -1370,7 +1375,7 @@ cpt_status cpt_attention(const cpt_plan *plan, const void *q, const void *k, con
     int dev = 0;
     cpt_status st = check_plan(plan, &dev);
     if (st) return st;
-    if ((st = check_attention(q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
+    if ((st = check_attention(plan, q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
     if (plan->Tpad == 0) return CPT_OK;
     const size_t qb = (size_t)plan->Tpad * q_heads * head_dim * 2, kb = (size_t)plan->T * kv_heads * head_dim * 2;
     std::vector<Range> r;
@@ -1400,7 +1405,7 @@ size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int32_t q_he
         fail(CPT_ERR_INVALID_ARG, "plan is NULL");
         return 0;
     }
-    if (check_attention(q_heads, kv_heads, head_dim, CPT_BF16, 1.0f, 0, 0) != CPT_OK) return 0;
+    if (check_attention(plan, q_heads, kv_heads, head_dim, CPT_BF16, 1.0f, 0, 0) != CPT_OK) return 0;
     return backward_workspace(plan, q_heads);
 }
 
@@ -1415,7 +1420,7 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
     int dev = 0;
     cpt_status st = check_plan(plan, &dev);
     if (st) return st;
-    if ((st = check_attention(q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
+    if ((st = check_attention(plan, q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
     if (dk_writers == nullptr || dv_writers == nullptr)
         return fail(CPT_ERR_INVALID_ARG, "dk_writers or dv_writers is NULL");
     if (plan->Tpad == 0) return CPT_OK;

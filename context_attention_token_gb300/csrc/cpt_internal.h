@@ -2,6 +2,7 @@
 // kernels. Not installed; callers use include/cpt.h.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -153,6 +154,11 @@ struct AttentionParams {
     float scale;
 };
 cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream);
+cudaError_t read_attention_wait_timeouts(unsigned int *count, bool reset);
+
+// A TMA map of a bf16 [rows][heads][D] tensor, in boxes of 64 elements of one
+// head in 128 rows, 128-byte swizzled.
+cudaError_t make_slab_map(CUtensorMap *map, const void *base, int D, int heads, int64_t rows);
 
 struct AttentionBackwardParams {
     AttentionParams a;             // out and lse are inputs here

@@ -1,0 +1,205 @@
+// Tensor memory, tcgen05 matrix instructions, tiled TMA loads and bounded
+// barrier waits: the pieces of the attention kernels, in inline PTX.
+//
+// Conventions of these kernels. Tiles are bf16 with 128-byte swizzled rows
+// of 64 elements ("slabs" of 128 rows, 16 KB); a head of more than 64 elements
+// is two slabs. The first operand has 128 rows; it comes from shared memory
+// (its inner dimension contiguous) or from tensor memory. The second has its
+// inner dimension contiguous (scores) or its outer one (products with V, K, Q
+// and dO, which are read as they lie).
+#pragma once
+
+#include <cuda.h>
+
+#include "cpt_device.cuh"
+
+namespace cpt {
+
+constexpr int kTile = 128;                 // rows of every tile
+constexpr uint32_t kSlab = 128 * 128;      // bytes of 128 rows x 64 bf16
+
+// ----------------------------------------------------------------- descriptors
+
+// Shared-memory operand with 128-byte swizzle whose inner dimension is
+// contiguous: groups of 8 rows are 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_inner(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
+           (2ull << 61);
+}
+
+// The same bytes read across: the outer dimension contiguous in blocks of 64
+// one slab apart, groups of 8 inner rows 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_outer(uint32_t addr)
+{
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kSlab >> 4) << 16) |
+           (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+
+// bf16 x bf16 into binary32, 128 rows, n columns (a multiple of 16).
+__device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_outer)
+{
+    return (1u << 4) | (1u << 7) | (1u << 10) | (b_outer ? 1u << 16 : 0u) | ((n >> 3) << 17) | (8u << 24);
+}
+
+// ----------------------------------------------------------------- matrix instructions
+
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add)
+{
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+        : "memory");
+}
+
+// Rows x columns of scores: both operands from shared memory, `steps` inner
+// steps of 16 (the second slab after four).
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
+{
+    for (int k = 0; k < steps; ++k) {
+        const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
+        mma_smem(d, desc_inner(a + at), desc_inner(b + at), shape, k > 0);
+    }
+}
+
+// An arrival on `bar` once every matrix instruction issued so far by this
+// thread has completed (and an arrival on behalf of its reads of shared memory).
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                     smem_addr(bar))
+                 : "memory");
+}
+
+__device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// ----------------------------------------------------------------- tensor memory
+
+// All 512 columns, by one warp; the kernels that call this run one CTA per SM.
+__device__ __forceinline__ void tmem_alloc(uint32_t *to)
+{
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(to)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+}
+
+__device__ __forceinline__ void tmem_free(uint32_t addr)
+{
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(addr) : "memory");
+}
+
+#define CPT_R4(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3])
+#define CPT_R16(a, i) CPT_R4(a, i), CPT_R4(a, i + 4), CPT_R4(a, i + 8), CPT_R4(a, i + 12)
+#define CPT_RR4(a, i) "+r"(a[i]), "+r"(a[i + 1]), "+r"(a[i + 2]), "+r"(a[i + 3])
+#define CPT_RR16(a, i) CPT_RR4(a, i), CPT_RR4(a, i + 4), CPT_RR4(a, i + 8), CPT_RR4(a, i + 12)
+#define CPT_IN4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
+#define CPT_IN16(a, i) CPT_IN4(a, i), CPT_IN4(a, i + 4), CPT_IN4(a, i + 8), CPT_IN4(a, i + 12)
+
+// 32 (or 16) neighbouring columns of this thread's lane. The values are there
+// only after tmem_wait_loads has taken the array.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : CPT_R16(r, 0), CPT_R16(r, 16)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[32])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" : CPT_RR16(r, 0), CPT_RR16(r, 16)::"memory");
+}
+
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
+        "tcgen05.wait::ld.sync.aligned;"
+        : CPT_R16(r, 0)
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr),
+        CPT_IN16(r, 0)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// ----------------------------------------------------------------- TMA
+
+// A box of 64 elements of one head in 128 neighbouring rows; rows and elements
+// outside the tensor arrive as zeros.
+__device__ __forceinline__ void tma_slab(uint32_t to, const CUtensorMap *map, int at, int head, int row,
+                                         uint64_t *bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(to),
+        "l"(map), "r"(at), "r"(head), "r"(row), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// ----------------------------------------------------------------- barriers
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar)
+{
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+// Waits of a kernel whose roles wait on one another: each gives up after
+// about a second, or as soon as another has given up (*stop, in shared memory).
+// The role then leaves its loop; the CTA ends without further work.
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile uint32_t *stop)
+{
+    const uint64_t t0 = global_timer_ns();
+    for (uint32_t it = 0; it < (1u << 24); ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*stop != 0) return false;
+        if (global_timer_ns() - t0 > 1000000000ull) break;
+    }
+    *stop = 1;
+    return false;
+}
+
+__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t *bar, uint32_t parity, volatile uint32_t *stop)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    return mbar_wait_slow(bar, parity, stop);
+}
+
+// ----------------------------------------------------------------- arithmetic
+
+__device__ __forceinline__ float exp2_fast(float x)
+{
+    float y;   // relative error 2^-22, exact zero for -inf
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The bits of columns [lo, hi) of a 128-column tile in its 32-column word w.
+__device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
+{
+    const int a = min(max(lo - 32 * w, 0), 32), b = min(max(hi - 32 * w, 0), 32);
+    return static_cast<uint32_t>((1ull << b) - 1) & ~static_cast<uint32_t>((1ull << a) - 1);
+}
+
+}  // namespace cpt

@@ -726,6 +726,8 @@ CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *pl
 
 /* Most query heads of one call. */
 #define CPT_ATTENTION_MAX_HEADS 1024
+/* Most tokens (T_pad of the plan). */
+#define CPT_ATTENTION_MAX_TOKENS 2147482624
 
 /* Causal attention over the plan's packed documents, every rank's queries in
  * one launch. The token at position u of its document sees position j of the
@@ -749,7 +751,7 @@ CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *pl
  *  Scores, softmax statistics and sums are binary32. Infinities and NaN reach
  *  the rows that see them and no others.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (dtype, head_dim, too many
- *  heads), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
+ *  heads or tokens), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
  *  another buffer), CPT_ERR_CUDA. */
 CPT_API cpt_status cpt_attention(const cpt_plan *plan, const void *q, const void *k, const void *v, void *out,
                                  float *lse, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
