@@ -120,12 +120,6 @@ __device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int
     return t;
 }
 
-// First key >= x of two spans; the largest int when there is none.
-__device__ __forceinline__ int next_key(int4 r, int x)
-{
-    return x < r.y ? max(x, r.x) : (x < r.w ? max(x, r.z) : 0x7FFFFFFF);
-}
-
 template <int DP>
 __global__ void __launch_bounds__(384, 1)
     attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
@@ -326,18 +320,9 @@ __global__ void __launch_bounds__(384, 1)
             const int b = k & 1;
             if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
             for (int i = threadIdx.x - 64; i < (pair ? kTile : 2 * kTile); i += 64) {
-                int4 r = make_int4(0, 0, 0, 0);
                 const int64_t row = t.row0 + i;
                 const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;
-                if (g >= 0) {
-                    const RowKeys w = keys_of_token(p, g);
-                    if (w.ns > 0) r.x = w.kb, r.y = w.kb + w.ns;
-                    if (w.lo <= g) r.z = w.lo, r.w = g + 1;
-                    if (r.y == r.z && r.w != 0 && r.y != 0) {   // one span
-                        r.z = r.x;
-                        r.x = r.y = 0;
-                    }
-                }
+                const int4 r = g >= 0 ? spans_of(p, g) : make_int4(0, 0, 0, 0);
                 sh.rows[b][i / kTile][i % kTile] = r;
             }
             mbar_arrive(&sh.rows_full[b]);

@@ -5,12 +5,18 @@
 //   dq_i = sum_j ds_ij k_j, and for the rows i of rank r alone
 //   dk_j(r) = sum_i ds_ij q_i, dv_j(r) = sum_i p_ij do_i.
 #include "attention_common.cuh"
+#include "tcgen05.cuh"
+
+#include <atomic>
 
 namespace cpt {
 
 namespace {
 
 typedef AttentionBackwardParams Params;
+
+// Waits that ran out (see cpt_kernel_wait_timeouts).
+__device__ unsigned int g_wait_timeouts;
 
 // p and ds of one (row, key) pair, the same in every lane.
 __device__ __forceinline__ void pair_grad(const Params &b, float4 q, float4 dout, float4 k, float4 v, float lse,
@@ -22,7 +28,9 @@ __device__ __forceinline__ void pair_grad(const Params &b, float4 q, float4 dout
     ds = p * (dp - delta) * b.a.scale;
 }
 
-__device__ void row_dq(const Params &b, int64_t row, int head)
+// A warp's computation of one row from the definition, for rows that an
+// infinity or NaN behind a hidden key or row spoiled in the tiled kernels.
+__device__ __noinline__ void row_dq(const Params &b, int64_t row, int head)
 {
     const AttentionParams &p = b.a;
     const int at = (threadIdx.x & 31) * 4, D = p.D;
@@ -49,7 +57,7 @@ __device__ void row_dq(const Params &b, int64_t row, int head)
 }
 
 // dK and dV of one raw key for one writer, over the rows of that rank.
-__device__ void key_dkdv(const Params &b, int32_t j, int rank, int kvh)
+__device__ __noinline__ void key_dkdv(const Params &b, int32_t j, int rank, int kvh)
 {
     const AttentionParams &p = b.a;
     const int lane = threadIdx.x & 31, at = lane * 4, D = p.D, G = p.Hq / p.Hkv;
@@ -85,66 +93,970 @@ __device__ void key_dkdv(const Params &b, int32_t j, int rank, int kvh)
     store4(const_cast<uint16_t *>(row_of(b.dv[rank], pos, p.Hkv, kvh, D)), at, D, dv);
 }
 
-constexpr int kWarps = 8;
+// ----------------------------------------------------------------- preparation
 
-__global__ void __launch_bounds__(32 * kWarps) delta_kernel(const __grid_constant__ Params b)
+constexpr int kPrepRows = 32;   // rows of one block: 8 lanes each
+
+// Rows: delta and the base-2 log-sum-exp of every (head, row), the spans of
+// keys that a row sees, zeros in the writers' padding positions. A row that
+// sees nothing gets lse2 = +inf, which makes all its weights zero.
+__global__ void __launch_bounds__(8 * kPrepRows) rows_kernel(const __grid_constant__ Params b)
 {
     const AttentionParams &p = b.a;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (i >= p.Tpad * p.Hq) return;
-    const int64_t row = i / p.Hq;
-    const int head = static_cast<int>(i % p.Hq), lane = threadIdx.x & 31;
-    const float d = warp_sum(dot4(load4(row_of(p.out, row, p.Hq, head, p.D), lane * 4, p.D),
-                                  load4(row_of(b.dout, row, p.Hq, head, p.D), lane * 4, p.D)));
-    if (lane == 0) b.delta[head * p.Tpad + row] = d;
-}
-
-__global__ void __launch_bounds__(32 * kWarps) dq_rows_kernel(const __grid_constant__ Params b)
-{
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (i >= b.a.Tpad * b.a.Hq) return;
-    row_dq(b, i % b.a.Tpad, static_cast<int>(i / b.a.Tpad));
-}
-
-// One warp per (writer, padded global position, kv head); positions of
-// padding are written as zeros.
-__global__ void __launch_bounds__(32 * kWarps) dkdv_rows_kernel(const __grid_constant__ Params b)
-{
-    const AttentionParams &p = b.a;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * kWarps + threadIdx.x / 32;
-    if (i >= p.Tpad * p.Hkv * p.P) return;
-    const int32_t pos = static_cast<int32_t>(i % p.Tpad);
-    const int kvh = static_cast<int>(i / p.Tpad % p.Hkv), rank = static_cast<int>(i / p.Tpad / p.Hkv);
-    const int32_t doc = find_doc(b.cup, p.n_docs, pos);
-    const int32_t j = pos - b.cup[doc] + p.cu[doc];
-    if (j < p.cu[doc + 1]) {
-        key_dkdv(b, j, rank, kvh);
-    } else {
-        const int at = (threadIdx.x & 31) * 4;
-        const float4 zero = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        store4(const_cast<uint16_t *>(row_of(b.dk[rank], pos, p.Hkv, kvh, p.D)), at, p.D, zero);
-        store4(const_cast<uint16_t *>(row_of(b.dv[rank], pos, p.Hkv, kvh, p.D)), at, p.D, zero);
+    const int head = static_cast<int>(blockIdx.x % p.Hq);
+    const int64_t row = blockIdx.x / p.Hq * kPrepRows + threadIdx.x / 8;
+    const int lane = threadIdx.x & 7;
+    float d = 0.0f;
+    const bool in = row < p.Tpad;
+    const int32_t g = in ? token_of_row(p, row) : -1;
+    if (g >= 0) {
+        const uint16_t *o = row_of(p.out, row, p.Hq, head, p.D), *w = row_of(b.dout, row, p.Hq, head, p.D);
+        for (int at = 8 * lane; at < p.D; at += 64)
+            d += dot4(load4(o, at, p.D), load4(w, at, p.D)) + dot4(load4(o, at + 4, p.D), load4(w, at + 4, p.D));
+    }
+#pragma unroll
+    for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+    if (!in) return;
+    const int64_t at = head * p.Tpad + row;
+    if (lane == 0) {
+        const float lse = g >= 0 ? p.lse[at] : -INFINITY;
+        b.delta[at] = d;
+        b.lse2[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
+    }
+    // the rows that see nothing: the matrix kernels pass them over
+    if (g < 0 || (p.window == 0 && p.sinks == 0)) {
+        uint16_t *dq = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, p.D));
+        for (int i = 8 * lane; i < p.D; i += 64) *reinterpret_cast<uint4 *>(dq + i) = make_uint4(0, 0, 0, 0);
+    }
+    if (head != 0) return;
+    if (lane == 0) {
+        int4 r = make_int4(0, 0, 0, 0);
+        if (g >= 0) r = spans_of(p, g);
+        b.spans[row] = r;
+    }
+    if (p.l2r[row] < 0) {
+        const int64_t bytes = static_cast<int64_t>(p.Hkv) * p.D * 2, pos = b.l2g[row];
+        if (in_bounds(pos >= 0 && pos < p.Tpad))
+            for (int r = 0; r < p.P; ++r)
+                for (int64_t i = 16 * lane; i < bytes; i += 128) {
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(b.dk[r]) + pos * bytes + i) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(b.dv[r]) + pos * bytes + i) = make_uint4(0, 0, 0, 0);
+                }
     }
 }
 
+// Rows of a rank whose (padded) global position is below x, a position of
+// document doc or its end.
+__device__ __forceinline__ int64_t rows_below(const Params &b, int rank, int32_t doc, int64_t x)
+{
+    const AttentionParams &p = b.a;
+    if (b.packed) return min(max(x - rank * p.Tp, (int64_t)0), p.Tp);
+    const int64_t begin = b.cup[doc], m = (b.cup[doc + 1] - begin) / (2 * p.P), u = x - begin;
+    return begin / p.P + min(max(u - rank * m, (int64_t)0), m) +
+           min(max(u - (2 * p.P - 1 - rank) * m, (int64_t)0), m);
+}
+
+// Padded global position of a raw token.
+__device__ __forceinline__ int32_t position_of_token(const Params &b, int32_t j)
+{
+    if (b.r2l == nullptr) return j;
+    const int32_t row = b.r2l[j];
+    return in_bounds(row >= 0 && row < b.a.Tpad) ? b.l2g[row] : -1;
+}
+
+// Key tiles of every rank: the local rows that may see one of the 128 keys, as
+// up to two ranges (the window's, and the rest of the documents whose
+// sinks lie in the tile); tiles that no row sees are written as zeros here.
+// The others go into a list, those with a range of sinks (the long ones) from
+// its front, the rest from its back. The order of the list sets which CTA takes
+// a tile and no result.
+__global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Params b, int tiles)
+{
+    const AttentionParams &p = b.a;
+    __shared__ int any;
+    const int rank = static_cast<int>(blockIdx.x % p.P), tile = static_cast<int>(blockIdx.x / p.P);
+    const int32_t k0 = tile * kTile, k1 = static_cast<int32_t>(min((int64_t)k0 + kTile, p.T)) - 1;
+    if (threadIdx.x == 0) {
+        const int32_t d0 = find_doc(p.cu, p.n_docs, k0), d1 = find_doc(p.cu, p.n_docs, k1);
+        const int64_t pos0 = b.cup[d0] + (k0 - p.cu[d0]), pos1 = b.cup[d1] + (k1 - p.cu[d1]), end = b.cup[d1 + 1];
+        int64_t w0 = 0, w1 = 0, s0 = 0, s1 = 0;
+        if (p.window > 0) {
+            w0 = rows_below(b, rank, d0, pos0);
+            w1 = rows_below(b, rank, d1, min(pos1 + p.window, end));
+        }
+        const bool own_sinks = k0 - p.cu[d0] < p.sinks;
+        if (p.sinks > 0 && (own_sinks || d1 > d0)) {
+            s0 = rows_below(b, rank, d0, own_sinks ? pos0 : (int64_t)b.cup[d0 + 1]);
+            s1 = rows_below(b, rank, d1, end);
+        }
+        const bool far = s1 > s0 && s1 > w1;
+        if (w1 <= w0) {
+            w0 = s0;
+            w1 = s1;
+            s0 = s1 = 0;
+        } else if (s1 <= s0) {
+            s0 = s1 = 0;
+        } else if (s0 <= w1) {
+            w1 = max(w1, s1);
+            s0 = s1 = 0;
+        }
+        const int i = tile * p.P + rank;
+        b.ranges[i] = make_int4((int)w0, (int)w1, (int)s0, (int)s1);
+        any = w1 > w0;
+        if (any) {
+            if (far) b.list[atomicAdd(&b.counters[0], 1)] = i;
+            else b.list[tiles * p.P - 1 - atomicAdd(&b.counters[1], 1)] = i;
+        }
+    }
+    __syncthreads();
+    if (any) return;
+    const int64_t bytes = static_cast<int64_t>(p.Hkv) * p.D * 2, units = bytes / 16;
+    for (int t = 0; t <= k1 - k0; ++t) {
+        const int64_t pos = position_of_token(b, k0 + t);
+        if (pos < 0) continue;
+        for (int64_t i = threadIdx.x; i < 2 * units; i += 256) {
+            uint8_t *to = static_cast<uint8_t *>(i < units ? b.dk[rank] : b.dv[rank]) + pos * bytes;
+            st_once(to + 16 * (i < units ? i : i - units), make_uint4(0, 0, 0, 0));
+        }
+    }
+}
+
+// ----------------------------------------------------------------- shared by both kernels
+
+constexpr int kRing = 8;       // tile announcements in flight
+constexpr uint32_t kFull = 1, kFirst = 2, kLast = 4, kStop = 8, kDirty = 16;
+
+template <int DP>
+struct Shape {
+    static constexpr int kSlabs = DP / 64;
+    static constexpr uint32_t kTileBytes = kSlabs * kSlab;
+};
+
+struct Maps {
+    CUtensorMap q, k, v, dout;
+};
+
+__device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, int slabs, int head, int64_t row,
+                                          uint64_t *bar)
+{
+    mbar_expect_tx(bar, slabs * kSlab);
+    for (int i = 0; i < slabs; ++i) tma_slab(to + i * kSlab, map, 64 * i, head, static_cast<int>(row), bar);
+}
+
+// D += A B, A [128 x 128] from tensor memory as two halves of 64 inner columns
+// (each over the first half of the columns of scores it came from), B read
+// across.
+__device__ __forceinline__ void mma_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+{
+    for (int k = 0; k < kTile / 16; ++k)
+        mma_tmem(d, a + (k >> 2) * 64 + (k & 3) * 8, desc_outer(b + 2048 * k), shape, add || k > 0);
+}
+
+// 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)
+// elements of a row.
+__device__ __forceinline__ void store_columns(uint16_t *row, int at, int D, uint32_t tmem, float scale, bool write,
+                                              float &bad)
+{
+    uint32_t o[16], w[8];
+    tmem_load16(tmem + at, o);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float x = __uint_as_float(o[2 * j]) * scale, y = __uint_as_float(o[2 * j + 1]) * scale;
+        bad = __fmaf_rn(x, 0.0f, __fmaf_rn(y, 0.0f, bad));   // NaN once anything is not finite
+        w[j] = pack_bf16x2(x, y);
+    }
+    if (!write) return;
+    *reinterpret_cast<uint4 *>(row + at) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (at + 8 < D) *reinterpret_cast<uint4 *>(row + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
+__device__ bool spoiled_row(const uint16_t *row, int D)
+{
+    bool bad = false;
+    for (int i = 0; i < D; ++i) bad |= (row[i] & 0x7F80) == 0x7F80;
+    return bad;
+}
+
+// The bits of a 32 x 32 matrix, one row per lane, transposed.
+__device__ __forceinline__ uint32_t transpose_bits(uint32_t x)
+{
+    const uint32_t lane = threadIdx.x & 31;
+    uint32_t m = 0x0000FFFFu;
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+        const uint32_t y = __shfl_xor_sync(0xFFFFFFFFu, x, j);
+        x = lane & j ? (x & ~m) | ((y & ~m) >> j) : (x & m) | ((y & m) << j);
+        m ^= m << (j >> 1);
+    }
+    return x;
+}
+
+__device__ __forceinline__ uint32_t visible_bits(int4 r, int key, int word)
+{
+    return span_bits(r.x - key, r.y - key, word) | span_bits(r.z - key, r.w - key, word);
+}
+
+// ----------------------------------------------------------------- dQ
+//
+// An item is 128 query rows of one head; Q and dO stay in shared memory, the
+// key tiles pass by as in the forward kernel. Per key tile three products,
+//   S = Q K^T, dP = dO V^T, dQ += dS K,
+// with dS = P (dP - delta), rounded to bf16 for the matrix unit, over S in
+// tensor memory. S is there twice and issued a tile ahead, so that while two
+// warpgroups (64 key columns each, one thread per row) make dS, the matrix unit
+// has the last tile's dQ and the next S to do.
+// Tensor memory: S, S, dP, dQ. Shared memory: Q, dO, 3 K, 2 V.
+
+template <int DP>
+struct DqShared {
+    static constexpr int kK = 3, kV = 2;
+    uint8_t q[Shape<DP>::kTileBytes], dout[Shape<DP>::kTileBytes];
+    uint8_t k[kK][Shape<DP>::kTileBytes], v[kV][Shape<DP>::kTileBytes];
+    uint64_t q_full, q_empty, do_full, do_empty;
+    uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
+    uint64_t info_full[kRing], info_empty[kRing];
+    uint64_t dp_ready, ds_ready, acc_done, drained;
+    int4 info[kRing];              // first key, flags, item
+    uint32_t tmem, stop, spoiled;
+};
+
+struct DqItem {
+    int rank, head;
+    int64_t row0;
+};
+
+__device__ __forceinline__ DqItem dq_item(const AttentionParams &p, int64_t i, int64_t row_tiles)
+{
+    DqItem t;
+    const int64_t per_head = row_tiles * p.P, h = i / per_head, j = i - h * per_head;
+    t.head = static_cast<int>(h);
+    t.rank = static_cast<int>(j % p.P);
+    t.row0 = (row_tiles - 1 - j / p.P) * kTile;
+    return t;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    dq_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t items, int64_t row_tiles)
+{
+    typedef DqShared<DP> Sh;
+    constexpr int kSlabs = Shape<DP>::kSlabs;
+    const AttentionParams &p = b.a;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Sh &sh = *reinterpret_cast<Sh *>(raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.q_full, 1);
+        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.do_full, 1);
+        mbar_init(&sh.do_empty, 1);
+        for (int i = 0; i < Sh::kK; ++i) {
+            mbar_init(&sh.k_full[i], 1);
+            mbar_init(&sh.k_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kV; ++i) {
+            mbar_init(&sh.v_full[i], 1);
+            mbar_init(&sh.v_empty[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh.info_full[i], 1);
+            mbar_init(&sh.info_empty[i], 9);      // issuer, 8 warps
+        }
+        mbar_init(&sh.dp_ready, 1);
+        mbar_init(&sh.ds_ready, 2 * kTile);
+        mbar_init(&sh.acc_done, 1);
+        mbar_init(&sh.drained, 1);
+        sh.spoiled = 0;
+        sh.stop = smem_addr(raw) & 1023 ? 1 : 0;  // the swizzle needs 1024-byte tiles
+        mbar_init_fence();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t *stop = &sh.stop;
+    const int steps = (p.D + 15) / 16;
+
+    if (warp == 0 && *stop == 0) {
+        // ------------------------------------------------------------- loader
+        uint32_t n = 0, k = 0;                    // tiles, items
+        uint32_t nk = 0, nv = 0, nq = 0, no = 0;  // loads issued
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+            return ok;
+        };
+        auto announce = [&](int key, uint32_t flags, int64_t item) {
+            const uint32_t s = n % kRing;
+            if (wait(&sh.info_empty[s], (n / kRing & 1) ^ 1) && lane == 0) {
+                sh.info[s] = make_int4(key, static_cast<int>(flags), static_cast<int>(item & 0xFFFFFFFF),
+                                       static_cast<int>(item >> 32));
+                mbar_arrive(&sh.info_full[s]);
+            }
+            return ok;
+        };
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+            const DqItem t = dq_item(p, it, row_tiles);
+            const int64_t row = t.rank * p.Tp + t.row0;
+            int4 r[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                r[i] = t.row0 + lane + 32 * i < p.Tp ? b.spans[row + lane + 32 * i] : make_int4(0, 0, 0, 0);
+            auto next = [&](int x) {
+                return __reduce_min_sync(0xFFFFFFFFu, min(min(next_key(r[0], x), next_key(r[1], x)),
+                                                          min(next_key(r[2], x), next_key(r[3], x))));
+            };
+            const int kvh = t.head / (p.Hq / p.Hkv);
+            int key = next(0);
+            if (key == 0x7FFFFFFF) continue;   // no row sees a key
+            if (!wait(&sh.q_empty, (k & 1) ^ 1)) break;
+            if (lane == 0) load_tile(&maps.q, smem_addr(sh.q), kSlabs, t.head, row, &sh.q_full);
+            ++nq;
+            for (uint32_t first = kFirst; ok && key != 0x7FFFFFFF; first = 0) {
+                const int end = key + kTile;
+                bool full = true;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    full &= (r[i].x <= key && r[i].y >= end) || (r[i].z <= key && r[i].w >= end) ||
+                            (r[i].y == 0 && r[i].w == 0);
+                uint32_t flags = first;
+                if (__all_sync(0xFFFFFFFFu, full)) flags |= kFull;
+                const int after = next(end);
+                if (after == 0x7FFFFFFF) flags |= kLast;
+                const uint32_t ks = n % Sh::kK, vs = n % Sh::kV;
+                // the issuer asks for a tile's K before the last item's dO is free
+                if (!announce(key, flags, it)) break;
+                if (!wait(&sh.k_empty[ks], (n / Sh::kK & 1) ^ 1)) break;
+                if (lane == 0) load_tile(&maps.k, smem_addr(sh.k[ks]), kSlabs, kvh, key, &sh.k_full[ks]);
+                ++nk;
+                if (first) {
+                    if (!wait(&sh.do_empty, (k & 1) ^ 1)) break;
+                    if (lane == 0) load_tile(&maps.dout, smem_addr(sh.dout), kSlabs, t.head, row, &sh.do_full);
+                    ++no;
+                }
+                if (!wait(&sh.v_empty[vs], (n / Sh::kV & 1) ^ 1)) break;
+                if (lane == 0) load_tile(&maps.v, smem_addr(sh.v[vs]), kSlabs, kvh, key, &sh.v_full[vs]);
+                ++nv;
+                ++n;
+                key = after;
+            }
+            ++k;
+        }
+        if (ok) announce(0, kStop, 0);
+        if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
+            for (uint32_t i = nk > Sh::kK ? nk - Sh::kK : 0; i < nk; ++i)
+                mbar_wait_bounded(&sh.k_full[i % Sh::kK], i / Sh::kK & 1);
+            for (uint32_t i = nv > Sh::kV ? nv - Sh::kV : 0; i < nv; ++i)
+                mbar_wait_bounded(&sh.v_full[i % Sh::kV], i / Sh::kV & 1);
+            if (nq > 0) mbar_wait_bounded(&sh.q_full, (nq - 1) & 1);
+            if (no > 0) mbar_wait_bounded(&sh.do_full, (no - 1) & 1);
+        }
+    } else if (warp == 1 && *stop == 0) {
+        // ------------------------------------------------------------- issuer
+        if (lane == 0) {
+            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+            uint32_t ns = 0, np = 0, iq = 0, id = 0;   // tiles whose S, dP is issued; items begun with each
+            uint32_t flags[2] = {0, 0};                // of the tiles between S and dQ
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait_or_stop(bar, parity, stop); };
+            auto issue_s = [&]() {   // false at the end
+                const uint32_t s = ns % kRing;
+                if (!wait(&sh.info_full[s], ns / kRing & 1)) return false;
+                const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
+                mbar_arrive(&sh.info_empty[s]);
+                if (e & kStop) return false;
+                if ((e & kFirst) && !wait(&sh.q_full, iq++ & 1)) return false;
+                if (!wait(&sh.k_full[ns % Sh::kK], ns / Sh::kK & 1)) return false;
+                mma_scores(tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ns % Sh::kK]), s_shape, steps);
+                if (e & kLast) mma_commit(&sh.q_empty);
+                flags[ns & 1] = e;
+                ++ns;
+                return true;
+            };
+            auto issue_dp = [&]() {
+                const uint32_t e = flags[np & 1], vs = np % Sh::kV;
+                if ((e & kFirst) && !wait(&sh.do_full, id++ & 1)) return;
+                if (!wait(&sh.v_full[vs], np / Sh::kV & 1)) return;
+                mma_scores(tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
+                mma_commit(&sh.dp_ready);
+                mma_commit(&sh.v_empty[vs]);
+                if (e & kLast) mma_commit(&sh.do_empty);
+                ++np;
+            };
+            bool more = issue_s();
+            if (more) {
+                more = issue_s();
+                if (ok) issue_dp();
+            }
+            for (uint32_t i = 0; ok && i < np; ++i) {
+                if (!wait(&sh.ds_ready, i & 1)) break;
+                tmem_fence_after();
+                const uint32_t e = flags[i & 1];
+                if (np < ns) issue_dp();
+                if (!ok) break;
+                mma_halves(tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[i % Sh::kK]), o_shape, !(e & kFirst));
+                mma_commit(&sh.k_empty[i % Sh::kK]);
+                if (e & kLast) mma_commit(&sh.acc_done);
+                if (more) more = issue_s();
+            }
+            mma_commit(&sh.drained);
+            mbar_wait_bounded(&sh.drained, 0);
+        }
+    } else if (warp >= 4 && *stop == 0) {
+        // ------------------------------------------------------------- scores to dS
+        const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const float c = p.scale * 1.4426950408889634f;
+        int4 r = make_int4(0, 0, 0, 0);
+        float lse2 = INFINITY, delta = 0.0f;
+        uint32_t done = 0;
+        bool spoiled = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+            const int4 e = sh.info[slot];
+            const uint32_t flags = static_cast<uint32_t>(e.y);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+            if (flags & kStop) break;
+            const DqItem d = dq_item(p, static_cast<int64_t>(e.w) << 32 | static_cast<uint32_t>(e.z), row_tiles);
+            const int64_t row = d.rank * p.Tp + d.row0 + t;
+            const bool valid = d.row0 + t < p.Tp;
+            if (flags & kFirst) {
+                r = make_int4(0, 0, 0, 0);
+                lse2 = INFINITY;
+                delta = 0.0f;
+                if (valid) {
+                    r = b.spans[row];
+                    lse2 = b.lse2[d.head * p.Tpad + row];
+                    delta = b.delta[d.head * p.Tpad + row];
+                }
+            }
+            if (!wait(&sh.dp_ready, n & 1)) break;
+            tmem_fence_after();
+            const uint32_t s_at = at + 128 * (n & 1) + 64 * y, dp_at = at + 256 + 64 * y;
+            uint32_t s[2][32], dp[2][32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_load32(s_at + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_load32(dp_at + 32 * i, dp[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                tmem_wait_loads(s[i]);
+                tmem_wait_loads(dp[i]);
+                const uint32_t bits = flags & kFull ? 0xFFFFFFFFu : visible_bits(r, e.x, 2 * y + i);
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    float ds[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float pr = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j + h]), c, -lse2));
+                        ds[h] = pr * (__uint_as_float(dp[i][2 * j + h]) - delta);
+                    }
+                    w[j] = pack_bf16x2(bits >> (2 * j) & 1 ? ds[0] : 0.0f, bits >> (2 * j + 1) & 1 ? ds[1] : 0.0f);
+                }
+                tmem_store16(s_at + 16 * i, w);
+            }
+            tmem_wait_stores();
+            tmem_fence_before();
+            mbar_arrive(&sh.ds_ready);
+            if (flags & kLast) {
+                if (!wait(&sh.acc_done, done++ & 1)) break;
+                tmem_fence_after();
+                float bad = 0.0f;
+                const bool write = valid && (r.y != 0 || r.w != 0);
+                uint16_t *out = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, d.head, p.D));
+                for (int i = y; i < steps; i += 2)
+                    store_columns(out, 16 * i, p.D, at + 384, p.scale, write, bad);
+                tmem_fence_before();
+                spoiled |= write && bad != 0.0f;
+            }
+        }
+        if (spoiled) sh.spoiled = 1;
+    }
+    __syncthreads();
+    if (warp == 2) tmem_free(tmem);
+    if (sh.stop != 0) {
+        if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
+        return;
+    }
+    if (sh.spoiled == 0) return;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const DqItem d = dq_item(p, it, row_tiles);
+        for (int i = warp; i < kTile && d.row0 + i < p.Tp; i += 12) {
+            const int64_t row = d.rank * p.Tp + d.row0 + i;
+            if (spoiled_row(row_of(b.dq, row, p.Hq, d.head, p.D), p.D)) row_dq(b, row, d.head);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- dK and dV
+//
+// An item is 128 keys of one kv head for one writer; K and V stay in shared
+// memory, the row tiles that see them (of every query head of the group) pass
+// by. Scores are transposed, so that P and dS are first operands in tensor
+// memory:
+//   S' = K Q^T, dP' = V dO^T, dV += P' dO, dK += dS' Q,
+// issued as dV(i) S(i+1) dK(i) dP(i+1): the matrix unit works on two products
+// while two warpgroups (64 row columns each, one thread per key) make P, and on
+// the other two while they make dS.
+// Tensor memory: S', dP', dV, dK. Shared memory: K, V, 3 Q, 2 dO.
+
+template <int DP>
+struct DkvShared {
+    static constexpr int kQ = 3, kO = 2;
+    uint8_t k[Shape<DP>::kTileBytes], v[Shape<DP>::kTileBytes];
+    uint8_t q[kQ][Shape<DP>::kTileBytes], dout[kO][Shape<DP>::kTileBytes];
+    float lse2[2][kTile], delta[2][kTile];
+    uint64_t kv_full, kv_empty;
+    uint64_t q_full[kQ], q_empty[kQ], do_full[kO], do_empty[kO];
+    uint64_t info_full[kRing], info_empty[kRing];
+    uint64_t aux_full[2], aux_empty[2];
+    uint64_t s_ready, p_ready, dp_ready, ds_ready, acc_done, drained;
+    int4 info[kRing];              // first row, flags and head, tile * P + rank
+    uint32_t tmem, stop, spoiled;
+};
+
+// Item i of the list: heads fastest, the long tiles first.
+__device__ __forceinline__ void dkv_item(const Params &b, int64_t i, int64_t slots, int front, int &entry, int &kvh)
+{
+    const int64_t at = i / b.a.Hkv;
+    kvh = static_cast<int>(i - at * b.a.Hkv);
+    entry = b.list[at < front ? at : slots - 1 - (at - front)];
+}
+
+template <int DP>
+__global__ void __launch_bounds__(384, 1)
+    dkdv_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t slots)
+{
+    typedef DkvShared<DP> Sh;
+    constexpr int kSlabs = Shape<DP>::kSlabs;
+    const AttentionParams &p = b.a;
+    extern __shared__ __align__(1024) uint8_t raw[];
+    Sh &sh = *reinterpret_cast<Sh *>(raw);
+    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (threadIdx.x == 0) {
+        mbar_init(&sh.kv_full, 1);
+        mbar_init(&sh.kv_empty, 1);
+        for (int i = 0; i < Sh::kQ; ++i) {
+            mbar_init(&sh.q_full[i], 1);
+            mbar_init(&sh.q_empty[i], 1);
+        }
+        for (int i = 0; i < Sh::kO; ++i) {
+            mbar_init(&sh.do_full[i], 1);
+            mbar_init(&sh.do_empty[i], 1);
+        }
+        for (int i = 0; i < kRing; ++i) {
+            mbar_init(&sh.info_full[i], 1);
+            mbar_init(&sh.info_empty[i], 11);     // issuer, 2 statistics warps, 8 warps
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.aux_full[i], 64);
+            mbar_init(&sh.aux_empty[i], 8);
+        }
+        mbar_init(&sh.s_ready, 1);
+        mbar_init(&sh.p_ready, 2 * kTile);
+        mbar_init(&sh.dp_ready, 1);
+        mbar_init(&sh.ds_ready, 2 * kTile);
+        mbar_init(&sh.acc_done, 1);
+        mbar_init(&sh.drained, 1);
+        sh.spoiled = 0;
+        sh.stop = smem_addr(raw) & 1023 ? 1 : 0;
+        mbar_init_fence();
+    }
+    tmem_fence_before();
+    __syncthreads();
+    tmem_fence_after();
+    const uint32_t tmem = sh.tmem;
+    volatile uint32_t *stop = &sh.stop;
+    const int steps = (p.D + 15) / 16, group = p.Hq / p.Hkv;
+    const int front = b.counters[0];
+    const int64_t items = static_cast<int64_t>(front + b.counters[1]) * p.Hkv;
+
+    if (warp == 0 && *stop == 0) {
+        // ------------------------------------------------------------- loader
+        uint32_t n = 0, k = 0;                 // tiles, items
+        uint32_t nq = 0, no = 0, nkv = 0;      // loads issued
+        bool ok = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+            return ok;
+        };
+        auto announce = [&](int row, uint32_t flags, int entry) {
+            const uint32_t s = n % kRing;
+            if (wait(&sh.info_empty[s], (n / kRing & 1) ^ 1) && lane == 0) {
+                sh.info[s] = make_int4(row, static_cast<int>(flags), entry, 0);
+                mbar_arrive(&sh.info_full[s]);
+            }
+            return ok;
+        };
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++k) {
+            int entry, kvh;
+            dkv_item(b, it, slots, front, entry, kvh);
+            const int4 range = b.ranges[entry];
+            const int rank = entry % p.P, key = entry / p.P * kTile;
+            const int64_t base = rank * p.Tp;
+            bool loaded = false;
+            for (int h = 0; ok && h < group; ++h) {
+                const int head = kvh * group + h;
+                int from = range.x, to = range.y;
+                while (ok) {
+                    // whether all rows see all keys, and whether some are not rows of this rank
+                    bool full = true, dirty = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int64_t row = from + lane + 32 * i;
+                        const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
+                        full &= (r.x <= key && r.y >= key + kTile) || (r.z <= key && r.w >= key + kTile);
+                        dirty |= r.y == 0 && r.w == 0;
+                    }
+                    uint32_t flags = static_cast<uint32_t>(head) << 16;
+                    if (__all_sync(0xFFFFFFFFu, full)) flags |= kFull;
+                    if (__any_sync(0xFFFFFFFFu, dirty)) flags |= kDirty;
+                    if (!loaded) flags |= kFirst;
+                    const int row0 = from;
+                    from += kTile;
+                    bool end = from >= to;
+                    if (end && to == range.y && range.w > from) {
+                        // the last tile may have reached into the second range
+                        from = max(from, range.z);
+                        to = range.w;
+                        end = false;
+                    }
+                    if (end && h == group - 1) flags |= kLast;
+                    if (!announce(row0, flags, entry)) break;
+                    if (!loaded) {
+                        if (!wait(&sh.kv_empty, (k & 1) ^ 1)) break;
+                        if (lane == 0) {
+                            mbar_expect_tx(&sh.kv_full, 2 * kSlabs * kSlab);
+                            for (int i = 0; i < kSlabs; ++i) {
+                                tma_slab(smem_addr(sh.k) + i * kSlab, &maps.k, 64 * i, kvh, key, &sh.kv_full);
+                                tma_slab(smem_addr(sh.v) + i * kSlab, &maps.v, 64 * i, kvh, key, &sh.kv_full);
+                            }
+                        }
+                        loaded = true;
+                        ++nkv;
+                    }
+                    const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
+                    if (!wait(&sh.q_empty[qs], (n / Sh::kQ & 1) ^ 1)) break;
+                    if (lane == 0) load_tile(&maps.q, smem_addr(sh.q[qs]), kSlabs, head, base + row0, &sh.q_full[qs]);
+                    ++nq;
+                    if (!wait(&sh.do_empty[os], (n / Sh::kO & 1) ^ 1)) break;
+                    if (lane == 0)
+                        load_tile(&maps.dout, smem_addr(sh.dout[os]), kSlabs, head, base + row0, &sh.do_full[os]);
+                    ++no;
+                    ++n;
+                    if (end) break;
+                }
+            }
+        }
+        if (ok) announce(0, kStop, 0);
+        if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
+            for (uint32_t i = nq > Sh::kQ ? nq - Sh::kQ : 0; i < nq; ++i)
+                mbar_wait_bounded(&sh.q_full[i % Sh::kQ], i / Sh::kQ & 1);
+            for (uint32_t i = no > Sh::kO ? no - Sh::kO : 0; i < no; ++i)
+                mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
+            if (nkv > 0) mbar_wait_bounded(&sh.kv_full, (nkv - 1) & 1);
+        }
+    } else if (warp == 1 && *stop == 0) {
+        // ------------------------------------------------------------- issuer
+        if (lane == 0) {
+            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+            uint32_t prev = 0, k = 0;   // flags of the last tile, items begun
+            bool ok = true;
+            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait_or_stop(bar, parity, stop); };
+            const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
+            for (uint32_t n = 0; ok; ++n) {
+                const uint32_t slot = n % kRing;
+                if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+                const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
+                mbar_arrive(&sh.info_empty[slot]);
+                const uint32_t i = n - 1, qp = i % Sh::kQ, op = i % Sh::kO, qs = n % Sh::kQ, os = n % Sh::kO;
+                auto dv = [&]() {
+                    if (!wait(&sh.p_ready, i & 1)) return;
+                    tmem_fence_after();
+                    mma_halves(dv_at, s_at, smem_addr(sh.dout[op]), o_shape, !(prev & kFirst));
+                    mma_commit(&sh.do_empty[op]);
+                };
+                auto dk = [&]() {
+                    if (!wait(&sh.ds_ready, i & 1)) return;
+                    tmem_fence_after();
+                    mma_halves(dk_at, dp_at, smem_addr(sh.q[qp]), o_shape, !(prev & kFirst));
+                    mma_commit(&sh.q_empty[qp]);
+                    if (prev & kLast) mma_commit(&sh.acc_done);
+                };
+                // a new item's K and V may wait for the last one's: its products go first
+                const bool fresh = (e & (kFirst | kStop)) != 0;
+                if (n > 0) dv();
+                if (n > 0 && fresh && ok) dk();
+                if (ok && !(e & kStop)) {
+                    if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
+                    if (!wait(&sh.q_full[qs], n / Sh::kQ & 1)) break;
+                    mma_scores(s_at, smem_addr(sh.k), smem_addr(sh.q[qs]), s_shape, steps);
+                    mma_commit(&sh.s_ready);
+                }
+                if (n > 0 && !fresh && ok) dk();
+                if (!ok || (e & kStop)) break;
+                if (!wait(&sh.do_full[os], n / Sh::kO & 1)) break;
+                mma_scores(dp_at, smem_addr(sh.v), smem_addr(sh.dout[os]), s_shape, steps);
+                mma_commit(&sh.dp_ready);
+                if (e & kLast) mma_commit(&sh.kv_empty);
+                prev = e;
+            }
+            mma_commit(&sh.drained);
+            mbar_wait_bounded(&sh.drained, 0);
+        }
+    } else if (warp < 4 && *stop == 0) {
+        // ------------------------------------------------------------- statistics of the rows
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing, s = n & 1;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_full[slot], n / kRing & 1, stop))) break;
+            const int4 e = sh.info[slot];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+            if (e.y & kStop) break;
+            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.aux_empty[s], (n / 2 & 1) ^ 1, stop))) break;
+            const int64_t base = static_cast<int64_t>(e.y >> 16) * p.Tpad + e.z % p.P * p.Tp;
+            for (int i = threadIdx.x - 64; i < kTile; i += 64) {
+                const int64_t row = e.x + i;
+                const bool in = row < p.Tp;
+                sh.lse2[s][i] = in ? b.lse2[base + row] : INFINITY;
+                sh.delta[s][i] = in ? b.delta[base + row] : 0.0f;
+            }
+            mbar_arrive(&sh.aux_full[s]);
+        }
+    } else if (warp >= 4 && *stop == 0) {
+        // ------------------------------------------------------------- scores to P and dS
+        const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
+        const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
+        const uint32_t s_at = at + 64 * y, dp_at = at + 128 + 64 * y;
+        const float c = p.scale * 1.4426950408889634f;
+        uint32_t done = 0;
+        bool spoiled = false;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing, a = n & 1;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+            const int4 e = sh.info[slot];
+            const uint32_t flags = static_cast<uint32_t>(e.y);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
+            if (flags & kStop) break;
+            const int rank = e.z % p.P, key = e.z / p.P * kTile;
+            const int64_t base = rank * p.Tp;
+            // bit j of bits[i]: whether this thread's key is seen by row 64 y + 32 i + j
+            uint32_t bits[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            if (!(flags & kFull)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int64_t row = e.x + 64 * y + 32 * i + lane;
+                    const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
+                    bits[i] = transpose_bits(visible_bits(r, key, warp & 3));
+                }
+            }
+            if (!wait(&sh.aux_full[a], n / 2 & 1)) break;
+            if (!wait(&sh.s_ready, n & 1)) break;
+            if (flags & kDirty) {
+                // Rows that are not this rank's, or padding, may hold anything: a weight of zero does
+                // not keep a NaN out of a product, so they become zeros.
+                if (!wait(&sh.dp_ready, n & 1)) break;
+                const int64_t row = e.x + t;
+                const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
+                if (r.y == 0 && r.w == 0) {
+                    uint8_t *tile = y == 0 ? sh.dout[n % Sh::kO] : sh.q[n % Sh::kQ];
+                    for (int i = 0; i < kSlabs; ++i)
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4 *>(tile + i * kSlab + t * 128 + j * 16) = make_uint4(0, 0, 0, 0);
+                }
+                fence_proxy_async_smem();
+            }
+            tmem_fence_after();
+            uint32_t s[2][32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_load32(s_at + 32 * i, s[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                tmem_wait_loads(s[i]);
+                const float4 *l4 = reinterpret_cast<const float4 *>(&sh.lse2[a][64 * y + 32 * i]);
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 l = l4[j];
+                    const float ls[4] = {l.x, l.y, l.z, l.w};
+                    float pr[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        pr[h] = exp2_fast(__fmaf_rn(__uint_as_float(s[i][4 * j + h]), c, -ls[h]));
+                        pr[h] = bits[i] >> (4 * j + h) & 1 ? pr[h] : 0.0f;
+                        s[i][4 * j + h] = __float_as_uint(pr[h]);
+                    }
+                    w[2 * j] = pack_bf16x2(pr[0], pr[1]);
+                    w[2 * j + 1] = pack_bf16x2(pr[2], pr[3]);
+                }
+                tmem_store16(s_at + 16 * i, w);
+            }
+            tmem_wait_stores();
+            tmem_fence_before();
+            mbar_arrive(&sh.p_ready);
+            if (!wait(&sh.dp_ready, n & 1)) break;
+            tmem_fence_after();
+            uint32_t dp[2][32];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_load32(dp_at + 32 * i, dp[i]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                tmem_wait_loads(dp[i]);
+                const float4 *d4 = reinterpret_cast<const float4 *>(&sh.delta[a][64 * y + 32 * i]);
+                uint32_t w[16];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float4 l = d4[j];
+                    const float de[4] = {l.x, l.y, l.z, l.w};
+                    float ds[4];
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) {
+                        ds[h] = __uint_as_float(s[i][4 * j + h]) * (__uint_as_float(dp[i][4 * j + h]) - de[h]);
+                        ds[h] = bits[i] >> (4 * j + h) & 1 ? ds[h] : 0.0f;
+                    }
+                    w[2 * j] = pack_bf16x2(ds[0], ds[1]);
+                    w[2 * j + 1] = pack_bf16x2(ds[2], ds[3]);
+                }
+                tmem_store16(dp_at + 16 * i, w);
+            }
+            tmem_wait_stores();
+            tmem_fence_before();
+            mbar_arrive(&sh.ds_ready);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.aux_empty[a]);
+            if (flags & kLast) {
+                const int32_t pos = key + t < p.T ? position_of_token(b, key + t) : -1;
+                const int kvh = static_cast<int>(flags >> 16) / group;
+                if (!wait(&sh.acc_done, done++ & 1)) break;
+                tmem_fence_after();
+                float bad = 0.0f;
+                uint16_t *out = const_cast<uint16_t *>(row_of(y == 0 ? b.dv[rank] : b.dk[rank], pos, p.Hkv, kvh, p.D));
+                for (int i = 0; i < steps; ++i)
+                    store_columns(out, 16 * i, p.D, at + (y == 0 ? 256 : 384), y == 0 ? 1.0f : p.scale, pos >= 0, bad);
+                tmem_fence_before();
+                spoiled |= pos >= 0 && bad != 0.0f;
+            }
+        }
+        if (spoiled) sh.spoiled = 1;
+    }
+    __syncthreads();
+    if (warp == 2) tmem_free(tmem);
+    if (sh.stop != 0) {
+        if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
+        return;
+    }
+    if (sh.spoiled == 0) return;
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        int entry, kvh;
+        dkv_item(b, it, slots, front, entry, kvh);
+        const int rank = entry % p.P, key = entry / p.P * kTile;
+        for (int i = warp; i < kTile && key + i < p.T; i += 12) {
+            const int32_t pos = position_of_token(b, key + i);
+            if (pos < 0) continue;
+            if (spoiled_row(row_of(b.dk[rank], pos, p.Hkv, kvh, p.D), p.D) ||
+                spoiled_row(row_of(b.dv[rank], pos, p.Hkv, kvh, p.D), p.D))
+                key_dkdv(b, key + i, rank, kvh);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- launch
+
+template <int DP>
+cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStream_t stream)
+{
+    const AttentionParams &p = b.a;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    static std::atomic<bool> attr_set[64];
+    if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
+        e = cudaFuncSetAttribute(dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DqShared<DP>));
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(dkdv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DkvShared<DP>));
+        if (e != cudaSuccess) return e;
+        if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
+    }
+    const int64_t sms = sm_count(dev), row_tiles = (p.Tp + kTile - 1) / kTile, items = row_tiles * p.P * p.Hq;
+    dq_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), 384, sizeof(DqShared<DP>), stream>>>(
+        b, maps, items, row_tiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    const int64_t slots = static_cast<int64_t>(tiles) * p.P, most = slots * p.Hkv;
+    dkdv_kernel<DP><<<static_cast<unsigned>(most < sms ? most : sms), 384, sizeof(DkvShared<DP>), stream>>>(b, maps,
+                                                                                                         slots);
+    return cudaGetLastError();
+}
+
+int64_t align256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
+
 }  // namespace
 
-cudaError_t launch_attention_backward(const AttentionBackwardParams &b, cudaStream_t stream)
+// delta and lse2 of every (head, row), the spans of every row, the ranges and
+// the list of every (tile, rank), two counters.
+int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq)
+{
+    const int64_t slots = (T + kTile - 1) / kTile * P;
+    return 2 * align256(4 * Tpad * Hq) + align256(16 * Tpad) + align256(16 * slots) + align256(4 * slots) + 256;
+}
+
+cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace, cudaStream_t stream)
 {
     const AttentionParams &p = b.a;
     if (p.Tpad == 0) return cudaSuccess;
-    const int64_t rows = (p.Tpad * p.Hq + kWarps - 1) / kWarps;
-    const int64_t keys = (p.Tpad * p.Hkv * p.P + kWarps - 1) / kWarps;
-    if (rows > 0x7FFFFFFF || keys > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    delta_kernel<<<static_cast<unsigned>(rows), 32 * kWarps, 0, stream>>>(b);
-    dq_rows_kernel<<<static_cast<unsigned>(rows), 32 * kWarps, 0, stream>>>(b);
-    dkdv_rows_kernel<<<static_cast<unsigned>(keys), 32 * kWarps, 0, stream>>>(b);
-    return cudaGetLastError();
+    const int tiles = static_cast<int>((p.T + kTile - 1) / kTile);
+    const int64_t slots = static_cast<int64_t>(tiles) * p.P;
+    uint8_t *w = static_cast<uint8_t *>(workspace);
+    b.delta = reinterpret_cast<float *>(w);
+    w += align256(4 * p.Tpad * p.Hq);
+    b.lse2 = reinterpret_cast<float *>(w);
+    w += align256(4 * p.Tpad * p.Hq);
+    b.spans = reinterpret_cast<int4 *>(w);
+    w += align256(16 * p.Tpad);
+    b.ranges = reinterpret_cast<int4 *>(w);
+    w += align256(16 * slots);
+    b.list = reinterpret_cast<int32_t *>(w);
+    w += align256(4 * slots);
+    b.counters = reinterpret_cast<int32_t *>(w);
+    Maps maps;
+    cudaError_t e = make_slab_map(&maps.q, p.q, p.D, p.Hq, p.Tpad);
+    if (e == cudaSuccess) e = make_slab_map(&maps.k, p.k, p.D, p.Hkv, p.T);
+    if (e == cudaSuccess) e = make_slab_map(&maps.v, p.v, p.D, p.Hkv, p.T);
+    if (e == cudaSuccess) e = make_slab_map(&maps.dout, b.dout, p.D, p.Hq, p.Tpad);
+    if (e != cudaSuccess) return e;
+    const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * p.Hq;
+    if (row_blocks > 0x7FFFFFFF || slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if ((e = cudaMemsetAsync(b.counters, 0, 8, stream)) != cudaSuccess) return e;
+    rows_kernel<<<static_cast<unsigned>(row_blocks), 8 * kPrepRows, 0, stream>>>(b);
+    tiles_kernel<<<static_cast<unsigned>(slots), 256, 0, stream>>>(b, tiles);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    return p.D <= 64 ? launch_tiled<64>(b, maps, tiles, stream) : launch_tiled<128>(b, maps, tiles, stream);
 }
 
 cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset)
 {
     return read_bounds_counter(count, reset);
+}
+
+cudaError_t read_attention_backward_wait_timeouts(unsigned int *count, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned int));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 }  // namespace cpt

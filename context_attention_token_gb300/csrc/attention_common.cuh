@@ -39,6 +39,33 @@ __device__ __forceinline__ RowKeys keys_of_token(const AttentionParams &p, int32
     return r;
 }
 
+// The same as up to two spans [x, y) and [z, w) of tokens in ascending order,
+// (0, 0) when empty, one span alone in the second place.
+__device__ __forceinline__ int4 spans_of(const AttentionParams &p, int32_t g)
+{
+    const RowKeys k = keys_of_token(p, g);
+    int4 r = make_int4(0, 0, 0, 0);
+    if (k.ns > 0) {
+        r.x = k.kb;
+        r.y = k.kb + k.ns;
+    }
+    if (k.lo <= g) {
+        r.z = k.lo;
+        r.w = g + 1;
+        if (r.y == r.z && k.ns > 0) {
+            r.z = r.x;
+            r.x = r.y = 0;
+        }
+    }
+    return r;
+}
+
+// First key >= x of a row's spans; the largest int when there is none.
+__device__ __forceinline__ int next_key(int4 r, int x)
+{
+    return x < r.y ? max(x, r.x) : (x < r.w ? max(x, r.z) : 0x7FFFFFFF);
+}
+
 // Raw token of a local row; -1 for padding (and for an entry that fails its check).
 __device__ __forceinline__ int32_t token_of_row(const AttentionParams &p, int64_t row)
 {

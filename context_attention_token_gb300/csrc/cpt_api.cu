@@ -1086,14 +1086,15 @@ cpt_status cpt_kernel_wait_timeouts(uint32_t *count, int32_t reset)
     if (count == nullptr) return fail(CPT_ERR_INVALID_ARG, "NULL argument");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0;
+    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0, u = 0;
     cudaError_t e = read_wait_timeouts(&v, reset != 0);
     if (e == cudaSuccess) e = read_slot_reduce_wait_timeouts(&w, reset != 0);
     if (e == cudaSuccess) e = read_gather_wait_timeouts(&x, reset != 0);
     if (e == cudaSuccess) e = read_ceiling_wait_timeouts(&y, reset != 0);
     if (e == cudaSuccess) e = read_attention_wait_timeouts(&z, reset != 0);
+    if (e == cudaSuccess) e = read_attention_backward_wait_timeouts(&u, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "wait-timeout counter read");
-    *count = v + w + x + y + z;
+    *count = v + w + x + y + z + u;
     return CPT_OK;
 }
 
@@ -1360,7 +1361,7 @@ void fill_attention(AttentionParams &p, const cpt_plan *plan, const void *q, con
 
 size_t backward_workspace(const cpt_plan *plan, int32_t q_heads)
 {
-    return align256(sizeof(float) * (size_t)q_heads * (size_t)plan->Tpad);
+    return (size_t)attention_backward_workspace(plan->T, plan->Tpad, plan->P, q_heads);
 }
 
 }  // namespace
@@ -1461,9 +1462,11 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
     p.dout = dout;
     p.dq = dq;
     p.g2l = plan->g2l;
+    p.l2g = plan->l2g;
+    p.r2l = plan->r2l;
     p.cup = plan->cup;
-    p.delta = static_cast<float *>(workspace);
-    cudaError_t e = launch_attention_backward(p, static_cast<cudaStream_t>(stream));
+    p.packed = plan->layout == CPT_LAYOUT_PACKED_CONTIGUOUS;
+    cudaError_t e = launch_attention_backward(p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CPT_OK : cuda_fail(e, "attention backward launch");
 }
 

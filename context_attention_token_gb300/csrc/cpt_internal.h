@@ -166,10 +166,19 @@ struct AttentionBackwardParams {
     void *dq;                      // bf16 [Tpad][Hq][D]
     void *dk[kMaxCp], *dv[kMaxCp]; // writer r's bf16 [Tpad][Hkv][D]
     const int32_t *g2l;            // local row of every (padded) global position
+    const int32_t *l2g;            // and back
+    const int32_t *r2l;            // local row of every raw token (nullptr: position = token)
     const int32_t *cup;            // padded document boundaries [n_docs + 1]
-    float *delta;                  // workspace [Hq][Tpad]
+    bool packed;                   // packed-contiguous ownership
+    // in the workspace, set by the launcher
+    float *delta, *lse2;           // [Hq][Tpad]
+    int4 *spans;                   // [Tpad] keys every row sees
+    int4 *ranges;                  // [key tiles][P] rows that see a tile
+    int32_t *list, *counters;      // tiles that some row sees
 };
-cudaError_t launch_attention_backward(const AttentionBackwardParams &p, cudaStream_t stream);
+int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq);
+cudaError_t launch_attention_backward(AttentionBackwardParams p, void *workspace, cudaStream_t stream);
+cudaError_t read_attention_backward_wait_timeouts(unsigned int *count, bool reset);
 
 // Streaming ceiling: dst = copy of srcs[0], srcs[1..n_src) read and
 // discarded, through the bulk-copy engine in blocks of block_bytes and a ring
