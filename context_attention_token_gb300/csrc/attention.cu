@@ -88,7 +88,7 @@ struct Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t rows_full[2], rows_empty[2];
-    uint64_t s_ready[2], p_ready[2], pv_done[2], drained;
+    uint64_t s_ready[2], p_half[2], p_ready[2], pv_done[2], drained;
     int2 info[kRing];                  // first key, flags
     int4 rows[2][2][kTile];            // two visible spans of every row of an item
     uint32_t tmem;
@@ -148,6 +148,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&sh.rows_full[i], 64);
             mbar_init(&sh.rows_empty[i], 9);     // loader, 8 softmax warps
             mbar_init(&sh.s_ready[i], 1);
+            mbar_init(&sh.p_half[i], kTile);
             mbar_init(&sh.p_ready[i], kTile);
             mbar_init(&sh.pv_done[i], 1);
         }
@@ -163,6 +164,9 @@ __global__ void __launch_bounds__(384, 1)
     const int group = p.Hq / p.Hkv;
     const int steps = (p.D + 15) / 16;
 
+    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    if (warp < 4) {
+    fewer_registers<96>();
     if (warp == 0) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, c = 0, k = 0;   // announcements, ring loads, items
@@ -278,13 +282,17 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (prev & (kNeed << x)) {
+                        if (!(ok = mbar_wait_or_stop(&sh.p_half[x], ps[x] & 1, stop))) break;
+                        tmem_fence_after();
+                        const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
+                        for (int k = 0; k < 4; ++k)
+                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape,
+                                     started[x] || k > 0);
                         if (!(ok = mbar_wait_or_stop(&sh.p_ready[x], ps[x] & 1, stop))) break;
                         ++ps[x];
                         tmem_fence_after();
-                        const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
-                        for (int k = 0; k < kTile / 16; ++k)
-                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape,
-                                     started[x] || k > 0);
+                        for (int k = 4; k < 8; ++k)
+                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape, true);
                         started[x] = true;
                         mma_commit(&sh.pv_done[x]);
                     }
@@ -312,7 +320,7 @@ __global__ void __launch_bounds__(384, 1)
             mma_commit(&sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
-    } else if (warp < 4) {
+    } else {
         // ------------------------------------------------------------- rows
         uint32_t k = 0;
         for (int64_t it = blockIdx.x; it < items; it += gridDim.x, ++k) {
@@ -327,7 +335,9 @@ __global__ void __launch_bounds__(384, 1)
             }
             mbar_arrive(&sh.rows_full[b]);
         }
+    }
     } else {
+        more_registers<200>();
         // ------------------------------------------------------------- softmax
         const int x = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
@@ -377,11 +387,15 @@ __global__ void __launch_bounds__(384, 1)
                             if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
                     }
                 }
-                float mx = __uint_as_float(s[0][0]);
+                float top[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < 4; ++i) {
+                    top[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(s[i][j]));
+                    for (int j = 2; j < 32; j += 2)
+                        top[i] = fmaxf(top[i], fmaxf(__uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1])));
+                }
+                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                 mx = fmaxf(m, mx);
                 // The maximum in use may lag behind by a factor of 2^8 in the weights: binary32 sums
                 // have the room, and O is rarely read back to be scaled.
@@ -403,22 +417,28 @@ __global__ void __launch_bounds__(384, 1)
                     }
                 }
                 const float mc = m == -INFINITY ? 0.0f : m * c;
-                float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                const F2 c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
+                F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float a = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j]), c, -mc));
-                        const float b = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j + 1]), c, -mc));
-                        sum[j & 1] += a;
-                        sum[2 + (j & 1)] += b;
+                        const float2 a = both(fma2(pair_of(s[i][2 * j], s[i][2 * j + 1]), c2, mc2));
+                        const float x0 = exp2_fast(a.x), x1 = exp2_fast(a.y);
+                        sum[j & 1] = add2(sum[j & 1], pair_of(x0, x1));
                         // weights are rounded to bf16 for the matrix instruction; their sum is not
-                        w[j] = pack_bf16x2(a, b);
+                        w[j] = pack_bf16x2(x0, x1);
                     }
                     tmem_store16(s_at + 16 * i, w);
+                    if (i == 1) {   // the product can begin with the first 64 keys
+                        tmem_wait_stores();
+                        tmem_fence_before();
+                        mbar_arrive(&sh.p_half[x]);
+                    }
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                const float2 total = both(add2(sum[0], sum[1]));
+                l += total.x + total.y;
                 tmem_wait_stores();
                 tmem_fence_before();
                 mbar_arrive(&sh.p_ready[x]);

@@ -315,7 +315,7 @@ struct DqShared {
     uint64_t q_full, q_empty, do_full, do_empty;
     uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
     uint64_t info_full[kRing], info_empty[kRing];
-    uint64_t dp_ready, ds_ready, acc_done, drained;
+    uint64_t dp_ready, dp_free, ds_ready, acc_done, drained;
     int4 info[kRing];              // first key, flags, item
     uint32_t tmem, stop, spoiled;
 };
@@ -364,6 +364,7 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&sh.info_empty[i], 9);      // issuer, 8 warps
         }
         mbar_init(&sh.dp_ready, 1);
+        mbar_init(&sh.dp_free, 2 * kTile);
         mbar_init(&sh.ds_ready, 2 * kTile);
         mbar_init(&sh.acc_done, 1);
         mbar_init(&sh.drained, 1);
@@ -377,7 +378,9 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = (p.D + 15) / 16;
-
+    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    if (warp < 4) {
+    fewer_registers<96>();
     if (warp == 0 && *stop == 0) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, k = 0;                    // tiles, items
@@ -490,11 +493,14 @@ __global__ void __launch_bounds__(384, 1)
                 if (ok) issue_dp();
             }
             for (uint32_t i = 0; ok && i < np; ++i) {
+                if (np < ns) {   // dP's columns are in registers long before dS is made of them
+                    if (!wait(&sh.dp_free, i & 1)) break;
+                    tmem_fence_after();
+                    issue_dp();
+                }
                 if (!wait(&sh.ds_ready, i & 1)) break;
                 tmem_fence_after();
                 const uint32_t e = flags[i & 1];
-                if (np < ns) issue_dp();
-                if (!ok) break;
                 mma_halves(tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[i % Sh::kK]), o_shape, !(e & kFirst));
                 mma_commit(&sh.k_empty[i % Sh::kK]);
                 if (e & kLast) mma_commit(&sh.acc_done);
@@ -503,7 +509,9 @@ __global__ void __launch_bounds__(384, 1)
             mma_commit(&sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
-    } else if (warp >= 4 && *stop == 0) {
+    }
+    } else {
+        more_registers<200>();
         // ------------------------------------------------------------- scores to dS
         const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -515,7 +523,7 @@ __global__ void __launch_bounds__(384, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
         };
-        for (uint32_t n = 0;; ++n) {
+        for (uint32_t n = 0; *stop == 0; ++n) {
             const uint32_t slot = n % kRing;
             if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int4 e = sh.info[slot];
@@ -548,17 +556,28 @@ __global__ void __launch_bounds__(384, 1)
             for (int i = 0; i < 2; ++i) {
                 tmem_wait_loads(s[i]);
                 tmem_wait_loads(dp[i]);
-                const uint32_t bits = flags & kFull ? 0xFFFFFFFFu : visible_bits(r, e.x, 2 * y + i);
+            }
+            tmem_fence_before();
+            mbar_arrive(&sh.dp_free);
+            if (!(flags & kFull)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t bits = visible_bits(r, e.x, 2 * y + i);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
+                }
+            }
+            const F2 c2 = pair_of(c, c), lse22 = pair_of(-lse2, -lse2), delta2 = pair_of(-delta, -delta);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
                 uint32_t w[16];
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {
-                    float ds[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const float pr = exp2_fast(__fmaf_rn(__uint_as_float(s[i][2 * j + h]), c, -lse2));
-                        ds[h] = pr * (__uint_as_float(dp[i][2 * j + h]) - delta);
-                    }
-                    w[j] = pack_bf16x2(bits >> (2 * j) & 1 ? ds[0] : 0.0f, bits >> (2 * j + 1) & 1 ? ds[1] : 0.0f);
+                    const float2 a = both(fma2(pair_of(s[i][2 * j], s[i][2 * j + 1]), c2, lse22));
+                    const F2 pr = pair_of(exp2_fast(a.x), exp2_fast(a.y));
+                    const float2 ds = both(mul2(pr, add2(pair_of(dp[i][2 * j], dp[i][2 * j + 1]), delta2)));
+                    w[j] = pack_bf16x2(ds.x, ds.y);
                 }
                 tmem_store16(s_at + 16 * i, w);
             }
@@ -678,7 +697,9 @@ __global__ void __launch_bounds__(384, 1)
     const int steps = (p.D + 15) / 16, group = p.Hq / p.Hkv;
     const int front = b.counters[0];
     const int64_t items = static_cast<int64_t>(front + b.counters[1]) * p.Hkv;
-
+    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    if (warp < 4) {
+    fewer_registers<96>();
     if (warp == 0 && *stop == 0) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, k = 0;                 // tiles, items
@@ -812,7 +833,7 @@ __global__ void __launch_bounds__(384, 1)
             mma_commit(&sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
-    } else if (warp < 4 && *stop == 0) {
+    } else if (warp > 1 && *stop == 0) {
         // ------------------------------------------------------------- statistics of the rows
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing, s = n & 1;
@@ -826,12 +847,14 @@ __global__ void __launch_bounds__(384, 1)
             for (int i = threadIdx.x - 64; i < kTile; i += 64) {
                 const int64_t row = e.x + i;
                 const bool in = row < p.Tp;
-                sh.lse2[s][i] = in ? b.lse2[base + row] : INFINITY;
-                sh.delta[s][i] = in ? b.delta[base + row] : 0.0f;
+                sh.lse2[s][i] = in ? -b.lse2[base + row] : -INFINITY;   // negated, as they are added
+                sh.delta[s][i] = in ? -b.delta[base + row] : 0.0f;
             }
             mbar_arrive(&sh.aux_full[s]);
         }
-    } else if (warp >= 4 && *stop == 0) {
+    }
+    } else {
+        more_registers<200>();
         // ------------------------------------------------------------- scores to P and dS
         const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -842,7 +865,7 @@ __global__ void __launch_bounds__(384, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
         };
-        for (uint32_t n = 0;; ++n) {
+        for (uint32_t n = 0; *stop == 0; ++n) {
             const uint32_t slot = n % kRing, a = n & 1;
             if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int4 e = sh.info[slot];
@@ -883,23 +906,29 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) tmem_load32(s_at + 32 * i, s[i]);
 #pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_wait_loads(s[i]);
+            if (!(flags & kFull)) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!(bits[i] >> j & 1)) s[i][j] = 0xFF800000u;
+            }
+            const F2 c2 = pair_of(c, c);
+#pragma unroll
             for (int i = 0; i < 2; ++i) {
-                tmem_wait_loads(s[i]);
                 const float4 *l4 = reinterpret_cast<const float4 *>(&sh.lse2[a][64 * y + 32 * i]);
                 uint32_t w[16];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float4 l = l4[j];
-                    const float ls[4] = {l.x, l.y, l.z, l.w};
-                    float pr[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        pr[h] = exp2_fast(__fmaf_rn(__uint_as_float(s[i][4 * j + h]), c, -ls[h]));
-                        pr[h] = bits[i] >> (4 * j + h) & 1 ? pr[h] : 0.0f;
-                        s[i][4 * j + h] = __float_as_uint(pr[h]);
-                    }
+                    const float4 l = l4[j];   // negated
+                    const float2 u = both(fma2(pair_of(s[i][4 * j], s[i][4 * j + 1]), c2, pair_of(l.x, l.y)));
+                    const float2 v = both(fma2(pair_of(s[i][4 * j + 2], s[i][4 * j + 3]), c2, pair_of(l.z, l.w)));
+                    const float pr[4] = {exp2_fast(u.x), exp2_fast(u.y), exp2_fast(v.x), exp2_fast(v.y)};
                     w[2 * j] = pack_bf16x2(pr[0], pr[1]);
                     w[2 * j + 1] = pack_bf16x2(pr[2], pr[3]);
+#pragma unroll
+                    for (int h = 0; h < 4; ++h) s[i][4 * j + h] = __float_as_uint(pr[h]);
                 }
                 tmem_store16(s_at + 16 * i, w);
             }
@@ -912,22 +941,27 @@ __global__ void __launch_bounds__(384, 1)
 #pragma unroll
             for (int i = 0; i < 2; ++i) tmem_load32(dp_at + 32 * i, dp[i]);
 #pragma unroll
+            for (int i = 0; i < 2; ++i) tmem_wait_loads(dp[i]);
+            if (!(flags & kFull)) {   // a row that is none may have left a NaN
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!(bits[i] >> j & 1)) dp[i][j] = 0;
+            }
+#pragma unroll
             for (int i = 0; i < 2; ++i) {
-                tmem_wait_loads(dp[i]);
                 const float4 *d4 = reinterpret_cast<const float4 *>(&sh.delta[a][64 * y + 32 * i]);
                 uint32_t w[16];
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    const float4 l = d4[j];
-                    const float de[4] = {l.x, l.y, l.z, l.w};
-                    float ds[4];
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) {
-                        ds[h] = __uint_as_float(s[i][4 * j + h]) * (__uint_as_float(dp[i][4 * j + h]) - de[h]);
-                        ds[h] = bits[i] >> (4 * j + h) & 1 ? ds[h] : 0.0f;
-                    }
-                    w[2 * j] = pack_bf16x2(ds[0], ds[1]);
-                    w[2 * j + 1] = pack_bf16x2(ds[2], ds[3]);
+                    const float4 l = d4[j];   // negated
+                    const float2 u = both(mul2(pair_of(s[i][4 * j], s[i][4 * j + 1]),
+                                               add2(pair_of(dp[i][4 * j], dp[i][4 * j + 1]), pair_of(l.x, l.y))));
+                    const float2 v = both(mul2(pair_of(s[i][4 * j + 2], s[i][4 * j + 3]),
+                                               add2(pair_of(dp[i][4 * j + 2], dp[i][4 * j + 3]), pair_of(l.z, l.w))));
+                    w[2 * j] = pack_bf16x2(u.x, u.y);
+                    w[2 * j + 1] = pack_bf16x2(v.x, v.y);
                 }
                 tmem_store16(dp_at + 16 * i, w);
             }

@@ -195,6 +195,62 @@ __device__ __forceinline__ float exp2_fast(float x)
     return y;
 }
 
+// Two binary32 values in one register pair, and their arithmetic (round to
+// nearest): one issue slot for two elements.
+struct F2 {
+    uint64_t v;
+};
+
+__device__ __forceinline__ F2 pair_of(uint32_t a, uint32_t b)
+{
+    F2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ F2 pair_of(float a, float b) { return pair_of(__float_as_uint(a), __float_as_uint(b)); }
+
+__device__ __forceinline__ float2 both(F2 a)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c)
+{
+    F2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 add2(F2 a, F2 b)
+{
+    F2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+__device__ __forceinline__ F2 mul2(F2 a, F2 b)
+{
+    F2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+
+// Registers of a warpgroup: given back, or taken from what others gave back.
+template <int N>
+__device__ __forceinline__ void fewer_registers()
+{
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers()
+{
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // The bits of columns [lo, hi) of a 128-column tile in its 32-column word w.
 __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
 {
