@@ -285,14 +285,11 @@ __global__ void __launch_bounds__(384, 1)
                         if (!(ok = mbar_wait_or_stop(&sh.p_half[x], ps[x] & 1, stop))) break;
                         tmem_fence_after();
                         const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
-                        for (int k = 0; k < 4; ++k)
-                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape,
-                                     started[x] || k > 0);
+                        mma_weights<0, 4, 0>(tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, started[x]);
                         if (!(ok = mbar_wait_or_stop(&sh.p_ready[x], ps[x] & 1, stop))) break;
                         ++ps[x];
                         tmem_fence_after();
-                        for (int k = 4; k < 8; ++k)
-                            mma_tmem(tmem + 256 + 128 * x, tmem + 128 * x + 8 * k, desc_outer(v + 2048 * k), o_shape, true);
+                        mma_weights<4, 8, 0>(tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, true);
                         started[x] = true;
                         mma_commit(&sh.pv_done[x]);
                     }

@@ -243,13 +243,11 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
     for (int i = 0; i < slabs; ++i) tma_slab(to + i * kSlab, map, 64 * i, head, static_cast<int>(row), bar);
 }
 
-// D += A B, A [128 x 128] from tensor memory as two halves of 64 inner columns
-// (each over the first half of the columns of scores it came from), B read
-// across.
+// The weights of a tile lie as two halves of 64 inner columns, each over the
+// first half of the columns of scores that it came from.
 __device__ __forceinline__ void mma_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-    for (int k = 0; k < kTile / 16; ++k)
-        mma_tmem(d, a + (k >> 2) * 64 + (k & 3) * 8, desc_outer(b + 2048 * k), shape, add || k > 0);
+    mma_weights<0, 8, 32>(d, a, b, shape, add);
 }
 
 // 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)

@@ -62,14 +62,40 @@ __device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uin
         : "memory");
 }
 
-// Rows x columns of scores: both operands from shared memory, `steps` inner
-// steps of 16 (the second slab after four).
+// One thread issues every matrix instruction, so the loops are unrolled and
+// the descriptors advance by constants: with address arithmetic in the loop an
+// instruction took 100 cycles to issue, against 64 to run.
+
+// A descriptor as a value that the compiler does not look into: with nvcc 13.0 a
+// tile at a constant shared address got wrong bits once sums with it were
+// folded into constants.
+__device__ __forceinline__ uint64_t opaque(uint64_t desc)
+{
+    asm volatile("" : "+l"(desc));
+    return desc;
+}
+
+// Rows x columns of scores: both operands from shared memory, `steps` (at most
+// 8) inner steps of 16, the second slab after four.
 __device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
-    for (int k = 0; k < steps; ++k) {
-        const uint32_t at = (k >> 2) * kSlab + (k & 3) * 32;
-        mma_smem(d, desc_inner(a + at), desc_inner(b + at), shape, k > 0);
+    const uint64_t da = opaque(desc_inner(a)), db = opaque(desc_inner(b));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        if (k < steps) mma_smem(d, da + at, db + at, shape, k > 0);
     }
+}
+
+// d (+)= A B over inner steps [FROM, TO) of 16: A from tensor memory, 8 columns
+// a step (the second half of the steps GAP columns further), B read across.
+template <int FROM, int TO, int GAP>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+{
+    const uint64_t db = opaque(desc_outer(b));
+#pragma unroll
+    for (int k = FROM; k < TO; ++k)
+        mma_tmem(d, a + 8 * k + (k >> 2) * GAP, db + k * (2048 >> 4), shape, k > FROM || add);
 }
 
 // An arrival on `bar` once every matrix instruction issued so far by this
