@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(384, 1)
     __shared__ Shared sh;
     const uint32_t base = (smem_addr(raw) + 1023) & ~1023u;
     const uint32_t q_at = base, kv_at = base + 2 * Sh::kTileBytes;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
     if (warp == 2) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
@@ -259,7 +259,11 @@ __global__ void __launch_bounds__(384, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------- issuer
-        if (lane == 0) {
+        {
+            const bool leader = lane == 0;
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+            };
             const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
             uint32_t c = 0, items_seen = 0, ps[2] = {0, 0};
             uint32_t prev = 0, v_stage = 0;   // flags of the last key tile, the stage of its V
@@ -267,54 +271,55 @@ __global__ void __launch_bounds__(384, 1)
             bool ok = true;
             for (uint32_t n = 0; ok; ++n) {
                 const uint32_t s = n % kRing;
-                if (!(ok = mbar_wait_or_stop(&sh.info_full[s], n / kRing & 1, stop))) break;
+                if (!(ok = wait(&sh.info_full[s], n / kRing & 1))) break;
                 const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
-                mbar_arrive(&sh.info_empty[s]);
+                __syncwarp();
+                if (leader) mbar_arrive(&sh.info_empty[s]);
                 const bool tile = (e & (3 * kNeed)) != 0;
                 const uint32_t k_stage = c % Sh::kStages, k_parity = c / Sh::kStages & 1;
-                if ((e & kFirst) && !(ok = mbar_wait_or_stop(&sh.q_full, items_seen & 1, stop))) break;
+                if ((e & kFirst) && !(ok = wait(&sh.q_full, items_seen & 1))) break;
                 if (prev & (3 * kNeed)) {
                     // its V was loaded right after its K
                     const uint32_t vc = v_stage;
-                    if (!(ok = mbar_wait_or_stop(&sh.kv_full[vc % Sh::kStages], vc / Sh::kStages & 1, stop))) break;
+                    if (!(ok = wait(&sh.kv_full[vc % Sh::kStages], vc / Sh::kStages & 1))) break;
                 }
-                if (tile && !(ok = mbar_wait_or_stop(&sh.kv_full[k_stage], k_parity, stop))) break;
+                if (tile && !(ok = wait(&sh.kv_full[k_stage], k_parity))) break;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     if (prev & (kNeed << x)) {
-                        if (!(ok = mbar_wait_or_stop(&sh.p_half[x], ps[x] & 1, stop))) break;
+                        if (!(ok = wait(&sh.p_half[x], ps[x] & 1))) break;
                         tmem_fence_after();
                         const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
-                        mma_weights<0, 4, 0>(tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, started[x]);
-                        if (!(ok = mbar_wait_or_stop(&sh.p_ready[x], ps[x] & 1, stop))) break;
+                        mma_weights<0, 4, 0>(leader, tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, started[x]);
+                        if (!(ok = wait(&sh.p_ready[x], ps[x] & 1))) break;
                         ++ps[x];
                         tmem_fence_after();
-                        mma_weights<4, 8, 0>(tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, true);
+                        mma_weights<4, 8, 0>(leader, tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, true);
                         started[x] = true;
-                        mma_commit(&sh.pv_done[x]);
+                        mma_commit(leader, &sh.pv_done[x]);
                     }
                     if (e & kFirst) started[x] = false;
                     if (e & (kNeed << x)) {
-                        mma_scores(tmem + 128 * x, q_at + x * Sh::kTileBytes, kv_at + k_stage * Sh::kTileBytes, s_shape,
+                        mma_scores(leader, tmem + 128 * x, q_at + x * Sh::kTileBytes, kv_at + k_stage * Sh::kTileBytes, s_shape,
                                    steps);
-                        mma_commit(&sh.s_ready[x]);
+                        mma_commit(leader, &sh.s_ready[x]);
                     }
                 }
                 if (!ok) break;
-                if (prev & (3 * kNeed)) mma_commit(&sh.kv_empty[v_stage % Sh::kStages]);
+                if (prev & (3 * kNeed)) mma_commit(leader, &sh.kv_empty[v_stage % Sh::kStages]);
                 if (tile) {
-                    mma_commit(&sh.kv_empty[k_stage]);
+                    mma_commit(leader, &sh.kv_empty[k_stage]);
                     v_stage = c + 1;
                     c += 2;
                 }
                 if (e & kLast) {
-                    mma_commit(&sh.q_empty);
+                    mma_commit(leader, &sh.q_empty);
                     ++items_seen;
                 }
                 prev = e;
                 if (e & kStop) break;
             }
-            mma_commit(&sh.drained);
+            mma_commit(leader, &sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
     } else {

@@ -245,9 +245,9 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
 
 // The weights of a tile lie as two halves of 64 inner columns, each over the
 // first half of the columns of scores that it came from.
-__device__ __forceinline__ void mma_halves(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_halves(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-    mma_weights<0, 8, 32>(d, a, b, shape, add);
+    mma_weights<0, 8, 32>(leader, d, a, b, shape, add);
 }
 
 // 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)
@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(384, 1)
     const AttentionParams &p = b.a;
     extern __shared__ __align__(1024) uint8_t raw[];
     Sh &sh = *reinterpret_cast<Sh *>(raw);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const bool aligned = (smem_addr(raw) & 1023) == 0;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     if (warp == 2) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(&sh.acc_done, 1);
         mbar_init(&sh.drained, 1);
         sh.spoiled = 0;
-        sh.stop = smem_addr(raw) & 1023 ? 1 : 0;  // the swizzle needs 1024-byte tiles
+        sh.stop = aligned ? 0 : 1;  // the swizzle needs 1024-byte tiles
         mbar_init_fence();
     }
     tmem_fence_before();
@@ -379,7 +380,7 @@ __global__ void __launch_bounds__(384, 1)
     // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
     if (warp < 4) {
     fewer_registers<96>();
-    if (warp == 0 && *stop == 0) {
+    if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, k = 0;                    // tiles, items
         uint32_t nk = 0, nv = 0, nq = 0, no = 0;  // loads issued
@@ -453,24 +454,28 @@ __global__ void __launch_bounds__(384, 1)
             if (nq > 0) mbar_wait_bounded(&sh.q_full, (nq - 1) & 1);
             if (no > 0) mbar_wait_bounded(&sh.do_full, (no - 1) & 1);
         }
-    } else if (warp == 1 && *stop == 0) {
+    } else if (warp == 1 && aligned) {
         // ------------------------------------------------------------- issuer
-        if (lane == 0) {
+        {
+            const bool leader = lane == 0;
             const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
             uint32_t ns = 0, np = 0, iq = 0, id = 0;   // tiles whose S, dP is issued; items begun with each
             uint32_t flags[2] = {0, 0};                // of the tiles between S and dQ
             bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait_or_stop(bar, parity, stop); };
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+            };
             auto issue_s = [&]() {   // false at the end
                 const uint32_t s = ns % kRing;
                 if (!wait(&sh.info_full[s], ns / kRing & 1)) return false;
                 const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
-                mbar_arrive(&sh.info_empty[s]);
+                __syncwarp();
+                if (leader) mbar_arrive(&sh.info_empty[s]);
                 if (e & kStop) return false;
                 if ((e & kFirst) && !wait(&sh.q_full, iq++ & 1)) return false;
                 if (!wait(&sh.k_full[ns % Sh::kK], ns / Sh::kK & 1)) return false;
-                mma_scores(tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ns % Sh::kK]), s_shape, steps);
-                if (e & kLast) mma_commit(&sh.q_empty);
+                mma_scores(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ns % Sh::kK]), s_shape, steps);
+                if (e & kLast) mma_commit(leader, &sh.q_empty);
                 flags[ns & 1] = e;
                 ++ns;
                 return true;
@@ -479,10 +484,10 @@ __global__ void __launch_bounds__(384, 1)
                 const uint32_t e = flags[np & 1], vs = np % Sh::kV;
                 if ((e & kFirst) && !wait(&sh.do_full, id++ & 1)) return;
                 if (!wait(&sh.v_full[vs], np / Sh::kV & 1)) return;
-                mma_scores(tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
-                mma_commit(&sh.dp_ready);
-                mma_commit(&sh.v_empty[vs]);
-                if (e & kLast) mma_commit(&sh.do_empty);
+                mma_scores(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
+                mma_commit(leader, &sh.dp_ready);
+                mma_commit(leader, &sh.v_empty[vs]);
+                if (e & kLast) mma_commit(leader, &sh.do_empty);
                 ++np;
             };
             bool more = issue_s();
@@ -499,12 +504,12 @@ __global__ void __launch_bounds__(384, 1)
                 if (!wait(&sh.ds_ready, i & 1)) break;
                 tmem_fence_after();
                 const uint32_t e = flags[i & 1];
-                mma_halves(tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[i % Sh::kK]), o_shape, !(e & kFirst));
-                mma_commit(&sh.k_empty[i % Sh::kK]);
-                if (e & kLast) mma_commit(&sh.acc_done);
+                mma_halves(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[i % Sh::kK]), o_shape, !(e & kFirst));
+                mma_commit(leader, &sh.k_empty[i % Sh::kK]);
+                if (e & kLast) mma_commit(leader, &sh.acc_done);
                 if (more) more = issue_s();
             }
-            mma_commit(&sh.drained);
+            mma_commit(leader, &sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
     }
@@ -521,7 +526,7 @@ __global__ void __launch_bounds__(384, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
         };
-        for (uint32_t n = 0; *stop == 0; ++n) {
+        for (uint32_t n = 0; aligned; ++n) {
             const uint32_t slot = n % kRing;
             if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int4 e = sh.info[slot];
@@ -656,7 +661,8 @@ __global__ void __launch_bounds__(384, 1)
     const AttentionParams &p = b.a;
     extern __shared__ __align__(1024) uint8_t raw[];
     Sh &sh = *reinterpret_cast<Sh *>(raw);
-    const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    const bool aligned = (smem_addr(raw) & 1023) == 0;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
     if (warp == 2) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.kv_full, 1);
@@ -684,7 +690,7 @@ __global__ void __launch_bounds__(384, 1)
         mbar_init(&sh.acc_done, 1);
         mbar_init(&sh.drained, 1);
         sh.spoiled = 0;
-        sh.stop = smem_addr(raw) & 1023 ? 1 : 0;
+        sh.stop = aligned ? 0 : 1;
         mbar_init_fence();
     }
     tmem_fence_before();
@@ -698,7 +704,7 @@ __global__ void __launch_bounds__(384, 1)
     // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
     if (warp < 4) {
     fewer_registers<96>();
-    if (warp == 0 && *stop == 0) {
+    if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, k = 0;                 // tiles, items
         uint32_t nq = 0, no = 0, nkv = 0;      // loads issued
@@ -783,32 +789,36 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
             if (nkv > 0) mbar_wait_bounded(&sh.kv_full, (nkv - 1) & 1);
         }
-    } else if (warp == 1 && *stop == 0) {
+    } else if (warp == 1 && aligned) {
         // ------------------------------------------------------------- issuer
-        if (lane == 0) {
+        {
+            const bool leader = lane == 0;
             const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
             uint32_t prev = 0, k = 0;   // flags of the last tile, items begun
             bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) { return ok = ok && mbar_wait_or_stop(bar, parity, stop); };
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+            };
             const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
             for (uint32_t n = 0; ok; ++n) {
                 const uint32_t slot = n % kRing;
                 if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
                 const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
-                mbar_arrive(&sh.info_empty[slot]);
+                __syncwarp();
+                if (leader) mbar_arrive(&sh.info_empty[slot]);
                 const uint32_t i = n - 1, qp = i % Sh::kQ, op = i % Sh::kO, qs = n % Sh::kQ, os = n % Sh::kO;
                 auto dv = [&]() {
                     if (!wait(&sh.p_ready, i & 1)) return;
                     tmem_fence_after();
-                    mma_halves(dv_at, s_at, smem_addr(sh.dout[op]), o_shape, !(prev & kFirst));
-                    mma_commit(&sh.do_empty[op]);
+                    mma_halves(leader, dv_at, s_at, smem_addr(sh.dout[op]), o_shape, !(prev & kFirst));
+                    mma_commit(leader, &sh.do_empty[op]);
                 };
                 auto dk = [&]() {
                     if (!wait(&sh.ds_ready, i & 1)) return;
                     tmem_fence_after();
-                    mma_halves(dk_at, dp_at, smem_addr(sh.q[qp]), o_shape, !(prev & kFirst));
-                    mma_commit(&sh.q_empty[qp]);
-                    if (prev & kLast) mma_commit(&sh.acc_done);
+                    mma_halves(leader, dk_at, dp_at, smem_addr(sh.q[qp]), o_shape, !(prev & kFirst));
+                    mma_commit(leader, &sh.q_empty[qp]);
+                    if (prev & kLast) mma_commit(leader, &sh.acc_done);
                 };
                 // a new item's K and V may wait for the last one's: its products go first
                 const bool fresh = (e & (kFirst | kStop)) != 0;
@@ -817,21 +827,21 @@ __global__ void __launch_bounds__(384, 1)
                 if (ok && !(e & kStop)) {
                     if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
                     if (!wait(&sh.q_full[qs], n / Sh::kQ & 1)) break;
-                    mma_scores(s_at, smem_addr(sh.k), smem_addr(sh.q[qs]), s_shape, steps);
-                    mma_commit(&sh.s_ready);
+                    mma_scores(leader, s_at, smem_addr(sh.k), smem_addr(sh.q[qs]), s_shape, steps);
+                    mma_commit(leader, &sh.s_ready);
                 }
                 if (n > 0 && !fresh && ok) dk();
                 if (!ok || (e & kStop)) break;
                 if (!wait(&sh.do_full[os], n / Sh::kO & 1)) break;
-                mma_scores(dp_at, smem_addr(sh.v), smem_addr(sh.dout[os]), s_shape, steps);
-                mma_commit(&sh.dp_ready);
-                if (e & kLast) mma_commit(&sh.kv_empty);
+                mma_scores(leader, dp_at, smem_addr(sh.v), smem_addr(sh.dout[os]), s_shape, steps);
+                mma_commit(leader, &sh.dp_ready);
+                if (e & kLast) mma_commit(leader, &sh.kv_empty);
                 prev = e;
             }
-            mma_commit(&sh.drained);
+            mma_commit(leader, &sh.drained);
             mbar_wait_bounded(&sh.drained, 0);
         }
-    } else if (warp > 1 && *stop == 0) {
+    } else if (warp > 1 && aligned) {
         // ------------------------------------------------------------- statistics of the rows
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing, s = n & 1;
@@ -863,7 +873,7 @@ __global__ void __launch_bounds__(384, 1)
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
         };
-        for (uint32_t n = 0; *stop == 0; ++n) {
+        for (uint32_t n = 0; aligned; ++n) {
             const uint32_t slot = n % kRing, a = n & 1;
             if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int4 e = sh.info[slot];

@@ -44,25 +44,28 @@ __device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_outer)
 
 // ----------------------------------------------------------------- matrix instructions
 
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add)
+// The whole warp runs the issuing code, so that addresses and descriptors stay
+// in uniform registers; its lane 0 (`leader`) alone issues.
+
+__device__ __forceinline__ void mma_smem(bool leader, uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
+        "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0;\n"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u)
+        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
+        "r"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
         : "memory");
 }
 
-// One thread issues every matrix instruction, so the loops are unrolled and
+// One warp issues every matrix instruction, so the loops are unrolled and
 // the descriptors advance by constants: with address arithmetic in the loop an
 // instruction took 100 cycles to issue, against 64 to run.
 
@@ -77,34 +80,36 @@ __device__ __forceinline__ uint64_t opaque(uint64_t desc)
 
 // Rows x columns of scores: both operands from shared memory, `steps` (at most
 // 8) inner steps of 16, the second slab after four.
-__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
+__device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
     const uint64_t da = opaque(desc_inner(a)), db = opaque(desc_inner(b));
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
         const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        if (k < steps) mma_smem(d, da + at, db + at, shape, k > 0);
+        if (k < steps) mma_smem(leader, d, da + at, db + at, shape, k > 0);
     }
 }
 
 // d (+)= A B over inner steps [FROM, TO) of 16: A from tensor memory, 8 columns
 // a step (the second half of the steps GAP columns further), B read across.
 template <int FROM, int TO, int GAP>
-__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_weights(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
     const uint64_t db = opaque(desc_outer(b));
 #pragma unroll
     for (int k = FROM; k < TO; ++k)
-        mma_tmem(d, a + 8 * k + (k >> 2) * GAP, db + k * (2048 >> 4), shape, k > FROM || add);
+        mma_tmem(leader, d, a + 8 * k + (k >> 2) * GAP, db + k * (2048 >> 4), shape, k > FROM || add);
 }
 
 // An arrival on `bar` once every matrix instruction issued so far by this
 // thread has completed (and an arrival on behalf of its reads of shared memory).
-__device__ __forceinline__ void mma_commit(uint64_t *bar)
+__device__ __forceinline__ void mma_commit(bool leader, uint64_t *bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                     smem_addr(bar))
-                 : "memory");
+    asm volatile(
+        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_addr(bar)),
+        "r"(leader ? 1u : 0u)
+        : "memory");
 }
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
