@@ -59,10 +59,10 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 // is persistent (one per SM) and split into roles that hand tiles on through
 // barriers, so that loads, matrix instructions and softmax of different tiles
 // run at the same time, across items too:
-//   rows     (2 warps)  which keys every row of the next item sees;
+//   rows     (1 warp)   which keys every row of the next item sees;
 //   loader   (1 warp)   the item's list of key tiles, its Q, K and V by TMA;
-//   issuer   (1 thread) the matrix instructions: S = Q K^T into tensor memory,
-//                       then O += P V with P read from tensor memory;
+//   issuers  (2 warps)  the matrix instructions of one query tile each: S = Q K^T
+//                       into tensor memory, then O += P V with P read from there;
 //   softmax  (2 x 4 warps, one warpgroup per query tile, one thread per row)
 //            scores to weights in place, statistics, the final division.
 // Tensor memory: S of both tiles (P over it), O of both tiles: 4 x 128 columns.
@@ -88,7 +88,7 @@ struct Shared {
     uint64_t kv_full[8], kv_empty[8];
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t rows_full[2], rows_empty[2];
-    uint64_t s_ready[2], p_half[2], p_ready[2], pv_done[2], drained;
+    uint64_t s_ready[2], p_half[2], p_ready[2], pv_done[2], turn[2], drained[2];
     int2 info[kRing];                  // first key, flags
     int4 rows[2][2][kTile];            // two visible spans of every row of an item
     uint32_t tmem;
@@ -132,27 +132,28 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t q_at = base, kv_at = base + 2 * Sh::kTileBytes;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
 
-    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (warp == 3) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
+        mbar_init(&sh.q_empty, 2);
         for (int i = 0; i < Sh::kStages; ++i) {
             mbar_init(&sh.kv_full[i], 1);
-            mbar_init(&sh.kv_empty[i], 1);
+            mbar_init(&sh.kv_empty[i], 2);     // both issuers
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 9);     // issuer, 8 softmax warps
+            mbar_init(&sh.info_empty[i], 10);    // issuers, 8 softmax warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.rows_full[i], 64);
+            mbar_init(&sh.rows_full[i], 32);
             mbar_init(&sh.rows_empty[i], 9);     // loader, 8 softmax warps
             mbar_init(&sh.s_ready[i], 1);
             mbar_init(&sh.p_half[i], kTile);
             mbar_init(&sh.p_ready[i], kTile);
             mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.turn[i], 1);
+            mbar_init(&sh.drained[i], 1);
         }
-        mbar_init(&sh.drained, 1);
         sh.stop = 0;
         mbar_init_fence();
     }
@@ -257,71 +258,65 @@ __global__ void __launch_bounds__(384, 1)
             if (k > 0) mbar_wait_bounded(&sh.q_full, (k - 1) & 1);
             mbar_wait_bounded(&sh.q_full, k & 1);
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------- issuer
-        {
-            const bool leader = lane == 0;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
-            };
-            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
-            uint32_t c = 0, items_seen = 0, ps[2] = {0, 0};
-            uint32_t prev = 0, v_stage = 0;   // flags of the last key tile, the stage of its V
-            bool started[2] = {false, false};
-            bool ok = true;
-            for (uint32_t n = 0; ok; ++n) {
-                const uint32_t s = n % kRing;
-                if (!(ok = wait(&sh.info_full[s], n / kRing & 1))) break;
-                const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
-                __syncwarp();
-                if (leader) mbar_arrive(&sh.info_empty[s]);
-                const bool tile = (e & (3 * kNeed)) != 0;
-                const uint32_t k_stage = c % Sh::kStages, k_parity = c / Sh::kStages & 1;
-                if ((e & kFirst) && !(ok = wait(&sh.q_full, items_seen & 1))) break;
-                if (prev & (3 * kNeed)) {
-                    // its V was loaded right after its K
-                    const uint32_t vc = v_stage;
-                    if (!(ok = wait(&sh.kv_full[vc % Sh::kStages], vc / Sh::kStages & 1))) break;
-                }
-                if (tile && !(ok = wait(&sh.kv_full[k_stage], k_parity))) break;
-#pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    if (prev & (kNeed << x)) {
-                        if (!(ok = wait(&sh.p_half[x], ps[x] & 1))) break;
-                        tmem_fence_after();
-                        const uint32_t v = kv_at + (v_stage % Sh::kStages) * Sh::kTileBytes;
-                        mma_weights<0, 4, 0>(leader, tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, started[x]);
-                        if (!(ok = wait(&sh.p_ready[x], ps[x] & 1))) break;
-                        ++ps[x];
-                        tmem_fence_after();
-                        mma_weights<4, 8, 0>(leader, tmem + 256 + 128 * x, tmem + 128 * x, v, o_shape, true);
-                        started[x] = true;
-                        mma_commit(leader, &sh.pv_done[x]);
-                    }
-                    if (e & kFirst) started[x] = false;
-                    if (e & (kNeed << x)) {
-                        mma_scores(leader, tmem + 128 * x, q_at + x * Sh::kTileBytes, kv_at + k_stage * Sh::kTileBytes, s_shape,
-                                   steps);
-                        mma_commit(leader, &sh.s_ready[x]);
-                    }
-                }
-                if (!ok) break;
-                if (prev & (3 * kNeed)) mma_commit(leader, &sh.kv_empty[v_stage % Sh::kStages]);
-                if (tile) {
-                    mma_commit(leader, &sh.kv_empty[k_stage]);
-                    v_stage = c + 1;
-                    c += 2;
-                }
-                if (e & kLast) {
-                    mma_commit(leader, &sh.q_empty);
-                    ++items_seen;
-                }
-                prev = e;
-                if (e & kStop) break;
+    } else if (warp < 3) {
+        // ------------------------------------------------------------- issuers
+        // One warp for each query tile: what one spends on barriers passes while the matrix unit works
+        // for the other (one warp for both left it idle for a quarter of the time). They take turns,
+        // one tile's two products at a time: left to themselves they fall into step, and the
+        // matrix unit then waits for both softmaxes.
+        const int x = warp - 1;
+        const bool leader = lane == 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+        const uint32_t s_at = tmem + 128 * x, o_at = tmem + 256 + 128 * x, q = q_at + x * Sh::kTileBytes;
+        uint32_t c = 0, items_seen = 0, ps = 0;
+        uint32_t prev = 0, v = 0;   // flags of the last key tile, the ring place of its V
+        bool started = false;
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+            const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
+            __syncwarp();
+            if (leader) mbar_arrive(&sh.info_empty[slot]);
+            const bool of_prev = (prev & (kNeed << x)) != 0, of_this = (e & (kNeed << x)) != 0;
+            const uint32_t vs = v % Sh::kStages, ks = c % Sh::kStages;
+            if (of_prev && !(wait(&sh.kv_full[vs], v / Sh::kStages & 1) && wait(&sh.p_half[x], ps & 1))) break;
+            if ((e & kFirst) && !wait(&sh.q_full, items_seen & 1)) break;
+            if (of_this && !wait(&sh.kv_full[ks], c / Sh::kStages & 1)) break;
+            if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
+            if (of_prev) {
+                tmem_fence_after();
+                mma_weights<0, 4, 0>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
+                if (!wait(&sh.p_ready[x], ps & 1)) break;
+                ++ps;
+                tmem_fence_after();
+                mma_weights<4, 8, 0>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, true);
+                started = true;
+                mma_commit(leader, &sh.pv_done[x]);
             }
-            mma_commit(leader, &sh.drained);
-            mbar_wait_bounded(&sh.drained, 0);
+            if (of_this) {
+                mma_scores(leader, s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
+                mma_commit(leader, &sh.s_ready[x]);
+            }
+            if (leader) mbar_arrive(&sh.turn[1 - x]);
+            if (prev & (3 * kNeed)) mma_commit(leader, &sh.kv_empty[vs]);
+            if (e & kStop) break;
+            if (e & kFirst) started = false;
+            if (e & (3 * kNeed)) {
+                mma_commit(leader, &sh.kv_empty[ks]);
+                v = c + 1;
+                c += 2;
+            }
+            if (e & kLast) {
+                mma_commit(leader, &sh.q_empty);
+                ++items_seen;
+            }
+            prev = e;
         }
+        mma_commit(leader, &sh.drained[x]);
+        mbar_wait_bounded(&sh.drained[x], 0);
     } else {
         // ------------------------------------------------------------- rows
         uint32_t k = 0;
@@ -329,7 +324,7 @@ __global__ void __launch_bounds__(384, 1)
             const Item t = item_at(p, it, row_tiles, pair);
             const int b = k & 1;
             if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
-            for (int i = threadIdx.x - 64; i < (pair ? kTile : 2 * kTile); i += 64) {
+            for (int i = lane; i < (pair ? kTile : 2 * kTile); i += 32) {
                 const int64_t row = t.row0 + i;
                 const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;
                 const int4 r = g >= 0 ? spans_of(p, g) : make_int4(0, 0, 0, 0);
@@ -347,7 +342,7 @@ __global__ void __launch_bounds__(384, 1)
         const float c = p.scale * 1.4426950408889634f;
         uint32_t k = 0, ns = 0;
         int4 r = make_int4(0, 0, 0, 0);
-        float m = -INFINITY, l = 0.0f;
+        float ref = -INFINITY, l = 0.0f;   // the weights are 2^(score c - ref)
         bool used = false, spoiled = false, done = false;
         int64_t it = blockIdx.x;
         for (uint32_t n = 0;; ++n) {
@@ -367,7 +362,7 @@ __global__ void __launch_bounds__(384, 1)
                 r = sh.rows[b][pair ? 0 : x][t];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
-                m = -INFINITY;
+                ref = -INFINITY;
                 l = 0.0f;
                 used = false;
             }
@@ -389,25 +384,26 @@ __global__ void __launch_bounds__(384, 1)
                             if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
                     }
                 }
-                float top[4];
+                // A row's reference is the largest score of the first tile that it sees (times c). The
+                // weights of later tiles may pass 1: only their sum is watched, and once it
+                // is past 2^40 reference, sum and O are scaled by a power of two. So no tile but the
+                // first waits for its maximum. Weights that pass 2^127 within one tile end as an
+                // infinity or NaN in the output and the row is computed again below.
+                if (__any_sync(0xFFFFFFFFu, ref == -INFINITY)) {
+                    float mx = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    top[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 2; j < 32; j += 2)
-                        top[i] = fmaxf(top[i], fmaxf(__uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1])));
+                        for (int j = 0; j < 32; j += 2)
+                            mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1])));
+                    if (ref == -INFINITY) ref = mx * c;
                 }
-                float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-                mx = fmaxf(m, mx);
-                // The maximum in use may lag behind by a factor of 2^8 in the weights: binary32 sums
-                // have the room, and O is rarely read back to be scaled.
-                bool late = false;
-                if (m == -INFINITY) m = mx;
-                else late = (mx - m) * c > 8.0f;
-                if (__any_sync(0xFFFFFFFFu, late)) {
-                    const float f = late ? exp2_fast((m - mx) * c) : 1.0f;
+                const bool big = l > 1.0995116e12f && l < INFINITY;
+                if (__any_sync(0xFFFFFFFFu, big)) {
+                    const int up = big ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
+                    const float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
                     l *= f;
-                    if (late) m = mx;
+                    ref += static_cast<float>(up);
                     if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.pv_done[x], (ns - 1) & 1, stop))) break;
                     tmem_fence_after();
                     for (int i = 0; i < steps; ++i) {
@@ -418,7 +414,7 @@ __global__ void __launch_bounds__(384, 1)
                         tmem_store16(o_at + 16 * i, o);
                     }
                 }
-                const float mc = m == -INFINITY ? 0.0f : m * c;
+                const float mc = ref == -INFINITY ? 0.0f : ref;
                 const F2 c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
                 F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
 #pragma unroll
@@ -479,7 +475,7 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 if (valid)
                     p.lse[head * p.Tpad + row] =
-                        sees_any && l != 0.0f ? (m * c + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        sees_any && l != 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 spoiled |= valid && bad != 0.0f;   // NaN
                 it += gridDim.x;
                 ++k;
@@ -506,7 +502,7 @@ __global__ void __launch_bounds__(384, 1)
         }
     }
     __syncthreads();
-    if (warp == 2) tmem_free(tmem);
+    if (warp == 3) tmem_free(tmem);
     if (threadIdx.x == 0 && sh.stop != 0) atomicAdd(&g_wait_timeouts, 1u);
 }
 

@@ -313,7 +313,7 @@ struct DqShared {
     uint64_t q_full, q_empty, do_full, do_empty;
     uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
     uint64_t info_full[kRing], info_empty[kRing];
-    uint64_t dp_ready, dp_free, ds_ready, acc_done, drained;
+    uint64_t s_ready[2], dp_ready, dp_free, ds_ready, acc_done, drained[2];
     int4 info[kRing];              // first key, flags, item
     uint32_t tmem, stop, spoiled;
 };
@@ -344,7 +344,7 @@ __global__ void __launch_bounds__(384, 1)
     Sh &sh = *reinterpret_cast<Sh *>(raw);
     const bool aligned = (smem_addr(raw) & 1023) == 0;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (warp == 3) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 1);
@@ -360,13 +360,16 @@ __global__ void __launch_bounds__(384, 1)
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 9);      // issuer, 8 warps
+            mbar_init(&sh.info_empty[i], 10);     // issuers, 8 warps
         }
+        mbar_init(&sh.s_ready[0], 1);
+        mbar_init(&sh.s_ready[1], 1);
         mbar_init(&sh.dp_ready, 1);
         mbar_init(&sh.dp_free, 2 * kTile);
         mbar_init(&sh.ds_ready, 2 * kTile);
         mbar_init(&sh.acc_done, 1);
-        mbar_init(&sh.drained, 1);
+        mbar_init(&sh.drained[0], 1);
+        mbar_init(&sh.drained[1], 1);
         sh.spoiled = 0;
         sh.stop = aligned ? 0 : 1;  // the swizzle needs 1024-byte tiles
         mbar_init_fence();
@@ -454,64 +457,66 @@ __global__ void __launch_bounds__(384, 1)
             if (nq > 0) mbar_wait_bounded(&sh.q_full, (nq - 1) & 1);
             if (no > 0) mbar_wait_bounded(&sh.do_full, (no - 1) & 1);
         }
-    } else if (warp == 1 && aligned) {
-        // ------------------------------------------------------------- issuer
-        {
-            const bool leader = lane == 0;
-            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
-            uint32_t ns = 0, np = 0, iq = 0, id = 0;   // tiles whose S, dP is issued; items begun with each
-            uint32_t flags[2] = {0, 0};                // of the tiles between S and dQ
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
-            };
-            auto issue_s = [&]() {   // false at the end
-                const uint32_t s = ns % kRing;
-                if (!wait(&sh.info_full[s], ns / kRing & 1)) return false;
-                const uint32_t e = static_cast<uint32_t>(sh.info[s].y);
+    } else if (warp < 3 && aligned) {
+        // ------------------------------------------------------------- issuers
+        // One warp for S and dQ, one for dP: what one spends on barriers passes while the matrix unit
+        // works for the other.
+        const bool leader = lane == 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+        if (warp == 1) {
+            uint32_t ns = 0, items_seen = 0;   // tiles whose S is issued, items begun
+            uint32_t flags[2] = {0, 0};        // of the tiles between S and dQ
+            auto issue_s = [&]() {             // false at the end
+                const uint32_t slot = ns % kRing, ks = ns % Sh::kK;
+                if (!wait(&sh.info_full[slot], ns / kRing & 1)) return false;
+                const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
                 __syncwarp();
-                if (leader) mbar_arrive(&sh.info_empty[s]);
+                if (leader) mbar_arrive(&sh.info_empty[slot]);
                 if (e & kStop) return false;
-                if ((e & kFirst) && !wait(&sh.q_full, iq++ & 1)) return false;
-                if (!wait(&sh.k_full[ns % Sh::kK], ns / Sh::kK & 1)) return false;
-                mma_scores(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ns % Sh::kK]), s_shape, steps);
+                if ((e & kFirst) && !wait(&sh.q_full, items_seen++ & 1)) return false;
+                if (!wait(&sh.k_full[ks], ns / Sh::kK & 1)) return false;
+                mma_scores(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
+                mma_commit(leader, &sh.s_ready[ns & 1]);
                 if (e & kLast) mma_commit(leader, &sh.q_empty);
                 flags[ns & 1] = e;
                 ++ns;
                 return true;
             };
-            auto issue_dp = [&]() {
-                const uint32_t e = flags[np & 1], vs = np % Sh::kV;
-                if ((e & kFirst) && !wait(&sh.do_full, id++ & 1)) return;
-                if (!wait(&sh.v_full[vs], np / Sh::kV & 1)) return;
+            bool more = issue_s() && issue_s();
+            for (uint32_t i = 0; i < ns; ++i) {
+                if (!wait(&sh.ds_ready, i & 1)) break;
+                tmem_fence_after();
+                const uint32_t e = flags[i & 1], ks = i % Sh::kK;
+                mma_halves(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
+                if (e & kLast) mma_commit(leader, &sh.acc_done);
+                mma_commit(leader, &sh.k_empty[ks]);
+                if (more) more = issue_s();
+            }
+        } else {
+            uint32_t items_seen = 0;
+            for (uint32_t n = 0;; ++n) {
+                const uint32_t slot = n % kRing, vs = n % Sh::kV;
+                if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+                const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
+                __syncwarp();
+                if (leader) mbar_arrive(&sh.info_empty[slot]);
+                if (e & kStop) break;
+                if ((e & kFirst) && !wait(&sh.do_full, items_seen++ & 1)) break;
+                if (!wait(&sh.v_full[vs], n / Sh::kV & 1)) break;
+                // dP's columns are in registers long before dS is made of them
+                if (n > 0 && !wait(&sh.dp_free, (n - 1) & 1)) break;
+                tmem_fence_after();
                 mma_scores(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
                 mma_commit(leader, &sh.dp_ready);
                 mma_commit(leader, &sh.v_empty[vs]);
                 if (e & kLast) mma_commit(leader, &sh.do_empty);
-                ++np;
-            };
-            bool more = issue_s();
-            if (more) {
-                more = issue_s();
-                if (ok) issue_dp();
             }
-            for (uint32_t i = 0; ok && i < np; ++i) {
-                if (np < ns) {   // dP's columns are in registers long before dS is made of them
-                    if (!wait(&sh.dp_free, i & 1)) break;
-                    tmem_fence_after();
-                    issue_dp();
-                }
-                if (!wait(&sh.ds_ready, i & 1)) break;
-                tmem_fence_after();
-                const uint32_t e = flags[i & 1];
-                mma_halves(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[i % Sh::kK]), o_shape, !(e & kFirst));
-                mma_commit(leader, &sh.k_empty[i % Sh::kK]);
-                if (e & kLast) mma_commit(leader, &sh.acc_done);
-                if (more) more = issue_s();
-            }
-            mma_commit(leader, &sh.drained);
-            mbar_wait_bounded(&sh.drained, 0);
         }
+        mma_commit(leader, &sh.drained[warp - 1]);
+        mbar_wait_bounded(&sh.drained[warp - 1], 0);
     }
     } else {
         more_registers<200>();
@@ -547,7 +552,7 @@ __global__ void __launch_bounds__(384, 1)
                     delta = b.delta[d.head * p.Tpad + row];
                 }
             }
-            if (!wait(&sh.dp_ready, n & 1)) break;
+            if (!wait(&sh.s_ready[n & 1], n / 2 & 1) || !wait(&sh.dp_ready, n & 1)) break;
             tmem_fence_after();
             const uint32_t s_at = at + 128 * (n & 1) + 64 * y, dp_at = at + 256 + 64 * y;
             uint32_t s[2][32], dp[2][32];
@@ -602,7 +607,7 @@ __global__ void __launch_bounds__(384, 1)
         if (spoiled) sh.spoiled = 1;
     }
     __syncthreads();
-    if (warp == 2) tmem_free(tmem);
+    if (warp == 3) tmem_free(tmem);
     if (sh.stop != 0) {
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
@@ -624,9 +629,9 @@ __global__ void __launch_bounds__(384, 1)
 // by. Scores are transposed, so that P and dS are first operands in tensor
 // memory:
 //   S' = K Q^T, dP' = V dO^T, dV += P' dO, dK += dS' Q,
-// issued as dV(i) S(i+1) dK(i) dP(i+1): the matrix unit works on two products
-// while two warpgroups (64 row columns each, one thread per key) make P, and on
-// the other two while they make dS.
+// issued as dV(i) S(i+1) by one warp and dK(i) dP(i+1) by another: the matrix
+// unit works on two products while two warpgroups (64 row columns each, one
+// thread per key) make P, and on the other two while they make dS.
 // Tensor memory: S', dP', dV, dK. Shared memory: K, V, 3 Q, 2 dO.
 
 template <int DP>
@@ -639,7 +644,7 @@ struct DkvShared {
     uint64_t q_full[kQ], q_empty[kQ], do_full[kO], do_empty[kO];
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t aux_full[2], aux_empty[2];
-    uint64_t s_ready, p_ready, dp_ready, ds_ready, acc_done, drained;
+    uint64_t s_ready, p_ready, dp_ready, ds_ready, acc_done[2], drained[2];
     int4 info[kRing];              // first row, flags and head, tile * P + rank
     uint32_t tmem, stop, spoiled;
 };
@@ -663,32 +668,34 @@ __global__ void __launch_bounds__(384, 1)
     Sh &sh = *reinterpret_cast<Sh *>(raw);
     const bool aligned = (smem_addr(raw) & 1023) == 0;
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x / 32, 0), lane = threadIdx.x & 31;
-    if (warp == 2) tmem_alloc(&sh.tmem);
+    if (warp == 3) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.kv_full, 1);
-        mbar_init(&sh.kv_empty, 1);
+        mbar_init(&sh.kv_empty, 2);
         for (int i = 0; i < Sh::kQ; ++i) {
             mbar_init(&sh.q_full[i], 1);
             mbar_init(&sh.q_empty[i], 1);
         }
         for (int i = 0; i < Sh::kO; ++i) {
             mbar_init(&sh.do_full[i], 1);
-            mbar_init(&sh.do_empty[i], 1);
+            mbar_init(&sh.do_empty[i], 2);
         }
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 11);     // issuer, 2 statistics warps, 8 warps
+            mbar_init(&sh.info_empty[i], 11);     // issuers, statistics, 8 warps
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sh.aux_full[i], 64);
+            mbar_init(&sh.aux_full[i], 32);
             mbar_init(&sh.aux_empty[i], 8);
         }
         mbar_init(&sh.s_ready, 1);
         mbar_init(&sh.p_ready, 2 * kTile);
         mbar_init(&sh.dp_ready, 1);
         mbar_init(&sh.ds_ready, 2 * kTile);
-        mbar_init(&sh.acc_done, 1);
-        mbar_init(&sh.drained, 1);
+        mbar_init(&sh.acc_done[0], 1);
+        mbar_init(&sh.acc_done[1], 1);
+        mbar_init(&sh.drained[0], 1);
+        mbar_init(&sh.drained[1], 1);
         sh.spoiled = 0;
         sh.stop = aligned ? 0 : 1;
         mbar_init_fence();
@@ -789,59 +796,45 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
             if (nkv > 0) mbar_wait_bounded(&sh.kv_full, (nkv - 1) & 1);
         }
-    } else if (warp == 1 && aligned) {
-        // ------------------------------------------------------------- issuer
-        {
-            const bool leader = lane == 0;
-            const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
-            uint32_t prev = 0, k = 0;   // flags of the last tile, items begun
-            bool ok = true;
-            auto wait = [&](uint64_t *bar, uint32_t parity) {
-                return ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
-            };
-            const uint32_t s_at = tmem, dp_at = tmem + 128, dv_at = tmem + 256, dk_at = tmem + 384;
-            for (uint32_t n = 0; ok; ++n) {
-                const uint32_t slot = n % kRing;
-                if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
-                const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
-                __syncwarp();
-                if (leader) mbar_arrive(&sh.info_empty[slot]);
-                const uint32_t i = n - 1, qp = i % Sh::kQ, op = i % Sh::kO, qs = n % Sh::kQ, os = n % Sh::kO;
-                auto dv = [&]() {
-                    if (!wait(&sh.p_ready, i & 1)) return;
-                    tmem_fence_after();
-                    mma_halves(leader, dv_at, s_at, smem_addr(sh.dout[op]), o_shape, !(prev & kFirst));
-                    mma_commit(leader, &sh.do_empty[op]);
-                };
-                auto dk = [&]() {
-                    if (!wait(&sh.ds_ready, i & 1)) return;
-                    tmem_fence_after();
-                    mma_halves(leader, dk_at, dp_at, smem_addr(sh.q[qp]), o_shape, !(prev & kFirst));
-                    mma_commit(leader, &sh.q_empty[qp]);
-                    if (prev & kLast) mma_commit(leader, &sh.acc_done);
-                };
-                // a new item's K and V may wait for the last one's: its products go first
-                const bool fresh = (e & (kFirst | kStop)) != 0;
-                if (n > 0) dv();
-                if (n > 0 && fresh && ok) dk();
-                if (ok && !(e & kStop)) {
-                    if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
-                    if (!wait(&sh.q_full[qs], n / Sh::kQ & 1)) break;
-                    mma_scores(leader, s_at, smem_addr(sh.k), smem_addr(sh.q[qs]), s_shape, steps);
-                    mma_commit(leader, &sh.s_ready);
-                }
-                if (n > 0 && !fresh && ok) dk();
-                if (!ok || (e & kStop)) break;
-                if (!wait(&sh.do_full[os], n / Sh::kO & 1)) break;
-                mma_scores(leader, dp_at, smem_addr(sh.v), smem_addr(sh.dout[os]), s_shape, steps);
-                mma_commit(leader, &sh.dp_ready);
-                if (e & kLast) mma_commit(leader, &sh.kv_empty);
-                prev = e;
+    } else if (warp < 3 && aligned) {
+        // ------------------------------------------------------------- issuers
+        // One warp for S' and dV, one for dP' and dK: the same loop, on other barriers and operands.
+        const bool leader = lane == 0, first = warp == 1;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
+        const uint32_t scores = tmem + (first ? 0 : 128), acc = tmem + (first ? 256 : 384);
+        const uint32_t key_at = first ? smem_addr(sh.k) : smem_addr(sh.v);
+        uint32_t prev = 0, k = 0;   // flags of the last tile, items begun
+        for (uint32_t n = 0;; ++n) {
+            const uint32_t slot = n % kRing;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
+            const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
+            __syncwarp();
+            if (leader) mbar_arrive(&sh.info_empty[slot]);
+            if (n > 0) {
+                const uint32_t i = n - 1, qp = i % Sh::kQ, op = i % Sh::kO;
+                if (!wait(first ? &sh.p_ready : &sh.ds_ready, i & 1)) break;
+                tmem_fence_after();
+                mma_halves(leader, acc, scores, first ? smem_addr(sh.dout[op]) : smem_addr(sh.q[qp]), o_shape,
+                           !(prev & kFirst));
+                if (prev & kLast) mma_commit(leader, &sh.acc_done[warp - 1]);
+                mma_commit(leader, first ? &sh.do_empty[op] : &sh.q_empty[qp]);
             }
-            mma_commit(leader, &sh.drained);
-            mbar_wait_bounded(&sh.drained, 0);
+            if (e & kStop) break;
+            const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
+            if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
+            if (first ? !wait(&sh.q_full[qs], n / Sh::kQ & 1) : !wait(&sh.do_full[os], n / Sh::kO & 1)) break;
+            mma_scores(leader, scores, key_at, first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
+            mma_commit(leader, first ? &sh.s_ready : &sh.dp_ready);
+            if (!first) mma_commit(leader, &sh.do_empty[os]);
+            if (e & kLast) mma_commit(leader, &sh.kv_empty);
+            prev = e;
         }
-    } else if (warp > 1 && aligned) {
+        mma_commit(leader, &sh.drained[warp - 1]);
+        mbar_wait_bounded(&sh.drained[warp - 1], 0);
+    } else if (warp == 3 && aligned) {
         // ------------------------------------------------------------- statistics of the rows
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing, s = n & 1;
@@ -852,7 +845,7 @@ __global__ void __launch_bounds__(384, 1)
             if (e.y & kStop) break;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.aux_empty[s], (n / 2 & 1) ^ 1, stop))) break;
             const int64_t base = static_cast<int64_t>(e.y >> 16) * p.Tpad + e.z % p.P * p.Tp;
-            for (int i = threadIdx.x - 64; i < kTile; i += 64) {
+            for (int i = lane; i < kTile; i += 32) {
                 const int64_t row = e.x + i;
                 const bool in = row < p.Tp;
                 sh.lse2[s][i] = in ? -b.lse2[base + row] : -INFINITY;   // negated, as they are added
@@ -981,7 +974,7 @@ __global__ void __launch_bounds__(384, 1)
             if (flags & kLast) {
                 const int32_t pos = key + t < p.T ? position_of_token(b, key + t) : -1;
                 const int kvh = static_cast<int>(flags >> 16) / group;
-                if (!wait(&sh.acc_done, done++ & 1)) break;
+                if (!wait(&sh.acc_done[y], done++ & 1)) break;
                 tmem_fence_after();
                 float bad = 0.0f;
                 uint16_t *out = const_cast<uint16_t *>(row_of(y == 0 ? b.dv[rank] : b.dk[rank], pos, p.Hkv, kvh, p.D));
@@ -994,7 +987,7 @@ __global__ void __launch_bounds__(384, 1)
         if (spoiled) sh.spoiled = 1;
     }
     __syncthreads();
-    if (warp == 2) tmem_free(tmem);
+    if (warp == 3) tmem_free(tmem);
     if (sh.stop != 0) {
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
