@@ -73,6 +73,7 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 // at most one partly used tile per contiguous span.
 
 constexpr int kRing = 8;       // key-tile announcements in flight
+constexpr int kSteps = 8;      // barriers of the steps: more than a step can be ahead of whoever waits for it
 constexpr uint32_t kNeed = 1, kFull = 4, kFirst = 16, kLast = 32, kStop = 64;   // kNeed, kFull: << query tile
 
 template <int DP>
@@ -85,10 +86,11 @@ struct Shape {
 
 struct Shared {
     uint64_t q_full, q_empty;
-    uint64_t kv_full[8], kv_empty[8];
+    uint64_t kv_full[8];
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t rows_full[2], rows_empty[2];
-    uint64_t s_ready[2], p_half[2], p_ready[2], pv_done[2], turn[2], drained[2];
+    uint64_t step[2][kSteps];          // S of a tile is there and PV of the one before is done, tiles in turn
+    uint64_t p_half[2], p_ready[2], out_done[2], turn[2], drained[2];
     int2 info[kRing];                  // first key, flags
     int4 rows[2][2][kTile];            // two visible spans of every row of an item
     uint32_t tmem;
@@ -136,10 +138,7 @@ __global__ void __launch_bounds__(384, 1)
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
         mbar_init(&sh.q_empty, 2);
-        for (int i = 0; i < Sh::kStages; ++i) {
-            mbar_init(&sh.kv_full[i], 1);
-            mbar_init(&sh.kv_empty[i], 2);     // both issuers
-        }
+        for (int i = 0; i < Sh::kStages; ++i) mbar_init(&sh.kv_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
             mbar_init(&sh.info_empty[i], 10);    // issuers, 8 softmax warps
@@ -147,10 +146,10 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.rows_full[i], 32);
             mbar_init(&sh.rows_empty[i], 9);     // loader, 8 softmax warps
-            mbar_init(&sh.s_ready[i], 1);
+            for (int j = 0; j < kSteps; ++j) mbar_init(&sh.step[i][j], 1);
             mbar_init(&sh.p_half[i], kTile);
             mbar_init(&sh.p_ready[i], kTile);
-            mbar_init(&sh.pv_done[i], 1);
+            mbar_init(&sh.out_done[i], 1);
             mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
@@ -182,9 +181,15 @@ __global__ void __launch_bounds__(384, 1)
             ++n;
             return ok;
         };
+        // Ring places are K, V, K, V ...: tile j's K is free with step j, its V with step j + 1. The place
+        // of load c was that of load c - kStages.
         auto load = [&](const CUtensorMap *map, int head, int key) {
             const uint32_t s = c % Sh::kStages;
-            ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.kv_empty[s], (c / Sh::kStages & 1) ^ 1, stop));
+            if (c >= Sh::kStages) {
+                const uint32_t was = c - Sh::kStages, j = was / 2 + (was & 1);
+                for (int x = 0; ok && x < 2; ++x)
+                    ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.step[x][j % kSteps], j / kSteps & 1, stop));
+            }
             if (!ok) return false;
             if (lane == 0) {
                 mbar_expect_tx(&sh.kv_full[s], Sh::kTileBytes);
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
         const uint32_t s_at = tmem + 128 * x, o_at = tmem + 256 + 128 * x, q = q_at + x * Sh::kTileBytes;
         uint32_t c = 0, items_seen = 0, ps = 0;
-        uint32_t prev = 0, v = 0;   // flags of the last key tile, the ring place of its V
+        uint32_t prev = 0, v = 0;   // flags of the last announcement, the ring place of its V
         bool started = false;
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing;
@@ -294,18 +299,15 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_fence_after();
                 mma_weights<4, 8, 0>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, true);
                 started = true;
-                mma_commit(leader, &sh.pv_done[x]);
             }
-            if (of_this) {
+            if (prev & kLast) mma_commit(leader, &sh.out_done[x]);
+            if (of_this)
                 mma_scores(leader, s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
-                mma_commit(leader, &sh.s_ready[x]);
-            }
             if (leader) mbar_arrive(&sh.turn[1 - x]);
-            if (prev & (3 * kNeed)) mma_commit(leader, &sh.kv_empty[vs]);
             if (e & kStop) break;
             if (e & kFirst) started = false;
             if (e & (3 * kNeed)) {
-                mma_commit(leader, &sh.kv_empty[ks]);
+                mma_commit(leader, &sh.step[x][c / 2 % kSteps]);
                 v = c + 1;
                 c += 2;
             }
@@ -340,7 +342,7 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_at = tmem + lanes + 128 * x, o_at = tmem + lanes + 256 + 128 * x;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t k = 0, ns = 0;
+        uint32_t k = 0, j_tile = 0;   // items, tiles
         int4 r = make_int4(0, 0, 0, 0);
         float ref = -INFINITY, l = 0.0f;   // the weights are 2^(score c - ref)
         bool used = false, spoiled = false, done = false;
@@ -362,12 +364,14 @@ __global__ void __launch_bounds__(384, 1)
                 r = sh.rows[b][pair ? 0 : x][t];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
+                ++k;
                 ref = -INFINITY;
                 l = 0.0f;
                 used = false;
             }
             if (flags & (kNeed << x)) {
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.s_ready[x], ns & 1, stop))) break;
+                // the last tile's PV is done too
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1, stop))) break;
                 tmem_fence_after();
                 uint32_t s[4][32];
 #pragma unroll
@@ -404,8 +408,6 @@ __global__ void __launch_bounds__(384, 1)
                     const float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
                     l *= f;
                     ref += static_cast<float>(up);
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.pv_done[x], (ns - 1) & 1, stop))) break;
-                    tmem_fence_after();
                     for (int i = 0; i < steps; ++i) {
                         uint32_t o[16];
                         tmem_load16(o_at + 16 * i, o);
@@ -440,9 +442,9 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_wait_stores();
                 tmem_fence_before();
                 mbar_arrive(&sh.p_ready[x]);
-                ++ns;
                 used = true;
             }
+            if (flags & (3 * kNeed)) ++j_tile;
             if (flags & kLast) {
                 const Item d = item_at(p, it, row_tiles, pair);
                 const int head = d.head + (pair ? x : 0);
@@ -451,10 +453,8 @@ __global__ void __launch_bounds__(384, 1)
                 const bool valid = in_rank < p.Tp, sees_any = r.y != 0 || r.w != 0;
                 const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
                 float bad = 0.0f;
-                if (used) {
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.pv_done[x], (ns - 1) & 1, stop))) break;
-                    tmem_fence_after();
-                }
+                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.out_done[x], k - 1 & 1, stop))) break;
+                tmem_fence_after();
                 uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
                 for (int i = 0; i < steps; ++i) {
                     uint32_t o[16] = {};
@@ -478,7 +478,6 @@ __global__ void __launch_bounds__(384, 1)
                         sees_any && l != 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 spoiled |= valid && bad != 0.0f;   // NaN
                 it += gridDim.x;
-                ++k;
             }
         }
         // Rows with an infinity or NaN once more, one at a time, when no other role waits.

@@ -310,10 +310,10 @@ struct DqShared {
     static constexpr int kK = 3, kV = 2;
     uint8_t q[Shape<DP>::kTileBytes], dout[Shape<DP>::kTileBytes];
     uint8_t k[kK][Shape<DP>::kTileBytes], v[kV][Shape<DP>::kTileBytes];
-    uint64_t q_full, q_empty, do_full, do_empty;
-    uint64_t k_full[kK], k_empty[kK], v_full[kV], v_empty[kV];
+    uint64_t q_full, do_full;
+    uint64_t k_full[kK], k_empty[kK], v_full[kV];
     uint64_t info_full[kRing], info_empty[kRing];
-    uint64_t s_ready[2], dp_ready, dp_free, ds_ready, acc_done, drained[2];
+    uint64_t s_ready[2], dp_ready[2], dp_free, ds_ready, acc_done, drained[2];
     int4 info[kRing];              // first key, flags, item
     uint32_t tmem, stop, spoiled;
 };
@@ -347,24 +347,20 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 3) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.q_full, 1);
-        mbar_init(&sh.q_empty, 1);
         mbar_init(&sh.do_full, 1);
-        mbar_init(&sh.do_empty, 1);
         for (int i = 0; i < Sh::kK; ++i) {
             mbar_init(&sh.k_full[i], 1);
             mbar_init(&sh.k_empty[i], 1);
         }
-        for (int i = 0; i < Sh::kV; ++i) {
-            mbar_init(&sh.v_full[i], 1);
-            mbar_init(&sh.v_empty[i], 1);
-        }
+        for (int i = 0; i < Sh::kV; ++i) mbar_init(&sh.v_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
             mbar_init(&sh.info_empty[i], 10);     // issuers, 8 warps
         }
-        mbar_init(&sh.s_ready[0], 1);
-        mbar_init(&sh.s_ready[1], 1);
-        mbar_init(&sh.dp_ready, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_ready[i], 1);
+            mbar_init(&sh.dp_ready[i], 1);
+        }
         mbar_init(&sh.dp_free, 2 * kTile);
         mbar_init(&sh.ds_ready, 2 * kTile);
         mbar_init(&sh.acc_done, 1);
@@ -385,7 +381,7 @@ __global__ void __launch_bounds__(384, 1)
     fewer_registers<96>();
     if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
-        uint32_t n = 0, k = 0;                    // tiles, items
+        uint32_t n = 0;                           // tiles
         uint32_t nk = 0, nv = 0, nq = 0, no = 0;  // loads issued
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -415,7 +411,10 @@ __global__ void __launch_bounds__(384, 1)
             const int kvh = t.head / (p.Hq / p.Hkv);
             int key = next(0);
             if (key == 0x7FFFFFFF) continue;   // no row sees a key
-            if (!wait(&sh.q_empty, (k & 1) ^ 1)) break;
+            // the last item's Q is free with its last S, its dO with its last dP; a V with its dP (by tile
+            // parity: the next tile's may be ready too by the time this one's is asked for)
+            const uint32_t m = n - 1;
+            if (n > 0 && !wait(&sh.s_ready[m & 1], m / 2 & 1)) break;
             if (lane == 0) load_tile(&maps.q, smem_addr(sh.q), kSlabs, t.head, row, &sh.q_full);
             ++nq;
             for (uint32_t first = kFirst; ok && key != 0x7FFFFFFF; first = 0) {
@@ -436,17 +435,16 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) load_tile(&maps.k, smem_addr(sh.k[ks]), kSlabs, kvh, key, &sh.k_full[ks]);
                 ++nk;
                 if (first) {
-                    if (!wait(&sh.do_empty, (k & 1) ^ 1)) break;
+                    if (n > 0 && !wait(&sh.dp_ready[m & 1], m / 2 & 1)) break;
                     if (lane == 0) load_tile(&maps.dout, smem_addr(sh.dout), kSlabs, t.head, row, &sh.do_full);
                     ++no;
                 }
-                if (!wait(&sh.v_empty[vs], (n / Sh::kV & 1) ^ 1)) break;
+                if (n >= Sh::kV && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
                 if (lane == 0) load_tile(&maps.v, smem_addr(sh.v[vs]), kSlabs, kvh, key, &sh.v_full[vs]);
                 ++nv;
                 ++n;
                 key = after;
             }
-            ++k;
         }
         if (ok) announce(0, kStop, 0);
         if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
@@ -480,7 +478,6 @@ __global__ void __launch_bounds__(384, 1)
                 if (!wait(&sh.k_full[ks], ns / Sh::kK & 1)) return false;
                 mma_scores(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
                 mma_commit(leader, &sh.s_ready[ns & 1]);
-                if (e & kLast) mma_commit(leader, &sh.q_empty);
                 flags[ns & 1] = e;
                 ++ns;
                 return true;
@@ -510,9 +507,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (n > 0 && !wait(&sh.dp_free, (n - 1) & 1)) break;
                 tmem_fence_after();
                 mma_scores(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
-                mma_commit(leader, &sh.dp_ready);
-                mma_commit(leader, &sh.v_empty[vs]);
-                if (e & kLast) mma_commit(leader, &sh.do_empty);
+                mma_commit(leader, &sh.dp_ready[n & 1]);
             }
         }
         mma_commit(leader, &sh.drained[warp - 1]);
@@ -526,6 +521,9 @@ __global__ void __launch_bounds__(384, 1)
         const float c = p.scale * 1.4426950408889634f;
         int4 r = make_int4(0, 0, 0, 0);
         float lse2 = INFINITY, delta = 0.0f;
+        int head = 0;
+        int64_t row = 0;
+        bool valid = false;
         uint32_t done = 0;
         bool spoiled = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -539,20 +537,21 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
             if (flags & kStop) break;
-            const DqItem d = dq_item(p, static_cast<int64_t>(e.w) << 32 | static_cast<uint32_t>(e.z), row_tiles);
-            const int64_t row = d.rank * p.Tp + d.row0 + t;
-            const bool valid = d.row0 + t < p.Tp;
             if (flags & kFirst) {
+                const DqItem d = dq_item(p, static_cast<int64_t>(e.w) << 32 | static_cast<uint32_t>(e.z), row_tiles);
+                head = d.head;
+                row = d.rank * p.Tp + d.row0 + t;
+                valid = d.row0 + t < p.Tp;
                 r = make_int4(0, 0, 0, 0);
                 lse2 = INFINITY;
                 delta = 0.0f;
                 if (valid) {
                     r = b.spans[row];
-                    lse2 = b.lse2[d.head * p.Tpad + row];
-                    delta = b.delta[d.head * p.Tpad + row];
+                    lse2 = b.lse2[head * p.Tpad + row];
+                    delta = b.delta[head * p.Tpad + row];
                 }
             }
-            if (!wait(&sh.s_ready[n & 1], n / 2 & 1) || !wait(&sh.dp_ready, n & 1)) break;
+            if (!wait(&sh.s_ready[n & 1], n / 2 & 1) || !wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
             tmem_fence_after();
             const uint32_t s_at = at + 128 * (n & 1) + 64 * y, dp_at = at + 256 + 64 * y;
             uint32_t s[2][32], dp[2][32];
@@ -597,7 +596,7 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_fence_after();
                 float bad = 0.0f;
                 const bool write = valid && (r.y != 0 || r.w != 0);
-                uint16_t *out = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, d.head, p.D));
+                uint16_t *out = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, p.D));
                 for (int i = y; i < steps; i += 2)
                     store_columns(out, 16 * i, p.D, at + 384, p.scale, write, bad);
                 tmem_fence_before();
@@ -640,11 +639,11 @@ struct DkvShared {
     uint8_t k[Shape<DP>::kTileBytes], v[Shape<DP>::kTileBytes];
     uint8_t q[kQ][Shape<DP>::kTileBytes], dout[kO][Shape<DP>::kTileBytes];
     float lse2[2][kTile], delta[2][kTile];
-    uint64_t kv_full, kv_empty;
-    uint64_t q_full[kQ], q_empty[kQ], do_full[kO], do_empty[kO];
+    uint64_t kv_full, q_full[kQ], do_full[kO];
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t aux_full[2], aux_empty[2];
-    uint64_t s_ready, p_ready, dp_ready, ds_ready, acc_done[2], drained[2];
+    uint64_t s_ready[2], dp_ready[2];  // S' and dV of the tile before, dP' and dK of it: by tile parity
+    uint64_t p_ready, ds_ready, acc_done[2], drained[2];
     int4 info[kRing];              // first row, flags and head, tile * P + rank
     uint32_t tmem, stop, spoiled;
 };
@@ -671,15 +670,8 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 3) tmem_alloc(&sh.tmem);
     if (threadIdx.x == 0) {
         mbar_init(&sh.kv_full, 1);
-        mbar_init(&sh.kv_empty, 2);
-        for (int i = 0; i < Sh::kQ; ++i) {
-            mbar_init(&sh.q_full[i], 1);
-            mbar_init(&sh.q_empty[i], 1);
-        }
-        for (int i = 0; i < Sh::kO; ++i) {
-            mbar_init(&sh.do_full[i], 1);
-            mbar_init(&sh.do_empty[i], 2);
-        }
+        for (int i = 0; i < Sh::kQ; ++i) mbar_init(&sh.q_full[i], 1);
+        for (int i = 0; i < Sh::kO; ++i) mbar_init(&sh.do_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
             mbar_init(&sh.info_empty[i], 11);     // issuers, statistics, 8 warps
@@ -688,14 +680,14 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&sh.aux_full[i], 32);
             mbar_init(&sh.aux_empty[i], 8);
         }
-        mbar_init(&sh.s_ready, 1);
         mbar_init(&sh.p_ready, 2 * kTile);
-        mbar_init(&sh.dp_ready, 1);
         mbar_init(&sh.ds_ready, 2 * kTile);
-        mbar_init(&sh.acc_done[0], 1);
-        mbar_init(&sh.acc_done[1], 1);
-        mbar_init(&sh.drained[0], 1);
-        mbar_init(&sh.drained[1], 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sh.s_ready[i], 1);
+            mbar_init(&sh.dp_ready[i], 1);
+            mbar_init(&sh.acc_done[i], 1);
+            mbar_init(&sh.drained[i], 1);
+        }
         sh.spoiled = 0;
         sh.stop = aligned ? 0 : 1;
         mbar_init_fence();
@@ -713,7 +705,7 @@ __global__ void __launch_bounds__(384, 1)
     fewer_registers<96>();
     if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
-        uint32_t n = 0, k = 0;                 // tiles, items
+        uint32_t n = 0;                        // tiles
         uint32_t nq = 0, no = 0, nkv = 0;      // loads issued
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -728,7 +720,7 @@ __global__ void __launch_bounds__(384, 1)
             }
             return ok;
         };
-        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++k) {
+        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
             int entry, kvh;
             dkv_item(b, it, slots, front, entry, kvh);
             const int4 range = b.ranges[entry];
@@ -764,7 +756,10 @@ __global__ void __launch_bounds__(384, 1)
                     if (end && h == group - 1) flags |= kLast;
                     if (!announce(row0, flags, entry)) break;
                     if (!loaded) {
-                        if (!wait(&sh.kv_empty, (k & 1) ^ 1)) break;
+                        // the last item's last tile has its S' and dP'
+                        const uint32_t m = n - 1;
+                        if (n > 0 && !(wait(&sh.s_ready[m & 1], m / 2 & 1) && wait(&sh.dp_ready[m & 1], m / 2 & 1)))
+                            break;
                         if (lane == 0) {
                             mbar_expect_tx(&sh.kv_full, 2 * kSlabs * kSlab);
                             for (int i = 0; i < kSlabs; ++i) {
@@ -776,10 +771,14 @@ __global__ void __launch_bounds__(384, 1)
                         ++nkv;
                     }
                     const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
-                    if (!wait(&sh.q_empty[qs], (n / Sh::kQ & 1) ^ 1)) break;
+                    // the Q of tile j is free with tile j + 1's dP' (which its dK precedes), its dO with tile
+                    // j + 1's S' (which its dV precedes) and its own dP'
+                    if (n >= Sh::kQ && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
                     if (lane == 0) load_tile(&maps.q, smem_addr(sh.q[qs]), kSlabs, head, base + row0, &sh.q_full[qs]);
                     ++nq;
-                    if (!wait(&sh.do_empty[os], (n / Sh::kO & 1) ^ 1)) break;
+                    if (n >= Sh::kO && !(wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1) &&
+                                         wait(&sh.s_ready[(n - 1) & 1], (n - 1) / 2 & 1)))
+                        break;
                     if (lane == 0)
                         load_tile(&maps.dout, smem_addr(sh.dout[os]), kSlabs, head, base + row0, &sh.do_full[os]);
                     ++no;
@@ -820,22 +819,20 @@ __global__ void __launch_bounds__(384, 1)
                 mma_halves(leader, acc, scores, first ? smem_addr(sh.dout[op]) : smem_addr(sh.q[qp]), o_shape,
                            !(prev & kFirst));
                 if (prev & kLast) mma_commit(leader, &sh.acc_done[warp - 1]);
-                mma_commit(leader, first ? &sh.do_empty[op] : &sh.q_empty[qp]);
             }
             if (e & kStop) break;
             const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
             if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
             if (first ? !wait(&sh.q_full[qs], n / Sh::kQ & 1) : !wait(&sh.do_full[os], n / Sh::kO & 1)) break;
             mma_scores(leader, scores, key_at, first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
-            mma_commit(leader, first ? &sh.s_ready : &sh.dp_ready);
-            if (!first) mma_commit(leader, &sh.do_empty[os]);
-            if (e & kLast) mma_commit(leader, &sh.kv_empty);
+            mma_commit(leader, first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
             prev = e;
         }
         mma_commit(leader, &sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
     } else if (warp == 3 && aligned) {
         // ------------------------------------------------------------- statistics of the rows
+        int64_t rank_row = 0;
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing, s = n & 1;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_full[slot], n / kRing & 1, stop))) break;
@@ -844,7 +841,8 @@ __global__ void __launch_bounds__(384, 1)
             if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
             if (e.y & kStop) break;
             if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.aux_empty[s], (n / 2 & 1) ^ 1, stop))) break;
-            const int64_t base = static_cast<int64_t>(e.y >> 16) * p.Tpad + e.z % p.P * p.Tp;
+            if (e.y & kFirst) rank_row = e.z % p.P * p.Tp;
+            const int64_t base = static_cast<int64_t>(e.y >> 16) * p.Tpad + rank_row;
             for (int i = lane; i < kTile; i += 32) {
                 const int64_t row = e.x + i;
                 const bool in = row < p.Tp;
@@ -861,6 +859,8 @@ __global__ void __launch_bounds__(384, 1)
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
         const uint32_t s_at = at + 64 * y, dp_at = at + 128 + 64 * y;
         const float c = p.scale * 1.4426950408889634f;
+        int rank = 0, key = 0;
+        int64_t base = 0;
         uint32_t done = 0;
         bool spoiled = false;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
@@ -874,8 +874,11 @@ __global__ void __launch_bounds__(384, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
             if (flags & kStop) break;
-            const int rank = e.z % p.P, key = e.z / p.P * kTile;
-            const int64_t base = rank * p.Tp;
+            if (flags & kFirst) {
+                rank = e.z % p.P;
+                key = e.z / p.P * kTile;
+                base = rank * p.Tp;
+            }
             // bit j of bits[i]: whether this thread's key is seen by row 64 y + 32 i + j
             uint32_t bits[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
             if (!(flags & kFull)) {
@@ -887,11 +890,11 @@ __global__ void __launch_bounds__(384, 1)
                 }
             }
             if (!wait(&sh.aux_full[a], n / 2 & 1)) break;
-            if (!wait(&sh.s_ready, n & 1)) break;
+            if (!wait(&sh.s_ready[n & 1], n / 2 & 1)) break;
             if (flags & kDirty) {
                 // Rows that are not this rank's, or padding, may hold anything: a weight of zero does
                 // not keep a NaN out of a product, so they become zeros.
-                if (!wait(&sh.dp_ready, n & 1)) break;
+                if (!wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
                 const int64_t row = e.x + t;
                 const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
                 if (r.y == 0 && r.w == 0) {
@@ -936,7 +939,7 @@ __global__ void __launch_bounds__(384, 1)
             tmem_wait_stores();
             tmem_fence_before();
             mbar_arrive(&sh.p_ready);
-            if (!wait(&sh.dp_ready, n & 1)) break;
+            if (!wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
             tmem_fence_after();
             uint32_t dp[2][32];
 #pragma unroll

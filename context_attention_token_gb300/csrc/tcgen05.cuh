@@ -65,9 +65,12 @@ __device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, ui
         : "memory");
 }
 
-// One warp issues every matrix instruction, so the loops are unrolled and
-// the descriptors advance by constants: with address arithmetic in the loop an
-// instruction took 100 cycles to issue, against 64 to run.
+// A product of 128 x 128 x 16 takes 64 cycles, and a warp can run ahead of the
+// matrix unit by about two of them. So that they follow one another without
+// gaps the loops are unrolled, the descriptors advance by constants (with address
+// arithmetic in the loop an instruction took 100 cycles to issue), and commits,
+// which cost some 20 cycles each, are few: one commit stands for everything
+// that its warp issued before it.
 
 // A descriptor as a value that the compiler does not look into: with nvcc 13.0 a
 // tile at a constant shared address got wrong bits once sums with it were
@@ -80,13 +83,28 @@ __device__ __forceinline__ uint64_t opaque(uint64_t desc)
 
 // Rows x columns of scores: both operands from shared memory, `steps` (at most
 // 8) inner steps of 16, the second slab after four.
+template <int STEPS>
+__device__ __forceinline__ void mma_scores_fixed(bool leader, uint32_t d, uint64_t da, uint64_t db, uint32_t shape)
+{
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        mma_smem(leader, d, da + at, db + at, shape, k > 0);
+    }
+}
+
 __device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
     const uint64_t da = opaque(desc_inner(a)), db = opaque(desc_inner(b));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        if (k < steps) mma_smem(leader, d, da + at, db + at, shape, k > 0);
+    if (steps == 8) {
+        mma_scores_fixed<8>(leader, d, da, db, shape);
+    } else if (steps == 4) {
+        mma_scores_fixed<4>(leader, d, da, db, shape);
+    } else {
+        for (int k = 0; k < steps; ++k) {
+            const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+            mma_smem(leader, d, da + at, db + at, shape, k > 0);
+        }
     }
 }
 
