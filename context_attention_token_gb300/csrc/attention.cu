@@ -293,11 +293,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
-                mma_weights<0, 4, 0>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
+                mma_weights(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
                 if (!wait(&sh.p_ready[x], ps & 1)) break;
                 ++ps;
                 tmem_fence_after();
-                mma_weights<4, 8, 0>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, true);
+                mma_weights(leader, o_at, s_at + 32, kv_at + vs * Sh::kTileBytes + 8192, o_shape, true);
                 started = true;
             }
             if (prev & kLast) mma_commit(leader, &sh.out_done[x]);
@@ -373,33 +373,35 @@ __global__ void __launch_bounds__(384, 1)
                 // the last tile's PV is done too
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1, stop))) break;
                 tmem_fence_after();
-                uint32_t s[4][32];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_load32(s_at + 32 * i, s[i]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) tmem_wait_loads(s[i]);
-                if (!(flags & (kFull << x))) {
-                    const int a0 = r.x - e.x, a1 = r.y - e.x, b0 = r.z - e.x, b1 = r.w - e.x;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t bits = span_bits(a0, a1, i) | span_bits(b0, b1, i);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
-                    }
-                }
                 // A row's reference is the largest score of the first tile that it sees (times c). The
                 // weights of later tiles may pass 1: only their sum is watched, and once it
                 // is past 2^40 reference, sum and O are scaled by a power of two. So no tile but the
                 // first waits for its maximum. Weights that pass 2^127 within one tile end as an
                 // infinity or NaN in the output and the row is computed again below.
+                const int a0 = r.x - e.x, a1 = r.y - e.x, b0 = r.z - e.x, b1 = r.w - e.x;
+                const bool full = (flags & (kFull << x)) != 0;
+                auto load = [&](int i, uint32_t (&s)[32]) {
+                    tmem_load32(s_at + 32 * i, s);
+                };
+                auto hide = [&](int i, uint32_t (&s)[32]) {
+                    if (full) return;
+                    const uint32_t bits = span_bits(a0, a1, i) | span_bits(b0, b1, i);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        if (!(bits >> j & 1)) s[j] = 0xFF800000u;
+                };
                 if (__any_sync(0xFFFFFFFFu, ref == -INFINITY)) {
                     float mx = -INFINITY;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
+#pragma unroll 1
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t s[32];
+                        load(i, s);
+                        tmem_wait_loads(s);
+                        hide(i, s);
 #pragma unroll
                         for (int j = 0; j < 32; j += 2)
-                            mx = fmaxf(mx, fmaxf(__uint_as_float(s[i][j]), __uint_as_float(s[i][j + 1])));
+                            mx = fmaxf(mx, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+                    }
                     if (ref == -INFINITY) ref = mx * c;
                 }
                 const bool big = l > 1.0995116e12f && l < INFINITY;
@@ -419,29 +421,38 @@ __global__ void __launch_bounds__(384, 1)
                 const float mc = ref == -INFINITY ? 0.0f : ref;
                 const F2 c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
                 F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
+                auto weigh = [&](int i, uint32_t (&s)[32]) {
+                    hide(i, s);
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
-                        const float2 a = both(fma2(pair_of(s[i][2 * j], s[i][2 * j + 1]), c2, mc2));
+                        const float2 a = both(fma2(pair_of(s[2 * j], s[2 * j + 1]), c2, mc2));
                         const float x0 = exp2_fast(a.x), x1 = exp2_fast(a.y);
                         sum[j & 1] = add2(sum[j & 1], pair_of(x0, x1));
                         // weights are rounded to bf16 for the matrix instruction; their sum is not
                         w[j] = pack_bf16x2(x0, x1);
                     }
                     tmem_store16(s_at + 16 * i, w);
-                    if (i == 1) {   // the product can begin with the first 64 keys
-                        tmem_wait_stores();
-                        tmem_fence_before();
-                        mbar_arrive(&sh.p_half[x]);
-                    }
+                };
+                // Weights go over scores that are in registers already. A loop and not 128 columns of
+                // straight code: the instruction caches are shared with the issuers.
+                uint32_t s0[32], s1[32];
+                load(0, s0);
+#pragma unroll 1
+                for (int i = 0; i < 4; i += 2) {
+                    tmem_wait_loads(s0);
+                    load(i + 1, s1);
+                    weigh(i, s0);
+                    tmem_wait_loads(s1);
+                    if (i == 0) load(2, s0);
+                    weigh(i + 1, s1);
+                    tmem_wait_stores();
+                    tmem_fence_before();
+                    // the product can begin with the first 64 keys
+                    mbar_arrive(i == 0 ? &sh.p_half[x] : &sh.p_ready[x]);
                 }
                 const float2 total = both(add2(sum[0], sum[1]));
                 l += total.x + total.y;
-                tmem_wait_stores();
-                tmem_fence_before();
-                mbar_arrive(&sh.p_ready[x]);
                 used = true;
             }
             if (flags & (3 * kNeed)) ++j_tile;

@@ -247,7 +247,8 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
 // first half of the columns of scores that it came from.
 __device__ __forceinline__ void mma_halves(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-    mma_weights<0, 8, 32>(leader, d, a, b, shape, add);
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) mma_weights(leader, d, a + 64 * h, b + 8192 * h, shape, add || h > 0);
 }
 
 // 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)

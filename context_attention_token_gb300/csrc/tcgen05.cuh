@@ -21,19 +21,25 @@ constexpr uint32_t kSlab = 128 * 128;      // bytes of 128 rows x 64 bf16
 // ----------------------------------------------------------------- descriptors
 
 // Shared-memory operand with 128-byte swizzle whose inner dimension is
-// contiguous: groups of 8 rows are 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_inner(uint32_t addr)
+// contiguous: groups of 8 rows are 1024 bytes apart. The address is made opaque:
+// with nvcc 13.0 a tile at a constant shared address got wrong bits once sums
+// with it were folded into constants.
+constexpr uint32_t kInnerUpper = 64u | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ uint32_t inner_lower(uint32_t addr)
 {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (1ull << 16) | (64ull << 32) | (1ull << 46) |
-           (2ull << 61);
+    asm volatile("" : "+r"(addr));
+    return (addr >> 4) | (1u << 16);
 }
 
 // The same bytes read across: the outer dimension contiguous in blocks of 64
 // one slab apart, groups of 8 inner rows 1024 bytes apart.
-__device__ __forceinline__ uint64_t desc_outer(uint32_t addr)
+constexpr uint32_t kOuterUpper = kInnerUpper;
+
+__device__ __forceinline__ uint32_t outer_lower(uint32_t addr)
 {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFF) | (static_cast<uint64_t>(kSlab >> 4) << 16) |
-           (64ull << 32) | (1ull << 46) | (2ull << 61);
+    asm volatile("" : "+r"(addr));
+    return (addr >> 4) | ((kSlab >> 4) << 16);
 }
 
 // bf16 x bf16 into binary32, 128 rows, n columns (a multiple of 16).
@@ -47,76 +53,67 @@ __device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_outer)
 // The whole warp runs the issuing code, so that addresses and descriptors stay
 // in uniform registers; its lane 0 (`leader`) alone issues.
 
-__device__ __forceinline__ void mma_smem(bool leader, uint32_t d, uint64_t a, uint64_t b, uint32_t shape, bool add)
+// Descriptors come as two words: the lower one moves with the address, the
+// upper one is constant.
+
+__device__ __forceinline__ void mma_smem(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
+                                         uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-        "l"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
+        "{ .reg .pred p, q; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};\n"
+        "setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, uint64_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
+                                         uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p, q; setp.ne.b32 p, %4, 0; setp.ne.b32 q, %5, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(d),
-        "r"(a), "l"(b), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
+        "{ .reg .pred p, q; .reg .b64 b; mov.b64 b, {%2, %3};\n"
+        "setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0;\n"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
         : "memory");
 }
 
 // A product of 128 x 128 x 16 takes 64 cycles, and a warp can run ahead of the
 // matrix unit by about two of them. So that they follow one another without
-// gaps the loops are unrolled, the descriptors advance by constants (with address
-// arithmetic in the loop an instruction took 100 cycles to issue), and commits,
-// which cost some 20 cycles each, are few: one commit stands for everything
-// that its warp issued before it.
-
-// A descriptor as a value that the compiler does not look into: with nvcc 13.0 a
-// tile at a constant shared address got wrong bits once sums with it were
-// folded into constants.
-__device__ __forceinline__ uint64_t opaque(uint64_t desc)
-{
-    asm volatile("" : "+l"(desc));
-    return desc;
-}
+// gaps, descriptors advance by constants (with address arithmetic in the loop an
+// instruction took 100 cycles to issue), loops are unrolled four times and no
+// more (the instruction caches are shared with the softmax), and commits, which
+// cost some 20 cycles each, are few: one commit stands for everything that its
+// warp issued before it.
 
 // Rows x columns of scores: both operands from shared memory, `steps` (at most
-// 8) inner steps of 16, the second slab after four.
-template <int STEPS>
-__device__ __forceinline__ void mma_scores_fixed(bool leader, uint32_t d, uint64_t da, uint64_t db, uint32_t shape)
-{
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        mma_smem(leader, d, da + at, db + at, shape, k > 0);
-    }
-}
-
+// 8) inner steps of 16, four to a slab.
 __device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
-    const uint64_t da = opaque(desc_inner(a)), db = opaque(desc_inner(b));
-    if (steps == 8) {
-        mma_scores_fixed<8>(leader, d, da, db, shape);
-    } else if (steps == 4) {
-        mma_scores_fixed<4>(leader, d, da, db, shape);
-    } else {
-        for (int k = 0; k < steps; ++k) {
-            const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-            mma_smem(leader, d, da + at, db + at, shape, k > 0);
+    uint32_t da = inner_lower(a), db = inner_lower(b);
+#pragma unroll 1
+    for (int k = 0; k < steps; k += 4) {
+        if (k + 4 <= steps) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma_smem(leader, d, da + 2 * i, db + 2 * i, kInnerUpper, shape, i > 0 || k > 0);
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < steps - k; ++i)
+                mma_smem(leader, d, da + 2 * i, db + 2 * i, kInnerUpper, shape, i > 0 || k > 0);
         }
+        da += kSlab >> 4;
+        db += kSlab >> 4;
     }
 }
 
-// d (+)= A B over inner steps [FROM, TO) of 16: A from tensor memory, 8 columns
-// a step (the second half of the steps GAP columns further), B read across.
-template <int FROM, int TO, int GAP>
+// d (+)= A B over four inner steps of 16: A from tensor memory, 8 columns a
+// step, B read across.
 __device__ __forceinline__ void mma_weights(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-    const uint64_t db = opaque(desc_outer(b));
+    const uint32_t db = outer_lower(b);
 #pragma unroll
-    for (int k = FROM; k < TO; ++k)
-        mma_tmem(leader, d, a + 8 * k + (k >> 2) * GAP, db + k * (2048 >> 4), shape, k > FROM || add);
+    for (int k = 0; k < 4; ++k)
+        mma_tmem(leader, d, a + 8 * k, db + k * (2048 >> 4), kOuterUpper, shape, k > 0 || add);
 }
 
 // An arrival on `bar` once every matrix instruction issued so far by this
