@@ -247,7 +247,7 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
 // first half of the columns of scores that it came from.
 __device__ __forceinline__ void mma_halves(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-#pragma unroll 1
+#pragma unroll
     for (int h = 0; h < 2; ++h) mma_weights(leader, d, a + 64 * h, b + 8192 * h, shape, add || h > 0);
 }
 

@@ -80,29 +80,36 @@ __device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, ui
 
 // A product of 128 x 128 x 16 takes 64 cycles, and a warp can run ahead of the
 // matrix unit by about two of them. So that they follow one another without
-// gaps, descriptors advance by constants (with address arithmetic in the loop an
-// instruction took 100 cycles to issue), loops are unrolled four times and no
-// more (the instruction caches are shared with the softmax), and commits, which
-// cost some 20 cycles each, are few: one commit stands for everything that its
-// warp issued before it.
+// gaps while the softmax takes its share of the issue slots, loops are unrolled
+// and descriptors advance by constants (with address arithmetic in the loop an
+// instruction took 100 cycles to issue, with a loop of four 75), and commits,
+// which cost some 20 cycles each, are few: one commit stands for everything that
+// its warp issued before it.
+
+template <int STEPS>
+__device__ __forceinline__ void mma_scores_fixed(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape)
+{
+#pragma unroll
+    for (int k = 0; k < STEPS; ++k) {
+        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        mma_smem(leader, d, a + at, b + at, kInnerUpper, shape, k > 0);
+    }
+}
 
 // Rows x columns of scores: both operands from shared memory, `steps` (at most
 // 8) inner steps of 16, four to a slab.
 __device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
-    uint32_t da = inner_lower(a), db = inner_lower(b);
-#pragma unroll 1
-    for (int k = 0; k < steps; k += 4) {
-        if (k + 4 <= steps) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) mma_smem(leader, d, da + 2 * i, db + 2 * i, kInnerUpper, shape, i > 0 || k > 0);
-        } else {
-#pragma unroll 1
-            for (int i = 0; i < steps - k; ++i)
-                mma_smem(leader, d, da + 2 * i, db + 2 * i, kInnerUpper, shape, i > 0 || k > 0);
+    const uint32_t da = inner_lower(a), db = inner_lower(b);
+    if (steps == 8) {
+        mma_scores_fixed<8>(leader, d, da, db, shape);
+    } else if (steps == 4) {
+        mma_scores_fixed<4>(leader, d, da, db, shape);
+    } else {
+        for (int k = 0; k < steps; ++k) {
+            const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+            mma_smem(leader, d, da + at, db + at, kInnerUpper, shape, k > 0);
         }
-        da += kSlab >> 4;
-        db += kSlab >> 4;
     }
 }
 
