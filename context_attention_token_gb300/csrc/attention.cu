@@ -293,11 +293,11 @@ __global__ void __launch_bounds__(384, 1)
             if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
-                mma_weights(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
+                mma_weights<4>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
                 if (!wait(&sh.p_ready[x], ps & 1)) break;
                 ++ps;
                 tmem_fence_after();
-                mma_weights(leader, o_at, s_at + 32, kv_at + vs * Sh::kTileBytes + 8192, o_shape, true);
+                mma_weights<4>(leader, o_at, s_at + 32, kv_at + vs * Sh::kTileBytes + 8192, o_shape, true);
                 started = true;
             }
             if (prev & kLast) mma_commit(leader, &sh.out_done[x]);

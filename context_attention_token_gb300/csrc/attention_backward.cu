@@ -100,11 +100,11 @@ constexpr int kPrepRows = 32;   // rows of one block: 8 lanes each
 // Rows: delta and the base-2 log-sum-exp of every (head, row), the spans of
 // keys that a row sees, zeros in the writers' padding positions. A row that
 // sees nothing gets lse2 = +inf, which makes all its weights zero.
-__global__ void __launch_bounds__(8 * kPrepRows) rows_kernel(const __grid_constant__ Params b)
+__device__ __forceinline__ void prepare_rows(const Params &b, int64_t block)
 {
     const AttentionParams &p = b.a;
-    const int head = static_cast<int>(blockIdx.x % p.Hq);
-    const int64_t row = blockIdx.x / p.Hq * kPrepRows + threadIdx.x / 8;
+    const int head = static_cast<int>(block % p.Hq);
+    const int64_t row = block / p.Hq * kPrepRows + threadIdx.x / 8;
     const int lane = threadIdx.x & 7;
     float d = 0.0f;
     const bool in = row < p.Tpad;
@@ -170,11 +170,11 @@ __device__ __forceinline__ int32_t position_of_token(const Params &b, int32_t j)
 // The others go into a list, those with a range of sinks (the long ones) from
 // its front, the rest from its back. The order of the list sets which CTA takes
 // a tile and no result.
-__global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Params b, int tiles)
+__device__ __forceinline__ void prepare_tile(const Params &b, int block, int tiles)
 {
     const AttentionParams &p = b.a;
     __shared__ int any;
-    const int rank = static_cast<int>(blockIdx.x % p.P), tile = static_cast<int>(blockIdx.x / p.P);
+    const int rank = block % p.P, tile = block / p.P;
     const int32_t k0 = tile * kTile, k1 = static_cast<int32_t>(min((int64_t)k0 + kTile, p.T)) - 1;
     if (threadIdx.x == 0) {
         const int32_t d0 = find_doc(p.cu, p.n_docs, k0), d1 = find_doc(p.cu, p.n_docs, k1);
@@ -221,6 +221,15 @@ __global__ void __launch_bounds__(256) tiles_kernel(const __grid_constant__ Para
     }
 }
 
+// One launch for both, the tiles first: they are few, and their zeros are the
+// larger part of the writes.
+__global__ void __launch_bounds__(8 * kPrepRows) prepare_kernel(const __grid_constant__ Params b, int tiles)
+{
+    const int slots = tiles * b.a.P;
+    if (static_cast<int64_t>(blockIdx.x) < slots) prepare_tile(b, blockIdx.x, tiles);
+    else prepare_rows(b, static_cast<int64_t>(blockIdx.x) - slots);
+}
+
 // ----------------------------------------------------------------- shared by both kernels
 
 constexpr int kRing = 8;       // tile announcements in flight
@@ -243,12 +252,14 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
     for (int i = 0; i < slabs; ++i) tma_slab(to + i * kSlab, map, 64 * i, head, static_cast<int>(row), bar);
 }
 
-// The weights of a tile lie as two halves of 64 inner columns, each over the
-// first half of the columns of scores that it came from.
-__device__ __forceinline__ void mma_halves(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+// The weights of a tile lie as two halves of 64 inner columns (one for each
+// warpgroup), each over the first half of the columns of scores it came from.
+// One PART is the first or second 32 inner columns of both.
+template <int PART>
+__device__ __forceinline__ void mma_part(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) mma_weights(leader, d, a + 64 * h, b + 8192 * h, shape, add || h > 0);
+    mma_weights<2>(leader, d, a + 16 * PART, b + 4096 * PART, shape, add);
+    mma_weights<2>(leader, d, a + 64 + 16 * PART, b + 8192 + 4096 * PART, shape, true);
 }
 
 // 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)
@@ -267,13 +278,6 @@ __device__ __forceinline__ void store_columns(uint16_t *row, int at, int D, uint
     if (!write) return;
     *reinterpret_cast<uint4 *>(row + at) = make_uint4(w[0], w[1], w[2], w[3]);
     if (at + 8 < D) *reinterpret_cast<uint4 *>(row + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
-__device__ bool spoiled_row(const uint16_t *row, int D)
-{
-    bool bad = false;
-    for (int i = 0; i < D; ++i) bad |= (row[i] & 0x7F80) == 0x7F80;
-    return bad;
 }
 
 // The bits of a 32 x 32 matrix, one row per lane, transposed.
@@ -488,7 +492,8 @@ __global__ void __launch_bounds__(384, 1)
                 if (!wait(&sh.ds_ready, i & 1)) break;
                 tmem_fence_after();
                 const uint32_t e = flags[i & 1], ks = i % Sh::kK;
-                mma_halves(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
+                mma_part<0>(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
+                mma_part<1>(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, true);
                 if (e & kLast) mma_commit(leader, &sh.acc_done);
                 mma_commit(leader, &sh.k_empty[ks]);
                 if (more) more = issue_s();
@@ -612,14 +617,7 @@ __global__ void __launch_bounds__(384, 1)
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
     }
-    if (sh.spoiled == 0) return;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const DqItem d = dq_item(p, it, row_tiles);
-        for (int i = warp; i < kTile && d.row0 + i < p.Tp; i += 12) {
-            const int64_t row = d.rank * p.Tp + d.row0 + i;
-            if (spoiled_row(row_of(b.dq, row, p.Hq, d.head, p.D), p.D)) row_dq(b, row, d.head);
-        }
-    }
+    if (threadIdx.x == 0 && sh.spoiled != 0) b.counters[3] = 1;
 }
 
 // ----------------------------------------------------------------- dK and dV
@@ -644,7 +642,8 @@ struct DkvShared {
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t aux_full[2], aux_empty[2];
     uint64_t s_ready[2], dp_ready[2];  // S' and dV of the tile before, dP' and dK of it: by tile parity
-    uint64_t p_ready, ds_ready, acc_done[2], drained[2];
+    uint64_t half[2], whole[2];        // P and dS in tensor memory: the first 32 columns of both halves, all
+    uint64_t acc_done[2], drained[2];
     int4 info[kRing];              // first row, flags and head, tile * P + rank
     uint32_t tmem, stop, spoiled;
 };
@@ -681,11 +680,11 @@ __global__ void __launch_bounds__(384, 1)
             mbar_init(&sh.aux_full[i], 32);
             mbar_init(&sh.aux_empty[i], 8);
         }
-        mbar_init(&sh.p_ready, 2 * kTile);
-        mbar_init(&sh.ds_ready, 2 * kTile);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_ready[i], 1);
             mbar_init(&sh.dp_ready[i], 1);
+            mbar_init(&sh.half[i], 2 * kTile);
+            mbar_init(&sh.whole[i], 2 * kTile);
             mbar_init(&sh.acc_done[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
@@ -721,7 +720,13 @@ __global__ void __launch_bounds__(384, 1)
             }
             return ok;
         };
-        for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x) {
+        // Items are as long as the rows that see their keys are many, so each is taken when the CTA is
+        // free for it (dealt out in turn, the CTAs ended up to a fifth apart). The number of the next one
+        // is asked for an item ahead.
+        int64_t it = blockIdx.x;
+        while (ok && it < items) {
+            int ahead = 0;
+            if (lane == 0) ahead = atomicAdd(&b.counters[2], 1);
             int entry, kvh;
             dkv_item(b, it, slots, front, entry, kvh);
             const int4 range = b.ranges[entry];
@@ -787,6 +792,7 @@ __global__ void __launch_bounds__(384, 1)
                     if (end) break;
                 }
             }
+            it = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, ahead, 0);
         }
         if (ok) announce(0, kStop, 0);
         if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
@@ -813,18 +819,25 @@ __global__ void __launch_bounds__(384, 1)
             const uint32_t e = static_cast<uint32_t>(sh.info[slot].y);
             __syncwarp();
             if (leader) mbar_arrive(&sh.info_empty[slot]);
+            const uint32_t i = n - 1, qs = n % Sh::kQ, os = n % Sh::kO;
+            const bool fresh = (e & kFirst) != 0, more = !(e & kStop);
+            // before a new item's K and V, the last one's products
+            auto operand = [&]() {
+                return first ? wait(&sh.q_full[qs], n / Sh::kQ & 1) : wait(&sh.do_full[os], n / Sh::kO & 1);
+            };
+            if (more && !fresh && !operand()) break;
             if (n > 0) {
-                const uint32_t i = n - 1, qp = i % Sh::kQ, op = i % Sh::kO;
-                if (!wait(first ? &sh.p_ready : &sh.ds_ready, i & 1)) break;
+                const uint32_t with = first ? smem_addr(sh.dout[i % Sh::kO]) : smem_addr(sh.q[i % Sh::kQ]);
+                if (!wait(&sh.half[warp - 1], i & 1)) break;
                 tmem_fence_after();
-                mma_halves(leader, acc, scores, first ? smem_addr(sh.dout[op]) : smem_addr(sh.q[qp]), o_shape,
-                           !(prev & kFirst));
+                mma_part<0>(leader, acc, scores, with, o_shape, !(prev & kFirst));
+                if (!wait(&sh.whole[warp - 1], i & 1)) break;
+                tmem_fence_after();
+                mma_part<1>(leader, acc, scores, with, o_shape, true);
                 if (prev & kLast) mma_commit(leader, &sh.acc_done[warp - 1]);
             }
-            if (e & kStop) break;
-            const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
-            if ((e & kFirst) && !wait(&sh.kv_full, k++ & 1)) break;
-            if (first ? !wait(&sh.q_full[qs], n / Sh::kQ & 1) : !wait(&sh.do_full[os], n / Sh::kO & 1)) break;
+            if (!more) break;
+            if (fresh && !(wait(&sh.kv_full, k++ & 1) && operand())) break;
             mma_scores(leader, scores, key_at, first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
             mma_commit(leader, first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
             prev = e;
@@ -936,10 +949,10 @@ __global__ void __launch_bounds__(384, 1)
                     for (int h = 0; h < 4; ++h) s[i][4 * j + h] = __float_as_uint(pr[h]);
                 }
                 tmem_store16(s_at + 16 * i, w);
+                tmem_wait_stores();
+                tmem_fence_before();
+                mbar_arrive(i == 0 ? &sh.half[0] : &sh.whole[0]);
             }
-            tmem_wait_stores();
-            tmem_fence_before();
-            mbar_arrive(&sh.p_ready);
             if (!wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
             tmem_fence_after();
             uint32_t dp[2][32];
@@ -969,10 +982,10 @@ __global__ void __launch_bounds__(384, 1)
                     w[2 * j + 1] = pack_bf16x2(v.x, v.y);
                 }
                 tmem_store16(dp_at + 16 * i, w);
+                tmem_wait_stores();
+                tmem_fence_before();
+                mbar_arrive(i == 0 ? &sh.half[1] : &sh.whole[1]);
             }
-            tmem_wait_stores();
-            tmem_fence_before();
-            mbar_arrive(&sh.ds_ready);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.aux_empty[a]);
             if (flags & kLast) {
@@ -996,18 +1009,41 @@ __global__ void __launch_bounds__(384, 1)
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
     }
-    if (sh.spoiled == 0) return;
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        int entry, kvh;
-        dkv_item(b, it, slots, front, entry, kvh);
-        const int rank = entry % p.P, key = entry / p.P * kTile;
-        for (int i = warp; i < kTile && key + i < p.T; i += 12) {
-            const int32_t pos = position_of_token(b, key + i);
-            if (pos < 0) continue;
-            if (spoiled_row(row_of(b.dk[rank], pos, p.Hkv, kvh, p.D), p.D) ||
-                spoiled_row(row_of(b.dv[rank], pos, p.Hkv, kvh, p.D), p.D))
-                key_dkdv(b, key + i, rank, kvh);
-        }
+    if (threadIdx.x == 0 && sh.spoiled != 0) b.counters[3] = 1;
+}
+
+// ----------------------------------------------------------------- repair
+//
+// Only where the kernels above have seen an infinity or NaN in an output: all
+// rows that hold one are computed again from the definitions, without a
+// multiplication by what is hidden. Without one the launch ends at once.
+
+__device__ bool spoiled_row(const uint16_t *row, int D)
+{
+    const int at = (threadIdx.x & 31) * 4;
+    bool bad = false;
+    if (at < D)
+        for (int i = 0; i < 4; ++i) bad |= (row[at + i] & 0x7F80) == 0x7F80;
+    return __any_sync(0xFFFFFFFFu, bad);
+}
+
+__global__ void __launch_bounds__(256) repair_kernel(const __grid_constant__ Params b)
+{
+    if (b.counters[3] == 0) return;
+    const AttentionParams &p = b.a;
+    const int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32, warps = gridDim.x * 8ll;
+    for (int64_t i = warp; i < p.Tpad * p.Hq; i += warps) {
+        const int64_t row = i / p.Hq;
+        const int head = static_cast<int>(i % p.Hq);
+        if (p.l2r[row] >= 0 && spoiled_row(row_of(b.dq, row, p.Hq, head, p.D), p.D)) row_dq(b, row, head);
+    }
+    for (int64_t i = warp; i < p.T * p.Hkv * p.P; i += warps) {
+        const int32_t key = static_cast<int32_t>(i / p.Hkv / p.P);
+        const int rank = static_cast<int>(i / p.Hkv % p.P), kvh = static_cast<int>(i % p.Hkv);
+        const int32_t pos = position_of_token(b, key);
+        if (pos >= 0 && (spoiled_row(row_of(b.dk[rank], pos, p.Hkv, kvh, p.D), p.D) ||
+                         spoiled_row(row_of(b.dv[rank], pos, p.Hkv, kvh, p.D), p.D)))
+            key_dkdv(b, key, rank, kvh);
     }
 }
 
@@ -1043,7 +1079,7 @@ int64_t align256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
 }  // namespace
 
 // delta and lse2 of every (head, row), the spans of every row, the ranges and
-// the list of every (tile, rank), two counters.
+// the list of every (tile, rank), four counters.
 int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq)
 {
     const int64_t slots = (T + kTile - 1) / kTile * P;
@@ -1075,12 +1111,14 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     if (e == cudaSuccess) e = make_slab_map(&maps.dout, b.dout, p.D, p.Hq, p.Tpad);
     if (e != cudaSuccess) return e;
     const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * p.Hq;
-    if (row_blocks > 0x7FFFFFFF || slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    if ((e = cudaMemsetAsync(b.counters, 0, 8, stream)) != cudaSuccess) return e;
-    rows_kernel<<<static_cast<unsigned>(row_blocks), 8 * kPrepRows, 0, stream>>>(b);
-    tiles_kernel<<<static_cast<unsigned>(slots), 256, 0, stream>>>(b, tiles);
+    if (row_blocks + slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    if ((e = cudaMemsetAsync(b.counters, 0, 16, stream)) != cudaSuccess) return e;
+    prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(b, tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    return p.D <= 64 ? launch_tiled<64>(b, maps, tiles, stream) : launch_tiled<128>(b, maps, tiles, stream);
+    e = p.D <= 64 ? launch_tiled<64>(b, maps, tiles, stream) : launch_tiled<128>(b, maps, tiles, stream);
+    if (e != cudaSuccess) return e;
+    repair_kernel<<<static_cast<unsigned>(4 * sm_count(-1)), 256, 0, stream>>>(b);
+    return cudaGetLastError();
 }
 
 cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset)

@@ -174,7 +174,8 @@ struct AttentionBackwardParams {
     float *delta, *lse2;           // [Hq][Tpad]
     int4 *spans;                   // [Tpad] keys every row sees
     int4 *ranges;                  // [key tiles][P] rows that see a tile
-    int32_t *list, *counters;      // tiles that some row sees
+    int32_t *list;                 // tiles that some row sees, long ones from the front, others from the back
+    int32_t *counters;             // of both parts, items taken, whether an output is to be computed again
 };
 int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq);
 cudaError_t launch_attention_backward(AttentionBackwardParams p, void *workspace, cudaStream_t stream);

@@ -113,13 +113,14 @@ __device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, 
     }
 }
 
-// d (+)= A B over four inner steps of 16: A from tensor memory, 8 columns a
+// d (+)= A B over STEPS inner steps of 16: A from tensor memory, 8 columns a
 // step, B read across.
+template <int STEPS>
 __device__ __forceinline__ void mma_weights(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
     const uint32_t db = outer_lower(b);
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < STEPS; ++k)
         mma_tmem(leader, d, a + 8 * k, db + k * (2048 >> 4), kOuterUpper, shape, k > 0 || add);
 }
 
