@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(384, 1)
         uint32_t k = 0, j_tile = 0;   // items, tiles
         int4 r = make_int4(0, 0, 0, 0);
         float ref = -INFINITY, l = 0.0f;   // the weights are 2^(score c - ref)
-        bool used = false, spoiled = false, done = false;
+        bool spoiled = false, done = false;
         int64_t it = blockIdx.x;
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing;
@@ -367,7 +367,6 @@ __global__ void __launch_bounds__(384, 1)
                 ++k;
                 ref = -INFINITY;
                 l = 0.0f;
-                used = false;
             }
             if (flags & (kNeed << x)) {
                 // the last tile's PV is done too
@@ -453,7 +452,6 @@ __global__ void __launch_bounds__(384, 1)
                 }
                 const float2 total = both(add2(sum[0], sum[1]));
                 l += total.x + total.y;
-                used = true;
             }
             if (flags & (3 * kNeed)) ++j_tile;
             if (flags & kLast) {
@@ -467,23 +465,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.out_done[x], k - 1 & 1, stop))) break;
                 tmem_fence_after();
                 uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
-                for (int i = 0; i < steps; ++i) {
-                    uint32_t o[16] = {};
-                    if (used) tmem_load16(o_at + 16 * i, o);
-                    uint32_t w[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float a = sees_any ? __uint_as_float(o[2 * j]) * inv : 0.0f;
-                        const float b = sees_any ? __uint_as_float(o[2 * j + 1]) * inv : 0.0f;
-                        bad = __fmaf_rn(a, 0.0f, __fmaf_rn(b, 0.0f, bad));
-                        w[j] = pack_bf16x2(a, b);
-                    }
-                    if (valid) {
-                        *reinterpret_cast<uint4 *>(out + 16 * i) = make_uint4(w[0], w[1], w[2], w[3]);
-                        if (16 * i + 8 < p.D)
-                            *reinterpret_cast<uint4 *>(out + 16 * i + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-                    }
-                }
+                for (int i = 0; 32 * i < p.D; ++i) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
                 if (valid)
                     p.lse[head * p.Tpad + row] =
                         sees_any && l != 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;

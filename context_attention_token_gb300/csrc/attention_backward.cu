@@ -262,24 +262,6 @@ __device__ __forceinline__ void mma_part(bool leader, uint32_t d, uint32_t a, ui
     mma_weights<2>(leader, d, a + 64 + 16 * PART, b + 8192 + 4096 * PART, shape, true);
 }
 
-// 16 columns of an accumulator, scaled and rounded, to 16 (or the last 8)
-// elements of a row.
-__device__ __forceinline__ void store_columns(uint16_t *row, int at, int D, uint32_t tmem, float scale, bool write,
-                                              float &bad)
-{
-    uint32_t o[16], w[8];
-    tmem_load16(tmem + at, o);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float x = __uint_as_float(o[2 * j]) * scale, y = __uint_as_float(o[2 * j + 1]) * scale;
-        bad = __fmaf_rn(x, 0.0f, __fmaf_rn(y, 0.0f, bad));   // NaN once anything is not finite
-        w[j] = pack_bf16x2(x, y);
-    }
-    if (!write) return;
-    *reinterpret_cast<uint4 *>(row + at) = make_uint4(w[0], w[1], w[2], w[3]);
-    if (at + 8 < D) *reinterpret_cast<uint4 *>(row + at + 8) = make_uint4(w[4], w[5], w[6], w[7]);
-}
-
 // The bits of a 32 x 32 matrix, one row per lane, transposed.
 __device__ __forceinline__ uint32_t transpose_bits(uint32_t x)
 {
@@ -603,8 +585,7 @@ __global__ void __launch_bounds__(384, 1)
                 float bad = 0.0f;
                 const bool write = valid && (r.y != 0 || r.w != 0);
                 uint16_t *out = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, p.D));
-                for (int i = y; i < steps; i += 2)
-                    store_columns(out, 16 * i, p.D, at + 384, p.scale, write, bad);
+                for (int i = y; 32 * i < p.D; i += 2) store_block(at + 384, i, p.D, p.scale, write, out, write, bad);
                 tmem_fence_before();
                 spoiled |= write && bad != 0.0f;
             }
@@ -706,7 +687,7 @@ __global__ void __launch_bounds__(384, 1)
     if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0;                        // tiles
-        uint32_t nq = 0, no = 0, nkv = 0;      // loads issued
+        uint32_t nq = 0, nkv = 0;              // loads issued
         bool ok = true;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
@@ -732,65 +713,66 @@ __global__ void __launch_bounds__(384, 1)
             const int4 range = b.ranges[entry];
             const int rank = entry % p.P, key = entry / p.P * kTile;
             const int64_t base = rank * p.Tp;
-            bool loaded = false;
-            for (int h = 0; ok && h < group; ++h) {
-                const int head = kvh * group + h;
-                int from = range.x, to = range.y;
-                while (ok) {
-                    // whether all rows see all keys, and whether some are not rows of this rank
-                    bool full = true, dirty = false;
+            int4 r[4];
+            auto load_spans = [&](int from) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int64_t row = from + lane + 32 * i;
-                        const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
-                        full &= (r.x <= key && r.y >= key + kTile) || (r.z <= key && r.w >= key + kTile);
-                        dirty |= r.y == 0 && r.w == 0;
-                    }
-                    uint32_t flags = static_cast<uint32_t>(head) << 16;
-                    if (__all_sync(0xFFFFFFFFu, full)) flags |= kFull;
-                    if (__any_sync(0xFFFFFFFFu, dirty)) flags |= kDirty;
-                    if (!loaded) flags |= kFirst;
-                    const int row0 = from;
-                    from += kTile;
-                    bool end = from >= to;
-                    if (end && to == range.y && range.w > from) {
+                for (int i = 0; i < 4; ++i) {
+                    const int64_t row = from + lane + 32 * i;
+                    r[i] = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
+                }
+            };
+            int h = 0, from = range.x, to = range.y;
+            load_spans(from);
+            for (uint32_t first = kFirst; ok; first = 0) {
+                // whether all rows see all keys, and whether some are not rows of this rank
+                bool full = true, dirty = false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    full &= (r[i].x <= key && r[i].y >= key + kTile) || (r[i].z <= key && r[i].w >= key + kTile);
+                    dirty |= r[i].y == 0 && r[i].w == 0;
+                }
+                const int head = kvh * group + h, row0 = from;
+                uint32_t flags = static_cast<uint32_t>(head) << 16 | first;
+                if (__all_sync(0xFFFFFFFFu, full)) flags |= kFull;
+                if (__any_sync(0xFFFFFFFFu, dirty)) flags |= kDirty;
+                from += kTile;
+                bool end = false;
+                if (from >= to) {
+                    if (to == range.y && range.w > from) {
                         // the last tile may have reached into the second range
                         from = max(from, range.z);
                         to = range.w;
-                        end = false;
+                    } else if (++h < group) {
+                        from = range.x;
+                        to = range.y;
+                    } else {
+                        end = true;
                     }
-                    if (end && h == group - 1) flags |= kLast;
-                    if (!announce(row0, flags, entry)) break;
-                    if (!loaded) {
-                        // the last item's last tile has its S' and dP'
-                        const uint32_t m = n - 1;
-                        if (n > 0 && !(wait(&sh.s_ready[m & 1], m / 2 & 1) && wait(&sh.dp_ready[m & 1], m / 2 & 1)))
-                            break;
-                        if (lane == 0) {
-                            mbar_expect_tx(&sh.kv_full, 2 * kSlabs * kSlab);
-                            for (int i = 0; i < kSlabs; ++i) {
-                                tma_slab(smem_addr(sh.k) + i * kSlab, &maps.k, 64 * i, kvh, key, &sh.kv_full);
-                                tma_slab(smem_addr(sh.v) + i * kSlab, &maps.v, 64 * i, kvh, key, &sh.kv_full);
-                            }
-                        }
-                        loaded = true;
-                        ++nkv;
-                    }
-                    const uint32_t qs = n % Sh::kQ, os = n % Sh::kO;
-                    // the Q of tile j is free with tile j + 1's dP' (which its dK precedes), its dO with tile
-                    // j + 1's S' (which its dV precedes) and its own dP'
-                    if (n >= Sh::kQ && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
-                    if (lane == 0) load_tile(&maps.q, smem_addr(sh.q[qs]), kSlabs, head, base + row0, &sh.q_full[qs]);
-                    ++nq;
-                    if (n >= Sh::kO && !(wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1) &&
-                                         wait(&sh.s_ready[(n - 1) & 1], (n - 1) / 2 & 1)))
-                        break;
-                    if (lane == 0)
-                        load_tile(&maps.dout, smem_addr(sh.dout[os]), kSlabs, head, base + row0, &sh.do_full[os]);
-                    ++no;
-                    ++n;
-                    if (end) break;
                 }
+                if (end) flags |= kLast;
+                else load_spans(from);   // while the barriers below are waited for
+                // The Q of tile j is free with tile j + 1's dP', which its dK precedes. This is waited for
+                // before the tile is announced, so that its own dP' cannot come between.
+                const uint32_t qs = n % Sh::kQ;
+                if (n >= Sh::kQ && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
+                if (!announce(row0, flags, entry)) break;
+                if (first) {
+                    // the last item's last tile has its S' and dP'
+                    const uint32_t m = n - 1;
+                    if (n > 0 && !(wait(&sh.s_ready[m & 1], m / 2 & 1) && wait(&sh.dp_ready[m & 1], m / 2 & 1))) break;
+                    if (lane == 0) {
+                        mbar_expect_tx(&sh.kv_full, 2 * kSlabs * kSlab);
+                        for (int i = 0; i < kSlabs; ++i) {
+                            tma_slab(smem_addr(sh.k) + i * kSlab, &maps.k, 64 * i, kvh, key, &sh.kv_full);
+                            tma_slab(smem_addr(sh.v) + i * kSlab, &maps.v, 64 * i, kvh, key, &sh.kv_full);
+                        }
+                    }
+                    ++nkv;
+                }
+                if (lane == 0) load_tile(&maps.q, smem_addr(sh.q[qs]), kSlabs, head, base + row0, &sh.q_full[qs]);
+                ++nq;
+                ++n;
+                if (end) break;
             }
             it = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, ahead, 0);
         }
@@ -798,8 +780,6 @@ __global__ void __launch_bounds__(384, 1)
         if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
             for (uint32_t i = nq > Sh::kQ ? nq - Sh::kQ : 0; i < nq; ++i)
                 mbar_wait_bounded(&sh.q_full[i % Sh::kQ], i / Sh::kQ & 1);
-            for (uint32_t i = no > Sh::kO ? no - Sh::kO : 0; i < no; ++i)
-                mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
             if (nkv > 0) mbar_wait_bounded(&sh.kv_full, (nkv - 1) & 1);
         }
     } else if (warp < 3 && aligned) {
@@ -845,26 +825,47 @@ __global__ void __launch_bounds__(384, 1)
         mma_commit(leader, &sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
     } else if (warp == 3 && aligned) {
-        // ------------------------------------------------------------- statistics of the rows
+        // ------------------------------------------------------------- statistics of the rows, dO
+        // A loader of its own: dO has two places and waits longer for one than Q does.
         int64_t rank_row = 0;
-        for (uint32_t n = 0;; ++n) {
-            const uint32_t slot = n % kRing, s = n & 1;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_full[slot], n / kRing & 1, stop))) break;
+        uint32_t n = 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        for (;; ++n) {
+            const uint32_t slot = n % kRing, s = n & 1, os = n % Sh::kO;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int4 e = sh.info[slot];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
             if (e.y & kStop) break;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.aux_empty[s], (n / 2 & 1) ^ 1, stop))) break;
             if (e.y & kFirst) rank_row = e.z % p.P * p.Tp;
-            const int64_t base = static_cast<int64_t>(e.y >> 16) * p.Tpad + rank_row;
-            for (int i = lane; i < kTile; i += 32) {
-                const int64_t row = e.x + i;
-                const bool in = row < p.Tp;
-                sh.lse2[s][i] = in ? -b.lse2[base + row] : -INFINITY;   // negated, as they are added
-                sh.delta[s][i] = in ? -b.delta[base + row] : 0.0f;
+            const int head = e.y >> 16;
+            const int64_t base = head * p.Tpad + rank_row;
+            float lse2[4], delta[4];   // negated, as they are added
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int64_t row = e.x + lane + 32 * i;
+                lse2[i] = row < p.Tp ? -b.lse2[base + row] : -INFINITY;
+                delta[i] = row < p.Tp ? -b.delta[base + row] : 0.0f;
+            }
+            // the dO of tile j is free with tile j + 1's S' (which its dV precedes) and its own dP'
+            if (n >= Sh::kO && !(wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1) &&
+                                 wait(&sh.s_ready[(n - 1) & 1], (n - 1) / 2 & 1)))
+                break;
+            if (lane == 0)
+                load_tile(&maps.dout, smem_addr(sh.dout[os]), kSlabs, head, rank_row + e.x, &sh.do_full[os]);
+            if (!wait(&sh.aux_empty[s], (n / 2 & 1) ^ 1)) break;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                sh.lse2[s][lane + 32 * i] = lse2[i];
+                sh.delta[s][lane + 32 * i] = delta[i];
             }
             mbar_arrive(&sh.aux_full[s]);
         }
+        if (*stop != 0 && lane == 0)
+            for (uint32_t i = n > Sh::kO ? n - Sh::kO : 0; i < n; ++i)
+                mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
     }
     } else {
         more_registers<200>();
@@ -995,8 +996,8 @@ __global__ void __launch_bounds__(384, 1)
                 tmem_fence_after();
                 float bad = 0.0f;
                 uint16_t *out = const_cast<uint16_t *>(row_of(y == 0 ? b.dv[rank] : b.dk[rank], pos, p.Hkv, kvh, p.D));
-                for (int i = 0; i < steps; ++i)
-                    store_columns(out, 16 * i, p.D, at + (y == 0 ? 256 : 384), y == 0 ? 1.0f : p.scale, pos >= 0, bad);
+                for (int i = 0; 32 * i < p.D; ++i)
+                    store_block(at + (y == 0 ? 256 : 384), i, p.D, y == 0 ? 1.0f : p.scale, true, out, pos >= 0, bad);
                 tmem_fence_before();
                 spoiled |= pos >= 0 && bad != 0.0f;
             }

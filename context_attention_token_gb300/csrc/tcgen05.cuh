@@ -312,4 +312,58 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
     return static_cast<uint32_t>((1ull << b) - 1) & ~static_cast<uint32_t>((1ull << a) - 1);
 }
 
+// ----------------------------------------------------------------- rows out
+//
+// Every lane holds one row of an accumulator. Written as they are, 16 bytes of 32
+// rows at a time, rows cost 32 wavefronts an instruction (5000 cycles for a
+// tile of 128 x 128). So four lanes exchange their 16-byte units first and
+// write 64 neighbouring bytes of a row together.
+
+// Columns [32 block, 32 block + 32) below D of this warp's 32 rows: scaled,
+// rounded to bf16 and written where `write` holds; zeros where `live` does not.
+// Returns NaN (added to `bad`) once a written value is not finite.
+__device__ __forceinline__ void store_block(uint32_t tmem, int block, int D, float scale, bool live, uint16_t *row,
+                                            bool write, float &bad)
+{
+    const int lane = threadIdx.x & 31;
+    uint32_t o[32];
+    tmem_load32(tmem + 32 * block, o);
+    tmem_wait_loads(o);
+    uint4 u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = live ? __uint_as_float(o[8 * i + 2 * j]) * scale : 0.0f;
+            const float y = live ? __uint_as_float(o[8 * i + 2 * j + 1]) * scale : 0.0f;
+            if (32 * block + 8 * i < D) bad = __fmaf_rn(x, 0.0f, __fmaf_rn(y, 0.0f, bad));
+            w[j] = pack_bf16x2(x, y);
+        }
+        u[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    auto swap = [&](uint4 &low, uint4 &high, int bit) {   // lanes without the bit keep `low`, the others `high`
+        const bool upper = (lane & bit) != 0;
+        uint4 s = upper ? low : high;
+        s.x = __shfl_xor_sync(0xFFFFFFFFu, s.x, bit);
+        s.y = __shfl_xor_sync(0xFFFFFFFFu, s.y, bit);
+        s.z = __shfl_xor_sync(0xFFFFFFFFu, s.z, bit);
+        s.w = __shfl_xor_sync(0xFFFFFFFFu, s.w, bit);
+        if (upper) low = s;
+        else high = s;
+    };
+    swap(u[0], u[1], 1);
+    swap(u[2], u[3], 1);
+    swap(u[0], u[2], 2);
+    swap(u[1], u[3], 2);
+    const int at = 32 * block + 8 * (lane & 3);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {   // unit lane & 3 of row k of the four
+        const int from = (lane & ~3) + k;
+        const unsigned long long to = __shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(row), from);
+        const bool ok = __shfl_sync(0xFFFFFFFFu, write ? 1 : 0, from) != 0;
+        if (ok && at < D) *reinterpret_cast<uint4 *>(reinterpret_cast<uint16_t *>(to) + at) = u[k];
+    }
+}
+
 }  // namespace cpt
