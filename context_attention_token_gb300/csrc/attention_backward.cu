@@ -164,6 +164,14 @@ __device__ __forceinline__ int32_t position_of_token(const Params &b, int32_t j)
     return in_bounds(row >= 0 && row < b.a.Tpad) ? b.l2g[row] : -1;
 }
 
+// Tiles of 128 rows in a key tile's ranges: of the first, where the second
+// begins (the last tile of the first may reach into it), of both.
+__device__ __forceinline__ int3 row_tiles_of(int4 range)
+{
+    const int first = (range.y - range.x + kTile - 1) / kTile, from = max(range.z, range.x + first * kTile);
+    return make_int3(first, from, first + (range.w > from ? (range.w - from + kTile - 1) / kTile : 0));
+}
+
 // Key tiles of every rank: the local rows that may see one of the 128 keys, as
 // up to two ranges (the window's, and the rest of the documents whose
 // sinks lie in the tile); tiles that no row sees are written as zeros here.
@@ -204,6 +212,9 @@ __device__ __forceinline__ void prepare_tile(const Params &b, int block, int til
         b.ranges[i] = make_int4((int)w0, (int)w1, (int)s0, (int)s1);
         any = w1 > w0;
         if (any) {
+            // row tiles of all heads of a group
+            const long long entries = static_cast<long long>(row_tiles_of(b.ranges[i]).z) * (p.Hq / p.Hkv);
+            atomicAdd(reinterpret_cast<unsigned long long *>(b.counters + 4), static_cast<unsigned long long>(entries));
             if (far) b.list[atomicAdd(&b.counters[0], 1)] = i;
             else b.list[tiles * p.P - 1 - atomicAdd(&b.counters[1], 1)] = i;
         }
@@ -233,7 +244,8 @@ __global__ void __launch_bounds__(8 * kPrepRows) prepare_kernel(const __grid_con
 // ----------------------------------------------------------------- shared by both kernels
 
 constexpr int kRing = 8;       // tile announcements in flight
-constexpr uint32_t kFull = 1, kFirst = 2, kLast = 4, kStop = 8, kDirty = 16;
+constexpr int kThreads = 640;  // 4 warps that load and issue, 4 warpgroups that compute
+constexpr uint32_t kFull = 1, kFirst = 2, kLast = 4, kStop = 8, kDirty = 16, kPart = 32;
 
 template <int DP>
 struct Shape {
@@ -252,14 +264,30 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
     for (int i = 0; i < slabs; ++i) tma_slab(to + i * kSlab, map, 64 * i, head, static_cast<int>(row), bar);
 }
 
-// The weights of a tile lie as two halves of 64 inner columns (one for each
-// warpgroup), each over the first half of the columns of scores it came from.
-// One PART is the first or second 32 inner columns of both.
-template <int PART>
-__device__ __forceinline__ void mma_part(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+// d (+)= A B with the weights of a tile, which lie as four quarters of 32 inner
+// columns (one for each warpgroup), each over the first half of the columns of
+// scores that it came from.
+__device__ __forceinline__ void mma_quarters(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-    mma_weights<2>(leader, d, a + 16 * PART, b + 4096 * PART, shape, add);
-    mma_weights<2>(leader, d, a + 64 + 16 * PART, b + 8192 + 4096 * PART, shape, true);
+#pragma unroll
+    for (int w = 0; w < 4; ++w) mma_weights<2>(leader, d, a + 32 * w, b + 4096 * w, shape, add || w > 0);
+}
+
+// The same over the first or second 16 inner columns of every quarter.
+template <int PART>
+__device__ __forceinline__ void mma_half(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+{
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+        mma_weights<1>(leader, d, a + 32 * w + 8 * PART, b + 4096 * w + 2048 * PART, shape, add || w > 0);
+}
+
+// One arrival of a warp whose lanes have all written (or read) tensor memory.
+__device__ __forceinline__ void warp_arrive(uint64_t *bar)
+{
+    tmem_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 
 // The bits of a 32 x 32 matrix, one row per lane, transposed.
@@ -281,14 +309,60 @@ __device__ __forceinline__ uint32_t visible_bits(int4 r, int key, int word)
     return span_bits(r.x - key, r.y - key, word) | span_bits(r.z - key, r.w - key, word);
 }
 
+// ----------------------------------------------------------------- units of work
+//
+// A key tile takes as many row tiles as see it: few behind a window, all of a
+// document under the whole triangle or where its sinks lie. Those with more
+// than half of a CTA's share of all row tiles (kLeastPart at least) are cut into
+// parts, which leave binary32 sums in the workspace; whichever part ends last
+// adds them up in their order. So no CTA is left with a long tile alone, and
+// small batches use more CTAs than they have key tiles.
+
+constexpr int kLeastPart = 8;
+
+// Lists the units: {slot, part, parts, place of the first part's sums}. One warp.
+__device__ void list_units(const Params &b, int slots, int sms)
+{
+    const int lane = threadIdx.x & 31, group = b.a.Hq / b.a.Hkv;
+    const int front = b.counters[0], n = front + b.counters[1];
+    const long long entries = *reinterpret_cast<const long long *>(b.counters + 4) * b.a.Hkv;
+    const long long share = (entries + 2 * sms - 1) / (2 * sms);
+    const int most = static_cast<int>(min(max(share, (long long)kLeastPart), 0x40000000ll));
+    int units = 0, places = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        int slot = 0, parts = 0;
+        if (i < n) {
+            slot = b.list[i < front ? i : slots - 1 - (i - front)];
+            parts = (row_tiles_of(b.ranges[slot]).z * group + most - 1) / most;
+        }
+        const int need = parts > 1 ? parts : 0;
+        int u = parts, q = need;   // inclusive sums over the warp
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int du = __shfl_up_sync(0xFFFFFFFFu, u, s), dq = __shfl_up_sync(0xFFFFFFFFu, q, s);
+            if (lane >= s) {
+                u += du;
+                q += dq;
+            }
+        }
+        for (int k = 0; k < parts; ++k)
+            if (in_bounds(units + u - parts + k < b.unit_places))
+                b.units[units + u - parts + k] = make_int4(slot, k, parts, places + q - need);
+        units += __shfl_sync(0xFFFFFFFFu, u, 31);
+        places += __shfl_sync(0xFFFFFFFFu, q, 31);
+    }
+    if (lane == 0) b.counters[6] = units;
+}
+
 // ----------------------------------------------------------------- dQ
 //
 // An item is 128 query rows of one head; Q and dO stay in shared memory, the
 // key tiles pass by as in the forward kernel. Per key tile three products,
 //   S = Q K^T, dP = dO V^T, dQ += dS K,
 // with dS = P (dP - delta), rounded to bf16 for the matrix unit, over S in
-// tensor memory. S is there twice and issued a tile ahead, so that while two
-// warpgroups (64 key columns each, one thread per row) make dS, the matrix unit
+// tensor memory. S is there twice and issued a tile ahead, so that while four
+// warpgroups (32 key columns each, one thread per row) make dS, the matrix unit
 // has the last tile's dQ and the next S to do.
 // Tensor memory: S, S, dP, dQ. Shared memory: Q, dO, 3 K, 2 V.
 
@@ -300,7 +374,9 @@ struct DqShared {
     uint64_t q_full, do_full;
     uint64_t k_full[kK], k_empty[kK], v_full[kV];
     uint64_t info_full[kRing], info_empty[kRing];
-    uint64_t s_ready[2], dp_ready[2], dp_free, ds_ready, acc_done, drained[2];
+    uint64_t s_ready[2], dp_ready[2], dp_free;
+    uint64_t ds_ready[2];              // by tile parity: a warp may be a tile ahead of another
+    uint64_t acc_done, drained[2];
     int4 info[kRing];              // first key, flags, item
     uint32_t tmem, stop, spoiled;
 };
@@ -321,8 +397,9 @@ __device__ __forceinline__ DqItem dq_item(const AttentionParams &p, int64_t i, i
 }
 
 template <int DP>
-__global__ void __launch_bounds__(384, 1)
-    dq_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t items, int64_t row_tiles)
+__global__ void __launch_bounds__(kThreads, 1)
+    dq_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t items, int64_t row_tiles,
+              int slots, int sms)
 {
     typedef DqShared<DP> Sh;
     constexpr int kSlabs = Shape<DP>::kSlabs;
@@ -342,14 +419,14 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < Sh::kV; ++i) mbar_init(&sh.v_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 10);     // issuers, 8 warps
+            mbar_init(&sh.info_empty[i], 18);     // issuers, 16 warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_ready[i], 1);
             mbar_init(&sh.dp_ready[i], 1);
+            mbar_init(&sh.ds_ready[i], 16);
         }
-        mbar_init(&sh.dp_free, 2 * kTile);
-        mbar_init(&sh.ds_ready, 2 * kTile);
+        mbar_init(&sh.dp_free, 16);
         mbar_init(&sh.acc_done, 1);
         mbar_init(&sh.drained[0], 1);
         mbar_init(&sh.drained[1], 1);
@@ -363,9 +440,9 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = (p.D + 15) / 16;
-    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    // 128 x 64 + 512 x 104 of the 640 x 96 registers of the launch
     if (warp < 4) {
-    fewer_registers<96>();
+    fewer_registers<64>();
     if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0;                           // tiles
@@ -471,11 +548,10 @@ __global__ void __launch_bounds__(384, 1)
             };
             bool more = issue_s() && issue_s();
             for (uint32_t i = 0; i < ns; ++i) {
-                if (!wait(&sh.ds_ready, i & 1)) break;
+                if (!wait(&sh.ds_ready[i & 1], i / 2 & 1)) break;
                 tmem_fence_after();
                 const uint32_t e = flags[i & 1], ks = i % Sh::kK;
-                mma_part<0>(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
-                mma_part<1>(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, true);
+                mma_quarters(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
                 if (e & kLast) mma_commit(leader, &sh.acc_done);
                 mma_commit(leader, &sh.k_empty[ks]);
                 if (more) more = issue_s();
@@ -500,9 +576,12 @@ __global__ void __launch_bounds__(384, 1)
         }
         mma_commit(leader, &sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
+    } else if (warp == 3 && blockIdx.x == 0) {
+        // ------------------------------------------------------------- the next kernel's units
+        list_units(b, slots, sms);
     }
     } else {
-        more_registers<200>();
+        more_registers<104>();
         // ------------------------------------------------------------- scores to dS
         const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
@@ -541,51 +620,37 @@ __global__ void __launch_bounds__(384, 1)
             }
             if (!wait(&sh.s_ready[n & 1], n / 2 & 1) || !wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
             tmem_fence_after();
-            const uint32_t s_at = at + 128 * (n & 1) + 64 * y, dp_at = at + 256 + 64 * y;
-            uint32_t s[2][32], dp[2][32];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_load32(s_at + 32 * i, s[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_load32(dp_at + 32 * i, dp[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                tmem_wait_loads(s[i]);
-                tmem_wait_loads(dp[i]);
-            }
-            tmem_fence_before();
-            mbar_arrive(&sh.dp_free);
+            const uint32_t s_at = at + 128 * (n & 1) + 32 * y;
+            uint32_t s[32], dp[32], w[16];
+            tmem_load32(s_at, s);
+            tmem_load32(at + 256 + 32 * y, dp);
+            tmem_wait_loads(s);
+            tmem_wait_loads(dp);
+            warp_arrive(&sh.dp_free);
             if (!(flags & kFull)) {
+                const uint32_t bits = visible_bits(r, e.x, y);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint32_t bits = visible_bits(r, e.x, 2 * y + i);
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!(bits >> j & 1)) s[i][j] = 0xFF800000u;
-                }
+                for (int j = 0; j < 32; ++j)
+                    if (!(bits >> j & 1)) s[j] = 0xFF800000u;
             }
             const F2 c2 = pair_of(c, c), lse22 = pair_of(-lse2, -lse2), delta2 = pair_of(-delta, -delta);
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float2 a = both(fma2(pair_of(s[i][2 * j], s[i][2 * j + 1]), c2, lse22));
-                    const F2 pr = pair_of(exp2_fast(a.x), exp2_fast(a.y));
-                    const float2 ds = both(mul2(pr, add2(pair_of(dp[i][2 * j], dp[i][2 * j + 1]), delta2)));
-                    w[j] = pack_bf16x2(ds.x, ds.y);
-                }
-                tmem_store16(s_at + 16 * i, w);
+            for (int j = 0; j < 16; ++j) {
+                const float2 a = both(fma2(pair_of(s[2 * j], s[2 * j + 1]), c2, lse22));
+                const F2 pr = pair_of(exp2_fast(a.x), exp2_fast(a.y));
+                const float2 ds = both(mul2(pr, add2(pair_of(dp[2 * j], dp[2 * j + 1]), delta2)));
+                w[j] = pack_bf16x2(ds.x, ds.y);
             }
+            tmem_store16(s_at, w);
             tmem_wait_stores();
-            tmem_fence_before();
-            mbar_arrive(&sh.ds_ready);
+            warp_arrive(&sh.ds_ready[n & 1]);
             if (flags & kLast) {
                 if (!wait(&sh.acc_done, done++ & 1)) break;
                 tmem_fence_after();
                 float bad = 0.0f;
                 const bool write = valid && (r.y != 0 || r.w != 0);
                 uint16_t *out = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, p.D));
-                for (int i = y; 32 * i < p.D; i += 2) store_block(at + 384, i, p.D, p.scale, write, out, write, bad);
+                if (32 * y < p.D) store_block(at + 384, y, p.D, p.scale, write, out, write, bad);
                 tmem_fence_before();
                 spoiled |= write && bad != 0.0f;
             }
@@ -609,13 +674,19 @@ __global__ void __launch_bounds__(384, 1)
 // memory:
 //   S' = K Q^T, dP' = V dO^T, dV += P' dO, dK += dS' Q,
 // issued as dV(i) S(i+1) by one warp and dK(i) dP(i+1) by another: the matrix
-// unit works on two products while two warpgroups (64 row columns each, one
+// unit works on two products while four warpgroups (32 row columns each, one
 // thread per key) make P, and on the other two while they make dS.
 // Tensor memory: S', dP', dV, dK. Shared memory: K, V, 3 Q, 2 dO.
+// With heads of up to 64 elements the sums need half the columns, S' is there
+// twice, and S(i+1) goes before dV(i) instead of waiting for P(i). With longer
+// heads P lies over the only S' and S(i+1) waits for dV(i): there the products
+// begin with the first half of P (and dS), while the second is made.
 
 template <int DP>
 struct DkvShared {
     static constexpr int kQ = 3, kO = 2;
+    static constexpr bool kTwice = DP == 64;          // S' twice
+    static constexpr uint32_t kDp = kTwice ? 256 : 128, kDv = kTwice ? 384 : 256, kDk = kTwice ? 448 : 384;
     uint8_t k[Shape<DP>::kTileBytes], v[Shape<DP>::kTileBytes];
     uint8_t q[kQ][Shape<DP>::kTileBytes], dout[kO][Shape<DP>::kTileBytes];
     float lse2[2][kTile], delta[2][kTile];
@@ -623,23 +694,65 @@ struct DkvShared {
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t aux_full[2], aux_empty[2];
     uint64_t s_ready[2], dp_ready[2];  // S' and dV of the tile before, dP' and dK of it: by tile parity
-    uint64_t half[2], whole[2];        // P and dS in tensor memory: the first 32 columns of both halves, all
+    uint64_t half[2], weights[2][2];   // P, dS in tensor memory: the first half of every quarter; all, by tile
+                                       // parity (with S' twice a warp may be a tile ahead of another)
+    uint64_t dv_done[2];               // with S' twice: dV of a tile, by tile parity
     uint64_t acc_done[2], drained[2];
     int4 info[kRing];              // first row, flags and head, tile * P + rank
     uint32_t tmem, stop, spoiled;
 };
 
-// Item i of the list: heads fastest, the long tiles first.
-__device__ __forceinline__ void dkv_item(const Params &b, int64_t i, int64_t slots, int front, int &entry, int &kvh)
+static_assert(sizeof(DkvShared<128>) <= 232448 && sizeof(DqShared<128>) <= 232448, "shared memory of a block");
+
+// A warp's columns of a part's sums go to the workspace; the warp that is the
+// last of all parts to come by gets their total, in the order of the parts, back
+// into its tensor memory. [place][dV, dK][column][key]
+__device__ __noinline__ bool add_parts(const Params &b, int4 unit, int kvh, int warp, int of_k, int odd, uint32_t acc)
 {
-    const int64_t at = i / b.a.Hkv;
-    kvh = static_cast<int>(i - at * b.a.Hkv);
-    entry = b.list[at < front ? at : slots - 1 - (at - front)];
+    const int lane = threadIdx.x & 31, D32 = (b.a.D + 31) / 32 * 32, key = (warp & 3) * 32 + lane;
+    const int64_t tile = 2ll * D32 * kTile, place0 = static_cast<int64_t>(unit.w) * b.a.Hkv + kvh;
+    auto at = [&](int part, int column) {
+        return b.sums + (place0 + static_cast<int64_t>(part) * b.a.Hkv) * tile + (of_k * D32 + column) * kTile + key;
+    };
+    for (int i = odd; 32 * i < b.a.D; i += 2) {
+        uint32_t o[32];
+        tmem_load32(acc + 32 * i, o);
+        tmem_wait_loads(o);
+        float *to = at(unit.y, 32 * i);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) __stcg(to + j * kTile, __uint_as_float(o[j]));
+    }
+    __threadfence();
+    __syncwarp();
+    int before = 0;
+    if (lane == 0) before = atomicAdd(&b.arrived[place0 * 16 + warp], 1);
+    before = __shfl_sync(0xFFFFFFFFu, before, 0);
+    if (before != unit.z - 1) return false;
+    __threadfence();
+    for (int i = odd; 32 * i < b.a.D; i += 2) {
+        float sum[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) sum[j] = 0.0f;
+        for (int part = 0; part < unit.z; ++part) {
+            const float *from = at(part, 32 * i);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) sum[j] += __ldcg(from + j * kTile);
+        }
+        uint32_t o[16];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(sum[16 * h + j]);
+            tmem_store16(acc + 32 * i + 16 * h, o);
+        }
+        tmem_wait_stores();
+    }
+    return true;
 }
 
 template <int DP>
-__global__ void __launch_bounds__(384, 1)
-    dkdv_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t slots)
+__global__ void __launch_bounds__(kThreads, 1)
+    dkdv_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps)
 {
     typedef DkvShared<DP> Sh;
     constexpr int kSlabs = Shape<DP>::kSlabs;
@@ -655,17 +768,19 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < Sh::kO; ++i) mbar_init(&sh.do_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 11);     // issuers, statistics, 8 warps
+            mbar_init(&sh.info_empty[i], 19);     // issuers, statistics, 16 warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.aux_full[i], 32);
-            mbar_init(&sh.aux_empty[i], 8);
+            mbar_init(&sh.aux_empty[i], 16);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.s_ready[i], 1);
             mbar_init(&sh.dp_ready[i], 1);
-            mbar_init(&sh.half[i], 2 * kTile);
-            mbar_init(&sh.whole[i], 2 * kTile);
+            mbar_init(&sh.half[i], 16);
+            mbar_init(&sh.weights[i][0], 16);
+            mbar_init(&sh.weights[i][1], 16);
+            mbar_init(&sh.dv_done[i], 1);
             mbar_init(&sh.acc_done[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
@@ -679,11 +794,10 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = (p.D + 15) / 16, group = p.Hq / p.Hkv;
-    const int front = b.counters[0];
-    const int64_t items = static_cast<int64_t>(front + b.counters[1]) * p.Hkv;
-    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    const int64_t items = static_cast<int64_t>(b.counters[6]) * p.Hkv;
+    // 128 x 64 + 512 x 104 of the 640 x 96 registers of the launch
     if (warp < 4) {
-    fewer_registers<96>();
+    fewer_registers<64>();
     if (warp == 0 && aligned) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0;                        // tiles
@@ -693,10 +807,10 @@ __global__ void __launch_bounds__(384, 1)
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
             return ok;
         };
-        auto announce = [&](int row, uint32_t flags, int entry) {
+        auto announce = [&](int row, uint32_t flags, int slot, int unit) {
             const uint32_t s = n % kRing;
             if (wait(&sh.info_empty[s], (n / kRing & 1) ^ 1) && lane == 0) {
-                sh.info[s] = make_int4(row, static_cast<int>(flags), entry, 0);
+                sh.info[s] = make_int4(row, static_cast<int>(flags), slot, unit);
                 mbar_arrive(&sh.info_full[s]);
             }
             return ok;
@@ -708,10 +822,10 @@ __global__ void __launch_bounds__(384, 1)
         while (ok && it < items) {
             int ahead = 0;
             if (lane == 0) ahead = atomicAdd(&b.counters[2], 1);
-            int entry, kvh;
-            dkv_item(b, it, slots, front, entry, kvh);
-            const int4 range = b.ranges[entry];
-            const int rank = entry % p.P, key = entry / p.P * kTile;
+            const int index = static_cast<int>(it / p.Hkv), kvh = static_cast<int>(it - index * (int64_t)p.Hkv);
+            const int4 unit = b.units[index];
+            const int4 range = b.ranges[unit.x];
+            const int rank = unit.x % p.P, key = unit.x / p.P * kTile;
             const int64_t base = rank * p.Tp;
             int4 r[4];
             auto load_spans = [&](int from) {
@@ -721,9 +835,16 @@ __global__ void __launch_bounds__(384, 1)
                     r[i] = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
                 }
             };
-            int h = 0, from = range.x, to = range.y;
-            load_spans(from);
-            for (uint32_t first = kFirst; ok; first = 0) {
+            const int3 tiles = row_tiles_of(range);
+            const int total = tiles.z * group;
+            const int e0 = static_cast<int>(static_cast<int64_t>(total) * unit.y / unit.z);
+            const int e1 = static_cast<int>(static_cast<int64_t>(total) * (unit.y + 1) / unit.z);
+            int h = e0 / tiles.z, j = e0 - h * tiles.z;
+            auto row_of_tile = [&](int j) {
+                return j < tiles.x ? range.x + j * kTile : tiles.y + (j - tiles.x) * kTile;
+            };
+            load_spans(row_of_tile(j));
+            for (int e = e0; ok && e < e1; ++e) {
                 // whether all rows see all keys, and whether some are not rows of this rank
                 bool full = true, dirty = false;
 #pragma unroll
@@ -731,32 +852,24 @@ __global__ void __launch_bounds__(384, 1)
                     full &= (r[i].x <= key && r[i].y >= key + kTile) || (r[i].z <= key && r[i].w >= key + kTile);
                     dirty |= r[i].y == 0 && r[i].w == 0;
                 }
-                const int head = kvh * group + h, row0 = from;
-                uint32_t flags = static_cast<uint32_t>(head) << 16 | first;
+                const int head = kvh * group + h, row0 = row_of_tile(j);
+                uint32_t flags = static_cast<uint32_t>(head) << 16;
                 if (__all_sync(0xFFFFFFFFu, full)) flags |= kFull;
                 if (__any_sync(0xFFFFFFFFu, dirty)) flags |= kDirty;
-                from += kTile;
-                bool end = false;
-                if (from >= to) {
-                    if (to == range.y && range.w > from) {
-                        // the last tile may have reached into the second range
-                        from = max(from, range.z);
-                        to = range.w;
-                    } else if (++h < group) {
-                        from = range.x;
-                        to = range.y;
-                    } else {
-                        end = true;
-                    }
+                if (e == e0) flags |= kFirst;
+                if (unit.z > 1) flags |= kPart;
+                if (++j == tiles.z) {
+                    j = 0;
+                    ++h;
                 }
-                if (end) flags |= kLast;
-                else load_spans(from);   // while the barriers below are waited for
+                if (e == e1 - 1) flags |= kLast;
+                else load_spans(row_of_tile(j));   // while the barriers below are waited for
                 // The Q of tile j is free with tile j + 1's dP', which its dK precedes. This is waited for
                 // before the tile is announced, so that its own dP' cannot come between.
                 const uint32_t qs = n % Sh::kQ;
                 if (n >= Sh::kQ && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
-                if (!announce(row0, flags, entry)) break;
-                if (first) {
+                if (!announce(row0, flags, unit.x, index)) break;
+                if (e == e0) {
                     // the last item's last tile has its S' and dP'
                     const uint32_t m = n - 1;
                     if (n > 0 && !(wait(&sh.s_ready[m & 1], m / 2 & 1) && wait(&sh.dp_ready[m & 1], m / 2 & 1))) break;
@@ -772,11 +885,10 @@ __global__ void __launch_bounds__(384, 1)
                 if (lane == 0) load_tile(&maps.q, smem_addr(sh.q[qs]), kSlabs, head, base + row0, &sh.q_full[qs]);
                 ++nq;
                 ++n;
-                if (end) break;
             }
             it = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, ahead, 0);
         }
-        if (ok) announce(0, kStop, 0);
+        if (ok) announce(0, kStop, 0, 0);
         if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
             for (uint32_t i = nq > Sh::kQ ? nq - Sh::kQ : 0; i < nq; ++i)
                 mbar_wait_bounded(&sh.q_full[i % Sh::kQ], i / Sh::kQ & 1);
@@ -790,7 +902,7 @@ __global__ void __launch_bounds__(384, 1)
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
         };
         const uint32_t s_shape = mma_shape(kTile, false), o_shape = mma_shape(16 * steps, true);
-        const uint32_t scores = tmem + (first ? 0 : 128), acc = tmem + (first ? 256 : 384);
+        const uint32_t scores_at = tmem + (first ? 0 : Sh::kDp), acc = tmem + (first ? Sh::kDv : Sh::kDk);
         const uint32_t key_at = first ? smem_addr(sh.k) : smem_addr(sh.v);
         uint32_t prev = 0, k = 0;   // flags of the last tile, items begun
         for (uint32_t n = 0;; ++n) {
@@ -805,21 +917,39 @@ __global__ void __launch_bounds__(384, 1)
             auto operand = [&]() {
                 return first ? wait(&sh.q_full[qs], n / Sh::kQ & 1) : wait(&sh.do_full[os], n / Sh::kO & 1);
             };
-            if (more && !fresh && !operand()) break;
-            if (n > 0) {
-                const uint32_t with = first ? smem_addr(sh.dout[i % Sh::kO]) : smem_addr(sh.q[i % Sh::kQ]);
-                if (!wait(&sh.half[warp - 1], i & 1)) break;
-                tmem_fence_after();
-                mma_part<0>(leader, acc, scores, with, o_shape, !(prev & kFirst));
-                if (!wait(&sh.whole[warp - 1], i & 1)) break;
-                tmem_fence_after();
-                mma_part<1>(leader, acc, scores, with, o_shape, true);
+            const uint32_t with = first ? smem_addr(sh.dout[i % Sh::kO]) : smem_addr(sh.q[i % Sh::kQ]);
+            const bool twice = Sh::kTwice && first;
+            auto product = [&]() {
+                const uint32_t weights = scores_at + (twice ? 128 * (i & 1) : 0);
+                if (!Sh::kTwice) {
+                    if (!wait(&sh.half[warp - 1], i & 1)) return false;
+                    tmem_fence_after();
+                    mma_half<0>(leader, acc, weights, with, o_shape, !(prev & kFirst));
+                    if (!wait(&sh.weights[warp - 1][i & 1], i / 2 & 1)) return false;
+                    tmem_fence_after();
+                    mma_half<1>(leader, acc, weights, with, o_shape, true);
+                } else {
+                    if (!wait(&sh.weights[warp - 1][i & 1], i / 2 & 1)) return false;
+                    tmem_fence_after();
+                    mma_quarters(leader, acc, weights, with, o_shape, !(prev & kFirst));
+                }
                 if (prev & kLast) mma_commit(leader, &sh.acc_done[warp - 1]);
-            }
+                return true;
+            };
+            const bool late = n > 0 && twice && more && !fresh;   // the product after the next scores
+            if (more && !fresh && !operand()) break;
+            if (n > 0 && !late && !product()) break;
             if (!more) break;
             if (fresh && !(wait(&sh.kv_full, k++ & 1) && operand())) break;
-            mma_scores(leader, scores, key_at, first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
+            mma_scores(leader, scores_at + (twice ? 128 * (n & 1) : 0), key_at,
+                       first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
             mma_commit(leader, first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
+            if (late) {
+                if (!product()) break;
+                mma_commit(leader, &sh.dv_done[i & 1]);
+            } else if (Sh::kTwice && first && n > 0) {
+                mma_commit(leader, &sh.dv_done[i & 1]);
+            }
             prev = e;
         }
         mma_commit(leader, &sh.drained[warp - 1]);
@@ -849,9 +979,11 @@ __global__ void __launch_bounds__(384, 1)
                 lse2[i] = row < p.Tp ? -b.lse2[base + row] : -INFINITY;
                 delta[i] = row < p.Tp ? -b.delta[base + row] : 0.0f;
             }
-            // the dO of tile j is free with tile j + 1's S' (which its dV precedes) and its own dP'
-            if (n >= Sh::kO && !(wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1) &&
-                                 wait(&sh.s_ready[(n - 1) & 1], (n - 1) / 2 & 1)))
+            // the dO of tile j is free with its dV (which tile j + 1's S' follows, or which is told of by
+            // itself) and its dP'
+            if (n >= Sh::kO && !wait(&sh.dp_ready[n & 1], (n - 2) / 2 & 1)) break;
+            if (n >= Sh::kO && !(Sh::kTwice ? wait(&sh.dv_done[n & 1], (n - 2) / 2 & 1)
+                                            : wait(&sh.s_ready[(n - 1) & 1], (n - 1) / 2 & 1)))
                 break;
             if (lane == 0)
                 load_tile(&maps.dout, smem_addr(sh.dout[os]), kSlabs, head, rank_row + e.x, &sh.do_full[os]);
@@ -868,11 +1000,11 @@ __global__ void __launch_bounds__(384, 1)
                 mbar_wait_bounded(&sh.do_full[i % Sh::kO], i / Sh::kO & 1);
     }
     } else {
-        more_registers<200>();
+        more_registers<104>();
         // ------------------------------------------------------------- scores to P and dS
         const int y = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
         const uint32_t at = tmem + (static_cast<uint32_t>(warp & 3) << 21);
-        const uint32_t s_at = at + 64 * y, dp_at = at + 128 + 64 * y;
+        const uint32_t s_base = at + 32 * y, dp_at = at + Sh::kDp + 32 * y;
         const float c = p.scale * 1.4426950408889634f;
         int rank = 0, key = 0;
         int64_t base = 0;
@@ -894,15 +1026,12 @@ __global__ void __launch_bounds__(384, 1)
                 key = e.z / p.P * kTile;
                 base = rank * p.Tp;
             }
-            // bit j of bits[i]: whether this thread's key is seen by row 64 y + 32 i + j
-            uint32_t bits[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+            // bit j: whether this thread's key is seen by row 32 y + j
+            uint32_t bits = 0xFFFFFFFFu;
             if (!(flags & kFull)) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int64_t row = e.x + 64 * y + 32 * i + lane;
-                    const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
-                    bits[i] = transpose_bits(visible_bits(r, key, warp & 3));
-                }
+                const int64_t row = e.x + 32 * y + lane;
+                const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
+                bits = transpose_bits(visible_bits(r, key, warp & 3));
             }
             if (!wait(&sh.aux_full[a], n / 2 & 1)) break;
             if (!wait(&sh.s_ready[n & 1], n / 2 & 1)) break;
@@ -912,7 +1041,7 @@ __global__ void __launch_bounds__(384, 1)
                 if (!wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
                 const int64_t row = e.x + t;
                 const int4 r = row < p.Tp ? b.spans[base + row] : make_int4(0, 0, 0, 0);
-                if (r.y == 0 && r.w == 0) {
+                if (y < 2 && r.y == 0 && r.w == 0) {
                     uint8_t *tile = y == 0 ? sh.dout[n % Sh::kO] : sh.q[n % Sh::kQ];
                     for (int i = 0; i < kSlabs; ++i)
                         for (int j = 0; j < 8; ++j)
@@ -921,85 +1050,84 @@ __global__ void __launch_bounds__(384, 1)
                 fence_proxy_async_smem();
             }
             tmem_fence_after();
-            uint32_t s[2][32];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_load32(s_at + 32 * i, s[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_wait_loads(s[i]);
+            const uint32_t s_at = s_base + (Sh::kTwice ? 128 * (n & 1) : 0);
+            uint32_t s[32], dp[32], w[16];
+            tmem_load32(s_at, s);
+            tmem_wait_loads(s);
             if (!(flags & kFull)) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!(bits[i] >> j & 1)) s[i][j] = 0xFF800000u;
+                for (int j = 0; j < 32; ++j)
+                    if (!(bits >> j & 1)) s[j] = 0xFF800000u;
             }
             const F2 c2 = pair_of(c, c);
+            const float4 *l4 = reinterpret_cast<const float4 *>(&sh.lse2[a][32 * y]);   // negated
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 *l4 = reinterpret_cast<const float4 *>(&sh.lse2[a][64 * y + 32 * i]);
-                uint32_t w[16];
+            for (int j = 0; j < 8; ++j) {
+                const float4 l = l4[j];
+                const float2 u = both(fma2(pair_of(s[4 * j], s[4 * j + 1]), c2, pair_of(l.x, l.y)));
+                const float2 v = both(fma2(pair_of(s[4 * j + 2], s[4 * j + 3]), c2, pair_of(l.z, l.w)));
+                const float pr[4] = {exp2_fast(u.x), exp2_fast(u.y), exp2_fast(v.x), exp2_fast(v.y)};
+                w[2 * j] = pack_bf16x2(pr[0], pr[1]);
+                w[2 * j + 1] = pack_bf16x2(pr[2], pr[3]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 l = l4[j];   // negated
-                    const float2 u = both(fma2(pair_of(s[i][4 * j], s[i][4 * j + 1]), c2, pair_of(l.x, l.y)));
-                    const float2 v = both(fma2(pair_of(s[i][4 * j + 2], s[i][4 * j + 3]), c2, pair_of(l.z, l.w)));
-                    const float pr[4] = {exp2_fast(u.x), exp2_fast(u.y), exp2_fast(v.x), exp2_fast(v.y)};
-                    w[2 * j] = pack_bf16x2(pr[0], pr[1]);
-                    w[2 * j + 1] = pack_bf16x2(pr[2], pr[3]);
-#pragma unroll
-                    for (int h = 0; h < 4; ++h) s[i][4 * j + h] = __float_as_uint(pr[h]);
+                for (int h = 0; h < 4; ++h) s[4 * j + h] = __float_as_uint(pr[h]);
+                if (!Sh::kTwice && j == 3) {
+                    tmem_store8(s_at, w);
+                    tmem_wait_stores();
+                    warp_arrive(&sh.half[0]);
                 }
-                tmem_store16(s_at + 16 * i, w);
-                tmem_wait_stores();
-                tmem_fence_before();
-                mbar_arrive(i == 0 ? &sh.half[0] : &sh.whole[0]);
             }
+            if (Sh::kTwice) tmem_store16(s_at, w);
+            else tmem_store8(s_at + 8, w + 8);
+            tmem_wait_stores();
+            warp_arrive(&sh.weights[0][n & 1]);
             if (!wait(&sh.dp_ready[n & 1], n / 2 & 1)) break;
             tmem_fence_after();
-            uint32_t dp[2][32];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_load32(dp_at + 32 * i, dp[i]);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) tmem_wait_loads(dp[i]);
+            tmem_load32(dp_at, dp);
+            tmem_wait_loads(dp);
             if (!(flags & kFull)) {   // a row that is none may have left a NaN
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (!(bits[i] >> j & 1)) dp[i][j] = 0;
+                for (int j = 0; j < 32; ++j)
+                    if (!(bits >> j & 1)) dp[j] = 0;
             }
+            const float4 *d4 = reinterpret_cast<const float4 *>(&sh.delta[a][32 * y]);   // negated
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float4 *d4 = reinterpret_cast<const float4 *>(&sh.delta[a][64 * y + 32 * i]);
-                uint32_t w[16];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float4 l = d4[j];   // negated
-                    const float2 u = both(mul2(pair_of(s[i][4 * j], s[i][4 * j + 1]),
-                                               add2(pair_of(dp[i][4 * j], dp[i][4 * j + 1]), pair_of(l.x, l.y))));
-                    const float2 v = both(mul2(pair_of(s[i][4 * j + 2], s[i][4 * j + 3]),
-                                               add2(pair_of(dp[i][4 * j + 2], dp[i][4 * j + 3]), pair_of(l.z, l.w))));
-                    w[2 * j] = pack_bf16x2(u.x, u.y);
-                    w[2 * j + 1] = pack_bf16x2(v.x, v.y);
+            for (int j = 0; j < 8; ++j) {
+                const float4 l = d4[j];
+                const float2 u = both(mul2(pair_of(s[4 * j], s[4 * j + 1]),
+                                           add2(pair_of(dp[4 * j], dp[4 * j + 1]), pair_of(l.x, l.y))));
+                const float2 v = both(mul2(pair_of(s[4 * j + 2], s[4 * j + 3]),
+                                           add2(pair_of(dp[4 * j + 2], dp[4 * j + 3]), pair_of(l.z, l.w))));
+                w[2 * j] = pack_bf16x2(u.x, u.y);
+                w[2 * j + 1] = pack_bf16x2(v.x, v.y);
+                if (!Sh::kTwice && j == 3) {
+                    tmem_store8(dp_at, w);
+                    tmem_wait_stores();
+                    warp_arrive(&sh.half[1]);
                 }
-                tmem_store16(dp_at + 16 * i, w);
-                tmem_wait_stores();
-                tmem_fence_before();
-                mbar_arrive(i == 0 ? &sh.half[1] : &sh.whole[1]);
             }
+            if (Sh::kTwice) tmem_store16(dp_at, w);
+            else tmem_store8(dp_at + 8, w + 8);
+            tmem_wait_stores();
+            warp_arrive(&sh.weights[1][n & 1]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.aux_empty[a]);
             if (flags & kLast) {
                 const int32_t pos = key + t < p.T ? position_of_token(b, key + t) : -1;
                 const int kvh = static_cast<int>(flags >> 16) / group;
-                if (!wait(&sh.acc_done[y], done++ & 1)) break;
+                const int of_k = y >> 1;   // two warpgroups write dV, two dK, every other 32 columns
+                if (!wait(&sh.acc_done[of_k], done++ & 1)) break;
                 tmem_fence_after();
+                const uint32_t acc = at + (of_k ? Sh::kDk : Sh::kDv);
+                bool write = pos >= 0;
+                if (flags & kPart) write = add_parts(b, b.units[e.w], kvh, warp - 4, of_k, y & 1, acc) && write;
                 float bad = 0.0f;
-                uint16_t *out = const_cast<uint16_t *>(row_of(y == 0 ? b.dv[rank] : b.dk[rank], pos, p.Hkv, kvh, p.D));
-                for (int i = 0; 32 * i < p.D; ++i)
-                    store_block(at + (y == 0 ? 256 : 384), i, p.D, y == 0 ? 1.0f : p.scale, true, out, pos >= 0, bad);
+                uint16_t *out = const_cast<uint16_t *>(row_of(of_k ? b.dk[rank] : b.dv[rank], pos, p.Hkv, kvh, p.D));
+                if (__any_sync(0xFFFFFFFFu, write))
+                    for (int i = y & 1; 32 * i < p.D; i += 2)
+                        store_block(acc, i, p.D, of_k ? p.scale : 1.0f, true, out, write, bad);
                 tmem_fence_before();
-                spoiled |= pos >= 0 && bad != 0.0f;
+                spoiled |= write && bad != 0.0f;
             }
         }
         if (spoiled) sh.spoiled = 1;
@@ -1066,25 +1194,59 @@ cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStrea
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
     const int64_t sms = sm_count(dev), row_tiles = (p.Tp + kTile - 1) / kTile, items = row_tiles * p.P * p.Hq;
-    dq_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), 384, sizeof(DqShared<DP>), stream>>>(
-        b, maps, items, row_tiles);
+    dq_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, sizeof(DqShared<DP>), stream>>>(
+        b, maps, items, row_tiles, tiles * p.P, static_cast<int>(sms));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    const int64_t slots = static_cast<int64_t>(tiles) * p.P, most = slots * p.Hkv;
-    dkdv_kernel<DP><<<static_cast<unsigned>(most < sms ? most : sms), 384, sizeof(DkvShared<DP>), stream>>>(b, maps,
-                                                                                                         slots);
+    const int64_t most = static_cast<int64_t>(b.unit_places) * p.Hkv;
+    dkdv_kernel<DP><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, sizeof(DkvShared<DP>), stream>>>(b, maps);
     return cudaGetLastError();
 }
 
 int64_t align256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
 
+// The workspace: delta and lse2 of every (head, row), the spans of every row, the
+// ranges and the list of every (tile, rank), the units, and the counters and
+// binary32 sums of the parts.
+struct Space {
+    int64_t lse2, spans, ranges, list, units, counters, counter_bytes, sums, total;
+    int32_t unit_places;
+};
+
+Space space_of(int64_t T, int64_t Tpad, int P, int Hq, int Hkv, int D)
+{
+    const int64_t slots = (T + kTile - 1) / kTile * P, Tp = Tpad / P, sms = sm_count(-1);
+    // Parts of one kv head: each tile that is cut has over `most` entries, so it makes at most twice its
+    // entries / most parts, and `most` is at least a half of a CTA's share and kLeastPart.
+    const int64_t entries = slots * ((Tp + kTile - 1) / kTile + 1) * (Hq / Hkv);
+    int64_t parts = 4 * sms / Hkv + 2;
+    if (parts > 2 * entries / kLeastPart) parts = 2 * entries / kLeastPart;
+    Space s;
+    int64_t at = align256(4 * Tpad * Hq);
+    s.lse2 = at;
+    at += align256(4 * Tpad * Hq);
+    s.spans = at;
+    at += align256(16 * Tpad);
+    s.ranges = at;
+    at += align256(16 * slots);
+    s.list = at;
+    at += align256(4 * slots);
+    s.units = at;
+    s.unit_places = static_cast<int32_t>(slots + parts);
+    at += align256(16 * (slots + parts));
+    s.counters = at;
+    s.counter_bytes = 256 + 64 * parts * Hkv;
+    at += align256(s.counter_bytes);
+    s.sums = at;
+    at += parts * Hkv * 2 * ((D + 31) / 32 * 32) * kTile * 4;
+    s.total = at;
+    return s;
+}
+
 }  // namespace
 
-// delta and lse2 of every (head, row), the spans of every row, the ranges and
-// the list of every (tile, rank), four counters.
-int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq)
+int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq, int Hkv, int D)
 {
-    const int64_t slots = (T + kTile - 1) / kTile * P;
-    return 2 * align256(4 * Tpad * Hq) + align256(16 * Tpad) + align256(16 * slots) + align256(4 * slots) + 256;
+    return space_of(T, Tpad, P, Hq, Hkv, D).total;
 }
 
 cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace, cudaStream_t stream)
@@ -1093,18 +1255,18 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     if (p.Tpad == 0) return cudaSuccess;
     const int tiles = static_cast<int>((p.T + kTile - 1) / kTile);
     const int64_t slots = static_cast<int64_t>(tiles) * p.P;
+    const Space s = space_of(p.T, p.Tpad, p.P, p.Hq, p.Hkv, p.D);
     uint8_t *w = static_cast<uint8_t *>(workspace);
     b.delta = reinterpret_cast<float *>(w);
-    w += align256(4 * p.Tpad * p.Hq);
-    b.lse2 = reinterpret_cast<float *>(w);
-    w += align256(4 * p.Tpad * p.Hq);
-    b.spans = reinterpret_cast<int4 *>(w);
-    w += align256(16 * p.Tpad);
-    b.ranges = reinterpret_cast<int4 *>(w);
-    w += align256(16 * slots);
-    b.list = reinterpret_cast<int32_t *>(w);
-    w += align256(4 * slots);
-    b.counters = reinterpret_cast<int32_t *>(w);
+    b.lse2 = reinterpret_cast<float *>(w + s.lse2);
+    b.spans = reinterpret_cast<int4 *>(w + s.spans);
+    b.ranges = reinterpret_cast<int4 *>(w + s.ranges);
+    b.list = reinterpret_cast<int32_t *>(w + s.list);
+    b.units = reinterpret_cast<int4 *>(w + s.units);
+    b.unit_places = s.unit_places;
+    b.counters = reinterpret_cast<int32_t *>(w + s.counters);
+    b.arrived = b.counters + 64;
+    b.sums = reinterpret_cast<float *>(w + s.sums);
     Maps maps;
     cudaError_t e = make_slab_map(&maps.q, p.q, p.D, p.Hq, p.Tpad);
     if (e == cudaSuccess) e = make_slab_map(&maps.k, p.k, p.D, p.Hkv, p.T);
@@ -1113,7 +1275,7 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     if (e != cudaSuccess) return e;
     const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * p.Hq;
     if (row_blocks + slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
-    if ((e = cudaMemsetAsync(b.counters, 0, 16, stream)) != cudaSuccess) return e;
+    if ((e = cudaMemsetAsync(b.counters, 0, s.counter_bytes, stream)) != cudaSuccess) return e;
     prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(b, tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     e = p.D <= 64 ? launch_tiled<64>(b, maps, tiles, stream) : launch_tiled<128>(b, maps, tiles, stream);

@@ -1359,9 +1359,9 @@ void fill_attention(AttentionParams &p, const cpt_plan *plan, const void *q, con
     p.scale = scale;
 }
 
-size_t backward_workspace(const cpt_plan *plan, int32_t q_heads)
+size_t backward_workspace(const cpt_plan *plan, int32_t q_heads, int32_t kv_heads, int32_t head_dim)
 {
-    return (size_t)attention_backward_workspace(plan->T, plan->Tpad, plan->P, q_heads);
+    return (size_t)attention_backward_workspace(plan->T, plan->Tpad, plan->P, q_heads, kv_heads, head_dim);
 }
 
 }  // namespace
@@ -1407,7 +1407,7 @@ size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int32_t q_he
         return 0;
     }
     if (check_attention(plan, q_heads, kv_heads, head_dim, CPT_BF16, 1.0f, 0, 0) != CPT_OK) return 0;
-    return backward_workspace(plan, q_heads);
+    return backward_workspace(plan, q_heads, kv_heads, head_dim);
 }
 
 cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,
@@ -1425,7 +1425,7 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
     if (dk_writers == nullptr || dv_writers == nullptr)
         return fail(CPT_ERR_INVALID_ARG, "dk_writers or dv_writers is NULL");
     if (plan->Tpad == 0) return CPT_OK;
-    const size_t need = backward_workspace(plan, q_heads);
+    const size_t need = backward_workspace(plan, q_heads, kv_heads, head_dim);
     if (workspace == nullptr) return fail(CPT_ERR_WORKSPACE, "workspace is NULL");
     if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
         return fail(CPT_ERR_WORKSPACE, "workspace is not 256-byte aligned");

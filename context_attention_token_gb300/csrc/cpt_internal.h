@@ -175,9 +175,14 @@ struct AttentionBackwardParams {
     int4 *spans;                   // [Tpad] keys every row sees
     int4 *ranges;                  // [key tiles][P] rows that see a tile
     int32_t *list;                 // tiles that some row sees, long ones from the front, others from the back
-    int32_t *counters;             // of both parts, items taken, whether an output is to be computed again
+    int4 *units;                   // these as whole or in parts
+    int32_t unit_places;
+    int32_t *counters;             // 0, 1: tiles in both parts of the list; 2: units taken; 3: an output is to be
+                                   // computed again; 4, 5: row tiles of all, 64 bits; 6: units
+    int32_t *arrived;              // parts of a tile that have come by, per place and warp
+    float *sums;                   // of the parts
 };
-int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq);
+int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq, int Hkv, int D);
 cudaError_t launch_attention_backward(AttentionBackwardParams p, void *workspace, cudaStream_t stream);
 cudaError_t read_attention_backward_wait_timeouts(unsigned int *count, bool reset);
 

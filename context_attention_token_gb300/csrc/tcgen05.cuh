@@ -196,6 +196,14 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[
         : "memory");
 }
 
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t *r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), CPT_IN4(r, 0),
+        CPT_IN4(r, 4)
+        : "memory");
+}
+
 __device__ __forceinline__ void tmem_wait_stores() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // ----------------------------------------------------------------- TMA

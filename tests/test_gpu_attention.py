@@ -139,6 +139,25 @@ def test_longer_documents(cpt, cuda_device, window, sinks):
     both(cpt, 3, 3, [1999, 601, 450], 2, 2, 64, window, sinks)
 
 
+@pytest.mark.parametrize("layout,P,lens,Hq,Hk,D,window,sinks", [
+    (0, 1, [4096], 2, 1, 64, 64, 4),          # a tile of sinks that every row sees, among short ones
+    (1, 2, [3000, 1096], 2, 1, 128, 70, 5),
+    (0, 2, [4096], 1, 1, 128, 1 << 20, 0),    # the whole triangle of one head
+    (3, 1, [3001], 4, 2, 80, 33, 130)])
+def test_long_documents_with_few_heads(cpt, cuda_device, layout, P, lens, Hq, Hk, D, window, sinks):
+    """Key tiles that many rows see are cut into parts; the sums of the parts are
+    the same in every run."""
+    b = both(cpt, layout, P, lens, Hq, Hk, D, window, sinks)
+    first = [x.t.clone() for x in [b.dq] + b.dk + b.dv]
+    ws = b.workspace()
+    for _ in range(20):
+        b.backward(ws.t)
+    torch.cuda.synchronize()
+    for x, y in zip([b.dq] + b.dk + b.dv, first):
+        assert torch.equal(x.t, y)
+    assert ws.bands_intact() and cpt.cpt_kernel_wait_timeouts() == 0
+
+
 def test_many_short_documents(cpt, cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(0, 40, 90)]
