@@ -122,7 +122,7 @@ __device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int
     return t;
 }
 
-template <int DP>
+template <int DP, int STEPS>
 __global__ void __launch_bounds__(384, 1)
     attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
                      int64_t row_tiles, bool pair)
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(384, 1)
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int group = p.Hq / p.Hkv;
-    const int steps = (p.D + 15) / 16;
+    const int steps = STEPS ? STEPS : (p.D + 15) / 16;
 
     // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
     if (warp < 4) {
@@ -287,9 +287,13 @@ __global__ void __launch_bounds__(384, 1)
             if (leader) mbar_arrive(&sh.info_empty[slot]);
             const bool of_prev = (prev & (kNeed << x)) != 0, of_this = (e & (kNeed << x)) != 0;
             const uint32_t vs = v % Sh::kStages, ks = c % Sh::kStages;
+            // what is waited for outside the turn; a new item's Q and K only after the last one's product
+            auto operands = [&]() {
+                return (!(e & kFirst) || wait(&sh.q_full, items_seen & 1)) &&
+                       (!of_this || wait(&sh.kv_full[ks], c / Sh::kStages & 1));
+            };
             if (of_prev && !(wait(&sh.kv_full[vs], v / Sh::kStages & 1) && wait(&sh.p_half[x], ps & 1))) break;
-            if ((e & kFirst) && !wait(&sh.q_full, items_seen & 1)) break;
-            if (of_this && !wait(&sh.kv_full[ks], c / Sh::kStages & 1)) break;
+            if (!(e & kFirst) && !operands()) break;
             if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
@@ -301,8 +305,9 @@ __global__ void __launch_bounds__(384, 1)
                 started = true;
             }
             if (prev & kLast) mma_commit(leader, &sh.out_done[x]);
+            if ((e & kFirst) && !operands()) break;
             if (of_this)
-                mma_scores(leader, s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
+                mma_scores<STEPS>(leader, s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
             if (leader) mbar_arrive(&sh.turn[1 - x]);
             if (e & kStop) break;
             if (e & kFirst) started = false;
@@ -390,18 +395,22 @@ __global__ void __launch_bounds__(384, 1)
                         if (!(bits >> j & 1)) s[j] = 0xFF800000u;
                 };
                 if (__any_sync(0xFFFFFFFFu, ref == -INFINITY)) {
-                    float mx = -INFINITY;
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll 1
-                    for (int i = 0; i < 4; ++i) {
-                        uint32_t s[32];
-                        load(i, s);
-                        tmem_wait_loads(s);
-                        hide(i, s);
+                    for (int i = 0; i < 4; i += 2) {
+                        uint32_t s[2][32];
+                        load(i, s[0]);
+                        load(i + 1, s[1]);
 #pragma unroll
-                        for (int j = 0; j < 32; j += 2)
-                            mx = fmaxf(mx, fmaxf(__uint_as_float(s[j]), __uint_as_float(s[j + 1])));
+                        for (int h = 0; h < 2; ++h) {
+                            tmem_wait_loads(s[h]);
+                            hide(i + h, s[h]);
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[h][j]));
+                        }
                     }
-                    if (ref == -INFINITY) ref = mx * c;
+                    mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (ref == -INFINITY) ref = mx[0] * c;
                 }
                 const bool big = l > 1.0995116e12f && l < INFINITY;
                 if (__any_sync(0xFFFFFFFFu, big)) {
@@ -538,7 +547,7 @@ cudaError_t make_slab_map(CUtensorMap *map, const void *base, int D, int heads, 
 
 namespace {
 
-template <int DP>
+template <int DP, int STEPS>
 cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_t stream)
 {
     int dev = 0;
@@ -546,7 +555,7 @@ cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_
     if (e != cudaSuccess) return e;
     static std::atomic<bool> attr_set[64];
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(attention_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+        e = cudaFuncSetAttribute(attention_kernel<DP, STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
@@ -556,7 +565,7 @@ cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_
     const int64_t row_tiles = (p.Tp + rows - 1) / rows;
     const int64_t items = row_tiles * p.P * (pair ? p.Hq / 2 : p.Hq);
     const int64_t sms = sm_count(dev);
-    attention_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), 384, Shape<DP>::kSmem, stream>>>(
+    attention_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), 384, Shape<DP>::kSmem, stream>>>(
         p, maps, items, row_tiles, pair);
     return cudaGetLastError();
 }
@@ -571,7 +580,10 @@ cudaError_t launch_attention(const AttentionParams &p, cudaStream_t stream)
     if (e == cudaSuccess) e = make_slab_map(&maps.k, p.k, p.D, p.Hkv, p.T);
     if (e == cudaSuccess) e = make_slab_map(&maps.v, p.v, p.D, p.Hkv, p.T);
     if (e != cudaSuccess) return e;
-    return p.D <= 64 ? launch_tiled<64>(p, maps, stream) : launch_tiled<128>(p, maps, stream);
+    // the common heads have kernels of their own (see mma_scores)
+    if (p.D == 64) return launch_tiled<64, 4>(p, maps, stream);
+    if (p.D == 128) return launch_tiled<128, 8>(p, maps, stream);
+    return p.D < 64 ? launch_tiled<64, 0>(p, maps, stream) : launch_tiled<128, 0>(p, maps, stream);
 }
 
 cudaError_t read_attention_bounds_violations(unsigned int *count, bool reset)

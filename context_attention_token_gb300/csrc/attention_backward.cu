@@ -396,7 +396,7 @@ __device__ __forceinline__ DqItem dq_item(const AttentionParams &p, int64_t i, i
     return t;
 }
 
-template <int DP>
+template <int DP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t items, int64_t row_tiles,
               int slots, int sms)
@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
-    const int steps = (p.D + 15) / 16;
+    const int steps = STEPS ? STEPS : (p.D + 15) / 16;
     // 128 x 64 + 512 x 104 of the 640 x 96 registers of the launch
     if (warp < 4) {
     fewer_registers<64>();
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (e & kStop) return false;
                 if ((e & kFirst) && !wait(&sh.q_full, items_seen++ & 1)) return false;
                 if (!wait(&sh.k_full[ks], ns / Sh::kK & 1)) return false;
-                mma_scores(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
+                mma_scores<STEPS>(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
                 mma_commit(leader, &sh.s_ready[ns & 1]);
                 flags[ns & 1] = e;
                 ++ns;
@@ -570,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // dP's columns are in registers long before dS is made of them
                 if (n > 0 && !wait(&sh.dp_free, (n - 1) & 1)) break;
                 tmem_fence_after();
-                mma_scores(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
+                mma_scores<STEPS>(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
                 mma_commit(leader, &sh.dp_ready[n & 1]);
             }
         }
@@ -750,7 +750,7 @@ __device__ __noinline__ bool add_parts(const Params &b, int4 unit, int kvh, int 
     return true;
 }
 
-template <int DP>
+template <int DP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1)
     dkdv_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps)
 {
@@ -793,7 +793,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_after();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
-    const int steps = (p.D + 15) / 16, group = p.Hq / p.Hkv;
+    const int steps = STEPS ? STEPS : (p.D + 15) / 16, group = p.Hq / p.Hkv;
     const int64_t items = static_cast<int64_t>(b.counters[6]) * p.Hkv;
     // 128 x 64 + 512 x 104 of the 640 x 96 registers of the launch
     if (warp < 4) {
@@ -941,7 +941,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0 && !late && !product()) break;
             if (!more) break;
             if (fresh && !(wait(&sh.kv_full, k++ & 1) && operand())) break;
-            mma_scores(leader, scores_at + (twice ? 128 * (n & 1) : 0), key_at,
+            mma_scores<STEPS>(leader, scores_at + (twice ? 128 * (n & 1) : 0), key_at,
                        first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
             mma_commit(leader, first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
             if (late) {
@@ -1178,7 +1178,7 @@ __global__ void __launch_bounds__(256) repair_kernel(const __grid_constant__ Par
 
 // ----------------------------------------------------------------- launch
 
-template <int DP>
+template <int DP, int STEPS>
 cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStream_t stream)
 {
     const AttentionParams &p = b.a;
@@ -1187,18 +1187,18 @@ cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStrea
     if (e != cudaSuccess) return e;
     static std::atomic<bool> attr_set[64];
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(dq_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DqShared<DP>));
+        e = cudaFuncSetAttribute(dq_kernel<DP, STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DqShared<DP>));
         if (e != cudaSuccess) return e;
-        e = cudaFuncSetAttribute(dkdv_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DkvShared<DP>));
+        e = cudaFuncSetAttribute(dkdv_kernel<DP, STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, sizeof(DkvShared<DP>));
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
     const int64_t sms = sm_count(dev), row_tiles = (p.Tp + kTile - 1) / kTile, items = row_tiles * p.P * p.Hq;
-    dq_kernel<DP><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, sizeof(DqShared<DP>), stream>>>(
+    dq_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, sizeof(DqShared<DP>), stream>>>(
         b, maps, items, row_tiles, tiles * p.P, static_cast<int>(sms));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     const int64_t most = static_cast<int64_t>(b.unit_places) * p.Hkv;
-    dkdv_kernel<DP><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, sizeof(DkvShared<DP>), stream>>>(b, maps);
+    dkdv_kernel<DP, STEPS><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, sizeof(DkvShared<DP>), stream>>>(b, maps);
     return cudaGetLastError();
 }
 
@@ -1278,7 +1278,10 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     if ((e = cudaMemsetAsync(b.counters, 0, s.counter_bytes, stream)) != cudaSuccess) return e;
     prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(b, tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    e = p.D <= 64 ? launch_tiled<64>(b, maps, tiles, stream) : launch_tiled<128>(b, maps, tiles, stream);
+    // the common heads have kernels of their own (see mma_scores)
+    if (p.D == 64) e = launch_tiled<64, 4>(b, maps, tiles, stream);
+    else if (p.D == 128) e = launch_tiled<128, 8>(b, maps, tiles, stream);
+    else e = p.D < 64 ? launch_tiled<64, 0>(b, maps, tiles, stream) : launch_tiled<128, 0>(b, maps, tiles, stream);
     if (e != cudaSuccess) return e;
     repair_kernel<<<static_cast<unsigned>(4 * sm_count(-1)), 256, 0, stream>>>(b);
     return cudaGetLastError();

@@ -86,30 +86,17 @@ __device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, ui
 // which cost some 20 cycles each, are few: one commit stands for everything that
 // its warp issued before it.
 
-template <int STEPS>
-__device__ __forceinline__ void mma_scores_fixed(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape)
-{
-#pragma unroll
-    for (int k = 0; k < STEPS; ++k) {
-        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        mma_smem(leader, d, a + at, b + at, kInnerUpper, shape, k > 0);
-    }
-}
-
 // Rows x columns of scores: both operands from shared memory, `steps` (at most
-// 8) inner steps of 16, four to a slab.
+// 8) inner steps of 16, four to a slab. STEPS, unless 0, is their number: code
+// for others in the same kernel costs it 2 to 6 %.
+template <int STEPS>
 __device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
     const uint32_t da = inner_lower(a), db = inner_lower(b);
-    if (steps == 8) {
-        mma_scores_fixed<8>(leader, d, da, db, shape);
-    } else if (steps == 4) {
-        mma_scores_fixed<4>(leader, d, da, db, shape);
-    } else {
-        for (int k = 0; k < steps; ++k) {
-            const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-            mma_smem(leader, d, da + at, db + at, kInnerUpper, shape, k > 0);
-        }
+#pragma unroll
+    for (int k = 0; k < (STEPS ? STEPS : 8); ++k) {
+        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+        if (STEPS || k < steps) mma_smem(leader, d, da + at, db + at, kInnerUpper, shape, k > 0);
     }
 }
 
@@ -329,7 +316,7 @@ __device__ __forceinline__ uint32_t span_bits(int lo, int hi, int w)
 
 // Columns [32 block, 32 block + 32) below D of this warp's 32 rows: scaled,
 // rounded to bf16 and written where `write` holds; zeros where `live` does not.
-// Returns NaN (added to `bad`) once a written value is not finite.
+// `bad` becomes NaN once a value is not finite.
 __device__ __forceinline__ void store_block(uint32_t tmem, int block, int D, float scale, bool live, uint16_t *row,
                                             bool write, float &bad)
 {
@@ -338,18 +325,27 @@ __device__ __forceinline__ void store_block(uint32_t tmem, int block, int D, flo
     tmem_load32(tmem + 32 * block, o);
     tmem_wait_loads(o);
     uint4 u[4];
+    const F2 zero = pair_of(0.0f, 0.0f), by = pair_of(scale, scale);
+    F2 odd[4] = {zero, zero, zero, zero};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const float x = live ? __uint_as_float(o[8 * i + 2 * j]) * scale : 0.0f;
-            const float y = live ? __uint_as_float(o[8 * i + 2 * j + 1]) * scale : 0.0f;
-            if (32 * block + 8 * i < D) bad = __fmaf_rn(x, 0.0f, __fmaf_rn(y, 0.0f, bad));
-            w[j] = pack_bf16x2(x, y);
+            const F2 x = mul2(pair_of(o[8 * i + 2 * j], o[8 * i + 2 * j + 1]), by);
+            odd[i] = fma2(x, zero, odd[i]);
+            const float2 v = both(x);
+            w[j] = live ? pack_bf16x2(v.x, v.y) : 0;
         }
         u[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    float sum = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 v = both(odd[i]);
+        if (32 * block + 8 * i < D) sum += v.x + v.y;
+    }
+    if (live) bad += sum;
     auto swap = [&](uint4 &low, uint4 &high, int bit) {   // lanes without the bit keep `low`, the others `high`
         const bool upper = (lane & bit) != 0;
         uint4 s = upper ? low : high;
