@@ -173,8 +173,16 @@ def cpt_status_string(status: int) -> str:
 
 # ------------------------------------------------------------------ marshalling
 
+# The current stream's handle without building a Stream object (3 us less a
+# call); torch builds that lack these calls take the public way.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None and _raw_device is not None and torch.cuda.is_initialized():
+            return _raw_stream(_raw_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -633,39 +641,47 @@ def cpt_rotary_apply(rotary: Rotary, plan: Plan, srcs, dsts, positions: torch.Te
         raise ValueError("srcs and dsts differ in length")
     if not srcs:
         raise ValueError("no tensors")
-    rows = {CPT_ORDER_GLOBAL: plan.total_tokens, CPT_ORDER_LOCAL: plan.padded_tokens}
-    if src_order not in rows or dst_order not in rows:
+    if src_order not in (0, 1) or dst_order not in (0, 1):
         raise ValueError("unknown order")
-    heads = []
-    for i, (a, b) in enumerate(zip(srcs, dsts)):
-        if a.dtype != srcs[0].dtype or b.dtype != srcs[0].dtype:
+    rows_in = plan.padded_tokens if src_order else plan.total_tokens
+    rows_out = plan.padded_tokens if dst_order else plan.total_tokens
+    dtype, d, heads, n = srcs[0].dtype, rotary.head_dim, [], len(srcs)
+    for i in range(n):
+        a, b = srcs[i], dsts[i]
+        if a.dtype != dtype or b.dtype != dtype:
             raise ValueError("srcs and dsts must share one dtype")
-        for t, what in ((a, "srcs"), (b, "dsts")):
-            if t.dim() < 2 or t.shape[-1] != rotary.head_dim:
-                raise ValueError(f"{what}[{i}] has no heads of {rotary.head_dim} elements")
-        if a.shape[-2] != b.shape[-2]:
+        sa, sb = a.shape, b.shape
+        if len(sa) < 2 or sa[-1] != d or len(sb) < 2 or sb[-1] != d:
+            raise ValueError(f"srcs[{i}] or dsts[{i}] has no heads of {d} elements")
+        h = sa[-2]
+        if sb[-2] != h:
             raise ValueError(f"srcs[{i}] and dsts[{i}] differ in heads")
-        heads.append(int(a.shape[-2]))
-        row = heads[-1] * rotary.head_dim * a.element_size()
-        _need(a, rows[src_order] * row, f"srcs[{i}]")
-        _need(b, rows[dst_order] * row, f"dsts[{i}]")
-    _need(positions, 4 * rotary.n_axes * plan.total_tokens, "positions", torch.int32)
-    _check(_lib.cpt_rotary_apply(rotary.handle, plan.handle, len(srcs), _ptr_array(srcs), _ptr_array(dsts),
-                                 (_i32 * len(heads))(*heads), _dtype_code(srcs[0]), _ptr(positions),
+        heads.append(h)
+        if a.numel() < rows_in * h * d or b.numel() < rows_out * h * d:
+            raise ValueError(f"srcs[{i}] or dsts[{i}] holds fewer than {rows_in} and {rows_out} rows")
+    if positions.dtype != torch.int32 or positions.numel() < rotary.n_axes * plan.total_tokens:
+        raise ValueError("positions must hold n_axes * total_tokens int32 values")
+    _check(_lib.cpt_rotary_apply(rotary.handle, plan.handle, n, _ptr_array(srcs), _ptr_array(dsts),
+                                 (_i32 * n)(*heads), _dtype_code(srcs[0]), _ptr(positions),
                                  src_order, dst_order, 1 if inverse else 0, _stream(stream)))
 
 
-def _attention_shape(plan: Plan, q, k, same_as_q, same_as_k, lse):
+def _attention_shape(plan: Plan, q, k, like_q, like_k, lse):
     """(q_heads, kv_heads, head_dim, dtype code), every buffer large enough."""
-    if q.dim() < 2 or k.dim() < 2 or q.shape[-1] != k.shape[-1]:
+    qs, ks = q.shape, k.shape
+    if len(qs) < 2 or len(ks) < 2 or qs[-1] != ks[-1]:
         raise ValueError("q and k must end in [heads, head_dim] with one head_dim")
-    hq, hk, d = int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1])
-    for group, like, rows, heads in ((same_as_q, q, plan.padded_tokens, hq), (same_as_k, k, plan.total_tokens, hk)):
-        for t, what in group:
-            if t.dtype != q.dtype or t.dim() < 2 or t.shape[-2:] != like.shape[-2:]:
-                raise ValueError(f"{what} differs in dtype, heads or head_dim")
-            _need(t, rows * heads * d * t.element_size(), what)
-    _need(lse, 4 * hq * plan.padded_tokens, "lse", torch.float32)
+    hq, hk, d, dtype = qs[-2], ks[-2], qs[-1], q.dtype
+    for group, heads, rows in ((like_q, hq, plan.padded_tokens), (like_k, hk, plan.total_tokens)):
+        need = rows * heads * d
+        for t in group:
+            s = t.shape
+            if t.dtype != dtype or len(s) < 2 or s[-1] != d or s[-2] != heads:
+                raise ValueError("tensors of q's or k's kind differ in dtype, heads or head_dim")
+            if t.numel() < need:
+                raise ValueError(f"a tensor of {heads} heads holds {t.numel()} elements but the call touches {need}")
+    if lse.dtype != torch.float32 or lse.numel() < hq * plan.padded_tokens:
+        raise ValueError("lse must hold q_heads * padded_tokens float32 values")
     return hq, hk, d, _dtype_code(q)
 
 
@@ -674,7 +690,7 @@ def cpt_attention(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """out ([P, T_pad/P, Hq, D], like q) and lse ([Hq, T_pad]) = causal attention
     of rank-local queries over the packed documents' keys and values ([T, Hkv,
     D], global order) with a sliding window and `sinks` first tokens."""
-    hq, hk, d, code = _attention_shape(plan, q, k, ((q, "q"), (out, "out")), ((k, "k"), (v, "v")), lse)
+    hq, hk, d, code = _attention_shape(plan, q, k, (q, out), (k, v), lse)
     _check(_lib.cpt_attention(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), hq, hk, d, code,
                               scale, window, sinks, _stream(stream)))
 
@@ -688,8 +704,7 @@ def cpt_attention_backward(plan: Plan, q, k, v, out, lse, dout, dq, dk_writers, 
     """dq (like q) and every writer's dk and dv ([P, T_pad, Hkv, D] or lists of P
     tensors) of cpt_attention. Without a workspace the binding allocates one
     from torch on the current stream."""
-    hq, hk, d, code = _attention_shape(plan, q, k, ((q, "q"), (out, "out"), (dout, "dout"), (dq, "dq")),
-                                       ((k, "k"), (v, "v")), lse)
+    hq, hk, d, code = _attention_shape(plan, q, k, (q, out, dout, dq), (k, v), lse)
     P = plan.cp_size
     dkw, dvw = _Parts(dk_writers, P), _Parts(dv_writers, P)
     for parts, what in ((dkw, "dk_writers"), (dvw, "dv_writers")):
