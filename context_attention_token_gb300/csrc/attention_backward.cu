@@ -920,6 +920,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t with = first ? smem_addr(sh.dout[i % Sh::kO]) : smem_addr(sh.q[i % Sh::kQ]);
             const bool twice = Sh::kTwice && first;
             auto product = [&]() {
+                // dV reads dO, for which P has not waited
+                if (first && !wait(&sh.do_full[i % Sh::kO], i / Sh::kO & 1)) return false;
                 const uint32_t weights = scores_at + (twice ? 128 * (i & 1) : 0);
                 if (!Sh::kTwice) {
                     if (!wait(&sh.half[warp - 1], i & 1)) return false;

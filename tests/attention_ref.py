@@ -120,6 +120,54 @@ def _writers(p, ds, err, qd, do, P, G, Tpad):
     return res
 
 
+def sampled_rows(b, rows):
+    """out, lse and dq of some local rows against all keys, with their bounds
+    (the rows' own masks; lse and delta from b.out, b.lse)."""
+    see = visible(b.l2r[rows], b.cu, b.T, b.window, b.sinks, "cuda")
+    at = torch.from_numpy(rows).cuda()
+    out, lse, tol = attention64(b.q[at], b.k, b.v, see, b.scale)
+    dq, dq_tol, _ = backward64(b.q[at], b.k, b.v, b.out.t[at], b.dout[at], see, b.scale, 1)
+    return out, lse, tol, dq, dq_tol
+
+
+def sampled_keys(b, keys):
+    """For every rank (dk, bound, dv, bound) of some raw keys, from the rows'
+    log-sum-exp in b.lse and the outputs in b.out."""
+    G, Tp = b.Hq // b.Hk, b.Tpad // b.P
+    at = torch.from_numpy(keys).cuda()
+    kk, vv = (x[at].double().repeat_interleave(G, 1) for x in (b.k, b.v))
+    res = []
+    for r in range(b.P):
+        rows = slice(r * Tp, (r + 1) * Tp)
+        q, do, o = b.q[rows].double(), b.dout[rows].double(), b.out.t[rows].double()
+        see = visible_keys(b, rows, keys)
+        s = torch.einsum("ihd,jhd->hij", q, kk) * b.scale
+        p = torch.where(see, torch.exp(s - b.lse.t[:, rows, None].double()), 0.0)
+        dp = torch.einsum("ihd,jhd->hij", do, vv)
+        delta = (do * o).sum(-1).t()[..., None]
+        mag = torch.einsum("ihd,jhd->hij", do.abs(), vv.abs()) + (do * o).abs().sum(-1).t()[..., None]
+        ds = torch.where(see, p * (dp - delta), 0.0) * b.scale
+        err = torch.where(see, p * mag, 0.0) * b.scale * 2 * E32 + U * ds.abs()
+        one = []
+        for w, e, x in ((ds, err, q), (p, p * (U + 2 * E32), do)):
+            g = torch.einsum("hij,ihd->jhd", w, x).reshape(len(keys), b.Hk, G, b.D).sum(2)
+            m = torch.einsum("hij,ihd->jhd", e, x.abs()).reshape(len(keys), b.Hk, G, b.D).sum(2)
+            one.append((g, m + U * (1 + U) * g.abs() + 1e-30))
+        res.append(one)
+    return res
+
+
+def visible_keys(b, rows, keys):
+    l2r = b.l2r[rows]
+    doc = np.searchsorted(b.cu, np.maximum(l2r, 0), side="right") - 1
+    kdoc = np.searchsorted(b.cu, keys, side="right") - 1
+    u = torch.from_numpy(np.maximum(l2r, 0) - b.cu[doc]).cuda()[:, None]
+    j = torch.from_numpy(keys - b.cu[kdoc]).cuda()[None]
+    same = torch.from_numpy(doc).cuda()[:, None] == torch.from_numpy(kdoc).cuda()[None]
+    real = torch.from_numpy(l2r >= 0).cuda()[:, None]
+    return real & same & (u >= j) & ((u - j < b.window) | (j < b.sinks))
+
+
 def to_padded(x, cu, cup, Tpad):
     """Raw global rows placed in padded global order, zeros in padding."""
     out = torch.zeros((Tpad,) + tuple(x.shape[1:]), dtype=x.dtype, device=x.device)

@@ -158,6 +158,43 @@ def test_long_documents_with_few_heads(cpt, cuda_device, layout, P, lens, Hq, Hk
     assert ws.bands_intact() and cpt.cpt_kernel_wait_timeouts() == 0
 
 
+@pytest.mark.parametrize("layout,P,lens,Hq,Hk,D,window,sinks", [
+    (0, 4, [32768], 8, 8, 128, 4096, 4),
+    (1, 4, [20000, 3000, 777, 1, 9000, 22], 8, 2, 64, 1000, 5),
+    (3, 3, [12000, 40, 9001], 6, 3, 80, 500, 0)])
+def test_large_batches(cpt, cuda_device, layout, P, lens, Hq, Hk, D, window, sinks):
+    """Batches that keep every SM busy for many tiles: the same bits in every run,
+    whatever the workspace and the outputs held, and some rows and keys checked."""
+    if layout == 1:
+        lens = lens + [-sum(lens) % P]
+    b = Batch(cpt, layout, P, lens, Hq, Hk, D, window, sinks)
+    ws, first = b.workspace(), None
+    for fill in (0x00, 0xFF, 0x7F, 0x3C):
+        ws.t.fill_(fill)
+        for x in [b.out, b.lse, b.dq] + b.dk + b.dv:
+            x.t.view(torch.uint8).fill_(fill)
+        b.forward()
+        b.backward(ws.t)
+        torch.cuda.synchronize()
+        got = [x.t.clone() for x in [b.out, b.lse, b.dq] + b.dk + b.dv]
+        first = first or got
+        for x, y in zip(got, first):
+            assert torch.equal(x, y)
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+    rng = np.random.default_rng(3)
+    rows = np.sort(rng.choice(np.flatnonzero(b.l2r >= 0), 96, replace=False))
+    at = torch.from_numpy(rows).cuda()
+    out, lse, tol, dq, dq_tol = ref.sampled_rows(b, rows)
+    assert ((b.out.t[at].double() - out).abs() <= tol).all()
+    assert ((b.lse.t[:, at].double() - lse).abs() <= ref.E32 + 2.0 ** -22 * lse.abs()).all()
+    assert ((b.dq.t[at].double() - dq).abs() <= dq_tol).all()
+    keys = np.unique(np.concatenate([rng.choice(b.T, 40), b.cu[:-1][np.diff(b.cu) > 0]]))
+    for r, pair in enumerate(ref.sampled_keys(b, keys)):
+        for buf, (want, bound) in zip((b.dk[r], b.dv[r]), pair):
+            diff = (ref_raw(b, buf.t.double())[torch.from_numpy(keys).cuda()] - want).abs()
+            assert (diff <= bound).all(), (r, float((diff - bound).max()))
+
+
 def test_many_short_documents(cpt, cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(0, 40, 90)]
