@@ -297,32 +297,32 @@ __global__ void __launch_bounds__(384, 1)
             if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
-                mma_weights<4>(leader, o_at, s_at, kv_at + vs * Sh::kTileBytes, o_shape, started);
+                mma_weights<1, 4>(o_at, s_at, 0, kv_at + vs * Sh::kTileBytes, 0, o_shape, started);
                 if (!wait(&sh.p_ready[x], ps & 1)) break;
                 ++ps;
                 tmem_fence_after();
-                mma_weights<4>(leader, o_at, s_at + 32, kv_at + vs * Sh::kTileBytes + 8192, o_shape, true);
+                mma_weights<1, 4>(o_at, s_at + 32, 0, kv_at + vs * Sh::kTileBytes + 8192, 0, o_shape, true);
                 started = true;
             }
-            if (prev & kLast) mma_commit(leader, &sh.out_done[x]);
+            if (prev & kLast) mma_commit(&sh.out_done[x]);
             if ((e & kFirst) && !operands()) break;
             if (of_this)
-                mma_scores<STEPS>(leader, s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
+                mma_scores<STEPS>(s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
             if (leader) mbar_arrive(&sh.turn[1 - x]);
             if (e & kStop) break;
             if (e & kFirst) started = false;
             if (e & (3 * kNeed)) {
-                mma_commit(leader, &sh.step[x][c / 2 % kSteps]);
+                mma_commit(&sh.step[x][c / 2 % kSteps]);
                 v = c + 1;
                 c += 2;
             }
             if (e & kLast) {
-                mma_commit(leader, &sh.q_empty);
+                mma_commit(&sh.q_empty);
                 ++items_seen;
             }
             prev = e;
         }
-        mma_commit(leader, &sh.drained[x]);
+        mma_commit(&sh.drained[x]);
         mbar_wait_bounded(&sh.drained[x], 0);
     } else {
         // ------------------------------------------------------------- rows

@@ -267,19 +267,16 @@ __device__ __forceinline__ void load_tile(const CUtensorMap *map, uint32_t to, i
 // d (+)= A B with the weights of a tile, which lie as four quarters of 32 inner
 // columns (one for each warpgroup), each over the first half of the columns of
 // scores that it came from.
-__device__ __forceinline__ void mma_quarters(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_quarters(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-#pragma unroll
-    for (int w = 0; w < 4; ++w) mma_weights<2>(leader, d, a + 32 * w, b + 4096 * w, shape, add || w > 0);
+    mma_weights<4, 2>(d, a, 32, b, 4096, shape, add);
 }
 
 // The same over the first or second 16 inner columns of every quarter.
 template <int PART>
-__device__ __forceinline__ void mma_half(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+__device__ __forceinline__ void mma_half(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
 {
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-        mma_weights<1>(leader, d, a + 32 * w + 8 * PART, b + 4096 * w + 2048 * PART, shape, add || w > 0);
+    mma_weights<4, 1>(d, a + 8 * PART, 32, b + 2048 * PART, 4096, shape, add);
 }
 
 // One arrival of a warp whose lanes have all written (or read) tensor memory.
@@ -540,8 +537,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (e & kStop) return false;
                 if ((e & kFirst) && !wait(&sh.q_full, items_seen++ & 1)) return false;
                 if (!wait(&sh.k_full[ks], ns / Sh::kK & 1)) return false;
-                mma_scores<STEPS>(leader, tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
-                mma_commit(leader, &sh.s_ready[ns & 1]);
+                mma_scores<STEPS>(tmem + 128 * (ns & 1), smem_addr(sh.q), smem_addr(sh.k[ks]), s_shape, steps);
+                mma_commit(&sh.s_ready[ns & 1]);
                 flags[ns & 1] = e;
                 ++ns;
                 return true;
@@ -551,9 +548,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!wait(&sh.ds_ready[i & 1], i / 2 & 1)) break;
                 tmem_fence_after();
                 const uint32_t e = flags[i & 1], ks = i % Sh::kK;
-                mma_quarters(leader, tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
-                if (e & kLast) mma_commit(leader, &sh.acc_done);
-                mma_commit(leader, &sh.k_empty[ks]);
+                mma_quarters(tmem + 384, tmem + 128 * (i & 1), smem_addr(sh.k[ks]), o_shape, !(e & kFirst));
+                if (e & kLast) mma_commit(&sh.acc_done);
+                mma_commit(&sh.k_empty[ks]);
                 if (more) more = issue_s();
             }
         } else {
@@ -570,11 +567,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // dP's columns are in registers long before dS is made of them
                 if (n > 0 && !wait(&sh.dp_free, (n - 1) & 1)) break;
                 tmem_fence_after();
-                mma_scores<STEPS>(leader, tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
-                mma_commit(leader, &sh.dp_ready[n & 1]);
+                mma_scores<STEPS>(tmem + 256, smem_addr(sh.dout), smem_addr(sh.v[vs]), s_shape, steps);
+                mma_commit(&sh.dp_ready[n & 1]);
             }
         }
-        mma_commit(leader, &sh.drained[warp - 1]);
+        mma_commit(&sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
     } else if (warp == 3 && blockIdx.x == 0) {
         // ------------------------------------------------------------- the next kernel's units
@@ -926,16 +923,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!Sh::kTwice) {
                     if (!wait(&sh.half[warp - 1], i & 1)) return false;
                     tmem_fence_after();
-                    mma_half<0>(leader, acc, weights, with, o_shape, !(prev & kFirst));
+                    mma_half<0>(acc, weights, with, o_shape, !(prev & kFirst));
                     if (!wait(&sh.weights[warp - 1][i & 1], i / 2 & 1)) return false;
                     tmem_fence_after();
-                    mma_half<1>(leader, acc, weights, with, o_shape, true);
+                    mma_half<1>(acc, weights, with, o_shape, true);
                 } else {
                     if (!wait(&sh.weights[warp - 1][i & 1], i / 2 & 1)) return false;
                     tmem_fence_after();
-                    mma_quarters(leader, acc, weights, with, o_shape, !(prev & kFirst));
+                    mma_quarters(acc, weights, with, o_shape, !(prev & kFirst));
                 }
-                if (prev & kLast) mma_commit(leader, &sh.acc_done[warp - 1]);
+                if (prev & kLast) mma_commit(&sh.acc_done[warp - 1]);
                 return true;
             };
             const bool late = n > 0 && twice && more && !fresh;   // the product after the next scores
@@ -943,18 +940,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (n > 0 && !late && !product()) break;
             if (!more) break;
             if (fresh && !(wait(&sh.kv_full, k++ & 1) && operand())) break;
-            mma_scores<STEPS>(leader, scores_at + (twice ? 128 * (n & 1) : 0), key_at,
+            mma_scores<STEPS>(scores_at + (twice ? 128 * (n & 1) : 0), key_at,
                        first ? smem_addr(sh.q[qs]) : smem_addr(sh.dout[os]), s_shape, steps);
-            mma_commit(leader, first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
+            mma_commit(first ? &sh.s_ready[n & 1] : &sh.dp_ready[n & 1]);
             if (late) {
                 if (!product()) break;
-                mma_commit(leader, &sh.dv_done[i & 1]);
+                mma_commit(&sh.dv_done[i & 1]);
             } else if (Sh::kTwice && first && n > 0) {
-                mma_commit(leader, &sh.dv_done[i & 1]);
+                mma_commit(&sh.dv_done[i & 1]);
             }
             prev = e;
         }
-        mma_commit(leader, &sh.drained[warp - 1]);
+        mma_commit(&sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
     } else if (warp == 3 && aligned) {
         // ------------------------------------------------------------- statistics of the rows, dO

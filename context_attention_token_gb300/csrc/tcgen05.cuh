@@ -51,30 +51,39 @@ __device__ __forceinline__ uint32_t mma_shape(uint32_t n, bool b_outer)
 // ----------------------------------------------------------------- matrix instructions
 
 // The whole warp runs the issuing code, so that addresses and descriptors stay
-// in uniform registers; its lane 0 (`leader`) alone issues.
+// in uniform registers; one lane issues, elected (the same one every time) for a
+// run of instructions. With a predicate on each instruction instead an
+// instruction took 88 cycles to issue next to the softmax, against 74 so.
+
+__device__ __forceinline__ bool elect_lane()
+{
+    uint32_t r;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.b32 %0, 1, 0, p; }" : "=r"(r));
+    return r != 0;
+}
 
 // Descriptors come as two words: the lower one moves with the address, the
 // upper one is constant.
 
-__device__ __forceinline__ void mma_smem(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
+__device__ __forceinline__ void mma_smem(uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
                                          uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p, q; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};\n"
-        "setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p; }" ::"r"(d),
-        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
+        "{ .reg .pred p; .reg .b64 a, b; mov.b64 a, {%1, %3}; mov.b64 b, {%2, %3};\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u)
         : "memory");
 }
 
-__device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint32_t b, uint32_t upper,
                                          uint32_t shape, bool add)
 {
     asm volatile(
-        "{ .reg .pred p, q; .reg .b64 b; mov.b64 b, {%2, %3};\n"
-        "setp.ne.b32 p, %5, 0; setp.ne.b32 q, %6, 0;\n"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d),
-        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u), "r"(leader ? 1u : 0u)
+        "{ .reg .pred p; .reg .b64 b; mov.b64 b, {%2, %3};\n"
+        "setp.ne.b32 p, %5, 0;\n"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(upper), "r"(shape), "r"(add ? 1u : 0u)
         : "memory");
 }
 
@@ -90,36 +99,43 @@ __device__ __forceinline__ void mma_tmem(bool leader, uint32_t d, uint32_t a, ui
 // 8) inner steps of 16, four to a slab. STEPS, unless 0, is their number: code
 // for others in the same kernel costs it 2 to 6 %.
 template <int STEPS>
-__device__ __forceinline__ void mma_scores(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
+__device__ __forceinline__ void mma_scores(uint32_t d, uint32_t a, uint32_t b, uint32_t shape, int steps)
 {
     const uint32_t da = inner_lower(a), db = inner_lower(b);
+    if (elect_lane()) {
 #pragma unroll
-    for (int k = 0; k < (STEPS ? STEPS : 8); ++k) {
-        const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
-        if (STEPS || k < steps) mma_smem(leader, d, da + at, db + at, kInnerUpper, shape, k > 0);
+        for (int k = 0; k < (STEPS ? STEPS : 8); ++k) {
+            const uint32_t at = ((k >> 2) * kSlab + (k & 3) * 32) >> 4;
+            if (STEPS || k < steps) mma_smem(d, da + at, db + at, kInnerUpper, shape, k > 0);
+        }
     }
 }
 
-// d (+)= A B over STEPS inner steps of 16: A from tensor memory, 8 columns a
-// step, B read across.
-template <int STEPS>
-__device__ __forceinline__ void mma_weights(bool leader, uint32_t d, uint32_t a, uint32_t b, uint32_t shape, bool add)
+// d (+)= A B over RUNS x STEPS inner steps of 16: A from tensor memory, 8 columns
+// a step, B read across. A run begins a_gap columns and b_gap bytes behind the
+// one before.
+template <int RUNS, int STEPS>
+__device__ __forceinline__ void mma_weights(uint32_t d, uint32_t a, uint32_t a_gap, uint32_t b, uint32_t b_gap,
+                                            uint32_t shape, bool add)
 {
     const uint32_t db = outer_lower(b);
+    if (elect_lane()) {
 #pragma unroll
-    for (int k = 0; k < STEPS; ++k)
-        mma_tmem(leader, d, a + 8 * k, db + k * (2048 >> 4), kOuterUpper, shape, k > 0 || add);
+        for (int r = 0; r < RUNS; ++r)
+#pragma unroll
+            for (int k = 0; k < STEPS; ++k)
+                mma_tmem(d, a + r * a_gap + 8 * k, db + r * (b_gap >> 4) + k * (2048 >> 4), kOuterUpper, shape,
+                         r > 0 || k > 0 || add);
+    }
 }
 
 // An arrival on `bar` once every matrix instruction issued so far by this
 // thread has completed (and an arrival on behalf of its reads of shared memory).
-__device__ __forceinline__ void mma_commit(bool leader, uint64_t *bar)
+__device__ __forceinline__ void mma_commit(uint64_t *bar)
 {
-    asm volatile(
-        "{ .reg .pred q; setp.ne.b32 q, %1, 0;\n"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0]; }" ::"r"(smem_addr(bar)),
-        "r"(leader ? 1u : 0u)
-        : "memory");
+    if (elect_lane())
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                     : "memory");
 }
 
 __device__ __forceinline__ void tmem_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
