@@ -63,15 +63,17 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 //   loader   (1 warp)   the item's list of key tiles, its Q, K and V by TMA;
 //   issuers  (2 warps)  the matrix instructions of one query tile each: S = Q K^T
 //                       into tensor memory, then O += P V with P read from there;
-//   softmax  (2 x 4 warps, one warpgroup per query tile, one thread per row)
-//            scores to weights in place, statistics, the final division.
-// Tensor memory: S of both tiles (P over it), O of both tiles: 4 x 128 columns.
+//   softmax  (2 x 8 warps: two warpgroups per query tile, one thread per row and
+//            64 of the keys) scores to weights in place, statistics, the division.
+// Tensor memory: S of both tiles (the weights of 64 keys over the first half of
+// their scores), O of both tiles: 4 x 128 columns.
 //
 // Key tiles start anywhere: the next one starts at the first key at or behind
 // the last one's end that any row of the item sees. This covers windows,
 // sinks, jumps between a rank's chunks and short documents in one rule, with
 // at most one partly used tile per contiguous span.
 
+constexpr int kThreads = 640;  // 4 warps that load and issue, 4 warpgroups of softmax
 constexpr int kRing = 8;       // key-tile announcements in flight
 constexpr int kSteps = 8;      // barriers of the steps: more than a step can be ahead of whoever waits for it
 constexpr uint32_t kNeed = 1, kFull = 4, kFirst = 16, kLast = 32, kStop = 64;   // kNeed, kFull: << query tile
@@ -90,11 +92,15 @@ struct Shared {
     uint64_t info_full[kRing], info_empty[kRing];
     uint64_t rows_full[2], rows_empty[2];
     uint64_t step[2][kSteps];          // S of a tile is there and PV of the one before is done, tiles in turn
-    uint64_t p_half[2], p_ready[2], out_done[2], turn[2], drained[2];
+    uint64_t p_ready[2][2];            // the weights of the first 32 keys of both halves, of all
+    uint64_t out_done[2], turn[2], drained[2];
+    uint64_t pair[2][4];               // two warps with the same rows meet, to exchange a number per row
+    float given[2][2][2][kTile];       // ... by turns in two places
+
     int2 info[kRing];                  // first key, flags
     int4 rows[2][2][kTile];            // two visible spans of every row of an item
     uint32_t tmem;
-    uint32_t stop;
+    uint32_t stop, spoiled;
 };
 
 struct Maps {
@@ -123,7 +129,7 @@ __device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int
 }
 
 template <int DP, int STEPS>
-__global__ void __launch_bounds__(384, 1)
+__global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
                      int64_t row_tiles, bool pair)
 {
@@ -141,19 +147,20 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < Sh::kStages; ++i) mbar_init(&sh.kv_full[i], 1);
         for (int i = 0; i < kRing; ++i) {
             mbar_init(&sh.info_full[i], 1);
-            mbar_init(&sh.info_empty[i], 10);    // issuers, 8 softmax warps
+            mbar_init(&sh.info_empty[i], 18);    // issuers, 16 softmax warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sh.rows_full[i], 32);
-            mbar_init(&sh.rows_empty[i], 9);     // loader, 8 softmax warps
+            mbar_init(&sh.rows_empty[i], 17);    // loader, 16 softmax warps
             for (int j = 0; j < kSteps; ++j) mbar_init(&sh.step[i][j], 1);
-            mbar_init(&sh.p_half[i], kTile);
-            mbar_init(&sh.p_ready[i], kTile);
+            mbar_init(&sh.p_ready[i][0], 8);
+            mbar_init(&sh.p_ready[i][1], 8);
+            for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
             mbar_init(&sh.out_done[i], 1);
             mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
-        sh.stop = 0;
+        sh.stop = sh.spoiled = 0;
         mbar_init_fence();
     }
     tmem_fence_before();
@@ -164,9 +171,9 @@ __global__ void __launch_bounds__(384, 1)
     const int group = p.Hq / p.Hkv;
     const int steps = STEPS ? STEPS : (p.D + 15) / 16;
 
-    // 128 x 96 + 256 x 200 of the 384 x 168 registers of the launch
+    // 128 x 64 + 512 x 104 of the 640 x 96 registers of the launch
     if (warp < 4) {
-    fewer_registers<96>();
+    fewer_registers<64>();
     if (warp == 0) {
         // ------------------------------------------------------------- loader
         uint32_t n = 0, c = 0, k = 0;   // announcements, ring loads, items
@@ -292,16 +299,16 @@ __global__ void __launch_bounds__(384, 1)
                 return (!(e & kFirst) || wait(&sh.q_full, items_seen & 1)) &&
                        (!of_this || wait(&sh.kv_full[ks], c / Sh::kStages & 1));
             };
-            if (of_prev && !(wait(&sh.kv_full[vs], v / Sh::kStages & 1) && wait(&sh.p_half[x], ps & 1))) break;
+            if (of_prev && !(wait(&sh.kv_full[vs], v / Sh::kStages & 1) && wait(&sh.p_ready[x][0], ps & 1))) break;
             if (!(e & kFirst) && !operands()) break;
             if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
-                mma_weights<1, 4>(o_at, s_at, 0, kv_at + vs * Sh::kTileBytes, 0, o_shape, started);
-                if (!wait(&sh.p_ready[x], ps & 1)) break;
+                mma_weights<2, 2>(o_at, s_at, 64, kv_at + vs * Sh::kTileBytes, 8192, o_shape, started);
+                if (!wait(&sh.p_ready[x][1], ps & 1)) break;
                 ++ps;
                 tmem_fence_after();
-                mma_weights<1, 4>(o_at, s_at + 32, 0, kv_at + vs * Sh::kTileBytes + 8192, 0, o_shape, true);
+                mma_weights<2, 2>(o_at, s_at + 16, 64, kv_at + vs * Sh::kTileBytes + 4096, 8192, o_shape, true);
                 started = true;
             }
             if (prev & kLast) mma_commit(&sh.out_done[x]);
@@ -341,52 +348,54 @@ __global__ void __launch_bounds__(384, 1)
         }
     }
     } else {
-        more_registers<200>();
+        more_registers<104>();
         // ------------------------------------------------------------- softmax
-        const int x = warp / 4 - 1, t = threadIdx.x & (kTile - 1);
+        const int x = (warp - 4) / 8, half = (warp / 4 - 1) & 1, t = threadIdx.x & (kTile - 1);
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
-        const uint32_t s_at = tmem + lanes + 128 * x, o_at = tmem + lanes + 256 + 128 * x;
+        const uint32_t s_at = tmem + lanes + 128 * x + 64 * half, o_at = tmem + lanes + 256 + 128 * x;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t k = 0, j_tile = 0;   // items, tiles
+        uint32_t k = 0, j_tile = 0, met = 0;   // items, tiles, exchanges
         int4 r = make_int4(0, 0, 0, 0);
-        float ref = -INFINITY, l = 0.0f;   // the weights are 2^(score c - ref)
-        bool spoiled = false, done = false;
+        float ref = -INFINITY, l = 0.0f;       // the weights are 2^(score c - ref)
+        bool spoiled = false;
         int64_t it = blockIdx.x;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
+        };
+        // The number of the other warpgroup's thread for this row; false when the kernel stops.
+        auto exchange = [&](float mine, float &other) {
+            sh.given[met & 1][x][half][t] = mine;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pair[x][warp & 3]);
+            if (!wait(&sh.pair[x][warp & 3], met & 1)) return false;
+            other = sh.given[met & 1][x][half ^ 1][t];
+            ++met;
+            return true;
+        };
         for (uint32_t n = 0;; ++n) {
             const uint32_t slot = n % kRing;
-            if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.info_full[slot], n / kRing & 1, stop))) break;
+            if (!wait(&sh.info_full[slot], n / kRing & 1)) break;
             const int2 e = sh.info[slot];
             const uint32_t flags = static_cast<uint32_t>(e.y);
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.info_empty[slot]);
-            if (flags & kStop) {
-                done = true;
-                break;
-            }
+            if (flags & kStop) break;
             if (flags & kFirst) {
                 const int b = k & 1;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.rows_full[b], k / 2 & 1, stop))) break;
+                if (!wait(&sh.rows_full[b], k / 2 & 1)) break;
                 r = sh.rows[b][pair ? 0 : x][t];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
                 ++k;
-                ref = -INFINITY;
+                ref = r.y != 0 || r.w != 0 ? -INFINITY : 0.0f;   // a row that sees nothing needs none
                 l = 0.0f;
             }
             if (flags & (kNeed << x)) {
                 // the last tile's PV is done too
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1, stop))) break;
+                if (!wait(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1)) break;
                 tmem_fence_after();
-                // A row's reference is the largest score of the first tile that it sees (times c). The
-                // weights of later tiles may pass 1: only their sum is watched, and once it
-                // is past 2^40 reference, sum and O are scaled by a power of two. So no tile but the
-                // first waits for its maximum. Weights that pass 2^127 within one tile end as an
-                // infinity or NaN in the output and the row is computed again below.
-                const int a0 = r.x - e.x, a1 = r.y - e.x, b0 = r.z - e.x, b1 = r.w - e.x;
+                const int first = e.x + 64 * half, a0 = r.x - first, a1 = r.y - first, b0 = r.z - first, b1 = r.w - first;
                 const bool full = (flags & (kFull << x)) != 0;
-                auto load = [&](int i, uint32_t (&s)[32]) {
-                    tmem_load32(s_at + 32 * i, s);
-                };
                 auto hide = [&](int i, uint32_t (&s)[32]) {
                     if (full) return;
                     const uint32_t bits = span_bits(a0, a1, i) | span_bits(b0, b1, i);
@@ -394,43 +403,31 @@ __global__ void __launch_bounds__(384, 1)
                     for (int j = 0; j < 32; ++j)
                         if (!(bits >> j & 1)) s[j] = 0xFF800000u;
                 };
+                uint32_t s0[32], s1[32];
+                tmem_load32(s_at, s0);
+                tmem_load32(s_at + 32, s1);
+                tmem_wait_loads(s0);
+                tmem_wait_loads(s1);
+                hide(0, s0);
+                hide(1, s1);
+                // A row's reference is the largest score of the first tile that it sees (times c); the
+                // weights of later tiles may pass 1. So no tile but the first waits for a maximum. Weights
+                // or sums that leave binary32 (scores 88 above the reference, in natural units) end as an
+                // infinity or NaN in the output, and the row is computed again below.
                 if (__any_sync(0xFFFFFFFFu, ref == -INFINITY)) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll 1
-                    for (int i = 0; i < 4; i += 2) {
-                        uint32_t s[2][32];
-                        load(i, s[0]);
-                        load(i + 1, s[1]);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tmem_wait_loads(s[h]);
-                            hide(i + h, s[h]);
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) mx[j & 3] = fmaxf(mx[j & 3], __uint_as_float(s[h][j]));
-                        }
-                    }
-                    mx[0] = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-                    if (ref == -INFINITY) ref = mx[0] * c;
-                }
-                const bool big = l > 1.0995116e12f && l < INFINITY;
-                if (__any_sync(0xFFFFFFFFu, big)) {
-                    const int up = big ? static_cast<int>(__float_as_uint(l) >> 23) - 127 : 0;
-                    const float f = __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-                    l *= f;
-                    ref += static_cast<float>(up);
-                    for (int i = 0; i < steps; ++i) {
-                        uint32_t o[16];
-                        tmem_load16(o_at + 16 * i, o);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_store16(o_at + 16 * i, o);
-                    }
+                    for (int j = 0; j < 32; ++j)
+                        mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(s0[j]), __uint_as_float(s1[j])));
+                    float other;
+                    const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                    if (!exchange(mine, other)) break;
+                    if (ref == -INFINITY) ref = fmaxf(mine, other) * c;
                 }
                 const float mc = ref == -INFINITY ? 0.0f : ref;
                 const F2 c2 = pair_of(c, c), mc2 = pair_of(-mc, -mc);
                 F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
                 auto weigh = [&](int i, uint32_t (&s)[32]) {
-                    hide(i, s);
                     uint32_t w[16];
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
@@ -441,24 +438,13 @@ __global__ void __launch_bounds__(384, 1)
                         w[j] = pack_bf16x2(x0, x1);
                     }
                     tmem_store16(s_at + 16 * i, w);
-                };
-                // Weights go over scores that are in registers already. A loop and not 128 columns of
-                // straight code: the instruction caches are shared with the issuers.
-                uint32_t s0[32], s1[32];
-                load(0, s0);
-#pragma unroll 1
-                for (int i = 0; i < 4; i += 2) {
-                    tmem_wait_loads(s0);
-                    load(i + 1, s1);
-                    weigh(i, s0);
-                    tmem_wait_loads(s1);
-                    if (i == 0) load(2, s0);
-                    weigh(i + 1, s1);
                     tmem_wait_stores();
                     tmem_fence_before();
-                    // the product can begin with the first 64 keys
-                    mbar_arrive(i == 0 ? &sh.p_half[x] : &sh.p_ready[x]);
-                }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.p_ready[x][i]);   // the product can begin with half
+                };
+                weigh(0, s0);
+                weigh(1, s1);
                 const float2 total = both(add2(sum[0], sum[1]));
                 l += total.x + total.y;
             }
@@ -469,42 +455,45 @@ __global__ void __launch_bounds__(384, 1)
                 const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t;
                 const int64_t row = d.rank * p.Tp + in_rank;
                 const bool valid = in_rank < p.Tp, sees_any = r.y != 0 || r.w != 0;
+                float other;
+                if (!exchange(l, other)) break;
+                l = half == 0 ? l + other : other + l;
                 const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
                 float bad = 0.0f;
-                if (!__all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.out_done[x], k - 1 & 1, stop))) break;
+                if (!wait(&sh.out_done[x], (k - 1) & 1)) break;
                 tmem_fence_after();
                 uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
-                for (int i = 0; 32 * i < p.D; ++i) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
-                if (valid)
+                for (int i = half; 32 * i < p.D; i += 2) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
+                if (valid && half == 0)
                     p.lse[head * p.Tpad + row] =
                         sees_any && l != 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 spoiled |= valid && bad != 0.0f;   // NaN
                 it += gridDim.x;
             }
         }
-        // Rows with an infinity or NaN once more, one at a time, when no other role waits.
-        if (done && __any_sync(0xFFFFFFFFu, spoiled)) {
-            for (it = blockIdx.x; it < items; it += gridDim.x) {
-                const Item d = item_at(p, it, row_tiles, pair);
-                const int head = d.head + (pair ? x : 0);
-                const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t, row = d.rank * p.Tp + in_rank;
-                bool bad = false;
-                if (in_rank < p.Tp) {
-                    const uint16_t *out = row_of(p.out, row, p.Hq, head, p.D);
-                    for (int i = 0; i < p.D; ++i) bad |= (out[i] & 0x7F80) == 0x7F80;
-                }
-                unsigned todo = __ballot_sync(0xFFFFFFFFu, bad);
-                while (todo) {
-                    const int from = __ffs(todo) - 1;
-                    todo &= todo - 1;
-                    row_forward(p, __shfl_sync(0xFFFFFFFFu, row, from), head);
-                }
-            }
-        }
+        if (spoiled) sh.spoiled = 1;
     }
     __syncthreads();
     if (warp == 3) tmem_free(tmem);
-    if (threadIdx.x == 0 && sh.stop != 0) atomicAdd(&g_wait_timeouts, 1u);
+    if (sh.stop != 0) {
+        if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
+        return;
+    }
+    if (sh.spoiled == 0) return;
+    // Rows with an infinity or NaN once more, one warp to a row, when no role waits for another.
+    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+        const Item d = item_at(p, it, row_tiles, pair);
+        for (int i = warp; i < 2 * kTile; i += kThreads / 32) {
+            const int head = d.head + (pair ? i / kTile : 0);
+            const int64_t in_rank = d.row0 + (pair ? i % kTile : i), row = d.rank * p.Tp + in_rank;
+            if (in_rank >= p.Tp) continue;
+            const uint16_t *out = row_of(p.out, row, p.Hq, head, p.D);
+            bool bad = false;
+            if (4 * lane < p.D)
+                for (int j = 0; j < 4; ++j) bad |= (out[4 * lane + j] & 0x7F80) == 0x7F80;
+            if (__any_sync(0xFFFFFFFFu, bad)) row_forward(p, row, head);
+        }
+    }
 }
 
 // ----------------------------------------------------------------- launch
@@ -565,7 +554,7 @@ cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_
     const int64_t row_tiles = (p.Tp + rows - 1) / rows;
     const int64_t items = row_tiles * p.P * (pair ? p.Hq / 2 : p.Hq);
     const int64_t sms = sm_count(dev);
-    attention_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), 384, Shape<DP>::kSmem, stream>>>(
+    attention_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, Shape<DP>::kSmem, stream>>>(
         p, maps, items, row_tiles, pair);
     return cudaGetLastError();
 }
