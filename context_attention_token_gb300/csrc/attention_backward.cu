@@ -474,7 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (key == 0x7FFFFFFF) continue;   // no row sees a key
             // the last item's Q is free with its last S, its dO with its last dP; a V with its dP (by tile
             // parity: the next tile's may be ready too by the time this one's is asked for)
+            // A wait by parity takes a phase that has not begun for one that is over, so the S before is waited
+            // for first: with three tiles so far nothing else has waited for S(0), on whose barrier S(2)
+            // comes (dP(0), without Q, may be there long before it).
             const uint32_t m = n - 1;
+            if (n > 1 && !wait(&sh.s_ready[(m - 1) & 1], (m - 1) / 2 & 1)) break;
             if (n > 0 && !wait(&sh.s_ready[m & 1], m / 2 & 1)) break;
             if (lane == 0) load_tile(&maps.q, smem_addr(sh.q), kSlabs, t.head, row, &sh.q_full);
             ++nq;

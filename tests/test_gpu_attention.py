@@ -195,6 +195,35 @@ def test_large_batches(cpt, cuda_device, layout, P, lens, Hq, Hk, D, window, sin
             assert (diff <= bound).all(), (r, float((diff - bound).max()))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [129, 257, 385])
+def test_few_key_tiles_from_a_cold_cache(cpt, cuda_device, D, window):
+    """Every row tile sees two, three or four key tiles, and what is loaded arrives late and out of
+    order: no tile may make way for the next item's before it has been read."""
+    b = Batch(cpt, 0, 1, [8192], 8, 4, D, window, 0)
+    ws, first = b.workspace(), None
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")   # twice the L2 cache
+    results = [b.out, b.lse, b.dq] + b.dk + b.dv
+    for i in range(30):
+        for x in results:
+            x.t.view(torch.uint8).fill_(0xFF)
+        flush.fill_(i)
+        b.forward()
+        flush.fill_(i)
+        b.backward(ws.t)
+        torch.cuda.synchronize()
+        got = [x.t.clone() for x in results]
+        first = first or got
+        for x, y in zip(got, first):
+            assert torch.equal(x, y), i
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+    rows = np.arange(0, b.T, 67)
+    at = torch.from_numpy(rows).cuda()
+    out, lse, tol, dq, dq_tol = ref.sampled_rows(b, rows)
+    assert ((b.out.t[at].double() - out).abs() <= tol).all()
+    assert ((b.dq.t[at].double() - dq).abs() <= dq_tol).all()
+
+
 def test_many_short_documents(cpt, cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(0, 40, 90)]
