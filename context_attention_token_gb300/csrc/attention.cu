@@ -311,7 +311,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_weights<2, 2>(o_at, s_at + 16, 64, kv_at + vs * Sh::kTileBytes + 4096, 8192, o_shape, true);
                 started = true;
             }
-            if (prev & kLast) mma_commit(&sh.out_done[x]);
+            // (an item that needs nothing of this tile has no phase: nothing would keep it from passing two)
+            if ((prev & kLast) && started) mma_commit(&sh.out_done[x]);
             if ((e & kFirst) && !operands()) break;
             if (of_this)
                 mma_scores<STEPS>(s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
@@ -354,7 +355,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_at = tmem + lanes + 128 * x + 64 * half, o_at = tmem + lanes + 256 + 128 * x;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t k = 0, j_tile = 0, met = 0;   // items, tiles, exchanges
+        uint32_t k = 0, j_tile = 0, met = 0, done = 0;   // items, tiles, exchanges, items with a product
+        bool any = false;                                // whether this item has one
         int4 r = make_int4(0, 0, 0, 0);
         float ref = -INFINITY, l = 0.0f;       // the weights are 2^(score c - ref)
         bool spoiled = false;
@@ -389,8 +391,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++k;
                 ref = r.y != 0 || r.w != 0 ? -INFINITY : 0.0f;   // a row that sees nothing needs none
                 l = 0.0f;
+                any = false;
             }
             if (flags & (kNeed << x)) {
+                any = true;
                 // the last tile's PV is done too
                 if (!wait(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1)) break;
                 tmem_fence_after();
@@ -460,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = half == 0 ? l + other : other + l;
                 const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
                 float bad = 0.0f;
-                if (!wait(&sh.out_done[x], (k - 1) & 1)) break;
+                if (any && !wait(&sh.out_done[x], done++ & 1)) break;
                 tmem_fence_after();
                 uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
                 for (int i = half; 32 * i < p.D; i += 2) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
@@ -479,11 +483,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
     }
-    if (sh.spoiled == 0) return;
-    // Rows with an infinity or NaN once more, one warp to a row, when no role waits for another.
+    if (sh.spoiled == 0 || warp < 4) return;
+    // Rows with an infinity or NaN once more, one warp to a row, when no role waits for another (by the
+    // warps that kept their registers).
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const Item d = item_at(p, it, row_tiles, pair);
-        for (int i = warp; i < 2 * kTile; i += kThreads / 32) {
+        for (int i = warp - 4; i < 2 * kTile; i += kThreads / 32 - 4) {
             const int head = d.head + (pair ? i / kTile : 0);
             const int64_t in_rank = d.row0 + (pair ? i % kTile : i), row = d.rank * p.Tp + in_rank;
             if (in_rank >= p.Tp) continue;

@@ -224,6 +224,34 @@ def test_few_key_tiles_from_a_cold_cache(cpt, cuda_device, D, window):
     assert ((b.dq.t[at].double() - dq).abs() <= dq_tol).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_runs_of_rows_that_see_nothing(cpt, cuda_device, D):
+    """Documents of one token leave the later ranks hundreds of padding rows in a run: row tiles
+    that see nothing follow one another, between others that do."""
+    lens = [1500] + [1] * 900 + [700] + [1] * 900
+    b = Batch(cpt, 3, 4, lens, 12, 4, D, 300, 3)
+    ws, first = b.workspace(), None
+    results = [b.out, b.lse, b.dq] + b.dk + b.dv
+    for _ in range(10):
+        for x in results:
+            x.t.view(torch.uint8).fill_(0xFF)
+        b.forward()
+        b.backward(ws.t)
+        torch.cuda.synchronize()
+        got = [x.t.clone() for x in results]
+        first = first or got
+        for x, y in zip(got, first):
+            assert torch.equal(x, y)
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+    empty = torch.from_numpy(np.flatnonzero(b.l2r < 0)).cuda()
+    assert (b.out.t[empty] == 0).all() and (b.lse.t[:, empty] == -math.inf).all() and (b.dq.t[empty] == 0).all()
+    rows = np.flatnonzero(b.l2r >= 0)[::41]
+    at = torch.from_numpy(rows).cuda()
+    out, lse, tol, dq, dq_tol = ref.sampled_rows(b, rows)
+    assert ((b.out.t[at].double() - out).abs() <= tol).all()
+    assert ((b.dq.t[at].double() - dq).abs() <= dq_tol).all()
+
+
 def test_many_short_documents(cpt, cuda_device):
     rng = np.random.default_rng(5)
     lens = [int(x) for x in rng.integers(0, 40, 90)]
