@@ -93,7 +93,8 @@ struct Shared {
     uint64_t rows_full[2], rows_empty[2];
     uint64_t step[2][kSteps];          // S of a tile is there and PV of the one before is done, tiles in turn
     uint64_t p_ready[2][2];            // the weights of the first 32 keys of both halves, of all
-    uint64_t out_done[2], turn[2], drained[2];
+    uint64_t out_done[2][4];           // by item: while its rows are not taken, no third one after it is done
+    uint64_t turn[2], drained[2];
     uint64_t pair[2][4];               // two warps with the same rows meet, to exchange a number per row
     float given[2][2][2][kTile];       // ... by turns in two places
 
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.p_ready[i][0], 8);
             mbar_init(&sh.p_ready[i][1], 8);
             for (int j = 0; j < 4; ++j) mbar_init(&sh.pair[i][j], 2);
-            mbar_init(&sh.out_done[i], 1);
+            for (int j = 0; j < 4; ++j) mbar_init(&sh.out_done[i][j], 1);
             mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
@@ -311,8 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 mma_weights<2, 2>(o_at, s_at + 16, 64, kv_at + vs * Sh::kTileBytes + 4096, 8192, o_shape, true);
                 started = true;
             }
-            // (an item that needs nothing of this tile has no phase: nothing would keep it from passing two)
-            if ((prev & kLast) && started) mma_commit(&sh.out_done[x]);
+            if (prev & kLast) mma_commit(&sh.out_done[x][(items_seen - 1) & 3]);
             if ((e & kFirst) && !operands()) break;
             if (of_this)
                 mma_scores<STEPS>(s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
@@ -355,8 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;
         const uint32_t s_at = tmem + lanes + 128 * x + 64 * half, o_at = tmem + lanes + 256 + 128 * x;
         const float c = p.scale * 1.4426950408889634f;
-        uint32_t k = 0, j_tile = 0, met = 0, done = 0;   // items, tiles, exchanges, items with a product
-        bool any = false;                                // whether this item has one
+        uint32_t k = 0, j_tile = 0, met = 0;   // items, tiles, exchanges
         int4 r = make_int4(0, 0, 0, 0);
         float ref = -INFINITY, l = 0.0f;       // the weights are 2^(score c - ref)
         bool spoiled = false;
@@ -391,10 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++k;
                 ref = r.y != 0 || r.w != 0 ? -INFINITY : 0.0f;   // a row that sees nothing needs none
                 l = 0.0f;
-                any = false;
             }
             if (flags & (kNeed << x)) {
-                any = true;
                 // the last tile's PV is done too
                 if (!wait(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1)) break;
                 tmem_fence_after();
@@ -464,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = half == 0 ? l + other : other + l;
                 const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
                 float bad = 0.0f;
-                if (any && !wait(&sh.out_done[x], done++ & 1)) break;
+                if (!wait(&sh.out_done[x][(k - 1) & 3], (k - 1) / 4 & 1)) break;
                 tmem_fence_after();
                 uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, p.D));
                 for (int i = half; 32 * i < p.D; i += 2) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
