@@ -172,16 +172,63 @@ __device__ __forceinline__ int3 row_tiles_of(int4 range)
     return make_int3(first, from, first + (range.w > from ? (range.w - from + kTile - 1) / kTile : 0));
 }
 
+// ----------------------------------------------------------------- units of work
+//
+// A key tile takes as many row tiles as see it: few behind a window, all of a
+// document under the whole triangle or where its sinks lie. Those with more
+// than half of a CTA's share of all row tiles (kLeastPart at least) are cut into
+// parts, which leave binary32 sums in the workspace; whichever part ends last
+// adds them up in their order. So no CTA is left with a long tile alone, and
+// small batches use more CTAs than they have key tiles.
+
+constexpr int kLeastPart = 8;
+
+// Lists the units: {slot, part, parts, place of the first part's sums}. One warp,
+// of the last block to have put its tile in the list.
+__device__ void list_units(const Params &b, int slots, int sms)
+{
+    const int lane = threadIdx.x & 31, group = b.a.Hq / b.a.Hkv;
+    const int front = __ldcg(&b.counters[0]), n = front + __ldcg(&b.counters[1]);
+    const long long entries = __ldcg(reinterpret_cast<const long long *>(b.counters + 4)) * b.a.Hkv;
+    const long long share = (entries + 2 * sms - 1) / (2 * sms);
+    const int most = static_cast<int>(min(max(share, (long long)kLeastPart), 0x40000000ll));
+    int units = 0, places = 0;
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        int slot = 0, parts = 0;
+        if (i < n) {
+            slot = __ldcg(&b.list[i < front ? i : slots - 1 - (i - front)]);
+            parts = (row_tiles_of(__ldcg(&b.ranges[slot])).z * group + most - 1) / most;
+        }
+        const int need = parts > 1 ? parts : 0;
+        int u = parts, q = need;   // inclusive sums over the warp
+#pragma unroll
+        for (int s = 1; s < 32; s <<= 1) {
+            const int du = __shfl_up_sync(0xFFFFFFFFu, u, s), dq = __shfl_up_sync(0xFFFFFFFFu, q, s);
+            if (lane >= s) {
+                u += du;
+                q += dq;
+            }
+        }
+        for (int k = 0; k < parts; ++k)
+            if (in_bounds(units + u - parts + k < b.unit_places))
+                b.units[units + u - parts + k] = make_int4(slot, k, parts, places + q - need);
+        units += __shfl_sync(0xFFFFFFFFu, u, 31);
+        places += __shfl_sync(0xFFFFFFFFu, q, 31);
+    }
+    if (lane == 0) b.counters[6] = units;
+}
+
 // Key tiles of every rank: the local rows that may see one of the 128 keys, as
 // up to two ranges (the window's, and the rest of the documents whose
-// sinks lie in the tile); tiles that no row sees are written as zeros here.
+// sinks lie in the tile); tiles that no row sees keep an empty one.
 // The others go into a list, those with a range of sinks (the long ones) from
 // its front, the rest from its back. The order of the list sets which CTA takes
 // a tile and no result.
-__device__ __forceinline__ void prepare_tile(const Params &b, int block, int tiles)
+__device__ __forceinline__ void prepare_tile(const Params &b, int block, int tiles, int sms)
 {
     const AttentionParams &p = b.a;
-    __shared__ int any;
+    __shared__ bool last;
     const int rank = block % p.P, tile = block / p.P;
     const int32_t k0 = tile * kTile, k1 = static_cast<int32_t>(min((int64_t)k0 + kTile, p.T)) - 1;
     if (threadIdx.x == 0) {
@@ -210,34 +257,55 @@ __device__ __forceinline__ void prepare_tile(const Params &b, int block, int til
         }
         const int i = tile * p.P + rank;
         b.ranges[i] = make_int4((int)w0, (int)w1, (int)s0, (int)s1);
-        any = w1 > w0;
-        if (any) {
+        if (w1 > w0) {
             // row tiles of all heads of a group
             const long long entries = static_cast<long long>(row_tiles_of(b.ranges[i]).z) * (p.Hq / p.Hkv);
             atomicAdd(reinterpret_cast<unsigned long long *>(b.counters + 4), static_cast<unsigned long long>(entries));
             if (far) b.list[atomicAdd(&b.counters[0], 1)] = i;
             else b.list[tiles * p.P - 1 - atomicAdd(&b.counters[1], 1)] = i;
         }
+        __threadfence();
+        last = atomicAdd(&b.counters[7], 1) == tiles * p.P - 1;
+        __threadfence();
     }
     __syncthreads();
-    if (any) return;
-    const int64_t bytes = static_cast<int64_t>(p.Hkv) * p.D * 2, units = bytes / 16;
-    for (int t = 0; t <= k1 - k0; ++t) {
-        const int64_t pos = position_of_token(b, k0 + t);
-        if (pos < 0) continue;
-        for (int64_t i = threadIdx.x; i < 2 * units; i += 256) {
-            uint8_t *to = static_cast<uint8_t *>(i < units ? b.dk[rank] : b.dv[rank]) + pos * bytes;
-            st_once(to + 16 * (i < units ? i : i - units), make_uint4(0, 0, 0, 0));
+    if (last && threadIdx.x < 32) list_units(b, tiles * p.P, sms);
+}
+
+// Zeros in the gradients of key tiles that no row of the rank sees. One warp, which
+// has nothing else to do while the matrix unit is busy; as a part of the
+// preparation these writes were a sixteenth of the backward of 131072 tokens.
+__device__ void zero_unseen(const Params &b, int slots)
+{
+    const AttentionParams &p = b.a;
+    const int lane = threadIdx.x & 31;
+    const int64_t bytes = static_cast<int64_t>(p.Hkv) * p.D * 2;
+    for (int i = blockIdx.x; i < slots; i += gridDim.x) {
+        const int4 range = b.ranges[i];
+        if (range.y > range.x) continue;
+        const int32_t k0 = i / p.P * kTile;
+        uint8_t *dk = static_cast<uint8_t *>(b.dk[i % p.P]), *dv = static_cast<uint8_t *>(b.dv[i % p.P]);
+        for (int t0 = 0; t0 < kTile; t0 += 32) {
+            const int32_t mine = k0 + t0 + lane < p.T ? position_of_token(b, k0 + t0 + lane) : -1;
+            for (int t = 0; t < 32; ++t) {
+                const int64_t pos = __shfl_sync(0xFFFFFFFFu, mine, t);
+                if (pos < 0) continue;
+                for (int64_t at = pos * bytes + 16 * lane; at < (pos + 1) * bytes; at += 512) {
+                    st_once(dk + at, make_uint4(0, 0, 0, 0));
+                    st_once(dv + at, make_uint4(0, 0, 0, 0));
+                }
+            }
         }
     }
 }
 
-// One launch for both, the tiles first: they are few, and their zeros are the
-// larger part of the writes.
-__global__ void __launch_bounds__(8 * kPrepRows) prepare_kernel(const __grid_constant__ Params b, int tiles)
+// One launch for both, the tiles first, so that the units are listed while rows
+// are still read.
+__global__ void __launch_bounds__(8 * kPrepRows) prepare_kernel(const __grid_constant__ Params b, int tiles, int sms)
 {
+    next_grid_may_start();
     const int slots = tiles * b.a.P;
-    if (static_cast<int64_t>(blockIdx.x) < slots) prepare_tile(b, blockIdx.x, tiles);
+    if (static_cast<int64_t>(blockIdx.x) < slots) prepare_tile(b, blockIdx.x, tiles, sms);
     else prepare_rows(b, static_cast<int64_t>(blockIdx.x) - slots);
 }
 
@@ -306,52 +374,6 @@ __device__ __forceinline__ uint32_t visible_bits(int4 r, int key, int word)
     return span_bits(r.x - key, r.y - key, word) | span_bits(r.z - key, r.w - key, word);
 }
 
-// ----------------------------------------------------------------- units of work
-//
-// A key tile takes as many row tiles as see it: few behind a window, all of a
-// document under the whole triangle or where its sinks lie. Those with more
-// than half of a CTA's share of all row tiles (kLeastPart at least) are cut into
-// parts, which leave binary32 sums in the workspace; whichever part ends last
-// adds them up in their order. So no CTA is left with a long tile alone, and
-// small batches use more CTAs than they have key tiles.
-
-constexpr int kLeastPart = 8;
-
-// Lists the units: {slot, part, parts, place of the first part's sums}. One warp.
-__device__ void list_units(const Params &b, int slots, int sms)
-{
-    const int lane = threadIdx.x & 31, group = b.a.Hq / b.a.Hkv;
-    const int front = b.counters[0], n = front + b.counters[1];
-    const long long entries = *reinterpret_cast<const long long *>(b.counters + 4) * b.a.Hkv;
-    const long long share = (entries + 2 * sms - 1) / (2 * sms);
-    const int most = static_cast<int>(min(max(share, (long long)kLeastPart), 0x40000000ll));
-    int units = 0, places = 0;
-    for (int i0 = 0; i0 < n; i0 += 32) {
-        const int i = i0 + lane;
-        int slot = 0, parts = 0;
-        if (i < n) {
-            slot = b.list[i < front ? i : slots - 1 - (i - front)];
-            parts = (row_tiles_of(b.ranges[slot]).z * group + most - 1) / most;
-        }
-        const int need = parts > 1 ? parts : 0;
-        int u = parts, q = need;   // inclusive sums over the warp
-#pragma unroll
-        for (int s = 1; s < 32; s <<= 1) {
-            const int du = __shfl_up_sync(0xFFFFFFFFu, u, s), dq = __shfl_up_sync(0xFFFFFFFFu, q, s);
-            if (lane >= s) {
-                u += du;
-                q += dq;
-            }
-        }
-        for (int k = 0; k < parts; ++k)
-            if (in_bounds(units + u - parts + k < b.unit_places))
-                b.units[units + u - parts + k] = make_int4(slot, k, parts, places + q - need);
-        units += __shfl_sync(0xFFFFFFFFu, u, 31);
-        places += __shfl_sync(0xFFFFFFFFu, q, 31);
-    }
-    if (lane == 0) b.counters[6] = units;
-}
-
 // ----------------------------------------------------------------- dQ
 //
 // An item is 128 query rows of one head; Q and dO stay in shared memory, the
@@ -396,7 +418,7 @@ __device__ __forceinline__ DqItem dq_item(const AttentionParams &p, int64_t i, i
 template <int DP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1)
     dq_kernel(const __grid_constant__ Params b, const __grid_constant__ Maps maps, int64_t items, int64_t row_tiles,
-              int slots, int sms)
+              int slots)
 {
     typedef DqShared<DP> Sh;
     constexpr int kSlabs = Shape<DP>::kSlabs;
@@ -434,6 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    // from here on what the preparation has left is read; dK and dV need nothing of this kernel's
+    wait_for_last_grid();
+    next_grid_may_start();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = STEPS ? STEPS : (p.D + 15) / 16;
@@ -577,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         mma_commit(&sh.drained[warp - 1]);
         mbar_wait_bounded(&sh.drained[warp - 1], 0);
-    } else if (warp == 3 && blockIdx.x == 0) {
-        // ------------------------------------------------------------- the next kernel's units
-        list_units(b, slots, sms);
+    } else if (warp == 3) {
+        // ------------------------------------------------------------- tiles that no row sees
+        zero_unseen(b, slots);
     }
     } else {
         more_registers<104>();
@@ -792,6 +817,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
+    next_grid_may_start();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = STEPS ? STEPS : (p.D + 15) / 16, group = p.Hq / p.Hkv;
@@ -817,12 +843,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             return ok;
         };
         // Items are as long as the rows that see their keys are many, so each is taken when the CTA is
-        // free for it (dealt out in turn, the CTAs ended up to a fifth apart). The number of the next one
-        // is asked for an item ahead.
-        int64_t it = blockIdx.x;
+        // free for it (dealt out in turn, the CTAs ended up to a fifth apart; this one may have started
+        // late). The number of the next one is asked for an item ahead.
+        auto take = [&]() { return lane == 0 ? atomicAdd(&b.counters[2], 1) : 0; };
+        int64_t it = __shfl_sync(0xFFFFFFFFu, take(), 0);
         while (ok && it < items) {
-            int ahead = 0;
-            if (lane == 0) ahead = atomicAdd(&b.counters[2], 1);
+            const int ahead = take();
             const int index = static_cast<int>(it / p.Hkv), kvh = static_cast<int>(it - index * (int64_t)p.Hkv);
             const int4 unit = b.units[index];
             const int4 range = b.ranges[unit.x];
@@ -887,7 +913,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++nq;
                 ++n;
             }
-            it = static_cast<int64_t>(gridDim.x) + __shfl_sync(0xFFFFFFFFu, ahead, 0);
+            it = __shfl_sync(0xFFFFFFFFu, ahead, 0);
         }
         if (ok) announce(0, kStop, 0, 0);
         if (*stop != 0 && lane == 0) {   // copies in flight end before the CTA does
@@ -1137,6 +1163,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (warp == 3) tmem_free(tmem);
+    wait_for_last_grid();   // this grid ends after the one of dQ
     if (sh.stop != 0) {
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
@@ -1161,6 +1188,7 @@ __device__ bool spoiled_row(const uint16_t *row, int D)
 
 __global__ void __launch_bounds__(256) repair_kernel(const __grid_constant__ Params b)
 {
+    wait_for_last_grid();
     if (b.counters[3] == 0) return;
     const AttentionParams &p = b.a;
     const int64_t warp = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / 32, warps = gridDim.x * 8ll;
@@ -1181,6 +1209,29 @@ __global__ void __launch_bounds__(256) repair_kernel(const __grid_constant__ Par
 
 // ----------------------------------------------------------------- launch
 
+// A launch whose blocks may start before the last grid has ended, once all of
+// that grid's blocks have said next_grid_may_start (or ended); what needs the
+// last grid's results comes behind wait_for_last_grid. So dK and dV begin on the
+// SMs that dQ has left, or never took; no block waits for one that has not
+// started. (The backward of 2 x 1 heads of 64 and 200 tokens took 32 us with the
+// kernels one after the other.)
+template <class... Formal, class... Actual>
+cudaError_t launch_after(void (*kernel)(Formal...), int64_t blocks, int threads, size_t shared, cudaStream_t stream,
+                         Actual... args)
+{
+    cudaLaunchAttribute early;
+    early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    early.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(static_cast<unsigned>(blocks));
+    c.blockDim = dim3(threads);
+    c.dynamicSmemBytes = shared;
+    c.stream = stream;
+    c.attrs = &early;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, kernel, static_cast<Formal>(args)...);
+}
+
 template <int DP, int STEPS>
 cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStream_t stream)
 {
@@ -1197,12 +1248,12 @@ cudaError_t launch_tiled(const Params &b, const Maps &maps, int tiles, cudaStrea
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
     const int64_t sms = sm_count(dev), row_tiles = (p.Tp + kTile - 1) / kTile, items = row_tiles * p.P * p.Hq;
-    dq_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, sizeof(DqShared<DP>), stream>>>(
-        b, maps, items, row_tiles, tiles * p.P, static_cast<int>(sms));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_after(dq_kernel<DP, STEPS>, items < sms ? items : sms, kThreads, sizeof(DqShared<DP>), stream, b, maps,
+                     items, row_tiles, static_cast<int>(tiles * p.P));
+    if (e != cudaSuccess) return e;
     const int64_t most = static_cast<int64_t>(b.unit_places) * p.Hkv;
-    dkdv_kernel<DP, STEPS><<<static_cast<unsigned>(most < sms ? most : sms), kThreads, sizeof(DkvShared<DP>), stream>>>(b, maps);
-    return cudaGetLastError();
+    return launch_after(dkdv_kernel<DP, STEPS>, most < sms ? most : sms, kThreads, sizeof(DkvShared<DP>), stream, b,
+                        maps);
 }
 
 int64_t align256(int64_t x) { return (x + 255) & ~static_cast<int64_t>(255); }
@@ -1279,15 +1330,15 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * p.Hq;
     if (row_blocks + slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if ((e = cudaMemsetAsync(b.counters, 0, s.counter_bytes, stream)) != cudaSuccess) return e;
-    prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(b, tiles);
+    prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(
+        b, tiles, sm_count(-1));
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     // the common heads have kernels of their own (see mma_scores)
     if (p.D == 64) e = launch_tiled<64, 4>(b, maps, tiles, stream);
     else if (p.D == 128) e = launch_tiled<128, 8>(b, maps, tiles, stream);
     else e = p.D < 64 ? launch_tiled<64, 0>(b, maps, tiles, stream) : launch_tiled<128, 0>(b, maps, tiles, stream);
     if (e != cudaSuccess) return e;
-    repair_kernel<<<static_cast<unsigned>(4 * sm_count(-1)), 256, 0, stream>>>(b);
-    return cudaGetLastError();
+    return launch_after(repair_kernel, 4 * sm_count(-1), 256, 0, stream, b);
 }
 
 cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset)

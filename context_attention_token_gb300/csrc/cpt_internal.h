@@ -178,7 +178,8 @@ struct AttentionBackwardParams {
     int4 *units;                   // these as whole or in parts
     int32_t unit_places;
     int32_t *counters;             // 0, 1: tiles in both parts of the list; 2: units taken; 3: an output is to be
-                                   // computed again; 4, 5: row tiles of all, 64 bits; 6: units
+                                   // computed again; 4, 5: row tiles of all, 64 bits; 6: units;
+                                   // 7: tiles that the preparation has seen
     int32_t *arrived;              // parts of a tile that have come by, per place and warp
     float *sums;                   // of the parts
 };

@@ -251,6 +251,13 @@ __device__ __forceinline__ bool mbar_wait_or_stop(uint64_t *bar, uint32_t parity
     return mbar_wait_slow(bar, parity, stop);
 }
 
+// ----------------------------------------------------------------- grids in order
+
+// See launch_after. All memory operations of the last grid are visible behind the
+// wait; without that launch both end at once.
+__device__ __forceinline__ void wait_for_last_grid() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void next_grid_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ----------------------------------------------------------------- arithmetic
 
 __device__ __forceinline__ float exp2_fast(float x)
