@@ -85,24 +85,27 @@ bool dtype_ok(cpt_dtype d) { return d == CPT_F32 || d == CPT_BF16; }
 // A device buffer of the current device, aligned to `align` bytes.
 cpt_status check_ptr(const void *p, int device, size_t align, const char *what, int idx = -1)
 {
+    cudaPointerAttributes a;
+    cudaError_t e = cudaSuccess;
+    if (p != nullptr && reinterpret_cast<uintptr_t>(p) % align == 0) {
+        e = cudaPointerGetAttributes(&a, p);
+        if (e == cudaSuccess && (a.type == cudaMemoryTypeDevice || a.type == cudaMemoryTypeManaged) &&
+            a.device == device)
+            return CPT_OK;
+    }
     char name[64];
     if (idx >= 0) snprintf(name, sizeof name, "%s[%d]", what, idx);
     else snprintf(name, sizeof name, "%s", what);
     if (p == nullptr) return fail(CPT_ERR_INVALID_ARG, "%s is NULL", name);
     if (reinterpret_cast<uintptr_t>(p) % align != 0)
         return fail(CPT_ERR_ALIGNMENT, "%s is not %zu-byte aligned", name, align);
-    cudaPointerAttributes a;
-    cudaError_t e = cudaPointerGetAttributes(&a, p);
     if (e != cudaSuccess) {
         cudaGetLastError();
         return fail(CPT_ERR_DEVICE, "%s is not CUDA memory (%s)", name, cudaGetErrorString(e));
     }
     if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
         return fail(CPT_ERR_DEVICE, "%s is not device memory", name);
-    if (a.device != device)
-        return fail(CPT_ERR_DEVICE, "%s is on device %d but the current device is %d", name,
-                    a.device, device);
-    return CPT_OK;
+    return fail(CPT_ERR_DEVICE, "%s is on device %d but the current device is %d", name, a.device, device);
 }
 
 struct Range {
@@ -120,11 +123,24 @@ void add_range(std::vector<Range> &v, const void *p, size_t bytes, bool output, 
     v.push_back({lo, lo + bytes, output, what, idx});
 }
 
-// Outputs may overlap nothing; inputs may overlap each other.
-cpt_status check_overlaps(const std::vector<Range> &v)
+// Ranges of a call that has few, without an allocation that could fail.
+struct Ranges {
+    Range at[9 + 2 * CPT_MAX_CP_SIZE];
+    size_t n = 0;
+};
+
+void add_range(Ranges &v, const void *p, size_t bytes, bool output, const char *what, int idx = -1)
 {
-    for (size_t a = 0; a < v.size(); ++a)
-        for (size_t b = a + 1; b < v.size(); ++b) {
+    if (p == nullptr || bytes == 0) return;
+    const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
+    v.at[v.n++] = {lo, lo + bytes, output, what, idx};
+}
+
+// Outputs may overlap nothing; inputs may overlap each other.
+cpt_status check_overlaps(const Range *v, size_t n)
+{
+    for (size_t a = 0; a < n; ++a)
+        for (size_t b = a + 1; b < n; ++b) {
             if (!v[a].output && !v[b].output) continue;
             if (v[a].lo < v[b].hi && v[b].lo < v[a].hi)
                 return fail(CPT_ERR_ALIAS, "%s[%d] overlaps %s[%d]", v[a].what, v[a].idx, v[b].what,
@@ -132,6 +148,9 @@ cpt_status check_overlaps(const std::vector<Range> &v)
         }
     return CPT_OK;
 }
+
+cpt_status check_overlaps(const std::vector<Range> &v) { return check_overlaps(v.data(), v.size()); }
+cpt_status check_overlaps(const Ranges &v) { return check_overlaps(v.at, v.n); }
 
 // ----------------------------------------------------------------- driver
 
@@ -1270,7 +1289,7 @@ cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *plan, int3
         return fail(CPT_ERR_INVALID_ARG, "%lld heads are too many", (long long)heads_total);
     p.heads_total = (int32_t)heads_total;
     if (plan->T == 0) return CPT_OK;
-    std::vector<Range> r;
+    Ranges r;
     add_range(r, plan->ws, plan->ws_bytes, false, "workspace");
     if ((st = check_ptr(positions, dev, 4, "positions"))) return st;
     add_range(r, positions, sizeof(int32_t) * (size_t)rotary->axes * (size_t)plan->T, false, "positions");
@@ -1379,7 +1398,7 @@ cpt_status cpt_attention(const cpt_plan *plan, const void *q, const void *k, con
     if ((st = check_attention(plan, q_heads, kv_heads, head_dim, dtype, scale, window, sinks))) return st;
     if (plan->Tpad == 0) return CPT_OK;
     const size_t qb = (size_t)plan->Tpad * q_heads * head_dim * 2, kb = (size_t)plan->T * kv_heads * head_dim * 2;
-    std::vector<Range> r;
+    Ranges r;
     add_range(r, plan->ws, plan->ws_bytes, false, "workspace");
     if ((st = check_ptr(q, dev, 16, "q"))) return st;
     if ((st = check_ptr(k, dev, 16, "k"))) return st;
@@ -1439,7 +1458,7 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
         {q, qb, false, "q"},     {k, kb, false, "k"},       {v, kb, false, "v"},  {out, qb, false, "out"},
         {lse, lb, false, "lse"}, {dout, qb, false, "dout"}, {dq, qb, true, "dq"},
     };
-    std::vector<Range> r;
+    Ranges r;
     add_range(r, plan->ws, plan->ws_bytes, false, "plan workspace");
     add_range(r, workspace, need, true, "workspace");
     for (const auto &b : bufs) {
