@@ -392,17 +392,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                 l = 0.0f;
             }
             if (flags & (kNeed << x)) {
+                // Which of 32 rows see which of 32 keys. Three of four such blocks of a masked tile are seen or
+                // hidden as a whole; the warp finds that out before the scores are there, and masks no element
+                // of the former and computes none of the latter (65521 packed tokens of 16(4) heads of 80:
+                // 0.551 -> 0.517 ms).
+                uint32_t bits[2] = {0xFFFFFFFFu, 0xFFFFFFFFu};
+                bool mixed[2] = {false, false}, none[2] = {false, false};
+                if (!(flags & (kFull << x))) {
+                    const int first = e.x + 64 * half;
+                    const int a0 = r.x - first, a1 = r.y - first, b0 = r.z - first, b1 = r.w - first;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        bits[i] = span_bits(a0, a1, i) | span_bits(b0, b1, i);
+                        mixed[i] = !__all_sync(0xFFFFFFFFu, bits[i] == 0xFFFFFFFFu);
+                        none[i] = !__any_sync(0xFFFFFFFFu, bits[i] != 0);
+                    }
+                }
                 // the last tile's PV is done too
                 if (!wait(&sh.step[x][j_tile % kSteps], j_tile / kSteps & 1)) break;
                 tmem_fence_after();
-                const int first = e.x + 64 * half, a0 = r.x - first, a1 = r.y - first, b0 = r.z - first, b1 = r.w - first;
-                const bool full = (flags & (kFull << x)) != 0;
                 auto hide = [&](int i, uint32_t (&s)[32]) {
-                    if (full) return;
-                    const uint32_t bits = span_bits(a0, a1, i) | span_bits(b0, b1, i);
+                    if (!mixed[i]) return;
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        if (!(bits >> j & 1)) s[j] = 0xFF800000u;
+                        if (!(bits[i] >> j & 1)) s[j] = 0xFF800000u;
                 };
                 uint32_t s0[32], s1[32];
                 tmem_load32(s_at, s0);
@@ -430,6 +443,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 F2 sum[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
                 auto weigh = [&](int i, uint32_t (&s)[32]) {
                     uint32_t w[16];
+                    if (none[i]) {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) w[j] = 0;
+                        tmem_store16(s_at + 16 * i, w);
+                        tmem_wait_stores();
+                        tmem_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.p_ready[x][i]);
+                        return;
+                    }
 #pragma unroll
                     for (int j = 0; j < 16; ++j) {
                         const float2 a = both(fma2(pair_of(s[2 * j], s[2 * j + 1]), c2, mc2));
