@@ -809,14 +809,15 @@ def cpt_bounds_violations(reset: bool = False) -> int:
 
 
 def cpt_test_stall_bulk_waits(on: bool):
-    """Test switch: make every bulk-copy wait of later launches run out of its
-    budget (on) or behave normally (off)."""
+    """Test switch: make every bulk-copy wait of later launches of the row gather,
+    the gradient return and the slot reduce run out of its budget (on) or
+    behave normally (off)."""
     _check(_lib.cpt_test_stall_bulk_waits(1 if on else 0))
 
 
 def cpt_kernel_wait_timeouts(reset: bool = False) -> int:
-    """Bulk-copy waits in the library's kernels that ran out of their budget
-    on the current device (blocking; non-zero means an earlier output is not
+    """Waits in the library's kernels (on bulk copies, and between the warps of the
+    attention kernels) that ran out of their budget on the current device (blocking; non-zero means an earlier output is not
     valid)."""
     v = ctypes.c_uint32()
     _check(_lib.cpt_kernel_wait_timeouts(ctypes.byref(v), 1 if reset else 0))

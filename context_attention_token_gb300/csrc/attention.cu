@@ -72,6 +72,10 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 // the last one's end that any row of the item sees. This covers windows,
 // sinks, jumps between a rank's chunks and short documents in one rule, with
 // at most one partly used tile per contiguous span.
+//
+// Bound by the matrix unit with heads of 128: 32768 x 8 x 128, window 4096, takes
+// 0.346 ms (1.49 PFLOP/s, the unit busy for 75 % of it); by the softmax and
+// the masked tiles with documents: 65521 x 16(4) x 80, window 1000, 0.508 ms.
 
 constexpr int kThreads = 640;  // 4 warps that load and issue, 4 warpgroups of softmax
 constexpr int kRing = 8;       // key-tile announcements in flight

@@ -46,8 +46,8 @@
  *               size check). On failure nothing is enqueued, the call returns a
  *               non-zero cpt_status and cpt_last_error_string() explains it.
  *               Device-side failures go to device memory the host reads:
- *               an epoch wait timeout to a status word, a bulk-copy wait
- *               that ran out to a counter (cpt_kernel_wait_timeouts), and
+ *               an epoch wait timeout to a status word, a wait inside a
+ *               kernel that ran out to a counter (cpt_kernel_wait_timeouts), and
  *               in the bounds-checked build a failed index check to another
  *               (cpt_bounds_violations). Nothing aborts or traps.
  *   Threads     Calls are thread-safe; the error string is per thread.
@@ -590,10 +590,11 @@ CPT_API cpt_status cpt_epoch_status(const cpt_epoch *ep, int32_t owner, void *st
  * reset (the pages have no counterpart: it is this implementation's failure
  * report). The bulk-copy kernels of the row gather, the gradient return and
  * the slot reduce move data through shared memory, each copy completing on
- * an mbarrier. Every wait on one gives up after about a second or 2^24 polls.
- * A wait that gives up is counted here, its warp stops, and the outputs it
- * had not reached are left unwritten. A non-zero count means some output
- * of an earlier call is not valid.
+ * an mbarrier; the attention kernels hand tiles from warp to warp on such
+ * barriers too. Every wait on one gives up after about a second or 2^24 polls.
+ * A wait that gives up is counted here, its warp (in the attention kernels its
+ * CTA) stops, and the outputs it had not reached are left unwritten. A non-zero
+ * count means some output of an earlier call is not valid.
  *  count  host, receives the count.
  *  reset  non-zero: set the count back to zero after reading it.
  *  Blocking: reads device memory synchronously. Synchronise the streams of
@@ -622,7 +623,8 @@ CPT_API int32_t cpt_bounds_checked(void);
  *  CPT_ERR_INVALID_ARG (NULL count), CPT_ERR_DEVICE, CPT_ERR_CUDA. */
 CPT_API cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset);
 
-/* Test switch for the failure path of the bulk-copy kernels (the pages have no
+/* Test switch for the failure path of the bulk-copy kernels of the row gather,
+ * the gradient return and the slot reduce (the pages have no
  * counterpart). While on, every bulk-copy mbarrier of later launches on the
  * current device announces 16 bytes more than its copies deliver. Every
  * copy still completes, and nothing faults, but each wait runs out of its
@@ -748,8 +750,10 @@ CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *pl
  *  window     >= 0; a window of the longest document or more is the whole
  *             causal triangle.
  *  sinks      >= 0, first tokens of every document that stay visible.
- *  Scores, softmax statistics and sums are binary32. Infinities and NaN reach
- *  the rows that see them and no others.
+ *  Scores, softmax statistics and sums are binary32; the weights are rounded
+ *  to bf16 once, for their product with V. Infinities and NaN reach the rows that
+ *  see them and no others. Rows with one, and rows whose scores spread over more than
+ *  88, may be computed a second time, one key after the other, which is slow.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (dtype, head_dim, too many
  *  heads or tokens), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
  *  another buffer), CPT_ERR_CUDA. */
@@ -775,7 +779,8 @@ CPT_API size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int3
  *  workspace  device, 256-byte aligned, >= cpt_attention_backward_workspace_bytes;
  *             needed until the stream has passed the call. Calls that may run
  *             at the same time (two streams, two graphs) need one each.
- *  Sums are binary32 in a fixed order: a repeated call gives the same bits.
+ *  Sums are binary32 in a fixed order: a repeated call gives the same bits. The
+ *  weights and the gradients of the scores are rounded to bf16 once, for their products.
  *  Padding rows of q, out, lse and dout are not used. Other arguments and errors:
  *  as cpt_attention, and CPT_ERR_WORKSPACE. */
 CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,

@@ -1,6 +1,8 @@
 """Windowed attention with sinks and its gradient on the GPU, against dense
 64-bit forms. The bounds of every error are derived in attention_ref."""
 import math
+import os
+import re
 
 import numpy as np
 import pytest
@@ -514,3 +516,38 @@ def test_a_whole_step(cpt, cuda_device):
     for got, want in ((got_out, out.detach()), (gq, x[0].grad), (gk, x[1].grad), (gv, x[2].grad)):
         rel = (got.double().cpu() - want).norm() / want.norm()
         assert rel <= 6 * ref.U, float(rel)
+
+
+def test_readme_example_of_the_layer(cpt, cuda_device):
+    """The README's second example runs as written, after its first; rows checked against 64 bits."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        text = f.read()
+    env = {}
+    for kind in ("python", "py"):
+        exec(compile(re.search(rf"```{kind}\n(.*?)```", text, flags=re.S).group(1), "README.md", "exec"), env)
+    torch.cuda.synchronize()
+    S, H, KV, D = env["S"], env["H"], env["KV"], env["D"]
+    l2g = torch.empty(S, dtype=torch.int32, device="cuda")
+    cpt.cpt_index_map(env["plan"], l2g, None)
+    freq = torch.tensor([10000.0 ** (-i / 64) for i in range(64)], dtype=torch.float64, device="cuda")
+
+    def turn(x, at):
+        theta = at.double()[:, None, None] * freq
+        z = torch.complex(x[..., :64].double(), x[..., 64:].double()) * torch.polar(torch.ones_like(theta), theta)
+        return torch.cat([z.real, z.imag], -1)
+
+    for row in (0, 1, 40000, 131071, 262143):
+        i = int(l2g[row])
+        keys = torch.arange(S, device="cuda")
+        keys = keys[(keys <= i) & ((i - keys < env["window"]) | (keys < env["sinks"]))]
+        q = turn(env["q"][i:i + 1], torch.tensor([i], device="cuda"))[0]
+        k = turn(env["k"][keys], keys).repeat_interleave(H // KV, 1)
+        p = torch.softmax(torch.einsum("hd,jhd->hj", q, k) * env["scale"], 1)
+        want = torch.einsum("hj,jhd->hd", p, env["v"][keys].double().repeat_interleave(H // KV, 1))
+        # by norms: rotated q and k move the scores, and p and out are rounded, by at most U each
+        got = env["out"].view(S, H, D)[row].double()
+        assert (got - want).norm() <= 6 * ref.U * want.norm(), row
+    # the turn back undoes the turn: the same norms, up to the two roundings
+    a, b = env["dq"].double().norm(), env["dq_global"].double().norm()
+    assert abs(a - b) <= 2 * ref.U * a
+    assert env["dk_turned"].isfinite().all() and env["dv"].isfinite().all()
