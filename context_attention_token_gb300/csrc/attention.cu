@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float other;
                 if (!exchange(l, other)) break;
                 l = half == 0 ? l + other : other + l;
-                const float inv = sees_any && (l > 0.0f || l != l) ? 1.0f / l : 0.0f;
+                // a sum past binary32 may go with a finite product: it has to be seen in the output
+                const float inv = !sees_any || l == 0.0f ? 0.0f : l == INFINITY ? NAN : 1.0f / l;
                 float bad = 0.0f;
                 if (!wait(&sh.out_done[x][(k - 1) & 3], (k - 1) / 4 & 1)) break;
                 tmem_fence_after();

@@ -825,6 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tmem_fence_after();
     next_grid_may_start();
+    __threadfence();   // the preparation, which the grid before has waited for, and not the SM's old cache lines
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = STEPS ? STEPS : (p.D + 15) / 16, group = p.Hq / p.Hkv;

@@ -45,6 +45,11 @@ class Batch:
                                         self.dq.t, [x.t for x in self.dk], [x.t for x in self.dv], self.scale,
                                         self.window, self.sinks, workspace=workspace, stream=stream)
 
+    def l2r_order(self):
+        """Local rows in the order of the tokens they hold."""
+        rows = np.flatnonzero(self.l2r >= 0)
+        return torch.from_numpy(rows[np.argsort(self.l2r[rows])]).cuda()
+
     def workspace(self, extra=0):
         need = self.cpt.cpt_attention_backward_workspace_bytes(self.plan, self.Hq, self.Hk, self.D)
         return Guarded((need,), torch.uint8)
@@ -275,6 +280,31 @@ def test_scales(cpt, cuda_device, scale):
         b.check_backward()
     finally:
         ref.E32 = e
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("score", [80.0, 88.5, 95.0])
+def test_weights_that_leave_binary32(cpt, cuda_device, D, score):
+    """Two late keys score 80 to 95 above all others: a weight relative to the first tile's, or only
+    the sum of two, is past the largest binary32, with small V the product is not."""
+    b = Batch(cpt, 0, 1, [512], 2, 1, D, 512, 0, scale=1.0)
+    b.q.zero_()
+    b.q[..., 0] = 8.0
+    b.k.zero_()
+    b.k[300:302, :, 0] = score / 8   # a bf16 value
+    b.v.copy_((torch.rand(b.v.shape, device="cuda") / 8).to(torch.bfloat16))
+    b.forward()
+    out, v = b.out.t.reshape(b.Tpad, 2, D)[b.l2r_order()].double(), b.v[:, 0].double()
+    mean = torch.cumsum(v, 0) / torch.arange(1, 513, device="cuda")[:, None]
+    late = (v[300] + v[301]) / 2
+    # equal weights; from key 300 on the others weigh exp(-80) at most. Weights and out are rounded, and sums of
+    # n binary32 terms are off by n E at most
+    for want, rows in ((mean[:300], out[:300]), (v[300:301], out[300:301]), (late.expand(211, D), out[301:])):
+        assert ((rows - want[:, None]).abs() <= (2 * ref.U + 512 * 2.0 ** -24) * want[:, None].abs()).all()
+    lse = b.lse.t[:, b.l2r_order()].double()
+    assert ((lse[:, 301:] - score - math.log(2)).abs() <= 1e-4).all()   # 2^-22 of 95, and the exponentials
+    b.backward()
+    assert b.dq.t.isfinite().all() and all(x.t.isfinite().all() for x in b.dk + b.dv)
 
 
 def test_first_row_of_every_document_copies_v(cpt, cuda_device):
