@@ -459,6 +459,43 @@ def test_streams_and_graphs(cpt, cuda_device):
         check()
 
 
+def test_calls_in_a_row_and_on_two_streams(cpt, cuda_device):
+    """Inputs and outputs change hands between calls without a synchronisation, on one stream and
+    on two at once: the same bits as with the device waited for after every step."""
+    shapes = [(0, 4, [4096], 6, 6, 128, 1500, 4), (1, 4, [1000, 3, 2005, 988], 8, 2, 64, 300, 2)]
+    batches = [Batch(cpt, *s) for s in shapes]
+    spaces = [b.workspace() for b in batches]
+    inputs = [[(torch.randn_like(b.q), torch.randn_like(b.k), torch.randn_like(b.dout)) for _ in range(6)]
+              for b in batches]
+
+    def run(wait, streams):
+        got = [[], []]
+        for i in range(6):
+            for b, w, s, given, res in zip(batches, spaces, streams, inputs, got):
+                with torch.cuda.stream(s):
+                    for to, x in zip((b.q, b.k, b.dout), given[i]):
+                        to.copy_(x)
+                    for step in (b.forward, lambda: b.backward(w.t)):
+                        step()
+                        if wait:
+                            torch.cuda.synchronize()
+                    res.append([x.t.clone() for x in [b.out, b.lse, b.dq] + b.dk + b.dv])
+                    b.out.t.zero_()
+                    b.lse.t.zero_()
+        torch.cuda.synchronize()
+        return got
+
+    torch.cuda.synchronize()
+    one = torch.cuda.Stream()
+    want = run(True, [one, one])
+    for streams in ([one, one], [one, torch.cuda.Stream()], [torch.cuda.default_stream()] * 2):
+        for b, x, y in zip(batches, run(False, streams), want):
+            for i, (u, v) in enumerate(zip(x, y)):
+                for s, t in zip(u, v):
+                    assert torch.equal(s, t), i
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+
+
 def test_refusals_on_the_device(cpt, cuda_device):
     b = Batch(cpt, 0, 2, [64], 2, 1, 64, 16, 0)
     ok = dict(q=b.q, k=b.k, v=b.v, out=b.out.t, lse=b.lse.t, scale=1.0, window=4, sinks=0)
