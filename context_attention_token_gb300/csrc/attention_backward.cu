@@ -103,6 +103,12 @@ __device__ __noinline__ void key_dkdv(const Params &b, int32_t j, int rank, int 
 // ----------------------------------------------------------------- preparation
 
 constexpr int kPrepRows = 32;   // rows of one block: 8 lanes each
+constexpr int kPrepHeads = 4;   // and heads, whose loads are in flight together
+
+__device__ __forceinline__ float4 floats(uint32_t a, uint32_t b)
+{
+    return make_float4(bf16_lo(a), bf16_hi(a), bf16_lo(b), bf16_hi(b));
+}
 
 // Rows: delta and the base-2 log-sum-exp of every (head, row), the spans of
 // keys that a row sees, zeros in the writers' padding positions. A row that
@@ -110,32 +116,48 @@ constexpr int kPrepRows = 32;   // rows of one block: 8 lanes each
 __device__ __forceinline__ void prepare_rows(const Params &b, int64_t block)
 {
     const AttentionParams &p = b.a;
-    const int head = static_cast<int>(block % p.Hq);
-    const int64_t row = block / p.Hq * kPrepRows + threadIdx.x / 8;
+    const int groups = (p.Hq + kPrepHeads - 1) / kPrepHeads;
+    const int head0 = static_cast<int>(block % groups) * kPrepHeads;
+    const int64_t row = block / groups * kPrepRows + threadIdx.x / 8;
     const int lane = threadIdx.x & 7;
-    float d = 0.0f;
     const bool in = row < p.Tpad;
     const int32_t g = in ? token_of_row(p, row) : -1;
-    if (g >= 0) {
-        const uint16_t *o = row_of(p.out, row, p.Hq, head, p.D), *w = row_of(b.dout, row, p.Hq, head, p.D);
-        for (int at = 8 * lane; at < p.D; at += 64)
-            d += dot4(load4(o, at, p.D), load4(w, at, p.D)) + dot4(load4(o, at + 4, p.D), load4(w, at + 4, p.D));
-    }
+    float d[kPrepHeads];
 #pragma unroll
-    for (int s = 4; s > 0; s >>= 1) d += __shfl_xor_sync(0xFFFFFFFFu, d, s);
+    for (int h = 0; h < kPrepHeads; ++h) {
+        d[h] = 0.0f;
+        if (g < 0 || head0 + h >= p.Hq) continue;
+        const uint16_t *o = row_of(p.out, row, p.Hq, head0 + h, p.D), *w = row_of(b.dout, row, p.Hq, head0 + h, p.D);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {   // up to 128 elements
+            const int at = 8 * lane + 64 * i;
+            if (at < p.D) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(o + at), y = *reinterpret_cast<const uint4 *>(w + at);
+                d[h] += dot4(floats(x.x, x.y), floats(y.x, y.y)) + dot4(floats(x.z, x.w), floats(y.z, y.w));
+            }
+        }
+    }
+    float mine = 0.0f;   // lane h keeps head h's
+#pragma unroll
+    for (int h = 0; h < kPrepHeads; ++h) {
+#pragma unroll
+        for (int s = 4; s > 0; s >>= 1) d[h] += __shfl_xor_sync(0xFFFFFFFFu, d[h], s);
+        if (lane == h) mine = d[h];
+    }
     if (!in) return;
-    const int64_t at = head * p.Tpad + row;
-    if (lane == 0) {
+    if (lane < kPrepHeads && head0 + lane < p.Hq) {
+        const int64_t at = (head0 + lane) * p.Tpad + row;
         const float lse = g >= 0 ? p.lse[at] : -INFINITY;
-        b.delta[at] = d;
+        b.delta[at] = mine;
         b.lse2[at] = lse == -INFINITY ? INFINITY : lse * 1.4426950408889634f;
     }
     // the rows that see nothing: the matrix kernels pass them over
     if (g < 0 || (p.window == 0 && p.sinks == 0)) {
-        uint16_t *dq = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, p.D));
-        for (int i = 8 * lane; i < p.D; i += 64) *reinterpret_cast<uint4 *>(dq + i) = make_uint4(0, 0, 0, 0);
+        uint16_t *dq = const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head0, p.D));
+        const int elements = min(kPrepHeads, p.Hq - head0) * p.D;   // neighbouring heads
+        for (int i = 8 * lane; i < elements; i += 64) *reinterpret_cast<uint4 *>(dq + i) = make_uint4(0, 0, 0, 0);
     }
-    if (head != 0) return;
+    if (head0 != 0) return;
     if (lane == 0) {
         int4 r = make_int4(0, 0, 0, 0);
         if (g >= 0) r = spans_of(p, g);
@@ -1335,7 +1357,7 @@ cudaError_t launch_attention_backward(AttentionBackwardParams b, void *workspace
     if (e == cudaSuccess) e = make_slab_map(&maps.v, p.v, p.D, p.Hkv, p.T);
     if (e == cudaSuccess) e = make_slab_map(&maps.dout, b.dout, p.D, p.Hq, p.Tpad);
     if (e != cudaSuccess) return e;
-    const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * p.Hq;
+    const int64_t row_blocks = (p.Tpad + kPrepRows - 1) / kPrepRows * ((p.Hq + kPrepHeads - 1) / kPrepHeads);
     if (row_blocks + slots > 0x7FFFFFFF) return cudaErrorInvalidValue;
     if ((e = cudaMemsetAsync(b.counters, 0, s.counter_bytes, stream)) != cudaSuccess) return e;
     prepare_kernel<<<static_cast<unsigned>(row_blocks + slots), 8 * kPrepRows, 0, stream>>>(
