@@ -10,7 +10,7 @@
 // parts, is added up in their order) and a repeated call gives the same bits.
 // p and ds are rounded to bf16 once, for the matrix unit; it bounds both:
 // 8192 x 16 x 128, whole triangle, takes 0.26 ms for dQ (the unit busy for 79 % of
-// it) and 0.35 ms for dK and dV (71 %), 0.64 ms in all.
+// it) and 0.35 ms for dK and dV (71 %), 0.61 to 0.67 ms in all.
 #include "attention_common.cuh"
 #include "tcgen05.cuh"
 
@@ -846,7 +846,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    next_grid_may_start();
     __threadfence();   // the preparation, which the grid before has waited for, and not the SM's old cache lines
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
@@ -1193,7 +1192,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
     if (warp == 3) tmem_free(tmem);
-    wait_for_last_grid();   // this grid ends after the one of dQ
+    // The repair may start; earlier its blocks, and here idle blocks of this grid, would keep SMs that other
+    // streams could use. One block's wait makes this grid end after the one of dQ.
+    next_grid_may_start();
+    if (blockIdx.x == 0) wait_for_last_grid();
     if (sh.stop != 0) {
         if (threadIdx.x == 0) atomicAdd(&g_wait_timeouts, 1u);
         return;
