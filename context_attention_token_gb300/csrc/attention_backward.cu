@@ -303,7 +303,7 @@ __device__ __forceinline__ void prepare_tile(const Params &b, int block, int til
 
 // Zeros in the gradients of key tiles that no row of the rank sees. One warp, which
 // has nothing else to do while the matrix unit is busy; as a part of the
-// preparation these writes were a sixteenth of the backward of 131072 tokens.
+// preparation these writes took it from 0.07 to 0.2 ms (32768 x 20 x 128, 4 ranks).
 __device__ void zero_unseen(const Params &b, int slots)
 {
     const AttentionParams &p = b.a;
@@ -1245,8 +1245,8 @@ __global__ void __launch_bounds__(256) repair_kernel(const __grid_constant__ Par
 // that grid's blocks have said next_grid_may_start (or ended); what needs the
 // last grid's results comes behind wait_for_last_grid. So dK and dV begin on the
 // SMs that dQ has left, or never took; no block waits for one that has not
-// started. (The backward of 2 x 1 heads of 64 and 200 tokens took 32 us with the
-// kernels one after the other.)
+// started. (8192 x 16 x 128, whole triangle: 0.695 ms with the kernels one after
+// the other, 0.640 so.)
 template <class... Formal, class... Actual>
 cudaError_t launch_after(void (*kernel)(Formal...), int64_t blocks, int threads, size_t shared, cudaStream_t stream,
                          Actual... args)
