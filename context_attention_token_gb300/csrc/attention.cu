@@ -55,7 +55,8 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 // ----------------------------------------------------------------- tiled kernel
 //
 // A CTA works on items of two tiles of 128 query rows against one kv head: the
-// same rows of two heads that share it, or neighbouring rows of one head. It
+// same rows of two heads that share it, or neighbouring rows of one head (of one
+// tile alone where there are few). It
 // is persistent (one per SM) and split into roles that hand tiles on through
 // barriers, so that loads, matrix instructions and softmax of different tiles
 // run at the same time, across items too:
@@ -119,7 +120,8 @@ struct Item {
     bool pair;           // two heads, not two row tiles
 };
 
-__device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int64_t row_tiles, bool pair)
+__device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int64_t row_tiles, bool pair,
+                                        int item_rows)
 {
     // heads slowest, so that neighbouring CTAs share keys in L2; within a head the
     // later rows first, which see the most keys when the window is long
@@ -129,14 +131,14 @@ __device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int
     const int64_t h = i / per_head, j = i - h * per_head;
     t.head = static_cast<int>(pair ? 2 * h : h);
     t.rank = static_cast<int>(j % p.P);
-    t.row0 = (row_tiles - 1 - j / p.P) * (pair ? kTile : 2 * kTile);
+    t.row0 = (row_tiles - 1 - j / p.P) * item_rows;
     return t;
 }
 
 template <int DP, int STEPS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
-                     int64_t row_tiles, bool pair)
+                     int64_t row_tiles, bool pair, int item_rows)
 {
     typedef Shape<DP> Sh;
     extern __shared__ uint8_t raw[];
@@ -212,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return true;
         };
         for (int64_t it = blockIdx.x; ok && it < items; it += gridDim.x, ++k) {
-            const Item t = item_at(p, it, row_tiles, pair);
+            const Item t = item_at(p, it, row_tiles, pair, item_rows);
             const int b = k & 1;
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.rows_full[b], k / 2 & 1, stop));
             if (!ok) break;
@@ -340,12 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ------------------------------------------------------------- rows
         uint32_t k = 0;
         for (int64_t it = blockIdx.x; it < items; it += gridDim.x, ++k) {
-            const Item t = item_at(p, it, row_tiles, pair);
+            const Item t = item_at(p, it, row_tiles, pair, item_rows);
             const int b = k & 1;
             if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
             for (int i = lane; i < (pair ? kTile : 2 * kTile); i += 32) {
                 const int64_t row = t.row0 + i;
-                const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;
+                const int32_t g = row < p.Tp && i < item_rows ? token_of_row(p, t.rank * p.Tp + row) : -1;
                 const int4 r = g >= 0 ? spans_of(p, g) : make_int4(0, 0, 0, 0);
                 sh.rows[b][i / kTile][i % kTile] = r;
             }
@@ -478,11 +480,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (flags & (3 * kNeed)) ++j_tile;
             if (flags & kLast) {
-                const Item d = item_at(p, it, row_tiles, pair);
+                const Item d = item_at(p, it, row_tiles, pair, item_rows);
                 const int head = d.head + (pair ? x : 0);
                 const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t;
                 const int64_t row = d.rank * p.Tp + in_rank;
-                const bool valid = in_rank < p.Tp, sees_any = r.y != 0 || r.w != 0;
+                const bool valid = in_rank < p.Tp && (pair || x * kTile < item_rows), sees_any = r.y != 0 || r.w != 0;
                 float other;
                 if (!exchange(l, other)) break;
                 l = half == 0 ? l + other : other + l;
@@ -512,8 +514,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Rows with an infinity or NaN once more, one warp to a row, when no role waits for another (by the
     // warps that kept their registers).
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const Item d = item_at(p, it, row_tiles, pair);
-        for (int i = warp - 4; i < 2 * kTile; i += kThreads / 32 - 4) {
+        const Item d = item_at(p, it, row_tiles, pair, item_rows);
+        for (int i = warp - 4; i < (pair ? 2 * kTile : item_rows); i += kThreads / 32 - 4) {
             const int head = d.head + (pair ? i / kTile : 0);
             const int64_t in_rank = d.row0 + (pair ? i % kTile : i), row = d.rank * p.Tp + in_rank;
             if (in_rank >= p.Tp) continue;
@@ -578,14 +580,16 @@ cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
-    // two heads of one kv head see the same keys and share every K and V tile
-    const bool pair = p.Hq / p.Hkv % 2 == 0;
-    const int64_t rows = pair ? kTile : 2 * kTile;
+    // Two heads of one kv head see the same keys and share every K and V tile. Where the items of two tiles
+    // would be for half of the SMs at most, an item is one tile: 8192 x 2 x 128, whole triangle, 90 -> 84.5 us,
+    // 4096 x 4(2) x 64, window 1000, 26.0 -> 24.0 us.
+    const int64_t sms = sm_count(dev), one = (p.Tp + kTile - 1) / kTile * p.P * p.Hq;   // tiles of all heads
+    const bool single = one <= sms, pair = !single && p.Hq / p.Hkv % 2 == 0;
+    const int rows = single || pair ? kTile : 2 * kTile;
     const int64_t row_tiles = (p.Tp + rows - 1) / rows;
     const int64_t items = row_tiles * p.P * (pair ? p.Hq / 2 : p.Hq);
-    const int64_t sms = sm_count(dev);
     attention_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, Shape<DP>::kSmem, stream>>>(
-        p, maps, items, row_tiles, pair);
+        p, maps, items, row_tiles, pair, rows);
     return cudaGetLastError();
 }
 
