@@ -100,6 +100,8 @@ struct Shared {
     uint64_t p_ready[2][2];            // the weights of the first 32 keys of both halves, of all
     uint64_t out_done[2][4];           // by item: while its rows are not taken, no third one after it is done
     uint64_t turn[2], drained[2];
+    uint64_t join_full, join_empty;
+    float join_ref[kTile], join_l[kTile];   // of the second tile's roles, by row
     uint64_t pair[2][4];               // two warps with the same rows meet, to exchange a number per row
     float given[2][2][2][kTile];       // ... by turns in two places
 
@@ -135,11 +137,15 @@ __device__ __forceinline__ Item item_at(const AttentionParams &p, int64_t i, int
     return t;
 }
 
-template <int DP, int STEPS>
+// KEYS: an item is one tile of rows of one head, and the two tiles' roles take its
+// key tiles in turn, without turns of their issuers; their sums are joined at its end.
+template <int DP, int STEPS, bool KEYS>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_kernel(const __grid_constant__ AttentionParams p, const __grid_constant__ Maps maps, int64_t items,
-                     int64_t row_tiles, bool pair, int item_rows)
+                     int64_t row_tiles, bool pair)
 {
+    const bool same_rows = KEYS || pair;
+    const int item_rows = same_rows ? kTile : 2 * kTile;
     typedef Shape<DP> Sh;
     extern __shared__ uint8_t raw[];
     __shared__ Shared sh;
@@ -167,6 +173,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_init(&sh.turn[i], 1);
             mbar_init(&sh.drained[i], 1);
         }
+        mbar_init(&sh.join_full, 4);
+        mbar_init(&sh.join_empty, 8);
         sh.stop = sh.spoiled = 0;
         mbar_init_fence();
     }
@@ -222,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) r[x][i] = sh.rows[b][pair ? 0 : x][lane + 32 * i];
+                for (int i = 0; i < 4; ++i) r[x][i] = sh.rows[b][same_rows ? 0 : x][lane + 32 * i];
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
             ok = __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(&sh.q_empty, (k & 1) ^ 1, stop));
@@ -232,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int x = 0; x < 2; ++x)
                     for (int i = 0; i < Sh::kSlabs; ++i)
                         tma_slab(q_at + x * Sh::kTileBytes + i * kSlab, &maps.q, 64 * i, t.head + (pair ? x : 0),
-                                 static_cast<int>(t.rank * p.Tp + t.row0 + (pair ? 0 : x * kTile)), &sh.q_full);
+                                 static_cast<int>(t.rank * p.Tp + t.row0 + (same_rows ? 0 : x * kTile)), &sh.q_full);
             }
             auto next = [&](int x) {
                 int m = 0x7FFFFFFF;
@@ -242,7 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             const int kvh = t.head / group;
             int key = next(0);
-            uint32_t first = kFirst;
+            uint32_t first = kFirst, whose = 0;
             if (key == 0x7FFFFFFF) announce(0, kFirst | kLast);
             while (ok && key != 0x7FFFFFFF) {
                 const int end = key + kTile;   // below 2^31: a tile starts at a token
@@ -260,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint32_t flags = first;
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
-                    if (__any_sync(0xFFFFFFFFu, need[x])) flags |= kNeed << x;
+                    if (__any_sync(0xFFFFFFFFu, need[x]) && (!KEYS || whose == x)) flags |= kNeed << x;
                     if (__all_sync(0xFFFFFFFFu, full[x])) flags |= kFull << x;
                 }
                 const int nk = next(end);
@@ -268,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (!announce(key, flags) || !load(&maps.k, kvh, key) || !load(&maps.v, kvh, key)) break;
                 key = nk;
                 first = 0;
+                whose ^= 1;
             }
         }
         if (ok) announce(0, kStop);
@@ -308,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             };
             if (of_prev && !(wait(&sh.kv_full[vs], v / Sh::kStages & 1) && wait(&sh.p_ready[x][0], ps & 1))) break;
             if (!(e & kFirst) && !operands()) break;
-            if (!wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
+            if (!KEYS && !wait(&sh.turn[x], x == 0 ? (n & 1) ^ 1 : n & 1)) break;
             if (of_prev) {
                 tmem_fence_after();
                 mma_weights<2, 2>(o_at, s_at, 64, kv_at + vs * Sh::kTileBytes, 8192, o_shape, started);
@@ -322,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if ((e & kFirst) && !operands()) break;
             if (of_this)
                 mma_scores<STEPS>(s_at, q, kv_at + ks * Sh::kTileBytes, s_shape, steps);
-            if (leader) mbar_arrive(&sh.turn[1 - x]);
+            if (!KEYS && leader) mbar_arrive(&sh.turn[1 - x]);
             if (e & kStop) break;
             if (e & kFirst) started = false;
             if (e & (3 * kNeed)) {
@@ -345,9 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const Item t = item_at(p, it, row_tiles, pair, item_rows);
             const int b = k & 1;
             if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
-            for (int i = lane; i < (pair ? kTile : 2 * kTile); i += 32) {
+            for (int i = lane; i < item_rows; i += 32) {
                 const int64_t row = t.row0 + i;
-                const int32_t g = row < p.Tp && i < item_rows ? token_of_row(p, t.rank * p.Tp + row) : -1;
+                const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;
                 const int4 r = g >= 0 ? spans_of(p, g) : make_int4(0, 0, 0, 0);
                 sh.rows[b][i / kTile][i % kTile] = r;
             }
@@ -364,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t k = 0, j_tile = 0, met = 0;   // items, tiles, exchanges
         int4 r = make_int4(0, 0, 0, 0);
         float ref = -INFINITY, l = 0.0f;       // the weights are 2^(score c - ref)
-        bool spoiled = false;
+        bool spoiled = false, joined = false;  // joined: the second tile's roles have a part of this item
         int64_t it = blockIdx.x;
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xFFFFFFFFu, mbar_wait_or_stop(bar, parity, stop));
@@ -390,13 +399,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (flags & kFirst) {
                 const int b = k & 1;
                 if (!wait(&sh.rows_full[b], k / 2 & 1)) break;
-                r = sh.rows[b][pair ? 0 : x][t];
+                r = sh.rows[b][same_rows ? 0 : x][t];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.rows_empty[b]);
                 ++k;
                 ref = r.y != 0 || r.w != 0 ? -INFINITY : 0.0f;   // a row that sees nothing needs none
                 l = 0.0f;
+                joined = false;
             }
+            if (KEYS) joined |= (flags & (kNeed << 1)) != 0;
             if (flags & (kNeed << x)) {
                 // Which of 32 rows see which of 32 keys. Three of four such blocks of a masked tile are seen or
                 // hidden as a whole; the warp finds that out before the scores are there, and masks no element
@@ -482,12 +493,56 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (flags & kLast) {
                 const Item d = item_at(p, it, row_tiles, pair, item_rows);
                 const int head = d.head + (pair ? x : 0);
-                const int64_t in_rank = d.row0 + (pair ? 0 : x * kTile) + t;
+                const int64_t in_rank = d.row0 + (same_rows ? 0 : x * kTile) + t;
                 const int64_t row = d.rank * p.Tp + in_rank;
-                const bool valid = in_rank < p.Tp && (pair || x * kTile < item_rows), sees_any = r.y != 0 || r.w != 0;
+                const bool valid = in_rank < p.Tp, sees_any = r.y != 0 || r.w != 0;
                 float other;
                 if (!exchange(l, other)) break;
                 l = half == 0 ? l + other : other + l;
+                if (KEYS && x == 1) {   // the first tile's roles write the row
+                    if (half == 0) {
+                        sh.join_ref[t] = ref;
+                        sh.join_l[t] = l;
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&sh.join_full);
+                    }
+                    if (!wait(&sh.join_empty, (k - 1) & 1)) break;
+                    it += gridDim.x;
+                    continue;
+                }
+                if (KEYS) {
+                    if (!wait(&sh.join_full, (k - 1) & 1)) break;
+                    if (joined) {
+                        const float ref1 = sh.join_ref[t], l1 = sh.join_l[t], m = fmaxf(ref, ref1);
+                        const float a = ref == -INFINITY ? 0.0f : exp2_fast(ref - m);
+                        const float b = ref1 == -INFINITY ? 0.0f : exp2_fast(ref1 - m);
+                        l = l * a + l1 * b;
+                        ref = m;
+                        if (!wait(&sh.out_done[0][(k - 1) & 3], (k - 1) / 4 & 1) ||
+                            !wait(&sh.out_done[1][(k - 1) & 3], (k - 1) / 4 & 1))
+                            break;
+                        tmem_fence_after();
+                        for (int i = half; 32 * i < p.D; i += 2) {
+                            uint32_t o0[32], o1[32], w[16];
+                            tmem_load32(o_at + 32 * i, o0);
+                            tmem_load32(o_at + 128 + 32 * i, o1);
+                            tmem_wait_loads(o0);
+                            tmem_wait_loads(o1);
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                                for (int j = 16 * h; j < 16 * h + 16; ++j)
+                                    w[j - 16 * h] = __float_as_uint(
+                                        __fmaf_rn(__uint_as_float(o0[j]), a, __uint_as_float(o1[j]) * b));
+                                tmem_store16(o_at + 32 * i + 16 * h, w);
+                            }
+                            tmem_wait_stores();
+                        }
+                        tmem_fence_before();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&sh.join_empty);
+                }
                 // a sum past binary32 may go with a finite product: it has to be seen in the output
                 const float inv = !sees_any || l == 0.0f ? 0.0f : l == INFINITY ? NAN : 1.0f / l;
                 float bad = 0.0f;
@@ -515,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // warps that kept their registers).
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const Item d = item_at(p, it, row_tiles, pair, item_rows);
-        for (int i = warp - 4; i < (pair ? 2 * kTile : item_rows); i += kThreads / 32 - 4) {
+        for (int i = warp - 4; i < (KEYS ? kTile : 2 * kTile); i += kThreads / 32 - 4) {
             const int head = d.head + (pair ? i / kTile : 0);
             const int64_t in_rank = d.row0 + (pair ? i % kTile : i), row = d.rank * p.Tp + in_rank;
             if (in_rank >= p.Tp) continue;
@@ -576,20 +631,28 @@ cudaError_t launch_tiled(const AttentionParams &p, const Maps &maps, cudaStream_
     if (e != cudaSuccess) return e;
     static std::atomic<bool> attr_set[64];
     if (dev >= 64 || !attr_set[dev].load(std::memory_order_acquire)) {
-        e = cudaFuncSetAttribute(attention_kernel<DP, STEPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape<DP>::kSmem);
+        e = cudaFuncSetAttribute(attention_kernel<DP, STEPS, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Shape<DP>::kSmem);
+        if (e != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(attention_kernel<DP, STEPS, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 Shape<DP>::kSmem);
         if (e != cudaSuccess) return e;
         if (dev < 64) attr_set[dev].store(true, std::memory_order_release);
     }
     // Two heads of one kv head see the same keys and share every K and V tile. Where the items of two tiles
-    // would be for half of the SMs at most, an item is one tile: 8192 x 2 x 128, whole triangle, 90 -> 84.5 us,
-    // 4096 x 4(2) x 64, window 1000, 26.0 -> 24.0 us.
+    // would be for half of the SMs at most, an item is one tile and its keys are shared out:
+    // 8192 x 2 x 128, whole triangle, 90 -> 68 us, 9728 x 2 x 128, window 2048, 59 -> 45 us,
+    // 4096 x 4(2) x 64, window 1000, 26 -> 23 us.
     const int64_t sms = sm_count(dev), one = (p.Tp + kTile - 1) / kTile * p.P * p.Hq;   // tiles of all heads
     const bool single = one <= sms, pair = !single && p.Hq / p.Hkv % 2 == 0;
     const int rows = single || pair ? kTile : 2 * kTile;
     const int64_t row_tiles = (p.Tp + rows - 1) / rows;
     const int64_t items = row_tiles * p.P * (pair ? p.Hq / 2 : p.Hq);
-    attention_kernel<DP, STEPS><<<static_cast<unsigned>(items < sms ? items : sms), kThreads, Shape<DP>::kSmem, stream>>>(
-        p, maps, items, row_tiles, pair, rows);
+    const unsigned grid = static_cast<unsigned>(items < sms ? items : sms);
+    if (single)
+        attention_kernel<DP, STEPS, true><<<grid, kThreads, Shape<DP>::kSmem, stream>>>(p, maps, items, row_tiles, false);
+    else
+        attention_kernel<DP, STEPS, false><<<grid, kThreads, Shape<DP>::kSmem, stream>>>(p, maps, items, row_tiles, pair);
     return cudaGetLastError();
 }
 

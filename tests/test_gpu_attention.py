@@ -202,6 +202,30 @@ def test_large_batches(cpt, cuda_device, layout, P, lens, Hq, Hk, D, window, sin
             assert (diff <= bound).all(), (r, float((diff - bound).max()))
 
 
+@pytest.mark.parametrize("Hq,Hk", [(52, 26), (51, 17), (56, 7), (51, 51)])
+@pytest.mark.parametrize("D,window,sinks", [
+    (8, 100, 3), (48, 127, 0), (64, 1, 0), (64, 200, 130), (64, 1 << 31, 0), (72, 60, 2), (120, 129, 1), (128, 0, 4),
+    (128, 90, 7), (128, 1 << 31, 0)])
+def test_many_heads(cpt, cuda_device, Hq, Hk, D, window, sinks):
+    """More query tiles than SMs: items of two heads, or of two tiles of one."""
+    both(cpt, 3, 3, [1, 250, 130, 0, 7, 383], Hq, Hk, D, window, sinks)
+
+
+@pytest.mark.parametrize("D", [16, 64, 80, 128])
+@pytest.mark.parametrize("window,sinks", [(1 << 31, 0), (700, 5), (1, 300)])
+def test_few_heads(cpt, cuda_device, D, window, sinks):
+    """No more query tiles than SMs: an item's key tiles are shared out and joined, again and again the same."""
+    b = both(cpt, 0, 2, [2048, 12, 1500], 2, 1, D, window, sinks)
+    first = [x.t.clone() for x in (b.out, b.lse)]
+    flush = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for i in range(20):
+        flush.fill_(i)
+        b.forward()
+        torch.cuda.synchronize()
+        assert torch.equal(b.out.t, first[0]) and torch.equal(b.lse.t, first[1])
+    assert cpt.cpt_kernel_wait_timeouts() == 0
+
+
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("window", [129, 257, 385])
 def test_few_key_tiles_from_a_cold_cache(cpt, cuda_device, D, window):
@@ -347,14 +371,16 @@ def ref_raw(b, x):
     return x[torch.from_numpy(at).cuda()]
 
 
+# few tiles of query rows, or enough of them for the kernel of two tiles (two heads that share keys, or not)
+@pytest.mark.parametrize("heads", [(2, 1), (40, 20), (44, 44)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("D", [64, 128])
-def test_infinities_and_nan_stay_where_they_are_seen(cpt, cuda_device, bad, D):
+def test_infinities_and_nan_stay_where_they_are_seen(cpt, cuda_device, bad, D, heads):
     """K and V rows of one document, a key past its window and the last key
     of a document hold NaN or infinities: rows that do not see them are as if
     they were finite, in both directions."""
     lens, W, S = [100, 90, 260], 70, 2
-    b = Batch(cpt, 3, 2, lens, 2, 1, D, W, S)
+    b = Batch(cpt, 3, 2, lens, *heads, D, W, S)
     spoiled = [99, 120, 190 + 40]          # raw tokens: last of document 0, inside 1, past sinks of 2
     k, v = b.k, b.v
     b.k, b.v = k.clone(), v.clone()
@@ -381,9 +407,10 @@ def test_infinities_and_nan_stay_where_they_are_seen(cpt, cuda_device, bad, D):
             assert ((ref_raw(b, buf.t.double()) - want).abs() <= tol)[free].all()
 
 
+@pytest.mark.parametrize("heads", [(4, 2), (40, 20), (39, 39)])
 @pytest.mark.parametrize("D", [64, 128])
-def test_garbage_in_padding_rows_is_not_used(cpt, cuda_device, D):
-    b = Batch(cpt, 3, 4, [3, 1, 150, 47, 9], 4, 2, D, 60, 2)
+def test_garbage_in_padding_rows_is_not_used(cpt, cuda_device, D, heads):
+    b = Batch(cpt, 3, 4, [3, 1, 150, 47, 9], *heads, D, 60, 2)
     q, dout = b.q.clone(), b.dout.clone()
     q[b.pad] = 0
     dout[b.pad] = 0
