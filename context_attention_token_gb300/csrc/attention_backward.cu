@@ -210,7 +210,10 @@ __device__ __forceinline__ int3 row_tiles_of(int4 range)
 // adds them up in their order. So no CTA is left with a long tile alone, and
 // small batches use more CTAs than they have key tiles.
 
-constexpr int kLeastPart = 8;
+// Parts of at least 2, 4, 8, 16, 32 row tiles: 4799 tokens in documents x 4(2) x 128, window 18, take 80, 73, 76,
+// 87, 100 us, 4096 x 4(2) x 128, window 1000, 91, 90, 96, 92, 111 us, 65536 x 2(1) x 64, window 64, 179, 178,
+// 179, 161, 192 us; larger batches do not cut that fine.
+constexpr int kLeastPart = 4;
 
 // Lists the units: {slot, part, parts, place of the first part's sums}. One warp,
 // of the last block to have put its tile in the list.
