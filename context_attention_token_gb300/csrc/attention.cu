@@ -513,10 +513,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (KEYS) {
                     if (!wait(&sh.join_full, (k - 1) & 1)) break;
                     if (joined) {
+                        // Each side's sums are relative to the first tile that it saw, and may be as large as
+                        // binary32 goes: the factor of the lower reference comes in two parts, so that it does
+                        // not vanish while its product with them still counts (below 2^-222 that is under
+                        // 2^-95, of a sum of at least 1).
                         const float ref1 = sh.join_ref[t], l1 = sh.join_l[t], m = fmaxf(ref, ref1);
-                        const float a = ref == -INFINITY ? 0.0f : exp2_fast(ref - m);
-                        const float b = ref1 == -INFINITY ? 0.0f : exp2_fast(ref1 - m);
-                        l = l * a + l1 * b;
+                        const float a = ref == -INFINITY ? 0.0f : exp2_fast(fmaxf(ref - m, -96.0f));
+                        const float b = ref1 == -INFINITY ? 0.0f : exp2_fast(fmaxf(ref1 - m, -96.0f));
+                        const float a2 = exp2_fast(fminf(ref - m + 96.0f, 0.0f));
+                        const float b2 = exp2_fast(fminf(ref1 - m + 96.0f, 0.0f));
+                        l = l * a2 * a + l1 * b2 * b;
                         ref = m;
                         if (!wait(&sh.out_done[0][(k - 1) & 3], (k - 1) / 4 & 1) ||
                             !wait(&sh.out_done[1][(k - 1) & 3], (k - 1) / 4 & 1))
@@ -532,8 +538,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int h = 0; h < 2; ++h) {
 #pragma unroll
                                 for (int j = 16 * h; j < 16 * h + 16; ++j)
-                                    w[j - 16 * h] = __float_as_uint(
-                                        __fmaf_rn(__uint_as_float(o0[j]), a, __uint_as_float(o1[j]) * b));
+                                    w[j - 16 * h] = __float_as_uint(__fmaf_rn(
+                                        __uint_as_float(o0[j]) * a2, a, __uint_as_float(o1[j]) * b2 * b));
                                 tmem_store16(o_at + 32 * i + 16 * h, w);
                             }
                             tmem_wait_stores();
