@@ -83,6 +83,12 @@ constexpr int kRing = 8;       // key-tile announcements in flight
 constexpr int kSteps = 8;      // barriers of the steps: more than a step can be ahead of whoever waits for it
 constexpr uint32_t kNeed = 1, kFull = 4, kFirst = 16, kLast = 32, kStop = 64;   // kNeed, kFull: << query tile
 
+// The largest weight of a row's first tile is 1 but for the rounding of its reference. That is off by half a step,
+// which is tens of units from scores of 2^30 on: the weights may then all be infinite or all vanish, and
+// past binary32 (scores of 2^127) the reference is infinite. A row whose sum is below this bound is computed
+// again as one with an infinity is. (A row whose scores are all -inf is too: it has out = 0 and lse = -inf.)
+constexpr float kLeastSum = 5.4210108624275222e-20f;   // 2^-64
+
 template <int DP>
 struct Shape {
     static constexpr int kSlabs = DP / 64;
@@ -443,8 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 hide(1, s1);
                 // A row's reference is the largest score of the first tile that it sees (times c); the
                 // weights of later tiles may pass 1. So no tile but the first waits for a maximum. Weights
-                // or sums that leave binary32 (scores 88 above the reference, in natural units) end as an
-                // infinity or NaN in the output, and the row is computed again below.
+                // or sums that leave binary32 (scores 88 above the reference, in natural units; see also
+                // kLeastSum) end as an infinity or NaN in the output, and the row is computed again below.
                 if (__any_sync(0xFFFFFFFFu, ref == -INFINITY)) {
                     float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -499,6 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 float other;
                 if (!exchange(l, other)) break;
                 l = half == 0 ? l + other : other + l;
+                if (ref != -INFINITY && l < kLeastSum) l = INFINITY;   // not to be lost in the join
                 if (KEYS && x == 1) {   // the first tile's roles write the row
                     if (half == 0) {
                         sh.join_ref[t] = ref;
@@ -549,8 +556,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&sh.join_empty);
                 }
-                // a sum past binary32 may go with a finite product: it has to be seen in the output
-                const float inv = !sees_any || l == 0.0f ? 0.0f : l == INFINITY ? NAN : 1.0f / l;
+                // a sum past binary32 may go with a finite product, and one too small (see kLeastSum) with a
+                // product of zero: both have to be seen in the output
+                const float inv = !sees_any ? 0.0f : l == INFINITY || l < kLeastSum ? NAN : 1.0f / l;
                 float bad = 0.0f;
                 if (!wait(&sh.out_done[x][(k - 1) & 3], (k - 1) / 4 & 1)) break;
                 tmem_fence_after();
@@ -558,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = half; 32 * i < p.D; i += 2) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
                 if (valid && half == 0)
                     p.lse[head * p.Tpad + row] =
-                        sees_any && l != 0.0f ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        sees_any ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 spoiled |= valid && bad != 0.0f;   // NaN
                 it += gridDim.x;
             }

@@ -753,7 +753,7 @@ CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *pl
  *  Scores, softmax statistics and sums are binary32; the weights are rounded
  *  to bf16 once, for their product with V. Infinities and NaN reach the rows that
  *  see them and no others. Rows with one, and rows whose scores spread over more than
- *  88, may be computed a second time, one key after the other, which is slow.
+ *  88 or pass 2^30, may be computed a second time, one key after the other, which is slow.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (dtype, head_dim, too many
  *  heads or tokens), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
  *  another buffer), CPT_ERR_CUDA. */
@@ -781,6 +781,8 @@ CPT_API size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int3
  *             at the same time (two streams, two graphs) need one each.
  *  Sums are binary32 in a fixed order: a repeated call gives the same bits. The
  *  weights and the gradients of the scores are rounded to bf16 once, for their products.
+ *  The weights are exp(scale q . k - lse) in binary32, as lse is: their relative error grows to
+ *  2^-22 |lse|, so with |lse| from some 10^4 on the gradient has fewer bits than its type.
  *  Padding rows of q, out, lse and dout are not used. Other arguments and errors:
  *  as cpt_attention, and CPT_ERR_WORKSPACE. */
 CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,
