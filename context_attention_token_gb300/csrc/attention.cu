@@ -7,6 +7,7 @@
 #include "tcgen05.cuh"
 
 #include <atomic>
+#include <cfloat>
 
 namespace cpt {
 
@@ -19,11 +20,15 @@ __device__ unsigned int g_wait_timeouts;
 // elements each, keys come one at a time, the softmax keeps its running
 // maximum and sum. The tiled kernel multiplies hidden keys by a weight of zero,
 // which an infinity or NaN in their V turns into NaN: it gives such rows to
-// this function, which never touches a hidden key.
+// this function, which never touches a hidden key. A NaN stays one whatever comes
+// behind it, so the keys end once every element that the tiled kernel left without a
+// finite value is NaN (the others are right, as lse is where it is finite).
 __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, int head)
 {
     const int lane = threadIdx.x & 31, at = lane * 4, D = p.D;
     const int kvh = head / (p.Hq / p.Hkv);
+    uint16_t *out = const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, D));
+    float *lse = p.lse + head * p.Tpad + row;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float m = -INFINITY, l = 0.0f;
     const int32_t g = token_of_row(p, row);
@@ -43,13 +48,20 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
             o = make_float4(o.x * c, o.y * c, o.z * c, o.w * c);
             axpy4(o, w, v);
             m = mn;
+            if ((j & 15) == 0) {
+                if (l != l) break;
+                const float4 tiled = load4(out, at, D);
+                if (isfinite(*lse) && !__any_sync(0xFFFFFFFFu, any_open(tiled, o))) {
+                    store4(out, at, D, finite_or_nan(tiled));
+                    return;
+                }
+            }
             ++j;
         }
     }
     const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-    store4(const_cast<uint16_t *>(row_of(p.out, row, p.Hq, head, D)), at, D,
-           make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (lane == 0) p.lse[head * p.Tpad + row] = m + logf(l);
+    store4(out, at, D, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (lane == 0) *lse = m + logf(l);
 }
 
 // ----------------------------------------------------------------- tiled kernel
@@ -529,7 +541,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const float b = ref1 == -INFINITY ? 0.0f : exp2_fast(fmaxf(ref1 - m, -96.0f));
                         const float a2 = exp2_fast(fminf(ref - m + 96.0f, 0.0f));
                         const float b2 = exp2_fast(fminf(ref1 - m + 96.0f, 0.0f));
-                        l = l * a2 * a + l1 * b2 * b;
+                        const bool again = l == INFINITY || l1 == INFINITY;   // and no NaN of a score
+                        l = again ? INFINITY : l * a2 * a + l1 * b2 * b;
                         ref = m;
                         if (!wait(&sh.out_done[0][(k - 1) & 3], (k - 1) / 4 & 1) ||
                             !wait(&sh.out_done[1][(k - 1) & 3], (k - 1) / 4 & 1))
@@ -557,8 +570,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (lane == 0) mbar_arrive(&sh.join_empty);
                 }
                 // a sum past binary32 may go with a finite product, and one too small (see kLeastSum) with a
-                // product of zero: both have to be seen in the output
-                const float inv = !sees_any ? 0.0f : l == INFINITY || l < kLeastSum ? NAN : 1.0f / l;
+                // product of zero: both have to be seen in the output, and lse tells them from a NaN
+                if (l < kLeastSum) l = INFINITY;
+                const float inv = !sees_any ? 0.0f : l == INFINITY ? NAN : 1.0f / l;
                 float bad = 0.0f;
                 if (!wait(&sh.out_done[x][(k - 1) & 3], (k - 1) / 4 & 1)) break;
                 tmem_fence_after();
@@ -566,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = half; 32 * i < p.D; i += 2) store_block(o_at, i, p.D, inv, sees_any, out, valid, bad);
                 if (valid && half == 0)
                     p.lse[head * p.Tpad + row] =
-                        sees_any ? (ref + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        sees_any ? (fmaxf(ref, -FLT_MAX) + log2f(l)) * 0.69314718055994531f : -INFINITY;
                 spoiled |= valid && bad != 0.0f;   // NaN
                 it += gridDim.x;
             }
@@ -581,13 +595,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (sh.spoiled == 0 || warp < 4) return;
     // Rows with an infinity or NaN once more, one warp to a row, when no role waits for another (by the
-    // warps that kept their registers).
+    // warps that kept their registers). A NaN in lse is that of a score that the row sees (as long as the
+    // scale in base 2 is finite): such a row is NaN throughout, and stays as it is.
+    const bool nan_is_final = p.scale * 1.4426950408889634f < INFINITY;
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const Item d = item_at(p, it, row_tiles, pair, item_rows);
         for (int i = warp - 4; i < (KEYS ? kTile : 2 * kTile); i += kThreads / 32 - 4) {
             const int head = d.head + (pair ? i / kTile : 0);
             const int64_t in_rank = d.row0 + (pair ? i % kTile : i), row = d.rank * p.Tp + in_rank;
             if (in_rank >= p.Tp) continue;
+            const float lse = p.lse[head * p.Tpad + row];
+            if (nan_is_final && lse != lse) continue;
             const uint16_t *out = row_of(p.out, row, p.Hq, head, p.D);
             bool bad = false;
             if (4 * lane < p.D)

@@ -36,7 +36,9 @@ __device__ __forceinline__ void pair_grad(const Params &b, float4 q, float4 dout
 }
 
 // A warp's computation of one row from the definition, for rows that an
-// infinity or NaN behind a hidden key or row spoiled in the tiled kernels.
+// infinity or NaN behind a hidden key or row spoiled in the tiled kernels. A NaN in
+// lse or delta is in every ds of the row, and what is NaN stays so: the keys
+// end with the last element that can be anything else.
 __device__ __noinline__ void row_dq(const Params &b, int64_t row, int head)
 {
     const AttentionParams &p = b.a;
@@ -50,6 +52,10 @@ __device__ __noinline__ void row_dq(const Params &b, int64_t row, int head)
         const float lse = p.lse[head * p.Tpad + row], delta = b.delta[head * p.Tpad + row];
         const RowKeys r = keys_of_token(p, g);
         int32_t j = r.kb;
+        if (lse != lse || delta != delta) {
+            dq = make_float4(NAN, NAN, NAN, NAN);
+            j = g + 1;
+        }
         while (true) {
             if (j == r.kb + r.ns) j = r.lo;
             if (j > g) break;
@@ -57,34 +63,77 @@ __device__ __noinline__ void row_dq(const Params &b, int64_t row, int head)
             float w, ds;
             pair_grad(b, q, dout, k, load4(row_of(p.v, j, p.Hkv, kvh, D), at, D), lse, delta, w, ds);
             axpy4(dq, ds, k);
+            if (!__any_sync(0xFFFFFFFFu, at < D && !all_nan(dq))) break;
             ++j;
         }
     }
     store4(const_cast<uint16_t *>(row_of(b.dq, row, p.Hq, head, D)), at, D, dq);
 }
 
-// dK and dV of one raw key for one writer, over the rows of that rank.
+// Rows of a rank whose (padded) global position is below x, a position of
+// document doc or its end.
+__device__ __forceinline__ int64_t rows_below(const Params &b, int rank, int32_t doc, int64_t x)
+{
+    const AttentionParams &p = b.a;
+    if (b.packed) return min(max(x - rank * p.Tp, (int64_t)0), p.Tp);
+    const int64_t begin = b.cup[doc], m = (b.cup[doc + 1] - begin) / (2 * p.P), u = x - begin;
+    return begin / p.P + min(max(u - rank * m, (int64_t)0), m) +
+           min(max(u - (2 * p.P - 1 - rank) * m, (int64_t)0), m);
+}
+
+// dK and dV of one raw key for one writer, over the rows of that rank. What a NaN in the
+// rows' lse or delta settles is looked up first, 128 rows at a time: lse makes
+// both NaN throughout, delta dK, and dV where that row's dO holds one (which is in its delta).
+// Other elements are right where the tiled kernel's are finite.
 __device__ __noinline__ void key_dkdv(const Params &b, int32_t j, int rank, int kvh)
 {
     const AttentionParams &p = b.a;
     const int lane = threadIdx.x & 31, at = lane * 4, D = p.D, G = p.Hq / p.Hkv;
     const int32_t doc = find_doc(p.cu, p.n_docs, j);
     const int32_t kb = p.cu[doc], end = p.cu[doc + 1], pos0 = b.cup[doc] - kb;
-    const float4 k = load4(row_of(p.k, j, p.Hkv, kvh, D), at, D);
-    const float4 v = load4(row_of(p.v, j, p.Hkv, kvh, D), at, D);
-    float4 dk = make_float4(0.0f, 0.0f, 0.0f, 0.0f), dv = dk;
+    const int64_t pos = pos0 + j;
+    uint16_t *const dk_row = const_cast<uint16_t *>(row_of(b.dk[rank], pos, p.Hkv, kvh, D));
+    uint16_t *const dv_row = const_cast<uint16_t *>(row_of(b.dv[rank], pos, p.Hkv, kvh, D));
+    // the rows that see the key
     const int32_t last = j - kb < p.sinks ? end : static_cast<int32_t>(min((int64_t)end, (int64_t)j + p.window));
-    for (int32_t i0 = j; i0 < last; i0 += 32) {
-        int64_t row = -1;
-        if (i0 + lane < last) {
-            row = b.g2l[pos0 + i0 + lane];
-            if (row / p.Tp != rank || !in_bounds(row < p.Tpad)) row = -1;
+    const int64_t row0 = rank * p.Tp + rows_below(b, rank, doc, pos);
+    const int64_t row1 = rank * p.Tp + rows_below(b, rank, doc, (int64_t)pos0 + last);
+    float4 dk = load4(dk_row, at, D), dv = load4(dv_row, at, D), seen = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float4 all = make_float4(NAN, NAN, NAN, NAN), tiled = dv;
+    const bool dk_finite = !__any_sync(0xFFFFFFFFu, !all_finite(dk));
+    bool lse_nan = false, delta_nan = false, settled = false;
+    for (int64_t i0 = row0; !settled && i0 < row1; i0 += 128)
+        for (int h = kvh * G; !settled && h < (kvh + 1) * G; ++h) {
+            float lse[4], delta[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = i0 + 32 * u + lane, x = h * p.Tpad + i;
+                lse[u] = i < row1 ? p.lse[x] : 0.0f;
+                delta[u] = i < row1 ? b.delta[x] : 0.0f;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) lse_nan |= lse[u] != lse[u];
+            lse_nan = __any_sync(0xFFFFFFFFu, lse_nan);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                unsigned todo = __ballot_sync(0xFFFFFFFFu, delta[u] != delta[u]);
+                delta_nan |= todo != 0;
+                while (!lse_nan && todo && __any_sync(0xFFFFFFFFu, any_open(tiled, seen))) {
+                    const int64_t i = i0 + 32 * u + __ffs(todo) - 1;
+                    todo &= todo - 1;
+                    note_nan(seen, load4(row_of(b.dout, i, p.Hq, h, D), at, D));
+                }
+            }
+            settled = lse_nan || ((delta_nan || dk_finite) && !__any_sync(0xFFFFFFFFu, any_open(tiled, seen)));
         }
-        unsigned todo = __ballot_sync(0xFFFFFFFFu, row >= 0);
-        while (todo) {
-            const int from = __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int64_t i = __shfl_sync(0xFFFFFFFFu, row, from);
+    if (settled) {
+        if (lse_nan || delta_nan) dk = all;
+        dv = lse_nan ? all : finite_or_nan(tiled);
+    } else {
+        const float4 k = load4(row_of(p.k, j, p.Hkv, kvh, D), at, D);
+        const float4 v = load4(row_of(p.v, j, p.Hkv, kvh, D), at, D);
+        dk = dv = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int64_t i = row0; i < row1; ++i) {
             for (int h = kvh * G; h < (kvh + 1) * G; ++h) {
                 const float4 q = load4(row_of(p.q, i, p.Hq, h, D), at, D);
                 const float4 dout = load4(row_of(b.dout, i, p.Hq, h, D), at, D);
@@ -93,11 +142,11 @@ __device__ __noinline__ void key_dkdv(const Params &b, int32_t j, int rank, int 
                 axpy4(dk, ds, q);
                 axpy4(dv, w, dout);
             }
+            if (!__any_sync(0xFFFFFFFFu, at < D && !(all_nan(dk) && all_nan(dv)))) break;
         }
     }
-    const int64_t pos = pos0 + j;
-    store4(const_cast<uint16_t *>(row_of(b.dk[rank], pos, p.Hkv, kvh, D)), at, D, dk);
-    store4(const_cast<uint16_t *>(row_of(b.dv[rank], pos, p.Hkv, kvh, D)), at, D, dv);
+    store4(dk_row, at, D, dk);
+    store4(dv_row, at, D, dv);
 }
 
 // ----------------------------------------------------------------- preparation
@@ -172,17 +221,6 @@ __device__ __forceinline__ void prepare_rows(const Params &b, int64_t block)
                     *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(b.dv[r]) + pos * bytes + i) = make_uint4(0, 0, 0, 0);
                 }
     }
-}
-
-// Rows of a rank whose (padded) global position is below x, a position of
-// document doc or its end.
-__device__ __forceinline__ int64_t rows_below(const Params &b, int rank, int32_t doc, int64_t x)
-{
-    const AttentionParams &p = b.a;
-    if (b.packed) return min(max(x - rank * p.Tp, (int64_t)0), p.Tp);
-    const int64_t begin = b.cup[doc], m = (b.cup[doc + 1] - begin) / (2 * p.P), u = x - begin;
-    return begin / p.P + min(max(u - rank * m, (int64_t)0), m) +
-           min(max(u - (2 * p.P - 1 - rank) * m, (int64_t)0), m);
 }
 
 // Padded global position of a raw token.

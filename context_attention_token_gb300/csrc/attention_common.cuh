@@ -114,6 +114,35 @@ __device__ __forceinline__ void axpy4(float4 &y, float a, float4 x)
     y.w = __fmaf_rn(a, x.w, y.w);
 }
 
+// For rows that are computed again: whether one of four elements that the tiled kernels left
+// without a finite value is not NaN in `now` (it stays NaN once it is).
+__device__ __forceinline__ bool any_open(float4 tiled, float4 now)
+{
+    return (!isfinite(tiled.x) && now.x == now.x) || (!isfinite(tiled.y) && now.y == now.y) ||
+           (!isfinite(tiled.z) && now.z == now.z) || (!isfinite(tiled.w) && now.w == now.w);
+}
+
+__device__ __forceinline__ float4 finite_or_nan(float4 x)
+{
+    return make_float4(isfinite(x.x) ? x.x : NAN, isfinite(x.y) ? x.y : NAN, isfinite(x.z) ? x.z : NAN,
+                       isfinite(x.w) ? x.w : NAN);
+}
+
+__device__ __forceinline__ void note_nan(float4 &to, float4 x)
+{
+    if (x.x != x.x) to.x = NAN;
+    if (x.y != x.y) to.y = NAN;
+    if (x.z != x.z) to.z = NAN;
+    if (x.w != x.w) to.w = NAN;
+}
+
+__device__ __forceinline__ bool all_nan(float4 x) { return x.x != x.x && x.y != x.y && x.z != x.z && x.w != x.w; }
+
+__device__ __forceinline__ bool all_finite(float4 x)
+{
+    return isfinite(x.x) && isfinite(x.y) && isfinite(x.z) && isfinite(x.w);
+}
+
 __device__ __forceinline__ const uint16_t *row_of(const void *base, int64_t row, int heads, int head, int D)
 {
     return static_cast<const uint16_t *>(base) + (row * heads + head) * D;

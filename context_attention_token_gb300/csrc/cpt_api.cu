@@ -1480,7 +1480,6 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
                    head_dim, scale, window, sinks);
     p.dout = dout;
     p.dq = dq;
-    p.g2l = plan->g2l;
     p.l2g = plan->l2g;
     p.r2l = plan->r2l;
     p.cup = plan->cup;

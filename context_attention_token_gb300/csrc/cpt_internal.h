@@ -165,8 +165,7 @@ struct AttentionBackwardParams {
     const void *dout;              // bf16 [Tpad][Hq][D]
     void *dq;                      // bf16 [Tpad][Hq][D]
     void *dk[kMaxCp], *dv[kMaxCp]; // writer r's bf16 [Tpad][Hkv][D]
-    const int32_t *g2l;            // local row of every (padded) global position
-    const int32_t *l2g;            // and back
+    const int32_t *l2g;            // (padded) global position of every local row
     const int32_t *r2l;            // local row of every raw token (nullptr: position = token)
     const int32_t *cup;            // padded document boundaries [n_docs + 1]
     bool packed;                   // packed-contiguous ownership

@@ -752,8 +752,12 @@ CPT_API cpt_status cpt_rotary_apply(const cpt_rotary *rotary, const cpt_plan *pl
  *  sinks      >= 0, first tokens of every document that stay visible.
  *  Scores, softmax statistics and sums are binary32; the weights are rounded
  *  to bf16 once, for their product with V. Infinities and NaN reach the rows that
- *  see them and no others. Rows with one, and rows whose scores spread over more than
- *  88 or pass 2^30, may be computed a second time, one key after the other, which is slow.
+ *  see them and no others. Some rows are computed a second time, one key after the other,
+ *  which is slow (1000 times as slow as the rest where it meets every row of a long document):
+ *  those with a score more than 88 above the largest of the first 128 keys or so that they see,
+ *  or past 2^30; those that see an infinity; those that see a NaN in V, up to its key; and those that have an
+ *  infinity or NaN in a hidden V of the same 128 keys as one that they see.
+ *  What a NaN in a score makes NaN costs nothing more.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (dtype, head_dim, too many
  *  heads or tokens), CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS (out or lse overlaps
  *  another buffer), CPT_ERR_CUDA. */
@@ -783,6 +787,8 @@ CPT_API size_t cpt_attention_backward_workspace_bytes(const cpt_plan *plan, int3
  *  weights and the gradients of the scores are rounded to bf16 once, for their products.
  *  The weights are exp(scale q . k - lse) in binary32, as lse is: their relative error grows to
  *  2^-22 |lse|, so with |lse| from some 10^4 on the gradient has fewer bits than its type.
+ *  Infinities and hidden NaN are dealt with as in cpt_attention, keys like rows: where a NaN in lse or in
+ *  dout . out settles a gradient, that costs little, else it is computed again, slowly.
  *  Padding rows of q, out, lse and dout are not used. Other arguments and errors:
  *  as cpt_attention, and CPT_ERR_WORKSPACE. */
 CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const void *k, const void *v,
