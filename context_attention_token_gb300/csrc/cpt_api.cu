@@ -1191,9 +1191,11 @@ namespace {
 
 // f / 2 pi modulo one turn, as a 64-bit fixed-point fraction. The quotient is
 // carried in two doubles, so the fraction is right to its last bits and a
-// position of 2^31 still has its angle to 2^-30 of a turn.
+// position of 2^31 still has its angle to 2^-31 of a turn. A negative f is the
+// fraction of -f negated (1 - x would round away the last bits of a small x).
 uint64_t turn_of(double f)
 {
+    if (f < 0.0) return 0 - turn_of(-f);
     const double two_pi_hi = 6.283185307179586477, two_pi_lo = 2.449293598294706414e-16;
     const double t0 = f / two_pi_hi;
     const double rest = std::fma(-t0, two_pi_hi, f) - t0 * two_pi_lo;
