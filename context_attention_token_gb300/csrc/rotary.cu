@@ -12,10 +12,11 @@
 // rate. Only the angle modulo one turn matters, so f_i / 2 pi is held as a
 // 64-bit fixed-point fraction F_i of a turn and pos * F_i is taken modulo
 // 2^64: an exact reduction in one integer multiplication, whatever the
-// position. Its top two bits (rounded) are the quadrant; the rest is an angle
-// in [-pi/4, pi/4] with an error below 2.5e-8 rad, for which the Taylor
-// polynomials of sine (to x^9, remainder 1.8e-9) and cosine (to x^10,
-// remainder 1.2e-10) hold in binary32.
+// position. Its top two bits (rounded) are the quadrant; the next 30 are an angle
+// in [-pi/4, pi/4]. In binary32 that is off by up to 8e-8 rad (2^-26 of a turn: the
+// conversion 2.4e-8, the constant 2.2e-8, the product 3e-8), which stands beside
+// the 6e-8 of a result's own rounding. The Taylor polynomials of sine (to x^9,
+// remainder 1.8e-9) and cosine (to x^10, remainder 1.2e-10) hold in binary32.
 //
 // Traffic. Every row is read once and written once, so HBM bounds it. All
 // heads of a token share its angles: a CTA computes the sines and cosines of

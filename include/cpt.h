@@ -711,7 +711,8 @@ CPT_API cpt_status cpt_rotary_destroy(cpt_rotary *rotary);
  *  heads      host int32[n_tensors]; heads[t] * head_dim elements must be a
  *             multiple of 16 bytes.
  *  positions  device int32[n_axes][T], of the raw tokens in global order; any
- *             values. Angles are exact to 2^-31 of a turn at any position.
+ *             values. Angles are reduced exactly, to 2^-31 of a turn at any position,
+ *             and held to 2^-26 of a turn (8e-8 rad) in binary32.
  *  inverse    non-zero: turn back. This is the gradient of the forward call
  *             with the two orders exchanged.
  *  Arithmetic is binary32, with one rounding to bf16 at the end. Padding rows of
