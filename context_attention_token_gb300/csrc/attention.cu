@@ -367,11 +367,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_wait_bounded(&sh.drained[x], 0);
     } else {
         // ------------------------------------------------------------- rows
+        // This warp alone waits for a whole item, which takes some 1.6 us for each key tile that its rows see, 0.8 s
+        // for 2^26 tokens. (All others wait for a few tiles.)
+        const uint32_t limit = 1 + static_cast<uint32_t>(p.T >> 25);
         uint32_t k = 0;
         for (int64_t it = blockIdx.x; it < items; it += gridDim.x, ++k) {
             const Item t = item_at(p, it, row_tiles, pair, item_rows);
             const int b = k & 1;
-            if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop)) break;
+            if (!mbar_wait_or_stop(&sh.rows_empty[b], (k / 2 & 1) ^ 1, stop, limit)) break;
             for (int i = lane; i < item_rows; i += 32) {
                 const int64_t row = t.row0 + i;
                 const int32_t g = row < p.Tp ? token_of_row(p, t.rank * p.Tp + row) : -1;

@@ -231,24 +231,25 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar)
 }
 
 // Waits of a kernel whose roles wait on one another: each gives up after
-// about a second, or as soon as another has given up (*stop, in shared memory).
-// The role then leaves its loop; the CTA ends without further work.
-__device__ __forceinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile uint32_t *stop)
+// about a second (`limit` times that, at most 128), or as soon as another has given
+// up (*stop, in shared memory). The role then leaves its loop; the CTA ends without further work.
+__device__ __forceinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile uint32_t *stop, uint32_t limit)
 {
     const uint64_t t0 = global_timer_ns();
-    for (uint32_t it = 0; it < (1u << 24); ++it) {
+    for (uint32_t it = 0; it < (limit << 24); ++it) {
         if (mbar_try_wait(bar, parity)) return true;
         if (*stop != 0) return false;
-        if (global_timer_ns() - t0 > 1000000000ull) break;
+        if (global_timer_ns() - t0 > limit * 1000000000ull) break;
     }
     *stop = 1;
     return false;
 }
 
-__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t *bar, uint32_t parity, volatile uint32_t *stop)
+__device__ __forceinline__ bool mbar_wait_or_stop(uint64_t *bar, uint32_t parity, volatile uint32_t *stop,
+                                                  uint32_t limit = 1)
 {
     if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_slow(bar, parity, stop);
+    return mbar_wait_slow(bar, parity, stop, limit);
 }
 
 // ----------------------------------------------------------------- grids in order

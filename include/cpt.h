@@ -591,7 +591,8 @@ CPT_API cpt_status cpt_epoch_status(const cpt_epoch *ep, int32_t owner, void *st
  * report). The bulk-copy kernels of the row gather, the gradient return and
  * the slot reduce move data through shared memory, each copy completing on
  * an mbarrier; the attention kernels hand tiles from warp to warp on such
- * barriers too. Every wait on one gives up after about a second or 2^24 polls.
+ * barriers too. Every wait on one gives up after about a second or 2^24 polls
+ * (one wait of the attention kernel after more, with more than 2^25 tokens).
  * A wait that gives up is counted here, its warp (in the attention kernels its
  * CTA) stops, and the outputs it had not reached are left unwritten. A non-zero
  * count means some output of an earlier call is not valid.
