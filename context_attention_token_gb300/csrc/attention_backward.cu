@@ -887,7 +887,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_fence_before();
     __syncthreads();
     tmem_fence_after();
-    __threadfence();   // the preparation, which the grid before has waited for, and not the SM's old cache lines
+    // What the preparation has left is read from here on, without a wait for the grid before (dQ), beside which this
+    // one runs. Blocks start only once every block of dQ has said next_grid_may_start, which each does behind its
+    // own wait for the preparation: that grid has ended by then, and its writes are in L2, which all
+    // SMs share. The fence, of every thread that reads, keeps it from older lines of its SM's own cache.
+    __threadfence();
     const uint32_t tmem = sh.tmem;
     volatile uint32_t *stop = &sh.stop;
     const int steps = STEPS ? STEPS : (p.D + 15) / 16, group = p.Hq / p.Hkv;

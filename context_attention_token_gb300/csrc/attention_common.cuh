@@ -73,12 +73,6 @@ __device__ __forceinline__ int32_t token_of_row(const AttentionParams &p, int64_
     return g >= 0 && in_bounds(g < p.T) ? g : -1;
 }
 
-// Whether the row at position u of its document sees position j <= u.
-__device__ __forceinline__ bool sees(const AttentionParams &p, int32_t u, int32_t j)
-{
-    return u - j < p.window || j < p.sinks;
-}
-
 // Four neighbouring bf16 elements, widened (zeros at and past `D`).
 __device__ __forceinline__ float4 load4(const void *row, int at, int D)
 {

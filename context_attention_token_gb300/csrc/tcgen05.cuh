@@ -162,7 +162,7 @@ __device__ __forceinline__ void tmem_free(uint32_t addr)
 #define CPT_IN4(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3])
 #define CPT_IN16(a, i) CPT_IN4(a, i), CPT_IN4(a, i + 4), CPT_IN4(a, i + 8), CPT_IN4(a, i + 12)
 
-// 32 (or 16) neighbouring columns of this thread's lane. The values are there
+// 32 neighbouring columns of this thread's lane. The values are there
 // only after tmem_wait_loads has taken the array.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
 {
@@ -177,17 +177,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
 __device__ __forceinline__ void tmem_wait_loads(uint32_t (&r)[32])
 {
     asm volatile("tcgen05.wait::ld.sync.aligned;" : CPT_RR16(r, 0), CPT_RR16(r, 16)::"memory");
-}
-
-__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16])
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n"
-        "tcgen05.wait::ld.sync.aligned;"
-        : CPT_R16(r, 0)
-        : "r"(addr)
-        : "memory");
 }
 
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16])
