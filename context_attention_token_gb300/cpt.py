@@ -685,10 +685,13 @@ def _attention_shape(plan: Plan, q, k, like_q, like_k, lse):
     return hq, hk, d, _dtype_code(q)
 
 
-def _mask_argument(x, bits: int):
+_WINDOW_MAX, _SINKS_MAX = (1 << 63) - 1, (1 << 31) - 1
+
+
+def _mask_argument(x, most: int):
     """A window or a number of sinks beyond the C type's range as its largest value (no document is
     longer), one below as -1, which the library refuses: ctypes would keep their lowest bits."""
-    return min(max(x, -1), (1 << bits) - 1)
+    return x if -1 <= x <= most else (most if x > most else -1)
 
 
 def cpt_attention(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, out: torch.Tensor,
@@ -697,7 +700,7 @@ def cpt_attention(plan: Plan, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     of rank-local queries over the packed documents' keys and values ([T, Hkv,
     D], global order) with a sliding window and `sinks` first tokens."""
     hq, hk, d, code = _attention_shape(plan, q, k, (q, out), (k, v), lse)
-    window, sinks = _mask_argument(window, 63), _mask_argument(sinks, 31)
+    window, sinks = _mask_argument(window, _WINDOW_MAX), _mask_argument(sinks, _SINKS_MAX)
     _check(_lib.cpt_attention(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), hq, hk, d, code,
                               scale, window, sinks, _stream(stream)))
 
@@ -712,7 +715,7 @@ def cpt_attention_backward(plan: Plan, q, k, v, out, lse, dout, dq, dk_writers, 
     tensors) of cpt_attention. Without a workspace the binding allocates one
     from torch on the current stream."""
     hq, hk, d, code = _attention_shape(plan, q, k, (q, out, dout, dq), (k, v), lse)
-    window, sinks = _mask_argument(window, 63), _mask_argument(sinks, 31)
+    window, sinks = _mask_argument(window, _WINDOW_MAX), _mask_argument(sinks, _SINKS_MAX)
     P = plan.cp_size
     dkw, dvw = _Parts(dk_writers, P), _Parts(dv_writers, P)
     for parts, what in ((dkw, "dk_writers"), (dvw, "dv_writers")):
