@@ -86,9 +86,9 @@ __device__ __noinline__ void row_forward(const AttentionParams &p, int64_t row, 
 // sinks, jumps between a rank's chunks and short documents in one rule, with
 // at most one partly used tile per contiguous span.
 //
-// Bound by the matrix unit with heads of 128: 32768 x 8 x 128, window 4096, takes
-// 0.346 ms (1.49 PFLOP/s, the unit busy for 75 % of it); by the softmax and
-// the masked tiles with documents: 65521 x 16(4) x 80, window 1000, 0.508 ms.
+// Bound by the matrix unit with heads of 128: 32768 x 8 x 128, window 4096, takes 0.34 ms on a cool GPU
+// (1.52 PFLOP/s, the unit busy for 75 % of it) and 0.36 ms in a loop (1.43); by the masked tiles, the softmax and
+// items of uneven length with documents: 65521 x 16(4) x 80, window 1000, 0.51 ms.
 
 constexpr int kThreads = 640;  // 4 warps that load and issue, 4 warpgroups of softmax
 constexpr int kRing = 8;       // key-tile announcements in flight
