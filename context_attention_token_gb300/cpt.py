@@ -67,6 +67,10 @@ CPT_ROTARY_INTERLEAVED = 1
 CPT_ROTARY_MAX_AXES = 8
 CPT_ORDER_GLOBAL = 0
 CPT_ORDER_LOCAL = 1
+CPT_GATE_NONE = 0
+CPT_GATE_TOKEN = 1
+CPT_GATE_DOCUMENT = 2
+CPT_RESIDUAL_MAX_ROW = 8192
 CPT_ATTENTION_MAX_HEADS = 1024
 CPT_ATTENTION_MAX_TOKENS = 2147482624
 
@@ -131,6 +135,27 @@ _sig("cpt_attention", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32, _i
 _sig("cpt_attention_backward_workspace_bytes", _sz, _vp, _i32, _i32, _i32)
 _sig("cpt_attention_backward", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i32, _i32,
      _i32, ctypes.c_int, ctypes.c_float, _i64, _i32, _vp, _sz, _vp)
+
+
+class _Residual(ctypes.Structure):
+    """struct cpt_residual"""
+
+    _fields_ = [("post_weight", _vp), ("pre_weight", _vp), ("gate", _vp), ("gate_kind", ctypes.c_int),
+                ("scale", ctypes.c_float), ("eps", ctypes.c_float), ("p", ctypes.c_double), ("rng", _vp),
+                ("site", ctypes.c_uint32)]
+
+
+_sig("cpt_dropout", ctypes.c_int, _vp, _vp, _vp, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_double, _vp,
+     ctypes.c_uint32, _vp)
+_sig("cpt_residual_norm", ctypes.c_int, _vp, _vp, _vp, _vp, _vp, _i64, ctypes.c_int, ctypes.c_int,
+     ctypes.POINTER(_Residual), _vp)
+_sig("cpt_residual_norm_backward_workspace_bytes", _sz, _vp, _i64, ctypes.c_int)
+_sig("cpt_residual_norm_backward", ctypes.c_int, *[_vp] * 10, _i64, ctypes.c_int, ctypes.c_int,
+     ctypes.POINTER(_Residual), _vp, _sz, _vp)
+_sig("cpt_token_logprob", ctypes.c_int, *[_vp] * 5, _i64, _i64, ctypes.c_int, ctypes.c_int, ctypes.c_float, _vp)
+_sig("cpt_token_logprob_backward", ctypes.c_int, *[_vp] * 6, _i64, _i64, ctypes.c_int, ctypes.c_int,
+     ctypes.c_float, _vp)
+_sig("cpt_policy_loss", ctypes.c_int, *[_vp] * 7, ctypes.c_double, ctypes.c_double, ctypes.c_double, _vp, _vp, _vp)
 _sig("cpt_bounds_checked", _i32)
 _sig("cpt_bounds_violations", ctypes.c_int, ctypes.POINTER(ctypes.c_uint32), _i32)
 
@@ -730,6 +755,180 @@ def cpt_attention_backward(plan: Plan, q, k, v, out, lse, dout, dq, dk_writers, 
     _check(_lib.cpt_attention_backward(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse), _ptr(dout),
                                        _ptr(dq), dkw.array(), dvw.array(), hq, hk, d, code, scale, window, sinks,
                                        _ptr(workspace), _nbytes(workspace), _stream(stream)))
+
+
+# ------------------------------------------------------------------ token rows
+
+def _row_count(plan: Plan, order: int) -> int:
+    if order not in (CPT_ORDER_GLOBAL, CPT_ORDER_LOCAL):
+        raise ValueError("unknown order")
+    return plan.padded_tokens if order else plan.total_tokens
+
+
+def _row_width(plan: Plan, order: int, t: torch.Tensor) -> int:
+    """Elements of a row of [P, T_pad/P, ...] or [T_pad, ...] (LOCAL), [T, ...] (GLOBAL)."""
+    rows, shape = _row_count(plan, order), t.shape
+    lead = 2 if order and len(shape) > 2 and shape[0] == plan.cp_size and shape[0] * shape[1] == rows else 1
+    if len(shape) <= lead or (lead == 1 and shape[0] != rows):
+        raise ValueError(f"a tensor of shape {tuple(shape)} does not hold {rows} rows")
+    width = 1
+    for n in shape[lead:]:
+        width *= n
+    return width
+
+
+def _rows_of(plan: Plan, order: int, first, others, what: str) -> int:
+    """Elements of a row of `first`, like which the others must be."""
+    width = _row_width(plan, order, first)
+    for t in others:
+        if t is None:
+            continue
+        if t.dtype != first.dtype:
+            raise ValueError(f"{what} differ in dtype")
+        if _row_width(plan, order, t) != width:
+            raise ValueError(f"{what} differ in width")
+    return width
+
+
+def _there(t) -> int:
+    """The pointer of an optional tensor. One without elements (an empty batch) has none, but is given all the
+    same: the library does not look at it, only whether it is NULL."""
+    return 0 if t is None else _ptr(t) or 16
+
+
+def _rng_ptr(rng, p: float) -> int:
+    if rng is None:
+        return 0
+    if rng.dtype not in (torch.int64, torch.uint64) or rng.numel() < 2:
+        raise ValueError("rng must hold two 64-bit integers, seed and step")
+    return _ptr(rng)
+
+
+def cpt_dropout(plan: Plan, src: torch.Tensor, dst: torch.Tensor, p: float, rng: torch.Tensor | None = None,
+                site: int = 0, order: int = CPT_ORDER_LOCAL, stream=None):
+    """dst = dropout of src (dst may be src); the mask follows every row's token. `rng` is an int64
+    tensor {seed, step} on the device. The gradient is the same call on the gradient."""
+    width = _rows_of(plan, order, src, (dst,), "src and dst")
+    _check(_lib.cpt_dropout(plan.handle, _ptr(src), _ptr(dst), width, _dtype_code(src), order, p, _rng_ptr(rng, p),
+                            site & 0xFFFFFFFF, _stream(stream)))
+
+
+def _residual_options(plan: Plan, width: int, dtype, order: int, post_weight, gate, gate_per_document, scale, p, rng,
+                      site, pre_weight, eps):
+    o = _Residual()
+    for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
+        if w is None:
+            continue
+        if w.dtype != torch.float32 or w.numel() < width:
+            raise ValueError(f"{name} must hold {width} float32 values")
+        setattr(o, name, _ptr(w))
+    if gate is not None:
+        rows = plan.n_docs if gate_per_document else _row_count(plan, order)
+        if gate.dtype != dtype or gate.numel() < rows * width:
+            raise ValueError(f"gate must hold {rows} rows of {width} elements of the tensors' dtype")
+        o.gate = _there(gate)
+        o.gate_kind = CPT_GATE_DOCUMENT if gate_per_document else CPT_GATE_TOKEN
+    o.scale, o.eps, o.p = scale, eps, p
+    o.rng, o.site = _rng_ptr(rng, p), site & 0xFFFFFFFF
+    return o
+
+
+def cpt_residual_norm(plan: Plan, x: torch.Tensor, h, y, n, *, post_weight=None, gate=None,
+                      gate_per_document: bool = False, scale: float = 1.0, p: float = 0.0, rng=None, site: int = 0,
+                      pre_weight=None, eps: float = 1e-6, order: int = CPT_ORDER_LOCAL, stream=None):
+    """y = x + scale * dropout(gate * norm(h) * post_weight) and n = norm(y) * pre_weight. What is None is left
+    out: post_weight, gate (like h, or [n_docs, row] with gate_per_document), pre_weight with n, h with y. y may be x."""
+    width = _rows_of(plan, order, x, (h, y, n), "x, h, y and n")
+    o = _residual_options(plan, width, x.dtype, order, post_weight, gate, gate_per_document, scale, p, rng, site,
+                          pre_weight, eps)
+    _check(_lib.cpt_residual_norm(plan.handle, _ptr(x), _there(h), _there(y), _there(n), width, _dtype_code(x), order,
+                                  ctypes.byref(o), _stream(stream)))
+
+
+def cpt_residual_norm_backward_workspace_bytes(plan: Plan, row_elems: int, dtype: torch.dtype) -> int:
+    code = {torch.float32: CPT_F32, torch.bfloat16: CPT_BF16}.get(dtype, -1)
+    return int(_lib.cpt_residual_norm_backward_workspace_bytes(plan.handle, row_elems, code))
+
+
+def cpt_residual_norm_backward(plan: Plan, h, y, dy, dn, dx: torch.Tensor, dh, *, dgate=None, dpost_weight=None,
+                               dpre_weight=None, post_weight=None, gate=None, gate_per_document: bool = False,
+                               scale: float = 1.0, p: float = 0.0, rng=None, site: int = 0, pre_weight=None,
+                               eps: float = 1e-6, order: int = CPT_ORDER_LOCAL, workspace=None, stream=None):
+    """Gradients of cpt_residual_norm from h, y (x where there was no h), dy and dn. dgate is float32 [n_docs, row]
+    with gate_per_document; the weights' gradients are float32. dx may be dy. Without a workspace the
+    binding allocates one from torch on the current stream."""
+    width = _rows_of(plan, order, dx, (h, y, dy, dn, dh), "h, y, dy, dn, dx and dh")
+    o = _residual_options(plan, width, dx.dtype, order, post_weight, gate, gate_per_document, scale, p, rng, site,
+                          pre_weight, eps)
+    for name, w in (("dpost_weight", dpost_weight), ("dpre_weight", dpre_weight)):
+        if w is not None and (w.dtype != torch.float32 or w.numel() < width):
+            raise ValueError(f"{name} must hold {width} float32 values")
+    if dgate is not None:
+        rows, kind = (plan.n_docs, torch.float32) if gate_per_document else (_row_count(plan, order), dx.dtype)
+        if dgate.dtype != kind or dgate.numel() < rows * width:
+            raise ValueError(f"dgate must hold {rows} rows of {width} values of {kind}")
+    if workspace is None:
+        if stream is not None:
+            raise ValueError("give a workspace with a stream: torch allocates on its current stream only")
+        need = cpt_residual_norm_backward_workspace_bytes(plan, width, dx.dtype)
+        workspace = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
+    _check(_lib.cpt_residual_norm_backward(plan.handle, _there(h), _there(y), _there(dy), _there(dn), _there(dx),
+                                           _there(dh), _there(dgate), _ptr(dpost_weight), _ptr(dpre_weight), width,
+                                           _dtype_code(dx), order, ctypes.byref(o), _ptr(workspace), _nbytes(workspace),
+                                           _stream(stream)))
+
+
+def _logits_shape(plan: Plan, logits, vocab, order, targets, per_token):
+    """(vocab, vocab_padded) of rows of logits, every buffer large enough."""
+    rows, T = _row_count(plan, order), plan.total_tokens
+    width = logits.shape[-1] if logits.dim() > 0 else 0
+    if logits.numel() < rows * width:
+        raise ValueError(f"the logits hold {logits.numel()} elements but the call touches {rows} rows of {width}")
+    if targets.dtype != torch.int32 or targets.numel() < T:
+        raise ValueError(f"targets must hold {T} int32 values")
+    for t, count, what in per_token:
+        if t.dtype != torch.float32 or t.numel() < count * T:
+            raise ValueError(f"{what} must hold {count * T} float32 values")
+    return (width if vocab is None else vocab), width
+
+
+def cpt_token_logprob(plan: Plan, logits: torch.Tensor, targets: torch.Tensor, logp: torch.Tensor,
+                      stats: torch.Tensor, *, vocab: int | None = None, scale: float = 1.0,
+                      order: int = CPT_ORDER_LOCAL, stream=None):
+    """logp[g] = log of the probability that token g's logits give to targets[g] (int32, global order; negative:
+    none), over the first `vocab` columns (all, if None); stats [T, 2] for the gradient."""
+    v, width = _logits_shape(plan, logits, vocab, order, targets, ((logp, 1, "logp"), (stats, 2, "stats")))
+    _check(_lib.cpt_token_logprob(plan.handle, _ptr(logits), _ptr(targets), _ptr(logp), _ptr(stats), v, width,
+                                  _dtype_code(logits), order, scale, _stream(stream)))
+
+
+def cpt_token_logprob_backward(plan: Plan, logits: torch.Tensor, targets: torch.Tensor, stats: torch.Tensor,
+                               dlogp: torch.Tensor, dlogits: torch.Tensor, *, vocab: int | None = None,
+                               scale: float = 1.0, order: int = CPT_ORDER_LOCAL, stream=None):
+    """dlogits (may be logits) of cpt_token_logprob from the gradient of logp."""
+    v, width = _logits_shape(plan, logits, vocab, order, targets, ((stats, 2, "stats"), (dlogp, 1, "dlogp")))
+    if dlogits.dtype != logits.dtype or dlogits.numel() < _row_count(plan, order) * width:
+        raise ValueError("dlogits must be like logits")
+    _check(_lib.cpt_token_logprob_backward(plan.handle, _ptr(logits), _ptr(targets), _ptr(stats), _ptr(dlogp),
+                                           _ptr(dlogits), v, width, _dtype_code(logits), order, scale,
+                                           _stream(stream)))
+
+
+def cpt_policy_loss(plan: Plan, logp: torch.Tensor, logp_old: torch.Tensor, advantages: torch.Tensor,
+                    terms: torch.Tensor, dlogp: torch.Tensor, *, logp_ref=None, mask=None, weights=None,
+                    clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, stream=None):
+    """terms [n_docs, 4] (loss, KL, clipped share, tokens) of the clipped policy loss and dlogp [T], the gradient
+    of the documents' losses, weighted. mask is bool or uint8 [T]; weights None: 1 / n_docs each."""
+    T, n = plan.total_tokens, plan.n_docs
+    for t, count, what in ((logp, T, "logp"), (logp_old, T, "logp_old"), (logp_ref, T, "logp_ref"), (dlogp, T, "dlogp"),
+                           (advantages, n, "advantages"), (weights, n, "weights"), (terms, 4 * n, "terms")):
+        if t is not None and (t.dtype != torch.float32 or t.numel() < count):
+            raise ValueError(f"{what} must hold {count} float32 values")
+    if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.numel() < T):
+        raise ValueError(f"mask must hold {T} values of bool or uint8")
+    _check(_lib.cpt_policy_loss(plan.handle, _ptr(logp), _ptr(logp_old), _ptr(logp_ref), _ptr(mask), _ptr(advantages),
+                                _ptr(weights), clip_low, clip_high, kl_coef, _ptr(terms), _ptr(dlogp),
+                                _stream(stream)))
 
 
 # ------------------------------------------------------------------ epochs

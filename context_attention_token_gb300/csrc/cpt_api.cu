@@ -270,6 +270,7 @@ struct cpt_plan {
     int32_t *cu, *cup, *cu_local, *num_segs, *first, *offs, *l2g, *g2l, *l2r, *r2l;
     std::vector<int32_t> h_cu;   // host copy of cu_seqlens (the source of its device copy)
     std::vector<int32_t> h_cup;  // host copy of the padded boundaries
+    int32_t longest;  // tokens of the longest document
 };
 
 struct cpt_rotary {
@@ -463,6 +464,9 @@ cpt_status cpt_plan_create(cpt_layout layout, int32_t P, const int32_t *cu, int3
         p->r2l = nullptr;
     }
     p->Tp = p->Tpad / P;
+    p->longest = 0;
+    for (int32_t i = 0; i < n; ++i)
+        if (cu[i + 1] - cu[i] > p->longest) p->longest = cu[i + 1] - cu[i];
 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = cudaMemcpyAsync(p->cu, p->h_cu.data(), sizeof(int32_t) * (size_t)(n + 1),
@@ -1134,15 +1138,17 @@ cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset)
         return fail(CPT_ERR_UNSUPPORTED, "this library was built without CPT_CHECK_BOUNDS");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0;
     cudaError_t e = read_index_map_bounds_violations(&a, reset != 0);
     if (e == cudaSuccess) e = read_gather_bounds_violations(&b, reset != 0);
     if (e == cudaSuccess) e = read_grad_return_bounds_violations(&c, reset != 0);
     if (e == cudaSuccess) e = read_rotary_bounds_violations(&d, reset != 0);
     if (e == cudaSuccess) e = read_attention_bounds_violations(&f, reset != 0);
     if (e == cudaSuccess) e = read_attention_backward_bounds_violations(&g, reset != 0);
+    if (e == cudaSuccess) e = read_residual_bounds_violations(&h, reset != 0);
+    if (e == cudaSuccess) e = read_logprob_bounds_violations(&i, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "bounds counter read");
-    *count = a + b + c + d + f + g;
+    *count = a + b + c + d + f + g + h + i;
     return CPT_OK;
 }
 
@@ -1488,6 +1494,421 @@ cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, const voi
     p.packed = plan->layout == CPT_LAYOUT_PACKED_CONTIGUOUS;
     cudaError_t e = launch_attention_backward(p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CPT_OK : cuda_fail(e, "attention backward launch");
+}
+
+}  // extern "C"
+
+// ----------------------------------------------------------------- token rows
+
+namespace {
+
+// A buffer of a call; NULL or without bytes: not looked at.
+struct Buf {
+    const void *p;
+    size_t bytes;
+    size_t align;
+    bool output;
+    const char *what;
+};
+
+// Every buffer is aligned device memory, and outputs overlap nothing. (An input that an output may be is left
+// out by the caller where it is that output.)
+cpt_status check_buffers(const Buf *b, size_t n, const cpt_plan *plan, int dev)
+{
+    Ranges r;
+    add_range(r, plan->ws, plan->ws_bytes, false, "plan workspace");
+    cpt_status st;
+    for (size_t i = 0; i < n; ++i) {
+        if (b[i].p == nullptr || b[i].bytes == 0) continue;
+        if ((st = check_ptr(b[i].p, dev, b[i].align, b[i].what))) return st;
+        add_range(r, b[i].p, b[i].bytes, b[i].output, b[i].what);
+    }
+    return check_overlaps(r);
+}
+
+// Maps between the rows of `order` and raw tokens: rows of a tensor, the token of a row (nullptr: the row
+// itself) and the row of a token (nullptr: the token itself).
+struct RowMaps {
+    int64_t rows;
+    const int32_t *token_of_row, *row_of_token;
+};
+
+RowMaps row_maps(const cpt_plan *plan, cpt_order order)
+{
+    RowMaps m = {plan->T, nullptr, nullptr};
+    if (order == CPT_ORDER_LOCAL) {
+        m.rows = plan->Tpad;
+        if (plan->layout != CPT_LAYOUT_PACKED_CONTIGUOUS) {
+            const bool pad = is_padded(plan->layout);
+            m.token_of_row = pad ? plan->l2r : plan->l2g;
+            m.row_of_token = pad ? plan->r2l : plan->g2l;
+        }
+    }
+    return m;
+}
+
+// The rule of a dropout with probability p, its factor times `scale`.
+cpt_status drop_rule(double p, const uint64_t *rng, uint32_t site, float scale, DropRule *out)
+{
+    if (!(p >= 0.0 && p <= 1.0)) return fail(CPT_ERR_INVALID_ARG, "p is not a probability");
+    out->rng = nullptr;
+    out->site = site;
+    out->kept = 65536;
+    out->factor = scale;
+    if (p == 0.0) return CPT_OK;
+    if (rng == nullptr) return fail(CPT_ERR_INVALID_ARG, "rng is NULL");
+    out->rng = rng;
+    out->kept = static_cast<uint32_t>(std::floor((1.0 - p) * 65536.0 + 0.5));
+    out->factor = out->kept == 0 ? 0.0f : static_cast<float>(65536.0 / out->kept * scale);
+    return CPT_OK;
+}
+
+cpt_status check_residual(int64_t row_elems, cpt_dtype dtype, cpt_order order, const cpt_residual *o, bool branch,
+                          int64_t *units)
+{
+    cpt_status st;
+    if (o == nullptr) return fail(CPT_ERR_INVALID_ARG, "options is NULL");
+    if (!order_ok(order)) return fail(CPT_ERR_INVALID_ARG, "unknown order");
+    if ((st = check_row(row_elems, dtype, dtype, units))) return st;
+    if (row_elems > CPT_RESIDUAL_MAX_ROW)
+        return fail(CPT_ERR_UNSUPPORTED, "row of %lld elements is over %d", (long long)row_elems, CPT_RESIDUAL_MAX_ROW);
+    if (o->gate_kind != CPT_GATE_NONE && o->gate_kind != CPT_GATE_TOKEN && o->gate_kind != CPT_GATE_DOCUMENT)
+        return fail(CPT_ERR_INVALID_ARG, "unknown gate_kind %d", (int)o->gate_kind);
+    if ((o->gate_kind == CPT_GATE_NONE) != (o->gate == nullptr))
+        return fail(CPT_ERR_INVALID_ARG, "gate and gate_kind do not agree");
+    if (!std::isfinite(o->scale)) return fail(CPT_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(o->eps) || !(o->eps >= 0.0f))
+        return fail(CPT_ERR_INVALID_ARG, "eps is not a finite number of at least 0");
+    if (!branch && (o->post_weight != nullptr || o->gate != nullptr || o->p != 0.0))
+        return fail(CPT_ERR_INVALID_ARG, "post_weight, gate and p need a block's output");
+    if (!branch && o->pre_weight == nullptr)
+        return fail(CPT_ERR_INVALID_ARG, "neither a block's output nor a pre_weight: nothing to compute");
+    return CPT_OK;
+}
+
+void fill_residual(ResidualParams &p, const cpt_plan *plan, int64_t row_elems, cpt_order order, const cpt_residual *o)
+{
+    const RowMaps m = row_maps(plan, order);
+    p.gate = static_cast<const uint8_t *>(o->gate);
+    p.post = o->post_weight;
+    p.pre = o->pre_weight;
+    p.token_of_row = m.token_of_row;
+    p.row_of_token = m.row_of_token;
+    p.cu = plan->cu;
+    p.rows = m.rows;
+    p.T = plan->T;
+    p.n_docs = plan->n;
+    p.row_elems = static_cast<int32_t>(row_elems);
+    p.gate_kind = o->gate_kind;
+    p.scale = o->scale;
+    p.eps = o->eps;
+}
+
+size_t gate_bytes(const cpt_plan *plan, const cpt_residual *o, size_t row_tensor, size_t row_bytes)
+{
+    return o->gate_kind == CPT_GATE_DOCUMENT ? (size_t)plan->n * row_bytes : row_tensor;
+}
+
+// rows of logits: whole 16 bytes, the vocabulary inside them
+cpt_status check_logits(int64_t vocab, int64_t vocab_padded, cpt_dtype dtype, cpt_order order, float scale,
+                        int64_t *units)
+{
+    cpt_status st;
+    if (!order_ok(order)) return fail(CPT_ERR_INVALID_ARG, "unknown order");
+    if ((st = check_row(vocab_padded, dtype, dtype, units))) return st;
+    if (vocab < 1 || vocab > vocab_padded)
+        return fail(CPT_ERR_INVALID_ARG, "vocab %lld outside 1..%lld", (long long)vocab, (long long)vocab_padded);
+    if (!std::isfinite(scale) || !(scale > 0.0f))
+        return fail(CPT_ERR_INVALID_ARG, "scale is not a finite positive number");
+    return CPT_OK;
+}
+
+void fill_logprob(LogprobParams &p, const cpt_plan *plan, const void *logits, const int32_t *targets, const float *logp,
+                  const float *stats, int64_t vocab, int64_t units, cpt_order order, float scale)
+{
+    const RowMaps m = row_maps(plan, order);
+    p.logits = static_cast<const uint8_t *>(logits);
+    p.targets = targets;
+    p.logp = const_cast<float *>(logp);
+    p.stats = reinterpret_cast<float2 *>(const_cast<float *>(stats));
+    p.token_of_row = m.token_of_row;
+    p.row_of_token = m.row_of_token;
+    p.rows = m.rows;
+    p.T = plan->T;
+    p.units = units;
+    p.vocab = vocab;
+    p.scale = scale;
+}
+
+}  // namespace
+
+extern "C" {
+
+cpt_status cpt_dropout(const cpt_plan *plan, const void *src, void *dst, int64_t row_elems, cpt_dtype dtype,
+                       cpt_order order, double p, const uint64_t *rng, uint32_t site, void *stream)
+{
+    Trace trace("cpt_dropout");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    if (!order_ok(order)) return fail(CPT_ERR_INVALID_ARG, "unknown order");
+    int64_t units = 0;
+    if ((st = check_row(row_elems, dtype, dtype, &units))) return st;
+    DropoutParams a;
+    memset(&a, 0, sizeof a);
+    if ((st = drop_rule(p, rng, site, 1.0f, &a.rule))) return st;
+    const RowMaps m = row_maps(plan, order);
+    if (m.rows == 0) return CPT_OK;
+    if (src == nullptr) return fail(CPT_ERR_INVALID_ARG, "src is NULL");
+    if (dst == nullptr) return fail(CPT_ERR_INVALID_ARG, "dst is NULL");
+    const size_t bytes = (size_t)m.rows * (size_t)units * 16;
+    const Buf bufs[] = {
+        {src == dst ? nullptr : src, bytes, 16, false, "src"},
+        {dst, bytes, 16, true, "dst"},
+        {a.rule.rng, 16, 8, false, "rng"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    a.src = static_cast<const uint8_t *>(src);
+    a.dst = static_cast<uint8_t *>(dst);
+    a.token_of_row = m.token_of_row;
+    a.rows = m.rows;
+    a.units = static_cast<int32_t>(units);
+    const cudaError_t e = launch_dropout(a, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "dropout launch");
+}
+
+cpt_status cpt_residual_norm(const cpt_plan *plan, const void *x, const void *h, void *y, void *n, int64_t row_elems,
+                             cpt_dtype dtype, cpt_order order, const cpt_residual *options, void *stream)
+{
+    Trace trace("cpt_residual_norm");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    int64_t units = 0;
+    if ((st = check_residual(row_elems, dtype, order, options, h != nullptr, &units))) return st;
+    if ((h == nullptr) != (y == nullptr)) return fail(CPT_ERR_INVALID_ARG, "h and y must both be given or both NULL");
+    if ((n == nullptr) != (options->pre_weight == nullptr))
+        return fail(CPT_ERR_INVALID_ARG, "n and pre_weight must both be given or both NULL");
+    ResidualParams p;
+    memset(&p, 0, sizeof p);
+    if ((st = drop_rule(options->p, options->rng, options->site, options->scale, &p.rule))) return st;
+    fill_residual(p, plan, row_elems, order, options);
+    if (p.rows == 0) return CPT_OK;
+    if (x == nullptr) return fail(CPT_ERR_INVALID_ARG, "x is NULL");
+    const size_t row = (size_t)units * 16, all = (size_t)p.rows * row;
+    const Buf bufs[] = {
+        {x == y ? nullptr : x, all, 16, false, "x"},
+        {h, all, 16, false, "h"},
+        {y, all, 16, true, "y"},
+        {n, all, 16, true, "n"},
+        {options->gate, gate_bytes(plan, options, all, row), 16, false, "gate"},
+        {options->post_weight, sizeof(float) * (size_t)row_elems, 16, false, "post_weight"},
+        {options->pre_weight, sizeof(float) * (size_t)row_elems, 16, false, "pre_weight"},
+        {p.rule.rng, 16, 8, false, "rng"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    p.x = static_cast<const uint8_t *>(x);
+    p.h = static_cast<const uint8_t *>(h);
+    p.y = static_cast<uint8_t *>(y);
+    p.n = static_cast<uint8_t *>(n);
+    const cudaError_t e = launch_residual_norm(p, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "residual norm launch");
+}
+
+size_t cpt_residual_norm_backward_workspace_bytes(const cpt_plan *plan, int64_t row_elems, cpt_dtype dtype)
+{
+    if (plan == nullptr) {
+        fail(CPT_ERR_INVALID_ARG, "plan is NULL");
+        return 0;
+    }
+    int64_t units = 0;
+    if (check_row(row_elems, dtype, dtype, &units) != CPT_OK) return 0;
+    if (row_elems > CPT_RESIDUAL_MAX_ROW) {
+        fail(CPT_ERR_UNSUPPORTED, "row of %lld elements is over %d", (long long)row_elems, CPT_RESIDUAL_MAX_ROW);
+        return 0;
+    }
+    return (size_t)residual_backward_workspace(plan->T, row_elems, dtype, plan->device);
+}
+
+cpt_status cpt_residual_norm_backward(const cpt_plan *plan, const void *h, const void *y, const void *dy, const void *dn,
+                                      void *dx, void *dh, void *dgate, float *dpost_weight, float *dpre_weight,
+                                      int64_t row_elems, cpt_dtype dtype, cpt_order order, const cpt_residual *options,
+                                      void *workspace, size_t workspace_bytes, void *stream)
+{
+    Trace trace("cpt_residual_norm_backward");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    int64_t units = 0;
+    if ((st = check_residual(row_elems, dtype, order, options, dh != nullptr, &units))) return st;
+    const bool pre = options->pre_weight != nullptr, post = options->post_weight != nullptr;
+    const bool gated = options->gate_kind != CPT_GATE_NONE;
+    if (pre != (y != nullptr) || pre != (dn != nullptr) || pre != (dpre_weight != nullptr))
+        return fail(CPT_ERR_INVALID_ARG, "y, dn and dpre_weight must be given exactly with a pre_weight");
+    if (post != (dpost_weight != nullptr))
+        return fail(CPT_ERR_INVALID_ARG, "dpost_weight must be given exactly with a post_weight");
+    if (gated != (dgate != nullptr)) return fail(CPT_ERR_INVALID_ARG, "dgate must be given exactly with a gate");
+    if ((post || gated) && h == nullptr) return fail(CPT_ERR_INVALID_ARG, "h is NULL");
+    if (dh == nullptr && h != nullptr) return fail(CPT_ERR_INVALID_ARG, "dh is NULL");
+    if (!pre && dy == nullptr) return fail(CPT_ERR_INVALID_ARG, "neither dy nor dn: no gradient comes in");
+    if (dx == nullptr) return fail(CPT_ERR_INVALID_ARG, "dx is NULL");
+    ResidualParams p;
+    memset(&p, 0, sizeof p);
+    if ((st = drop_rule(options->p, options->rng, options->site, options->scale, &p.rule))) return st;
+    fill_residual(p, plan, row_elems, order, options);
+    const size_t need = (size_t)residual_backward_workspace(plan->T, row_elems, dtype, dev);
+    if (need > 0) {
+        if (workspace == nullptr) return fail(CPT_ERR_WORKSPACE, "workspace is NULL");
+        if (reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
+            return fail(CPT_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+        if (workspace_bytes < need)
+            return fail(CPT_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", workspace_bytes, need);
+    }
+    const size_t row = (size_t)units * 16, all = (size_t)p.rows * row, wide = sizeof(float) * (size_t)row_elems;
+    const bool per_document = options->gate_kind == CPT_GATE_DOCUMENT;
+    const Buf bufs[] = {
+        {h, all, 16, false, "h"},
+        {y, all, 16, false, "y"},
+        {dy == dx ? nullptr : dy, all, 16, false, "dy"},
+        {dn, all, 16, false, "dn"},
+        {dx, all, 16, true, "dx"},
+        {dh, all, 16, true, "dh"},
+        {options->gate, gate_bytes(plan, options, all, row), 16, false, "gate"},
+        {dgate, per_document ? (size_t)plan->n * wide : all, 16, true, "dgate"},
+        {options->post_weight, wide, 16, false, "post_weight"},
+        {dpost_weight, wide, 16, true, "dpost_weight"},
+        {options->pre_weight, wide, 16, false, "pre_weight"},
+        {dpre_weight, wide, 16, true, "dpre_weight"},
+        {p.rule.rng, 16, 8, false, "rng"},
+        {workspace, need, 256, true, "workspace"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    p.x = static_cast<const uint8_t *>(dy);
+    p.h = static_cast<const uint8_t *>(h);
+    p.y_in = static_cast<const uint8_t *>(y);
+    p.dn = static_cast<const uint8_t *>(dn);
+    p.y = static_cast<uint8_t *>(dx);
+    p.n = static_cast<uint8_t *>(dh);
+    p.dgate = static_cast<uint8_t *>(dgate);
+    p.dpost = dpost_weight;
+    p.dpre = dpre_weight;
+    const cudaError_t e = launch_residual_norm_backward(p, dtype, workspace, dev, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "residual norm backward launch");
+}
+
+cpt_status cpt_token_logprob(const cpt_plan *plan, const void *logits, const int32_t *targets, float *logp, float *stats,
+                             int64_t vocab, int64_t vocab_padded, cpt_dtype dtype, cpt_order order, float scale,
+                             void *stream)
+{
+    Trace trace("cpt_token_logprob");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    int64_t units = 0;
+    if ((st = check_logits(vocab, vocab_padded, dtype, order, scale, &units))) return st;
+    if (plan->T == 0) return CPT_OK;
+    LogprobParams p;
+    memset(&p, 0, sizeof p);
+    fill_logprob(p, plan, logits, targets, logp, stats, vocab, units, order, scale);
+    const size_t T = (size_t)plan->T;
+    if (logits == nullptr) return fail(CPT_ERR_INVALID_ARG, "logits is NULL");
+    if (targets == nullptr) return fail(CPT_ERR_INVALID_ARG, "targets is NULL");
+    if (logp == nullptr) return fail(CPT_ERR_INVALID_ARG, "logp is NULL");
+    if (stats == nullptr) return fail(CPT_ERR_INVALID_ARG, "stats is NULL");
+    const Buf bufs[] = {
+        {logits, (size_t)p.rows * (size_t)units * 16, 16, false, "logits"},
+        {targets, 4 * T, 4, false, "targets"},
+        {logp, 4 * T, 4, true, "logp"},
+        {stats, 8 * T, 8, true, "stats"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    const cudaError_t e = launch_token_logprob(p, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "log-probability launch");
+}
+
+cpt_status cpt_token_logprob_backward(const cpt_plan *plan, const void *logits, const int32_t *targets,
+                                      const float *stats, const float *dlogp, void *dlogits, int64_t vocab,
+                                      int64_t vocab_padded, cpt_dtype dtype, cpt_order order, float scale, void *stream)
+{
+    Trace trace("cpt_token_logprob_backward");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    int64_t units = 0;
+    if ((st = check_logits(vocab, vocab_padded, dtype, order, scale, &units))) return st;
+    LogprobParams p;
+    memset(&p, 0, sizeof p);
+    fill_logprob(p, plan, logits, targets, dlogp, stats, vocab, units, order, scale);
+    if (p.rows == 0) return CPT_OK;
+    if (logits == nullptr) return fail(CPT_ERR_INVALID_ARG, "logits is NULL");
+    if (dlogits == nullptr) return fail(CPT_ERR_INVALID_ARG, "dlogits is NULL");
+    if (targets == nullptr) return fail(CPT_ERR_INVALID_ARG, "targets is NULL");
+    if (stats == nullptr) return fail(CPT_ERR_INVALID_ARG, "stats is NULL");
+    if (dlogp == nullptr) return fail(CPT_ERR_INVALID_ARG, "dlogp is NULL");
+    const size_t T = (size_t)plan->T, all = (size_t)p.rows * (size_t)units * 16;
+    const Buf bufs[] = {
+        {logits == dlogits ? nullptr : logits, all, 16, false, "logits"},
+        {dlogits, all, 16, true, "dlogits"},
+        {targets, 4 * T, 4, false, "targets"},
+        {stats, 8 * T, 8, false, "stats"},
+        {dlogp, 4 * T, 4, false, "dlogp"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    p.dlogits = static_cast<uint8_t *>(dlogits);
+    const cudaError_t e = launch_token_logprob_backward(p, dtype, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "log-probability backward launch");
+}
+
+cpt_status cpt_policy_loss(const cpt_plan *plan, const float *logp, const float *logp_old, const float *logp_ref,
+                           const uint8_t *mask, const float *advantages, const float *weights, double clip_low,
+                           double clip_high, double kl_coef, float *terms, float *dlogp, void *stream)
+{
+    Trace trace("cpt_policy_loss");
+    int dev = 0;
+    cpt_status st = check_plan(plan, &dev);
+    if (st) return st;
+    if (!(clip_low >= 0.0 && clip_low <= 1.0)) return fail(CPT_ERR_INVALID_ARG, "clip_low is outside 0..1");
+    if (!(clip_high >= 0.0 && clip_high <= 1e30)) return fail(CPT_ERR_INVALID_ARG, "clip_high is outside 0..1e30");
+    if (!(kl_coef >= 0.0 && kl_coef <= 1e30)) return fail(CPT_ERR_INVALID_ARG, "kl_coef is outside 0..1e30");
+    if (logp_ref == nullptr && kl_coef != 0.0) return fail(CPT_ERR_INVALID_ARG, "a kl_coef needs logp_ref");
+    if (plan->n == 0) return CPT_OK;
+    if (advantages == nullptr) return fail(CPT_ERR_INVALID_ARG, "advantages is NULL");
+    if (terms == nullptr) return fail(CPT_ERR_INVALID_ARG, "terms is NULL");
+    const size_t T = (size_t)plan->T, n = (size_t)plan->n;
+    if (T > 0 && (logp == nullptr || logp_old == nullptr || dlogp == nullptr))
+        return fail(CPT_ERR_INVALID_ARG, "logp, logp_old or dlogp is NULL");
+    const Buf bufs[] = {
+        {logp, 4 * T, 4, false, "logp"},       {logp_old, 4 * T, 4, false, "logp_old"},
+        {logp_ref, 4 * T, 4, false, "logp_ref"}, {mask, T, 1, false, "mask"},
+        {advantages, 4 * n, 4, false, "advantages"}, {weights, 4 * n, 4, false, "weights"},
+        {terms, 16 * n, 16, true, "terms"},    {dlogp, 4 * T, 4, true, "dlogp"},
+    };
+    if ((st = check_buffers(bufs, sizeof bufs / sizeof bufs[0], plan, dev))) return st;
+    PolicyParams p;
+    memset(&p, 0, sizeof p);
+    p.logp = logp;
+    p.old = logp_old;
+    p.ref = logp_ref;
+    p.mask = mask;
+    p.advantages = advantages;
+    p.weights = weights;
+    p.cu = plan->cu;
+    p.n_docs = plan->n;
+    p.T = plan->T;
+    const double high = std::log1p(clip_high), low = clip_low < 1.0 ? std::log1p(-clip_low) : -HUGE_VAL;
+    p.high_hi = static_cast<float>(high);
+    p.high_lo = static_cast<float>(high - p.high_hi);
+    p.low_hi = static_cast<float>(low);
+    p.low_lo = clip_low < 1.0 ? static_cast<float>(low - p.low_hi) : 0.0f;
+    p.above = static_cast<float>(1.0 + clip_high);
+    p.below = static_cast<float>(1.0 - clip_low);
+    p.kl = static_cast<float>(kl_coef);
+    p.weight = static_cast<float>(1.0 / static_cast<double>(plan->n));
+    p.terms = reinterpret_cast<float4 *>(terms);
+    p.dlogp = dlogp;
+    p.longest = plan->longest;
+    const cudaError_t e = launch_policy_loss(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? CPT_OK : cuda_fail(e, "policy loss launch");
 }
 
 }  // extern "C"

@@ -186,6 +186,90 @@ int64_t attention_backward_workspace(int64_t T, int64_t Tpad, int P, int Hq, int
 cudaError_t launch_attention_backward(AttentionBackwardParams p, void *workspace, cudaStream_t stream);
 cudaError_t read_attention_backward_wait_timeouts(unsigned int *count, bool reset);
 
+// Dropout by token (the rule's constants and the generator: token_rows.cuh).
+struct DropRule {
+    const uint64_t *rng;   // device {seed, step}; nullptr: no dropout
+    uint32_t site;
+    uint32_t kept;         // of 2^16 values, those that keep an element
+    float factor;          // 2^16 / kept times the caller's scale (1 or the scale without dropout)
+};
+struct DropoutParams {
+    const uint8_t *src;
+    uint8_t *dst;
+    const int32_t *token_of_row;   // raw token of every row (-1: padding); nullptr: the row itself
+    int64_t rows;
+    int32_t units;                 // 16-byte units per row
+    DropRule rule;
+    int64_t step_rows;             // filled in by the launcher: a thread's step in rows and units
+    int32_t step_units;
+};
+cudaError_t launch_dropout(DropoutParams p, int dtype, cudaStream_t stream);
+
+// The residual stream between two blocks and its gradient.
+constexpr int kResidualMaxRow = 8192;
+struct ResidualParams {
+    const uint8_t *x, *h, *gate;       // x: dy in the gradient (may be nullptr there)
+    const uint8_t *y_in, *dn;          // gradient only
+    uint8_t *y, *n;                    // dx and dh in the gradient
+    uint8_t *dgate;                    // gradient only
+    float *dpost, *dpre;               // gradient only
+    const float *post, *pre;           // weights or nullptr
+    const int32_t *token_of_row;       // nullptr: the row itself
+    const int32_t *row_of_token;       // nullptr: the token itself
+    const int32_t *cu;                 // document boundaries [n_docs + 1]
+    int64_t rows, T;
+    int32_t n_docs;
+    int32_t row_elems;
+    int32_t units;
+    int32_t gate_kind;
+    float scale, eps;
+    DropRule rule;
+    // set by the launcher
+    int32_t group;                     // threads of a row
+    int64_t per_group;                 // rows or tokens that a group takes, neighbours
+    float *part_post, *part_pre;       // [CTAs][row_elems]
+    float *part_gate;                  // [groups][2][row_elems]: of a document begun earlier, of one that goes on
+    int32_t parts;
+};
+cudaError_t launch_residual_norm(ResidualParams p, int dtype, cudaStream_t stream);
+int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device);
+cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream);
+
+// Log-probabilities of targets, and their gradient.
+struct LogprobParams {
+    const uint8_t *logits;
+    uint8_t *dlogits;
+    const int32_t *targets;        // [T]
+    float *logp;                   // [T]; dlogp in the gradient
+    float2 *stats;                 // [T]
+    const int32_t *token_of_row, *row_of_token;
+    int64_t rows, T;
+    int64_t units;                 // 16-byte units of a row, padding included
+    int64_t vocab;
+    float scale;
+    int64_t step_rows, step_units; // filled in by the launcher
+};
+cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream);
+cudaError_t launch_token_logprob_backward(LogprobParams p, int dtype, cudaStream_t stream);
+
+// Clipped policy loss per document.
+struct PolicyParams {
+    const float *logp, *old, *ref;
+    const uint8_t *mask;
+    const float *advantages, *weights;
+    const int32_t *cu;
+    int32_t n_docs;
+    int64_t T;
+    float high_hi, high_lo, low_hi, low_lo;   // log(1 + clip_high), log(1 - clip_low), two floats each
+    float above, below;                       // 1 + clip_high, 1 - clip_low
+    float kl;
+    float weight;                             // of every document where weights is nullptr
+    float4 *terms;
+    float *dlogp;
+    int32_t longest;                          // tokens of the longest document
+};
+cudaError_t launch_policy_loss(const PolicyParams &p, cudaStream_t stream);
+
 // Streaming ceiling: dst = copy of srcs[0], srcs[1..n_src) read and
 // discarded, through the bulk-copy engine in blocks of block_bytes and a ring
 // of `stages` stages per CTA, at most ctas_per_sm CTAs per SM.
@@ -201,6 +285,8 @@ cudaError_t read_gather_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_grad_return_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_rotary_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_attention_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_residual_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_logprob_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset);
 
 // Bounded epoch check: one warp polls flags_row[0..P) with acquire loads until

@@ -12,7 +12,10 @@
  *   - the staged alternative (scatter, epoch publish, bounded epoch wait,
  *     slot reduce), and the ordered one-shot sum of P slot buffers,
  *   - the attention layer between the reorder and the return: rotary
- *     positions, attention with a sliding window and sinks, its gradient.
+ *     positions, attention with a sliding window and sinks, its gradient,
+ *   - what surrounds that layer on token rows: dropout by token, the
+ *     residual stream between two blocks and its gradient, the targets'
+ *     log-probabilities and their gradient, a clipped policy loss.
  *
  * Sources, by page title:
  *   [TE-3221] "[PyTorch] Add experimental packed-contiguous THD all-gather
@@ -54,7 +57,8 @@
  *   Graphs      cpt_index_map, cpt_thd_metadata, cpt_thd_real_lengths,
  *               cpt_partition, cpt_restore, cpt_grad_return(_accumulate),
  *               cpt_grad_scatter, cpt_slot_reduce, cpt_rotary_apply,
- *               cpt_attention and cpt_attention_backward only enqueue kernels,
+ *               cpt_attention and cpt_attention_backward, and the calls from
+ *               cpt_dropout to cpt_policy_loss only enqueue kernels,
  *               so they can be recorded into a CUDA graph (build the plan
  *               first). cpt_plan_create, cpt_grad_return_noalloc and the
  *               epoch publish/wait calls act on host state at call time and
@@ -799,6 +803,171 @@ CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, c
                                           int32_t kv_heads, int32_t head_dim, cpt_dtype dtype, float scale,
                                           int64_t window, int32_t sinks, void *workspace,
                                           size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Dropout by token                                                    */
+/* ------------------------------------------------------------------ */
+
+/* Around the attention layer a step works on token rows (the pages leave it to
+ * the caller). The calls from here on are for what has to know which token or
+ * document a row is: dropout, the residual stream between two blocks, and the
+ * loss. Their row tensors are [T][row] (GLOBAL) or [P][T_pad/P][row] (LOCAL).
+ *
+ * Random bits. Element (token g, column c) of a call has 16 bits of the ten-round
+ * Philox-4x32 generator (Salmon and others, "Parallel random numbers: as easy as
+ * 1, 2, 3", 2011): key = the seed (low word, high word), counter = (c / 8, g, low
+ * word of the step, site), and of the four words c mod 8 names the half: word
+ * (c mod 8) / 2, its low half for an even c. So the bits follow the token, not the row:
+ * both row orders, every layout and any cp_size have the same, and the gradient
+ * draws them again instead of keeping a mask.
+ *  rng   device uint64[2]: seed and step, read when the kernel runs, so that a
+ *        captured graph draws new bits when the caller advances the step. 8-byte aligned.
+ *  site  tells the calls of one step apart (a layer's number, say).
+ * With a probability p the element is kept when its bits are below
+ * kept = floor((1 - p) * 2^16 + 1/2), and then multiplied by 2^16 / kept, so the
+ * expectation is exact for the probability that 16 bits can hold. What is dropped is 0,
+ * whatever it was, infinities and NaN included. */
+
+/* dst = dropout of src, row by row; also the gradient, with the same rng and site.
+ *  src, dst   device [rows][row_elems], both in `order`. dst may be src; else
+ *             they must not overlap. Padding rows of LOCAL are written as zeros.
+ *  row_elems  a multiple of 16 bytes.
+ *  p          0..1; rng may be NULL when it is 0.
+ *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS,
+ *  CPT_ERR_CUDA. */
+CPT_API cpt_status cpt_dropout(const cpt_plan *plan, const void *src, void *dst, int64_t row_elems,
+                               cpt_dtype dtype, cpt_order order, double p, const uint64_t *rng,
+                               uint32_t site, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* The residual stream between two blocks                              */
+/* ------------------------------------------------------------------ */
+
+/* What a gate multiplies: nothing, every token's own row (in the call's order),
+ * or one row for all tokens of a document. */
+typedef enum cpt_gate { CPT_GATE_NONE = 0, CPT_GATE_TOKEN = 1, CPT_GATE_DOCUMENT = 2 } cpt_gate;
+
+/* Largest row_elems of cpt_residual_norm. */
+#define CPT_RESIDUAL_MAX_ROW 8192
+
+/* The options that cpt_residual_norm and its gradient share. */
+typedef struct cpt_residual {
+    const float *post_weight; /* device [row_elems]: weight of the block's own norm; NULL: no such norm */
+    const float *pre_weight;  /* device [row_elems]: weight of the next block's norm; NULL: no such norm */
+    const void *gate;         /* device [rows][row_elems] or [n_docs][row_elems], of the call's dtype */
+    cpt_gate gate_kind;
+    float scale;              /* of the branch; finite */
+    float eps;                /* added to the mean square; finite, >= 0 */
+    double p;                 /* dropout of the branch, as cpt_dropout; 0: none */
+    const uint64_t *rng;      /* may be NULL when p is 0 */
+    uint32_t site;
+} cpt_residual;
+
+/* The end of one block and the beginning of the next, in one pass:
+ *   b = norm(h) * post_weight (or h),  b = b * gate,  y = x + scale * dropout(b),
+ *   n = norm(y) * pre_weight,  norm(v) = v / sqrt(mean(v^2) + eps) over the row.
+ *  x      device, the residual stream.
+ *  h      device, the block's output; NULL before the first block: then y = x,
+ *         y must be NULL too, and post_weight, gate and p are not allowed.
+ *  y      device, the new residual stream; may be x.
+ *  n      device, the next block's input; NULL exactly when pre_weight is.
+ *  row_elems  at most CPT_RESIDUAL_MAX_ROW, a multiple of 16 bytes. x, h, y, n and
+ *         gate are of one dtype.
+ *  Arithmetic is binary32; y and n are rounded once each, n from the y before its
+ *  rounding. Padding rows of LOCAL are written as zeros and not used.
+ *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (row_elems), CPT_ERR_DEVICE,
+ *  CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS, CPT_ERR_CUDA. */
+CPT_API cpt_status cpt_residual_norm(const cpt_plan *plan, const void *x, const void *h, void *y, void *n,
+                                     int64_t row_elems, cpt_dtype dtype, cpt_order order,
+                                     const cpt_residual *options, void *stream);
+
+/* Device workspace bytes of cpt_residual_norm_backward on the current device, or 0
+ * for a NULL plan or a row that it refuses. */
+CPT_API size_t cpt_residual_norm_backward_workspace_bytes(const cpt_plan *plan, int64_t row_elems,
+                                                          cpt_dtype dtype);
+
+/* Gradient of cpt_residual_norm.
+ *  h      its input (NULL as there); not read, and may be NULL, when there is neither a
+ *         post_weight nor a gate, though dh is given.
+ *  y      its result (x where h is NULL there); NULL exactly when pre_weight is.
+ *  dy     the gradient that comes down the residual stream; NULL: none.
+ *  dn     the gradient of n; NULL exactly when pre_weight is.
+ *  dx     the gradient of x, which is the whole gradient of y. May be dy.
+ *  dh     the gradient of h; NULL where there is no block.
+ *  dgate  the gradient of the gate: of the call's dtype for a token's, float32 sums
+ *         over the tokens for a document's (zeros for a document without any). NULL
+ *         exactly when there is no gate.
+ *  dpost_weight, dpre_weight  float32 [row_elems], sums over all tokens; NULL exactly
+ *         when the weight is. Overwritten, like every output.
+ *  workspace  device, 256-byte aligned, needed until the stream has passed the call.
+ *         Calls that may run at the same time (two streams, two graphs) need one each.
+ *  The norms are computed again from h and y. Sums are binary32 in a fixed order: a
+ *  repeated call gives the same bits. Padding rows of dx, dh and a token's dgate are
+ *  zeros; those of inputs are not used.
+ *  Errors: as cpt_residual_norm, and CPT_ERR_WORKSPACE. */
+CPT_API cpt_status cpt_residual_norm_backward(const cpt_plan *plan, const void *h, const void *y, const void *dy,
+                                              const void *dn, void *dx, void *dh, void *dgate, float *dpost_weight,
+                                              float *dpre_weight, int64_t row_elems, cpt_dtype dtype,
+                                              cpt_order order, const cpt_residual *options, void *workspace,
+                                              size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------ */
+/* Losses                                                              */
+/* ------------------------------------------------------------------ */
+
+/* The logarithm of the probability that every token's logits give to its target:
+ *   logp[g] = scale * (x[target] - m) - l,  m = max x,  l = log sum exp(scale * (x - m))
+ * over the first `vocab` of the row's columns.
+ *  logits   device [rows][vocab_padded] in `order`; rows a multiple of 16 bytes. Columns
+ *           from vocab on are not used.
+ *  targets  device int32[T], raw global order. A target outside 0..vocab-1 is none:
+ *           the row is not read and logp and stats are 0.
+ *  scale    finite, positive: one over the temperature.
+ *  logp     device float32[T], raw global order.
+ *  stats    device float32[T][2], 8-byte aligned: m and l, for the gradient. The
+ *           logarithm of the row's sum is scale * m + l.
+ *  A row with no logit above -inf, with +inf or with NaN gives a NaN logp. Sums are
+ *  binary32 in a fixed order.
+ *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS,
+ *  CPT_ERR_CUDA. */
+CPT_API cpt_status cpt_token_logprob(const cpt_plan *plan, const void *logits, const int32_t *targets, float *logp,
+                                     float *stats, int64_t vocab, int64_t vocab_padded, cpt_dtype dtype,
+                                     cpt_order order, float scale, void *stream);
+
+/* Gradient of cpt_token_logprob:
+ *   dlogits[row][j] = dlogp[g] * scale * ([j = target] - exp(scale * (x[j] - m) - l)).
+ *  dlogp    device float32[T], raw global order. Where it is 0, where there is no
+ *           target, in padding rows and in columns from vocab on, dlogits is 0
+ *           and the logits are not read.
+ *  dlogits  device, like logits; may be logits.
+ *  Other arguments and errors: as cpt_token_logprob. */
+CPT_API cpt_status cpt_token_logprob_backward(const cpt_plan *plan, const void *logits, const int32_t *targets,
+                                              const float *stats, const float *dlogp, void *dlogits, int64_t vocab,
+                                              int64_t vocab_padded, cpt_dtype dtype, cpt_order order, float scale,
+                                              void *stream);
+
+/* A clipped policy loss with a KL term over the plan's documents, and its gradient.
+ * With r = exp(logp - logp_old), A the document's advantage, e = logp_ref - logp:
+ *   each token:    max(-A r, -A clip(r, 1 - clip_low, 1 + clip_high))
+ *                    + kl_coef * (exp(e) - e - 1)
+ *   document d:    L_d = the mean over its tokens with a mask (0 when there are none)
+ *   dlogp = the gradient of sum_d weights[d] * L_d (0 in tokens without a mask).
+ *  logp, logp_old, logp_ref, dlogp  device float32[T], raw global order. logp_ref may
+ *             be NULL: no KL term (kl_coef must be 0).
+ *  mask       device uint8[T], 0 for tokens that do not count (their other values
+ *             are not used); NULL: all count.
+ *  advantages, weights  device float32[n_docs]; weights NULL: 1 / n_docs each.
+ *  clip_low   0..1.  clip_high, kl_coef  0..1e30.
+ *  terms      device float32[n_docs][4]: L_d, the mean KL term, the share of tokens
+ *             whose ratio is held by the clip, the number of tokens that count. 16-byte aligned.
+ *  On which side of a border a ratio lies is settled without rounding logp - logp_old.
+ *  Sums are binary32 in a fixed order.
+ *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS,
+ *  CPT_ERR_CUDA. */
+CPT_API cpt_status cpt_policy_loss(const cpt_plan *plan, const float *logp, const float *logp_old,
+                                   const float *logp_ref, const uint8_t *mask, const float *advantages,
+                                   const float *weights, double clip_low, double clip_high, double kl_coef,
+                                   float *terms, float *dlogp, void *stream);
 
 /* ------------------------------------------------------------------ */
 /* Measurement                                                         */
