@@ -1109,15 +1109,16 @@ cpt_status cpt_kernel_wait_timeouts(uint32_t *count, int32_t reset)
     if (count == nullptr) return fail(CPT_ERR_INVALID_ARG, "NULL argument");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0, u = 0;
+    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0, u = 0, s = 0;
     cudaError_t e = read_wait_timeouts(&v, reset != 0);
     if (e == cudaSuccess) e = read_slot_reduce_wait_timeouts(&w, reset != 0);
     if (e == cudaSuccess) e = read_gather_wait_timeouts(&x, reset != 0);
     if (e == cudaSuccess) e = read_ceiling_wait_timeouts(&y, reset != 0);
     if (e == cudaSuccess) e = read_attention_wait_timeouts(&z, reset != 0);
     if (e == cudaSuccess) e = read_attention_backward_wait_timeouts(&u, reset != 0);
+    if (e == cudaSuccess) e = read_residual_wait_timeouts(&s, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "wait-timeout counter read");
-    *count = v + w + x + y + z + u;
+    *count = v + w + x + y + z + u + s;
     return CPT_OK;
 }
 
@@ -1559,6 +1560,10 @@ cpt_status drop_rule(double p, const uint64_t *rng, uint32_t site, float scale, 
     if (rng == nullptr) return fail(CPT_ERR_INVALID_ARG, "rng is NULL");
     out->rng = rng;
     out->kept = static_cast<uint32_t>(std::floor((1.0 - p) * 65536.0 + 0.5));
+    if (out->kept == 65536) {   // nothing to drop at 16 bits
+        out->rng = nullptr;
+        return CPT_OK;
+    }
     out->factor = out->kept == 0 ? 0.0f : static_cast<float>(65536.0 / out->kept * scale);
     return CPT_OK;
 }
@@ -1711,7 +1716,7 @@ cpt_status cpt_residual_norm(const cpt_plan *plan, const void *x, const void *h,
     p.h = static_cast<const uint8_t *>(h);
     p.y = static_cast<uint8_t *>(y);
     p.n = static_cast<uint8_t *>(n);
-    const cudaError_t e = launch_residual_norm(p, dtype, static_cast<cudaStream_t>(stream));
+    const cudaError_t e = launch_residual_norm(p, dtype, dev, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? CPT_OK : cuda_fail(e, "residual norm launch");
 }
 

@@ -230,10 +230,12 @@ struct ResidualParams {
     float *part_post, *part_pre;       // [CTAs][row_elems]
     float *part_gate;                  // [groups][2][row_elems]: of a document begun earlier, of one that goes on
     int32_t parts;
+    int32_t tensors, stages;           // of a ring
 };
-cudaError_t launch_residual_norm(ResidualParams p, int dtype, cudaStream_t stream);
+cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaStream_t stream);
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device);
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream);
+cudaError_t read_residual_wait_timeouts(unsigned int *count, bool reset);
 
 // Log-probabilities of targets, and their gradient.
 struct LogprobParams {

@@ -20,7 +20,8 @@ constexpr int kUnroll = 4;
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
 {
-    constexpr int E = Unit<BF16>::E;
+    constexpr int N = UnitPairs<BF16>::N;
+    const F2 factor = pair_of(p.rule.factor, p.rule.factor);
     DropKey key;
     key.load(p.rule);
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
@@ -52,15 +53,18 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
         for (int k = 0; k < kUnroll; ++k) {
             const int64_t j = i + k * stride;
             if (j >= items) continue;
-            float x[E];
-            Unit<BF16>::unpack(raw[k], x);
+            uint4 out = raw[k];
             if (token[k] < 0) {   // padding
-#pragma unroll
-                for (int e = 0; e < E; ++e) x[e] = 0.0f;
+                out = make_uint4(0, 0, 0, 0);
             } else if (p.rule.rng != nullptr) {
+                F2 x[N];
+                UnitPairs<BF16>::unpack(raw[k], x);
                 drop_unit<BF16>(p.rule, key, static_cast<uint32_t>(token[k]), at[k], x);
+#pragma unroll
+                for (int n = 0; n < N; ++n) x[n] = mul2(x[n], factor);
+                out = UnitPairs<BF16>::pack(x);
             }
-            __stcs(reinterpret_cast<uint4 *>(p.dst) + j, Unit<BF16>::pack(x));
+            __stcs(reinterpret_cast<uint4 *>(p.dst) + j, out);
         }
     }
 }

@@ -57,13 +57,13 @@ struct LongSum {
 
 __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_constant__ PolicyParams p)
 {
-    __shared__ float room[2 * kSumRoom];
-    int turn = 0;
+    __shared__ __align__(16) float room[256];
+    BlockSum sum(room);
     for (int64_t d = blockIdx.x; d < p.n_docs; d += gridDim.x) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
         const float A = p.advantages[d];
         // counted in whole numbers, in two floats of 2^24 each: exact for any length
-        float n[2] = {0.0f, 0.0f};
+        float n[3] = {0.0f, 0.0f, 0.0f};
         if (p.mask == nullptr) {
             n[0] = static_cast<float>(hi - lo);
         } else {
@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
             for (int64_t t = lo + threadIdx.x; t < hi; t += kThreads) mine += p.mask[t] != 0;
             n[0] = static_cast<float>(mine & 0xFFF);
             n[1] = static_cast<float>(mine >> 12);
-            block_sum<2>(n, room, turn);
+            sum(n);
             n[0] = __fmaf_rn(n[1], 4096.0f, n[0]);
         }
         const float share = __fdiv_rn(1.0f, fmaxf(n[0], 1.0f));
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
             p.dlogp[t] = g;
         }
         float s[3] = {loss.value(), kl.value(), static_cast<float>(held_count)};
-        block_sum<3>(s, room, turn);
+        sum(s);
         if (threadIdx.x == 0)
             p.terms[d] = make_float4(__fmul_rn(__fmaf_rn(p.kl, s[1], s[0]), share), __fmul_rn(s[1], share),
                                      __fmul_rn(s[2], share), n[0]);

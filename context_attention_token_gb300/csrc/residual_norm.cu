@@ -19,11 +19,17 @@
 #include "cpt_internal.h"
 #include "token_rows.cuh"
 
+#include <mutex>
+
 namespace cpt {
 
 namespace {
 
-constexpr int kSubThreads = 128;
+constexpr int kShortThreads = 128;
+constexpr int kLongThreads = 512;     // at most, so a thread has 128 registers
+constexpr int kMaxStages = 8;
+constexpr int kSharedBytes = 227 * 1024;   // of an SM
+constexpr int kOwnBytes = 2560;            // of a CTA, besides its ring
 constexpr int kGateToken = 1, kGateDocument = 2;
 
 // How rows of so many units are dealt to threads.
@@ -31,28 +37,34 @@ struct Shape {
     int group;        // threads of a row
     int per_thread;   // units of a thread
     int threads;      // of a CTA
-    int ctas_per_sm;  // of the gradient
-    bool sub;         // several rows a warp or CTA
+    int ctas_per_sm;
+    bool shorter;     // several rows a CTA
 };
 
-Shape shape_of(int units)
+Shape shape_of(int units, int dtype)
 {
     Shape s;
-    if (units <= 64) {
-        s.sub = true;
+    s.shorter = units <= 64;
+    if (s.shorter) {
         s.per_thread = units > 32 ? 2 : 1;
         s.group = 1;
         while (s.group * s.per_thread < units) s.group *= 2;
-        s.threads = kSubThreads;
-        s.ctas_per_sm = 6;
+        s.threads = kShortThreads;
+        s.ctas_per_sm = s.per_thread == 1 ? 4 : 2;
         return s;
     }
-    s.sub = false;
-    s.per_thread = units > 1024 ? 2 : 1;
+    s.per_thread = dtype == kBf16 ? 2 : 4;   // 16 columns
     s.group = ((units + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
     s.threads = s.group;
-    s.ctas_per_sm = s.group >= 512 ? 1 : 1024 / s.group < 8 ? 1024 / s.group : 8;
+    s.ctas_per_sm = kLongThreads / s.group;
     return s;
+}
+
+// Rows that a ring holds.
+int stages_of(const Shape &s, int64_t stage_bytes)
+{
+    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes) / stage_bytes;
+    return static_cast<int>(n < 1 ? 1 : n > kMaxStages ? kMaxStages : n);
 }
 
 // The document of a raw token: the last d with cu[d] <= t.
@@ -65,14 +77,6 @@ __device__ __forceinline__ int document_of(const int32_t *cu, int n, int64_t t)
         else hi = mid;
     }
     return lo;
-}
-
-// Sums of N values over the threads of a row.
-template <bool SUB, int N>
-__device__ __forceinline__ void row_sum(float (&v)[N], int group, float *room, int &turn)
-{
-    if constexpr (SUB) lanes_sum<N>(v, group);
-    else block_sum<N>(v, room, turn);
 }
 
 __device__ __forceinline__ float rsqrt_mean(float sum, float n, float eps)
@@ -110,43 +114,329 @@ __device__ __forceinline__ void store_unit(uint8_t *base, int64_t at, uint4 v)
     __stcs(reinterpret_cast<uint4 *>(base) + at, v);
 }
 
+__device__ __forceinline__ F2 twice(float x) { return pair_of(x, x); }
+
+__device__ __forceinline__ float sum_of(F2 x)
+{
+    const float2 f = both(x);
+    return __fadd_rn(f.x, f.y);
+}
+
+template <int U>
+struct Has {
+    bool at[U];   // whether unit lane + k * group is one of the row
+};
+
+// Weights of a thread's columns, 0 past the row's end.
+template <bool BF16, int U>
+__device__ __forceinline__ void load_weights(const float *w, const Has<U> &has, int lane, int group,
+                                             F2 (&out)[U][Unit<BF16>::E / 2])
+{
+    constexpr int E = Unit<BF16>::E;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        float f[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) f[e] = 0.0f;
+        if (w != nullptr && has.at[k]) load_floats<E>(w + static_cast<int64_t>(lane + k * group) * E, f);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) out[k][e / 2] = pair_of(f[e], f[e + 1]);
+    }
+}
+
+// One row of the forward call. x, h and gate give a unit's data, put_y and put_n take a unit's result, sum adds
+// over the row's threads.
+template <bool BF16, int U, class X, class H, class G, class Sum, class PutY, class PutN>
+__device__ __forceinline__ void forward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
+                                            uint32_t token, const F2 (&w1)[U][Unit<BF16>::E / 2],
+                                            const F2 (&w2)[U][Unit<BF16>::E / 2], X x, H h, G gate, Sum sum, PutY put_y,
+                                            PutN put_n)
+{
+    typedef UnitPairs<BF16> V;
+    constexpr int N = V::N;
+    const float C = static_cast<float>(p.row_elems);
+    F2 u[U][N], y[U][N];
+    float s[1];
+    if (p.post != nullptr) {
+        F2 q = twice(0.0f);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            V::unpack(h(k), u[k]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) q = fma2(u[k][i], u[k][i], q);
+        }
+        s[0] = sum_of(q);
+        sum(s);
+        const F2 r1 = twice(rsqrt_mean(s[0], C, p.eps));
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int i = 0; i < N; ++i) u[k][i] = mul2(mul2(u[k][i], r1), w1[k][i]);
+    } else if (p.h != nullptr) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) V::unpack(h(k), u[k]);
+    }
+    const F2 factor = twice(p.rule.factor);
+    F2 q = twice(0.0f);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        V::unpack(x(k), y[k]);
+        if (p.h != nullptr) {
+            if (p.gate_kind != 0) {
+                F2 g[N];
+                V::unpack(gate(k), g);
+#pragma unroll
+                for (int i = 0; i < N; ++i) u[k][i] = mul2(u[k][i], g[i]);
+            }
+            if (p.rule.rng != nullptr) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, u[k]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[k][i] = fma2(u[k][i], factor, y[k][i]);
+            if (has.at[k]) put_y(k, V::pack(y[k]));
+        }
+        if (has.at[k]) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) q = fma2(y[k][i], y[k][i], q);
+        }
+    }
+    if (p.pre == nullptr) return;
+    s[0] = sum_of(q);
+    sum(s);
+    const F2 r2 = twice(rsqrt_mean(s[0], C, p.eps));
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (!has.at[k]) continue;
+#pragma unroll
+        for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w2[k][i]);
+        put_n(k, V::pack(y[k]));
+    }
+}
+
+// What a thread adds up over its tokens.
+template <bool BF16, int U>
+struct Sums {
+    F2 post[U][Unit<BF16>::E / 2], pre[U][Unit<BF16>::E / 2], gate[U][Unit<BF16>::E / 2];
+};
+
+// One token of the gradient; dy to gate give a unit's data.
+template <bool BF16, int U, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
+__device__ __forceinline__ void backward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
+                                             uint32_t token, const F2 (&w1)[U][Unit<BF16>::E / 2],
+                                             const F2 (&w2)[U][Unit<BF16>::E / 2], Sums<BF16, U> &acc, DY dy, DN dn, Y y,
+                                             H h, G gate, Sum sum, PutX put_x, PutH put_h, PutG put_gate)
+{
+    typedef UnitPairs<BF16> V;
+    constexpr int N = V::N;
+    const float C = static_cast<float>(p.row_elems);
+    const bool post = p.post != nullptr, pre = p.pre != nullptr;
+    float s[3] = {0.0f, 0.0f, 0.0f};   // y^2, dn w2 y, h^2
+    if (pre || post) {
+        F2 q0 = twice(0.0f), q1 = q0, q2 = q0;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (pre) {
+                F2 a[N], b[N];
+                V::unpack(y(k), a);
+                V::unpack(dn(k), b);
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    q0 = fma2(a[i], a[i], q0);
+                    q1 = fma2(mul2(b[i], w2[k][i]), a[i], q1);
+                }
+            }
+            if (post) {
+                F2 a[N];
+                V::unpack(h(k), a);
+#pragma unroll
+                for (int i = 0; i < N; ++i) q2 = fma2(a[i], a[i], q2);
+            }
+        }
+        s[0] = sum_of(q0);
+        s[1] = sum_of(q1);
+        s[2] = sum_of(q2);
+        sum(s);
+    }
+    const float r2 = pre ? rsqrt_mean(s[0], C, p.eps) : 0.0f;
+    const float mean2 = pre ? __fdiv_rn(__fmul_rn(s[1], r2), C) : 0.0f;   // of dn w2 yn
+    const F2 r1 = twice(post ? rsqrt_mean(s[2], C, p.eps) : 1.0f), factor = twice(p.rule.factor);
+    F2 e[U][N], q = twice(0.0f);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        F2 d[N], hn[N];
+        V::unpack(dy(k), d);
+        if (pre) {
+            F2 a[N], b[N];
+            V::unpack(y(k), a);
+            V::unpack(dn(k), b);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const F2 yn = mul2(a[i], twice(r2));
+                acc.pre[k][i] = fma2(b[i], yn, acc.pre[k][i]);
+                d[i] = fma2(twice(r2), fma2(yn, twice(-mean2), mul2(b[i], w2[k][i])), d[i]);
+            }
+        }
+        if (has.at[k]) put_x(k, V::pack(d));
+        if (p.n == nullptr) continue;   // no block
+        if (p.rule.rng != nullptr) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, d);
+#pragma unroll
+        for (int i = 0; i < N; ++i) d[i] = mul2(d[i], factor);
+        if (post || p.gate_kind != 0) {
+            V::unpack(h(k), hn);
+            if (post) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], r1);
+            }
+        }
+        if (p.gate_kind != 0) {
+            F2 g[N], z[N];
+            V::unpack(gate(k), g);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                // what was dropped has no gradient, whatever it is multiplied by
+                const float2 c = both(d[i]), zz = both(mul2(d[i], post ? mul2(hn[i], w1[k][i]) : hn[i])), gg = both(mul2(d[i], g[i]));
+                z[i] = pair_of(c.x == 0.0f ? 0.0f : zz.x, c.y == 0.0f ? 0.0f : zz.y);
+                d[i] = pair_of(c.x == 0.0f ? 0.0f : gg.x, c.y == 0.0f ? 0.0f : gg.y);
+            }
+            if (p.gate_kind == kGateDocument) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
+            } else if (has.at[k]) {
+                put_gate(k, V::pack(z));
+            }
+        }
+        if (post) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
+                e[k][i] = mul2(d[i], w1[k][i]);
+                q = fma2(e[k][i], hn[i], q);
+            }
+        } else if (has.at[k]) {
+            put_h(k, V::pack(d));
+        }
+    }
+    if (!post) return;
+    float t[1] = {sum_of(q)};
+    sum(t);
+    const F2 mean1 = twice(-__fdiv_rn(t[0], C));
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (!has.at[k]) continue;
+        F2 hn[N];
+        V::unpack(h(k), hn);
+#pragma unroll
+        for (int i = 0; i < N; ++i) hn[i] = mul2(r1, fma2(mul2(hn[i], r1), mean1, e[k][i]));
+        put_h(k, V::pack(hn));
+    }
+}
+
+// The document that tokens are in, looked for when it changes.
+struct Document {
+    int at = 0;
+    int64_t lo = 0, hi = -1;   // its tokens
+    __device__ __forceinline__ bool enter(const ResidualParams &p, int64_t token)
+    {
+        if (token >= lo && token < hi) return false;
+        if (token == hi && at + 1 < p.n_docs && p.cu[at + 2] > token) ++at;   // the next one, mostly
+        else at = document_of(p.cu, p.n_docs, token);
+        lo = p.cu[at];
+        hi = p.cu[at + 1];
+        return true;
+    }
+};
+
+// The sum over a token's gate gradients leaves for where it belongs: the result when the document lies in this
+// group's tokens, part 0 when it began earlier, part 1 when it goes on.
+template <bool BF16, int U>
+__device__ __forceinline__ void leave_document(const ResidualParams &p, const Document &doc, int64_t which, int64_t begin,
+                                               int64_t end, const Has<U> &has, int lane, Sums<BF16, U> &acc)
+{
+    constexpr int E = Unit<BF16>::E;
+    float *to = reinterpret_cast<float *>(p.dgate) + static_cast<int64_t>(doc.at) * p.row_elems;
+    if (doc.lo < begin) to = p.part_gate + which * 2 * p.row_elems;
+    else if (doc.hi > end) to = p.part_gate + (which * 2 + 1) * p.row_elems;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        float f[E];
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) {
+            const float2 v = both(acc.gate[k][i]);
+            f[2 * i] = v.x;
+            f[2 * i + 1] = v.y;
+            acc.gate[k][i] = twice(0.0f);
+        }
+        if (has.at[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, f);
+    }
+}
+
+template <int E>
+__device__ __forceinline__ void spread(const F2 (&x)[E / 2], float (&f)[E])
+{
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i) {
+        const float2 v = both(x[i]);
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+}
+
+// Padding rows of the outputs, this CTA's share of all rows.
+template <int U>
+__device__ __forceinline__ void zero_padding(const ResidualParams &p, const Has<U> &has, int lane, int first, int step)
+{
+    if (p.token_of_row == nullptr || p.rows == p.T) return;
+    const int64_t share = (p.rows + gridDim.x - 1) / gridDim.x;
+    const int64_t last = min(static_cast<int64_t>(blockIdx.x + 1) * share, p.rows);
+    for (int64_t row = blockIdx.x * share + first; row < last; row += step) {
+        if (p.token_of_row[row] >= 0) continue;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            if (!has.at[k]) continue;
+            const int64_t at = row * p.units + lane + k * p.group;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            store_unit(p.y, at, zero);
+            if (p.n != nullptr) store_unit(p.n, at, zero);
+            if (p.gate_kind == kGateToken) store_unit(p.dgate, at, zero);
+        }
+    }
+}
+
+// ----------------------------------------------------------------- short rows: a part of a warp each
+
 // A row's data as it was loaded.
 template <int U>
-struct ForwardRaw {
-    uint4 x[U], h[U], gate[U];
+struct ShortRaw {
+    uint4 t[5][U];   // forward: x, h, gate; gradient: dy, dn, y, h, gate
+    int64_t row;
     int32_t token;
 };
 
-template <bool BF16, int U, bool SUB, int MAXT>
-__global__ void __launch_bounds__(MAXT) residual_norm_kernel(const __grid_constant__ ResidualParams p)
+template <int N>
+struct LanesSum {
+    int group;
+    __device__ __forceinline__ void operator()(float (&v)[N]) const { lanes_sum<N>(v, group); }
+};
+
+template <bool BF16, int U>
+__global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
-    __shared__ float room[SUB ? 1 : 2 * kSumRoom];
-    int turn = 0;
-    const int lane = SUB ? threadIdx.x % p.group : threadIdx.x;
-    const int64_t which = SUB ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / p.group) + threadIdx.x / p.group
-                              : blockIdx.x;
+    const int lane = threadIdx.x % p.group;
+    const int64_t which = static_cast<int64_t>(blockIdx.x) * (kShortThreads / p.group) + threadIdx.x / p.group;
     const int64_t begin = which * p.per_group;
-    const bool post = p.post != nullptr, pre = p.pre != nullptr, branch = p.h != nullptr;
-    const bool drop = p.rule.rng != nullptr;
-    const float C = static_cast<float>(p.row_elems);
     DropKey key;
     key.load(p.rule);
-    float w1[U][E], w2[U][E];
-    bool has[U];
+    Has<U> has;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int u = lane + k * p.group;
-        has[k] = u < p.units;
-        if (post && has[k]) load_floats<E>(p.post + static_cast<int64_t>(u) * E, w1[k]);
-        if (pre && has[k]) load_floats<E>(p.pre + static_cast<int64_t>(u) * E, w2[k]);
-    }
-    // the document of the current token: doc_lo <= token < doc_hi
-    int doc = 0;
-    int32_t doc_lo = 0, doc_hi = -1;
+    for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    Document doc;
 
-    auto load = [&](int64_t row, ForwardRaw<U> &r) {
+    auto load = [&](int64_t row, ShortRaw<U> &r) {
         r.token = -1;
+#pragma unroll
+        for (int k = 0; k < U; ++k) r.t[0][k] = r.t[1][k] = r.t[2][k] = make_uint4(0, 0, 0, 0);
         if (row >= p.rows) return;
         r.token = p.token_of_row == nullptr ? static_cast<int32_t>(row) : p.token_of_row[row];
         if (r.token >= 0 && !in_bounds(r.token < p.T, lane == 0)) r.token = -1;
@@ -154,152 +444,66 @@ __global__ void __launch_bounds__(MAXT) residual_norm_kernel(const __grid_consta
         const int64_t base = row * p.units + lane;
         int64_t gate_base = base;
         if (p.gate_kind == kGateDocument) {
-            if (r.token < doc_lo || r.token >= doc_hi) {
-                doc = document_of(p.cu, p.n_docs, r.token);
-                doc_lo = p.cu[doc];
-                doc_hi = p.cu[doc + 1];
-            }
-            gate_base = static_cast<int64_t>(doc) * p.units + lane;
+            doc.enter(p, r.token);
+            gate_base = static_cast<int64_t>(doc.at) * p.units + lane;
         }
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (!has[k]) continue;
-            r.x[k] = load_unit(p.x, base + k * p.group);
-            if (branch) r.h[k] = load_unit(p.h, base + k * p.group);
-            if (p.gate_kind == kGateToken) r.gate[k] = load_unit(p.gate, gate_base + k * p.group);
-            else if (p.gate_kind == kGateDocument) r.gate[k] = reinterpret_cast<const uint4 *>(p.gate)[gate_base + k * p.group];
+            if (!has.at[k]) continue;
+            r.t[0][k] = load_unit(p.x, base + k * p.group);
+            if (p.h != nullptr) r.t[1][k] = load_unit(p.h, base + k * p.group);
+            if (p.gate_kind == kGateToken) r.t[2][k] = load_unit(p.gate, base + k * p.group);
+            else if (p.gate_kind == kGateDocument) r.t[2][k] = reinterpret_cast<const uint4 *>(p.gate)[gate_base + k * p.group];
         }
     };
 
-    ForwardRaw<U> next;
+    ShortRaw<U> next;
     load(begin, next);
-    for (int64_t i = 0; i < p.per_group; ++i) {
+    for (int64_t i = 0; i < p.per_group; ++i) {   // as often for every lane of a warp: they share the sums
         const int64_t row = begin + i;
-        if (!SUB && row >= p.rows) break;   // the lanes of a warp go through the same sums
-        const ForwardRaw<U> r = next;
+        const ShortRaw<U> r = next;
         if (i + 1 < p.per_group) load(row + 1, next);
-        const bool real = r.token >= 0;
-        float u[U][E], y[U][E];
-        float s[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) u[k][e] = y[k][e] = 0.0f;
-            if (!has[k] || !real) continue;
-            Unit<BF16>::unpack(r.x[k], y[k]);
-            if (!branch) continue;
-            Unit<BF16>::unpack(r.h[k], u[k]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(u[k][e], u[k][e], s[0]);
-        }
-        if (post) {
-            row_sum<SUB, 1>(s, p.group, room, turn);
-            const float r1 = rsqrt_mean(s[0], C, p.eps);
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-#pragma unroll
-                for (int e = 0; e < E; ++e) u[k][e] = __fmul_rn(__fmul_rn(u[k][e], r1), w1[k][e]);
-        }
-        s[0] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (!has[k]) continue;
-            const int64_t at = row * p.units + lane + k * p.group;
-            if (branch && real) {
-                if (p.gate_kind != 0) {
-                    float g[E];
-                    Unit<BF16>::unpack(r.gate[k], g);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) u[k][e] = __fmul_rn(u[k][e], g[e]);
-                }
-                if (drop) {
-                    drop_unit<BF16>(p.rule, key, r.token, lane + k * p.group, u[k]);
-#pragma unroll
-                    for (int e = 0; e < E; ++e) y[k][e] = __fadd_rn(y[k][e], u[k][e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) y[k][e] = __fmaf_rn(u[k][e], p.scale, y[k][e]);
-                }
-            }
-            if (p.y != nullptr && row < p.rows) store_unit(p.y, at, Unit<BF16>::pack(y[k]));
-#pragma unroll
-            for (int e = 0; e < E; ++e) s[0] = __fmaf_rn(y[k][e], y[k][e], s[0]);
-        }
-        if (pre) {
-            row_sum<SUB, 1>(s, p.group, room, turn);
-            const float r2 = rsqrt_mean(s[0], C, p.eps);
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (!has[k] || row >= p.rows) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) y[k][e] = real ? __fmul_rn(__fmul_rn(y[k][e], r2), w2[k][e]) : 0.0f;
-                store_unit(p.n, row * p.units + lane + k * p.group, Unit<BF16>::pack(y[k]));
-            }
-        }
+        const bool in = row < p.rows, real = r.token >= 0;
+        const int64_t at = row * p.units + lane;
+        forward_row<BF16, U>(
+            p, key, has, lane, static_cast<uint32_t>(r.token), w1, w2, [&](int k) { return r.t[0][k]; },
+            [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, LanesSum<1>{p.group},
+            [&](int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
+            [&](int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
     }
 }
 
-// ----------------------------------------------------------------- gradient
-
-template <int U>
-struct BackwardRaw {
-    uint4 dy[U], dn[U], y[U], h[U], gate[U];
-    int64_t row;
-};
-
-template <bool BF16, int U, bool SUB, int MAXT>
-__global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const __grid_constant__ ResidualParams p)
+template <bool BF16, int U>
+__global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_backward_short_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
-    __shared__ float room[SUB ? 1 : 2 * kSumRoom];
-    int turn = 0;
-    const int lane = SUB ? threadIdx.x % p.group : threadIdx.x;
-    const int groups = SUB ? blockDim.x / p.group : 1;
-    const int64_t which = static_cast<int64_t>(blockIdx.x) * groups + (SUB ? threadIdx.x / p.group : 0);
-    const int64_t begin = which * p.per_group;
-    const int64_t end = min(begin + p.per_group, p.T);
-    const bool post = p.post != nullptr, pre = p.pre != nullptr, branch = p.n != nullptr;   // n: dh
-    const bool drop = p.rule.rng != nullptr, need_h = post || p.gate_kind != 0;
-    const float C = static_cast<float>(p.row_elems);
+    const int lane = threadIdx.x % p.group, groups = kShortThreads / p.group;
+    const int64_t which = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / p.group;
+    const int64_t begin = which * p.per_group, end = min(begin + p.per_group, p.T);
+    const bool need_h = p.post != nullptr || p.gate_kind != 0;
     DropKey key;
     key.load(p.rule);
-    float w1[U][E], w2[U][E], sum1[U][E], sum2[U][E], sumg[U][E];
-    bool has[U];
+    Has<U> has;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int u = lane + k * p.group;
-        has[k] = u < p.units;
+    for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    Sums<BF16, U> acc;
 #pragma unroll
-        for (int e = 0; e < E; ++e) w1[k][e] = w2[k][e] = sum1[k][e] = sum2[k][e] = sumg[k][e] = 0.0f;
-        if (post && has[k]) load_floats<E>(p.post + static_cast<int64_t>(u) * E, w1[k]);
-        if (pre && has[k]) load_floats<E>(p.pre + static_cast<int64_t>(u) * E, w2[k]);
-    }
-
-    // dgate of a document's tokens so far
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
+    Document doc;
     const bool by_document = p.gate_kind == kGateDocument;
-    int doc = 0;
-    int64_t doc_lo = 0, doc_hi = 0;
-    auto enter_document = [&](int64_t t) {
-        doc = document_of(p.cu, p.n_docs, t);
-        doc_lo = p.cu[doc];
-        doc_hi = p.cu[doc + 1];
-    };
-    auto leave_document = [&]() {
-        // whole in this group: the result; begun earlier: part 0; goes on: part 1
-        float *to = reinterpret_cast<float *>(p.dgate) + static_cast<int64_t>(doc) * p.row_elems;
-        if (doc_lo < begin) to = p.part_gate + (which * 2) * p.row_elems;
-        else if (doc_hi > end) to = p.part_gate + (which * 2 + 1) * p.row_elems;
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-            if (has[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, sumg[k]);
-#pragma unroll
-            for (int e = 0; e < E; ++e) sumg[k][e] = 0.0f;
-        }
-    };
-    if (by_document && begin < end) enter_document(begin);
+    if (by_document && begin < end) doc.enter(p, begin);
 
-    auto load = [&](int64_t t, BackwardRaw<U> &r) {
+    auto load = [&](int64_t t, ShortRaw<U> &r) {
         r.row = -1;
+#pragma unroll
+        for (int j = 0; j < 5; ++j)
+#pragma unroll
+            for (int k = 0; k < U; ++k) r.t[j][k] = make_uint4(0, 0, 0, 0);
         if (t >= end) return;
         const int64_t row = p.row_of_token == nullptr ? t : p.row_of_token[t];
         if (!in_bounds(row >= 0 && row < p.rows, lane == 0)) return;
@@ -307,178 +511,316 @@ __global__ void __launch_bounds__(MAXT) residual_norm_backward_kernel(const __gr
         const int64_t base = row * p.units + lane;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (!has[k]) continue;
-            r.dy[k] = p.x != nullptr ? load_unit(p.x, base + k * p.group) : make_uint4(0, 0, 0, 0);
-            if (pre) {
-                r.dn[k] = load_unit(p.dn, base + k * p.group);
-                r.y[k] = load_unit(p.y_in, base + k * p.group);
+            if (!has.at[k]) continue;
+            if (p.x != nullptr) r.t[0][k] = load_unit(p.x, base + k * p.group);
+            if (p.pre != nullptr) {
+                r.t[1][k] = load_unit(p.dn, base + k * p.group);
+                r.t[2][k] = load_unit(p.y_in, base + k * p.group);
             }
-            if (need_h) r.h[k] = load_unit(p.h, base + k * p.group);
-            if (p.gate_kind == kGateToken) r.gate[k] = load_unit(p.gate, base + k * p.group);
+            if (need_h) r.t[3][k] = load_unit(p.h, base + k * p.group);
+            if (p.gate_kind == kGateToken) r.t[4][k] = load_unit(p.gate, base + k * p.group);
         }
     };
 
-    BackwardRaw<U> next;
+    ShortRaw<U> next;
     load(begin, next);
     for (int64_t i = 0; i < p.per_group; ++i) {
         const int64_t t = begin + i;
-        if (!SUB && t >= end) break;
-        const BackwardRaw<U> r = next;
+        ShortRaw<U> r = next;
         if (i + 1 < p.per_group) load(t + 1, next);
         const bool real = r.row >= 0;
-        if (by_document && t < end && t >= doc_hi) {
-            leave_document();
-            enter_document(t);
+        if (by_document && real) {
+            if (t >= doc.hi) {
+                leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
+                doc.enter(p, t);
+            }
+#pragma unroll
+            for (int k = 0; k < U; ++k)
+                if (has.at[k]) r.t[4][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
         }
-        float d[U][E], e1[U][E], hn[U][E];
-        float s[3] = {0.0f, 0.0f, 0.0f};   // y^2, dn w2 y, h^2
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) d[k][e] = hn[k][e] = 0.0f;
-            if (!has[k] || !real) continue;
-            Unit<BF16>::unpack(r.dy[k], d[k]);
-            if (pre) {
-                float y[E], dn[E];
-                Unit<BF16>::unpack(r.y[k], y);
-                Unit<BF16>::unpack(r.dn[k], dn);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    s[0] = __fmaf_rn(y[e], y[e], s[0]);
-                    s[1] = __fmaf_rn(__fmul_rn(dn[e], w2[k][e]), y[e], s[1]);
-                }
-            }
-            if (need_h) {
-                Unit<BF16>::unpack(r.h[k], hn[k]);
-#pragma unroll
-                for (int e = 0; e < E; ++e) s[2] = __fmaf_rn(hn[k][e], hn[k][e], s[2]);
-            }
-        }
-        if (pre || post) row_sum<SUB, 3>(s, p.group, room, turn);
-        const float r1 = rsqrt_mean(s[2], C, p.eps);
-        if (pre) {
-            const float r2 = rsqrt_mean(s[0], C, p.eps);
-            const float mean = __fdiv_rn(__fmul_rn(s[1], r2), C);   // of dn w2 yn
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (!has[k] || !real) continue;
-                float y[E], dn[E];
-                Unit<BF16>::unpack(r.y[k], y);
-                Unit<BF16>::unpack(r.dn[k], dn);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const float yn = __fmul_rn(y[e], r2);
-                    sum2[k][e] = __fmaf_rn(dn[e], yn, sum2[k][e]);
-                    const float c = __fmaf_rn(-yn, mean, __fmul_rn(dn[e], w2[k][e]));
-                    d[k][e] = __fmaf_rn(r2, c, d[k][e]);
-                }
-            }
-        }
-        float q[1] = {0.0f};
-#pragma unroll
-        for (int k = 0; k < U; ++k) {
-#pragma unroll
-            for (int e = 0; e < E; ++e) e1[k][e] = 0.0f;
-            if (!has[k] || !real) continue;
-            const int64_t at = r.row * p.units + lane + k * p.group;
-            store_unit(p.y, at, Unit<BF16>::pack(d[k]));
-            if (!branch) continue;
-            if (drop) {
-                drop_unit<BF16>(p.rule, key, static_cast<uint32_t>(t), lane + k * p.group, d[k]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[k][e] = __fmul_rn(d[k][e], p.scale);
-            }
-            if (post) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) hn[k][e] = __fmul_rn(hn[k][e], r1);
-            }
-            if (p.gate_kind != 0) {
-                float g[E], z[E];
-                if (by_document) Unit<BF16>::unpack(reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc) * p.units + lane + k * p.group], g);
-                else Unit<BF16>::unpack(r.gate[k], g);
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    // what was dropped has no gradient, whatever it is multiplied by
-                    const bool zero = d[k][e] == 0.0f;
-                    z[e] = zero ? 0.0f : __fmul_rn(d[k][e], post ? __fmul_rn(hn[k][e], w1[k][e]) : hn[k][e]);
-                    d[k][e] = zero ? 0.0f : __fmul_rn(d[k][e], g[e]);
-                }
-                if (by_document) {
-#pragma unroll
-                    for (int e = 0; e < E; ++e) sumg[k][e] = __fadd_rn(sumg[k][e], z[e]);
-                } else {
-                    store_unit(p.dgate, at, Unit<BF16>::pack(z));
-                }
-            }
-            if (post) {
-#pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    sum1[k][e] = __fmaf_rn(d[k][e], hn[k][e], sum1[k][e]);
-                    e1[k][e] = __fmul_rn(d[k][e], w1[k][e]);
-                    q[0] = __fmaf_rn(e1[k][e], hn[k][e], q[0]);
-                }
-            } else {
-                store_unit(p.n, at, Unit<BF16>::pack(d[k]));
-            }
-        }
-        if (post) {
-            row_sum<SUB, 1>(q, p.group, room, turn);
-            const float mean = __fdiv_rn(q[0], C);
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (!has[k] || !real) continue;
-#pragma unroll
-                for (int e = 0; e < E; ++e) d[k][e] = __fmul_rn(r1, __fmaf_rn(-hn[k][e], mean, e1[k][e]));
-                store_unit(p.n, r.row * p.units + lane + k * p.group, Unit<BF16>::pack(d[k]));
-            }
-        }
+        const int64_t at = r.row * p.units + lane;
+        struct Sum {
+            int group;
+            __device__ __forceinline__ void operator()(float (&v)[1]) const { lanes_sum<1>(v, group); }
+            __device__ __forceinline__ void operator()(float (&v)[3]) const { lanes_sum<3>(v, group); }
+        };
+        backward_row<BF16, U>(
+            p, key, has, lane, static_cast<uint32_t>(t), w1, w2, acc, [&](int k) { return r.t[0][k]; },
+            [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; },
+            [&](int k) { return r.t[4][k]; }, Sum{p.group},
+            [&](int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
+            [&](int k, uint4 v) { if (real) store_unit(p.n, at + k * p.group, v); },
+            [&](int k, uint4 v) { if (real) store_unit(p.dgate, at + k * p.group, v); });
     }
-    if (by_document && begin < end) leave_document();
+    if (by_document && begin < end) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
 
     // the CTA's part of the weights' gradients, its groups added in order
-    __shared__ float join[SUB ? kSubThreads * U * E : 1];
+    __shared__ float join[kShortThreads * U * E];
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        if (w == 0 ? !post : !pre) continue;
+        if (w == 0 ? p.post == nullptr : p.pre == nullptr) continue;
         float *to = (w == 0 ? p.part_post : p.part_pre) + static_cast<int64_t>(blockIdx.x) * p.row_elems;
-        if constexpr (SUB) {
-            const int row = p.group * U * E;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    join[(threadIdx.x / p.group) * row + (lane + k * p.group) * E + e] = w == 0 ? sum1[k][e] : sum2[k][e];
-            __syncthreads();
-            for (int c = threadIdx.x; c < p.row_elems; c += blockDim.x) {
-                float v = join[c];
-                for (int g = 1; g < groups; ++g) v = __fadd_rn(v, join[g * row + c]);
-                to[c] = v;
-            }
-        } else {
-#pragma unroll
-            for (int k = 0; k < U; ++k)
-                if (has[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, w == 0 ? sum1[k] : sum2[k]);
-        }
-    }
-
-    // padding rows: every CTA zeroes its share
-    if (p.token_of_row == nullptr || p.rows == p.T) return;
-    const int64_t share = (p.rows + gridDim.x - 1) / gridDim.x;
-    const int64_t last = min(static_cast<int64_t>(blockIdx.x + 1) * share, p.rows);
-    for (int64_t row = blockIdx.x * share + (SUB ? threadIdx.x / p.group : 0); row < last; row += groups) {
-        if (p.token_of_row[row] >= 0) continue;
+        const int row = p.group * U * E;
+        __syncthreads();
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            if (!has[k]) continue;
-            const int64_t at = row * p.units + lane + k * p.group;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            store_unit(p.y, at, zero);
-            if (branch) store_unit(p.n, at, zero);
-            if (p.gate_kind == kGateToken) store_unit(p.dgate, at, zero);
+            float f[E];
+            spread<E>(w == 0 ? acc.post[k] : acc.pre[k], f);
+            store_floats<E>(join + (threadIdx.x / p.group) * row + (lane + k * p.group) * E, f);
+        }
+        __syncthreads();
+        for (int c = threadIdx.x; c < p.row_elems; c += kShortThreads) {
+            float v = join[c];
+            for (int g = 1; g < groups; ++g) v = __fadd_rn(v, join[g * row + c]);
+            to[c] = v;
         }
     }
+    zero_padding<U>(p, has, lane, threadIdx.x / p.group, groups);
+}
+
+// ----------------------------------------------------------------- long rows: a CTA each
+
+// A ring of rows in shared memory. Thread 0 has the bulk-copy engine fetch the rows of all input tensors, one
+// instruction a row, `stages` rows ahead.
+struct Ring {
+    uint8_t *smem;
+    uint64_t *full;
+    int stages;
+    uint32_t row_bytes, stage_bytes;
+    int slot = 0;
+    uint32_t phase = 0;
+
+    __device__ __forceinline__ const uint4 *row(int tensor) const
+    {
+        return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes + tensor * row_bytes);
+    }
+    __device__ __forceinline__ void advance()
+    {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
+    }
+};
+
+__device__ unsigned int g_wait_timeouts;
+
+// Waits for what thread 0 still has in flight, so that no copy ends in another CTA's shared memory.
+__device__ __forceinline__ void drain(Ring ring, int64_t waited, int64_t issued)
+{
+    for (int64_t i = waited; i < issued; ++i) {
+        mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+        ring.advance();
+    }
+}
+
+// Runs `row(t)` for t in [begin, end) with its data in the ring. `fetch(t, bytes at a stage, barrier)` issues a row's copies
+// and announces their bytes; it is called by thread 0, in order.
+template <class Fetch, class Row>
+__device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fetch fetch, Row row)
+{
+    int64_t issued = begin;
+    int put = 0;
+    auto issue = [&]() {
+        if (threadIdx.x == 0 && issued < end) {
+            fetch(issued, ring.smem + put * ring.stage_bytes, &ring.full[put]);
+        }
+        ++issued;
+        if (++put == ring.stages) put = 0;
+    };
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < ring.stages; ++s) mbar_init(&ring.full[s], 1);
+        mbar_init_fence();
+    }
+    __syncthreads();
+    for (int s = 0; s < ring.stages; ++s) issue();
+    for (int64_t t = begin; t < end; ++t) {
+        const bool ok = mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+        // every thread is done with the row before, whose place is filled again
+        if (__syncthreads_or(!ok)) {
+            if (threadIdx.x == 0) {
+                atomicAdd(&g_wait_timeouts, 1u);
+                drain(ring, t, min(issued, end));
+            }
+            return;
+        }
+        if (ring.stages > 1 && t > begin) issue();
+        row(t);
+        ring.advance();
+        if (ring.stages == 1) {
+            __syncthreads();
+            issue();
+        }
+    }
+}
+
+template <bool BF16, int U>
+__global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
+{
+    constexpr int E = Unit<BF16>::E;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float room[256];
+    __shared__ __align__(8) uint64_t full[kMaxStages];
+    __shared__ int32_t tokens[kMaxStages];
+    const int lane = threadIdx.x;
+    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.rows);
+    DropKey key;
+    key.load(p.rule);
+    Has<U> has;
+#pragma unroll
+    for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    Document doc;
+    BlockSum sum(room);
+    uint4 gate[U];
+    const uint32_t row_bytes = p.units * 16u;
+    Ring ring = {smem, full, p.stages, row_bytes, row_bytes * p.tensors};
+
+    auto token_of = [&](int64_t row) {
+        int32_t t = -1;
+        if (row < end) t = p.token_of_row == nullptr ? static_cast<int32_t>(row) : p.token_of_row[row];
+        return t >= 0 && in_bounds(t < p.T) ? t : -1;
+    };
+    int32_t ahead = threadIdx.x == 0 ? token_of(begin) : -1;   // looked up a row early
+    auto fetch = [&](int64_t row, uint8_t *to, uint64_t *bar) {
+        const int32_t token = ahead;
+        ahead = token_of(row + 1);
+        tokens[bar - full] = token;
+        if (token < 0) {   // padding is not read
+            mbar_expect_tx(bar, 0);
+            return;
+        }
+        mbar_expect_tx(bar, ring.stage_bytes);
+        const int64_t at = row * row_bytes;
+        bulk_load(to, p.x + at, row_bytes, bar);
+        if (p.h != nullptr) bulk_load(to + row_bytes, p.h + at, row_bytes, bar);
+        if (p.gate_kind == kGateToken) bulk_load(to + 2 * row_bytes, p.gate + at, row_bytes, bar);
+    };
+    walk(ring, begin, end, fetch, [&](int64_t row) {
+        const int32_t token = tokens[ring.slot];
+        const int64_t at = row * p.units + lane;
+        if (token < 0) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (!has.at[k]) continue;
+                if (p.y != nullptr) store_unit(p.y, at + k * p.group, make_uint4(0, 0, 0, 0));
+                if (p.n != nullptr) store_unit(p.n, at + k * p.group, make_uint4(0, 0, 0, 0));
+            }
+            return;
+        }
+        if (p.gate_kind == kGateDocument && doc.enter(p, token)) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                gate[k] = make_uint4(0, 0, 0, 0);
+                if (has.at[k]) gate[k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
+            }
+        }
+        auto from = [&](int tensor, int k) {
+            return has.at[k] ? ring.row(tensor)[lane + k * p.group] : make_uint4(0, 0, 0, 0);
+        };
+        forward_row<BF16, U>(
+            p, key, has, lane, static_cast<uint32_t>(token), w1, w2, [&](int k) { return from(0, k); },
+            [&](int k) { return from(1, k); }, [&](int k) { return p.gate_kind == kGateToken ? from(2, k) : gate[k]; },
+            [&](float (&v)[1]) { sum(v); }, [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
+            [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); });
+    });
+}
+
+template <bool BF16, int U>
+__global__ void __launch_bounds__(kLongThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
+{
+    constexpr int E = Unit<BF16>::E;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(16) float room[256];
+    __shared__ __align__(8) uint64_t full[kMaxStages];
+    __shared__ int32_t rows[kMaxStages];
+    const int lane = threadIdx.x;
+    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.T);
+    const bool need_h = p.post != nullptr || p.gate_kind != 0, pre = p.pre != nullptr;
+    DropKey key;
+    key.load(p.rule);
+    Has<U> has;
+#pragma unroll
+    for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    Sums<BF16, U> acc;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
+    const bool by_document = p.gate_kind == kGateDocument;
+    Document doc;
+    BlockSum sum(room);
+    const uint32_t row_bytes = p.units * 16u;
+    Ring ring = {smem, full, p.stages, row_bytes, row_bytes * p.tensors};
+    // places of the tensors in a stage
+    const int at_dn = p.x != nullptr, at_y = at_dn + pre, at_h = at_y + pre, at_gate = at_h + need_h;
+
+    auto row_of = [&](int64_t t) {
+        int64_t row = -1;
+        if (t < end) row = p.row_of_token == nullptr ? t : p.row_of_token[t];
+        return static_cast<int32_t>(row >= 0 && in_bounds(row < p.rows) ? row : -1);
+    };
+    int32_t ahead = threadIdx.x == 0 ? row_of(begin) : -1;   // looked up a token early
+    auto fetch = [&](int64_t t, uint8_t *to, uint64_t *bar) {
+        const int32_t row = ahead;
+        ahead = row_of(t + 1);
+        rows[bar - full] = row;
+        if (row < 0) {
+            mbar_expect_tx(bar, 0);
+            return;
+        }
+        mbar_expect_tx(bar, ring.stage_bytes);
+        const int64_t at = static_cast<int64_t>(row) * row_bytes;
+        if (p.x != nullptr) bulk_load(to, p.x + at, row_bytes, bar);
+        if (pre) {
+            bulk_load(to + at_dn * row_bytes, p.dn + at, row_bytes, bar);
+            bulk_load(to + at_y * row_bytes, p.y_in + at, row_bytes, bar);
+        }
+        if (need_h) bulk_load(to + at_h * row_bytes, p.h + at, row_bytes, bar);
+        if (p.gate_kind == kGateToken) bulk_load(to + at_gate * row_bytes, p.gate + at, row_bytes, bar);
+    };
+    walk(ring, begin, end, fetch, [&](int64_t t) {
+        const int32_t row = rows[ring.slot];
+        if (row < 0) return;
+        if (by_document) {
+            if (t > begin && t >= doc.hi) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+            doc.enter(p, t);
+        }
+        const int64_t at = static_cast<int64_t>(row) * p.units + lane;
+        auto from = [&](int tensor, int k) {
+            return has.at[k] ? ring.row(tensor)[lane + k * p.group] : make_uint4(0, 0, 0, 0);
+        };
+        auto document_gate = [&](int k) {
+            return has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group]
+                             : make_uint4(0, 0, 0, 0);
+        };
+        backward_row<BF16, U>(
+            p, key, has, lane, static_cast<uint32_t>(t), w1, w2, acc,
+            [&](int k) { return p.x != nullptr ? from(0, k) : make_uint4(0, 0, 0, 0); }, [&](int k) { return from(at_dn, k); },
+            [&](int k) { return from(at_y, k); }, [&](int k) { return from(at_h, k); },
+            [&](int k) { return by_document ? document_gate(k) : from(at_gate, k); }, [&](auto &v) { sum(v); },
+            [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
+            [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); },
+            [&](int k, uint4 v) { store_unit(p.dgate, at + k * p.group, v); });
+    });
+    if (by_document && begin < end) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+        if (w == 0 ? p.post == nullptr : p.pre == nullptr) continue;
+        float *to = (w == 0 ? p.part_post : p.part_pre) + static_cast<int64_t>(blockIdx.x) * p.row_elems;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            float f[E];
+            spread<E>(w == 0 ? acc.post[k] : acc.pre[k], f);
+            if (has.at[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, f);
+        }
+    }
+    zero_padding<U>(p, has, lane, 0, 1);
 }
 
 // Adds the parts: blockIdx.y 0 and 1 the weights', one warp every 32nd part; the others the documents that
@@ -523,42 +865,55 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
     }
 }
 
-template <bool BF16>
-cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned grid, cudaStream_t stream)
-{
-    if (s.sub) {
-        if (s.per_thread == 1) residual_norm_kernel<BF16, 1, true, kSubThreads><<<grid, s.threads, 0, stream>>>(p);
-        else residual_norm_kernel<BF16, 2, true, kSubThreads><<<grid, s.threads, 0, stream>>>(p);
-    } else if (s.per_thread == 1) {
-        if (s.threads <= 512) residual_norm_kernel<BF16, 1, false, 512><<<grid, s.threads, 0, stream>>>(p);
-        else residual_norm_kernel<BF16, 1, false, 1024><<<grid, s.threads, 0, stream>>>(p);
-    } else {
-        residual_norm_kernel<BF16, 2, false, 1024><<<grid, s.threads, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
-}
-
-template <bool BF16>
-cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned grid, cudaStream_t stream)
-{
-    if (s.sub) {
-        if (s.per_thread == 1) residual_norm_backward_kernel<BF16, 1, true, kSubThreads><<<grid, s.threads, 0, stream>>>(p);
-        else residual_norm_backward_kernel<BF16, 2, true, kSubThreads><<<grid, s.threads, 0, stream>>>(p);
-    } else if (s.per_thread == 1) {
-        if (s.threads <= 512) residual_norm_backward_kernel<BF16, 1, false, 512><<<grid, s.threads, 0, stream>>>(p);
-        else residual_norm_backward_kernel<BF16, 1, false, 1024><<<grid, s.threads, 0, stream>>>(p);
-    } else {
-        residual_norm_backward_kernel<BF16, 2, false, 1024><<<grid, s.threads, 0, stream>>>(p);
-    }
-    return cudaGetLastError();
-}
-
 int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems * (dtype == kBf16 ? 2 : 4) / 16); }
+
+// A kernel's limit of dynamic shared memory, raised once on each device.
+template <auto kernel>
+cudaError_t allow_shared(int device)
+{
+    static std::mutex mu;
+    static bool done[64] = {false};
+    std::lock_guard<std::mutex> lock(mu);
+    if (device >= 0 && device < 64 && done[device]) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - kOwnBytes);
+    if (e == cudaSuccess && device >= 0 && device < 64) done[device] = true;
+    return e;
+}
+
+template <bool BF16>
+cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned grid, int device, cudaStream_t stream)
+{
+    if (s.shorter) {
+        if (s.per_thread == 1) residual_norm_short_kernel<BF16, 1><<<grid, s.threads, 0, stream>>>(p);
+        else residual_norm_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    constexpr int U = BF16 ? 2 : 4;
+    const cudaError_t e = allow_shared<residual_norm_long_kernel<BF16, U>>(device);
+    if (e != cudaSuccess) return e;
+    residual_norm_long_kernel<BF16, U><<<grid, s.threads, static_cast<size_t>(p.stages) * p.tensors * p.units * 16, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <bool BF16>
+cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned grid, int device, cudaStream_t stream)
+{
+    if (s.shorter) {
+        if (s.per_thread == 1) residual_norm_backward_short_kernel<BF16, 1><<<grid, s.threads, 0, stream>>>(p);
+        else residual_norm_backward_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    constexpr int U = BF16 ? 2 : 4;
+    const cudaError_t e = allow_shared<residual_norm_backward_long_kernel<BF16, U>>(device);
+    if (e != cudaSuccess) return e;
+    residual_norm_backward_long_kernel<BF16, U><<<grid, s.threads, static_cast<size_t>(p.stages) * p.tensors * p.units * 16, stream>>>(p);
+    return cudaGetLastError();
+}
 
 // Tokens of a group of the gradient, and its CTAs.
 void deal(int64_t T, const Shape &s, int device, int64_t &per_group, int64_t &ctas)
 {
-    const int64_t groups = s.sub ? s.threads / s.group : 1;
+    const int64_t groups = s.threads / s.group;
     const int64_t most = static_cast<int64_t>(sm_count(device)) * s.ctas_per_sm * groups;
     per_group = (T + most - 1) / most;
     if (per_group < 1) per_group = 1;
@@ -567,35 +922,41 @@ void deal(int64_t T, const Shape &s, int device, int64_t &per_group, int64_t &ct
 
 }  // namespace
 
-cudaError_t launch_residual_norm(ResidualParams p, int dtype, cudaStream_t stream)
+cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaStream_t stream)
 {
     if (p.rows == 0) return cudaSuccess;
     p.units = row_units(p.row_elems, dtype);
-    const Shape s = shape_of(p.units);
-    const int64_t groups = s.sub ? s.threads / s.group : 1;
+    const Shape s = shape_of(p.units, dtype);
     p.group = s.group;
-    // rows of a group: enough to fetch ahead, few enough that all SMs get some
-    const int64_t even = p.rows / (static_cast<int64_t>(sm_count(-1)) * 8 * groups);
-    p.per_group = even < 1 ? 1 : even > 16 ? 16 : even;
-    const int64_t ctas = (p.rows + p.per_group * groups - 1) / (p.per_group * groups);
+    int64_t ctas;
+    if (s.shorter) {
+        // rows of a group: enough to fetch ahead, few enough that all SMs get some
+        const int64_t groups = s.threads / s.group;
+        const int64_t even = p.rows / (static_cast<int64_t>(sm_count(device)) * 8 * groups);
+        p.per_group = even < 1 ? 1 : even > 16 ? 16 : even;
+        ctas = (p.rows + p.per_group * groups - 1) / (p.per_group * groups);
+    } else {
+        deal(p.rows, s, device, p.per_group, ctas);
+        p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
+        p.stages = stages_of(s, static_cast<int64_t>(p.tensors) * p.units * 16);
+    }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
-    return dtype == kBf16 ? launch_forward<true>(p, s, grid, stream) : launch_forward<false>(p, s, grid, stream);
+    return dtype == kBf16 ? launch_forward<true>(p, s, grid, device, stream) : launch_forward<false>(p, s, grid, device, stream);
 }
 
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device)
 {
-    const Shape s = shape_of(row_units(row_elems, dtype));
+    const Shape s = shape_of(row_units(row_elems, dtype), dtype);
     int64_t per_group, ctas;
     deal(T, s, device, per_group, ctas);
-    const int64_t groups = s.sub ? s.threads / s.group : 1;
-    return (2 * ctas + 2 * ctas * groups) * row_elems * 4;
+    return (2 * ctas + 2 * ctas * (s.threads / s.group)) * row_elems * 4;
 }
 
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream)
 {
     p.units = row_units(p.row_elems, dtype);
-    const Shape s = shape_of(p.units);
+    const Shape s = shape_of(p.units, dtype);
     p.group = s.group;
     int64_t ctas;
     deal(p.T, s, device, p.per_group, ctas);
@@ -604,9 +965,12 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     p.part_pre = p.part_post + ctas * p.row_elems;
     p.part_gate = p.part_pre + ctas * p.row_elems;
     if (p.T > 0) {
+        const bool need_h = p.post != nullptr || p.gate_kind != 0;
+        p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
+        p.stages = s.shorter ? 0 : stages_of(s, static_cast<int64_t>(p.tensors) * p.units * 16);
         const unsigned grid = static_cast<unsigned>(ctas);
-        const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, stream)
-                                             : launch_backward<false>(p, s, grid, stream);
+        const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
+                                             : launch_backward<false>(p, s, grid, device, stream);
         if (e != cudaSuccess) return e;
     }
     const bool documents = p.gate_kind == kGateDocument && p.n_docs > 0;
@@ -616,6 +980,16 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     const dim3 grid(static_cast<unsigned>((p.row_elems + 31) / 32), static_cast<unsigned>(2 + docs));
     residual_join_kernel<<<grid, 1024, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t read_residual_wait_timeouts(unsigned int *count, bool reset)
+{
+    cudaError_t e = cudaMemcpyFromSymbol(count, g_wait_timeouts, sizeof(unsigned int));
+    if (e == cudaSuccess && reset) {
+        const unsigned int zero = 0;
+        e = cudaMemcpyToSymbol(g_wait_timeouts, &zero, sizeof(unsigned int));
+    }
+    return e;
 }
 
 cudaError_t read_residual_bounds_violations(unsigned int *count, bool reset)
