@@ -231,6 +231,7 @@ struct ResidualParams {
     float *part_gate;                  // [groups][2][row_elems]: of a document begun earlier, of one that goes on
     int32_t parts;
     int32_t tensors, stages;           // of a ring
+    float per_column;                  // 1 / row_elems
 };
 cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaStream_t stream);
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device);

@@ -41,7 +41,7 @@ struct Shape {
     bool shorter;     // several rows a CTA
 };
 
-Shape shape_of(int units, int dtype)
+Shape shape_of(int units, int dtype, bool gradient)
 {
     Shape s;
     s.shorter = units <= 64;
@@ -56,14 +56,18 @@ Shape shape_of(int units, int dtype)
     s.per_thread = dtype == kBf16 ? 2 : 4;   // 16 columns
     s.group = ((units + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
     s.threads = s.group;
-    s.ctas_per_sm = kLongThreads / s.group;
+    // as many CTAs as registers allow: 80 of a thread in the forward call, 96 in the gradient
+    s.ctas_per_sm = 65536 / ((gradient ? 96 : 80) * s.group);
     return s;
 }
 
+// Weights in shared memory: two rows of them, every thread's units whole.
+int64_t weight_bytes(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
+
 // Rows that a ring holds.
-int stages_of(const Shape &s, int64_t stage_bytes)
+int stages_of(const Shape &s, int dtype, int64_t stage_bytes)
 {
-    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes) / stage_bytes;
+    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - weight_bytes(s, dtype)) / stage_bytes;
     return static_cast<int>(n < 1 ? 1 : n > kMaxStages ? kMaxStages : n);
 }
 
@@ -79,9 +83,10 @@ __device__ __forceinline__ int document_of(const int32_t *cu, int n, int64_t t)
     return lo;
 }
 
-__device__ __forceinline__ float rsqrt_mean(float sum, float n, float eps)
+// 1 / sqrt(sum / C + eps), to 2 units in the last place of the function and one rounding of 1 / C.
+__device__ __forceinline__ float rsqrt_mean(const ResidualParams &p, float sum)
 {
-    return __frsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps));
+    return rsqrtf(__fmaf_rn(sum, p.per_column, p.eps));
 }
 
 template <int E>
@@ -144,17 +149,41 @@ __device__ __forceinline__ void load_weights(const float *w, const Has<U> &has, 
     }
 }
 
+// Weights in registers, or in shared memory (one row of them).
+template <bool BF16, int U>
+struct HeldWeights {
+    const F2 (&w)[U][Unit<BF16>::E / 2];
+    __device__ __forceinline__ void operator()(int k, F2 (&out)[Unit<BF16>::E / 2]) const
+    {
+#pragma unroll
+        for (int i = 0; i < Unit<BF16>::E / 2; ++i) out[i] = w[k][i];
+    }
+};
+
+template <bool BF16>
+struct SharedWeights {
+    const float *row;   // of this thread's unit 0
+    int step;           // floats to its next unit
+    __device__ __forceinline__ void operator()(int k, F2 (&out)[Unit<BF16>::E / 2]) const
+    {
+#pragma unroll
+        for (int i = 0; i < Unit<BF16>::E / 2; i += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + k * step + 2 * i);
+            out[i] = pair_of(v.x, v.y);
+            out[i + 1] = pair_of(v.z, v.w);
+        }
+    }
+};
+
 // One row of the forward call. x, h and gate give a unit's data, put_y and put_n take a unit's result, sum adds
 // over the row's threads.
-template <bool BF16, int U, class X, class H, class G, class Sum, class PutY, class PutN>
+template <bool BF16, int U, class W, class X, class H, class G, class Sum, class PutY, class PutN>
 __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
-                                            uint32_t token, const F2 (&w1)[U][Unit<BF16>::E / 2],
-                                            const F2 (&w2)[U][Unit<BF16>::E / 2], X x, H h, G gate, Sum sum, PutY put_y,
+                                            uint32_t token, W w1, W w2, X x, H h, G gate, Sum sum, PutY put_y,
                                             PutN put_n)
 {
     typedef UnitPairs<BF16> V;
     constexpr int N = V::N;
-    const float C = static_cast<float>(p.row_elems);
     F2 u[U][N], y[U][N];
     float s[1];
     if (p.post != nullptr) {
@@ -167,11 +196,14 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropK
         }
         s[0] = sum_of(q);
         sum(s);
-        const F2 r1 = twice(rsqrt_mean(s[0], C, p.eps));
+        const F2 r1 = twice(rsqrt_mean(p, s[0]));
 #pragma unroll
-        for (int k = 0; k < U; ++k)
+        for (int k = 0; k < U; ++k) {
+            F2 w[N];
+            w1(k, w);
 #pragma unroll
-            for (int i = 0; i < N; ++i) u[k][i] = mul2(mul2(u[k][i], r1), w1[k][i]);
+            for (int i = 0; i < N; ++i) u[k][i] = mul2(mul2(u[k][i], r1), w[i]);
+        }
     } else if (p.h != nullptr) {
 #pragma unroll
         for (int k = 0; k < U; ++k) V::unpack(h(k), u[k]);
@@ -201,12 +233,14 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropK
     if (p.pre == nullptr) return;
     s[0] = sum_of(q);
     sum(s);
-    const F2 r2 = twice(rsqrt_mean(s[0], C, p.eps));
+    const F2 r2 = twice(rsqrt_mean(p, s[0]));
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         if (!has.at[k]) continue;
+        F2 w[N];
+        w2(k, w);
 #pragma unroll
-        for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w2[k][i]);
+        for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w[i]);
         put_n(k, V::pack(y[k]));
     }
 }
@@ -218,15 +252,12 @@ struct Sums {
 };
 
 // One token of the gradient; dy to gate give a unit's data.
-template <bool BF16, int U, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
+template <bool BF16, int U, class W, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
 __device__ __forceinline__ void backward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
-                                             uint32_t token, const F2 (&w1)[U][Unit<BF16>::E / 2],
-                                             const F2 (&w2)[U][Unit<BF16>::E / 2], Sums<BF16, U> &acc, DY dy, DN dn, Y y,
-                                             H h, G gate, Sum sum, PutX put_x, PutH put_h, PutG put_gate)
+                                             uint32_t token, W w1, W w2, Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, G gate, Sum sum, PutX put_x, PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
     constexpr int N = V::N;
-    const float C = static_cast<float>(p.row_elems);
     const bool post = p.post != nullptr, pre = p.pre != nullptr;
     float s[3] = {0.0f, 0.0f, 0.0f};   // y^2, dn w2 y, h^2
     if (pre || post) {
@@ -234,13 +265,14 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             if (pre) {
-                F2 a[N], b[N];
+                F2 a[N], b[N], w[N];
                 V::unpack(y(k), a);
                 V::unpack(dn(k), b);
+                w2(k, w);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
                     q0 = fma2(a[i], a[i], q0);
-                    q1 = fma2(mul2(b[i], w2[k][i]), a[i], q1);
+                    q1 = fma2(mul2(b[i], w[i]), a[i], q1);
                 }
             }
             if (post) {
@@ -255,23 +287,24 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
         s[2] = sum_of(q2);
         sum(s);
     }
-    const float r2 = pre ? rsqrt_mean(s[0], C, p.eps) : 0.0f;
-    const float mean2 = pre ? __fdiv_rn(__fmul_rn(s[1], r2), C) : 0.0f;   // of dn w2 yn
-    const F2 r1 = twice(post ? rsqrt_mean(s[2], C, p.eps) : 1.0f), factor = twice(p.rule.factor);
+    const float r2 = pre ? rsqrt_mean(p, s[0]) : 0.0f;
+    const float mean2 = pre ? __fmul_rn(__fmul_rn(s[1], r2), p.per_column) : 0.0f;   // of dn w2 yn
+    const F2 r1 = twice(post ? rsqrt_mean(p, s[2]) : 1.0f), factor = twice(p.rule.factor);
     F2 e[U][N], q = twice(0.0f);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         F2 d[N], hn[N];
         V::unpack(dy(k), d);
         if (pre) {
-            F2 a[N], b[N];
+            F2 a[N], b[N], w[N];
             V::unpack(y(k), a);
             V::unpack(dn(k), b);
+            w2(k, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const F2 yn = mul2(a[i], twice(r2));
                 acc.pre[k][i] = fma2(b[i], yn, acc.pre[k][i]);
-                d[i] = fma2(twice(r2), fma2(yn, twice(-mean2), mul2(b[i], w2[k][i])), d[i]);
+                d[i] = fma2(twice(r2), fma2(yn, twice(-mean2), mul2(b[i], w[i])), d[i]);
             }
         }
         if (has.at[k]) put_x(k, V::pack(d));
@@ -286,15 +319,24 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
                 for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], r1);
             }
         }
+        F2 w[N];
+        if (post) w1(k, w);
         if (p.gate_kind != 0) {
             F2 g[N], z[N];
             V::unpack(gate(k), g);
+            // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a whole
+            // document shares, a row with an infinity is NaN throughout)
+            const bool guard = p.rule.rng != nullptr && !(post && p.gate_kind == kGateDocument);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                // what was dropped has no gradient, whatever it is multiplied by
-                const float2 c = both(d[i]), zz = both(mul2(d[i], post ? mul2(hn[i], w1[k][i]) : hn[i])), gg = both(mul2(d[i], g[i]));
-                z[i] = pair_of(c.x == 0.0f ? 0.0f : zz.x, c.y == 0.0f ? 0.0f : zz.y);
-                d[i] = pair_of(c.x == 0.0f ? 0.0f : gg.x, c.y == 0.0f ? 0.0f : gg.y);
+                z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
+                F2 dg = mul2(d[i], g[i]);
+                if (guard) {
+                    const float2 c = both(d[i]), zz = both(z[i]), gg = both(dg);
+                    z[i] = pair_of(c.x == 0.0f ? 0.0f : zz.x, c.y == 0.0f ? 0.0f : zz.y);
+                    dg = pair_of(c.x == 0.0f ? 0.0f : gg.x, c.y == 0.0f ? 0.0f : gg.y);
+                }
+                d[i] = dg;
             }
             if (p.gate_kind == kGateDocument) {
 #pragma unroll
@@ -307,7 +349,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
-                e[k][i] = mul2(d[i], w1[k][i]);
+                e[k][i] = mul2(d[i], w[i]);
                 q = fma2(e[k][i], hn[i], q);
             }
         } else if (has.at[k]) {
@@ -317,7 +359,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
     if (!post) return;
     float t[1] = {sum_of(q)};
     sum(t);
-    const F2 mean1 = twice(-__fdiv_rn(t[0], C));
+    const F2 mean1 = twice(-__fmul_rn(t[0], p.per_column));
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         if (!has.at[k]) continue;
@@ -466,7 +508,7 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
         const bool in = row < p.rows, real = r.token >= 0;
         const int64_t at = row * p.units + lane;
         forward_row<BF16, U>(
-            p, key, has, lane, static_cast<uint32_t>(r.token), w1, w2, [&](int k) { return r.t[0][k]; },
+            p, key, has, lane, static_cast<uint32_t>(r.token), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int k) { return r.t[0][k]; },
             [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, LanesSum<1>{p.group},
             [&](int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
             [&](int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
@@ -545,7 +587,7 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
             __device__ __forceinline__ void operator()(float (&v)[3]) const { lanes_sum<3>(v, group); }
         };
         backward_row<BF16, U>(
-            p, key, has, lane, static_cast<uint32_t>(t), w1, w2, acc, [&](int k) { return r.t[0][k]; },
+            p, key, has, lane, static_cast<uint32_t>(t), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; },
             [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; },
             [&](int k) { return r.t[4][k]; }, Sum{p.group},
             [&](int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
@@ -655,7 +697,7 @@ __device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fet
 }
 
 template <bool BF16, int U>
-__global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(768) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -669,9 +711,14 @@ __global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const 
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    F2 w1[U][E / 2], w2[U][E / 2];
-    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
-    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    // the weights stand behind the ring, a thread's units padded to whole ones
+    float *w1 = reinterpret_cast<float *>(smem + static_cast<size_t>(p.stages) * p.tensors * p.units * 16);
+    float *w2 = w1 + U * p.group * E;
+    for (int c = threadIdx.x; c < U * p.group * E; c += p.group) {
+        w1[c] = p.post != nullptr && c < p.row_elems ? p.post[c] : 0.0f;
+        w2[c] = p.pre != nullptr && c < p.row_elems ? p.pre[c] : 0.0f;
+    }
+    const SharedWeights<BF16> post_weights = {w1 + lane * E, p.group * E}, pre_weights = {w2 + lane * E, p.group * E};
     Document doc;
     BlockSum sum(room);
     uint4 gate[U];
@@ -721,7 +768,7 @@ __global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const 
             return has.at[k] ? ring.row(tensor)[lane + k * p.group] : make_uint4(0, 0, 0, 0);
         };
         forward_row<BF16, U>(
-            p, key, has, lane, static_cast<uint32_t>(token), w1, w2, [&](int k) { return from(0, k); },
+            p, key, has, lane, static_cast<uint32_t>(token), post_weights, pre_weights, [&](int k) { return from(0, k); },
             [&](int k) { return from(1, k); }, [&](int k) { return p.gate_kind == kGateToken ? from(2, k) : gate[k]; },
             [&](float (&v)[1]) { sum(v); }, [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
             [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); });
@@ -729,7 +776,7 @@ __global__ void __launch_bounds__(kLongThreads) residual_norm_long_kernel(const 
 }
 
 template <bool BF16, int U>
-__global__ void __launch_bounds__(kLongThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     extern __shared__ __align__(128) uint8_t smem[];
@@ -744,9 +791,14 @@ __global__ void __launch_bounds__(kLongThreads) residual_norm_backward_long_kern
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    F2 w1[U][E / 2], w2[U][E / 2];
-    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
-    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    // the weights stand behind the ring, a thread's units padded to whole ones
+    float *w1 = reinterpret_cast<float *>(smem + static_cast<size_t>(p.stages) * p.tensors * p.units * 16);
+    float *w2 = w1 + U * p.group * E;
+    for (int c = threadIdx.x; c < U * p.group * E; c += p.group) {
+        w1[c] = p.post != nullptr && c < p.row_elems ? p.post[c] : 0.0f;
+        w2[c] = p.pre != nullptr && c < p.row_elems ? p.pre[c] : 0.0f;
+    }
+    const SharedWeights<BF16> post_weights = {w1 + lane * E, p.group * E}, pre_weights = {w2 + lane * E, p.group * E};
     Sums<BF16, U> acc;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -800,7 +852,7 @@ __global__ void __launch_bounds__(kLongThreads) residual_norm_backward_long_kern
                              : make_uint4(0, 0, 0, 0);
         };
         backward_row<BF16, U>(
-            p, key, has, lane, static_cast<uint32_t>(t), w1, w2, acc,
+            p, key, has, lane, static_cast<uint32_t>(t), post_weights, pre_weights, acc,
             [&](int k) { return p.x != nullptr ? from(0, k) : make_uint4(0, 0, 0, 0); }, [&](int k) { return from(at_dn, k); },
             [&](int k) { return from(at_y, k); }, [&](int k) { return from(at_h, k); },
             [&](int k) { return by_document ? document_gate(k) : from(at_gate, k); }, [&](auto &v) { sum(v); },
@@ -867,6 +919,11 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
 
 int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems * (dtype == kBf16 ? 2 : 4) / 16); }
 
+size_t ring_bytes(const ResidualParams &p, const Shape &s, bool bf16)
+{
+    return static_cast<size_t>(p.stages) * p.tensors * p.units * 16 + weight_bytes(s, bf16 ? kBf16 : kF32);
+}
+
 // A kernel's limit of dynamic shared memory, raised once on each device.
 template <auto kernel>
 cudaError_t allow_shared(int device)
@@ -891,7 +948,7 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
     constexpr int U = BF16 ? 2 : 4;
     const cudaError_t e = allow_shared<residual_norm_long_kernel<BF16, U>>(device);
     if (e != cudaSuccess) return e;
-    residual_norm_long_kernel<BF16, U><<<grid, s.threads, static_cast<size_t>(p.stages) * p.tensors * p.units * 16, stream>>>(p);
+    residual_norm_long_kernel<BF16, U><<<grid, s.threads, ring_bytes(p, s, BF16), stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -906,7 +963,7 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
     constexpr int U = BF16 ? 2 : 4;
     const cudaError_t e = allow_shared<residual_norm_backward_long_kernel<BF16, U>>(device);
     if (e != cudaSuccess) return e;
-    residual_norm_backward_long_kernel<BF16, U><<<grid, s.threads, static_cast<size_t>(p.stages) * p.tensors * p.units * 16, stream>>>(p);
+    residual_norm_backward_long_kernel<BF16, U><<<grid, s.threads, ring_bytes(p, s, BF16), stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -926,7 +983,8 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
 {
     if (p.rows == 0) return cudaSuccess;
     p.units = row_units(p.row_elems, dtype);
-    const Shape s = shape_of(p.units, dtype);
+    p.per_column = 1.0f / static_cast<float>(p.row_elems);
+    const Shape s = shape_of(p.units, dtype, false);
     p.group = s.group;
     int64_t ctas;
     if (s.shorter) {
@@ -938,7 +996,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
     } else {
         deal(p.rows, s, device, p.per_group, ctas);
         p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
-        p.stages = stages_of(s, static_cast<int64_t>(p.tensors) * p.units * 16);
+        p.stages = stages_of(s, dtype, static_cast<int64_t>(p.tensors) * p.units * 16);
     }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
@@ -947,7 +1005,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
 
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device)
 {
-    const Shape s = shape_of(row_units(row_elems, dtype), dtype);
+    const Shape s = shape_of(row_units(row_elems, dtype), dtype, true);
     int64_t per_group, ctas;
     deal(T, s, device, per_group, ctas);
     return (2 * ctas + 2 * ctas * (s.threads / s.group)) * row_elems * 4;
@@ -956,7 +1014,8 @@ int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream)
 {
     p.units = row_units(p.row_elems, dtype);
-    const Shape s = shape_of(p.units, dtype);
+    p.per_column = 1.0f / static_cast<float>(p.row_elems);
+    const Shape s = shape_of(p.units, dtype, true);
     p.group = s.group;
     int64_t ctas;
     deal(p.T, s, device, p.per_group, ctas);
@@ -967,7 +1026,7 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     if (p.T > 0) {
         const bool need_h = p.post != nullptr || p.gate_kind != 0;
         p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
-        p.stages = s.shorter ? 0 : stages_of(s, static_cast<int64_t>(p.tensors) * p.units * 16);
+        p.stages = s.shorter ? 0 : stages_of(s, dtype, static_cast<int64_t>(p.tensors) * p.units * 16);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
                                              : launch_backward<false>(p, s, grid, device, stream);
