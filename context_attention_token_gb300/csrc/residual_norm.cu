@@ -20,13 +20,13 @@
 #include "token_rows.cuh"
 
 #include <mutex>
+#include <type_traits>
 
 namespace cpt {
 
 namespace {
 
 constexpr int kShortThreads = 128;
-constexpr int kLongThreads = 512;     // at most, so a thread has 128 registers
 constexpr int kMaxStages = 8;
 constexpr int kSharedBytes = 227 * 1024;   // of an SM
 constexpr int kOwnBytes = 2560;            // of a CTA, besides its ring
@@ -56,18 +56,19 @@ Shape shape_of(int units, int dtype, bool gradient)
     s.per_thread = dtype == kBf16 ? 2 : 4;   // 16 columns
     s.group = ((units + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
     s.threads = s.group;
-    // as many CTAs as registers allow: 80 of a thread in the forward call, 96 in the gradient
-    s.ctas_per_sm = 65536 / ((gradient ? 96 : 80) * s.group);
+    // as many CTAs as registers allow: 64 of a thread in the forward call, 96 in the gradient
+    s.ctas_per_sm = 65536 / ((gradient ? 96 : 64) * s.group);
     return s;
 }
 
-// Weights in shared memory: two rows of them, every thread's units whole.
-int64_t weight_bytes(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
+// A document's gate in shared memory.
+int64_t gate_place(const Shape &s, int gate_kind) { return gate_kind == kGateDocument ? s.per_thread * s.group * 16 : 0; }
 
 // Rows that a ring holds.
-int stages_of(const Shape &s, int dtype, int64_t stage_bytes)
+int stages_of(const Shape &s, int gate_kind, int tensors)
 {
-    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - weight_bytes(s, dtype)) / stage_bytes;
+    const int64_t stage = static_cast<int64_t>(tensors) * s.per_thread * s.group * 16;
+    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / stage;
     return static_cast<int>(n < 1 ? 1 : n > kMaxStages ? kMaxStages : n);
 }
 
@@ -127,6 +128,17 @@ __device__ __forceinline__ float sum_of(F2 x)
     return __fadd_rn(f.x, f.y);
 }
 
+// What a call asks for, known to the compiler (F >= 0: bits 0 post norm, 1 pre norm, 2 dropout, from 3 on the kind of
+// gate; there is a block's output) or read from the parameters (F = -1).
+template <int F>
+struct Asked {
+    static __device__ __forceinline__ bool post(const ResidualParams &p) { return F < 0 ? p.post != nullptr : F & 1; }
+    static __device__ __forceinline__ bool pre(const ResidualParams &p) { return F < 0 ? p.pre != nullptr : F & 2; }
+    static __device__ __forceinline__ bool drop(const ResidualParams &p) { return F < 0 ? p.rule.rng != nullptr : F & 4; }
+    static __device__ __forceinline__ int gate(const ResidualParams &p) { return F < 0 ? p.gate_kind : F >> 3; }
+    static __device__ __forceinline__ bool block(bool there) { return F < 0 ? there : true; }
+};
+
 template <int U>
 struct Has {
     bool at[U];   // whether unit lane + k * group is one of the row
@@ -149,7 +161,7 @@ __device__ __forceinline__ void load_weights(const float *w, const Has<U> &has, 
     }
 }
 
-// Weights in registers, or in shared memory (one row of them).
+// Weights in registers, or read anew from the SM's cache, which all its CTAs share.
 template <bool BF16, int U>
 struct HeldWeights {
     const F2 (&w)[U][Unit<BF16>::E / 2];
@@ -160,15 +172,17 @@ struct HeldWeights {
     }
 };
 
-template <bool BF16>
-struct SharedWeights {
+template <bool BF16, int U>
+struct CachedWeights {
     const float *row;   // of this thread's unit 0
     int step;           // floats to its next unit
+    const Has<U> &has;
     __device__ __forceinline__ void operator()(int k, F2 (&out)[Unit<BF16>::E / 2]) const
     {
 #pragma unroll
         for (int i = 0; i < Unit<BF16>::E / 2; i += 2) {
-            const float4 v = *reinterpret_cast<const float4 *>(row + k * step + 2 * i);
+            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (has.at[k]) v = __ldg(reinterpret_cast<const float4 *>(row + k * step + 2 * i));
             out[i] = pair_of(v.x, v.y);
             out[i + 1] = pair_of(v.z, v.w);
         }
@@ -177,16 +191,17 @@ struct SharedWeights {
 
 // One row of the forward call. x, h and gate give a unit's data, put_y and put_n take a unit's result, sum adds
 // over the row's threads.
-template <bool BF16, int U, class W, class X, class H, class G, class Sum, class PutY, class PutN>
+template <bool BF16, int U, int F, class W, class X, class H, class G, class Sum, class PutY, class PutN>
 __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
                                             uint32_t token, W w1, W w2, X x, H h, G gate, Sum sum, PutY put_y,
                                             PutN put_n)
 {
     typedef UnitPairs<BF16> V;
+    typedef Asked<F> A;
     constexpr int N = V::N;
     F2 u[U][N], y[U][N];
     float s[1];
-    if (p.post != nullptr) {
+    if (A::post(p)) {
         F2 q = twice(0.0f);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -204,7 +219,7 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropK
 #pragma unroll
             for (int i = 0; i < N; ++i) u[k][i] = mul2(mul2(u[k][i], r1), w[i]);
         }
-    } else if (p.h != nullptr) {
+    } else if (A::block(p.h != nullptr)) {
 #pragma unroll
         for (int k = 0; k < U; ++k) V::unpack(h(k), u[k]);
     }
@@ -213,35 +228,32 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const DropK
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         V::unpack(x(k), y[k]);
-        if (p.h != nullptr) {
-            if (p.gate_kind != 0) {
+        if (A::block(p.h != nullptr)) {
+            if (A::gate(p) != 0) {
                 F2 g[N];
                 V::unpack(gate(k), g);
 #pragma unroll
                 for (int i = 0; i < N; ++i) u[k][i] = mul2(u[k][i], g[i]);
             }
-            if (p.rule.rng != nullptr) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, u[k]);
+            if (A::drop(p)) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, u[k]);
 #pragma unroll
             for (int i = 0; i < N; ++i) y[k][i] = fma2(u[k][i], factor, y[k][i]);
             if (has.at[k]) put_y(k, V::pack(y[k]));
         }
-        if (has.at[k]) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) q = fma2(y[k][i], y[k][i], q);
-        }
+        for (int i = 0; i < N; ++i) q = fma2(y[k][i], y[k][i], q);   // past the row's end all data are 0
     }
-    if (p.pre == nullptr) return;
+    if (!A::pre(p)) return;
     s[0] = sum_of(q);
     sum(s);
     const F2 r2 = twice(rsqrt_mean(p, s[0]));
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        if (!has.at[k]) continue;
         F2 w[N];
         w2(k, w);
 #pragma unroll
         for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w[i]);
-        put_n(k, V::pack(y[k]));
+        if (has.at[k]) put_n(k, V::pack(y[k]));
     }
 }
 
@@ -252,13 +264,14 @@ struct Sums {
 };
 
 // One token of the gradient; dy to gate give a unit's data.
-template <bool BF16, int U, class W, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
+template <bool BF16, int U, int F, class W, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
 __device__ __forceinline__ void backward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
                                              uint32_t token, W w1, W w2, Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, G gate, Sum sum, PutX put_x, PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
+    typedef Asked<F> A;
     constexpr int N = V::N;
-    const bool post = p.post != nullptr, pre = p.pre != nullptr;
+    const bool post = A::post(p), pre = A::pre(p);
     float s[3] = {0.0f, 0.0f, 0.0f};   // y^2, dn w2 y, h^2
     if (pre || post) {
         F2 q0 = twice(0.0f), q1 = q0, q2 = q0;
@@ -308,11 +321,11 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
             }
         }
         if (has.at[k]) put_x(k, V::pack(d));
-        if (p.n == nullptr) continue;   // no block
-        if (p.rule.rng != nullptr) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, d);
+        if (!A::block(p.n != nullptr)) continue;
+        if (A::drop(p)) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, d);
 #pragma unroll
         for (int i = 0; i < N; ++i) d[i] = mul2(d[i], factor);
-        if (post || p.gate_kind != 0) {
+        if (post || A::gate(p) != 0) {
             V::unpack(h(k), hn);
             if (post) {
 #pragma unroll
@@ -321,12 +334,12 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
         }
         F2 w[N];
         if (post) w1(k, w);
-        if (p.gate_kind != 0) {
+        if (A::gate(p) != 0) {
             F2 g[N], z[N];
             V::unpack(gate(k), g);
             // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a whole
             // document shares, a row with an infinity is NaN throughout)
-            const bool guard = p.rule.rng != nullptr && !(post && p.gate_kind == kGateDocument);
+            const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
@@ -338,7 +351,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
                 }
                 d[i] = dg;
             }
-            if (p.gate_kind == kGateDocument) {
+            if (A::gate(p) == kGateDocument) {
 #pragma unroll
                 for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
             } else if (has.at[k]) {
@@ -362,12 +375,11 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Drop
     const F2 mean1 = twice(-__fmul_rn(t[0], p.per_column));
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        if (!has.at[k]) continue;
         F2 hn[N];
         V::unpack(h(k), hn);
 #pragma unroll
         for (int i = 0; i < N; ++i) hn[i] = mul2(r1, fma2(mul2(hn[i], r1), mean1, e[k][i]));
-        put_h(k, V::pack(hn));
+        if (has.at[k]) put_h(k, V::pack(hn));
     }
 }
 
@@ -507,7 +519,7 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
         if (i + 1 < p.per_group) load(row + 1, next);
         const bool in = row < p.rows, real = r.token >= 0;
         const int64_t at = row * p.units + lane;
-        forward_row<BF16, U>(
+        forward_row<BF16, U, -1>(
             p, key, has, lane, static_cast<uint32_t>(r.token), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int k) { return r.t[0][k]; },
             [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, LanesSum<1>{p.group},
             [&](int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
@@ -586,7 +598,7 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
             __device__ __forceinline__ void operator()(float (&v)[1]) const { lanes_sum<1>(v, group); }
             __device__ __forceinline__ void operator()(float (&v)[3]) const { lanes_sum<3>(v, group); }
         };
-        backward_row<BF16, U>(
+        backward_row<BF16, U, -1>(
             p, key, has, lane, static_cast<uint32_t>(t), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; },
             [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; },
             [&](int k) { return r.t[4][k]; }, Sum{p.group},
@@ -628,13 +640,20 @@ struct Ring {
     uint8_t *smem;
     uint64_t *full;
     int stages;
-    uint32_t row_bytes, stage_bytes;
+    uint32_t place, stage_bytes;   // bytes of a row's place (every thread's units whole) and of a stage
     int slot = 0;
     uint32_t phase = 0;
 
     __device__ __forceinline__ const uint4 *row(int tensor) const
     {
-        return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes + tensor * row_bytes);
+        return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes + tensor * place);
+    }
+    // What no copy writes: the ends of the places, behind the rows.
+    __device__ __forceinline__ void zero_ends(int tensors, uint32_t row_bytes)
+    {
+        for (int i = 0; i < stages * tensors; ++i)
+            for (uint32_t at = row_bytes + threadIdx.x * 16; at < place; at += blockDim.x * 16)
+                *reinterpret_cast<uint4 *>(smem + i * place + at) = make_uint4(0, 0, 0, 0);
     }
     __device__ __forceinline__ void advance()
     {
@@ -696,10 +715,11 @@ __device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fet
     }
 }
 
-template <bool BF16, int U>
-__global__ void __launch_bounds__(768) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
+template <bool BF16, int U, int F>
+__global__ void __launch_bounds__(1024) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
+    typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float room[256];
     __shared__ __align__(8) uint64_t full[kMaxStages];
@@ -711,19 +731,20 @@ __global__ void __launch_bounds__(768) residual_norm_long_kernel(const __grid_co
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    // the weights stand behind the ring, a thread's units padded to whole ones
-    float *w1 = reinterpret_cast<float *>(smem + static_cast<size_t>(p.stages) * p.tensors * p.units * 16);
-    float *w2 = w1 + U * p.group * E;
-    for (int c = threadIdx.x; c < U * p.group * E; c += p.group) {
-        w1[c] = p.post != nullptr && c < p.row_elems ? p.post[c] : 0.0f;
-        w2[c] = p.pre != nullptr && c < p.row_elems ? p.pre[c] : 0.0f;
-    }
-    const SharedWeights<BF16> post_weights = {w1 + lane * E, p.group * E}, pre_weights = {w2 + lane * E, p.group * E};
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
+    const CachedWeights<BF16, U> post_weights = {p.post + lane * E, p.group * E, has}, pre_weights = {p.pre + lane * E, p.group * E, has};
+    // behind the ring stands a document's gate, each thread's part its own
+    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
+    auto load_gate = [&](int doc) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            own_gate[k * p.group] = has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc) * p.units + lane + k * p.group]
+                                              : make_uint4(0, 0, 0, 0);
+    };
     Document doc;
     BlockSum sum(room);
-    uint4 gate[U];
-    const uint32_t row_bytes = p.units * 16u;
-    Ring ring = {smem, full, p.stages, row_bytes, row_bytes * p.tensors};
+    Ring ring = {smem, full, p.stages, place, place * p.tensors};
+    ring.zero_ends(p.tensors, row_bytes);
 
     auto token_of = [&](int64_t row) {
         int32_t t = -1;
@@ -739,11 +760,11 @@ __global__ void __launch_bounds__(768) residual_norm_long_kernel(const __grid_co
             mbar_expect_tx(bar, 0);
             return;
         }
-        mbar_expect_tx(bar, ring.stage_bytes);
+        mbar_expect_tx(bar, row_bytes * p.tensors);
         const int64_t at = row * row_bytes;
         bulk_load(to, p.x + at, row_bytes, bar);
-        if (p.h != nullptr) bulk_load(to + row_bytes, p.h + at, row_bytes, bar);
-        if (p.gate_kind == kGateToken) bulk_load(to + 2 * row_bytes, p.gate + at, row_bytes, bar);
+        if (A::block(p.h != nullptr)) bulk_load(to + place, p.h + at, row_bytes, bar);
+        if (A::gate(p) == kGateToken) bulk_load(to + 2 * place, p.gate + at, row_bytes, bar);
     };
     walk(ring, begin, end, fetch, [&](int64_t row) {
         const int32_t token = tokens[ring.slot];
@@ -757,58 +778,52 @@ __global__ void __launch_bounds__(768) residual_norm_long_kernel(const __grid_co
             }
             return;
         }
-        if (p.gate_kind == kGateDocument && doc.enter(p, token)) {
-#pragma unroll
-            for (int k = 0; k < U; ++k) {
-                gate[k] = make_uint4(0, 0, 0, 0);
-                if (has.at[k]) gate[k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
-            }
-        }
-        auto from = [&](int tensor, int k) {
-            return has.at[k] ? ring.row(tensor)[lane + k * p.group] : make_uint4(0, 0, 0, 0);
-        };
-        forward_row<BF16, U>(
+        if (A::gate(p) == kGateDocument && doc.enter(p, token)) load_gate(doc.at);
+        auto from = [&](int tensor, int k) { return ring.row(tensor)[lane + k * p.group]; };
+        forward_row<BF16, U, F>(
             p, key, has, lane, static_cast<uint32_t>(token), post_weights, pre_weights, [&](int k) { return from(0, k); },
-            [&](int k) { return from(1, k); }, [&](int k) { return p.gate_kind == kGateToken ? from(2, k) : gate[k]; },
+            [&](int k) { return from(1, k); }, [&](int k) { return A::gate(p) == kGateToken ? from(2, k) : own_gate[k * p.group]; },
             [&](float (&v)[1]) { sum(v); }, [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
             [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); });
     });
 }
 
-template <bool BF16, int U>
+template <bool BF16, int U, int F>
 __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
+    typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(16) float room[256];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     __shared__ int32_t rows[kMaxStages];
     const int lane = threadIdx.x;
     const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.T);
-    const bool need_h = p.post != nullptr || p.gate_kind != 0, pre = p.pre != nullptr;
+    const bool need_h = A::post(p) || A::gate(p) != 0, pre = A::pre(p), by_document = A::gate(p) == kGateDocument;
     DropKey key;
     key.load(p.rule);
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    // the weights stand behind the ring, a thread's units padded to whole ones
-    float *w1 = reinterpret_cast<float *>(smem + static_cast<size_t>(p.stages) * p.tensors * p.units * 16);
-    float *w2 = w1 + U * p.group * E;
-    for (int c = threadIdx.x; c < U * p.group * E; c += p.group) {
-        w1[c] = p.post != nullptr && c < p.row_elems ? p.post[c] : 0.0f;
-        w2[c] = p.pre != nullptr && c < p.row_elems ? p.pre[c] : 0.0f;
-    }
-    const SharedWeights<BF16> post_weights = {w1 + lane * E, p.group * E}, pre_weights = {w2 + lane * E, p.group * E};
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
+    const CachedWeights<BF16, U> post_weights = {p.post + lane * E, p.group * E, has}, pre_weights = {p.pre + lane * E, p.group * E, has};
+    // behind the ring stands a document's gate, each thread's part its own
+    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
+    auto load_gate = [&](int doc) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            own_gate[k * p.group] = has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc) * p.units + lane + k * p.group]
+                                              : make_uint4(0, 0, 0, 0);
+    };
     Sums<BF16, U> acc;
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
-    const bool by_document = p.gate_kind == kGateDocument;
     Document doc;
     BlockSum sum(room);
-    const uint32_t row_bytes = p.units * 16u;
-    Ring ring = {smem, full, p.stages, row_bytes, row_bytes * p.tensors};
+    Ring ring = {smem, full, p.stages, place, place * p.tensors};
+    ring.zero_ends(p.tensors, row_bytes);
     // places of the tensors in a stage
     const int at_dn = p.x != nullptr, at_y = at_dn + pre, at_h = at_y + pre, at_gate = at_h + need_h;
 
@@ -826,36 +841,30 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
             mbar_expect_tx(bar, 0);
             return;
         }
-        mbar_expect_tx(bar, ring.stage_bytes);
+        mbar_expect_tx(bar, row_bytes * p.tensors);
         const int64_t at = static_cast<int64_t>(row) * row_bytes;
         if (p.x != nullptr) bulk_load(to, p.x + at, row_bytes, bar);
         if (pre) {
-            bulk_load(to + at_dn * row_bytes, p.dn + at, row_bytes, bar);
-            bulk_load(to + at_y * row_bytes, p.y_in + at, row_bytes, bar);
+            bulk_load(to + at_dn * place, p.dn + at, row_bytes, bar);
+            bulk_load(to + at_y * place, p.y_in + at, row_bytes, bar);
         }
-        if (need_h) bulk_load(to + at_h * row_bytes, p.h + at, row_bytes, bar);
-        if (p.gate_kind == kGateToken) bulk_load(to + at_gate * row_bytes, p.gate + at, row_bytes, bar);
+        if (need_h) bulk_load(to + at_h * place, p.h + at, row_bytes, bar);
+        if (A::gate(p) == kGateToken) bulk_load(to + at_gate * place, p.gate + at, row_bytes, bar);
     };
     walk(ring, begin, end, fetch, [&](int64_t t) {
         const int32_t row = rows[ring.slot];
         if (row < 0) return;
         if (by_document) {
             if (t > begin && t >= doc.hi) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
-            doc.enter(p, t);
+            if (doc.enter(p, t)) load_gate(doc.at);
         }
         const int64_t at = static_cast<int64_t>(row) * p.units + lane;
-        auto from = [&](int tensor, int k) {
-            return has.at[k] ? ring.row(tensor)[lane + k * p.group] : make_uint4(0, 0, 0, 0);
-        };
-        auto document_gate = [&](int k) {
-            return has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group]
-                             : make_uint4(0, 0, 0, 0);
-        };
-        backward_row<BF16, U>(
+        auto from = [&](int tensor, int k) { return ring.row(tensor)[lane + k * p.group]; };
+        backward_row<BF16, U, F>(
             p, key, has, lane, static_cast<uint32_t>(t), post_weights, pre_weights, acc,
             [&](int k) { return p.x != nullptr ? from(0, k) : make_uint4(0, 0, 0, 0); }, [&](int k) { return from(at_dn, k); },
             [&](int k) { return from(at_y, k); }, [&](int k) { return from(at_h, k); },
-            [&](int k) { return by_document ? document_gate(k) : from(at_gate, k); }, [&](auto &v) { sum(v); },
+            [&](int k) { return by_document ? own_gate[k * p.group] : from(at_gate, k); }, [&](auto &v) { sum(v); },
             [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
             [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); },
             [&](int k, uint4 v) { store_unit(p.dgate, at + k * p.group, v); });
@@ -863,7 +872,7 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
     if (by_document && begin < end) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
-        if (w == 0 ? p.post == nullptr : p.pre == nullptr) continue;
+        if (w == 0 ? !A::post(p) : !A::pre(p)) continue;
         float *to = (w == 0 ? p.part_post : p.part_pre) + static_cast<int64_t>(blockIdx.x) * p.row_elems;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
@@ -919,9 +928,9 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
 
 int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems * (dtype == kBf16 ? 2 : 4) / 16); }
 
-size_t ring_bytes(const ResidualParams &p, const Shape &s, bool bf16)
+size_t ring_bytes(const ResidualParams &p, const Shape &s)
 {
-    return static_cast<size_t>(p.stages) * p.tensors * p.units * 16 + weight_bytes(s, bf16 ? kBf16 : kF32);
+    return static_cast<size_t>(p.stages) * p.tensors * s.per_thread * s.group * 16 + gate_place(s, p.gate_kind);
 }
 
 // A kernel's limit of dynamic shared memory, raised once on each device.
@@ -937,6 +946,26 @@ cudaError_t allow_shared(int device)
     return e;
 }
 
+// The kernel of its own for what is asked most: both norms, with any gate; the pre norm alone, without one. Each with
+// and without dropout. The others share one that looks at its parameters (262144 x 2560 bf16, both norms, dropout:
+// TIMES us).
+template <class Launch>
+cudaError_t with_asked(const ResidualParams &p, bool block, Launch launch)
+{
+    const int f = (p.post != nullptr) + 2 * (p.pre != nullptr) + 4 * (p.rule.rng != nullptr) + 8 * p.gate_kind;
+    switch (block ? f : -1) {
+    case 2: return launch(std::integral_constant<int, 2>());
+    case 3: return launch(std::integral_constant<int, 3>());
+    case 6: return launch(std::integral_constant<int, 6>());
+    case 7: return launch(std::integral_constant<int, 7>());
+    case 11: return launch(std::integral_constant<int, 11>());
+    case 15: return launch(std::integral_constant<int, 15>());
+    case 19: return launch(std::integral_constant<int, 19>());
+    case 23: return launch(std::integral_constant<int, 23>());
+    default: return launch(std::integral_constant<int, -1>());
+    }
+}
+
 template <bool BF16>
 cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned grid, int device, cudaStream_t stream)
 {
@@ -946,10 +975,13 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
         return cudaGetLastError();
     }
     constexpr int U = BF16 ? 2 : 4;
-    const cudaError_t e = allow_shared<residual_norm_long_kernel<BF16, U>>(device);
-    if (e != cudaSuccess) return e;
-    residual_norm_long_kernel<BF16, U><<<grid, s.threads, ring_bytes(p, s, BF16), stream>>>(p);
-    return cudaGetLastError();
+    return with_asked(p, p.h != nullptr, [&](auto f) {
+        constexpr auto kernel = residual_norm_long_kernel<BF16, U, decltype(f)::value>;
+        const cudaError_t e = allow_shared<kernel>(device);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        return cudaGetLastError();
+    });
 }
 
 template <bool BF16>
@@ -961,10 +993,13 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
         return cudaGetLastError();
     }
     constexpr int U = BF16 ? 2 : 4;
-    const cudaError_t e = allow_shared<residual_norm_backward_long_kernel<BF16, U>>(device);
-    if (e != cudaSuccess) return e;
-    residual_norm_backward_long_kernel<BF16, U><<<grid, s.threads, ring_bytes(p, s, BF16), stream>>>(p);
-    return cudaGetLastError();
+    return with_asked(p, p.n != nullptr, [&](auto f) {
+        constexpr auto kernel = residual_norm_backward_long_kernel<BF16, U, decltype(f)::value>;
+        const cudaError_t e = allow_shared<kernel>(device);
+        if (e != cudaSuccess) return e;
+        kernel<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        return cudaGetLastError();
+    });
 }
 
 // Tokens of a group of the gradient, and its CTAs.
@@ -996,7 +1031,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
     } else {
         deal(p.rows, s, device, p.per_group, ctas);
         p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
-        p.stages = stages_of(s, dtype, static_cast<int64_t>(p.tensors) * p.units * 16);
+        p.stages = stages_of(s, p.gate_kind, p.tensors);
     }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
@@ -1026,7 +1061,7 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     if (p.T > 0) {
         const bool need_h = p.post != nullptr || p.gate_kind != 0;
         p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
-        p.stages = s.shorter ? 0 : stages_of(s, dtype, static_cast<int64_t>(p.tensors) * p.units * 16);
+        p.stages = s.shorter ? 0 : stages_of(s, p.gate_kind, p.tensors);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
                                              : launch_backward<false>(p, s, grid, device, stream);
