@@ -59,7 +59,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
             } else if (p.rule.rng != nullptr) {
                 F2 x[N];
                 UnitPairs<BF16>::unpack(raw[k], x);
-                drop_unit<BF16>(p.rule, key, static_cast<uint32_t>(token[k]), at[k], x);
+                uint32_t bits[N];
+                unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(token[k]), at[k], bits);
+                keep_or_zero<N>(p.rule, bits, x);
 #pragma unroll
                 for (int n = 0; n < N; ++n) x[n] = mul2(x[n], factor);
                 out = UnitPairs<BF16>::pack(x);

@@ -57,13 +57,13 @@ struct LongSum {
 
 __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_constant__ PolicyParams p)
 {
-    __shared__ __align__(16) float room[256];
+    __shared__ float room[BlockSum::kRoom];
     BlockSum sum(room);
     for (int64_t d = blockIdx.x; d < p.n_docs; d += gridDim.x) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
         const float A = p.advantages[d];
         // counted in whole numbers, in two floats of 2^24 each: exact for any length
-        float n[3] = {0.0f, 0.0f, 0.0f};
+        float n[2] = {0.0f, 0.0f};
         if (p.mask == nullptr) {
             n[0] = static_cast<float>(hi - lo);
         } else {

@@ -27,6 +27,8 @@ namespace cpt {
 namespace {
 
 constexpr int kShortThreads = 128;
+constexpr int kForwardThreads = 1024;   // of an SM's long rows: 64 registers each
+constexpr int kBackwardThreads = 640;   // 96 registers each
 constexpr int kMaxStages = 8;
 constexpr int kSharedBytes = 227 * 1024;   // of an SM
 constexpr int kOwnBytes = 2560;            // of a CTA, besides its ring
@@ -37,6 +39,7 @@ struct Shape {
     int group;        // threads of a row
     int per_thread;   // units of a thread
     int threads;      // of a CTA
+    int rows;         // at a time, of a CTA's long rows
     int ctas_per_sm;
     bool shorter;     // several rows a CTA
 };
@@ -45,6 +48,7 @@ Shape shape_of(int units, int dtype, bool gradient)
 {
     Shape s;
     s.shorter = units <= 64;
+    s.rows = 1;
     if (s.shorter) {
         s.per_thread = units > 32 ? 2 : 1;
         s.group = 1;
@@ -53,11 +57,17 @@ Shape shape_of(int units, int dtype, bool gradient)
         s.ctas_per_sm = s.per_thread == 1 ? 4 : 2;
         return s;
     }
-    s.per_thread = dtype == kBf16 ? 2 : 4;   // 16 columns
+    // eight columns of two rows at a time, or sixteen of one
+    s.per_thread = dtype == kBf16 ? 1 : 2;
+    s.rows = 2;
+    if (units > s.per_thread * (gradient ? kBackwardThreads : kForwardThreads)) {   // of the gradient only: 8192 columns fit the other
+        s.per_thread *= 2;
+        s.rows = 1;
+    }
     s.group = ((units + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
     s.threads = s.group;
-    // as many CTAs as registers allow: 64 of a thread in the forward call, 96 in the gradient
-    s.ctas_per_sm = 65536 / ((gradient ? 96 : 64) * s.group);
+    // as many CTAs as registers allow
+    s.ctas_per_sm = (gradient ? kBackwardThreads : kForwardThreads) / s.group;
     return s;
 }
 
@@ -161,7 +171,7 @@ __device__ __forceinline__ void load_weights(const float *w, const Has<U> &has, 
     }
 }
 
-// Weights in registers, or read anew from the SM's cache, which all its CTAs share.
+// Weights in registers.
 template <bool BF16, int U>
 struct HeldWeights {
     const F2 (&w)[U][Unit<BF16>::E / 2];
@@ -172,88 +182,89 @@ struct HeldWeights {
     }
 };
 
-template <bool BF16, int U>
-struct CachedWeights {
-    const float *row;   // of this thread's unit 0
-    int step;           // floats to its next unit
-    const Has<U> &has;
-    __device__ __forceinline__ void operator()(int k, F2 (&out)[Unit<BF16>::E / 2]) const
-    {
-#pragma unroll
-        for (int i = 0; i < Unit<BF16>::E / 2; i += 2) {
-            float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (has.at[k]) v = __ldg(reinterpret_cast<const float4 *>(row + k * step + 2 * i));
-            out[i] = pair_of(v.x, v.y);
-            out[i + 1] = pair_of(v.z, v.w);
-        }
-    }
-};
-
-// One row of the forward call. x, h and gate give a unit's data, put_y and put_n take a unit's result, sum adds
-// over the row's threads.
-template <bool BF16, int U, int F, class W, class X, class H, class G, class Sum, class PutY, class PutN>
-__device__ __forceinline__ void forward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
-                                            uint32_t token, W w1, W w2, X x, H h, G gate, Sum sum, PutY put_y,
-                                            PutN put_n)
+// R rows of the forward call. x, h and gate give the data of a unit of a row, bits its random bits (all of a row's
+// at once), put_y and put_n take a unit's result, sum adds over the rows' threads.
+template <bool BF16, int U, int R, int F, class W, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
+__device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<U> &has, W w1, W w2, X x, H h, G gate,
+                                             Bits bits, Sum sum, PutY put_y, PutN put_n)
 {
     typedef UnitPairs<BF16> V;
     typedef Asked<F> A;
     constexpr int N = V::N;
-    F2 u[U][N], y[U][N];
-    float s[1];
+    const bool block = A::block(p.h != nullptr);
+    F2 u[R][U][N], y[R][U][N];
+    uint32_t rnd[R][U][N];
+    float s[R], r1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        F2 q = twice(0.0f);
+        if (block) {
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                V::unpack(h(r, k), u[r][k]);
+                if (A::post(p)) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) q = fma2(u[r][k][i], u[r][k][i], q);
+                }
+            }
+        }
+        s[r] = sum_of(q);
+        r1[r] = p.rule.factor;
+    }
+    // the generator needs no data: it runs while the sums are on their way
+    if (A::drop(p)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) bits(r, rnd[r]);
+    }
     if (A::post(p)) {
+        sum(s);
+#pragma unroll
+        for (int r = 0; r < R; ++r) r1[r] = __fmul_rn(rsqrt_mean(p, s[r]), p.rule.factor);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
         F2 q = twice(0.0f);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
-            V::unpack(h(k), u[k]);
+            V::unpack(x(r, k), y[r][k]);
+            if (block) {
+                if (A::post(p)) {
+                    F2 w[N];
+                    w1(k, w);
 #pragma unroll
-            for (int i = 0; i < N; ++i) q = fma2(u[k][i], u[k][i], q);
+                    for (int i = 0; i < N; ++i) u[r][k][i] = mul2(u[r][k][i], w[i]);
+                }
+                if (A::gate(p) != 0) {
+                    F2 g[N];
+                    V::unpack(gate(r, k), g);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) u[r][k][i] = mul2(u[r][k][i], g[i]);
+                }
+#pragma unroll
+                for (int i = 0; i < N; ++i) u[r][k][i] = fma2(u[r][k][i], twice(r1[r]), y[r][k][i]);
+                if (A::drop(p)) keep_or<N>(p.rule, rnd[r][k], u[r][k], y[r][k]);
+#pragma unroll
+                for (int i = 0; i < N; ++i) y[r][k][i] = u[r][k][i];
+                if (has.at[k]) put_y(r, k, V::pack(y[r][k]));
+            }
+#pragma unroll
+            for (int i = 0; i < N; ++i) q = fma2(y[r][k][i], y[r][k][i], q);   // past the row's end all data are 0
         }
-        s[0] = sum_of(q);
-        sum(s);
-        const F2 r1 = twice(rsqrt_mean(p, s[0]));
+        s[r] = sum_of(q);
+    }
+    if (!A::pre(p)) return;
+    sum(s);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        const F2 r2 = twice(rsqrt_mean(p, s[r]));
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             F2 w[N];
-            w1(k, w);
+            w2(k, w);
 #pragma unroll
-            for (int i = 0; i < N; ++i) u[k][i] = mul2(mul2(u[k][i], r1), w[i]);
+            for (int i = 0; i < N; ++i) y[r][k][i] = mul2(mul2(y[r][k][i], r2), w[i]);
+            if (has.at[k]) put_n(r, k, V::pack(y[r][k]));
         }
-    } else if (A::block(p.h != nullptr)) {
-#pragma unroll
-        for (int k = 0; k < U; ++k) V::unpack(h(k), u[k]);
-    }
-    const F2 factor = twice(p.rule.factor);
-    F2 q = twice(0.0f);
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-        V::unpack(x(k), y[k]);
-        if (A::block(p.h != nullptr)) {
-            if (A::gate(p) != 0) {
-                F2 g[N];
-                V::unpack(gate(k), g);
-#pragma unroll
-                for (int i = 0; i < N; ++i) u[k][i] = mul2(u[k][i], g[i]);
-            }
-            if (A::drop(p)) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, u[k]);
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[k][i] = fma2(u[k][i], factor, y[k][i]);
-            if (has.at[k]) put_y(k, V::pack(y[k]));
-        }
-#pragma unroll
-        for (int i = 0; i < N; ++i) q = fma2(y[k][i], y[k][i], q);   // past the row's end all data are 0
-    }
-    if (!A::pre(p)) return;
-    s[0] = sum_of(q);
-    sum(s);
-    const F2 r2 = twice(rsqrt_mean(p, s[0]));
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-        F2 w[N];
-        w2(k, w);
-#pragma unroll
-        for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w[i]);
-        if (has.at[k]) put_n(k, V::pack(y[k]));
     }
 }
 
@@ -263,123 +274,146 @@ struct Sums {
     F2 post[U][Unit<BF16>::E / 2], pre[U][Unit<BF16>::E / 2], gate[U][Unit<BF16>::E / 2];
 };
 
-// One token of the gradient; dy to gate give a unit's data.
-template <bool BF16, int U, int F, class W, class DY, class DN, class Y, class H, class G, class Sum, class PutX, class PutH, class PutG>
-__device__ __forceinline__ void backward_row(const ResidualParams &p, const DropKey &key, const Has<U> &has, int lane,
-                                             uint32_t token, W w1, W w2, Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, G gate, Sum sum, PutX put_x, PutH put_h, PutG put_gate)
+// R tokens of the gradient, of which `live` says which there are; dy to gate give the data of a unit of a row.
+// `enter(r)` is called before a token's gate is asked for.
+template <bool BF16, int U, int R, int F, class W, class Live, class DY, class DN, class Y, class H, class Enter, class G,
+          class Bits, class Sum, class PutX, class PutH, class PutG>
+__device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has<U> &has, W w1, W w2, Sums<BF16, U> &acc,
+                                              Live live, DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum,
+                                              PutX put_x, PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
     typedef Asked<F> A;
     constexpr int N = V::N;
-    const bool post = A::post(p), pre = A::pre(p);
-    float s[3] = {0.0f, 0.0f, 0.0f};   // y^2, dn w2 y, h^2
+    const bool post = A::post(p), pre = A::pre(p), block = A::block(p.n != nullptr);
+    uint32_t rnd[R][U][N];
+    float s[3 * R];   // of every row: y^2, dn w2 y, h^2
     if (pre || post) {
-        F2 q0 = twice(0.0f), q1 = q0, q2 = q0;
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            F2 q0 = twice(0.0f), q1 = q0, q2 = q0;
+#pragma unroll
+            for (int k = 0; k < U; ++k) {
+                if (pre) {
+                    F2 a[N], b[N], w[N];
+                    V::unpack(y(r, k), a);
+                    V::unpack(dn(r, k), b);
+                    w2(k, w);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) {
+                        q0 = fma2(a[i], a[i], q0);
+                        q1 = fma2(mul2(b[i], w[i]), a[i], q1);
+                    }
+                }
+                if (post) {
+                    F2 a[N];
+                    V::unpack(h(r, k), a);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) q2 = fma2(a[i], a[i], q2);
+                }
+            }
+            s[3 * r] = sum_of(q0);
+            s[3 * r + 1] = sum_of(q1);
+            s[3 * r + 2] = sum_of(q2);
+        }
+    }
+    // the generator needs no data: it runs while the sums are on their way
+    if (A::drop(p)) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) bits(r, rnd[r]);
+    }
+    if (pre || post) sum(s);
+    F2 e[R][U][N];
+    float t[R], r1[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+        t[r] = r1[r] = 0.0f;
+        if (!live(r)) continue;
+        if (A::gate(p) == kGateDocument) enter(r);
+        const float r2 = pre ? rsqrt_mean(p, s[3 * r]) : 0.0f;
+        // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
+        const float back = pre ? -__fmul_rn(__fmul_rn(r2, r2), __fmul_rn(__fmul_rn(s[3 * r + 1], r2), p.per_column)) : 0.0f;
+        r1[r] = post ? rsqrt_mean(p, s[3 * r + 2]) : 1.0f;
+        F2 q = twice(0.0f);
 #pragma unroll
         for (int k = 0; k < U; ++k) {
+            F2 d[N];
+            V::unpack(dy(r, k), d);
             if (pre) {
                 F2 a[N], b[N], w[N];
-                V::unpack(y(k), a);
-                V::unpack(dn(k), b);
+                V::unpack(y(r, k), a);
+                V::unpack(dn(r, k), b);
                 w2(k, w);
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    q0 = fma2(a[i], a[i], q0);
-                    q1 = fma2(mul2(b[i], w[i]), a[i], q1);
+                    acc.pre[k][i] = fma2(mul2(a[i], b[i]), twice(r2), acc.pre[k][i]);
+                    d[i] = fma2(a[i], twice(back), fma2(mul2(b[i], w[i]), twice(r2), d[i]));
                 }
             }
-            if (post) {
-                F2 a[N];
-                V::unpack(h(k), a);
+            if (has.at[k]) put_x(r, k, V::pack(d));
+            if (!block) continue;
+            if (A::drop(p)) keep_or_zero<N>(p.rule, rnd[r][k], d);
 #pragma unroll
-                for (int i = 0; i < N; ++i) q2 = fma2(a[i], a[i], q2);
+            for (int i = 0; i < N; ++i) d[i] = mul2(d[i], twice(p.rule.factor));
+            F2 hn[N], w[N];
+            if (post) w1(k, w);
+            if (post || A::gate(p) != 0) {
+                V::unpack(h(r, k), hn);
+                if (post) {
+#pragma unroll
+                    for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1[r]));
+                }
             }
-        }
-        s[0] = sum_of(q0);
-        s[1] = sum_of(q1);
-        s[2] = sum_of(q2);
-        sum(s);
-    }
-    const float r2 = pre ? rsqrt_mean(p, s[0]) : 0.0f;
-    const float mean2 = pre ? __fmul_rn(__fmul_rn(s[1], r2), p.per_column) : 0.0f;   // of dn w2 yn
-    const F2 r1 = twice(post ? rsqrt_mean(p, s[2]) : 1.0f), factor = twice(p.rule.factor);
-    F2 e[U][N], q = twice(0.0f);
+            if (A::gate(p) != 0) {
+                F2 g[N], z[N];
+                V::unpack(gate(r, k), g);
+                // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a
+                // whole document shares, a row with an infinity is NaN throughout)
+                const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        F2 d[N], hn[N];
-        V::unpack(dy(k), d);
-        if (pre) {
-            F2 a[N], b[N], w[N];
-            V::unpack(y(k), a);
-            V::unpack(dn(k), b);
-            w2(k, w);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const F2 yn = mul2(a[i], twice(r2));
-                acc.pre[k][i] = fma2(b[i], yn, acc.pre[k][i]);
-                d[i] = fma2(twice(r2), fma2(yn, twice(-mean2), mul2(b[i], w[i])), d[i]);
-            }
-        }
-        if (has.at[k]) put_x(k, V::pack(d));
-        if (!A::block(p.n != nullptr)) continue;
-        if (A::drop(p)) drop_unit<BF16>(p.rule, key, token, lane + k * p.group, d);
-#pragma unroll
-        for (int i = 0; i < N; ++i) d[i] = mul2(d[i], factor);
-        if (post || A::gate(p) != 0) {
-            V::unpack(h(k), hn);
-            if (post) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], r1);
-            }
-        }
-        F2 w[N];
-        if (post) w1(k, w);
-        if (A::gate(p) != 0) {
-            F2 g[N], z[N];
-            V::unpack(gate(k), g);
-            // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a whole
-            // document shares, a row with an infinity is NaN throughout)
-            const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
-                F2 dg = mul2(d[i], g[i]);
+                for (int i = 0; i < N; ++i) {
+                    z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
+                    d[i] = mul2(d[i], g[i]);
+                }
                 if (guard) {
-                    const float2 c = both(d[i]), zz = both(z[i]), gg = both(dg);
-                    z[i] = pair_of(c.x == 0.0f ? 0.0f : zz.x, c.y == 0.0f ? 0.0f : zz.y);
-                    dg = pair_of(c.x == 0.0f ? 0.0f : gg.x, c.y == 0.0f ? 0.0f : gg.y);
+                    keep_or_zero<N>(p.rule, rnd[r][k], z);
+                    keep_or_zero<N>(p.rule, rnd[r][k], d);
                 }
-                d[i] = dg;
-            }
-            if (A::gate(p) == kGateDocument) {
+                if (A::gate(p) == kGateDocument) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
+                    for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
+                } else if (has.at[k]) {
+                    put_gate(r, k, V::pack(z));
+                }
+            }
+            if (post) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
+                    e[r][k][i] = mul2(d[i], w[i]);
+                    q = fma2(e[r][k][i], hn[i], q);
+                }
             } else if (has.at[k]) {
-                put_gate(k, V::pack(z));
+                put_h(r, k, V::pack(d));
             }
         }
-        if (post) {
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
-                e[k][i] = mul2(d[i], w[i]);
-                q = fma2(e[k][i], hn[i], q);
-            }
-        } else if (has.at[k]) {
-            put_h(k, V::pack(d));
-        }
+        t[r] = sum_of(q);
     }
     if (!post) return;
-    float t[1] = {sum_of(q)};
     sum(t);
-    const F2 mean1 = twice(-__fmul_rn(t[0], p.per_column));
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        F2 hn[N];
-        V::unpack(h(k), hn);
+    for (int r = 0; r < R; ++r) {
+        if (!live(r)) continue;
+        // dh = r1 e - h r1^2 mean(e hn)
+        const F2 back = twice(-__fmul_rn(__fmul_rn(r1[r], r1[r]), __fmul_rn(t[r], p.per_column)));
 #pragma unroll
-        for (int i = 0; i < N; ++i) hn[i] = mul2(r1, fma2(mul2(hn[i], r1), mean1, e[k][i]));
-        if (has.at[k]) put_h(k, V::pack(hn));
+        for (int k = 0; k < U; ++k) {
+            F2 hn[N];
+            V::unpack(h(r, k), hn);
+#pragma unroll
+            for (int i = 0; i < N; ++i) hn[i] = fma2(hn[i], back, mul2(e[r][k][i], twice(r1[r])));
+            if (has.at[k]) put_h(r, k, V::pack(hn));
+        }
     }
 }
 
@@ -464,12 +498,6 @@ struct ShortRaw {
     int32_t token;
 };
 
-template <int N>
-struct LanesSum {
-    int group;
-    __device__ __forceinline__ void operator()(float (&v)[N]) const { lanes_sum<N>(v, group); }
-};
-
 template <bool BF16, int U>
 __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(const __grid_constant__ ResidualParams p)
 {
@@ -519,11 +547,16 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
         if (i + 1 < p.per_group) load(row + 1, next);
         const bool in = row < p.rows, real = r.token >= 0;
         const int64_t at = row * p.units + lane;
-        forward_row<BF16, U, -1>(
-            p, key, has, lane, static_cast<uint32_t>(r.token), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int k) { return r.t[0][k]; },
-            [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, LanesSum<1>{p.group},
-            [&](int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
-            [&](int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
+        forward_rows<BF16, U, 1, -1>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int, int k) { return r.t[0][k]; },
+            [&](int, int k) { return r.t[1][k]; }, [&](int, int k) { return r.t[2][k]; },
+            [&](int, uint32_t(&bits)[U][E / 2]) {
+#pragma unroll
+                for (int k = 0; k < U; ++k) unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(r.token), lane + k * p.group, bits[k]);
+            },
+            [&](float(&v)[1]) { lanes_sum<1>(v, p.group); },
+            [&](int, int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
+            [&](int, int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
     }
 }
 
@@ -593,18 +626,19 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
                 if (has.at[k]) r.t[4][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
         }
         const int64_t at = r.row * p.units + lane;
-        struct Sum {
-            int group;
-            __device__ __forceinline__ void operator()(float (&v)[1]) const { lanes_sum<1>(v, group); }
-            __device__ __forceinline__ void operator()(float (&v)[3]) const { lanes_sum<3>(v, group); }
-        };
-        backward_row<BF16, U, -1>(
-            p, key, has, lane, static_cast<uint32_t>(t), HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; },
-            [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; },
-            [&](int k) { return r.t[4][k]; }, Sum{p.group},
-            [&](int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
-            [&](int k, uint4 v) { if (real) store_unit(p.n, at + k * p.group, v); },
-            [&](int k, uint4 v) { if (real) store_unit(p.dgate, at + k * p.group, v); });
+        backward_rows<BF16, U, 1, -1>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int) { return true; },
+            [&](int, int k) { return r.t[0][k]; }, [&](int, int k) { return r.t[1][k]; },
+            [&](int, int k) { return r.t[2][k]; }, [&](int, int k) { return r.t[3][k]; }, [](int) {},
+            [&](int, int k) { return r.t[4][k]; },
+            [&](int, uint32_t(&bits)[U][E / 2]) {
+#pragma unroll
+                for (int k = 0; k < U; ++k) unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(t), lane + k * p.group, bits[k]);
+            },
+            [&](auto &v) { lanes_sum(v, p.group); },
+            [&](int, int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
+            [&](int, int k, uint4 v) { if (real) store_unit(p.n, at + k * p.group, v); },
+            [&](int, int k, uint4 v) { if (real) store_unit(p.dgate, at + k * p.group, v); });
     }
     if (by_document && begin < end) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
 
@@ -644,9 +678,19 @@ struct Ring {
     int slot = 0;
     uint32_t phase = 0;
 
-    __device__ __forceinline__ const uint4 *row(int tensor) const
+    // places of the r-th row from the current one
+    __device__ __forceinline__ int slot_of(int r) const { return slot + r < stages ? slot + r : slot + r - stages; }
+    __device__ __forceinline__ const uint4 *row(int r, int tensor) const
     {
-        return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes + tensor * place);
+        return reinterpret_cast<const uint4 *>(smem + slot_of(r) * stage_bytes + tensor * place);
+    }
+    __device__ __forceinline__ void advance(int rows = 1)
+    {
+        slot += rows;
+        if (slot >= stages) {
+            slot -= stages;
+            phase ^= 1;
+        }
     }
     // What no copy writes: the ends of the places, behind the rows.
     __device__ __forceinline__ void zero_ends(int tensors, uint32_t row_bytes)
@@ -654,13 +698,6 @@ struct Ring {
         for (int i = 0; i < stages * tensors; ++i)
             for (uint32_t at = row_bytes + threadIdx.x * 16; at < place; at += blockDim.x * 16)
                 *reinterpret_cast<uint4 *>(smem + i * place + at) = make_uint4(0, 0, 0, 0);
-    }
-    __device__ __forceinline__ void advance()
-    {
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
     }
 };
 
@@ -675,53 +712,57 @@ __device__ __forceinline__ void drain(Ring ring, int64_t waited, int64_t issued)
     }
 }
 
-// Runs `row(t)` for t in [begin, end) with its data in the ring. `fetch(t, bytes at a stage, barrier)` issues a row's copies
-// and announces their bytes; it is called by thread 0, in order.
-template <class Fetch, class Row>
-__device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fetch fetch, Row row)
+// Runs `rows(t)` for the R rows from every R-th t in [begin, end) on, with their data in the ring. `fetch(t, bytes at
+// a stage, slot)` issues a row's copies and announces their bytes; it is called by thread 0, in order.
+template <int R, class Fetch, class Rows>
+__device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fetch fetch, Rows rows)
 {
     int64_t issued = begin;
     int put = 0;
-    auto issue = [&]() {
-        if (threadIdx.x == 0 && issued < end) {
-            fetch(issued, ring.smem + put * ring.stage_bytes, &ring.full[put]);
+    auto issue = [&](int64_t until) {   // by thread 0
+        for (; issued < until && issued < end; ++issued) {
+            fetch(issued, ring.smem + put * ring.stage_bytes, put);
+            if (++put == ring.stages) put = 0;
         }
-        ++issued;
-        if (++put == ring.stages) put = 0;
     };
     if (threadIdx.x == 0) {
         for (int s = 0; s < ring.stages; ++s) mbar_init(&ring.full[s], 1);
         mbar_init_fence();
     }
     __syncthreads();
-    for (int s = 0; s < ring.stages; ++s) issue();
-    for (int64_t t = begin; t < end; ++t) {
-        const bool ok = mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
-        // every thread is done with the row before, whose place is filled again
+    if (threadIdx.x == 0) issue(begin + ring.stages);
+    const bool apart = ring.stages >= 2 * R;   // a row's place is not needed by the rows that come next
+    for (int64_t t = begin; t < end; t += R) {
+        bool ok = true;
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+            if (t + r < end)
+                ok = ok && mbar_wait_bounded(&ring.full[ring.slot_of(r)], ring.slot + r < ring.stages ? ring.phase : ring.phase ^ 1);
+        // every thread is done with the rows before, whose places are filled again
         if (__syncthreads_or(!ok)) {
             if (threadIdx.x == 0) {
                 atomicAdd(&g_wait_timeouts, 1u);
-                drain(ring, t, min(issued, end));
+                drain(ring, t, issued);
             }
             return;
         }
-        if (ring.stages > 1 && t > begin) issue();
-        row(t);
-        ring.advance();
-        if (ring.stages == 1) {
+        if (apart && threadIdx.x == 0) issue(t + ring.stages);
+        rows(t);
+        ring.advance(R);
+        if (!apart) {
             __syncthreads();
-            issue();
+            if (threadIdx.x == 0) issue(t + R + ring.stages);
         }
     }
 }
 
-template <bool BF16, int U, int F>
-__global__ void __launch_bounds__(1024) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
+template <bool BF16, int U, int R, int F>
+__global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) float room[256];
+    __shared__ float room[BlockSum::kRoom];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     __shared__ int32_t tokens[kMaxStages];
     const int lane = threadIdx.x;
@@ -731,18 +772,12 @@ __global__ void __launch_bounds__(1024) residual_norm_long_kernel(const __grid_c
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    const CachedWeights<BF16, U> post_weights = {p.post + lane * E, p.group * E, has}, pre_weights = {p.pre + lane * E, p.group * E, has};
-    // behind the ring stands a document's gate, each thread's part its own
-    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
-    auto load_gate = [&](int doc) {
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            own_gate[k * p.group] = has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc) * p.units + lane + k * p.group]
-                                              : make_uint4(0, 0, 0, 0);
-    };
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
     Document doc;
     BlockSum sum(room);
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
     Ring ring = {smem, full, p.stages, place, place * p.tensors};
     ring.zero_ends(p.tensors, row_bytes);
 
@@ -752,10 +787,11 @@ __global__ void __launch_bounds__(1024) residual_norm_long_kernel(const __grid_c
         return t >= 0 && in_bounds(t < p.T) ? t : -1;
     };
     int32_t ahead = threadIdx.x == 0 ? token_of(begin) : -1;   // looked up a row early
-    auto fetch = [&](int64_t row, uint8_t *to, uint64_t *bar) {
+    auto fetch = [&](int64_t row, uint8_t *to, int slot) {
         const int32_t token = ahead;
+        uint64_t *bar = full + slot;
         ahead = token_of(row + 1);
-        tokens[bar - full] = token;
+        tokens[slot] = token;
         if (token < 0) {   // padding is not read
             mbar_expect_tx(bar, 0);
             return;
@@ -766,35 +802,44 @@ __global__ void __launch_bounds__(1024) residual_norm_long_kernel(const __grid_c
         if (A::block(p.h != nullptr)) bulk_load(to + place, p.h + at, row_bytes, bar);
         if (A::gate(p) == kGateToken) bulk_load(to + 2 * place, p.gate + at, row_bytes, bar);
     };
-    walk(ring, begin, end, fetch, [&](int64_t row) {
-        const int32_t token = tokens[ring.slot];
-        const int64_t at = row * p.units + lane;
-        if (token < 0) {
+    walk<R>(ring, begin, end, fetch, [&](int64_t row) {
+        int32_t token[R];
+        uint4 gate[R][U];   // of the rows' documents
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (!has.at[k]) continue;
-                if (p.y != nullptr) store_unit(p.y, at + k * p.group, make_uint4(0, 0, 0, 0));
-                if (p.n != nullptr) store_unit(p.n, at + k * p.group, make_uint4(0, 0, 0, 0));
+        for (int r = 0; r < R; ++r) {
+            token[r] = row + r < end ? tokens[ring.slot_of(r)] : -1;
+            if (A::gate(p) == kGateDocument) {
+                if (token[r] >= 0) doc.enter(p, token[r]);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    gate[r][k] = make_uint4(0, 0, 0, 0);
+                    if (token[r] >= 0 && has.at[k])
+                        gate[r][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
+                }
             }
-            return;
         }
-        if (A::gate(p) == kGateDocument && doc.enter(p, token)) load_gate(doc.at);
-        auto from = [&](int tensor, int k) { return ring.row(tensor)[lane + k * p.group]; };
-        forward_row<BF16, U, F>(
-            p, key, has, lane, static_cast<uint32_t>(token), post_weights, pre_weights, [&](int k) { return from(0, k); },
-            [&](int k) { return from(1, k); }, [&](int k) { return A::gate(p) == kGateToken ? from(2, k) : own_gate[k * p.group]; },
-            [&](float (&v)[1]) { sum(v); }, [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
-            [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); });
+        const int64_t at = row * p.units + lane;
+        auto put = [&](uint8_t *to, int r, int k, uint4 v) {
+            if (row + r < end) store_unit(to, at + static_cast<int64_t>(r) * p.units + k * p.group, token[r] >= 0 ? v : make_uint4(0, 0, 0, 0));
+        };
+        auto from = [&](int r, int tensor, int k) { return ring.row(r, tensor)[lane + k * p.group]; };
+        forward_rows<BF16, U, R, F>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int r, int k) { return from(r, 0, k); },
+            [&](int r, int k) { return from(r, 1, k); },
+            [&](int r, int k) { return A::gate(p) == kGateToken ? from(r, 2, k) : gate[r][k]; },
+            [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(token[r]), lane, p.group, bits); },
+            [&](float(&v)[R]) { sum(v); }, [&](int r, int k, uint4 v) { put(p.y, r, k, v); },
+            [&](int r, int k, uint4 v) { put(p.n, r, k, v); });
     });
 }
 
-template <bool BF16, int U, int F>
-__global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
+template <bool BF16, int U, int R, int F>
+__global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(16) float room[256];
+    __shared__ float room[BlockSum::kRoom];
     __shared__ __align__(8) uint64_t full[kMaxStages];
     __shared__ int32_t rows[kMaxStages];
     const int lane = threadIdx.x;
@@ -805,16 +850,9 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    const CachedWeights<BF16, U> post_weights = {p.post + lane * E, p.group * E, has}, pre_weights = {p.pre + lane * E, p.group * E, has};
-    // behind the ring stands a document's gate, each thread's part its own
-    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
-    auto load_gate = [&](int doc) {
-#pragma unroll
-        for (int k = 0; k < U; ++k)
-            own_gate[k * p.group] = has.at[k] ? reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc) * p.units + lane + k * p.group]
-                                              : make_uint4(0, 0, 0, 0);
-    };
+    F2 w1[U][E / 2], w2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
     Sums<BF16, U> acc;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -822,8 +860,11 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
         for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
     Document doc;
     BlockSum sum(room);
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
     Ring ring = {smem, full, p.stages, place, place * p.tensors};
     ring.zero_ends(p.tensors, row_bytes);
+    // behind the ring stands a document's gate, each thread's part its own
+    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
     // places of the tensors in a stage
     const int at_dn = p.x != nullptr, at_y = at_dn + pre, at_h = at_y + pre, at_gate = at_h + need_h;
 
@@ -833,10 +874,11 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
         return static_cast<int32_t>(row >= 0 && in_bounds(row < p.rows) ? row : -1);
     };
     int32_t ahead = threadIdx.x == 0 ? row_of(begin) : -1;   // looked up a token early
-    auto fetch = [&](int64_t t, uint8_t *to, uint64_t *bar) {
+    auto fetch = [&](int64_t t, uint8_t *to, int slot) {
         const int32_t row = ahead;
+        uint64_t *bar = full + slot;
         ahead = row_of(t + 1);
-        rows[bar - full] = row;
+        rows[slot] = row;
         if (row < 0) {
             mbar_expect_tx(bar, 0);
             return;
@@ -851,25 +893,34 @@ __global__ void __launch_bounds__(640) residual_norm_backward_long_kernel(const 
         if (need_h) bulk_load(to + at_h * place, p.h + at, row_bytes, bar);
         if (A::gate(p) == kGateToken) bulk_load(to + at_gate * place, p.gate + at, row_bytes, bar);
     };
-    walk(ring, begin, end, fetch, [&](int64_t t) {
-        const int32_t row = rows[ring.slot];
-        if (row < 0) return;
-        if (by_document) {
-            if (t > begin && t >= doc.hi) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
-            if (doc.enter(p, t)) load_gate(doc.at);
-        }
-        const int64_t at = static_cast<int64_t>(row) * p.units + lane;
-        auto from = [&](int tensor, int k) { return ring.row(tensor)[lane + k * p.group]; };
-        backward_row<BF16, U, F>(
-            p, key, has, lane, static_cast<uint32_t>(t), post_weights, pre_weights, acc,
-            [&](int k) { return p.x != nullptr ? from(0, k) : make_uint4(0, 0, 0, 0); }, [&](int k) { return from(at_dn, k); },
-            [&](int k) { return from(at_y, k); }, [&](int k) { return from(at_h, k); },
-            [&](int k) { return by_document ? own_gate[k * p.group] : from(at_gate, k); }, [&](auto &v) { sum(v); },
-            [&](int k, uint4 v) { store_unit(p.y, at + k * p.group, v); },
-            [&](int k, uint4 v) { store_unit(p.n, at + k * p.group, v); },
-            [&](int k, uint4 v) { store_unit(p.dgate, at + k * p.group, v); });
+    walk<R>(ring, begin, end, fetch, [&](int64_t t) {
+        int32_t row[R];
+#pragma unroll
+        for (int r = 0; r < R; ++r) row[r] = t + r < end ? rows[ring.slot_of(r)] : -1;
+        auto from = [&](int r, int tensor, int k) { return ring.row(r, tensor)[lane + k * p.group]; };
+        auto put = [&](uint8_t *to, int r, int k, uint4 v) { store_unit(to, static_cast<int64_t>(row[r]) * p.units + lane + k * p.group, v); };
+        backward_rows<BF16, U, R, F>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int r) { return row[r] >= 0; },
+            [&](int r, int k) { return p.x != nullptr ? from(r, 0, k) : make_uint4(0, 0, 0, 0); },
+            [&](int r, int k) { return from(r, at_dn, k); }, [&](int r, int k) { return from(r, at_y, k); },
+            [&](int r, int k) { return from(r, at_h, k); },
+            [&](int r) {
+                if (t + r < doc.hi) return;
+                if (doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+                doc.enter(p, t + r);
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    uint4 g = make_uint4(0, 0, 0, 0);
+                    if (has.at[k]) g = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
+                    own_gate[k * p.group] = g;
+                }
+            },
+            [&](int r, int k) { return by_document ? own_gate[k * p.group] : from(r, at_gate, k); },
+            [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(t + r), lane, p.group, bits); },
+            [&](auto &v) { sum(v); }, [&](int r, int k, uint4 v) { put(p.y, r, k, v); },
+            [&](int r, int k, uint4 v) { put(p.n, r, k, v); }, [&](int r, int k, uint4 v) { put(p.dgate, r, k, v); });
     });
-    if (by_document && begin < end) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+    if (by_document && doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         if (w == 0 ? !A::post(p) : !A::pre(p)) continue;
@@ -966,6 +1017,12 @@ cudaError_t with_asked(const ResidualParams &p, bool block, Launch launch)
     }
 }
 
+// A kernel as a type.
+template <void (*K)(ResidualParams)>
+struct Kernel {
+    static constexpr auto value = K;
+};
+
 template <bool BF16>
 cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned grid, int device, cudaStream_t stream)
 {
@@ -974,14 +1031,14 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
         else residual_norm_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int U = BF16 ? 2 : 4;
-    return with_asked(p, p.h != nullptr, [&](auto f) {
-        constexpr auto kernel = residual_norm_long_kernel<BF16, U, decltype(f)::value>;
-        const cudaError_t e = allow_shared<kernel>(device);
+    constexpr int U = BF16 ? 1 : 2;
+    auto run = [&](auto kernel) {
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
         if (e != cudaSuccess) return e;
-        kernel<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
         return cudaGetLastError();
-    });
+    };
+    return with_asked(p, p.h != nullptr, [&](auto f) { return run(Kernel<residual_norm_long_kernel<BF16, U, 2, decltype(f)::value>>()); });
 }
 
 template <bool BF16>
@@ -992,14 +1049,15 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
         else residual_norm_backward_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int U = BF16 ? 2 : 4;
-    return with_asked(p, p.n != nullptr, [&](auto f) {
-        constexpr auto kernel = residual_norm_backward_long_kernel<BF16, U, decltype(f)::value>;
-        const cudaError_t e = allow_shared<kernel>(device);
+    constexpr int U = BF16 ? 1 : 2;
+    auto run = [&](auto kernel) {
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
         if (e != cudaSuccess) return e;
-        kernel<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
         return cudaGetLastError();
-    });
+    };
+    if (s.rows == 1) return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>());
+    return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, U, 2, decltype(f)::value>>()); });
 }
 
 // Tokens of a group of the gradient, and its CTAs.

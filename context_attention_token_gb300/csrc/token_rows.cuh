@@ -102,24 +102,69 @@ struct DropKey {
     }
 };
 
-// Which elements of unit `unit` of `token`'s row are kept; the others become 0, whatever they were. The factor
-// is the caller's to multiply by.
+// The random bits of a unit: a word for every two of its columns.
 template <bool BF16>
-__device__ __forceinline__ void drop_unit(const DropRule &r, const DropKey &key, uint32_t token, uint32_t unit,
-                                          F2 (&x)[Unit<BF16>::E / 2])
+__device__ __forceinline__ void unit_bits(const DropRule &r, const DropKey &key, uint32_t token, uint32_t unit,
+                                          uint32_t (&bits)[Unit<BF16>::E / 2])
 {
     const uint4 w = philox(key.k0, key.k1, make_uint4(BF16 ? unit : unit >> 1, token, key.step, r.site));
-    uint32_t h[4] = {w.x, w.y, w.z, w.w};
-    if (!BF16 && (unit & 1)) {   // a float32 unit is half a group of eight columns
-        h[0] = h[2];
-        h[1] = h[3];
+    if constexpr (BF16) {
+        bits[0] = w.x;
+        bits[1] = w.y;
+        bits[2] = w.z;
+        bits[3] = w.w;
+    } else {   // a float32 unit is half a group of eight columns
+        bits[0] = unit & 1 ? w.z : w.x;
+        bits[1] = unit & 1 ? w.w : w.y;
     }
+}
+
+// The bits of a thread's units lane, lane + group, ..., with even groups of whole warps. Two neighbouring lanes have
+// the halves of the same group of eight float32 columns: each calls the generator for one of two units and they
+// exchange what the other needs.
+template <bool BF16, int U>
+__device__ __forceinline__ void thread_bits(const DropRule &r, const DropKey &key, uint32_t token, int lane, int group,
+                                            uint32_t (&bits)[U][Unit<BF16>::E / 2])
+{
+    if constexpr (BF16) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) unit_bits<true>(r, key, token, lane + k * group, bits[k]);
+    } else {
+        static_assert(U % 2 == 0, "pairs of units");
+        const bool odd = lane & 1;
+#pragma unroll
+        for (int k = 0; k < U; k += 2) {
+            const uint32_t mine = lane + (k + odd) * group;
+            const uint4 w = philox(key.k0, key.k1, make_uint4(mine >> 1, token, key.step, r.site));
+            const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? w.x : w.z, 1);
+            const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? w.y : w.w, 1);
+            bits[k][0] = odd ? a : w.x;
+            bits[k][1] = odd ? b : w.y;
+            bits[k + 1][0] = odd ? w.z : a;
+            bits[k + 1][1] = odd ? w.w : b;
+        }
+    }
+}
+
+// x where an element is kept, `other` where it is dropped.
+template <int N>
+__device__ __forceinline__ void keep_or(const DropRule &r, const uint32_t (&bits)[N], F2 (&x)[N], const F2 (&other)[N])
+{
     const uint32_t below = r.kept << 16;   // kept is 0..65535 here, so a half compares as the top of a word
 #pragma unroll
-    for (int i = 0; i < Unit<BF16>::E / 2; ++i) {
-        const float2 f = both(x[i]);
-        x[i] = pair_of((h[i] << 16) < below ? f.x : 0.0f, h[i] < below ? f.y : 0.0f);
+    for (int i = 0; i < N; ++i) {
+        const float2 f = both(x[i]), o = both(other[i]);
+        x[i] = pair_of((bits[i] << 16) < below ? f.x : o.x, bits[i] < below ? f.y : o.y);
     }
+}
+
+template <int N>
+__device__ __forceinline__ void keep_or_zero(const DropRule &r, const uint32_t (&bits)[N], F2 (&x)[N])
+{
+    F2 zero[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) zero[i] = pair_of(0.0f, 0.0f);
+    keep_or<N>(r, bits, x, zero);
 }
 
 // Sums of N values over the `group` lanes of a warp that share a row (a power of two), in a fixed order.
@@ -135,47 +180,42 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N], int group)
 // Sums over a CTA of whole warps, in a fixed order. There are two places for the warps' sums; one is written
 // again only after every thread has passed the barrier of the other, so one barrier a sum is enough.
 struct BlockSum {
-    float *room;   // [2][32 * 4], shared, 16-byte aligned
+    static constexpr int kRoom = 2 * 256;   // floats
+    float *room;                            // shared
     int turn = 0;
     __device__ explicit BlockSum(float *r) : room(r) {}
 
-    // one value
-    __device__ __forceinline__ void operator()(float (&v)[1])
+    // N values: lanes give away those that they do not keep, so that (for N = 6) 9 shuffles do for 30
+    template <int N>
+    __device__ __forceinline__ void operator()(float (&v)[N])
     {
+        constexpr int W = N == 1 ? 1 : N == 2 ? 2 : N <= 4 ? 4 : 8;
+        static_assert(N <= 8, "at most eight values");
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-        float *at = room + turn * 128;
+        float *at = room + turn * 256;
         turn ^= 1;
+        float a[W];
 #pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], d));
-        if (lane == 0) at[warp] = v[0];
-        __syncthreads();
-        const int span = warps > 16 ? 32 : warps > 8 ? 16 : 8;   // every `span` lanes hold all of the warps' sums
-        v[0] = (lane & (span - 1)) < warps ? at[lane & (span - 1)] : 0.0f;
-        for (int d = span >> 1; d > 0; d >>= 1) v[0] = __fadd_rn(v[0], __shfl_xor_sync(0xFFFFFFFFu, v[0], d));
-    }
-
-    // three values: lanes give away those that they do not keep, so that 6 shuffles do for 15
-    __device__ __forceinline__ void operator()(float (&v)[3])
-    {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-        float *at = room + turn * 128;
-        turn ^= 1;
-        const bool odd = lane & 1, upper = lane & 2;
-        float a = odd ? v[1] : v[0], c = odd ? 0.0f : v[2];
-        a = __fadd_rn(a, __shfl_xor_sync(0xFFFFFFFFu, odd ? v[0] : v[1], 1));
-        c = __fadd_rn(c, __shfl_xor_sync(0xFFFFFFFFu, odd ? v[2] : 0.0f, 1));
-        float s = upper ? c : a;
-        s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, upper ? a : c, 2));
+        for (int i = 0; i < W; ++i) a[i] = i < N ? v[i] : 0.0f;
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
-        if (lane < 4) at[warp * 4 + lane] = s;   // lane i: value i
+        for (int bit = 1; bit < W; bit *= 2) {   // then a[i] is value 2 i + (the lane's bit) of before
+#pragma unroll
+            for (int i = 0; i < W / 2 / bit; ++i) {
+                const float keep = lane & bit ? a[2 * i + 1] : a[2 * i], give = lane & bit ? a[2 * i] : a[2 * i + 1];
+                a[i] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, bit));
+            }
+        }
+        float s = a[0];
+#pragma unroll
+        for (int d = W; d < 32; d *= 2) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
+        if (lane < W) at[warp * W + lane] = s;   // lane i: value i
         __syncthreads();
         s = 0.0f;
-        for (int i = lane; i < warps * 4; i += 32) s = __fadd_rn(s, at[i]);
+        for (int i = lane; i < warps * W; i += 32) s = __fadd_rn(s, at[i]);
 #pragma unroll
-        for (int d = 4; d < 32; d <<= 1) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
+        for (int d = W; d < 32; d *= 2) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
 #pragma unroll
-        for (int i = 0; i < 3; ++i) v[i] = __shfl_sync(0xFFFFFFFFu, s, i);
+        for (int i = 0; i < N; ++i) v[i] = W == 1 ? s : __shfl_sync(0xFFFFFFFFu, s, i);
     }
 };
 
