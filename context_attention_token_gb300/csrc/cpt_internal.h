@@ -230,7 +230,7 @@ struct ResidualParams {
     float *part_post, *part_pre;       // [CTAs][row_elems]
     float *part_gate;                  // [groups][2][row_elems]: of a document begun earlier, of one that goes on
     int32_t parts;
-    int32_t tensors, stages;           // of a ring
+    int32_t tensors, stages;           // of a ring: tensors that are read, chunks of rows
     float per_column;                  // 1 / row_elems
 };
 cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaStream_t stream);

@@ -29,9 +29,9 @@ namespace {
 constexpr int kShortThreads = 128;
 constexpr int kForwardThreads = 1024;   // of an SM's long rows: 64 registers each
 constexpr int kBackwardThreads = 640;   // 96 registers each
-constexpr int kMaxStages = 8;
+constexpr int kMaxChunks = 8;
 constexpr int kSharedBytes = 227 * 1024;   // of an SM
-constexpr int kOwnBytes = 2560;            // of a CTA, besides its ring
+constexpr int kOwnBytes = 3584;            // of a CTA, besides its ring
 constexpr int kGateToken = 1, kGateDocument = 2;
 
 // How rows of so many units are dealt to threads.
@@ -74,12 +74,12 @@ Shape shape_of(int units, int dtype, bool gradient)
 // A document's gate in shared memory.
 int64_t gate_place(const Shape &s, int gate_kind) { return gate_kind == kGateDocument ? s.per_thread * s.group * 16 : 0; }
 
-// Rows that a ring holds.
-int stages_of(const Shape &s, int gate_kind, int tensors)
+// Chunks of rows that a ring holds.
+int chunks_of(const Shape &s, int gate_kind, int tensors)
 {
-    const int64_t stage = static_cast<int64_t>(tensors) * s.per_thread * s.group * 16;
-    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / stage;
-    return static_cast<int>(n < 1 ? 1 : n > kMaxStages ? kMaxStages : n);
+    const int64_t chunk = static_cast<int64_t>(tensors) * s.rows * s.per_thread * s.group * 16;
+    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / chunk;
+    return static_cast<int>(n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : n);
 }
 
 // The document of a raw token: the last d with cu[d] <= t.
@@ -192,24 +192,22 @@ __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<
     typedef Asked<F> A;
     constexpr int N = V::N;
     const bool block = A::block(p.h != nullptr);
-    F2 u[R][U][N], y[R][U][N];
+    F2 y[R][U][N];
     uint32_t rnd[R][U][N];
     float s[R], r1[R];
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+        r1[r] = p.rule.factor;
+        if (!A::post(p)) continue;
         F2 q = twice(0.0f);
-        if (block) {
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                V::unpack(h(r, k), u[r][k]);
-                if (A::post(p)) {
+        for (int k = 0; k < U; ++k) {
+            F2 u[N];
+            V::unpack(h(r, k), u);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) q = fma2(u[r][k][i], u[r][k][i], q);
-                }
-            }
+            for (int i = 0; i < N; ++i) q = fma2(u[i], u[i], q);
         }
         s[r] = sum_of(q);
-        r1[r] = p.rule.factor;
     }
     // the generator needs no data: it runs while the sums are on their way
     if (A::drop(p)) {
@@ -228,23 +226,25 @@ __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<
         for (int k = 0; k < U; ++k) {
             V::unpack(x(r, k), y[r][k]);
             if (block) {
+                F2 u[N];   // h once more: kept over the sum it would cost registers that a CTA more is worth
+                V::unpack(h(r, k), u);
                 if (A::post(p)) {
                     F2 w[N];
                     w1(k, w);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) u[r][k][i] = mul2(u[r][k][i], w[i]);
+                    for (int i = 0; i < N; ++i) u[i] = mul2(u[i], w[i]);
                 }
                 if (A::gate(p) != 0) {
                     F2 g[N];
                     V::unpack(gate(r, k), g);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) u[r][k][i] = mul2(u[r][k][i], g[i]);
+                    for (int i = 0; i < N; ++i) u[i] = mul2(u[i], g[i]);
                 }
 #pragma unroll
-                for (int i = 0; i < N; ++i) u[r][k][i] = fma2(u[r][k][i], twice(r1[r]), y[r][k][i]);
-                if (A::drop(p)) keep_or<N>(p.rule, rnd[r][k], u[r][k], y[r][k]);
+                for (int i = 0; i < N; ++i) u[i] = fma2(u[i], twice(r1[r]), y[r][k][i]);
+                if (A::drop(p)) keep_or<N>(p.rule, rnd[r][k], u, y[r][k]);
 #pragma unroll
-                for (int i = 0; i < N; ++i) y[r][k][i] = u[r][k][i];
+                for (int i = 0; i < N; ++i) y[r][k][i] = u[i];
                 if (has.at[k]) put_y(r, k, V::pack(y[r][k]));
             }
 #pragma unroll
@@ -668,34 +668,27 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
 
 // ----------------------------------------------------------------- long rows: a CTA each
 
-// A ring of rows in shared memory. Thread 0 has the bulk-copy engine fetch the rows of all input tensors, one
-// instruction a row, `stages` rows ahead.
+// A ring of chunks of R rows in shared memory. The first warp has the bulk-copy engine fetch the rows of all input
+// tensors, one instruction a row, a lane for each.
+template <int R>
 struct Ring {
     uint8_t *smem;
-    uint64_t *full;
-    int stages;
-    uint32_t place, stage_bytes;   // bytes of a row's place (every thread's units whole) and of a stage
+    uint64_t *full;                // of every chunk
+    int32_t *index;                // [chunks][R]: of a chunk's rows, a forward call's token or a gradient's row (-1: none)
+    int chunks;
+    uint32_t place, stage_bytes;   // bytes of a row's place (every thread's units whole) and of all tensors'
     int slot = 0;
     uint32_t phase = 0;
 
-    // places of the r-th row from the current one
-    __device__ __forceinline__ int slot_of(int r) const { return slot + r < stages ? slot + r : slot + r - stages; }
-    __device__ __forceinline__ const uint4 *row(int r, int tensor) const
+    // the current chunk's row r of tensor 0
+    __device__ __forceinline__ const uint4 *row(int r) const
     {
-        return reinterpret_cast<const uint4 *>(smem + slot_of(r) * stage_bytes + tensor * place);
-    }
-    __device__ __forceinline__ void advance(int rows = 1)
-    {
-        slot += rows;
-        if (slot >= stages) {
-            slot -= stages;
-            phase ^= 1;
-        }
+        return reinterpret_cast<const uint4 *>(smem + (slot * R + r) * stage_bytes);
     }
     // What no copy writes: the ends of the places, behind the rows.
     __device__ __forceinline__ void zero_ends(int tensors, uint32_t row_bytes)
     {
-        for (int i = 0; i < stages * tensors; ++i)
+        for (int i = 0; i < chunks * R * tensors; ++i)
             for (uint32_t at = row_bytes + threadIdx.x * 16; at < place; at += blockDim.x * 16)
                 *reinterpret_cast<uint4 *>(smem + i * place + at) = make_uint4(0, 0, 0, 0);
     }
@@ -703,55 +696,67 @@ struct Ring {
 
 __device__ unsigned int g_wait_timeouts;
 
-// Waits for what thread 0 still has in flight, so that no copy ends in another CTA's shared memory.
-__device__ __forceinline__ void drain(Ring ring, int64_t waited, int64_t issued)
+// Runs `rows(i, after)` for i = 0, R, 2 R, ... below count with the chunk's data in the ring. It has to call after()
+// once behind its first barrier, where every thread is done with the chunk before; `sum` votes there whether a wait
+// has run out. index_of(i) looks the i-th up (-1: it is not read), row_of(i, index) is its row, base this lane's tensor.
+template <int R, class Index, class RowOf, class Rows>
+__device__ __forceinline__ void walk(Ring<R> &ring, BlockSum &sum, int64_t count, int tensors, uint32_t row_bytes,
+                                     const uint8_t *base, Index index_of, RowOf row_of, Rows rows)
 {
-    for (int64_t i = waited; i < issued; ++i) {
-        mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
-        ring.advance();
-    }
-}
-
-// Runs `rows(t)` for the R rows from every R-th t in [begin, end) on, with their data in the ring. `fetch(t, bytes at
-// a stage, slot)` issues a row's copies and announces their bytes; it is called by thread 0, in order.
-template <int R, class Fetch, class Rows>
-__device__ __forceinline__ void walk(Ring &ring, int64_t begin, int64_t end, Fetch fetch, Rows rows)
-{
-    int64_t issued = begin;
+    const int lane = threadIdx.x & 31, tensor = lane / R, r = lane - tensor * R;
+    const bool first = threadIdx.x < 32;
+    int64_t issued = 0;
     int put = 0;
-    auto issue = [&](int64_t until) {   // by thread 0
-        for (; issued < until && issued < end; ++issued) {
-            fetch(issued, ring.smem + put * ring.stage_bytes, put);
-            if (++put == ring.stages) put = 0;
-        }
+    int32_t ahead = first ? index_of(r) : -1;   // looked up a chunk early
+    auto issue = [&]() {   // by the first warp
+        if (issued >= count) return;
+        const int32_t index = ahead;
+        uint64_t *bar = &ring.full[put];
+        const int some = __popc(__ballot_sync(0xFFFFFFFFu, tensor == 0 && index >= 0));
+        if (tensor == 0) ring.index[put * R + r] = index;
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(some * tensors) * row_bytes);
+        if (tensor < tensors && index >= 0)
+            bulk_load(ring.smem + (put * R + r) * ring.stage_bytes + tensor * ring.place,
+                      base + row_of(issued + r, index) * row_bytes, row_bytes, bar);
+        issued += R;
+        ahead = index_of(issued + r);
+        if (++put == ring.chunks) put = 0;
     };
     if (threadIdx.x == 0) {
-        for (int s = 0; s < ring.stages; ++s) mbar_init(&ring.full[s], 1);
+        for (int c = 0; c < ring.chunks; ++c) mbar_init(&ring.full[c], 1);
         mbar_init_fence();
     }
     __syncthreads();
-    if (threadIdx.x == 0) issue(begin + ring.stages);
-    const bool apart = ring.stages >= 2 * R;   // a row's place is not needed by the rows that come next
-    for (int64_t t = begin; t < end; t += R) {
-        bool ok = true;
-#pragma unroll
-        for (int r = 0; r < R; ++r)
-            if (t + r < end)
-                ok = ok && mbar_wait_bounded(&ring.full[ring.slot_of(r)], ring.slot + r < ring.stages ? ring.phase : ring.phase ^ 1);
-        // every thread is done with the rows before, whose places are filled again
-        if (__syncthreads_or(!ok)) {
+    if (first)
+        for (int c = 0; c < ring.chunks; ++c) issue();
+    const bool several = ring.chunks > 1;
+    for (int64_t i = 0; i < count; i += R) {
+        if (!mbar_wait_bounded(&ring.full[ring.slot], ring.phase)) sum.ask = true;
+        // the place of the chunk before is filled again
+        rows(i, [&]() {
+            if (several && first && i > 0) issue();
+        });
+        if (++ring.slot == ring.chunks) {
+            ring.slot = 0;
+            ring.phase ^= 1;
+        }
+        if (!several) {
+            sum.stop = __syncthreads_or(sum.ask);
+            if (first && !sum.stop) issue();
+        }
+        if (sum.stop) {   // by all: no copy may end in another CTA's shared memory
             if (threadIdx.x == 0) {
                 atomicAdd(&g_wait_timeouts, 1u);
-                drain(ring, t, issued);
+                for (int64_t k = i + R; k < issued; k += R) {
+                    mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+                    if (++ring.slot == ring.chunks) {
+                        ring.slot = 0;
+                        ring.phase ^= 1;
+                    }
+                }
             }
             return;
-        }
-        if (apart && threadIdx.x == 0) issue(t + ring.stages);
-        rows(t);
-        ring.advance(R);
-        if (!apart) {
-            __syncthreads();
-            if (threadIdx.x == 0) issue(t + R + ring.stages);
         }
     }
 }
@@ -763,10 +768,10 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float room[BlockSum::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxStages];
-    __shared__ int32_t tokens[kMaxStages];
+    __shared__ __align__(8) uint64_t full[kMaxChunks];
+    __shared__ int32_t index[kMaxChunks * R];
     const int lane = threadIdx.x;
-    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.rows);
+    const int64_t begin = blockIdx.x * p.per_group, count = min(p.per_group, p.rows - begin);
     DropKey key;
     key.load(p.rule);
     Has<U> has;
@@ -778,58 +783,66 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     Document doc;
     BlockSum sum(room);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    Ring ring = {smem, full, p.stages, place, place * p.tensors};
+    Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
     ring.zero_ends(p.tensors, row_bytes);
 
-    auto token_of = [&](int64_t row) {
+    auto token_of = [&](int64_t i) {
         int32_t t = -1;
-        if (row < end) t = p.token_of_row == nullptr ? static_cast<int32_t>(row) : p.token_of_row[row];
+        if (i < count) t = p.token_of_row == nullptr ? static_cast<int32_t>(begin + i) : p.token_of_row[begin + i];
         return t >= 0 && in_bounds(t < p.T) ? t : -1;
     };
-    int32_t ahead = threadIdx.x == 0 ? token_of(begin) : -1;   // looked up a row early
-    auto fetch = [&](int64_t row, uint8_t *to, int slot) {
-        const int32_t token = ahead;
-        uint64_t *bar = full + slot;
-        ahead = token_of(row + 1);
-        tokens[slot] = token;
-        if (token < 0) {   // padding is not read
-            mbar_expect_tx(bar, 0);
-            return;
-        }
-        mbar_expect_tx(bar, row_bytes * p.tensors);
-        const int64_t at = row * row_bytes;
-        bulk_load(to, p.x + at, row_bytes, bar);
-        if (A::block(p.h != nullptr)) bulk_load(to + place, p.h + at, row_bytes, bar);
-        if (A::gate(p) == kGateToken) bulk_load(to + 2 * place, p.gate + at, row_bytes, bar);
-    };
-    walk<R>(ring, begin, end, fetch, [&](int64_t row) {
+    // the rows are neighbours, padding is not read
+    const int tensor = (lane & 31) / R;
+    const uint8_t *base = tensor == 0 ? p.x : tensor == 1 && A::block(p.h != nullptr) ? p.h : p.gate;
+    auto row_of = [&](int64_t i, int32_t) { return begin + i; };
+    uint8_t *y = p.y, *n = p.n;
+    walk<R>(ring, sum, count, p.tensors, row_bytes, base, token_of, row_of, [&](int64_t i, auto after) {
         int32_t token[R];
+        bool put[R];
         uint4 gate[R][U];   // of the rows' documents
+        const uint4 *data[R];
+        int64_t at[R];      // of this thread's first unit, in bytes
+        bool waiting = true;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            token[r] = row + r < end ? tokens[ring.slot_of(r)] : -1;
+            token[r] = ring.index[ring.slot * R + r];
+            put[r] = token[r] >= 0;
+            data[r] = ring.row(r) + lane;
+            at[r] = static_cast<int64_t>(static_cast<uint32_t>(begin) + static_cast<uint32_t>(i) + r) * row_bytes + lane * 16;
             if (A::gate(p) == kGateDocument) {
-                if (token[r] >= 0) doc.enter(p, token[r]);
+                if (put[r]) doc.enter(p, token[r]);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     gate[r][k] = make_uint4(0, 0, 0, 0);
-                    if (token[r] >= 0 && has.at[k])
+                    if (put[r] && has.at[k])
                         gate[r][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
                 }
             }
+            if (!put[r] && i + r < count) {   // padding
+#pragma unroll
+                for (int k = 0; k < U; ++k) {
+                    if (!has.at[k]) continue;
+                    if (y != nullptr) store_unit(y + at[r], k * p.group, make_uint4(0, 0, 0, 0));
+                    if (n != nullptr) store_unit(n + at[r], k * p.group, make_uint4(0, 0, 0, 0));
+                }
+            }
         }
-        const int64_t at = row * p.units + lane;
-        auto put = [&](uint8_t *to, int r, int k, uint4 v) {
-            if (row + r < end) store_unit(to, at + static_cast<int64_t>(r) * p.units + k * p.group, token[r] >= 0 ? v : make_uint4(0, 0, 0, 0));
-        };
-        auto from = [&](int r, int tensor, int k) { return ring.row(r, tensor)[lane + k * p.group]; };
         forward_rows<BF16, U, R, F>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int r, int k) { return from(r, 0, k); },
-            [&](int r, int k) { return from(r, 1, k); },
-            [&](int r, int k) { return A::gate(p) == kGateToken ? from(r, 2, k) : gate[r][k]; },
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int r, int k) { return data[r][k * p.group]; },
+            [&](int r, int k) { return data[r][(U + k) * p.group]; },
+            [&](int r, int k) { return A::gate(p) == kGateToken ? data[r][(2 * U + k) * p.group] : gate[r][k]; },
             [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(token[r]), lane, p.group, bits); },
-            [&](float(&v)[R]) { sum(v); }, [&](int r, int k, uint4 v) { put(p.y, r, k, v); },
-            [&](int r, int k, uint4 v) { put(p.n, r, k, v); });
+            [&](float(&v)[R]) {
+                sum(v);
+                if (waiting) after();
+                waiting = false;
+            },
+            [&](int r, int k, uint4 v) { if (put[r]) store_unit(y + at[r], k * p.group, v); },
+            [&](int r, int k, uint4 v) { if (put[r]) store_unit(n + at[r], k * p.group, v); });
+        if (waiting) {
+            sum.stop = __syncthreads_or(sum.ask);
+            after();
+        }
     });
 }
 
@@ -840,10 +853,10 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float room[BlockSum::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxStages];
-    __shared__ int32_t rows[kMaxStages];
+    __shared__ __align__(8) uint64_t full[kMaxChunks];
+    __shared__ int32_t index[kMaxChunks * R];
     const int lane = threadIdx.x;
-    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.T);
+    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.T), count = end - begin;
     const bool need_h = A::post(p) || A::gate(p) != 0, pre = A::pre(p), by_document = A::gate(p) == kGateDocument;
     DropKey key;
     key.load(p.rule);
@@ -861,49 +874,44 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
     Document doc;
     BlockSum sum(room);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    Ring ring = {smem, full, p.stages, place, place * p.tensors};
+    Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
     ring.zero_ends(p.tensors, row_bytes);
     // behind the ring stands a document's gate, each thread's part its own
-    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * p.tensors * place) + lane;
-    // places of the tensors in a stage
-    const int at_dn = p.x != nullptr, at_y = at_dn + pre, at_h = at_y + pre, at_gate = at_h + need_h;
+    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * R * p.tensors * place) + lane;
+    // places of the tensors in a stage, in units
+    const int step = U * p.group;
+    const int at_dn = p.x != nullptr ? step : 0, at_y = at_dn + (pre ? step : 0), at_h = at_y + (pre ? step : 0),
+              at_gate = at_h + (need_h ? step : 0);
+    // this lane's tensor
+    int left = (lane & 31) / R;
+    const uint8_t *base = nullptr;
+    for (const uint8_t *b : {p.x, pre ? p.dn : nullptr, pre ? p.y_in : nullptr, need_h ? p.h : nullptr,
+                             A::gate(p) == kGateToken ? p.gate : nullptr})
+        if (b != nullptr && left-- == 0) base = b;
 
-    auto row_of = [&](int64_t t) {
+    auto index_of = [&](int64_t i) {
         int64_t row = -1;
-        if (t < end) row = p.row_of_token == nullptr ? t : p.row_of_token[t];
+        if (i < count) row = p.row_of_token == nullptr ? begin + i : p.row_of_token[begin + i];
         return static_cast<int32_t>(row >= 0 && in_bounds(row < p.rows) ? row : -1);
     };
-    int32_t ahead = threadIdx.x == 0 ? row_of(begin) : -1;   // looked up a token early
-    auto fetch = [&](int64_t t, uint8_t *to, int slot) {
-        const int32_t row = ahead;
-        uint64_t *bar = full + slot;
-        ahead = row_of(t + 1);
-        rows[slot] = row;
-        if (row < 0) {
-            mbar_expect_tx(bar, 0);
-            return;
-        }
-        mbar_expect_tx(bar, row_bytes * p.tensors);
-        const int64_t at = static_cast<int64_t>(row) * row_bytes;
-        if (p.x != nullptr) bulk_load(to, p.x + at, row_bytes, bar);
-        if (pre) {
-            bulk_load(to + at_dn * place, p.dn + at, row_bytes, bar);
-            bulk_load(to + at_y * place, p.y_in + at, row_bytes, bar);
-        }
-        if (need_h) bulk_load(to + at_h * place, p.h + at, row_bytes, bar);
-        if (A::gate(p) == kGateToken) bulk_load(to + at_gate * place, p.gate + at, row_bytes, bar);
-    };
-    walk<R>(ring, begin, end, fetch, [&](int64_t t) {
-        int32_t row[R];
+    auto row_of = [&](int64_t, int32_t row) { return static_cast<int64_t>(row); };
+    walk<R>(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int64_t i, auto after) {
+        const uint4 *data[R];
+        int64_t at[R];      // of this thread's first unit, in bytes
+        bool there[R], waiting = true;
+        const int64_t t = begin + i;
 #pragma unroll
-        for (int r = 0; r < R; ++r) row[r] = t + r < end ? rows[ring.slot_of(r)] : -1;
-        auto from = [&](int r, int tensor, int k) { return ring.row(r, tensor)[lane + k * p.group]; };
-        auto put = [&](uint8_t *to, int r, int k, uint4 v) { store_unit(to, static_cast<int64_t>(row[r]) * p.units + lane + k * p.group, v); };
+        for (int r = 0; r < R; ++r) {
+            const int32_t row = ring.index[ring.slot * R + r];
+            there[r] = row >= 0;
+            at[r] = static_cast<int64_t>(row) * row_bytes + lane * 16;
+            data[r] = ring.row(r) + lane;
+        }
         backward_rows<BF16, U, R, F>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int r) { return row[r] >= 0; },
-            [&](int r, int k) { return p.x != nullptr ? from(r, 0, k) : make_uint4(0, 0, 0, 0); },
-            [&](int r, int k) { return from(r, at_dn, k); }, [&](int r, int k) { return from(r, at_y, k); },
-            [&](int r, int k) { return from(r, at_h, k); },
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int r) { return there[r]; },
+            [&](int r, int k) { return p.x != nullptr ? data[r][k * p.group] : make_uint4(0, 0, 0, 0); },
+            [&](int r, int k) { return data[r][at_dn + k * p.group]; }, [&](int r, int k) { return data[r][at_y + k * p.group]; },
+            [&](int r, int k) { return data[r][at_h + k * p.group]; },
             [&](int r) {
                 if (t + r < doc.hi) return;
                 if (doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
@@ -915,10 +923,20 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
                     own_gate[k * p.group] = g;
                 }
             },
-            [&](int r, int k) { return by_document ? own_gate[k * p.group] : from(r, at_gate, k); },
+            [&](int r, int k) { return by_document ? own_gate[k * p.group] : data[r][at_gate + k * p.group]; },
             [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(t + r), lane, p.group, bits); },
-            [&](auto &v) { sum(v); }, [&](int r, int k, uint4 v) { put(p.y, r, k, v); },
-            [&](int r, int k, uint4 v) { put(p.n, r, k, v); }, [&](int r, int k, uint4 v) { put(p.dgate, r, k, v); });
+            [&](auto &v) {
+                sum(v);
+                if (waiting) after();
+                waiting = false;
+            },
+            [&](int r, int k, uint4 v) { store_unit(p.y + at[r], k * p.group, v); },
+            [&](int r, int k, uint4 v) { store_unit(p.n + at[r], k * p.group, v); },
+            [&](int r, int k, uint4 v) { store_unit(p.dgate + at[r], k * p.group, v); });
+        if (waiting) {
+            sum.stop = __syncthreads_or(sum.ask);
+            after();
+        }
     });
     if (by_document && doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
 #pragma unroll
@@ -981,7 +999,7 @@ int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems 
 
 size_t ring_bytes(const ResidualParams &p, const Shape &s)
 {
-    return static_cast<size_t>(p.stages) * p.tensors * s.per_thread * s.group * 16 + gate_place(s, p.gate_kind);
+    return static_cast<size_t>(p.stages) * s.rows * p.tensors * s.per_thread * s.group * 16 + gate_place(s, p.gate_kind);
 }
 
 // A kernel's limit of dynamic shared memory, raised once on each device.
@@ -1089,7 +1107,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
     } else {
         deal(p.rows, s, device, p.per_group, ctas);
         p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
-        p.stages = stages_of(s, p.gate_kind, p.tensors);
+        p.stages = chunks_of(s, p.gate_kind, p.tensors);
     }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
@@ -1119,7 +1137,7 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     if (p.T > 0) {
         const bool need_h = p.post != nullptr || p.gate_kind != 0;
         p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
-        p.stages = s.shorter ? 0 : stages_of(s, p.gate_kind, p.tensors);
+        p.stages = s.shorter ? 0 : chunks_of(s, p.gate_kind, p.tensors);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
                                              : launch_backward<false>(p, s, grid, device, stream);

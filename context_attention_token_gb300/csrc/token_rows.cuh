@@ -183,6 +183,8 @@ struct BlockSum {
     static constexpr int kRoom = 2 * 256;   // floats
     float *room;                            // shared
     int turn = 0;
+    bool stop = false;                      // the vote of the last barrier: a thread has asked to stop
+    bool ask = false;
     __device__ explicit BlockSum(float *r) : room(r) {}
 
     // N values: lanes give away those that they do not keep, so that (for N = 6) 9 shuffles do for 30
@@ -209,7 +211,7 @@ struct BlockSum {
 #pragma unroll
         for (int d = W; d < 32; d *= 2) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
         if (lane < W) at[warp * W + lane] = s;   // lane i: value i
-        __syncthreads();
+        stop = __syncthreads_or(ask);
         s = 0.0f;
         for (int i = lane; i < warps * W; i += 32) s = __fadd_rn(s, at[i]);
 #pragma unroll
