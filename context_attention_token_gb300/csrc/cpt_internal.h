@@ -250,7 +250,7 @@ struct LogprobParams {
     int64_t units;                 // 16-byte units of a row, padding included
     int64_t vocab;
     float scale;
-    int64_t step_rows, step_units; // filled in by the launcher
+    int32_t split, group;          // filled in by the launcher: CTAs or lanes of a row
 };
 cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream);
 cudaError_t launch_token_logprob_backward(LogprobParams p, int dtype, cudaStream_t stream);

@@ -10,7 +10,10 @@
 #include "cpt_internal.h"
 #include "token_rows.cuh"
 
+#include <cooperative_groups.h>
 #include <math_constants.h>
+
+#include <cstring>
 
 namespace cpt {
 
@@ -18,6 +21,7 @@ namespace {
 
 constexpr float kLog2E = 1.4426950408889634f;
 
+// 2^x, off by 2^-22 of itself at most.
 __device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
@@ -45,20 +49,17 @@ __device__ __forceinline__ Sum joined(Sum a, Sum b, float c)
     return o;
 }
 
-constexpr int kRowThreads = 512;
-constexpr int kRowUnroll = 4;
-
-template <bool BF16>
-__device__ __forceinline__ void add_units(const uint4 (&raw)[kRowUnroll], const int64_t (&at)[kRowUnroll], int64_t vocab,
-                                          float c, Sum &sum)
+// Adds `N` units to a sum, the columns from `vocab` on left out.
+template <bool BF16, int N>
+__device__ __forceinline__ void add_units(const uint4 (&raw)[N], int64_t first, int64_t step, int64_t vocab, float c, Sum &sum)
 {
     constexpr int E = Unit<BF16>::E;
-    float x[kRowUnroll][E];
+    float x[N][E];
     float m = sum.m;
 #pragma unroll
-    for (int k = 0; k < kRowUnroll; ++k) {
+    for (int k = 0; k < N; ++k) {
         Unit<BF16>::unpack(raw[k], x[k]);
-        const int64_t left = vocab - at[k] * E;
+        const int64_t left = vocab - (first + k * step) * E;
         if (left < E) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -72,88 +73,163 @@ __device__ __forceinline__ void add_units(const uint4 (&raw)[kRowUnroll], const 
     sum.m = m;
     float s = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kRowUnroll; ++k)
+    for (int k = 0; k < N; ++k)
 #pragma unroll
         for (int e = 0; e < E; ++e) s = __fadd_rn(s, exp2_fast(__fmul_rn(__fsub_rn(x[k][e], r), c)));
     sum.s = __fadd_rn(sum.s, s);
 }
 
-// One CTA a token.
+// The row of a token that has a target, else -1.
+__device__ __forceinline__ int64_t scored_row(const LogprobParams &p, int64_t t, int64_t &target, bool count)
+{
+    target = p.targets[t];
+    if (target < 0 || target >= p.vocab) return -1;
+    const int64_t row = p.row_of_token == nullptr ? t : p.row_of_token[t];
+    return in_bounds(row >= 0 && row < p.rows, count) ? row : -1;
+}
+
+template <bool BF16>
+__device__ __forceinline__ float logit(const uint4 *row, int64_t column)
+{
+    if constexpr (BF16) return bf16_lo(reinterpret_cast<const uint16_t *>(row)[column]);
+    else return reinterpret_cast<const float *>(row)[column];
+}
+
+__device__ __forceinline__ void put_logprob(const LogprobParams &p, int64_t t, float wanted, Sum sum)
+{
+    const float l = logf(sum.s);
+    p.logp[t] = __fsub_rn(__fmul_rn(__fsub_rn(wanted, sum.m), p.scale), l);
+    p.stats[t] = make_float2(sum.m, l);
+}
+
+__device__ __forceinline__ void put_none(const LogprobParams &p, int64_t t)
+{
+    p.logp[t] = 0.0f;
+    p.stats[t] = make_float2(0.0f, 0.0f);
+}
+
+// Sum over the `group` lanes that share a row.
+__device__ __forceinline__ Sum lanes_joined(Sum sum, int group, float c)
+{
+    for (int d = group >> 1; d > 0; d >>= 1) {
+        const Sum other = {__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.s, d)};
+        sum = joined(sum, other, c);
+    }
+    return sum;
+}
+
+constexpr int kRowThreads = 512;
+constexpr int kRowUnroll = 4;
+constexpr int kShortThreads = 256;
+constexpr int kShortUnits = 512;   // of rows that a part of a warp reads
+
+// Long rows: p.split CTAs of a cluster a token, each a part of the row; their pairs are joined in the
+// first one's shared memory.
 template <bool BF16>
 __global__ void __launch_bounds__(kRowThreads) token_logprob_kernel(const __grid_constant__ LogprobParams p)
 {
     constexpr int E = Unit<BF16>::E;
-    __shared__ Sum room[32];
+    __shared__ Sum room[kRowThreads / 32], parts[8];
     const float c = __fmul_rn(p.scale, kLog2E);
     const int64_t units = (p.vocab + E - 1) / E;
-    for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
-        const int64_t target = p.targets[t];
-        const int64_t row = p.row_of_token == nullptr ? t : p.row_of_token[t];
-        if (target < 0 || target >= p.vocab || !in_bounds(row >= 0 && row < p.rows, threadIdx.x == 0)) {
-            if (threadIdx.x == 0) {
-                p.logp[t] = 0.0f;
-                p.stats[t] = make_float2(0.0f, 0.0f);
-            }
-            continue;
-        }
+    const int part = static_cast<int>(blockIdx.x % p.split);
+    const int64_t t = blockIdx.x / p.split;
+    const int64_t begin = units * part / p.split, end = units * (part + 1) / p.split;
+    int64_t target;
+    const int64_t row = scored_row(p, t, target, threadIdx.x == 0 && part == 0);
+    if (row < 0) {   // so in every CTA of the cluster
+        if (threadIdx.x == 0 && part == 0) put_none(p, t);
+        return;
+    }
+    const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + row * p.units;
+    float wanted = 0.0f;
+    if (threadIdx.x == 0 && part == 0) wanted = logit<BF16>(from, target);
+    Sum sum = {-CUDART_INF_F, 0.0f};
+    int64_t u = begin + threadIdx.x;
+    for (; u + (kRowUnroll - 1) * kRowThreads < end; u += kRowThreads * kRowUnroll) {
+        uint4 raw[kRowUnroll];
+#pragma unroll
+        for (int k = 0; k < kRowUnroll; ++k) raw[k] = ld_once(from + u + k * kRowThreads);
+        add_units<BF16, kRowUnroll>(raw, u, kRowThreads, p.vocab, c, sum);
+    }
+    for (; u < end; u += kRowThreads) {
+        uint4 raw[1] = {ld_once(from + u)};
+        add_units<BF16, 1>(raw, u, 0, p.vocab, c, sum);
+    }
+    sum = lanes_joined(sum, 32, c);
+    if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = sum;
+    __syncthreads();
+    if (threadIdx.x < 32) {
+        sum = threadIdx.x < kRowThreads / 32 ? room[threadIdx.x] : Sum{-CUDART_INF_F, 0.0f};
+        sum = lanes_joined(sum, 32, c);
+    }
+    if (p.split > 1) {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cluster = cg::this_cluster();
+        if (threadIdx.x == 0) *cluster.map_shared_rank(&parts[part], 0) = sum;
+        cluster.sync();
+        if (part != 0) return;
+        if (threadIdx.x == 0)
+            for (int i = 1; i < p.split; ++i) sum = joined(sum, parts[i], c);
+    }
+    if (threadIdx.x == 0) put_logprob(p, t, wanted, sum);
+}
+
+// Short rows: p.group lanes of a warp a token, the warp's tokens next to one another.
+template <bool BF16>
+__global__ void __launch_bounds__(kShortThreads) token_logprob_short_kernel(const __grid_constant__ LogprobParams p)
+{
+    constexpr int E = Unit<BF16>::E;
+    const float c = __fmul_rn(p.scale, kLog2E);
+    const int64_t units = (p.vocab + E - 1) / E;
+    const int lane = threadIdx.x & (p.group - 1);
+    const int64_t t = (static_cast<int64_t>(blockIdx.x) * kShortThreads + threadIdx.x) / p.group;
+    int64_t target = -1, row = -1;
+    if (t < p.T) row = scored_row(p, t, target, lane == 0);
+    Sum sum = {-CUDART_INF_F, 0.0f};
+    float wanted = 0.0f;
+    if (row >= 0) {
         const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + row * p.units;
-        float wanted = 0.0f;
-        if (threadIdx.x == 0) {
-            if (BF16) wanted = bf16_lo(reinterpret_cast<const uint16_t *>(from)[target]);
-            else wanted = reinterpret_cast<const float *>(from)[target];
-        }
-        Sum sum = {-CUDART_INF_F, 0.0f};
-        for (int64_t u = threadIdx.x; u < units; u += kRowThreads * kRowUnroll) {
+        if (lane == 0) wanted = logit<BF16>(from, target);
+        int64_t u = lane;
+        for (; u + (kRowUnroll - 1) * p.group < units; u += p.group * kRowUnroll) {
             uint4 raw[kRowUnroll];
-            int64_t at[kRowUnroll];
 #pragma unroll
-            for (int k = 0; k < kRowUnroll; ++k) {
-                at[k] = u + k * kRowThreads;
-                raw[k] = make_uint4(0, 0, 0, 0);
-                if (at[k] < units) raw[k] = ld_once(from + at[k]);
-            }
-            add_units<BF16>(raw, at, p.vocab, c, sum);
+            for (int k = 0; k < kRowUnroll; ++k) raw[k] = ld_once(from + u + k * p.group);
+            add_units<BF16, kRowUnroll>(raw, u, p.group, p.vocab, c, sum);
         }
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) {
-            Sum other = {__shfl_xor_sync(0xFFFFFFFFu, sum.m, d), __shfl_xor_sync(0xFFFFFFFFu, sum.s, d)};
-            sum = joined(sum, other, c);
-        }
-        __syncthreads();   // the last token's sums have been read
-        if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = sum;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kRowThreads / 32; ++w) sum = joined(sum, room[w], c);
-            const float l = logf(sum.s);
-            p.logp[t] = __fsub_rn(__fmul_rn(__fsub_rn(wanted, sum.m), p.scale), l);
-            p.stats[t] = make_float2(sum.m, l);
+        for (; u < units; u += p.group) {
+            uint4 raw[1] = {ld_once(from + u)};
+            add_units<BF16, 1>(raw, u, 0, p.vocab, c, sum);
         }
     }
+    sum = lanes_joined(sum, p.group, c);
+    if (lane != 0 || t >= p.T) return;
+    if (row < 0) put_none(p, t);
+    else put_logprob(p, t, wanted, sum);
 }
 
 // ----------------------------------------------------------------- gradient
 
-constexpr int kFlatThreads = 256;
-constexpr int kFlatUnroll = 4;
+constexpr int kTileThreads = 256;
+constexpr int kTileUnroll = 4;
+constexpr int kTileUnits = kTileThreads * kTileUnroll;
 
-// What a row's gradient needs besides its logits.
+// What a row's gradient needs besides its logits: dx = factor ([j = t] - 2^(c (x - m) - l2)).
 struct RowOf {
-    float m, l2, factor;   // dx = factor ([j = t] - 2^(c (x - m) - l2))
-    int64_t target;        // -1: the row is zeros
+    float m, l2, factor;
+    int32_t target;   // -1: the row is zeros
 };
 
 __device__ __forceinline__ RowOf row_of(const LogprobParams &p, int64_t row)
 {
-    RowOf r;
-    r.target = -1;
-    r.m = r.l2 = r.factor = 0.0f;
+    RowOf r = {0.0f, 0.0f, 0.0f, -1};
     const int64_t t = p.token_of_row == nullptr ? row : p.token_of_row[row];
     if (t < 0 || !in_bounds(t < p.T)) return r;
-    const int64_t target = p.targets[t];
-    if (target < 0 || target >= p.vocab) return r;
+    const int32_t target = p.targets[t];
     const float d = p.logp[t];
-    if (d == 0.0f) return r;
     const float2 st = p.stats[t];
+    if (target < 0 || target >= p.vocab || d == 0.0f) return r;
     r.target = target;
     r.m = st.x;
     r.l2 = __fmul_rn(st.y, kLog2E);
@@ -162,67 +238,71 @@ __device__ __forceinline__ RowOf row_of(const LogprobParams &p, int64_t row)
 }
 
 template <bool BF16>
-__device__ __forceinline__ uint4 gradient_unit(const uint4 &raw, const RowOf &r, int64_t unit, int64_t vocab, float c)
+__device__ __forceinline__ uint4 gradient_unit(const uint4 &raw, const RowOf &r, int32_t first, int32_t vocab, float c)
 {
     constexpr int E = Unit<BF16>::E;
-    float x[E];
-    Unit<BF16>::unpack(raw, x);
-    const int64_t first = unit * E;
+    typedef UnitPairs<BF16> V;
+    F2 x[V::N];
+    V::unpack(raw, x);
+    const F2 m = pair_of(-r.m, -r.m), cc = pair_of(c, c), l = pair_of(-r.l2, -r.l2), f = pair_of(-r.factor, -r.factor);
+    float y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) {
-        const float w = exp2_fast(__fmaf_rn(__fsub_rn(x[e], r.m), c, -r.l2));
-        x[e] = __fmul_rn(-r.factor, w);
+    for (int i = 0; i < V::N; ++i) {
+        const float2 a = both(fma2(add2(x[i], m), cc, l));
+        const float2 w = both(mul2(pair_of(exp2_fast(a.x), exp2_fast(a.y)), f));
+        y[2 * i] = w.x;
+        y[2 * i + 1] = w.y;
     }
-    const int64_t to = r.target - first;
-    if (to >= 0 && to < E) {
+    // the unit of the target, the one at the vocabulary's end
+    const uint32_t to = static_cast<uint32_t>(r.target - first);
+    if (to < E || first + E > vocab) {
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (e == to) x[e] = __fadd_rn(r.factor, x[e]);
+        for (int e = 0; e < E; ++e) {
+            if (e == to) y[e] = __fadd_rn(r.factor, y[e]);
+            if (first + e >= vocab) y[e] = 0.0f;
+        }
     }
-    if (first + E > vocab) {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            if (first + e >= vocab) x[e] = 0.0f;
-    }
-    return Unit<BF16>::pack(x);
+    return Unit<BF16>::pack(y);
 }
 
+// A CTA takes kTileUnits neighbouring units of the logits, of a part of a row or of several. What it needs of the rows is looked up
+// first, once a row.
 template <bool BF16>
-__global__ void __launch_bounds__(kFlatThreads) token_logprob_backward_kernel(const __grid_constant__ LogprobParams p)
+__global__ void __launch_bounds__(kTileThreads) token_logprob_backward_kernel(const __grid_constant__ LogprobParams p)
 {
+    constexpr int E = Unit<BF16>::E;
+    extern __shared__ __align__(16) uint8_t smem[];
+    RowOf *rows = reinterpret_cast<RowOf *>(smem);
     const float c = __fmul_rn(p.scale, kLog2E);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kFlatThreads;
-    const int64_t items = p.rows * p.units;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * kFlatThreads + threadIdx.x;
-    int64_t row = i / p.units, unit = i - row * p.units;
-    for (; i < items; i += stride * kFlatUnroll) {
-        uint4 raw[kFlatUnroll];
-        RowOf of[kFlatUnroll];
-        int64_t at[kFlatUnroll];
+    const int64_t items = p.rows * p.units, start = static_cast<int64_t>(blockIdx.x) * kTileUnits;
+    const int64_t row0 = start / p.units;
+    const uint32_t units = static_cast<uint32_t>(p.units), skip = static_cast<uint32_t>(start - row0 * p.units);
+    const uint32_t here = static_cast<uint32_t>(min(items - start, static_cast<int64_t>(kTileUnits)));
+    const uint32_t n = (skip + here - 1) / units + 1;
+    for (uint32_t i = threadIdx.x; i < n; i += kTileThreads) rows[i] = row_of(p, row0 + i);
+    __syncthreads();
+    const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + start;
+    uint4 *to = reinterpret_cast<uint4 *>(p.dlogits) + start;
+    uint4 raw[kTileUnroll];
+    RowOf of[kTileUnroll];
+    uint32_t column[kTileUnroll];
 #pragma unroll
-        for (int k = 0; k < kFlatUnroll; ++k) {
-            const int64_t j = i + k * stride;
-            at[k] = unit;
-            of[k].target = -1;
-            if (j < items) {
-                of[k] = row_of(p, row);
-                if (of[k].target >= 0) raw[k] = __ldcs(reinterpret_cast<const uint4 *>(p.logits) + j);
-            }
-            row += p.step_rows;
-            unit += p.step_units;
-            if (unit >= p.units) {
-                unit -= p.units;
-                ++row;
-            }
-        }
+    for (int k = 0; k < kTileUnroll; ++k) {
+        const uint32_t i = threadIdx.x + k * kTileThreads;
+        of[k].target = -1;
+        if (i >= here) continue;
+        const uint32_t q = (skip + i) / units;
+        column[k] = (skip + i - q * units) * E;
+        of[k] = rows[q];
+        if (of[k].target >= 0) raw[k] = __ldcs(from + i);
+    }
 #pragma unroll
-        for (int k = 0; k < kFlatUnroll; ++k) {
-            const int64_t j = i + k * stride;
-            if (j >= items) continue;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (of[k].target >= 0) v = gradient_unit<BF16>(raw[k], of[k], at[k], p.vocab, c);
-            __stcs(reinterpret_cast<uint4 *>(p.dlogits) + j, v);
-        }
+    for (int k = 0; k < kTileUnroll; ++k) {
+        const uint32_t i = threadIdx.x + k * kTileThreads;
+        if (i >= here) continue;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (of[k].target >= 0) v = gradient_unit<BF16>(raw[k], of[k], column[k], static_cast<int32_t>(p.vocab), c);
+        __stcs(to + i, v);
     }
 }
 
@@ -231,24 +311,48 @@ __global__ void __launch_bounds__(kFlatThreads) token_logprob_backward_kernel(co
 cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream)
 {
     if (p.T == 0) return cudaSuccess;
-    const unsigned grid = static_cast<unsigned>(p.T);
-    if (dtype == kBf16) token_logprob_kernel<true><<<grid, kRowThreads, 0, stream>>>(p);
-    else token_logprob_kernel<false><<<grid, kRowThreads, 0, stream>>>(p);
-    return cudaGetLastError();
+    const int per = dtype == kBf16 ? 8 : 4;
+    const int64_t units = (p.vocab + per - 1) / per;
+    if (units <= kShortUnits) {
+        p.group = 1;
+        while (p.group < 32 && p.group * 2 <= units) p.group *= 2;
+        const int64_t ctas = (p.T * p.group + kShortThreads - 1) / kShortThreads;
+        if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+        const unsigned grid = static_cast<unsigned>(ctas);
+        if (dtype == kBf16) token_logprob_short_kernel<true><<<grid, kShortThreads, 0, stream>>>(p);
+        else token_logprob_short_kernel<false><<<grid, kShortThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    // few tokens: a row's columns over several CTAs, as many as the SMs take at once, 512 units each at least
+    const int64_t room = 3 * static_cast<int64_t>(sm_count(-1));
+    p.split = 1;
+    while (p.split < 8 && p.T * p.split * 2 <= room && units >= p.split * 2 * kRowThreads) p.split *= 2;
+    if (p.T * p.split > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    cudaLaunchConfig_t config;
+    memset(&config, 0, sizeof config);
+    config.gridDim = dim3(static_cast<unsigned>(p.T * p.split));
+    config.blockDim = dim3(kRowThreads);
+    config.stream = stream;
+    cudaLaunchAttribute cluster;
+    cluster.id = cudaLaunchAttributeClusterDimension;
+    cluster.val.clusterDim = {static_cast<unsigned>(p.split), 1, 1};
+    config.attrs = &cluster;
+    config.numAttrs = p.split > 1 ? 1 : 0;
+    return dtype == kBf16 ? cudaLaunchKernelEx(&config, token_logprob_kernel<true>, p)
+                          : cudaLaunchKernelEx(&config, token_logprob_kernel<false>, p);
 }
 
 cudaError_t launch_token_logprob_backward(LogprobParams p, int dtype, cudaStream_t stream)
 {
     const int64_t items = p.rows * p.units;
     if (items == 0) return cudaSuccess;
-    const int64_t ctas = (items + kFlatThreads * kFlatUnroll - 1) / (kFlatThreads * kFlatUnroll);
-    const int64_t most = 8 * static_cast<int64_t>(sm_count(-1));
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    const int64_t stride = static_cast<int64_t>(grid) * kFlatThreads;
-    p.step_rows = stride / p.units;
-    p.step_units = stride % p.units;
-    if (dtype == kBf16) token_logprob_backward_kernel<true><<<grid, kFlatThreads, 0, stream>>>(p);
-    else token_logprob_backward_kernel<false><<<grid, kFlatThreads, 0, stream>>>(p);
+    const int64_t ctas = (items + kTileUnits - 1) / kTileUnits;
+    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(ctas);
+    // the most rows that a tile touches
+    const size_t shared = sizeof(RowOf) * static_cast<size_t>((kTileUnits - 1) / p.units + 2);
+    if (dtype == kBf16) token_logprob_backward_kernel<true><<<grid, kTileThreads, shared, stream>>>(p);
+    else token_logprob_backward_kernel<false><<<grid, kTileThreads, shared, stream>>>(p);
     return cudaGetLastError();
 }
 
