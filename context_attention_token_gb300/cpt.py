@@ -768,9 +768,15 @@ def _row_count(plan: Plan, order: int) -> int:
 def _row_width(plan: Plan, order: int, t: torch.Tensor) -> int:
     """Elements of a row of [P, T_pad/P, ...] or [T_pad, ...] (LOCAL), [T, ...] (GLOBAL)."""
     rows, shape = _row_count(plan, order), t.shape
-    lead = 2 if order and len(shape) > 2 and shape[0] == plan.cp_size and shape[0] * shape[1] == rows else 1
-    if len(shape) <= lead or (lead == 1 and shape[0] != rows):
+    dims = len(shape)
+    if order and dims > 2 and shape[0] == plan.cp_size and shape[0] * shape[1] == rows:
+        lead = 2
+    elif dims > 1 and shape[0] == rows:
+        lead = 1
+    else:
         raise ValueError(f"a tensor of shape {tuple(shape)} does not hold {rows} rows")
+    if rows:
+        return t.numel() // rows
     width = 1
     for n in shape[lead:]:
         width *= n
@@ -779,13 +785,13 @@ def _row_width(plan: Plan, order: int, t: torch.Tensor) -> int:
 
 def _rows_of(plan: Plan, order: int, first, others, what: str) -> int:
     """Elements of a row of `first`, like which the others must be."""
-    width = _row_width(plan, order, first)
+    width, shape, dtype = _row_width(plan, order, first), first.shape, first.dtype
     for t in others:
         if t is None:
             continue
-        if t.dtype != first.dtype:
+        if t.dtype != dtype:
             raise ValueError(f"{what} differ in dtype")
-        if _row_width(plan, order, t) != width:
+        if t.shape != shape and _row_width(plan, order, t) != width:
             raise ValueError(f"{what} differ in width")
     return width
 
@@ -813,24 +819,25 @@ def cpt_dropout(plan: Plan, src: torch.Tensor, dst: torch.Tensor, p: float, rng:
                             site & 0xFFFFFFFF, _stream(stream)))
 
 
+def _floats(t, count: int, what: str) -> int:
+    """The pointer of an optional float32 tensor of at least `count` elements."""
+    if t is None:
+        return 0
+    if t.dtype != torch.float32 or t.numel() < count:
+        raise ValueError(f"{what} must hold {count} float32 values")
+    return _ptr(t)
+
+
 def _residual_options(plan: Plan, width: int, dtype, order: int, post_weight, gate, gate_per_document, scale, p, rng,
                       site, pre_weight, eps):
-    o = _Residual()
-    for name, w in (("post_weight", post_weight), ("pre_weight", pre_weight)):
-        if w is None:
-            continue
-        if w.dtype != torch.float32 or w.numel() < width:
-            raise ValueError(f"{name} must hold {width} float32 values")
-        setattr(o, name, _ptr(w))
+    gate_ptr, kind = 0, CPT_GATE_NONE
     if gate is not None:
         rows = plan.n_docs if gate_per_document else _row_count(plan, order)
         if gate.dtype != dtype or gate.numel() < rows * width:
             raise ValueError(f"gate must hold {rows} rows of {width} elements of the tensors' dtype")
-        o.gate = _there(gate)
-        o.gate_kind = CPT_GATE_DOCUMENT if gate_per_document else CPT_GATE_TOKEN
-    o.scale, o.eps, o.p = scale, eps, p
-    o.rng, o.site = _rng_ptr(rng, p), site & 0xFFFFFFFF
-    return o
+        gate_ptr, kind = _there(gate), CPT_GATE_DOCUMENT if gate_per_document else CPT_GATE_TOKEN
+    return _Residual(_floats(post_weight, width, "post_weight"), _floats(pre_weight, width, "pre_weight"), gate_ptr, kind,
+                     scale, eps, p, _rng_ptr(rng, p), site & 0xFFFFFFFF)
 
 
 def cpt_residual_norm(plan: Plan, x: torch.Tensor, h, y, n, *, post_weight=None, gate=None,
@@ -860,9 +867,7 @@ def cpt_residual_norm_backward(plan: Plan, h, y, dy, dn, dx: torch.Tensor, dh, *
     width = _rows_of(plan, order, dx, (h, y, dy, dn, dh), "h, y, dy, dn, dx and dh")
     o = _residual_options(plan, width, dx.dtype, order, post_weight, gate, gate_per_document, scale, p, rng, site,
                           pre_weight, eps)
-    for name, w in (("dpost_weight", dpost_weight), ("dpre_weight", dpre_weight)):
-        if w is not None and (w.dtype != torch.float32 or w.numel() < width):
-            raise ValueError(f"{name} must hold {width} float32 values")
+    dpost, dpre = _floats(dpost_weight, width, "dpost_weight"), _floats(dpre_weight, width, "dpre_weight")
     if dgate is not None:
         rows, kind = (plan.n_docs, torch.float32) if gate_per_document else (_row_count(plan, order), dx.dtype)
         if dgate.dtype != kind or dgate.numel() < rows * width:
@@ -873,7 +878,7 @@ def cpt_residual_norm_backward(plan: Plan, h, y, dy, dn, dx: torch.Tensor, dh, *
         need = cpt_residual_norm_backward_workspace_bytes(plan, width, dx.dtype)
         workspace = torch.empty(max(need, 256), dtype=torch.uint8, device="cuda")
     _check(_lib.cpt_residual_norm_backward(plan.handle, _there(h), _there(y), _there(dy), _there(dn), _there(dx),
-                                           _there(dh), _there(dgate), _ptr(dpost_weight), _ptr(dpre_weight), width,
+                                           _there(dh), _there(dgate), dpost, dpre, width,
                                            _dtype_code(dx), order, ctypes.byref(o), _ptr(workspace), _nbytes(workspace),
                                            _stream(stream)))
 
@@ -920,15 +925,12 @@ def cpt_policy_loss(plan: Plan, logp: torch.Tensor, logp_old: torch.Tensor, adva
     """terms [n_docs, 4] (loss, KL, clipped share, tokens) of the clipped policy loss and dlogp [T], the gradient
     of the documents' losses, weighted. mask is bool or uint8 [T]; weights None: 1 / n_docs each."""
     T, n = plan.total_tokens, plan.n_docs
-    for t, count, what in ((logp, T, "logp"), (logp_old, T, "logp_old"), (logp_ref, T, "logp_ref"), (dlogp, T, "dlogp"),
-                           (advantages, n, "advantages"), (weights, n, "weights"), (terms, 4 * n, "terms")):
-        if t is not None and (t.dtype != torch.float32 or t.numel() < count):
-            raise ValueError(f"{what} must hold {count} float32 values")
     if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.numel() < T):
         raise ValueError(f"mask must hold {T} values of bool or uint8")
-    _check(_lib.cpt_policy_loss(plan.handle, _ptr(logp), _ptr(logp_old), _ptr(logp_ref), _ptr(mask), _ptr(advantages),
-                                _ptr(weights), clip_low, clip_high, kl_coef, _ptr(terms), _ptr(dlogp),
-                                _stream(stream)))
+    _check(_lib.cpt_policy_loss(plan.handle, _floats(logp, T, "logp"), _floats(logp_old, T, "logp_old"),
+                                _floats(logp_ref, T, "logp_ref"), _ptr(mask), _floats(advantages, n, "advantages"),
+                                _floats(weights, n, "weights"), clip_low, clip_high, kl_coef,
+                                _floats(terms, 4 * n, "terms"), _floats(dlogp, T, "dlogp"), _stream(stream)))
 
 
 # ------------------------------------------------------------------ epochs

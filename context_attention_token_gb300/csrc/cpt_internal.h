@@ -270,8 +270,9 @@ struct PolicyParams {
     float4 *terms;
     float *dlogp;
     int32_t longest;                          // tokens of the longest document
+    int32_t docs;                             // filled in by the launcher: documents of a cluster
 };
-cudaError_t launch_policy_loss(const PolicyParams &p, cudaStream_t stream);
+cudaError_t launch_policy_loss(PolicyParams p, cudaStream_t stream);
 
 // Streaming ceiling: dst = copy of srcs[0], srcs[1..n_src) read and
 // discarded, through the bulk-copy engine in blocks of block_bytes and a ring
