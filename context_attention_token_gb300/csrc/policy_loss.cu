@@ -8,8 +8,8 @@
 // as two floats (the rounded difference and its error), and so are the borders' logarithms. kl comes from its
 // series where the terms cancel.
 //
-// The gradient needs the number of tokens that count, so a document's mask is read first; its sums stay within a warp, a CTA or
-// a cluster, so that one launch does.
+// The gradient's weight needs the number of tokens that count. So the gradients wait for it in registers (in dlogp, where a
+// thread has more than kTokens), and a document's sums stay within a warp, a CTA or a cluster, so that one launch does.
 #include "cpt_internal.h"
 #include "token_rows.cuh"
 
@@ -22,8 +22,9 @@ namespace cpt {
 namespace {
 
 constexpr int kThreads = 512;
-constexpr int kWarpTokens = 512;       // of a document that a warp takes
-constexpr int kClusterTokens = 8192;   // of one that is worth a cluster
+constexpr int kTokens = 8;                            // of a thread at a time
+constexpr int kWarpTokens = 128;                      // of a document that a warp takes
+constexpr int kClusterTokens = kTokens * kThreads;    // a longer one is worth a cluster
 
 // a - b and what its rounding left out.
 __device__ __forceinline__ void exact_difference(float a, float b, float &d, float &rest)
@@ -65,16 +66,32 @@ struct LongSum {
 // What a thread finds in its tokens.
 struct Found {
     LongSum loss, kl;
-    int held = 0;
+    int held = 0, count = 0;
 };
 
-__device__ __forceinline__ void add_token(const PolicyParams &p, int64_t t, float A, float weight, Found &f)
+// K tokens from t on, every `step`-th below hi: into `f`, and the gradients before the weight into g.
+template <int K>
+__device__ __forceinline__ void add_tokens(const PolicyParams &p, int64_t t, int64_t step, int64_t hi, float A, Found &f, float (&g)[K])
 {
-    float g = 0.0f;
-    if (p.mask == nullptr || p.mask[t] != 0) {
-        const float logp = p.logp[t];
+    float logp[K], old[K], ref[K];
+    bool on[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {   // all loads at once; what is masked is not used
+        const int64_t at = t + k * step;
+        on[k] = false;
+        logp[k] = old[k] = ref[k] = 0.0f;
+        if (at >= hi) continue;
+        on[k] = p.mask == nullptr || p.mask[at] != 0;
+        logp[k] = p.logp[at];
+        old[k] = p.old[at];
+        if (p.ref != nullptr) ref[k] = p.ref[at];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        g[k] = 0.0f;
+        if (!on[k]) continue;
         float u, rest;
-        exact_difference(logp, p.old[t], u, rest);
+        exact_difference(logp[k], old[k], u, rest);
         const bool above = __fadd_rn(__fsub_rn(u, p.high_hi), __fsub_rn(rest, p.high_lo)) > 0.0f;
         const bool below = __fadd_rn(__fsub_rn(u, p.low_hi), __fsub_rn(rest, p.low_lo)) < 0.0f;
         const bool held = (above && A > 0.0f) || (below && A < 0.0f);
@@ -82,29 +99,19 @@ __device__ __forceinline__ void add_token(const PolicyParams &p, int64_t t, floa
         const float ar = __fmul_rn(-A, __fmul_rn(r, __fadd_rn(1.0f, rest)));
         f.loss.add(held ? __fmul_rn(-A, above ? p.above : p.below) : ar);
         f.held += held;
-        g = held ? 0.0f : ar;
+        ++f.count;
+        g[k] = held ? 0.0f : ar;
         if (p.ref != nullptr) {
-            const float e = __fsub_rn(p.ref[t], logp);
+            const float e = __fsub_rn(ref[k], logp[k]);
             f.kl.add(exp_less_line(e));
-            g = __fmaf_rn(-p.kl, expm1f(e), g);
+            g[k] = __fmaf_rn(-p.kl, expm1f(e), g[k]);
         }
-        g = __fmul_rn(g, weight);
     }
-    p.dlogp[t] = g;
 }
 
 __device__ __forceinline__ float4 terms_of(const PolicyParams &p, float loss, float kl, float held, float n, float share)
 {
     return make_float4(__fmul_rn(__fmaf_rn(p.kl, kl, loss), share), __fmul_rn(kl, share), __fmul_rn(held, share), n);
-}
-
-// Tokens of [lo, hi) that count, those of every `step`-th from lo + first on.
-__device__ __forceinline__ int count_tokens(const PolicyParams &p, int64_t lo, int64_t hi, int first, int step)
-{
-    int n = 0;
-#pragma unroll 8
-    for (int64_t t = lo + first; t < hi; t += step) n += p.mask[t] != 0;
-    return n;
 }
 
 // A cluster of S CTAs takes p.docs neighbouring documents: the short ones a warp each, then the others one after the
@@ -113,8 +120,9 @@ template <int S>
 __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_constant__ PolicyParams p)
 {
     namespace cg = cooperative_groups;
+    constexpr int kSums = 5;                   // loss, kl, held; tokens, in units of one and of 4096: exact for any length
     __shared__ float room[BlockSum::kRoom];
-    __shared__ float shares[2][8][5];   // of two documents in turn, every CTA's: counts (two floats), then sums
+    __shared__ float shares[2][S][kSums];      // of two documents in turn, every CTA's
     BlockSum sum(room);
     const int rank = S == 1 ? 0 : static_cast<int>(blockIdx.x % S), lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x / S) * p.docs;
@@ -123,68 +131,66 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
     for (int64_t d = first + rank * (kThreads / 32) + (threadIdx.x >> 5); d < last; d += S * (kThreads / 32)) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
         if (hi - lo > kWarpTokens) continue;
-        float n = static_cast<float>(hi - lo);
-        if (p.mask != nullptr) n = static_cast<float>(__reduce_add_sync(0xFFFFFFFFu, count_tokens(p, lo, hi, lane, 32)));
-        const float share = __fdiv_rn(1.0f, fmaxf(n, 1.0f));
-        const float weight = __fmul_rn(p.weights == nullptr ? p.weight : p.weights[d], share);
+        const float A = p.advantages[d], own = p.weights == nullptr ? p.weight : p.weights[d];
         Found f;
-        for (int64_t t = lo + lane; t < hi; t += 32) add_token(p, t, p.advantages[d], weight, f);
-        float v[3] = {f.loss.value(), f.kl.value(), static_cast<float>(f.held)};
-        lanes_sum<3>(v, 32);
-        if (lane == 0) p.terms[d] = terms_of(p, v[0], v[1], v[2], n, share);
+        float g[kWarpTokens / 32];
+        add_tokens<kWarpTokens / 32>(p, lo + lane, 32, hi, A, f, g);
+        float v[4] = {f.loss.value(), f.kl.value(), static_cast<float>(f.held), static_cast<float>(f.count)};
+        lanes_sum<4>(v, 32);
+        const float share = __fdiv_rn(1.0f, fmaxf(v[3], 1.0f)), weight = __fmul_rn(own, share);
+#pragma unroll
+        for (int k = 0; k < kWarpTokens / 32; ++k)
+            if (lo + lane + k * 32 < hi) p.dlogp[lo + lane + k * 32] = __fmul_rn(g[k], weight);
+        if (lane == 0) p.terms[d] = terms_of(p, v[0], v[1], v[2], v[3], share);
     }
 
     int turn = 0;
     for (int64_t d = first; d < last; ++d) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
         if (hi - lo <= kWarpTokens) continue;
-        float(*mine)[5] = shares[turn];
-        turn ^= 1;
-        const int at = rank * kThreads + threadIdx.x;
-        float n = static_cast<float>(hi - lo);
-        if (p.mask != nullptr) {
-            // whole numbers in two floats, of 4096 and of one: exact for any length
-            const int c = count_tokens(p, lo, hi, at, S * kThreads);
-            float v[2] = {static_cast<float>(c & 0xFFF), static_cast<float>(c >> 12)};
-            sum(v);
-            if constexpr (S > 1) {
-                cg::cluster_group cluster = cg::this_cluster();
-                if (threadIdx.x < S) {
-                    float *to = cluster.map_shared_rank(&mine[rank][0], threadIdx.x);
-                    to[0] = v[0];
-                    to[1] = v[1];
-                }
-                cluster.sync();
-                v[0] = v[1] = 0.0f;
-                for (int i = 0; i < S; ++i) {
-                    v[0] = __fadd_rn(v[0], mine[i][0]);
-                    v[1] = __fadd_rn(v[1], mine[i][1]);
-                }
-            }
-            n = __fmaf_rn(v[1], 4096.0f, v[0]);
-        }
-        const float share = __fdiv_rn(1.0f, fmaxf(n, 1.0f));
-        const float weight = __fmul_rn(p.weights == nullptr ? p.weight : p.weights[d], share);
-        const float A = p.advantages[d];
+        const float A = p.advantages[d], own = p.weights == nullptr ? p.weight : p.weights[d];
+        const int64_t t = lo + rank * kThreads + threadIdx.x, step = S * kThreads;
+        const bool held_back = hi - lo <= kTokens * step;   // a thread's gradients wait in registers for the weight
         Found f;
-#pragma unroll 4
-        for (int64_t t = lo + at; t < hi; t += S * kThreads) add_token(p, t, A, weight, f);
-        float v[3] = {f.loss.value(), f.kl.value(), static_cast<float>(f.held)};
+        float g[kTokens];
+        for (int64_t at = t; at < hi; at += kTokens * step) {
+            add_tokens<kTokens>(p, at, step, hi, A, f, g);
+            if (held_back) break;
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k)
+                if (at + k * step < hi) p.dlogp[at + k * step] = g[k];
+        }
+        float v[kSums] = {f.loss.value(), f.kl.value(), static_cast<float>(f.held), static_cast<float>(f.count & 0xFFF),
+                          static_cast<float>(f.count >> 12)};
         sum(v);
         if constexpr (S > 1) {
+            namespace cg = cooperative_groups;
             cg::cluster_group cluster = cg::this_cluster();
-            if (threadIdx.x == 0) {
-                float *to = cluster.map_shared_rank(&mine[rank][2], 0);
-                for (int i = 0; i < 3; ++i) to[i] = v[i];
+            float(*mine)[kSums] = shares[turn];
+            turn ^= 1;
+            if (threadIdx.x < S) {
+                float *to = cluster.map_shared_rank(&mine[rank][0], threadIdx.x);
+#pragma unroll
+                for (int j = 0; j < kSums; ++j) to[j] = v[j];
             }
-            // behind it the first CTA has all sums, and no CTA has ended that is still written to
+            // A place is written again two documents on, behind the barrier of the next, which every CTA reaches only
+            // after it has read; and behind this one no CTA is written to any more that may have ended.
             cluster.sync();
-            if (rank == 0 && threadIdx.x == 0) {
-                for (int j = 0; j < 3; ++j) {
-                    v[j] = mine[0][2 + j];
-                    for (int i = 1; i < S; ++i) v[j] = __fadd_rn(v[j], mine[i][2 + j]);
-                }
+#pragma unroll
+            for (int j = 0; j < kSums; ++j) {
+                v[j] = mine[0][j];
+                for (int i = 1; i < S; ++i) v[j] = __fadd_rn(v[j], mine[i][j]);
             }
+        }
+        const float n = __fmaf_rn(v[4], 4096.0f, v[3]);
+        const float share = __fdiv_rn(1.0f, fmaxf(n, 1.0f)), weight = __fmul_rn(own, share);
+        if (held_back) {
+#pragma unroll
+            for (int k = 0; k < kTokens; ++k)
+                if (t + k * step < hi) p.dlogp[t + k * step] = __fmul_rn(g[k], weight);
+        } else {
+#pragma unroll 4
+            for (int64_t at = t; at < hi; at += step) p.dlogp[at] = __fmul_rn(p.dlogp[at], weight);
         }
         if (rank == 0 && threadIdx.x == 0) p.terms[d] = terms_of(p, v[0], v[1], v[2], n, share);
     }

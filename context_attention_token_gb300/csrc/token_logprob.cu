@@ -49,34 +49,89 @@ __device__ __forceinline__ Sum joined(Sum a, Sum b, float c)
     return o;
 }
 
-// Adds `N` units to a sum, the columns from `vocab` on left out.
-template <bool BF16, int N>
-__device__ __forceinline__ void add_units(const uint4 (&raw)[N], int64_t first, int64_t step, int64_t vocab, float c, Sum &sum)
+// The larger of two bf16 pairs, half by half; a NaN loses.
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
 {
-    constexpr int E = Unit<BF16>::E;
-    float x[N][E];
+    uint32_t d;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// A word without weight: -inf in every column.
+template <bool BF16>
+constexpr uint32_t kNoWeight = BF16 ? 0xFF80FF80u : 0xFF800000u;
+
+// Adds N units to a sum.
+template <bool BF16, int N>
+__device__ __forceinline__ void add_units(const uint4 (&raw)[N], float c, Sum &sum)
+{
+    typedef UnitPairs<BF16> V;
     float m = sum.m;
+    if constexpr (BF16) {
+        uint32_t w = raw[0].x;
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        Unit<BF16>::unpack(raw[k], x[k]);
-        const int64_t left = vocab - (first + k * step) * E;
-        if (left < E) {
+        for (int k = 0; k < N; ++k) w = max_bf16x2(max_bf16x2(w, raw[k].x), max_bf16x2(raw[k].y, max_bf16x2(raw[k].z, raw[k].w)));
+        m = fmaxf(m, fmaxf(bf16_lo(w), bf16_hi(w)));
+    } else {
 #pragma unroll
-            for (int e = 0; e < E; ++e)
-                if (e >= left) x[k][e] = -CUDART_INF_F;
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e) m = fmaxf(m, x[k][e]);
+        for (int k = 0; k < N; ++k)
+            m = fmaxf(m, fmaxf(fmaxf(__uint_as_float(raw[k].x), __uint_as_float(raw[k].y)),
+                               fmaxf(__uint_as_float(raw[k].z), __uint_as_float(raw[k].w))));
     }
     const float r = reference(m);
     if (m != sum.m) sum.s = __fmul_rn(sum.s, exp2_fast(__fmul_rn(__fsub_rn(sum.m, r), c)));
     sum.m = m;
-    float s = 0.0f;
+    const F2 minus = pair_of(-r, -r), cc = pair_of(c, c);
+    F2 s[2] = {pair_of(0.0f, 0.0f), pair_of(0.0f, 0.0f)};
 #pragma unroll
-    for (int k = 0; k < N; ++k)
+    for (int k = 0; k < N; ++k) {
+        F2 x[V::N];
+        V::unpack(raw[k], x);
 #pragma unroll
-        for (int e = 0; e < E; ++e) s = __fadd_rn(s, exp2_fast(__fmul_rn(__fsub_rn(x[k][e], r), c)));
-    sum.s = __fadd_rn(sum.s, s);
+        for (int i = 0; i < V::N; ++i) {
+            const float2 a = both(mul2(add2(x[i], minus), cc));
+            s[i & 1] = add2(s[i & 1], pair_of(exp2_fast(a.x), exp2_fast(a.y)));
+        }
+    }
+    const float2 t = both(add2(s[0], s[1]));
+    sum.s = __fadd_rn(sum.s, __fadd_rn(t.x, t.y));
+}
+
+// The units from `u` on, every `step`-th below `end`, of a row of `vocab` columns.
+template <bool BF16, int N>
+__device__ __forceinline__ Sum sum_units(const uint4 *row, int64_t u, int64_t step, int64_t end, int64_t vocab, float c)
+{
+    constexpr int E = Unit<BF16>::E;
+    constexpr uint32_t none = kNoWeight<BF16>;
+    Sum sum = {-CUDART_INF_F, 0.0f};
+    for (; u < end; u += step * N) {
+        uint4 raw[N];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            raw[k] = make_uint4(none, none, none, none);
+            if (u + k * step < end) raw[k] = ld_once(row + u + k * step);
+        }
+        // the row's last unit may hold columns past the vocabulary
+        if ((u + (N - 1) * step + 1) * E > vocab) {
+#pragma unroll
+            for (int k = 0; k < N; ++k) {
+                const int64_t left = vocab - (u + k * step) * E;
+                uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (BF16) {
+                        if (2 * i + 1 >= left) w[i] = (w[i] & 0xFFFFu) | (none << 16);
+                        if (2 * i >= left) w[i] = none;
+                    } else if (i >= left) {
+                        w[i] = none;
+                    }
+                }
+                raw[k] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+        add_units<BF16, N>(raw, c, sum);
+    }
+    return sum;
 }
 
 // The row of a token that has a target, else -1.
@@ -119,7 +174,8 @@ __device__ __forceinline__ Sum lanes_joined(Sum sum, int group, float c)
 }
 
 constexpr int kRowThreads = 512;
-constexpr int kRowUnroll = 4;
+constexpr int kRowUnroll = 8;
+constexpr int kShortUnroll = 4;
 constexpr int kShortThreads = 256;
 constexpr int kShortUnits = 512;   // of rows that a part of a warp reads
 
@@ -144,18 +200,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logprob_kernel(const __grid
     const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + row * p.units;
     float wanted = 0.0f;
     if (threadIdx.x == 0 && part == 0) wanted = logit<BF16>(from, target);
-    Sum sum = {-CUDART_INF_F, 0.0f};
-    int64_t u = begin + threadIdx.x;
-    for (; u + (kRowUnroll - 1) * kRowThreads < end; u += kRowThreads * kRowUnroll) {
-        uint4 raw[kRowUnroll];
-#pragma unroll
-        for (int k = 0; k < kRowUnroll; ++k) raw[k] = ld_once(from + u + k * kRowThreads);
-        add_units<BF16, kRowUnroll>(raw, u, kRowThreads, p.vocab, c, sum);
-    }
-    for (; u < end; u += kRowThreads) {
-        uint4 raw[1] = {ld_once(from + u)};
-        add_units<BF16, 1>(raw, u, 0, p.vocab, c, sum);
-    }
+    Sum sum = sum_units<BF16, kRowUnroll>(from, begin + threadIdx.x, kRowThreads, end, p.vocab, c);
     sum = lanes_joined(sum, 32, c);
     if ((threadIdx.x & 31) == 0) room[threadIdx.x >> 5] = sum;
     __syncthreads();
@@ -191,17 +236,7 @@ __global__ void __launch_bounds__(kShortThreads) token_logprob_short_kernel(cons
     if (row >= 0) {
         const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + row * p.units;
         if (lane == 0) wanted = logit<BF16>(from, target);
-        int64_t u = lane;
-        for (; u + (kRowUnroll - 1) * p.group < units; u += p.group * kRowUnroll) {
-            uint4 raw[kRowUnroll];
-#pragma unroll
-            for (int k = 0; k < kRowUnroll; ++k) raw[k] = ld_once(from + u + k * p.group);
-            add_units<BF16, kRowUnroll>(raw, u, p.group, p.vocab, c, sum);
-        }
-        for (; u < units; u += p.group) {
-            uint4 raw[1] = {ld_once(from + u)};
-            add_units<BF16, 1>(raw, u, 0, p.vocab, c, sum);
-        }
+        sum = sum_units<BF16, kShortUnroll>(from, lane, p.group, units, p.vocab, c);
     }
     sum = lanes_joined(sum, p.group, c);
     if (lane != 0 || t >= p.T) return;
@@ -324,7 +359,7 @@ cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream
         return cudaGetLastError();
     }
     // few tokens: a row's columns over several CTAs, as many as the SMs take at once, 512 units each at least
-    const int64_t room = 3 * static_cast<int64_t>(sm_count(-1));
+    const int64_t room = 4 * static_cast<int64_t>(sm_count(-1));
     p.split = 1;
     while (p.split < 8 && p.T * p.split * 2 <= room && units >= p.split * 2 * kRowThreads) p.split *= 2;
     if (p.T * p.split > 0x7FFFFFFF) return cudaErrorInvalidValue;
