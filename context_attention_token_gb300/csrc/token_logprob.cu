@@ -173,9 +173,10 @@ __device__ __forceinline__ Sum lanes_joined(Sum sum, int group, float c)
     return sum;
 }
 
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 256;
 constexpr int kRowUnroll = 8;
 constexpr int kShortUnroll = 4;
+constexpr int kMostSplit = 4;      // CTAs of a long row
 constexpr int kShortThreads = 256;
 constexpr int kShortUnits = 512;   // of rows that a part of a warp reads
 
@@ -185,7 +186,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kRowThreads) token_logprob_kernel(const __grid_constant__ LogprobParams p)
 {
     constexpr int E = Unit<BF16>::E;
-    __shared__ Sum room[kRowThreads / 32], parts[8];
+    __shared__ Sum room[kRowThreads / 32], parts[kMostSplit];
     const float c = __fmul_rn(p.scale, kLog2E);
     const int64_t units = (p.vocab + E - 1) / E;
     const int part = static_cast<int>(blockIdx.x % p.split);
@@ -358,10 +359,11 @@ cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream
         else token_logprob_short_kernel<false><<<grid, kShortThreads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    // few tokens: a row's columns over several CTAs, as many as the SMs take at once, 512 units each at least
-    const int64_t room = 4 * static_cast<int64_t>(sm_count(-1));
+    // few tokens: a row's columns over the CTAs of a cluster, two CTAs an SM at most (64 rows of 157184 bf16: SPLITS).
+    // 256 threads read 8191 such rows in 360 us, 512 in 381, 1024 in 501.
+    const int64_t room = 2 * static_cast<int64_t>(sm_count(-1));
     p.split = 1;
-    while (p.split < 8 && p.T * p.split * 2 <= room && units >= p.split * 2 * kRowThreads) p.split *= 2;
+    while (p.split < kMostSplit && p.T * p.split * 2 <= room && units >= p.split * 2 * kRowThreads) p.split *= 2;
     if (p.T * p.split > 0x7FFFFFFF) return cudaErrorInvalidValue;
     cudaLaunchConfig_t config;
     memset(&config, 0, sizeof config);
