@@ -200,10 +200,8 @@ struct DropoutParams {
     int64_t rows;
     int32_t units;                 // 16-byte units per row
     DropRule rule;
-    int64_t step_rows;             // filled in by the launcher: a thread's step in rows and units
-    int32_t step_units;
 };
-cudaError_t launch_dropout(DropoutParams p, int dtype, cudaStream_t stream);
+cudaError_t launch_dropout(const DropoutParams &p, int dtype, cudaStream_t stream);
 
 // The residual stream between two blocks and its gradient.
 constexpr int kResidualMaxRow = 8192;

@@ -5,7 +5,7 @@
 // probability held, so the expectation is exact. One generator call serves the eight columns of a
 // 16-byte unit of bf16.
 //
-// HBM bounds it: every row is read and written once, units one after the other, four of every
+// HBM bounds it: every row is read and written once. A CTA takes a tile of neighbouring units, four of every
 // thread in flight.
 #include "cpt_internal.h"
 #include "token_rows.cuh"
@@ -16,6 +16,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kUnroll = 4;
+constexpr int kTile = kThreads * kUnroll;   // units of a CTA, neighbours
 
 template <bool BF16>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropoutParams p)
@@ -24,65 +25,54 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
     const F2 factor = pair_of(p.rule.factor, p.rule.factor);
     DropKey key;
     key.load(p.rule);
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
-    int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    int64_t row = i / p.units;
-    uint32_t unit = static_cast<uint32_t>(i - row * p.units);
-    const int64_t items = p.rows * p.units;
-    for (; i < items; i += stride * kUnroll) {
-        uint4 raw[kUnroll];
-        int32_t token[kUnroll];
-        uint32_t at[kUnroll];
+    const int64_t start = static_cast<int64_t>(blockIdx.x) * kTile;
+    const uint32_t here = static_cast<uint32_t>(min(p.rows * p.units - start, static_cast<int64_t>(kTile)));
+    const uint4 *from = reinterpret_cast<const uint4 *>(p.src) + start;
+    uint4 *to = reinterpret_cast<uint4 *>(p.dst) + start;
+    uint4 raw[kUnroll];
 #pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t j = i + k * stride;
-            token[k] = -1;
-            at[k] = unit;
-            if (j < items) {
-                raw[k] = __ldcs(reinterpret_cast<const uint4 *>(p.src) + j);
-                token[k] = p.token_of_row == nullptr ? static_cast<int32_t>(row) : p.token_of_row[row];
-            }
-            row += p.step_rows;
-            unit += p.step_units;
-            if (unit >= static_cast<uint32_t>(p.units)) {
-                unit -= p.units;
-                ++row;
-            }
+    for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t i = threadIdx.x + k * kThreads;
+        if (i < here) raw[k] = __ldcs(from + i);
+    }
+    const int64_t row0 = start / p.units;
+    const uint32_t units = static_cast<uint32_t>(p.units), skip = static_cast<uint32_t>(start - row0 * p.units);
+    uint32_t token[kUnroll], unit[kUnroll], bits[kUnroll][N];
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t i = min(threadIdx.x + k * kThreads, here - 1);
+        const uint32_t q = (skip + i) / units;
+        unit[k] = skip + i - q * units;
+        token[k] = static_cast<uint32_t>(p.token_of_row == nullptr ? row0 + q : p.token_of_row[row0 + q]);
+    }
+    if (p.rule.rng != nullptr) unit_bits<BF16, kUnroll>(p.rule, key, token, unit, bits);
+#pragma unroll
+    for (int k = 0; k < kUnroll; ++k) {
+        const uint32_t i = threadIdx.x + k * kThreads;
+        if (i >= here) continue;
+        uint4 out = raw[k];
+        if (p.rule.rng != nullptr) {
+            F2 x[N];
+            UnitPairs<BF16>::unpack(raw[k], x);
+            keep_or_zero<N>(p.rule, bits[k], x);
+#pragma unroll
+            for (int n = 0; n < N; ++n) x[n] = mul2(x[n], factor);
+            out = UnitPairs<BF16>::pack(x);
         }
-#pragma unroll
-        for (int k = 0; k < kUnroll; ++k) {
-            const int64_t j = i + k * stride;
-            if (j >= items) continue;
-            uint4 out = raw[k];
-            if (token[k] < 0) {   // padding
-                out = make_uint4(0, 0, 0, 0);
-            } else if (p.rule.rng != nullptr) {
-                F2 x[N];
-                UnitPairs<BF16>::unpack(raw[k], x);
-                uint32_t bits[N];
-                unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(token[k]), at[k], bits);
-                keep_or_zero<N>(p.rule, bits, x);
-#pragma unroll
-                for (int n = 0; n < N; ++n) x[n] = mul2(x[n], factor);
-                out = UnitPairs<BF16>::pack(x);
-            }
-            __stcs(reinterpret_cast<uint4 *>(p.dst) + j, out);
-        }
+        if (static_cast<int32_t>(token[k]) < 0) out = make_uint4(0, 0, 0, 0);   // padding
+        __stcs(to + i, out);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_dropout(DropoutParams p, int dtype, cudaStream_t stream)
+cudaError_t launch_dropout(const DropoutParams &p, int dtype, cudaStream_t stream)
 {
     const int64_t items = p.rows * p.units;
     if (items == 0) return cudaSuccess;
-    const int64_t ctas = (items + kThreads * kUnroll - 1) / (kThreads * kUnroll);
-    const int64_t most = 8 * static_cast<int64_t>(sm_count(-1));
-    const unsigned grid = static_cast<unsigned>(ctas < most ? ctas : most);
-    const int64_t stride = static_cast<int64_t>(grid) * kThreads;
-    p.step_rows = stride / p.units;
-    p.step_units = static_cast<int32_t>(stride % p.units);
+    const int64_t ctas = (items + kTile - 1) / kTile;
+    if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    const unsigned grid = static_cast<unsigned>(ctas);
     if (dtype == kBf16) dropout_kernel<true><<<grid, kThreads, 0, stream>>>(p);
     else dropout_kernel<false><<<grid, kThreads, 0, stream>>>(p);
     return cudaGetLastError();

@@ -182,8 +182,7 @@ struct HeldWeights {
     }
 };
 
-// R rows of the forward call. x, h and gate give the data of a unit of a row, bits its random bits (all of a row's
-// at once), put_y and put_n take a unit's result, sum adds over the rows' threads.
+// R rows of the forward call. x, h and gate give the data of a unit of a row, bits all random bits, put_y and put_n take a unit's result, sum adds over the rows' threads.
 template <bool BF16, int U, int R, int F, class W, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
 __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<U> &has, W w1, W w2, X x, H h, G gate,
                                              Bits bits, Sum sum, PutY put_y, PutN put_n)
@@ -210,10 +209,7 @@ __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<
         s[r] = sum_of(q);
     }
     // the generator needs no data: it runs while the sums are on their way
-    if (A::drop(p)) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) bits(r, rnd[r]);
-    }
+    if (A::drop(p)) bits(rnd);
     if (A::post(p)) {
         sum(s);
 #pragma unroll
@@ -318,10 +314,7 @@ __device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has
         }
     }
     // the generator needs no data: it runs while the sums are on their way
-    if (A::drop(p)) {
-#pragma unroll
-        for (int r = 0; r < R; ++r) bits(r, rnd[r]);
-    }
+    if (A::drop(p)) bits(rnd);
     if (pre || post) sum(s);
     F2 e[R][U][N];
     float t[R], r1[R];
@@ -499,6 +492,19 @@ struct ShortRaw {
 };
 
 template <bool BF16, int U>
+__device__ __forceinline__ void short_bits(const ResidualParams &p, const DropKey &key, uint32_t token, int lane,
+                                           uint32_t (&bits)[U][Unit<BF16>::E / 2])
+{
+    uint32_t tokens[U], units[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        tokens[k] = token;
+        units[k] = lane + k * p.group;
+    }
+    unit_bits<BF16, U>(p.rule, key, tokens, units, bits);
+}
+
+template <bool BF16, int U>
 __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
@@ -550,10 +556,7 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
         forward_rows<BF16, U, 1, -1>(
             p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int, int k) { return r.t[0][k]; },
             [&](int, int k) { return r.t[1][k]; }, [&](int, int k) { return r.t[2][k]; },
-            [&](int, uint32_t(&bits)[U][E / 2]) {
-#pragma unroll
-                for (int k = 0; k < U; ++k) unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(r.token), lane + k * p.group, bits[k]);
-            },
+            [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(r.token), lane, bits[0]); },
             [&](float(&v)[1]) { lanes_sum<1>(v, p.group); },
             [&](int, int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
             [&](int, int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
@@ -631,10 +634,7 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
             [&](int, int k) { return r.t[0][k]; }, [&](int, int k) { return r.t[1][k]; },
             [&](int, int k) { return r.t[2][k]; }, [&](int, int k) { return r.t[3][k]; }, [](int) {},
             [&](int, int k) { return r.t[4][k]; },
-            [&](int, uint32_t(&bits)[U][E / 2]) {
-#pragma unroll
-                for (int k = 0; k < U; ++k) unit_bits<BF16>(p.rule, key, static_cast<uint32_t>(t), lane + k * p.group, bits[k]);
-            },
+            [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits[0]); },
             [&](auto &v) { lanes_sum(v, p.group); },
             [&](int, int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
             [&](int, int k, uint4 v) { if (real) store_unit(p.n, at + k * p.group, v); },
@@ -831,7 +831,12 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
             p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int r, int k) { return data[r][k * p.group]; },
             [&](int r, int k) { return data[r][(U + k) * p.group]; },
             [&](int r, int k) { return A::gate(p) == kGateToken ? data[r][(2 * U + k) * p.group] : gate[r][k]; },
-            [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(token[r]), lane, p.group, bits); },
+            [&](uint32_t(&bits)[R][U][E / 2]) {
+                uint32_t tokens[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) tokens[r] = static_cast<uint32_t>(token[r]);
+                thread_bits<BF16, U, R>(p.rule, key, tokens, lane, p.group, bits);
+            },
             [&](float(&v)[R]) {
                 sum(v);
                 if (waiting) after();
@@ -924,7 +929,12 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
                 }
             },
             [&](int r, int k) { return by_document ? own_gate[k * p.group] : data[r][at_gate + k * p.group]; },
-            [&](int r, uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(t + r), lane, p.group, bits); },
+            [&](uint32_t(&bits)[R][U][E / 2]) {
+                uint32_t tokens[R];
+#pragma unroll
+                for (int r = 0; r < R; ++r) tokens[r] = static_cast<uint32_t>(t + r);
+                thread_bits<BF16, U, R>(p.rule, key, tokens, lane, p.group, bits);
+            },
             [&](auto &v) {
                 sum(v);
                 if (waiting) after();

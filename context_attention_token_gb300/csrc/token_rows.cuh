@@ -76,18 +76,22 @@ struct UnitPairs {
 // Philox-4x32 with ten rounds, from the published description (Salmon and others, "Parallel
 // random numbers: as easy as 1, 2, 3", 2011). Ten is the authors' recommendation; they found
 // seven enough for their tests. One call serves eight columns with 16 bits each.
-__device__ __forceinline__ uint4 philox(uint32_t k0, uint32_t k1, uint4 c)
+// The N counters of a call go through the rounds side by side, with one key schedule.
+template <int N>
+__device__ __forceinline__ void philox(uint32_t k0, uint32_t k1, uint4 (&c)[N])
 {
 #pragma unroll
     for (int i = 0; i < 10; ++i) {
-        const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
-        const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-        c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
-                       static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
+#pragma unroll
+        for (int n = 0; n < N; ++n) {
+            const uint64_t a = static_cast<uint64_t>(c[n].x) * 0xD2511F53u;
+            const uint64_t b = static_cast<uint64_t>(c[n].z) * 0xCD9E8D57u;
+            c[n] = make_uint4(static_cast<uint32_t>(b >> 32) ^ c[n].y ^ k0, static_cast<uint32_t>(b),
+                              static_cast<uint32_t>(a >> 32) ^ c[n].w ^ k1, static_cast<uint32_t>(a));
+        }
         k0 += 0x9E3779B9u;
         k1 += 0xBB67AE85u;
     }
-    return c;
 }
 
 struct DropKey {
@@ -102,46 +106,64 @@ struct DropKey {
     }
 };
 
-// The random bits of a unit: a word for every two of its columns.
-template <bool BF16>
-__device__ __forceinline__ void unit_bits(const DropRule &r, const DropKey &key, uint32_t token, uint32_t unit,
-                                          uint32_t (&bits)[Unit<BF16>::E / 2])
+// The random bits of N units: a word for every two of a unit's columns.
+template <bool BF16, int N>
+__device__ __forceinline__ void unit_bits(const DropRule &r, const DropKey &key, const uint32_t (&token)[N],
+                                          const uint32_t (&unit)[N], uint32_t (&bits)[N][Unit<BF16>::E / 2])
 {
-    const uint4 w = philox(key.k0, key.k1, make_uint4(BF16 ? unit : unit >> 1, token, key.step, r.site));
-    if constexpr (BF16) {
-        bits[0] = w.x;
-        bits[1] = w.y;
-        bits[2] = w.z;
-        bits[3] = w.w;
-    } else {   // a float32 unit is half a group of eight columns
-        bits[0] = unit & 1 ? w.z : w.x;
-        bits[1] = unit & 1 ? w.w : w.y;
+    uint4 w[N];
+#pragma unroll
+    for (int n = 0; n < N; ++n) w[n] = make_uint4(BF16 ? unit[n] : unit[n] >> 1, token[n], key.step, r.site);
+    philox<N>(key.k0, key.k1, w);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+        if constexpr (BF16) {
+            bits[n][0] = w[n].x;
+            bits[n][1] = w[n].y;
+            bits[n][2] = w[n].z;
+            bits[n][3] = w[n].w;
+        } else {   // a float32 unit is half a group of eight columns
+            bits[n][0] = unit[n] & 1 ? w[n].z : w[n].x;
+            bits[n][1] = unit[n] & 1 ? w[n].w : w[n].y;
+        }
     }
 }
 
-// The bits of a thread's units lane, lane + group, ..., with even groups of whole warps. Two neighbouring lanes have
-// the halves of the same group of eight float32 columns: each calls the generator for one of two units and they
-// exchange what the other needs.
-template <bool BF16, int U>
-__device__ __forceinline__ void thread_bits(const DropRule &r, const DropKey &key, uint32_t token, int lane, int group,
-                                            uint32_t (&bits)[U][Unit<BF16>::E / 2])
+// The bits of a thread's units lane, lane + group, ... of R tokens' rows, with even groups of whole warps. Two
+// neighbouring lanes have the halves of the same group of eight float32 columns: each calls the generator for one of
+// two units and they exchange what the other needs.
+template <bool BF16, int U, int R>
+__device__ __forceinline__ void thread_bits(const DropRule &r, const DropKey &key, const uint32_t (&token)[R], int lane,
+                                            int group, uint32_t (&bits)[R][U][Unit<BF16>::E / 2])
 {
-    if constexpr (BF16) {
+    constexpr int C = BF16 ? U : U / 2;   // calls for a row
+    static_assert(BF16 || U % 2 == 0, "pairs of units");
+    const bool odd = lane & 1;
+    uint4 w[R * C];
 #pragma unroll
-        for (int k = 0; k < U; ++k) unit_bits<true>(r, key, token, lane + k * group, bits[k]);
-    } else {
-        static_assert(U % 2 == 0, "pairs of units");
-        const bool odd = lane & 1;
+    for (int j = 0; j < R; ++j)
 #pragma unroll
-        for (int k = 0; k < U; k += 2) {
-            const uint32_t mine = lane + (k + odd) * group;
-            const uint4 w = philox(key.k0, key.k1, make_uint4(mine >> 1, token, key.step, r.site));
-            const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? w.x : w.z, 1);
-            const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? w.y : w.w, 1);
-            bits[k][0] = odd ? a : w.x;
-            bits[k][1] = odd ? b : w.y;
-            bits[k + 1][0] = odd ? w.z : a;
-            bits[k + 1][1] = odd ? w.w : b;
+        for (int k = 0; k < C; ++k)
+            w[j * C + k] = make_uint4(BF16 ? lane + k * group : (lane + (2 * k + odd) * group) >> 1, token[j], key.step, r.site);
+    philox<R * C>(key.k0, key.k1, w);
+#pragma unroll
+    for (int j = 0; j < R; ++j) {
+#pragma unroll
+        for (int k = 0; k < C; ++k) {
+            const uint4 v = w[j * C + k];
+            if constexpr (BF16) {
+                bits[j][k][0] = v.x;
+                bits[j][k][1] = v.y;
+                bits[j][k][2] = v.z;
+                bits[j][k][3] = v.w;
+            } else {
+                const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.z, 1);
+                const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.y : v.w, 1);
+                bits[j][2 * k][0] = odd ? a : v.x;
+                bits[j][2 * k][1] = odd ? b : v.y;
+                bits[j][2 * k + 1][0] = odd ? v.z : a;
+                bits[j][2 * k + 1][1] = odd ? v.w : b;
+            }
         }
     }
 }
