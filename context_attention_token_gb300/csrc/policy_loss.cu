@@ -123,9 +123,9 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
 {
     namespace cg = cooperative_groups;
     constexpr int kSums = 5;                   // loss, kl, held; tokens, in units of one and of 4096: exact for any length
-    __shared__ float room[BlockSum::kRoom];
+    __shared__ float room[TeamSum<128>::kRoom];
     __shared__ float shares[2][S][kSums];      // of two documents in turn, every CTA's
-    BlockSum sum(room);
+    TeamSum<128> sum(room, Team{static_cast<int>(threadIdx.x), kThreads, 1});
     const int rank = S == 1 ? 0 : static_cast<int>(blockIdx.x % S), lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x / S) * p.docs;
     const int64_t last = min(first + p.docs, static_cast<int64_t>(p.n_docs));

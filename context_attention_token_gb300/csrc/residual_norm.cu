@@ -27,10 +27,12 @@ namespace cpt {
 namespace {
 
 constexpr int kShortThreads = 128;
-constexpr int kForwardThreads = 1024;   // of an SM's long rows: 64 registers each
+constexpr int kForwardThreads = 640;    // of an SM's long rows: 96 registers each
 constexpr int kBackwardThreads = 640;   // 96 registers each
 constexpr int kMaxChunks = 8;
+constexpr int kMaxTeams = 10;              // of a forward CTA
 constexpr int kSharedBytes = 227 * 1024;   // of an SM
+constexpr int kForwardOwnBytes = 128 + kMaxTeams * (256 + kMaxChunks * 12);   // of a forward CTA, besides rings and weights
 constexpr int kOwnBytes = 3584;            // of a CTA, besides its ring
 constexpr int kGateToken = 1, kGateDocument = 2;
 
@@ -44,8 +46,13 @@ struct Shape {
     bool shorter;     // several rows a CTA
 };
 
-Shape shape_of(int units, int dtype, bool gradient)
+// Weights in the forward call's shared memory: two rows of them, every thread's units whole.
+int64_t forward_weights(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
+
+// tensors: those that are read, or 0 for the gradient, whose workspace does not depend on them.
+Shape shape_of(int units, int dtype, int tensors)
 {
+    const bool gradient = tensors == 0;
     Shape s;
     s.shorter = units <= 64;
     s.rows = 1;
@@ -57,17 +64,30 @@ Shape shape_of(int units, int dtype, bool gradient)
         s.ctas_per_sm = s.per_thread == 1 ? 4 : 2;
         return s;
     }
-    // eight columns of two rows at a time, or sixteen of one
-    s.per_thread = dtype == kBf16 ? 1 : 2;
-    s.rows = 2;
-    if (units > s.per_thread * (gradient ? kBackwardThreads : kForwardThreads)) {   // of the gradient only: 8192 columns fit the other
-        s.per_thread *= 2;
-        s.rows = 1;
+    const int eights = dtype == kBf16 ? units : (units + 1) / 2;   // groups of eight columns
+    int wide = 2;                                                  // of a thread
+    s.rows = gradient ? 2 : 1;
+    if (gradient) wide = eights <= kBackwardThreads ? 1 : 2;
+    else wide = eights <= 128 ? 2 : eights <= 192 ? 3 : 5;
+    s.per_thread = dtype == kBf16 ? wide : 2 * wide;
+    s.group = ((eights + wide - 1) / wide + 31) / 32 * 32;
+    const int64_t row = s.per_thread * s.group * 16;   // bytes
+    if (gradient) {
+        s.threads = s.group;
+        // two rows of the gradient's five tensors have to fit (float32 rows of up to 5120 columns do)
+        if (11 * row > kSharedBytes - kOwnBytes) s.rows = 1;
+        // as many CTAs as registers allow, of which each has room for two chunks
+        s.ctas_per_sm = kBackwardThreads / s.group;
+        const int64_t fit = kSharedBytes / (2 * 5 * s.rows * row + kOwnBytes);
+        if (s.ctas_per_sm > fit) s.ctas_per_sm = fit < 1 ? 1 : static_cast<int>(fit);
+        return s;
     }
-    s.group = ((units + s.per_thread - 1) / s.per_thread + 31) / 32 * 32;
-    s.threads = s.group;
-    // as many CTAs as registers allow
-    s.ctas_per_sm = (gradient ? kBackwardThreads : kForwardThreads) / s.group;
+    // one CTA an SM, of as many teams as registers, barriers and shared memory allow (two rows each, or else one)
+    s.ctas_per_sm = 1;
+    int teams = kForwardThreads / s.group < kMaxTeams ? kForwardThreads / s.group : kMaxTeams;
+    const int64_t left = kSharedBytes - kForwardOwnBytes - forward_weights(s, dtype);
+    if (teams > left / (tensors * row)) teams = static_cast<int>(left / (tensors * row));
+    s.threads = teams * s.group;
     return s;
 }
 
@@ -75,10 +95,11 @@ Shape shape_of(int units, int dtype, bool gradient)
 int64_t gate_place(const Shape &s, int gate_kind) { return gate_kind == kGateDocument ? s.per_thread * s.group * 16 : 0; }
 
 // Chunks of rows that a ring holds.
-int chunks_of(const Shape &s, int gate_kind, int tensors)
+int chunks_of(const Shape &s, int dtype, bool gradient, int gate_kind, int tensors)
 {
     const int64_t chunk = static_cast<int64_t>(tensors) * s.rows * s.per_thread * s.group * 16;
-    const int64_t n = (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / chunk;
+    const int64_t n = gradient ? (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / chunk
+                               : (kSharedBytes - kForwardOwnBytes - forward_weights(s, dtype)) / (chunk * (s.threads / s.group));
     return static_cast<int>(n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : n);
 }
 
@@ -179,6 +200,22 @@ struct HeldWeights {
     {
 #pragma unroll
         for (int i = 0; i < Unit<BF16>::E / 2; ++i) out[i] = w[k][i];
+    }
+};
+
+// Weights in shared memory.
+template <bool BF16>
+struct SharedWeights {
+    const float *row;   // of this thread's unit 0
+    int step;           // floats to its next unit
+    __device__ __forceinline__ void operator()(int k, F2 (&out)[Unit<BF16>::E / 2]) const
+    {
+#pragma unroll
+        for (int i = 0; i < Unit<BF16>::E / 2; i += 2) {
+            const float4 v = *reinterpret_cast<const float4 *>(row + k * step + 2 * i);
+            out[i] = pair_of(v.x, v.y);
+            out[i + 1] = pair_of(v.z, v.w);
+        }
     }
 };
 
@@ -668,7 +705,7 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
 
 // ----------------------------------------------------------------- long rows: a CTA each
 
-// A ring of chunks of R rows in shared memory. The first warp has the bulk-copy engine fetch the rows of all input
+// A ring of chunks of R rows in shared memory. A team's first warp has the bulk-copy engine fetch the rows of all input
 // tensors, one instruction a row, a lane for each.
 template <int R>
 struct Ring {
@@ -686,10 +723,10 @@ struct Ring {
         return reinterpret_cast<const uint4 *>(smem + (slot * R + r) * stage_bytes);
     }
     // What no copy writes: the ends of the places, behind the rows.
-    __device__ __forceinline__ void zero_ends(int tensors, uint32_t row_bytes)
+    __device__ __forceinline__ void zero_ends(const Team &team, int tensors, uint32_t row_bytes)
     {
         for (int i = 0; i < chunks * R * tensors; ++i)
-            for (uint32_t at = row_bytes + threadIdx.x * 16; at < place; at += blockDim.x * 16)
+            for (uint32_t at = row_bytes + team.thread * 16; at < place; at += team.threads * 16)
                 *reinterpret_cast<uint4 *>(smem + i * place + at) = make_uint4(0, 0, 0, 0);
     }
 };
@@ -699,12 +736,12 @@ __device__ unsigned int g_wait_timeouts;
 // Runs `rows(i, after)` for i = 0, R, 2 R, ... below count with the chunk's data in the ring. It has to call after()
 // once behind its first barrier, where every thread is done with the chunk before; `sum` votes there whether a wait
 // has run out. index_of(i) looks the i-th up (-1: it is not read), row_of(i, index) is its row, base this lane's tensor.
-template <int R, class Index, class RowOf, class Rows>
-__device__ __forceinline__ void walk(Ring<R> &ring, BlockSum &sum, int64_t count, int tensors, uint32_t row_bytes,
+template <int R, class Sum, class Index, class RowOf, class Rows>
+__device__ __forceinline__ void walk(Ring<R> &ring, Sum &sum, int64_t count, int tensors, uint32_t row_bytes,
                                      const uint8_t *base, Index index_of, RowOf row_of, Rows rows)
 {
-    const int lane = threadIdx.x & 31, tensor = lane / R, r = lane - tensor * R;
-    const bool first = threadIdx.x < 32;
+    const int lane = sum.team.thread & 31, tensor = lane / R, r = lane - tensor * R;
+    const bool first = sum.team.thread < 32;
     int64_t issued = 0;
     int put = 0;
     int32_t ahead = first ? index_of(r) : -1;   // looked up a chunk early
@@ -723,11 +760,11 @@ __device__ __forceinline__ void walk(Ring<R> &ring, BlockSum &sum, int64_t count
         ahead = index_of(issued + r);
         if (++put == ring.chunks) put = 0;
     };
-    if (threadIdx.x == 0) {
+    if (sum.team.thread == 0) {
         for (int c = 0; c < ring.chunks; ++c) mbar_init(&ring.full[c], 1);
         mbar_init_fence();
     }
-    __syncthreads();
+    __syncthreads();   // of all teams: what else was put into shared memory is there too
     if (first)
         for (int c = 0; c < ring.chunks; ++c) issue();
     const bool several = ring.chunks > 1;
@@ -742,11 +779,11 @@ __device__ __forceinline__ void walk(Ring<R> &ring, BlockSum &sum, int64_t count
             ring.phase ^= 1;
         }
         if (!several) {
-            sum.stop = __syncthreads_or(sum.ask);
+            sum.stop = sum.team.any(sum.ask);
             if (first && !sum.stop) issue();
         }
         if (sum.stop) {   // by all: no copy may end in another CTA's shared memory
-            if (threadIdx.x == 0) {
+            if (sum.team.thread == 0) {
                 atomicAdd(&g_wait_timeouts, 1u);
                 for (int64_t k = i + R; k < issued; k += R) {
                     mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
@@ -767,24 +804,32 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float room[BlockSum::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxChunks];
-    __shared__ int32_t index[kMaxChunks * R];
-    const int lane = threadIdx.x;
-    const int64_t begin = blockIdx.x * p.per_group, count = min(p.per_group, p.rows - begin);
+    __shared__ float room[kMaxTeams][TeamSum<32>::kRoom];
+    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxChunks];
+    __shared__ int32_t index[kMaxTeams][kMaxChunks * R];
+    const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
+    const Team team = {lane, p.group, mine + 1};
+    const int64_t begin = (static_cast<int64_t>(blockIdx.x) * teams + mine) * p.per_group;
+    const int64_t count = max(min(p.per_group, p.rows - begin), static_cast<int64_t>(0));
     DropKey key;
     key.load(p.rule);
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    F2 w1[U][E / 2], w2[U][E / 2];
-    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
-    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    // the weights of all teams, every thread's units whole
+    float *weights = reinterpret_cast<float *>(smem);
+    const int columns = U * p.group * E;
+    for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+        if (A::post(p)) weights[c] = c < p.row_elems ? p.post[c] : 0.0f;
+        if (A::pre(p)) weights[columns + c] = c < p.row_elems ? p.pre[c] : 0.0f;
+    }
+    const SharedWeights<BF16> w1 = {weights + lane * E, p.group * E}, w2 = {weights + columns + lane * E, p.group * E};
     Document doc;
-    BlockSum sum(room);
+    TeamSum<32> sum(room[mine], team);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
-    ring.zero_ends(p.tensors, row_bytes);
+    uint8_t *rings = smem + 2 * columns * sizeof(float);
+    Ring<R> ring = {rings + static_cast<size_t>(mine) * p.stages * R * p.tensors * place, full[mine], index[mine], p.stages, place, place * p.tensors};
+    ring.zero_ends(team, p.tensors, row_bytes);
 
     auto token_of = [&](int64_t i) {
         int32_t t = -1;
@@ -828,7 +873,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
             }
         }
         forward_rows<BF16, U, R, F>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int r, int k) { return data[r][k * p.group]; },
+            p, has, w1, w2, [&](int r, int k) { return data[r][k * p.group]; },
             [&](int r, int k) { return data[r][(U + k) * p.group]; },
             [&](int r, int k) { return A::gate(p) == kGateToken ? data[r][(2 * U + k) * p.group] : gate[r][k]; },
             [&](uint32_t(&bits)[R][U][E / 2]) {
@@ -845,19 +890,19 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
             [&](int r, int k, uint4 v) { if (put[r]) store_unit(y + at[r], k * p.group, v); },
             [&](int r, int k, uint4 v) { if (put[r]) store_unit(n + at[r], k * p.group, v); });
         if (waiting) {
-            sum.stop = __syncthreads_or(sum.ask);
+            sum.stop = sum.team.any(sum.ask);
             after();
         }
     });
 }
 
 template <bool BF16, int U, int R, int F>
-__global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads, 1) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float room[BlockSum::kRoom];
+    __shared__ float room[TeamSum<256>::kRoom];
     __shared__ __align__(8) uint64_t full[kMaxChunks];
     __shared__ int32_t index[kMaxChunks * R];
     const int lane = threadIdx.x;
@@ -868,19 +913,21 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    F2 w1[U][E / 2], w2[U][E / 2];
-    load_weights<BF16, U>(p.post, has, lane, p.group, w1);
-    load_weights<BF16, U>(p.pre, has, lane, p.group, w2);
+    F2 held1[U][E / 2], held2[U][E / 2];
+    load_weights<BF16, U>(p.post, has, lane, p.group, held1);
+    load_weights<BF16, U>(p.pre, has, lane, p.group, held2);
+    const HeldWeights<BF16, U> w1 = {held1}, w2 = {held2};
     Sums<BF16, U> acc;
 #pragma unroll
     for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
     Document doc;
-    BlockSum sum(room);
+    const Team team = {lane, p.group, 1};
+    TeamSum<256> sum(room, team);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
     Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
-    ring.zero_ends(p.tensors, row_bytes);
+    ring.zero_ends(team, p.tensors, row_bytes);
     // behind the ring stands a document's gate, each thread's part its own
     uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * R * p.tensors * place) + lane;
     // places of the tensors in a stage, in units
@@ -913,7 +960,7 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
             data[r] = ring.row(r) + lane;
         }
         backward_rows<BF16, U, R, F>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int r) { return there[r]; },
+            p, has, w1, w2, acc, [&](int r) { return there[r]; },
             [&](int r, int k) { return p.x != nullptr ? data[r][k * p.group] : make_uint4(0, 0, 0, 0); },
             [&](int r, int k) { return data[r][at_dn + k * p.group]; }, [&](int r, int k) { return data[r][at_y + k * p.group]; },
             [&](int r, int k) { return data[r][at_h + k * p.group]; },
@@ -944,7 +991,7 @@ __global__ void __launch_bounds__(R == 1 ? 512 : kBackwardThreads) residual_norm
             [&](int r, int k, uint4 v) { store_unit(p.n + at[r], k * p.group, v); },
             [&](int r, int k, uint4 v) { store_unit(p.dgate + at[r], k * p.group, v); });
         if (waiting) {
-            sum.stop = __syncthreads_or(sum.ask);
+            sum.stop = sum.team.any(sum.ask);
             after();
         }
     });
@@ -1007,20 +1054,22 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
 
 int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems * (dtype == kBf16 ? 2 : 4) / 16); }
 
-size_t ring_bytes(const ResidualParams &p, const Shape &s)
+size_t ring_bytes(const ResidualParams &p, const Shape &s, int dtype, bool gradient)
 {
+    if (!gradient)
+        return static_cast<size_t>(p.stages) * (s.threads / s.group) * p.tensors * s.per_thread * s.group * 16 + forward_weights(s, dtype);
     return static_cast<size_t>(p.stages) * s.rows * p.tensors * s.per_thread * s.group * 16 + gate_place(s, p.gate_kind);
 }
 
 // A kernel's limit of dynamic shared memory, raised once on each device.
 template <auto kernel>
-cudaError_t allow_shared(int device)
+cudaError_t allow_shared(int device, int most)
 {
     static std::mutex mu;
     static bool done[64] = {false};
     std::lock_guard<std::mutex> lock(mu);
     if (device >= 0 && device < 64 && done[device]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - kOwnBytes);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e == cudaSuccess && device >= 0 && device < 64) done[device] = true;
     return e;
 }
@@ -1059,14 +1108,19 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
         else residual_norm_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int U = BF16 ? 1 : 2;
+    constexpr int U = BF16 ? 1 : 2;   // units of eight columns
     auto run = [&](auto kernel) {
-        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device, kSharedBytes - kForwardOwnBytes);
         if (e != cudaSuccess) return e;
-        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s, BF16 ? kBf16 : kF32, false), stream>>>(p);
         return cudaGetLastError();
     };
-    return with_asked(p, p.h != nullptr, [&](auto f) { return run(Kernel<residual_norm_long_kernel<BF16, U, 2, decltype(f)::value>>()); });
+    return with_asked(p, p.h != nullptr, [&](auto f) {
+        constexpr int F = decltype(f)::value;
+        if (s.per_thread == 2 * U) return run(Kernel<residual_norm_long_kernel<BF16, 2 * U, 1, F>>());
+        if (s.per_thread == 3 * U) return run(Kernel<residual_norm_long_kernel<BF16, 3 * U, 1, F>>());
+        return run(Kernel<residual_norm_long_kernel<BF16, 5 * U, 1, F>>());
+    });
 }
 
 template <bool BF16>
@@ -1077,14 +1131,16 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
         else residual_norm_backward_short_kernel<BF16, 2><<<grid, s.threads, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    constexpr int U = BF16 ? 1 : 2;
+    constexpr int U = BF16 ? 1 : 2;   // units of eight columns
     auto run = [&](auto kernel) {
-        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device, kSharedBytes - kOwnBytes);
         if (e != cudaSuccess) return e;
-        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s, BF16 ? kBf16 : kF32, true), stream>>>(p);
         return cudaGetLastError();
     };
-    if (s.rows == 1) return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>());
+    if (s.per_thread == 2 * U)
+        return s.rows == 1 ? run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>())
+                           : run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 2, -1>>());
     return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, U, 2, decltype(f)::value>>()); });
 }
 
@@ -1105,7 +1161,8 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
     if (p.rows == 0) return cudaSuccess;
     p.units = row_units(p.row_elems, dtype);
     p.per_column = 1.0f / static_cast<float>(p.row_elems);
-    const Shape s = shape_of(p.units, dtype, false);
+    p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
+    const Shape s = shape_of(p.units, dtype, p.tensors);
     p.group = s.group;
     int64_t ctas;
     if (s.shorter) {
@@ -1116,8 +1173,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
         ctas = (p.rows + p.per_group * groups - 1) / (p.per_group * groups);
     } else {
         deal(p.rows, s, device, p.per_group, ctas);
-        p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
-        p.stages = chunks_of(s, p.gate_kind, p.tensors);
+        p.stages = chunks_of(s, dtype, false, p.gate_kind, p.tensors);
     }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
@@ -1126,7 +1182,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
 
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device)
 {
-    const Shape s = shape_of(row_units(row_elems, dtype), dtype, true);
+    const Shape s = shape_of(row_units(row_elems, dtype), dtype, 0);
     int64_t per_group, ctas;
     deal(T, s, device, per_group, ctas);
     return (2 * ctas + 2 * ctas * (s.threads / s.group)) * row_elems * 4;
@@ -1136,7 +1192,7 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
 {
     p.units = row_units(p.row_elems, dtype);
     p.per_column = 1.0f / static_cast<float>(p.row_elems);
-    const Shape s = shape_of(p.units, dtype, true);
+    const Shape s = shape_of(p.units, dtype, 0);
     p.group = s.group;
     int64_t ctas;
     deal(p.T, s, device, p.per_group, ctas);
@@ -1147,7 +1203,7 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     if (p.T > 0) {
         const bool need_h = p.post != nullptr || p.gate_kind != 0;
         p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
-        p.stages = s.shorter ? 0 : chunks_of(s, p.gate_kind, p.tensors);
+        p.stages = s.shorter ? 0 : chunks_of(s, dtype, true, p.gate_kind, p.tensors);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
                                              : launch_backward<false>(p, s, grid, device, stream);

@@ -199,15 +199,35 @@ __device__ __forceinline__ void lanes_sum(float (&v)[N], int group)
     }
 }
 
-// Sums over a CTA of whole warps, in a fixed order. There are two places for the warps' sums; one is written
-// again only after every thread has passed the barrier of the other, so one barrier a sum is enough.
-struct BlockSum {
-    static constexpr int kRoom = 2 * 256;   // floats
-    float *room;                            // shared
+// Threads of a CTA that work on the same rows: whole warps, with a barrier of their own (1..15).
+struct Team {
+    int thread, threads, barrier;
+    __device__ __forceinline__ int warp() const { return thread >> 5; }
+    __device__ __forceinline__ int warps() const { return threads >> 5; }
+    // Waits for all of the team; whether any has asked.
+    __device__ __forceinline__ bool any(bool ask) const
+    {
+        uint32_t r;
+        asm volatile(
+            "{ .reg .pred q, s; setp.ne.u32 q, %1, 0; barrier.cta.red.or.pred s, %2, %3, q; selp.u32 %0, 1, 0, s; }"
+            : "=r"(r)
+            : "r"(static_cast<uint32_t>(ask)), "r"(barrier), "r"(threads)
+            : "memory");
+        return r != 0;
+    }
+};
+
+// Sums over a team, in a fixed order. There are two places for the warps' sums; one is written again only after every
+// thread has passed the barrier of the other, so one barrier a sum is enough.
+template <int TURN>   // floats of a place: 1, 2, 4 or 8 for a warp's 1, 2, up to 4 or up to 8 values
+struct TeamSum {
+    static constexpr int kRoom = 2 * TURN;   // floats
+    float *room;                             // shared
+    Team team;
     int turn = 0;
-    bool stop = false;                      // the vote of the last barrier: a thread has asked to stop
+    bool stop = false;   // the vote of the last barrier: a thread has asked to stop
     bool ask = false;
-    __device__ explicit BlockSum(float *r) : room(r) {}
+    __device__ TeamSum(float *r, const Team &t) : room(r), team(t) {}
 
     // N values: lanes give away those that they do not keep, so that (for N = 6) 9 shuffles do for 30
     template <int N>
@@ -215,8 +235,8 @@ struct BlockSum {
     {
         constexpr int W = N == 1 ? 1 : N == 2 ? 2 : N <= 4 ? 4 : 8;
         static_assert(N <= 8, "at most eight values");
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-        float *at = room + turn * 256;
+        const int lane = team.thread & 31, warp = team.warp(), warps = team.warps();
+        float *at = room + turn * TURN;
         turn ^= 1;
         float a[W];
 #pragma unroll
@@ -233,7 +253,13 @@ struct BlockSum {
 #pragma unroll
         for (int d = W; d < 32; d *= 2) s = __fadd_rn(s, __shfl_xor_sync(0xFFFFFFFFu, s, d));
         if (lane < W) at[warp * W + lane] = s;   // lane i: value i
-        stop = __syncthreads_or(ask);
+        stop = team.any(ask);
+        if (W == 1 && warps <= 4) {
+            s = at[0];
+            for (int i = 1; i < warps; ++i) s = __fadd_rn(s, at[i]);
+            v[0] = s;
+            return;
+        }
         s = 0.0f;
         for (int i = lane; i < warps * W; i += 32) s = __fadd_rn(s, at[i]);
 #pragma unroll
