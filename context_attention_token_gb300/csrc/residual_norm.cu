@@ -31,9 +31,9 @@ constexpr int kForwardThreads = 640;    // of an SM's long rows: 96 registers ea
 constexpr int kBackwardThreads = 640;   // 96 registers each
 constexpr int kMaxChunks = 8;
 constexpr int kMaxTeams = 10;              // of a forward CTA
-constexpr int kSharedBytes = 227 * 1024;   // of an SM
-constexpr int kForwardOwnBytes = 128 + kMaxTeams * (256 + kMaxChunks * 12);   // of a forward CTA, besides rings and weights
-constexpr int kOwnBytes = 3584;            // of a CTA, besides its ring
+constexpr int kSharedBytes = 228 * 1024;   // of an SM, 1 KB of each CTA the system's
+constexpr int kForwardOwnBytes = 1024 + 128 + kMaxTeams * (256 + kMaxChunks * 12);   // of a forward CTA, besides rings and weights
+constexpr int kOwnBytes = 1024 + 2176;     // of a CTA of the gradient
 constexpr int kGateToken = 1, kGateDocument = 2;
 
 // How rows of so many units are dealt to threads.
@@ -46,13 +46,18 @@ struct Shape {
     bool shorter;     // several rows a CTA
 };
 
-// Weights in the forward call's shared memory: two rows of them, every thread's units whole.
-int64_t forward_weights(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
+// Weights in shared memory: two rows of them, every thread's units whole.
+int64_t weight_bytes(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
 
-// tensors: those that are read, or 0 for the gradient, whose workspace does not depend on them.
-Shape shape_of(int units, int dtype, int tensors)
+// What the gradient keeps in shared memory with a gate that a document shares: that, and the weights.
+int64_t gate_bytes(const Shape &s, int dtype, bool by_document)
 {
-    const bool gradient = tensors == 0;
+    return by_document ? s.per_thread * s.group * 16 + weight_bytes(s, dtype) : 0;
+}
+
+// tensors: those that are read.
+Shape shape_of(int units, int dtype, bool gradient, int tensors, bool by_document = false)
+{
     Shape s;
     s.shorter = units <= 64;
     s.rows = 1;
@@ -74,32 +79,31 @@ Shape shape_of(int units, int dtype, int tensors)
     const int64_t row = s.per_thread * s.group * 16;   // bytes
     if (gradient) {
         s.threads = s.group;
-        // two rows of the gradient's five tensors have to fit (float32 rows of up to 5120 columns do)
-        if (11 * row > kSharedBytes - kOwnBytes) s.rows = 1;
-        // as many CTAs as registers allow, of which each has room for two chunks
+        // two rows, where they fit in shared memory
+        const int64_t fixed = kOwnBytes + gate_bytes(s, dtype, by_document);
+        if (2 * tensors * row + fixed > kSharedBytes) s.rows = 1;
+        // as many CTAs as registers and shared memory allow: they hide more than chunks fetched ahead do (20011 x 1132
+        // float32, five tensors: 134 us with four CTAs of one chunk, 211 with one of two)
         s.ctas_per_sm = kBackwardThreads / s.group;
-        const int64_t fit = kSharedBytes / (2 * 5 * s.rows * row + kOwnBytes);
+        const int64_t fit = kSharedBytes / (tensors * s.rows * row + fixed);
         if (s.ctas_per_sm > fit) s.ctas_per_sm = fit < 1 ? 1 : static_cast<int>(fit);
         return s;
     }
     // one CTA an SM, of as many teams as registers, barriers and shared memory allow (two rows each, or else one)
     s.ctas_per_sm = 1;
     int teams = kForwardThreads / s.group < kMaxTeams ? kForwardThreads / s.group : kMaxTeams;
-    const int64_t left = kSharedBytes - kForwardOwnBytes - forward_weights(s, dtype);
+    const int64_t left = kSharedBytes - kForwardOwnBytes - weight_bytes(s, dtype);
     if (teams > left / (tensors * row)) teams = static_cast<int>(left / (tensors * row));
     s.threads = teams * s.group;
     return s;
 }
 
-// A document's gate in shared memory.
-int64_t gate_place(const Shape &s, int gate_kind) { return gate_kind == kGateDocument ? s.per_thread * s.group * 16 : 0; }
-
 // Chunks of rows that a ring holds.
 int chunks_of(const Shape &s, int dtype, bool gradient, int gate_kind, int tensors)
 {
     const int64_t chunk = static_cast<int64_t>(tensors) * s.rows * s.per_thread * s.group * 16;
-    const int64_t n = gradient ? (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_place(s, gate_kind)) / chunk
-                               : (kSharedBytes - kForwardOwnBytes - forward_weights(s, dtype)) / (chunk * (s.threads / s.group));
+    const int64_t n = gradient ? (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_bytes(s, dtype, gate_kind == kGateDocument)) / chunk
+                               : (kSharedBytes - kForwardOwnBytes - weight_bytes(s, dtype)) / (chunk * (s.threads / s.group));
     return static_cast<int>(n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : n);
 }
 
@@ -175,21 +179,25 @@ struct Has {
     bool at[U];   // whether unit lane + k * group is one of the row
 };
 
-// Weights of a thread's columns, 0 past the row's end.
+// The weights of a unit, 0 past the row's end.
+template <bool BF16>
+__device__ __forceinline__ void load_weight(const float *w, bool there, int unit, F2 (&out)[Unit<BF16>::E / 2])
+{
+    constexpr int E = Unit<BF16>::E;
+    float f[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) f[e] = 0.0f;
+    if (w != nullptr && there) load_floats<E>(w + static_cast<int64_t>(unit) * E, f);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) out[e / 2] = pair_of(f[e], f[e + 1]);
+}
+
 template <bool BF16, int U>
 __device__ __forceinline__ void load_weights(const float *w, const Has<U> &has, int lane, int group,
                                              F2 (&out)[U][Unit<BF16>::E / 2])
 {
-    constexpr int E = Unit<BF16>::E;
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        float f[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) f[e] = 0.0f;
-        if (w != nullptr && has.at[k]) load_floats<E>(w + static_cast<int64_t>(lane + k * group) * E, f);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) out[k][e / 2] = pair_of(f[e], f[e + 1]);
-    }
+    for (int k = 0; k < U; ++k) load_weight<BF16>(w, has.at[k], lane + k * group, out[k]);
 }
 
 // Weights in registers.
@@ -220,8 +228,8 @@ struct SharedWeights {
 };
 
 // R rows of the forward call. x, h and gate give the data of a unit of a row, bits all random bits, put_y and put_n take a unit's result, sum adds over the rows' threads.
-template <bool BF16, int U, int R, int F, class W, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
-__device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<U> &has, W w1, W w2, X x, H h, G gate,
+template <bool BF16, int U, int R, int F, class W1, class W2, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
+__device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, X x, H h, G gate,
                                              Bits bits, Sum sum, PutY put_y, PutN put_n)
 {
     typedef UnitPairs<BF16> V;
@@ -309,9 +317,9 @@ struct Sums {
 
 // R tokens of the gradient, of which `live` says which there are; dy to gate give the data of a unit of a row.
 // `enter(r)` is called before a token's gate is asked for.
-template <bool BF16, int U, int R, int F, class W, class Live, class DY, class DN, class Y, class H, class Enter, class G,
+template <bool BF16, int U, int R, int F, class W1, class W2, class Live, class DY, class DN, class Y, class H, class Enter, class G,
           class Bits, class Sum, class PutX, class PutH, class PutG>
-__device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has<U> &has, W w1, W w2, Sums<BF16, U> &acc,
+__device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, Sums<BF16, U> &acc,
                                               Live live, DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum,
                                               PutX put_x, PutH put_h, PutG put_gate)
 {
@@ -913,10 +921,6 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    F2 held1[U][E / 2], held2[U][E / 2];
-    load_weights<BF16, U>(p.post, has, lane, p.group, held1);
-    load_weights<BF16, U>(p.pre, has, lane, p.group, held2);
-    const HeldWeights<BF16, U> w1 = {held1}, w2 = {held2};
     Sums<BF16, U> acc;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -928,8 +932,32 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
     Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
     ring.zero_ends(team, p.tensors, row_bytes);
-    // behind the ring stands a document's gate, each thread's part its own
+    // behind the ring: a document's gate, each thread's part its own, and then also the weights, every thread's units whole.
+    // With the other gates' fewer sums the weights have room in registers, and shared memory for another CTA.
     uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * R * p.tensors * place) + lane;
+    constexpr bool kHeld = F >= 0 && F >> 3 != kGateDocument;
+    F2 held1[kHeld ? U : 1][E / 2], held2[kHeld ? U : 1][E / 2];
+    float *weights = reinterpret_cast<float *>(own_gate - lane + U * p.group);
+    const int columns = U * p.group * E;
+    if constexpr (kHeld) {
+        load_weights<BF16, U>(p.post, has, lane, p.group, held1);
+        load_weights<BF16, U>(p.pre, has, lane, p.group, held2);
+    } else if (by_document) {
+        for (int c = threadIdx.x; c < columns; c += p.group) {
+            weights[c] = A::post(p) && c < p.row_elems ? p.post[c] : 0.0f;
+            weights[columns + c] = A::pre(p) && c < p.row_elems ? p.pre[c] : 0.0f;
+        }
+    }
+    auto w1 = [&](int k, F2(&out)[E / 2]) {
+        if constexpr (kHeld) HeldWeights<BF16, U>{held1}(k, out);
+        else if (by_document) SharedWeights<BF16>{weights + lane * E, p.group * E}(k, out);
+        else load_weight<BF16>(p.post, has.at[k], lane + k * p.group, out);
+    };
+    auto w2 = [&](int k, F2(&out)[E / 2]) {
+        if constexpr (kHeld) HeldWeights<BF16, U>{held2}(k, out);
+        else if (by_document) SharedWeights<BF16>{weights + columns + lane * E, p.group * E}(k, out);
+        else load_weight<BF16>(p.pre, has.at[k], lane + k * p.group, out);
+    };
     // places of the tensors in a stage, in units
     const int step = U * p.group;
     const int at_dn = p.x != nullptr ? step : 0, at_y = at_dn + (pre ? step : 0), at_h = at_y + (pre ? step : 0),
@@ -1057,8 +1085,8 @@ int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems 
 size_t ring_bytes(const ResidualParams &p, const Shape &s, int dtype, bool gradient)
 {
     if (!gradient)
-        return static_cast<size_t>(p.stages) * (s.threads / s.group) * p.tensors * s.per_thread * s.group * 16 + forward_weights(s, dtype);
-    return static_cast<size_t>(p.stages) * s.rows * p.tensors * s.per_thread * s.group * 16 + gate_place(s, p.gate_kind);
+        return static_cast<size_t>(p.stages) * (s.threads / s.group) * p.tensors * s.per_thread * s.group * 16 + weight_bytes(s, dtype);
+    return static_cast<size_t>(p.stages) * s.rows * p.tensors * s.per_thread * s.group * 16 + gate_bytes(s, dtype, p.gate_kind == kGateDocument);
 }
 
 // A kernel's limit of dynamic shared memory, raised once on each device.
@@ -1162,7 +1190,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
     p.units = row_units(p.row_elems, dtype);
     p.per_column = 1.0f / static_cast<float>(p.row_elems);
     p.tensors = 1 + (p.h != nullptr) + (p.gate_kind == kGateToken);
-    const Shape s = shape_of(p.units, dtype, p.tensors);
+    const Shape s = shape_of(p.units, dtype, false, p.tensors);
     p.group = s.group;
     int64_t ctas;
     if (s.shorter) {
@@ -1182,17 +1210,22 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
 
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device)
 {
-    const Shape s = shape_of(row_units(row_elems, dtype), dtype, 0);
-    int64_t per_group, ctas;
-    deal(T, s, device, per_group, ctas);
-    return (2 * ctas + 2 * ctas * (s.threads / s.group)) * row_elems * 4;
+    // enough for any options: those that read least have the most CTAs
+    const Shape s = shape_of(row_units(row_elems, dtype), dtype, true, 1);
+    const int64_t groups = s.threads / s.group;
+    int64_t most = static_cast<int64_t>(sm_count(device)) * s.ctas_per_sm * groups;
+    if (most > T) most = T;
+    const int64_t ctas = (most + groups - 1) / groups;
+    return (2 * ctas + 2 * ctas * groups) * row_elems * 4;
 }
 
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream)
 {
     p.units = row_units(p.row_elems, dtype);
     p.per_column = 1.0f / static_cast<float>(p.row_elems);
-    const Shape s = shape_of(p.units, dtype, 0);
+    const bool need_h = p.post != nullptr || p.gate_kind != 0;
+    p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
+    const Shape s = shape_of(p.units, dtype, true, p.tensors, p.gate_kind == kGateDocument);
     p.group = s.group;
     int64_t ctas;
     deal(p.T, s, device, p.per_group, ctas);
@@ -1201,8 +1234,6 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     p.part_pre = p.part_post + ctas * p.row_elems;
     p.part_gate = p.part_pre + ctas * p.row_elems;
     if (p.T > 0) {
-        const bool need_h = p.post != nullptr || p.gate_kind != 0;
-        p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
         p.stages = s.shorter ? 0 : chunks_of(s, dtype, true, p.gate_kind, p.tensors);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
