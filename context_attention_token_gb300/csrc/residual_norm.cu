@@ -155,6 +155,15 @@ __device__ __forceinline__ void store_unit(uint8_t *base, int64_t at, uint4 v)
     __stcs(reinterpret_cast<uint4 *>(base) + at, v);
 }
 
+// A store under a predicate, without a branch that would keep apart what is computed on either side of it.
+__device__ __forceinline__ void store_unit_if(bool there, uint8_t *base, int64_t at, uint4 v)
+{
+    asm volatile("{ .reg .pred p; setp.ne.u32 p, %0, 0; @p st.global.cs.v4.u32 [%1], {%2, %3, %4, %5}; }" ::"r"(
+                     static_cast<uint32_t>(there)),
+                 "l"(reinterpret_cast<uint4 *>(base) + at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                 : "memory");
+}
+
 __device__ __forceinline__ F2 twice(float x) { return pair_of(x, x); }
 
 __device__ __forceinline__ float sum_of(F2 x)
@@ -286,7 +295,7 @@ __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<
                 if (A::drop(p)) keep_or<N>(p.rule, rnd[r][k], u, y[r][k]);
 #pragma unroll
                 for (int i = 0; i < N; ++i) y[r][k][i] = u[i];
-                if (has.at[k]) put_y(r, k, V::pack(y[r][k]));
+                put_y(r, k, has.at[k], V::pack(y[r][k]));
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) q = fma2(y[r][k][i], y[r][k][i], q);   // past the row's end all data are 0
@@ -304,7 +313,7 @@ __device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<
             w2(k, w);
 #pragma unroll
             for (int i = 0; i < N; ++i) y[r][k][i] = mul2(mul2(y[r][k][i], r2), w[i]);
-            if (has.at[k]) put_n(r, k, V::pack(y[r][k]));
+            put_n(r, k, has.at[k], V::pack(y[r][k]));
         }
     }
 }
@@ -388,7 +397,7 @@ __device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has
                     d[i] = fma2(a[i], twice(back), fma2(mul2(b[i], w[i]), twice(r2), d[i]));
                 }
             }
-            if (has.at[k]) put_x(r, k, V::pack(d));
+            put_x(r, k, has.at[k], V::pack(d));
             if (!block) continue;
             if (A::drop(p)) keep_or_zero<N>(p.rule, rnd[r][k], d);
 #pragma unroll
@@ -420,8 +429,8 @@ __device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has
                 if (A::gate(p) == kGateDocument) {
 #pragma unroll
                     for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
-                } else if (has.at[k]) {
-                    put_gate(r, k, V::pack(z));
+                } else {
+                    put_gate(r, k, has.at[k], V::pack(z));
                 }
             }
             if (post) {
@@ -431,8 +440,8 @@ __device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has
                     e[r][k][i] = mul2(d[i], w[i]);
                     q = fma2(e[r][k][i], hn[i], q);
                 }
-            } else if (has.at[k]) {
-                put_h(r, k, V::pack(d));
+            } else {
+                put_h(r, k, has.at[k], V::pack(d));
             }
         }
         t[r] = sum_of(q);
@@ -450,7 +459,7 @@ __device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has
             V::unpack(h(r, k), hn);
 #pragma unroll
             for (int i = 0; i < N; ++i) hn[i] = fma2(hn[i], back, mul2(e[r][k][i], twice(r1[r])));
-            if (has.at[k]) put_h(r, k, V::pack(hn));
+            put_h(r, k, has.at[k], V::pack(hn));
         }
     }
 }
@@ -603,8 +612,8 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
             [&](int, int k) { return r.t[1][k]; }, [&](int, int k) { return r.t[2][k]; },
             [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(r.token), lane, bits[0]); },
             [&](float(&v)[1]) { lanes_sum<1>(v, p.group); },
-            [&](int, int k, uint4 v) { if (in) store_unit(p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
-            [&](int, int k, uint4 v) { if (in) store_unit(p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
+            [&](int, int k, bool there, uint4 v) { store_unit_if(in && there, p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
+            [&](int, int k, bool there, uint4 v) { store_unit_if(in && there, p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
     }
 }
 
@@ -681,9 +690,9 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
             [&](int, int k) { return r.t[4][k]; },
             [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits[0]); },
             [&](auto &v) { lanes_sum(v, p.group); },
-            [&](int, int k, uint4 v) { if (real) store_unit(p.y, at + k * p.group, v); },
-            [&](int, int k, uint4 v) { if (real) store_unit(p.n, at + k * p.group, v); },
-            [&](int, int k, uint4 v) { if (real) store_unit(p.dgate, at + k * p.group, v); });
+            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.y, at + k * p.group, v); },
+            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.n, at + k * p.group, v); },
+            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.dgate, at + k * p.group, v); });
     }
     if (by_document && begin < end) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
 
@@ -895,8 +904,8 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
                 if (waiting) after();
                 waiting = false;
             },
-            [&](int r, int k, uint4 v) { if (put[r]) store_unit(y + at[r], k * p.group, v); },
-            [&](int r, int k, uint4 v) { if (put[r]) store_unit(n + at[r], k * p.group, v); });
+            [&](int r, int k, bool there, uint4 v) { store_unit_if(put[r] && there, y + at[r], k * p.group, v); },
+            [&](int r, int k, bool there, uint4 v) { store_unit_if(put[r] && there, n + at[r], k * p.group, v); });
         if (waiting) {
             sum.stop = sum.team.any(sum.ask);
             after();
@@ -1015,9 +1024,9 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
                 if (waiting) after();
                 waiting = false;
             },
-            [&](int r, int k, uint4 v) { store_unit(p.y + at[r], k * p.group, v); },
-            [&](int r, int k, uint4 v) { store_unit(p.n + at[r], k * p.group, v); },
-            [&](int r, int k, uint4 v) { store_unit(p.dgate + at[r], k * p.group, v); });
+            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.y + at[r], k * p.group, v); },
+            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.n + at[r], k * p.group, v); },
+            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.dgate + at[r], k * p.group, v); });
         if (waiting) {
             sum.stop = sum.team.any(sum.ask);
             after();
