@@ -28,12 +28,11 @@ namespace {
 
 constexpr int kShortThreads = 128;
 constexpr int kForwardThreads = 640;    // of an SM's long rows: 96 registers each
-constexpr int kBackwardThreads = 640;   // 96 registers each
+constexpr int kBackwardThreads = 512;   // 128 registers each
 constexpr int kMaxChunks = 8;
 constexpr int kMaxTeams = 10;              // of a forward CTA
 constexpr int kSharedBytes = 228 * 1024;   // of an SM, 1 KB of each CTA the system's
-constexpr int kForwardOwnBytes = 1024 + 128 + kMaxTeams * (256 + kMaxChunks * 12);   // of a forward CTA, besides rings and weights
-constexpr int kOwnBytes = 1024 + 2176;     // of a CTA of the gradient
+constexpr int kOwnBytes = 1024 + 128 + kMaxTeams * (512 + kMaxChunks * 12);   // of a CTA, besides rings and weights
 constexpr int kGateToken = 1, kGateDocument = 2;
 
 // How rows of so many units are dealt to threads.
@@ -41,26 +40,20 @@ struct Shape {
     int group;        // threads of a row
     int per_thread;   // units of a thread
     int threads;      // of a CTA
-    int rows;         // at a time, of a CTA's long rows
     int ctas_per_sm;
     bool shorter;     // several rows a CTA
+    bool hold;        // the weights in shared memory
 };
 
 // Weights in shared memory: two rows of them, every thread's units whole.
-int64_t weight_bytes(const Shape &s, int dtype) { return 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
-
-// What the gradient keeps in shared memory with a gate that a document shares: that, and the weights.
-int64_t gate_bytes(const Shape &s, int dtype, bool by_document)
-{
-    return by_document ? s.per_thread * s.group * 16 + weight_bytes(s, dtype) : 0;
-}
+int64_t weight_bytes(const Shape &s, int dtype) { return !s.hold ? 0 : 2 * s.per_thread * s.group * (dtype == kBf16 ? 8 : 4) * 4; }
 
 // tensors: those that are read.
 Shape shape_of(int units, int dtype, bool gradient, int tensors, bool by_document = false)
 {
     Shape s;
     s.shorter = units <= 64;
-    s.rows = 1;
+    s.hold = false;
     if (s.shorter) {
         s.per_thread = units > 32 ? 2 : 1;
         s.group = 1;
@@ -70,41 +63,28 @@ Shape shape_of(int units, int dtype, bool gradient, int tensors, bool by_documen
         return s;
     }
     const int eights = dtype == kBf16 ? units : (units + 1) / 2;   // groups of eight columns
-    int wide = 2;                                                  // of a thread
-    s.rows = gradient ? 2 : 1;
-    if (gradient) wide = eights <= kBackwardThreads ? 1 : 2;
-    else wide = eights <= 128 ? 2 : eights <= 192 ? 3 : 5;
+    const int wide = gradient || eights <= 128 ? 2 : eights <= 192 ? 3 : 5;   // of a thread
     s.per_thread = dtype == kBf16 ? wide : 2 * wide;
     s.group = ((eights + wide - 1) / wide + 31) / 32 * 32;
-    const int64_t row = s.per_thread * s.group * 16;   // bytes
-    if (gradient) {
-        s.threads = s.group;
-        // two rows, where they fit in shared memory
-        const int64_t fixed = kOwnBytes + gate_bytes(s, dtype, by_document);
-        if (2 * tensors * row + fixed > kSharedBytes) s.rows = 1;
-        // as many CTAs as registers and shared memory allow: they hide more than chunks fetched ahead do (20011 x 1132
-        // float32, five tensors: 134 us with four CTAs of one chunk, 211 with one of two)
-        s.ctas_per_sm = kBackwardThreads / s.group;
-        const int64_t fit = kSharedBytes / (tensors * s.rows * row + fixed);
-        if (s.ctas_per_sm > fit) s.ctas_per_sm = fit < 1 ? 1 : static_cast<int>(fit);
-        return s;
-    }
-    // one CTA an SM, of as many teams as registers, barriers and shared memory allow (two rows each, or else one)
+    // one CTA an SM, of as many teams as registers, barriers and shared memory allow (a row each at least)
     s.ctas_per_sm = 1;
-    int teams = kForwardThreads / s.group < kMaxTeams ? kForwardThreads / s.group : kMaxTeams;
-    const int64_t left = kSharedBytes - kForwardOwnBytes - weight_bytes(s, dtype);
-    if (teams > left / (tensors * row)) teams = static_cast<int>(left / (tensors * row));
-    s.threads = teams * s.group;
+    const int threads = gradient ? kBackwardThreads : kForwardThreads;
+    const int64_t row = s.per_thread * s.group * 16;   // bytes
+    // (the widest float32 rows of the gradient leave no room for the weights: they are read anew each time)
+    s.hold = true;
+    s.hold = kSharedBytes - kOwnBytes - weight_bytes(s, dtype) >= row * (tensors + by_document);
+    const int64_t left = (kSharedBytes - kOwnBytes - weight_bytes(s, dtype)) / (row * (tensors + by_document));
+    const int teams = threads / s.group < kMaxTeams ? threads / s.group : kMaxTeams;
+    s.threads = static_cast<int>(teams < left ? teams : left) * s.group;
     return s;
 }
 
-// Chunks of rows that a ring holds.
-int chunks_of(const Shape &s, int dtype, bool gradient, int gate_kind, int tensors)
+// Rows that a team's ring holds.
+int stages_of(const Shape &s, int dtype, int tensors, bool by_document)
 {
-    const int64_t chunk = static_cast<int64_t>(tensors) * s.rows * s.per_thread * s.group * 16;
-    const int64_t n = gradient ? (kSharedBytes / s.ctas_per_sm - kOwnBytes - gate_bytes(s, dtype, gate_kind == kGateDocument)) / chunk
-                               : (kSharedBytes - kForwardOwnBytes - weight_bytes(s, dtype)) / (chunk * (s.threads / s.group));
-    return static_cast<int>(n < 1 ? 1 : n > kMaxChunks ? kMaxChunks : n);
+    const int64_t row = static_cast<int64_t>(s.threads / s.group) * s.per_thread * s.group * 16;
+    const int64_t n = (kSharedBytes - kOwnBytes - weight_bytes(s, dtype) - (by_document ? row : 0)) / (row * tensors);
+    return static_cast<int>(n > kMaxChunks ? kMaxChunks : n);
 }
 
 // The document of a raw token: the last d with cu[d] <= t.
@@ -821,7 +801,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float room[kMaxTeams][TeamSum<32>::kRoom];
+    __shared__ float room[kMaxTeams][TeamSum<64>::kRoom];
     __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxChunks];
     __shared__ int32_t index[kMaxTeams][kMaxChunks * R];
     const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
@@ -842,7 +822,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     }
     const SharedWeights<BF16> w1 = {weights + lane * E, p.group * E}, w2 = {weights + columns + lane * E, p.group * E};
     Document doc;
-    TeamSum<32> sum(room[mine], team);
+    TeamSum<64> sum(room[mine], team);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
     uint8_t *rings = smem + 2 * columns * sizeof(float);
     Ring<R> ring = {rings + static_cast<size_t>(mine) * p.stages * R * p.tensors * place, full[mine], index[mine], p.stages, place, place * p.tensors};
@@ -914,16 +894,18 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
 }
 
 template <bool BF16, int U, int R, int F>
-__global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads, 1) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
+__global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ float room[TeamSum<256>::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxChunks];
-    __shared__ int32_t index[kMaxChunks * R];
-    const int lane = threadIdx.x;
-    const int64_t begin = blockIdx.x * p.per_group, end = min(begin + p.per_group, p.T), count = end - begin;
+    __shared__ float room[kMaxTeams][TeamSum<64>::kRoom];
+    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxChunks];
+    __shared__ int32_t index[kMaxTeams][kMaxChunks * R];
+    const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
+    const Team team = {lane, p.group, mine + 1};
+    const int64_t which = static_cast<int64_t>(blockIdx.x) * teams + mine;
+    const int64_t begin = which * p.per_group, end = max(min(begin + p.per_group, p.T), begin), count = end - begin;
     const bool need_h = A::post(p) || A::gate(p) != 0, pre = A::pre(p), by_document = A::gate(p) == kGateDocument;
     DropKey key;
     key.load(p.rule);
@@ -936,37 +918,30 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
     Document doc;
-    const Team team = {lane, p.group, 1};
-    TeamSum<256> sum(room, team);
+    TeamSum<64> sum(room[mine], team);
     const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    Ring<R> ring = {smem, full, index, p.stages, place, place * p.tensors};
-    ring.zero_ends(team, p.tensors, row_bytes);
-    // behind the ring: a document's gate, each thread's part its own, and then also the weights, every thread's units whole.
-    // With the other gates' fewer sums the weights have room in registers, and shared memory for another CTA.
-    uint4 *own_gate = reinterpret_cast<uint4 *>(smem + static_cast<size_t>(p.stages) * R * p.tensors * place) + lane;
-    constexpr bool kHeld = F >= 0 && F >> 3 != kGateDocument;
-    F2 held1[kHeld ? U : 1][E / 2], held2[kHeld ? U : 1][E / 2];
-    float *weights = reinterpret_cast<float *>(own_gate - lane + U * p.group);
-    const int columns = U * p.group * E;
-    if constexpr (kHeld) {
-        load_weights<BF16, U>(p.post, has, lane, p.group, held1);
-        load_weights<BF16, U>(p.pre, has, lane, p.group, held2);
-    } else if (by_document) {
-        for (int c = threadIdx.x; c < columns; c += p.group) {
-            weights[c] = A::post(p) && c < p.row_elems ? p.post[c] : 0.0f;
-            weights[columns + c] = A::pre(p) && c < p.row_elems ? p.pre[c] : 0.0f;
-        }
+    // the weights of all teams, every thread's units whole (or none, for a generic call whose rows leave no room)
+    const bool hold = F >= 0 || p.hold;
+    float *weights = reinterpret_cast<float *>(smem);
+    const int columns = hold ? U * p.group * E : 0;
+    for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+        if (A::post(p)) weights[c] = c < p.row_elems ? p.post[c] : 0.0f;
+        if (A::pre(p)) weights[columns + c] = c < p.row_elems ? p.pre[c] : 0.0f;
     }
     auto w1 = [&](int k, F2(&out)[E / 2]) {
-        if constexpr (kHeld) HeldWeights<BF16, U>{held1}(k, out);
-        else if (by_document) SharedWeights<BF16>{weights + lane * E, p.group * E}(k, out);
+        if (hold) SharedWeights<BF16>{weights + lane * E, p.group * E}(k, out);
         else load_weight<BF16>(p.post, has.at[k], lane + k * p.group, out);
     };
     auto w2 = [&](int k, F2(&out)[E / 2]) {
-        if constexpr (kHeld) HeldWeights<BF16, U>{held2}(k, out);
-        else if (by_document) SharedWeights<BF16>{weights + columns + lane * E, p.group * E}(k, out);
+        if (hold) SharedWeights<BF16>{weights + columns + lane * E, p.group * E}(k, out);
         else load_weight<BF16>(p.pre, has.at[k], lane + k * p.group, out);
     };
+    // a team's: a document's gate, each thread's part its own, and the ring
+    uint8_t *own = smem + 2 * columns * sizeof(float);
+    uint4 *own_gate = reinterpret_cast<uint4 *>(own + mine * place) + lane;
+    if (by_document) own += teams * place;
+    Ring<R> ring = {own + static_cast<size_t>(mine) * p.stages * R * p.tensors * place, full[mine], index[mine], p.stages, place, place * p.tensors};
+    ring.zero_ends(team, p.tensors, row_bytes);
     // places of the tensors in a stage, in units
     const int step = U * p.group;
     const int at_dn = p.x != nullptr ? step : 0, at_y = at_dn + (pre ? step : 0), at_h = at_y + (pre ? step : 0),
@@ -996,14 +971,20 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
             at[r] = static_cast<int64_t>(row) * row_bytes + lane * 16;
             data[r] = ring.row(r) + lane;
         }
+        static_assert(R == 1, "a row that is not there ends here");
+        if (!there[0]) {
+            sum.stop = sum.team.any(sum.ask);
+            after();
+            return;
+        }
         backward_rows<BF16, U, R, F>(
-            p, has, w1, w2, acc, [&](int r) { return there[r]; },
+            p, has, w1, w2, acc, [](int) { return true; },
             [&](int r, int k) { return p.x != nullptr ? data[r][k * p.group] : make_uint4(0, 0, 0, 0); },
             [&](int r, int k) { return data[r][at_dn + k * p.group]; }, [&](int r, int k) { return data[r][at_y + k * p.group]; },
             [&](int r, int k) { return data[r][at_h + k * p.group]; },
             [&](int r) {
                 if (t + r < doc.hi) return;
-                if (doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+                if (doc.hi >= 0) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
                 doc.enter(p, t + r);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
@@ -1032,11 +1013,11 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
             after();
         }
     });
-    if (by_document && doc.hi >= 0) leave_document<BF16, U>(p, doc, blockIdx.x, begin, end, has, lane, acc);
+    if (by_document && doc.hi >= 0) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
         if (w == 0 ? !A::post(p) : !A::pre(p)) continue;
-        float *to = (w == 0 ? p.part_post : p.part_pre) + static_cast<int64_t>(blockIdx.x) * p.row_elems;
+        float *to = (w == 0 ? p.part_post : p.part_pre) + which * p.row_elems;
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             float f[E];
@@ -1044,7 +1025,7 @@ __global__ void __launch_bounds__(U * Unit<BF16>::E > 8 ? 512 : kBackwardThreads
             if (has.at[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, f);
         }
     }
-    zero_padding<U>(p, has, lane, 0, 1);
+    zero_padding<U>(p, has, lane, mine, teams);
 }
 
 // Adds the parts: blockIdx.y 0 and 1 the weights', one warp every 32nd part; the others the documents that
@@ -1091,22 +1072,21 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
 
 int row_units(int64_t row_elems, int dtype) { return static_cast<int>(row_elems * (dtype == kBf16 ? 2 : 4) / 16); }
 
-size_t ring_bytes(const ResidualParams &p, const Shape &s, int dtype, bool gradient)
+size_t shared_bytes(const ResidualParams &p, const Shape &s, int dtype, bool gate)
 {
-    if (!gradient)
-        return static_cast<size_t>(p.stages) * (s.threads / s.group) * p.tensors * s.per_thread * s.group * 16 + weight_bytes(s, dtype);
-    return static_cast<size_t>(p.stages) * s.rows * p.tensors * s.per_thread * s.group * 16 + gate_bytes(s, dtype, p.gate_kind == kGateDocument);
+    const size_t row = static_cast<size_t>(s.threads / s.group) * s.per_thread * s.group * 16;
+    return weight_bytes(s, dtype) + (gate ? row : 0) + row * p.stages * p.tensors;
 }
 
 // A kernel's limit of dynamic shared memory, raised once on each device.
 template <auto kernel>
-cudaError_t allow_shared(int device, int most)
+cudaError_t allow_shared(int device)
 {
     static std::mutex mu;
     static bool done[64] = {false};
     std::lock_guard<std::mutex> lock(mu);
     if (device >= 0 && device < 64 && done[device]) return cudaSuccess;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedBytes - kOwnBytes);
     if (e == cudaSuccess && device >= 0 && device < 64) done[device] = true;
     return e;
 }
@@ -1147,9 +1127,9 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
     }
     constexpr int U = BF16 ? 1 : 2;   // units of eight columns
     auto run = [&](auto kernel) {
-        const cudaError_t e = allow_shared<decltype(kernel)::value>(device, kSharedBytes - kForwardOwnBytes);
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
         if (e != cudaSuccess) return e;
-        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s, BF16 ? kBf16 : kF32, false), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, shared_bytes(p, s, BF16 ? kBf16 : kF32, false), stream>>>(p);
         return cudaGetLastError();
     };
     return with_asked(p, p.h != nullptr, [&](auto f) {
@@ -1170,15 +1150,13 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
     }
     constexpr int U = BF16 ? 1 : 2;   // units of eight columns
     auto run = [&](auto kernel) {
-        const cudaError_t e = allow_shared<decltype(kernel)::value>(device, kSharedBytes - kOwnBytes);
+        const cudaError_t e = allow_shared<decltype(kernel)::value>(device);
         if (e != cudaSuccess) return e;
-        decltype(kernel)::value<<<grid, s.threads, ring_bytes(p, s, BF16 ? kBf16 : kF32, true), stream>>>(p);
+        decltype(kernel)::value<<<grid, s.threads, shared_bytes(p, s, BF16 ? kBf16 : kF32, p.gate_kind == kGateDocument), stream>>>(p);
         return cudaGetLastError();
     };
-    if (s.per_thread == 2 * U)
-        return s.rows == 1 ? run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>())
-                           : run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 2, -1>>());
-    return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, U, 2, decltype(f)::value>>()); });
+    if (!s.hold) return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>());
+    return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, decltype(f)::value>>()); });
 }
 
 // Tokens of a group of the gradient, and its CTAs.
@@ -1210,7 +1188,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
         ctas = (p.rows + p.per_group * groups - 1) / (p.per_group * groups);
     } else {
         deal(p.rows, s, device, p.per_group, ctas);
-        p.stages = chunks_of(s, dtype, false, p.gate_kind, p.tensors);
+        p.stages = stages_of(s, dtype, p.tensors, false);
     }
     if (ctas > 0x7FFFFFFF) return cudaErrorInvalidValue;
     const unsigned grid = static_cast<unsigned>(ctas);
@@ -1224,8 +1202,7 @@ int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int
     const int64_t groups = s.threads / s.group;
     int64_t most = static_cast<int64_t>(sm_count(device)) * s.ctas_per_sm * groups;
     if (most > T) most = T;
-    const int64_t ctas = (most + groups - 1) / groups;
-    return (2 * ctas + 2 * ctas * groups) * row_elems * 4;
+    return (most + groups - 1) / groups * groups * 4 * row_elems * 4;
 }
 
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream)
@@ -1236,14 +1213,16 @@ cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *wor
     p.tensors = (p.x != nullptr) + 2 * (p.pre != nullptr) + need_h + (p.gate_kind == kGateToken);
     const Shape s = shape_of(p.units, dtype, true, p.tensors, p.gate_kind == kGateDocument);
     p.group = s.group;
+    p.hold = s.hold;
     int64_t ctas;
     deal(p.T, s, device, p.per_group, ctas);
-    p.parts = static_cast<int32_t>(ctas);
+    // the weights' parts: a CTA's of short rows, a team's of long ones
+    p.parts = static_cast<int32_t>(s.shorter ? ctas : ctas * (s.threads / s.group));
     p.part_post = static_cast<float *>(workspace);
-    p.part_pre = p.part_post + ctas * p.row_elems;
-    p.part_gate = p.part_pre + ctas * p.row_elems;
+    p.part_pre = p.part_post + static_cast<int64_t>(p.parts) * p.row_elems;
+    p.part_gate = p.part_pre + static_cast<int64_t>(p.parts) * p.row_elems;
     if (p.T > 0) {
-        p.stages = s.shorter ? 0 : chunks_of(s, dtype, true, p.gate_kind, p.tensors);
+        p.stages = s.shorter ? 0 : stages_of(s, dtype, p.tensors, p.gate_kind == kGateDocument);
         const unsigned grid = static_cast<unsigned>(ctas);
         const cudaError_t e = dtype == kBf16 ? launch_backward<true>(p, s, grid, device, stream)
                                              : launch_backward<false>(p, s, grid, device, stream);
