@@ -29,10 +29,10 @@ namespace {
 constexpr int kShortThreads = 128;
 constexpr int kForwardThreads = 640;    // of an SM's long rows: 96 registers each
 constexpr int kBackwardThreads = 512;   // 128 registers each
-constexpr int kMaxChunks = 8;
+constexpr int kMaxStages = 8;
 constexpr int kMaxTeams = 10;              // of a forward CTA
 constexpr int kSharedBytes = 228 * 1024;   // of an SM, 1 KB of each CTA the system's
-constexpr int kOwnBytes = 1024 + 128 + kMaxTeams * (512 + kMaxChunks * 12);   // of a CTA, besides rings and weights
+constexpr int kOwnBytes = 1024 + 128 + kMaxTeams * (512 + kMaxStages * 12);   // of a CTA, besides rings and weights
 constexpr int kGateToken = 1, kGateDocument = 2;
 
 // How rows of so many units are dealt to threads.
@@ -84,7 +84,7 @@ int stages_of(const Shape &s, int dtype, int tensors, bool by_document)
 {
     const int64_t row = static_cast<int64_t>(s.threads / s.group) * s.per_thread * s.group * 16;
     const int64_t n = (kSharedBytes - kOwnBytes - weight_bytes(s, dtype) - (by_document ? row : 0)) / (row * tensors);
-    return static_cast<int>(n > kMaxChunks ? kMaxChunks : n);
+    return static_cast<int>(n > kMaxStages ? kMaxStages : n);
 }
 
 // The document of a raw token: the last d with cu[d] <= t.
@@ -216,85 +216,75 @@ struct SharedWeights {
     }
 };
 
-// R rows of the forward call. x, h and gate give the data of a unit of a row, bits all random bits, put_y and put_n take a unit's result, sum adds over the rows' threads.
-template <bool BF16, int U, int R, int F, class W1, class W2, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
-__device__ __forceinline__ void forward_rows(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, X x, H h, G gate,
-                                             Bits bits, Sum sum, PutY put_y, PutN put_n)
+// One row of the forward call. x, h and gate give the data of a unit of it (0 past the row's end), bits all random bits,
+// put_y and put_n take a unit's result and whether it is one of the row, sum adds over the row's threads.
+template <bool BF16, int U, int F, class W1, class W2, class X, class H, class G, class Bits, class Sum, class PutY, class PutN>
+__device__ __forceinline__ void forward_row(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, X x, H h, G gate,
+                                            Bits bits, Sum sum, PutY put_y, PutN put_n)
 {
     typedef UnitPairs<BF16> V;
     typedef Asked<F> A;
     constexpr int N = V::N;
-    const bool block = A::block(p.h != nullptr);
-    F2 y[R][U][N];
-    uint32_t rnd[R][U][N];
-    float s[R], r1[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-        r1[r] = p.rule.factor;
-        if (!A::post(p)) continue;
-        F2 q = twice(0.0f);
+    F2 y[U][N], q = twice(0.0f);
+    uint32_t rnd[U][N];
+    float s[1];
+    F2 factor = twice(p.rule.factor);
+    if (A::post(p)) {
 #pragma unroll
         for (int k = 0; k < U; ++k) {
             F2 u[N];
-            V::unpack(h(r, k), u);
+            V::unpack(h(k), u);
 #pragma unroll
             for (int i = 0; i < N; ++i) q = fma2(u[i], u[i], q);
         }
-        s[r] = sum_of(q);
     }
-    // the generator needs no data: it runs while the sums are on their way
+    // the generator needs no data: it runs while the sum is on its way
     if (A::drop(p)) bits(rnd);
     if (A::post(p)) {
+        s[0] = sum_of(q);
         sum(s);
-#pragma unroll
-        for (int r = 0; r < R; ++r) r1[r] = __fmul_rn(rsqrt_mean(p, s[r]), p.rule.factor);
+        factor = twice(__fmul_rn(rsqrt_mean(p, s[0]), p.rule.factor));
     }
+    q = twice(0.0f);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        F2 q = twice(0.0f);
+    for (int k = 0; k < U; ++k) {
+        V::unpack(x(k), y[k]);
+        if (A::block(p.h != nullptr)) {
+            F2 u[N];   // h once more: kept over the sum it would cost registers that more rows at a time are worth
+            V::unpack(h(k), u);
+            if (A::post(p)) {
+                F2 w[N];
+                w1(k, w);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            V::unpack(x(r, k), y[r][k]);
-            if (block) {
-                F2 u[N];   // h once more: kept over the sum it would cost registers that a CTA more is worth
-                V::unpack(h(r, k), u);
-                if (A::post(p)) {
-                    F2 w[N];
-                    w1(k, w);
+                for (int i = 0; i < N; ++i) u[i] = mul2(u[i], w[i]);
+            }
+            if (A::gate(p) != 0) {
+                F2 g[N];
+                V::unpack(gate(k), g);
 #pragma unroll
-                    for (int i = 0; i < N; ++i) u[i] = mul2(u[i], w[i]);
-                }
-                if (A::gate(p) != 0) {
-                    F2 g[N];
-                    V::unpack(gate(r, k), g);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) u[i] = mul2(u[i], g[i]);
-                }
-#pragma unroll
-                for (int i = 0; i < N; ++i) u[i] = fma2(u[i], twice(r1[r]), y[r][k][i]);
-                if (A::drop(p)) keep_or<N>(p.rule, rnd[r][k], u, y[r][k]);
-#pragma unroll
-                for (int i = 0; i < N; ++i) y[r][k][i] = u[i];
-                put_y(r, k, has.at[k], V::pack(y[r][k]));
+                for (int i = 0; i < N; ++i) u[i] = mul2(u[i], g[i]);
             }
 #pragma unroll
-            for (int i = 0; i < N; ++i) q = fma2(y[r][k][i], y[r][k][i], q);   // past the row's end all data are 0
+            for (int i = 0; i < N; ++i) u[i] = fma2(u[i], factor, y[k][i]);
+            if (A::drop(p)) keep_or<N>(p.rule, rnd[k], u, y[k]);
+#pragma unroll
+            for (int i = 0; i < N; ++i) y[k][i] = u[i];
+            put_y(k, has.at[k], V::pack(y[k]));
         }
-        s[r] = sum_of(q);
+#pragma unroll
+        for (int i = 0; i < N; ++i) q = fma2(y[k][i], y[k][i], q);
     }
     if (!A::pre(p)) return;
+    s[0] = sum_of(q);
     sum(s);
+    const F2 r2 = twice(rsqrt_mean(p, s[0]));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        const F2 r2 = twice(rsqrt_mean(p, s[r]));
+    for (int k = 0; k < U; ++k) {
+        F2 w[N];
+        w2(k, w);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            F2 w[N];
-            w2(k, w);
-#pragma unroll
-            for (int i = 0; i < N; ++i) y[r][k][i] = mul2(mul2(y[r][k][i], r2), w[i]);
-            put_n(r, k, has.at[k], V::pack(y[r][k]));
-        }
+        for (int i = 0; i < N; ++i) y[k][i] = mul2(mul2(y[k][i], r2), w[i]);
+        put_n(k, has.at[k], V::pack(y[k]));
     }
 }
 
@@ -304,143 +294,123 @@ struct Sums {
     F2 post[U][Unit<BF16>::E / 2], pre[U][Unit<BF16>::E / 2], gate[U][Unit<BF16>::E / 2];
 };
 
-// R tokens of the gradient, of which `live` says which there are; dy to gate give the data of a unit of a row.
-// `enter(r)` is called before a token's gate is asked for.
-template <bool BF16, int U, int R, int F, class W1, class W2, class Live, class DY, class DN, class Y, class H, class Enter, class G,
-          class Bits, class Sum, class PutX, class PutH, class PutG>
-__device__ __forceinline__ void backward_rows(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, Sums<BF16, U> &acc,
-                                              Live live, DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum,
-                                              PutX put_x, PutH put_h, PutG put_gate)
+// One token of the gradient; dy to gate give the data of a unit of its row (0 past the row's end). `enter` is called before
+// the gate is asked for.
+template <bool BF16, int U, int F, class W1, class W2, class DY, class DN, class Y, class H, class Enter, class G, class Bits,
+          class Sum, class PutX, class PutH, class PutG>
+__device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, Sums<BF16, U> &acc,
+                                             DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum, PutX put_x,
+                                             PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
     typedef Asked<F> A;
     constexpr int N = V::N;
-    const bool post = A::post(p), pre = A::pre(p), block = A::block(p.n != nullptr);
-    uint32_t rnd[R][U][N];
-    float s[3 * R];   // of every row: y^2, dn w2 y, h^2
-    if (pre || post) {
+    const bool post = A::post(p), pre = A::pre(p);
+    uint32_t rnd[U][N];
+    F2 q[3] = {twice(0.0f), twice(0.0f), twice(0.0f)};   // y^2, dn w2 y, h^2
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            F2 q0 = twice(0.0f), q1 = q0, q2 = q0;
+    for (int k = 0; k < U; ++k) {
+        if (pre) {
+            F2 a[N], b[N], w[N];
+            V::unpack(y(k), a);
+            V::unpack(dn(k), b);
+            w2(k, w);
 #pragma unroll
-            for (int k = 0; k < U; ++k) {
-                if (pre) {
-                    F2 a[N], b[N], w[N];
-                    V::unpack(y(r, k), a);
-                    V::unpack(dn(r, k), b);
-                    w2(k, w);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) {
-                        q0 = fma2(a[i], a[i], q0);
-                        q1 = fma2(mul2(b[i], w[i]), a[i], q1);
-                    }
-                }
-                if (post) {
-                    F2 a[N];
-                    V::unpack(h(r, k), a);
-#pragma unroll
-                    for (int i = 0; i < N; ++i) q2 = fma2(a[i], a[i], q2);
-                }
+            for (int i = 0; i < N; ++i) {
+                q[0] = fma2(a[i], a[i], q[0]);
+                q[1] = fma2(mul2(b[i], w[i]), a[i], q[1]);
             }
-            s[3 * r] = sum_of(q0);
-            s[3 * r + 1] = sum_of(q1);
-            s[3 * r + 2] = sum_of(q2);
+        }
+        if (post) {
+            F2 a[N];
+            V::unpack(h(k), a);
+#pragma unroll
+            for (int i = 0; i < N; ++i) q[2] = fma2(a[i], a[i], q[2]);
         }
     }
     // the generator needs no data: it runs while the sums are on their way
     if (A::drop(p)) bits(rnd);
+    float s[3] = {sum_of(q[0]), sum_of(q[1]), sum_of(q[2])};
     if (pre || post) sum(s);
-    F2 e[R][U][N];
-    float t[R], r1[R];
+    if (A::gate(p) == kGateDocument) enter();
+    const float r2 = pre ? rsqrt_mean(p, s[0]) : 0.0f, r1 = post ? rsqrt_mean(p, s[2]) : 1.0f;
+    // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
+    const F2 back2 = twice(pre ? -__fmul_rn(__fmul_rn(r2, r2), __fmul_rn(__fmul_rn(s[1], r2), p.per_column)) : 0.0f);
+    F2 e[U][N], t = twice(0.0f);
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        t[r] = r1[r] = 0.0f;
-        if (!live(r)) continue;
-        if (A::gate(p) == kGateDocument) enter(r);
-        const float r2 = pre ? rsqrt_mean(p, s[3 * r]) : 0.0f;
-        // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
-        const float back = pre ? -__fmul_rn(__fmul_rn(r2, r2), __fmul_rn(__fmul_rn(s[3 * r + 1], r2), p.per_column)) : 0.0f;
-        r1[r] = post ? rsqrt_mean(p, s[3 * r + 2]) : 1.0f;
-        F2 q = twice(0.0f);
+    for (int k = 0; k < U; ++k) {
+        F2 d[N];
+        V::unpack(dy(k), d);
+        if (pre) {
+            F2 a[N], b[N], w[N];
+            V::unpack(y(k), a);
+            V::unpack(dn(k), b);
+            w2(k, w);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            F2 d[N];
-            V::unpack(dy(r, k), d);
-            if (pre) {
-                F2 a[N], b[N], w[N];
-                V::unpack(y(r, k), a);
-                V::unpack(dn(r, k), b);
-                w2(k, w);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    acc.pre[k][i] = fma2(mul2(a[i], b[i]), twice(r2), acc.pre[k][i]);
-                    d[i] = fma2(a[i], twice(back), fma2(mul2(b[i], w[i]), twice(r2), d[i]));
-                }
+            for (int i = 0; i < N; ++i) {
+                acc.pre[k][i] = fma2(mul2(a[i], b[i]), twice(r2), acc.pre[k][i]);
+                d[i] = fma2(a[i], back2, fma2(mul2(b[i], w[i]), twice(r2), d[i]));
             }
-            put_x(r, k, has.at[k], V::pack(d));
-            if (!block) continue;
-            if (A::drop(p)) keep_or_zero<N>(p.rule, rnd[r][k], d);
+        }
+        put_x(k, has.at[k], V::pack(d));
+        if (!A::block(p.n != nullptr)) continue;
+        if (A::drop(p)) keep_or_zero<N>(p.rule, rnd[k], d);
 #pragma unroll
-            for (int i = 0; i < N; ++i) d[i] = mul2(d[i], twice(p.rule.factor));
-            F2 hn[N], w[N];
-            if (post) w1(k, w);
-            if (post || A::gate(p) != 0) {
-                V::unpack(h(r, k), hn);
-                if (post) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1[r]));
-                }
-            }
-            if (A::gate(p) != 0) {
-                F2 g[N], z[N];
-                V::unpack(gate(r, k), g);
-                // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a
-                // whole document shares, a row with an infinity is NaN throughout)
-                const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
-                    d[i] = mul2(d[i], g[i]);
-                }
-                if (guard) {
-                    keep_or_zero<N>(p.rule, rnd[r][k], z);
-                    keep_or_zero<N>(p.rule, rnd[r][k], d);
-                }
-                if (A::gate(p) == kGateDocument) {
-#pragma unroll
-                    for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
-                } else {
-                    put_gate(r, k, has.at[k], V::pack(z));
-                }
-            }
+        for (int i = 0; i < N; ++i) d[i] = mul2(d[i], twice(p.rule.factor));
+        F2 hn[N], w[N];
+        if (post) w1(k, w);
+        if (post || A::gate(p) != 0) {
+            V::unpack(h(k), hn);
             if (post) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
-                    e[r][k][i] = mul2(d[i], w[i]);
-                    q = fma2(e[r][k][i], hn[i], q);
-                }
-            } else {
-                put_h(r, k, has.at[k], V::pack(d));
+                for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1));
             }
         }
-        t[r] = sum_of(q);
+        if (A::gate(p) != 0) {
+            F2 g[N], z[N];
+            V::unpack(gate(k), g);
+            // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a whole
+            // document shares, a row with an infinity is NaN throughout)
+            const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
+                d[i] = mul2(d[i], g[i]);
+            }
+            if (guard) {
+                keep_or_zero<N>(p.rule, rnd[k], z);
+                keep_or_zero<N>(p.rule, rnd[k], d);
+            }
+            if (A::gate(p) == kGateDocument) {
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
+            } else {
+                put_gate(k, has.at[k], V::pack(z));
+            }
+        }
+        if (post) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
+                e[k][i] = mul2(d[i], w[i]);
+                t = fma2(e[k][i], hn[i], t);
+            }
+        } else {
+            put_h(k, has.at[k], V::pack(d));
+        }
     }
     if (!post) return;
-    sum(t);
+    float m[1] = {sum_of(t)};
+    sum(m);
+    // dh = r1 e - h r1^2 mean(e hn)
+    const F2 back1 = twice(-__fmul_rn(__fmul_rn(r1, r1), __fmul_rn(m[0], p.per_column)));
 #pragma unroll
-    for (int r = 0; r < R; ++r) {
-        if (!live(r)) continue;
-        // dh = r1 e - h r1^2 mean(e hn)
-        const F2 back = twice(-__fmul_rn(__fmul_rn(r1[r], r1[r]), __fmul_rn(t[r], p.per_column)));
+    for (int k = 0; k < U; ++k) {
+        F2 hn[N];
+        V::unpack(h(k), hn);
 #pragma unroll
-        for (int k = 0; k < U; ++k) {
-            F2 hn[N];
-            V::unpack(h(r, k), hn);
-#pragma unroll
-            for (int i = 0; i < N; ++i) hn[i] = fma2(hn[i], back, mul2(e[r][k][i], twice(r1[r])));
-            put_h(r, k, has.at[k], V::pack(hn));
-        }
+        for (int i = 0; i < N; ++i) hn[i] = fma2(hn[i], back1, mul2(e[k][i], twice(r1)));
+        put_h(k, has.at[k], V::pack(hn));
     }
 }
 
@@ -587,13 +557,13 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
         if (i + 1 < p.per_group) load(row + 1, next);
         const bool in = row < p.rows, real = r.token >= 0;
         const int64_t at = row * p.units + lane;
-        forward_rows<BF16, U, 1, -1>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int, int k) { return r.t[0][k]; },
-            [&](int, int k) { return r.t[1][k]; }, [&](int, int k) { return r.t[2][k]; },
-            [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(r.token), lane, bits[0]); },
+        forward_row<BF16, U, -1>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int k) { return r.t[0][k]; },
+            [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; },
+            [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(r.token), lane, bits); },
             [&](float(&v)[1]) { lanes_sum<1>(v, p.group); },
-            [&](int, int k, bool there, uint4 v) { store_unit_if(in && there, p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
-            [&](int, int k, bool there, uint4 v) { store_unit_if(in && there, p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
+            [&](int k, bool there, uint4 v) { store_unit_if(in && there, p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
+            [&](int k, bool there, uint4 v) { store_unit_if(in && there, p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
     }
 }
 
@@ -663,16 +633,15 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
                 if (has.at[k]) r.t[4][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
         }
         const int64_t at = r.row * p.units + lane;
-        backward_rows<BF16, U, 1, -1>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int) { return true; },
-            [&](int, int k) { return r.t[0][k]; }, [&](int, int k) { return r.t[1][k]; },
-            [&](int, int k) { return r.t[2][k]; }, [&](int, int k) { return r.t[3][k]; }, [](int) {},
-            [&](int, int k) { return r.t[4][k]; },
-            [&](uint32_t(&bits)[1][U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits[0]); },
+        backward_row<BF16, U, -1>(
+            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; }, [&](int k) { return r.t[1][k]; },
+            [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; }, []() {},
+            [&](int k) { return r.t[4][k]; },
+            [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits); },
             [&](auto &v) { lanes_sum(v, p.group); },
-            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.y, at + k * p.group, v); },
-            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.n, at + k * p.group, v); },
-            [&](int, int k, bool there, uint4 v) { store_unit_if(real && there, p.dgate, at + k * p.group, v); });
+            [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.y, at + k * p.group, v); },
+            [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.n, at + k * p.group, v); },
+            [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.dgate, at + k * p.group, v); });
     }
     if (by_document && begin < end) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
 
@@ -700,94 +669,87 @@ __global__ void __launch_bounds__(kShortThreads, U == 1 ? 4 : 2) residual_norm_b
     zero_padding<U>(p, has, lane, threadIdx.x / p.group, groups);
 }
 
-// ----------------------------------------------------------------- long rows: a CTA each
+// ----------------------------------------------------------------- long rows: a team of warps each
 
-// A ring of chunks of R rows in shared memory. A team's first warp has the bulk-copy engine fetch the rows of all input
-// tensors, one instruction a row, a lane for each.
-template <int R>
+// A ring of rows in shared memory. A team's first warp has the bulk-copy engine fetch the row of every input tensor, a
+// lane and one instruction for each.
 struct Ring {
     uint8_t *smem;
-    uint64_t *full;                // of every chunk
-    int32_t *index;                // [chunks][R]: of a chunk's rows, a forward call's token or a gradient's row (-1: none)
-    int chunks;
+    uint64_t *full;                // of every stage
+    int32_t *index;                // of every stage: a forward call's token or a gradient's row (-1: none)
+    int stages;
     uint32_t place, stage_bytes;   // bytes of a row's place (every thread's units whole) and of all tensors'
     int slot = 0;
     uint32_t phase = 0;
 
-    // the current chunk's row r of tensor 0
-    __device__ __forceinline__ const uint4 *row(int r) const
-    {
-        return reinterpret_cast<const uint4 *>(smem + (slot * R + r) * stage_bytes);
-    }
+    // the current row of tensor 0
+    __device__ __forceinline__ const uint4 *row() const { return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes); }
     // What no copy writes: the ends of the places, behind the rows.
     __device__ __forceinline__ void zero_ends(const Team &team, int tensors, uint32_t row_bytes)
     {
-        for (int i = 0; i < chunks * R * tensors; ++i)
+        for (int i = 0; i < stages * tensors; ++i)
             for (uint32_t at = row_bytes + team.thread * 16; at < place; at += team.threads * 16)
                 *reinterpret_cast<uint4 *>(smem + i * place + at) = make_uint4(0, 0, 0, 0);
+    }
+    __device__ __forceinline__ void advance()
+    {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
+        }
     }
 };
 
 __device__ unsigned int g_wait_timeouts;
 
-// Runs `rows(i, after)` for i = 0, R, 2 R, ... below count with the chunk's data in the ring. It has to call after()
-// once behind its first barrier, where every thread is done with the chunk before; `sum` votes there whether a wait
-// has run out. index_of(i) looks the i-th up (-1: it is not read), row_of(i, index) is its row, base this lane's tensor.
-template <int R, class Sum, class Index, class RowOf, class Rows>
-__device__ __forceinline__ void walk(Ring<R> &ring, Sum &sum, int64_t count, int tensors, uint32_t row_bytes,
-                                     const uint8_t *base, Index index_of, RowOf row_of, Rows rows)
+// Runs `work(i, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
+// first barrier, where every thread is done with the row before; `sum` votes there whether a wait has run
+// out. index_of(i) looks the i-th row up (-1: it is not read), row_of(i, index) is its place in this lane's tensor, `base`.
+template <class Sum, class Index, class RowOf, class Work>
+__device__ __forceinline__ void walk(Ring &ring, Sum &sum, int64_t count, int tensors, uint32_t row_bytes, const uint8_t *base,
+                                     Index index_of, RowOf row_of, Work work)
 {
-    const int lane = sum.team.thread & 31, tensor = lane / R, r = lane - tensor * R;
-    const bool first = sum.team.thread < 32;
+    const int lane = sum.team.thread & 31;
+    const bool first = sum.team.thread < 32, several = ring.stages > 1;
     int64_t issued = 0;
     int put = 0;
-    int32_t ahead = first ? index_of(r) : -1;   // looked up a chunk early
+    int32_t ahead = first ? index_of(0) : -1;   // looked up a row early
     auto issue = [&]() {   // by the first warp
         if (issued >= count) return;
-        const int32_t index = ahead;
         uint64_t *bar = &ring.full[put];
-        const int some = __popc(__ballot_sync(0xFFFFFFFFu, tensor == 0 && index >= 0));
-        if (tensor == 0) ring.index[put * R + r] = index;
+        if (lane == 0) {
+            ring.index[put] = ahead;
+            mbar_expect_tx(bar, ahead >= 0 ? static_cast<uint32_t>(tensors) * row_bytes : 0);
+        }
         __syncwarp();
-        if (lane == 0) mbar_expect_tx(bar, static_cast<uint32_t>(some * tensors) * row_bytes);
-        if (tensor < tensors && index >= 0)
-            bulk_load(ring.smem + (put * R + r) * ring.stage_bytes + tensor * ring.place,
-                      base + row_of(issued + r, index) * row_bytes, row_bytes, bar);
-        issued += R;
-        ahead = index_of(issued + r);
-        if (++put == ring.chunks) put = 0;
+        if (lane < tensors && ahead >= 0)
+            bulk_load(ring.smem + put * ring.stage_bytes + lane * ring.place, base + row_of(issued, ahead) * row_bytes, row_bytes, bar);
+        ahead = index_of(++issued);
+        if (++put == ring.stages) put = 0;
     };
     if (sum.team.thread == 0) {
-        for (int c = 0; c < ring.chunks; ++c) mbar_init(&ring.full[c], 1);
+        for (int c = 0; c < ring.stages; ++c) mbar_init(&ring.full[c], 1);
         mbar_init_fence();
     }
     __syncthreads();   // of all teams: what else was put into shared memory is there too
     if (first)
-        for (int c = 0; c < ring.chunks; ++c) issue();
-    const bool several = ring.chunks > 1;
-    for (int64_t i = 0; i < count; i += R) {
+        for (int c = 0; c < ring.stages; ++c) issue();
+    for (int64_t i = 0; i < count; ++i) {
         if (!mbar_wait_bounded(&ring.full[ring.slot], ring.phase)) sum.ask = true;
-        // the place of the chunk before is filled again
-        rows(i, [&]() {
-            if (several && first && i > 0) issue();
+        work(i, [&]() {
+            if (several && first && i > 0) issue();   // into the place of the row before
         });
-        if (++ring.slot == ring.chunks) {
-            ring.slot = 0;
-            ring.phase ^= 1;
-        }
+        ring.advance();
         if (!several) {
             sum.stop = sum.team.any(sum.ask);
             if (first && !sum.stop) issue();
         }
         if (sum.stop) {   // by all: no copy may end in another CTA's shared memory
-            if (sum.team.thread == 0) {
-                atomicAdd(&g_wait_timeouts, 1u);
-                for (int64_t k = i + R; k < issued; k += R) {
+            if (first) {
+                if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
+                for (int64_t k = i + 1; k < issued; ++k) {
                     mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
-                    if (++ring.slot == ring.chunks) {
-                        ring.slot = 0;
-                        ring.phase ^= 1;
-                    }
+                    ring.advance();
                 }
             }
             return;
@@ -795,15 +757,25 @@ __device__ __forceinline__ void walk(Ring<R> &ring, Sum &sum, int64_t count, int
     }
 }
 
-template <bool BF16, int U, int R, int F>
+// The weights of all teams in shared memory, every thread's units whole.
+template <int F>
+__device__ __forceinline__ void share_weights(const ResidualParams &p, float *to, int columns)
+{
+    for (int c = threadIdx.x; c < columns; c += blockDim.x) {
+        if (Asked<F>::post(p)) to[c] = c < p.row_elems ? p.post[c] : 0.0f;
+        if (Asked<F>::pre(p)) to[columns + c] = c < p.row_elems ? p.pre[c] : 0.0f;
+    }
+}
+
+template <bool BF16, int U, int F>
 __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float room[kMaxTeams][TeamSum<64>::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxChunks];
-    __shared__ int32_t index[kMaxTeams][kMaxChunks * R];
+    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxStages];
+    __shared__ int32_t index[kMaxTeams][kMaxStages];
     const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
     const Team team = {lane, p.group, mine + 1};
     const int64_t begin = (static_cast<int64_t>(blockIdx.x) * teams + mine) * p.per_group;
@@ -813,19 +785,15 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     Has<U> has;
 #pragma unroll
     for (int k = 0; k < U; ++k) has.at[k] = lane + k * p.group < p.units;
-    // the weights of all teams, every thread's units whole
     float *weights = reinterpret_cast<float *>(smem);
     const int columns = U * p.group * E;
-    for (int c = threadIdx.x; c < columns; c += blockDim.x) {
-        if (A::post(p)) weights[c] = c < p.row_elems ? p.post[c] : 0.0f;
-        if (A::pre(p)) weights[columns + c] = c < p.row_elems ? p.pre[c] : 0.0f;
-    }
+    share_weights<F>(p, weights, columns);
     const SharedWeights<BF16> w1 = {weights + lane * E, p.group * E}, w2 = {weights + columns + lane * E, p.group * E};
     Document doc;
     TeamSum<64> sum(room[mine], team);
-    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    uint8_t *rings = smem + 2 * columns * sizeof(float);
-    Ring<R> ring = {rings + static_cast<size_t>(mine) * p.stages * R * p.tensors * place, full[mine], index[mine], p.stages, place, place * p.tensors};
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u, stage = place * p.tensors;
+    Ring ring = {smem + 2 * columns * sizeof(float) + static_cast<size_t>(mine) * p.stages * stage, full[mine], index[mine],
+                 p.stages, place, stage};
     ring.zero_ends(team, p.tensors, row_bytes);
 
     auto token_of = [&](int64_t i) {
@@ -834,74 +802,60 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
         return t >= 0 && in_bounds(t < p.T) ? t : -1;
     };
     // the rows are neighbours, padding is not read
-    const int tensor = (lane & 31) / R;
-    const uint8_t *base = tensor == 0 ? p.x : tensor == 1 && A::block(p.h != nullptr) ? p.h : p.gate;
     auto row_of = [&](int64_t i, int32_t) { return begin + i; };
+    const int tensor = lane & 31;
+    const uint8_t *base = tensor == 0 ? p.x : tensor == 1 && A::block(p.h != nullptr) ? p.h : p.gate;
     uint8_t *y = p.y, *n = p.n;
-    walk<R>(ring, sum, count, p.tensors, row_bytes, base, token_of, row_of, [&](int64_t i, auto after) {
-        int32_t token[R];
-        bool put[R];
-        uint4 gate[R][U];   // of the rows' documents
-        const uint4 *data[R];
-        int64_t at[R];      // of this thread's first unit, in bytes
-        bool waiting = true;
+    walk(ring, sum, count, p.tensors, row_bytes, base, token_of, row_of, [&](int64_t i, auto after) {
+        const int32_t token = ring.index[ring.slot];
+        const bool real = token >= 0;
+        const uint4 *data = ring.row() + lane;
+        const int64_t at = (begin + i) * row_bytes + lane * 16;   // of this thread's first unit, in bytes
+        uint4 gate[U];                                            // of the row's document
+        if (A::gate(p) == kGateDocument) {
+            if (real) doc.enter(p, token);
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            token[r] = ring.index[ring.slot * R + r];
-            put[r] = token[r] >= 0;
-            data[r] = ring.row(r) + lane;
-            at[r] = static_cast<int64_t>(static_cast<uint32_t>(begin) + static_cast<uint32_t>(i) + r) * row_bytes + lane * 16;
-            if (A::gate(p) == kGateDocument) {
-                if (put[r]) doc.enter(p, token[r]);
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    gate[r][k] = make_uint4(0, 0, 0, 0);
-                    if (put[r] && has.at[k])
-                        gate[r][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
-                }
-            }
-            if (!put[r] && i + r < count) {   // padding
-#pragma unroll
-                for (int k = 0; k < U; ++k) {
-                    if (!has.at[k]) continue;
-                    if (y != nullptr) store_unit(y + at[r], k * p.group, make_uint4(0, 0, 0, 0));
-                    if (n != nullptr) store_unit(n + at[r], k * p.group, make_uint4(0, 0, 0, 0));
-                }
+            for (int k = 0; k < U; ++k) {
+                gate[k] = make_uint4(0, 0, 0, 0);
+                if (real && has.at[k])
+                    gate[k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
             }
         }
-        forward_rows<BF16, U, R, F>(
-            p, has, w1, w2, [&](int r, int k) { return data[r][k * p.group]; },
-            [&](int r, int k) { return data[r][(U + k) * p.group]; },
-            [&](int r, int k) { return A::gate(p) == kGateToken ? data[r][(2 * U + k) * p.group] : gate[r][k]; },
-            [&](uint32_t(&bits)[R][U][E / 2]) {
-                uint32_t tokens[R];
+        if (!real) {
 #pragma unroll
-                for (int r = 0; r < R; ++r) tokens[r] = static_cast<uint32_t>(token[r]);
-                thread_bits<BF16, U, R>(p.rule, key, tokens, lane, p.group, bits);
-            },
-            [&](float(&v)[R]) {
+            for (int k = 0; k < U; ++k) {
+                store_unit_if(has.at[k] && y != nullptr, y + at, k * p.group, make_uint4(0, 0, 0, 0));
+                store_unit_if(has.at[k] && n != nullptr, n + at, k * p.group, make_uint4(0, 0, 0, 0));
+            }
+        }
+        bool waiting = true;
+        forward_row<BF16, U, F>(
+            p, has, w1, w2, [&](int k) { return data[k * p.group]; }, [&](int k) { return data[(U + k) * p.group]; },
+            [&](int k) { return A::gate(p) == kGateToken ? data[(2 * U + k) * p.group] : gate[k]; },
+            [&](uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(token), lane, p.group, bits); },
+            [&](float(&v)[1]) {
                 sum(v);
                 if (waiting) after();
                 waiting = false;
             },
-            [&](int r, int k, bool there, uint4 v) { store_unit_if(put[r] && there, y + at[r], k * p.group, v); },
-            [&](int r, int k, bool there, uint4 v) { store_unit_if(put[r] && there, n + at[r], k * p.group, v); });
-        if (waiting) {
-            sum.stop = sum.team.any(sum.ask);
+            [&](int k, bool there, uint4 v) { store_unit_if(real && there, y + at, k * p.group, v); },
+            [&](int k, bool there, uint4 v) { store_unit_if(real && there, n + at, k * p.group, v); });
+        if (waiting) {   // no norm, no sum
+            sum.stop = team.any(sum.ask);
             after();
         }
     });
 }
 
-template <bool BF16, int U, int R, int F>
+template <bool BF16, int U, int F>
 __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_kernel(const __grid_constant__ ResidualParams p)
 {
     constexpr int E = Unit<BF16>::E;
     typedef Asked<F> A;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float room[kMaxTeams][TeamSum<64>::kRoom];
-    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxChunks];
-    __shared__ int32_t index[kMaxTeams][kMaxChunks * R];
+    __shared__ __align__(8) uint64_t full[kMaxTeams][kMaxStages];
+    __shared__ int32_t index[kMaxTeams][kMaxStages];
     const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
     const Team team = {lane, p.group, mine + 1};
     const int64_t which = static_cast<int64_t>(blockIdx.x) * teams + mine;
@@ -919,15 +873,12 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         for (int i = 0; i < E / 2; ++i) acc.post[k][i] = acc.pre[k][i] = acc.gate[k][i] = twice(0.0f);
     Document doc;
     TeamSum<64> sum(room[mine], team);
-    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u;
-    // the weights of all teams, every thread's units whole (or none, for a generic call whose rows leave no room)
+    const uint32_t place = U * p.group * 16u, row_bytes = p.units * 16u, stage = place * p.tensors;
+    // no weights are held for a call whose rows leave no room (a generic one)
     const bool hold = F >= 0 || p.hold;
     float *weights = reinterpret_cast<float *>(smem);
     const int columns = hold ? U * p.group * E : 0;
-    for (int c = threadIdx.x; c < columns; c += blockDim.x) {
-        if (A::post(p)) weights[c] = c < p.row_elems ? p.post[c] : 0.0f;
-        if (A::pre(p)) weights[columns + c] = c < p.row_elems ? p.pre[c] : 0.0f;
-    }
+    share_weights<F>(p, weights, columns);
     auto w1 = [&](int k, F2(&out)[E / 2]) {
         if (hold) SharedWeights<BF16>{weights + lane * E, p.group * E}(k, out);
         else load_weight<BF16>(p.post, has.at[k], lane + k * p.group, out);
@@ -936,18 +887,18 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         if (hold) SharedWeights<BF16>{weights + columns + lane * E, p.group * E}(k, out);
         else load_weight<BF16>(p.pre, has.at[k], lane + k * p.group, out);
     };
-    // a team's: a document's gate, each thread's part its own, and the ring
+    // a team's own: a document's gate, each thread's part written and read by itself, and the ring
     uint8_t *own = smem + 2 * columns * sizeof(float);
     uint4 *own_gate = reinterpret_cast<uint4 *>(own + mine * place) + lane;
     if (by_document) own += teams * place;
-    Ring<R> ring = {own + static_cast<size_t>(mine) * p.stages * R * p.tensors * place, full[mine], index[mine], p.stages, place, place * p.tensors};
+    Ring ring = {own + static_cast<size_t>(mine) * p.stages * stage, full[mine], index[mine], p.stages, place, stage};
     ring.zero_ends(team, p.tensors, row_bytes);
     // places of the tensors in a stage, in units
     const int step = U * p.group;
     const int at_dn = p.x != nullptr ? step : 0, at_y = at_dn + (pre ? step : 0), at_h = at_y + (pre ? step : 0),
               at_gate = at_h + (need_h ? step : 0);
     // this lane's tensor
-    int left = (lane & 31) / R;
+    int left = lane & 31;
     const uint8_t *base = nullptr;
     for (const uint8_t *b : {p.x, pre ? p.dn : nullptr, pre ? p.y_in : nullptr, need_h ? p.h : nullptr,
                              A::gate(p) == kGateToken ? p.gate : nullptr})
@@ -959,33 +910,24 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         return static_cast<int32_t>(row >= 0 && in_bounds(row < p.rows) ? row : -1);
     };
     auto row_of = [&](int64_t, int32_t row) { return static_cast<int64_t>(row); };
-    walk<R>(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int64_t i, auto after) {
-        const uint4 *data[R];
-        int64_t at[R];      // of this thread's first unit, in bytes
-        bool there[R], waiting = true;
-        const int64_t t = begin + i;
-#pragma unroll
-        for (int r = 0; r < R; ++r) {
-            const int32_t row = ring.index[ring.slot * R + r];
-            there[r] = row >= 0;
-            at[r] = static_cast<int64_t>(row) * row_bytes + lane * 16;
-            data[r] = ring.row(r) + lane;
-        }
-        static_assert(R == 1, "a row that is not there ends here");
-        if (!there[0]) {
-            sum.stop = sum.team.any(sum.ask);
+    walk(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int64_t i, auto after) {
+        const int32_t row = ring.index[ring.slot];
+        if (row < 0) {   // an index that a check refused
+            sum.stop = team.any(sum.ask);
             after();
             return;
         }
-        backward_rows<BF16, U, R, F>(
-            p, has, w1, w2, acc, [](int) { return true; },
-            [&](int r, int k) { return p.x != nullptr ? data[r][k * p.group] : make_uint4(0, 0, 0, 0); },
-            [&](int r, int k) { return data[r][at_dn + k * p.group]; }, [&](int r, int k) { return data[r][at_y + k * p.group]; },
-            [&](int r, int k) { return data[r][at_h + k * p.group]; },
-            [&](int r) {
-                if (t + r < doc.hi) return;
+        const int64_t t = begin + i, at = static_cast<int64_t>(row) * row_bytes + lane * 16;
+        const uint4 *data = ring.row() + lane;
+        bool waiting = true;
+        backward_row<BF16, U, F>(
+            p, has, w1, w2, acc, [&](int k) { return p.x != nullptr ? data[k * p.group] : make_uint4(0, 0, 0, 0); },
+            [&](int k) { return data[at_dn + k * p.group]; }, [&](int k) { return data[at_y + k * p.group]; },
+            [&](int k) { return data[at_h + k * p.group]; },
+            [&]() {
+                if (t < doc.hi) return;
                 if (doc.hi >= 0) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
-                doc.enter(p, t + r);
+                doc.enter(p, t);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     uint4 g = make_uint4(0, 0, 0, 0);
@@ -993,23 +935,18 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
                     own_gate[k * p.group] = g;
                 }
             },
-            [&](int r, int k) { return by_document ? own_gate[k * p.group] : data[r][at_gate + k * p.group]; },
-            [&](uint32_t(&bits)[R][U][E / 2]) {
-                uint32_t tokens[R];
-#pragma unroll
-                for (int r = 0; r < R; ++r) tokens[r] = static_cast<uint32_t>(t + r);
-                thread_bits<BF16, U, R>(p.rule, key, tokens, lane, p.group, bits);
-            },
+            [&](int k) { return by_document ? own_gate[k * p.group] : data[at_gate + k * p.group]; },
+            [&](uint32_t(&bits)[U][E / 2]) { thread_bits<BF16, U>(p.rule, key, static_cast<uint32_t>(t), lane, p.group, bits); },
             [&](auto &v) {
                 sum(v);
                 if (waiting) after();
                 waiting = false;
             },
-            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.y + at[r], k * p.group, v); },
-            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.n + at[r], k * p.group, v); },
-            [&](int r, int k, bool there_too, uint4 v) { store_unit_if(there_too, p.dgate + at[r], k * p.group, v); });
-        if (waiting) {
-            sum.stop = sum.team.any(sum.ask);
+            [&](int k, bool there, uint4 v) { store_unit_if(there, p.y + at, k * p.group, v); },
+            [&](int k, bool there, uint4 v) { store_unit_if(there, p.n + at, k * p.group, v); },
+            [&](int k, bool there, uint4 v) { store_unit_if(there, p.dgate + at, k * p.group, v); });
+        if (waiting) {   // no norm, no sum
+            sum.stop = team.any(sum.ask);
             after();
         }
     });
@@ -1134,9 +1071,9 @@ cudaError_t launch_forward(const ResidualParams &p, const Shape &s, unsigned gri
     };
     return with_asked(p, p.h != nullptr, [&](auto f) {
         constexpr int F = decltype(f)::value;
-        if (s.per_thread == 2 * U) return run(Kernel<residual_norm_long_kernel<BF16, 2 * U, 1, F>>());
-        if (s.per_thread == 3 * U) return run(Kernel<residual_norm_long_kernel<BF16, 3 * U, 1, F>>());
-        return run(Kernel<residual_norm_long_kernel<BF16, 5 * U, 1, F>>());
+        if (s.per_thread == 2 * U) return run(Kernel<residual_norm_long_kernel<BF16, 2 * U, F>>());
+        if (s.per_thread == 3 * U) return run(Kernel<residual_norm_long_kernel<BF16, 3 * U, F>>());
+        return run(Kernel<residual_norm_long_kernel<BF16, 5 * U, F>>());
     });
 }
 
@@ -1155,8 +1092,8 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, unsigned gr
         decltype(kernel)::value<<<grid, s.threads, shared_bytes(p, s, BF16 ? kBf16 : kF32, p.gate_kind == kGateDocument), stream>>>(p);
         return cudaGetLastError();
     };
-    if (!s.hold) return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, -1>>());
-    return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, 1, decltype(f)::value>>()); });
+    if (!s.hold) return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, -1>>());
+    return with_asked(p, p.n != nullptr, [&](auto f) { return run(Kernel<residual_norm_backward_long_kernel<BF16, 2 * U, decltype(f)::value>>()); });
 }
 
 // Tokens of a group of the gradient, and its CTAs.

@@ -129,41 +129,36 @@ __device__ __forceinline__ void unit_bits(const DropRule &r, const DropKey &key,
     }
 }
 
-// The bits of a thread's units lane, lane + group, ... of R tokens' rows, with even groups of whole warps. Two
-// neighbouring lanes have the halves of the same group of eight float32 columns: each calls the generator for one of
-// two units and they exchange what the other needs.
-template <bool BF16, int U, int R>
-__device__ __forceinline__ void thread_bits(const DropRule &r, const DropKey &key, const uint32_t (&token)[R], int lane,
-                                            int group, uint32_t (&bits)[R][U][Unit<BF16>::E / 2])
+// The bits of a thread's units lane, lane + group, ... of a token's row, with groups of whole warps. Two neighbouring
+// lanes have the halves of the same group of eight float32 columns: each calls the generator for one of two units
+// and they exchange what the other needs.
+template <bool BF16, int U>
+__device__ __forceinline__ void thread_bits(const DropRule &r, const DropKey &key, uint32_t token, int lane, int group,
+                                            uint32_t (&bits)[U][Unit<BF16>::E / 2])
 {
-    constexpr int C = BF16 ? U : U / 2;   // calls for a row
+    constexpr int C = BF16 ? U : U / 2;   // calls
     static_assert(BF16 || U % 2 == 0, "pairs of units");
     const bool odd = lane & 1;
-    uint4 w[R * C];
+    uint4 w[C];
 #pragma unroll
-    for (int j = 0; j < R; ++j)
+    for (int k = 0; k < C; ++k)
+        w[k] = make_uint4(BF16 ? lane + k * group : (lane + (2 * k + odd) * group) >> 1, token, key.step, r.site);
+    philox<C>(key.k0, key.k1, w);
 #pragma unroll
-        for (int k = 0; k < C; ++k)
-            w[j * C + k] = make_uint4(BF16 ? lane + k * group : (lane + (2 * k + odd) * group) >> 1, token[j], key.step, r.site);
-    philox<R * C>(key.k0, key.k1, w);
-#pragma unroll
-    for (int j = 0; j < R; ++j) {
-#pragma unroll
-        for (int k = 0; k < C; ++k) {
-            const uint4 v = w[j * C + k];
-            if constexpr (BF16) {
-                bits[j][k][0] = v.x;
-                bits[j][k][1] = v.y;
-                bits[j][k][2] = v.z;
-                bits[j][k][3] = v.w;
-            } else {
-                const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.z, 1);
-                const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.y : v.w, 1);
-                bits[j][2 * k][0] = odd ? a : v.x;
-                bits[j][2 * k][1] = odd ? b : v.y;
-                bits[j][2 * k + 1][0] = odd ? v.z : a;
-                bits[j][2 * k + 1][1] = odd ? v.w : b;
-            }
+    for (int k = 0; k < C; ++k) {
+        const uint4 v = w[k];
+        if constexpr (BF16) {
+            bits[k][0] = v.x;
+            bits[k][1] = v.y;
+            bits[k][2] = v.z;
+            bits[k][3] = v.w;
+        } else {
+            const uint32_t a = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.x : v.z, 1);
+            const uint32_t b = __shfl_xor_sync(0xFFFFFFFFu, odd ? v.y : v.w, 1);
+            bits[2 * k][0] = odd ? a : v.x;
+            bits[2 * k][1] = odd ? b : v.y;
+            bits[2 * k + 1][0] = odd ? v.z : a;
+            bits[2 * k + 1][1] = odd ? v.w : b;
         }
     }
 }
