@@ -1109,7 +1109,7 @@ cpt_status cpt_kernel_wait_timeouts(uint32_t *count, int32_t reset)
     if (count == nullptr) return fail(CPT_ERR_INVALID_ARG, "NULL argument");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0, u = 0, s = 0;
+    unsigned int v = 0, w = 0, x = 0, y = 0, z = 0, u = 0, s = 0, t = 0;
     cudaError_t e = read_wait_timeouts(&v, reset != 0);
     if (e == cudaSuccess) e = read_slot_reduce_wait_timeouts(&w, reset != 0);
     if (e == cudaSuccess) e = read_gather_wait_timeouts(&x, reset != 0);
@@ -1117,8 +1117,9 @@ cpt_status cpt_kernel_wait_timeouts(uint32_t *count, int32_t reset)
     if (e == cudaSuccess) e = read_attention_wait_timeouts(&z, reset != 0);
     if (e == cudaSuccess) e = read_attention_backward_wait_timeouts(&u, reset != 0);
     if (e == cudaSuccess) e = read_residual_wait_timeouts(&s, reset != 0);
+    if (e == cudaSuccess) e = read_residual_backward_wait_timeouts(&t, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "wait-timeout counter read");
-    *count = v + w + x + y + z + u + s;
+    *count = v + w + x + y + z + u + s + t;
     return CPT_OK;
 }
 
@@ -1139,7 +1140,7 @@ cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset)
         return fail(CPT_ERR_UNSUPPORTED, "this library was built without CPT_CHECK_BOUNDS");
     int dev = 0;
     if (!current_device(&dev)) return fail(CPT_ERR_DEVICE, "no current CUDA device");
-    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0;
+    unsigned int a = 0, b = 0, c = 0, d = 0, f = 0, g = 0, h = 0, i = 0, j = 0;
     cudaError_t e = read_index_map_bounds_violations(&a, reset != 0);
     if (e == cudaSuccess) e = read_gather_bounds_violations(&b, reset != 0);
     if (e == cudaSuccess) e = read_grad_return_bounds_violations(&c, reset != 0);
@@ -1148,8 +1149,9 @@ cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset)
     if (e == cudaSuccess) e = read_attention_backward_bounds_violations(&g, reset != 0);
     if (e == cudaSuccess) e = read_residual_bounds_violations(&h, reset != 0);
     if (e == cudaSuccess) e = read_logprob_bounds_violations(&i, reset != 0);
+    if (e == cudaSuccess) e = read_residual_backward_bounds_violations(&j, reset != 0);
     if (e != cudaSuccess) return cuda_fail(e, "bounds counter read");
-    *count = a + b + c + d + f + g + h + i;
+    *count = a + b + c + d + f + g + h + i + j;
     return CPT_OK;
 }
 

@@ -236,6 +236,7 @@ cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaSt
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device);
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream);
 cudaError_t read_residual_wait_timeouts(unsigned int *count, bool reset);
+cudaError_t read_residual_backward_wait_timeouts(unsigned int *count, bool reset);
 
 // Log-probabilities of targets, and their gradient.
 struct LogprobParams {
@@ -289,6 +290,7 @@ cudaError_t read_grad_return_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_rotary_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_attention_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_residual_bounds_violations(unsigned int *count, bool reset);
+cudaError_t read_residual_backward_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_logprob_bounds_violations(unsigned int *count, bool reset);
 cudaError_t read_attention_backward_bounds_violations(unsigned int *count, bool reset);
 
