@@ -95,7 +95,7 @@ inline int stages_of(const Shape &s, int dtype, int tensors, bool by_document)
 }
 
 // The document of a raw token: the last d with cu[d] <= t.
-__device__ __forceinline__ int document_of(const int32_t *cu, int n, int64_t t)
+__device__ __forceinline__ int document_of(const int32_t *cu, int n, int32_t t)
 {
     int lo = 0, hi = n;   // cu[lo] <= t < cu[hi]
     while (hi - lo > 1) {
@@ -226,8 +226,8 @@ struct SharedWeights {
 // The document that tokens are in, looked for when it changes.
 struct Document {
     int at = 0;
-    int64_t lo = 0, hi = -1;   // its tokens
-    __device__ __forceinline__ bool enter(const ResidualParams &p, int64_t token)
+    int32_t lo = 0, hi = -1;   // its tokens
+    __device__ __forceinline__ bool enter(const ResidualParams &p, int32_t token)
     {
         if (token >= lo && token < hi) return false;
         if (token == hi && at + 1 < p.n_docs && p.cu[at + 2] > token) ++at;   // the next one, mostly
@@ -307,14 +307,15 @@ static __device__ unsigned int g_wait_timeouts;   // of this translation unit
 
 // Runs `work(i, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
 // first barrier, where every thread is done with the row before; `sum` votes there whether a wait has run
-// out. index_of(i) looks the i-th row up (-1: it is not read), row_of(i, index) is its place in this lane's tensor, `base`.
-template <class Sum, class Index, class RowOf, class Work>
-__device__ __forceinline__ void walk(Ring &ring, Sum &sum, int64_t count, int tensors, uint32_t row_bytes, const uint8_t *base,
+// out. (Int: 64 bits forward, where 32 make the compiler's schedule 4 % slower; 32 in the gradient, which is short of
+// registers.) index_of(i) looks the i-th row up (-1: it is not read), row_of(i, index) is its place in this lane's tensor, `base`.
+template <class Int, class Sum, class Index, class RowOf, class Work>
+__device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensors, uint32_t row_bytes, const uint8_t *base,
                                      Index index_of, RowOf row_of, Work work)
 {
     const int lane = sum.team.thread & 31;
     const bool first = sum.team.thread < 32, several = ring.stages > 1;
-    int64_t issued = 0;
+    Int issued = 0;
     int put = 0;
     int32_t ahead = first ? index_of(0) : -1;   // looked up a row early
     auto issue = [&]() {   // by the first warp
@@ -337,7 +338,7 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, int64_t count, int te
     __syncthreads();   // of all teams: what else was put into shared memory is there too
     if (first)
         for (int c = 0; c < ring.stages; ++c) issue();
-    for (int64_t i = 0; i < count; ++i) {
+    for (Int i = 0; i < count; ++i) {
         if (!mbar_wait_bounded(&ring.full[ring.slot], ring.phase)) sum.ask = true;
         work(i, [&]() {
             if (several && first && i > 0) issue();   // into the place of the row before
@@ -350,7 +351,7 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, int64_t count, int te
         if (sum.stop) {   // by all: no copy may end in another CTA's shared memory
             if (first) {
                 if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
-                for (int64_t k = i + 1; k < issued; ++k) {
+                for (Int k = i + 1; k < issued; ++k) {
                     mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
                     ring.advance();
                 }

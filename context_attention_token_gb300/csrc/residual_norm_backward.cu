@@ -141,8 +141,8 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<
 // The sum over a token's gate gradients leaves for where it belongs: the result when the document lies in this
 // group's tokens, part 0 when it began earlier, part 1 when it goes on.
 template <bool BF16, int U>
-__device__ __forceinline__ void leave_document(const ResidualParams &p, const Document &doc, int64_t which, int64_t begin,
-                                               int64_t end, const Has<U> &has, int lane, Sums<BF16, U> &acc)
+__device__ __forceinline__ void leave_document(const ResidualParams &p, const Document &doc, int64_t which, int32_t begin,
+                                               int32_t end, const Has<U> &has, int lane, Sums<BF16, U> &acc)
 {
     constexpr int E = Unit<BF16>::E;
     float *to = reinterpret_cast<float *>(p.dgate) + static_cast<int64_t>(doc.at) * p.row_elems;
@@ -190,7 +190,8 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
     typedef Asked<F> A;
     const int lane = threadIdx.x % p.group, groups = kShortThreads / p.group;
     const int64_t which = static_cast<int64_t>(blockIdx.x) * groups + threadIdx.x / p.group;
-    const int64_t begin = which * p.per_group, end = min(begin + p.per_group, p.T);
+    const int32_t begin = static_cast<int32_t>(min(which * p.per_group, p.T));
+    const int32_t end = static_cast<int32_t>(min(begin + p.per_group, p.T)), count = end - begin;
     const bool need_h = A::post(p) || A::gate(p) != 0;
     DropKey key;
     key.load(p.rule);
@@ -209,13 +210,14 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
     const bool by_document = A::gate(p) == kGateDocument;
     if (by_document && begin < end) doc.enter(p, begin);
 
-    auto load = [&](int64_t t, ShortRaw<U> &r) {
+    auto load = [&](int32_t i, ShortRaw<U> &r) {   // token begin + i, if it is this group's
         r.row = -1;
 #pragma unroll
         for (int j = 0; j < 5; ++j)
 #pragma unroll
             for (int k = 0; k < U; ++k) r.t[j][k] = make_uint4(0, 0, 0, 0);
-        if (t >= end) return;
+        if (i >= count) return;
+        const int32_t t = begin + i;
         const int64_t row = p.row_of_token == nullptr ? t : p.row_of_token[t];
         if (!in_bounds(row >= 0 && row < p.rows, lane == 0)) return;
         r.row = row;
@@ -234,11 +236,11 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
     };
 
     ShortRaw<U> next;
-    load(begin, next);
-    for (int64_t i = 0; i < p.per_group; ++i) {
-        const int64_t t = begin + i;
+    load(0, next);
+    for (int32_t i = 0; i < p.per_group; ++i) {   // as often for every lane of a warp: they share the sums
+        const int32_t t = i < count ? begin + i : 0;
         ShortRaw<U> r = next;
-        if (i + 1 < p.per_group) load(t + 1, next);
+        load(i + 1, next);
         const bool real = r.row >= 0;
         if (by_document && real) {
             if (t >= doc.hi) {
@@ -297,8 +299,10 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
     __shared__ int32_t index[kMaxTeams][kMaxStages];
     const int mine = threadIdx.x / p.group, lane = threadIdx.x - mine * p.group, teams = blockDim.x / p.group;
     const Team team = {lane, p.group, mine + 1};
-    const int64_t which = static_cast<int64_t>(blockIdx.x) * teams + mine;
-    const int64_t begin = which * p.per_group, end = max(min(begin + p.per_group, p.T), begin), count = end - begin;
+    const int32_t which = blockIdx.x * teams + mine;
+    // there are fewer than 2^31 tokens
+    const int32_t begin = static_cast<int32_t>(min(which * p.per_group, p.T));
+    const int32_t end = static_cast<int32_t>(min(begin + p.per_group, p.T)), count = end - begin;
     const bool need_h = A::post(p) || A::gate(p) != 0, pre = A::pre(p), by_document = A::gate(p) == kGateDocument;
     DropKey key;
     key.load(p.rule);
@@ -343,20 +347,21 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
                              A::gate(p) == kGateToken ? p.gate : nullptr})
         if (b != nullptr && left-- == 0) base = b;
 
-    auto index_of = [&](int64_t i) {
-        int64_t row = -1;
+    auto index_of = [&](int32_t i) {
+        int32_t row = -1;
         if (i < count) row = p.row_of_token == nullptr ? begin + i : p.row_of_token[begin + i];
-        return static_cast<int32_t>(row >= 0 && in_bounds(row < p.rows) ? row : -1);
+        return row >= 0 && in_bounds(row < p.rows) ? row : -1;
     };
-    auto row_of = [&](int64_t, int32_t row) { return static_cast<int64_t>(row); };
-    walk(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int64_t i, auto after) {
+    auto row_of = [&](int32_t, int32_t row) { return static_cast<int64_t>(row); };
+    walk(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int32_t i, auto after) {
         const int32_t row = ring.index[ring.slot];
         if (row < 0) {   // an index that a check refused
             sum.stop = team.any(sum.ask);
             after();
             return;
         }
-        const int64_t t = begin + i, at = static_cast<int64_t>(row) * row_bytes + lane * 16;
+        const int32_t t = begin + i;
+        const int64_t at = static_cast<int64_t>(row) * row_bytes + lane * 16;
         const uint4 *data = ring.row() + lane;
         bool waiting = true;
         backward_row<BF16, U, F>(
