@@ -894,7 +894,11 @@ def _logits_shape(plan: Plan, logits, vocab, order, targets, per_token):
     for t, count, what in per_token:
         if t.dtype != torch.float32 or t.numel() < count * T:
             raise ValueError(f"{what} must hold {count * T} float32 values")
-    return (width if vocab is None else vocab), width
+    if vocab is None:
+        return width, width
+    if not 1 <= vocab <= width:     # before ctypes cuts it to 64 bits
+        raise ValueError(f"vocab {vocab} outside 1..{width}")
+    return vocab, width
 
 
 def cpt_token_logprob(plan: Plan, logits: torch.Tensor, targets: torch.Tensor, logp: torch.Tensor,

@@ -72,6 +72,10 @@ def test_binding_refuses_losses(cpt):
         lambda: cpt.cpt_token_logprob(plan, x, t, f, f, stream=0),
         lambda: cpt.cpt_token_logprob(plan, x, t, f.bfloat16(), two, stream=0),
         lambda: cpt.cpt_token_logprob(plan, x, t, f, two, order=5, stream=0),
+        lambda: cpt.cpt_token_logprob(plan, x, t, f, two, vocab=17, stream=0),
+        lambda: cpt.cpt_token_logprob(plan, x, t, f, two, vocab=0, stream=0),
+        lambda: cpt.cpt_token_logprob(plan, x, t, f, two, vocab=2 ** 64 + 5, stream=0),
+        lambda: cpt.cpt_token_logprob_backward(plan, x, t, two, f, x, vocab=5 - 2 ** 64, stream=0),
         lambda: cpt.cpt_token_logprob_backward(plan, x, t, two, f, x.bfloat16(), stream=0),
         lambda: cpt.cpt_token_logprob_backward(plan, x, t, two, f, x[:1], stream=0),
         lambda: cpt.cpt_policy_loss(plan, f[:15], f, one, four, f, stream=0),
