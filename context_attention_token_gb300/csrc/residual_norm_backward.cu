@@ -12,7 +12,8 @@ namespace cpt {
 
 namespace {
 
-// What a thread adds up over its tokens.
+// What a thread adds up over its tokens. With a gate that a document shares, gate holds sum d hn over the document's tokens so far:
+// w1 times it is dgate, and gate times it the document's part of dw1. So one product a column and token does for both.
 template <bool BF16, int U>
 struct Sums {
     F2 post[U][Unit<BF16>::E / 2], pre[U][Unit<BF16>::E / 2], gate[U][Unit<BF16>::E / 2];
@@ -90,32 +91,34 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<
                 for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1));
             }
         }
+        const bool by_document = A::gate(p) == kGateDocument;
         if (A::gate(p) != 0) {
-            F2 g[N], z[N];
+            F2 g[N];
             V::unpack(gate(k), g);
-            // what was dropped has no gradient, whatever it is multiplied by (behind a norm, and with a gate that a whole
-            // document shares, a row with an infinity is NaN throughout)
-            const bool guard = A::drop(p) && !(post && A::gate(p) == kGateDocument);
+            if (by_document) {   // its weights come in when the document is left
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
-                d[i] = mul2(d[i], g[i]);
-            }
-            if (guard) {
-                keep_or_zero<N>(p.rule, rnd[k], z);
-                keep_or_zero<N>(p.rule, rnd[k], d);
-            }
-            if (A::gate(p) == kGateDocument) {
-#pragma unroll
-                for (int i = 0; i < N; ++i) acc.gate[k][i] = add2(acc.gate[k][i], z[i]);
+                for (int i = 0; i < N; ++i) {
+                    acc.gate[k][i] = fma2(d[i], hn[i], acc.gate[k][i]);
+                    d[i] = mul2(d[i], g[i]);
+                }
             } else {
+                F2 z[N];
+#pragma unroll
+                for (int i = 0; i < N; ++i) {
+                    z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
+                    d[i] = mul2(d[i], g[i]);
+                }
+                if (A::drop(p)) {   // what was dropped has no gradient, whatever it is multiplied by
+                    keep_or_zero<N>(p.rule, rnd[k], z);
+                    keep_or_zero<N>(p.rule, rnd[k], d);
+                }
                 put_gate(k, has.at[k], V::pack(z));
             }
         }
         if (post) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
+                if (!by_document) acc.post[k][i] = fma2(d[i], hn[i], acc.post[k][i]);
                 e[k][i] = mul2(d[i], w[i]);
                 t = fma2(e[k][i], hn[i], t);
             }
@@ -138,11 +141,11 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<
     }
 }
 
-// The sum over a token's gate gradients leaves for where it belongs: the result when the document lies in this
-// group's tokens, part 0 when it began earlier, part 1 when it goes on.
-template <bool BF16, int U>
+// The sums over a document's tokens leave: dgate for where it belongs (the result when the document lies in this group's
+// tokens, part 0 when it began earlier, part 1 when it goes on), the document's part of dw1 to the others'.
+template <bool BF16, int U, int F, class W1>
 __device__ __forceinline__ void leave_document(const ResidualParams &p, const Document &doc, int64_t which, int32_t begin,
-                                               int32_t end, const Has<U> &has, int lane, Sums<BF16, U> &acc)
+                                               int32_t end, const Has<U> &has, int lane, W1 w1, Sums<BF16, U> &acc)
 {
     constexpr int E = Unit<BF16>::E;
     float *to = reinterpret_cast<float *>(p.dgate) + static_cast<int64_t>(doc.at) * p.row_elems;
@@ -150,14 +153,26 @@ __device__ __forceinline__ void leave_document(const ResidualParams &p, const Do
     else if (doc.hi > end) to = p.part_gate + (which * 2 + 1) * p.row_elems;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        float f[E];
+        F2 z[E / 2];
 #pragma unroll
         for (int i = 0; i < E / 2; ++i) {
-            const float2 v = both(acc.gate[k][i]);
-            f[2 * i] = v.x;
-            f[2 * i + 1] = v.y;
+            z[i] = acc.gate[k][i];
             acc.gate[k][i] = twice(0.0f);
         }
+        if (Asked<F>::post(p)) {
+            F2 w[E / 2], g[E / 2];
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (has.at[k]) raw = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
+            UnitPairs<BF16>::unpack(raw, g);
+            w1(k, w);
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                acc.post[k][i] = fma2(z[i], g[i], acc.post[k][i]);
+                z[i] = mul2(z[i], w[i]);
+            }
+        }
+        float f[E];
+        spread<E>(z, f);
         if (has.at[k]) store_floats<E>(to + static_cast<int64_t>(lane + k * p.group) * E, f);
     }
 }
@@ -244,7 +259,7 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
         const bool real = r.row >= 0;
         if (by_document && real) {
             if (t >= doc.hi) {
-                leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
+                leave_document<BF16, U, F>(p, doc, which, begin, end, has, lane, HeldWeights<BF16, U>{w1}, acc);
                 doc.enter(p, t);
             }
 #pragma unroll
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.n, at + k * p.group, v); },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.dgate, at + k * p.group, v); });
     }
-    if (by_document && begin < end) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
+    if (by_document && begin < end) leave_document<BF16, U, F>(p, doc, which, begin, end, has, lane, HeldWeights<BF16, U>{w1}, acc);
 
     // the CTA's part of the weights' gradients, its groups added in order
     __shared__ float join[kShortThreads * U * E];
@@ -370,7 +385,7 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
             [&](int k) { return data[at_h + k * p.group]; },
             [&]() {
                 if (t < doc.hi) return;
-                if (doc.hi >= 0) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
+                if (doc.hi >= 0) leave_document<BF16, U, F>(p, doc, which, begin, end, has, lane, w1, acc);
                 doc.enter(p, t);
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
@@ -394,7 +409,7 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
             after();
         }
     });
-    if (by_document && doc.hi >= 0) leave_document<BF16, U>(p, doc, which, begin, end, has, lane, acc);
+    if (by_document && doc.hi >= 0) leave_document<BF16, U, F>(p, doc, which, begin, end, has, lane, w1, acc);
     // the CTA's part of the weights' gradients, its teams added in order; a team's ring has room for a row of sums (a
     // norm's gradient reads two tensors at least)
 #pragma unroll
@@ -419,14 +434,29 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
     zero_padding<U>(p, has, lane, mine, teams);
 }
 
-// Adds the parts: blockIdx.y 0 and 1 the weights', one warp every 32nd part; the others the documents that
-// reach over several groups, a warp each. 32 columns a block.
+// The sum of v over the block's 32 warps, of column `warp` in every lane.
+__device__ __forceinline__ float across_warps(float (*room)[33], float v)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __syncthreads();
+    room[warp][lane] = v;
+    __syncthreads();
+    v = room[lane][warp];
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+constexpr int kWideDocument = 8;   // groups beyond its first that a warp still adds alone
+
+// Adds the parts, in a fixed order, 32 columns a block: blockIdx.y 0 and 1 the weights', a warp every 32nd part; the
+// others the documents that reach over several groups.
 __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_constant__ ResidualParams p)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + lane;
+    __shared__ float room[32][33];
     if (blockIdx.y < 2) {
-        __shared__ float room[32][33];
         const float *from = blockIdx.y == 0 ? p.part_post : p.part_pre;
         float *to = blockIdx.y == 0 ? p.dpost : p.dpre;
         if (to == nullptr) return;
@@ -435,29 +465,46 @@ __global__ void __launch_bounds__(1024) residual_join_kernel(const __grid_consta
 #pragma unroll 8
             for (int i = warp; i < p.parts; i += 32) v = __fadd_rn(v, from[static_cast<int64_t>(i) * p.row_elems + c]);
         }
-        room[warp][lane] = v;
-        __syncthreads();
-        v = room[lane][warp];   // this warp's column warp, part lane
-#pragma unroll
-        for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+        v = across_warps(room, v);
         if (lane == 0 && blockIdx.x * 32 + warp < p.row_elems) to[blockIdx.x * 32 + warp] = v;
         return;
     }
-    if (c >= p.row_elems) return;
+    // a warp a document, but for those that reach over many groups: these all warps share out
+    __shared__ int32_t wide[32];
     float *dgate = reinterpret_cast<float *>(p.dgate);
-    const int64_t step = static_cast<int64_t>(gridDim.y - 2) * 32;
-    for (int64_t d = (blockIdx.y - 2) * 32 + warp; d < p.n_docs; d += step) {
-        const int64_t lo = p.cu[d], hi = p.cu[d + 1];
-        if (lo >= hi) {
-            dgate[d * p.row_elems + c] = 0.0f;
-            continue;
+    const bool there = c < p.row_elems;
+    for (int64_t d0 = (blockIdx.y - 2) * 32; d0 < p.n_docs; d0 += static_cast<int64_t>(gridDim.y - 2) * 32) {
+        const int64_t d = d0 + warp;
+        int64_t first = 0, last = 0;
+        bool empty = false;
+        if (d < p.n_docs) {
+            const int64_t lo = p.cu[d], hi = p.cu[d + 1];
+            empty = lo >= hi;
+            first = lo / p.per_group;
+            last = empty ? first : (hi - 1) / p.per_group;
         }
-        const int64_t first = lo / p.per_group, last = (hi - 1) / p.per_group;
-        if (first == last) continue;
-        float v = p.part_gate[(first * 2 + 1) * p.row_elems + c];
+        if (lane == 0) wide[warp] = last - first > kWideDocument;
+        if (empty && there) dgate[d * p.row_elems + c] = 0.0f;
+        if (last > first && last - first <= kWideDocument && there) {
+            float v = p.part_gate[(first * 2 + 1) * p.row_elems + c];
 #pragma unroll 8
-        for (int64_t g = first + 1; g <= last; ++g) v = __fadd_rn(v, p.part_gate[g * 2 * p.row_elems + c]);
-        dgate[d * p.row_elems + c] = v;
+            for (int64_t g = first + 1; g <= last; ++g) v = __fadd_rn(v, p.part_gate[g * 2 * p.row_elems + c]);
+            dgate[d * p.row_elems + c] = v;
+        }
+        __syncthreads();
+        for (int w = 0; w < 32; ++w) {
+            if (!wide[w]) continue;
+            const int64_t from = p.cu[d0 + w] / p.per_group, to = (p.cu[d0 + w + 1] - 1) / p.per_group;
+            float v = 0.0f;
+            if (there) {
+                if (warp == 0) v = p.part_gate[(from * 2 + 1) * p.row_elems + c];
+#pragma unroll 8
+                for (int64_t g = from + 1 + warp; g <= to; g += 32) v = __fadd_rn(v, p.part_gate[g * 2 * p.row_elems + c]);
+            }
+            v = across_warps(room, v);
+            if (lane == 0 && blockIdx.x * 32 + warp < p.row_elems) dgate[(d0 + w) * p.row_elems + blockIdx.x * 32 + warp] = v;
+        }
+        __syncthreads();
     }
 }
 
