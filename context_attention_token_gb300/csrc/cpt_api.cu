@@ -16,6 +16,7 @@
 #include <cuda.h>
 #include <nvtx3/nvToolsExt.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -26,6 +27,8 @@
 #include <vector>
 
 namespace {
+
+std::atomic<uint32_t> g_ring_stall{0};   // cpt_test_stall_bulk_waits
 
 using namespace cpt;
 
@@ -1100,6 +1103,7 @@ cpt_status cpt_test_stall_bulk_waits(int32_t on)
     if (e == cudaSuccess) e = set_stall_slot_reduce(extra);
     if (e == cudaSuccess) e = set_stall_gather(extra);
     if (e != cudaSuccess) return cuda_fail(e, "stall switch");
+    g_ring_stall = extra;
     return CPT_OK;
 }
 
@@ -1609,6 +1613,7 @@ void fill_residual(ResidualParams &p, const cpt_plan *plan, int64_t row_elems, c
     p.gate_kind = o->gate_kind;
     p.scale = o->scale;
     p.eps = o->eps;
+    p.stall = g_ring_stall.load();
 }
 
 size_t gate_bytes(const cpt_plan *plan, const cpt_residual *o, size_t row_tensor, size_t row_bytes)

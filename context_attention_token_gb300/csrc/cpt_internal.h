@@ -231,6 +231,7 @@ struct ResidualParams {
     int32_t tensors, stages;           // of a ring: tensors that are read, chunks of rows
     float per_column;                  // 1 / row_elems
     bool hold;                         // the gradient's weights stand in shared memory
+    uint32_t stall;                    // bytes that a ring's copies announce and do not deliver (0 but in a test)
 };
 cudaError_t launch_residual_norm(ResidualParams p, int dtype, int device, cudaStream_t stream);
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device);

@@ -1,7 +1,7 @@
 // The residual stream between two blocks, forward: y = x + scale drop(norm(h) gate), n = norm(y). Mathematics, layout and
 // reasons: residual_norm.cuh.
 //
-// 262144 x 2560 bf16 with both norms and dropout takes 864 us (6.21 TB/s, 0.92 of a copy). What bounds it: HBM, with issue slots near.
+// 262144 x 2560 bf16 with both norms and dropout takes 869 us (6.18 TB/s, 0.91 of a copy). What bounds it: HBM, with issue slots half busy.
 #include "residual_norm.cuh"
 
 namespace cpt {
@@ -34,7 +34,7 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const Has<U
     if (A::drop(p)) bits(rnd);
     if (A::post(p)) {
         s[0] = sum_of(q);
-        sum(s);
+        if (sum(s)) return;
         factor = twice(__fmul_rn(rsqrt_mean(p, s[0]), p.rule.factor));
     }
     q = twice(0.0f);
@@ -68,7 +68,7 @@ __device__ __forceinline__ void forward_row(const ResidualParams &p, const Has<U
     }
     if (!A::pre(p)) return;
     s[0] = sum_of(q);
-    sum(s);
+    if (sum(s)) return;
     const F2 r2 = twice(rsqrt_mean(p, s[0]));
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -134,7 +134,10 @@ __global__ void __launch_bounds__(kShortThreads) residual_norm_short_kernel(cons
             p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, [&](int k) { return r.t[0][k]; },
             [&](int k) { return r.t[1][k]; }, [&](int k) { return r.t[2][k]; },
             [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(r.token), lane, bits); },
-            [&](float(&v)[1]) { lanes_sum<1>(v, p.group); },
+            [&](float(&v)[1]) {
+                lanes_sum<1>(v, p.group);
+                return false;
+            },
             [&](int k, bool there, uint4 v) { store_unit_if(in && there, p.y, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); },
             [&](int k, bool there, uint4 v) { store_unit_if(in && there, p.n, at + k * p.group, real ? v : make_uint4(0, 0, 0, 0)); });
     }
@@ -179,8 +182,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     const int tensor = lane & 31;
     const uint8_t *base = tensor == 0 ? p.x : tensor == 1 && A::block(p.h != nullptr) ? p.h : p.gate;
     uint8_t *y = p.y, *n = p.n;
-    walk(ring, sum, count, p.tensors, row_bytes, base, token_of, row_of, [&](int64_t i, auto after) {
-        const int32_t token = ring.index[ring.slot];
+    walk(ring, sum, count, p.tensors, row_bytes, p.stall, base, token_of, row_of, [&](int64_t i, int32_t token, auto after) {
         const bool real = token >= 0;
         const uint4 *data = ring.row() + lane;
         const int64_t at = (begin + i) * row_bytes + lane * 16;   // of this thread's first unit, in bytes
@@ -194,7 +196,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
                     gate[k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
             }
         }
-        if (!real) {
+        if (token == -1) {   // padding
 #pragma unroll
             for (int k = 0; k < U; ++k) {
                 store_unit_if(has.at[k] && y != nullptr, y + at, k * p.group, make_uint4(0, 0, 0, 0));
@@ -210,6 +212,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
                 sum(v);
                 if (waiting) after();
                 waiting = false;
+                return sum.stop;
             },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, y + at, k * p.group, v); },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, n + at, k * p.group, v); });

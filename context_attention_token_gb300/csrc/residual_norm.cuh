@@ -17,7 +17,8 @@
 // Longer ones take a team of a few warps with a barrier of its own; its rows come through a ring in shared memory,
 // filled by the bulk-copy engine, and the weights stand there once for all teams of the SM's only CTA. Measured for 262144 x 2560
 // bf16 with both norms and dropout: CTAs of 320 threads that load into registers 2543 us, a ring for each 1336, a CTA's weights
-// from the cache and two rows at a time 1069, teams of 64 threads with 40 columns each 907, stores under predicates 864.
+// from the cache and two rows at a time 1069, teams of 64 threads with 40 columns each 907, stores under predicates 864
+// (869 since a row that could not be waited for is not stored).
 #pragma once
 
 #include "cpt_internal.h"
@@ -305,13 +306,15 @@ struct Ring {
 
 static __device__ unsigned int g_wait_timeouts;   // of this translation unit
 
-// Runs `work(i, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
+constexpr int32_t kUnknown = -2;   // a row's index for a thread whose wait has run out: it uses and stores nothing of the row
+
+// Runs `work(i, index, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
 // first barrier, where every thread is done with the row before; `sum` votes there whether a wait has run
-// out. (Int: 64 bits forward, where 32 make the compiler's schedule 4 % slower; 32 in the gradient, which is short of
+// out, and then nothing that depends on other threads' data may be stored. (Int: 64 bits forward, where 32 make the compiler's schedule 4 % slower; 32 in the gradient, which is short of
 // registers.) index_of(i) looks the i-th row up (-1: it is not read), row_of(i, index) is its place in this lane's tensor, `base`.
 template <class Int, class Sum, class Index, class RowOf, class Work>
-__device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensors, uint32_t row_bytes, const uint8_t *base,
-                                     Index index_of, RowOf row_of, Work work)
+__device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensors, uint32_t row_bytes, uint32_t stall,
+                                     const uint8_t *base, Index index_of, RowOf row_of, Work work)
 {
     const int lane = sum.team.thread & 31;
     const bool first = sum.team.thread < 32, several = ring.stages > 1;
@@ -323,7 +326,7 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensor
         uint64_t *bar = &ring.full[put];
         if (lane == 0) {
             ring.index[put] = ahead;
-            mbar_expect_tx(bar, ahead >= 0 ? static_cast<uint32_t>(tensors) * row_bytes : 0);
+            mbar_expect_tx(bar, ahead >= 0 ? static_cast<uint32_t>(tensors) * row_bytes + stall : 0);
         }
         __syncwarp();
         if (lane < tensors && ahead >= 0)
@@ -339,11 +342,11 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensor
     if (first)
         for (int c = 0; c < ring.stages; ++c) issue();
     for (Int i = 0; i < count; ++i) {
-        if (!mbar_wait_bounded(&ring.full[ring.slot], ring.phase)) sum.ask = true;
-        work(i, [&]() {
+        const bool come = mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+        if (!come) sum.ask = true;
+        work(i, come ? ring.index[ring.slot] : kUnknown, [&]() {
             if (several && first && i > 0) issue();   // into the place of the row before
         });
-        ring.advance();
         if (!several) {
             sum.stop = sum.team.any(sum.ask);
             if (first && !sum.stop) issue();
@@ -351,13 +354,12 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensor
         if (sum.stop) {   // by all: no copy may end in another CTA's shared memory
             if (first) {
                 if (lane == 0) atomicAdd(&g_wait_timeouts, 1u);
-                for (Int k = i + 1; k < issued; ++k) {
-                    mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
-                    ring.advance();
-                }
+                // (one wait that runs out here has given every copy in flight its second)
+                for (Int k = i; k < issued && mbar_wait_bounded(&ring.full[ring.slot], ring.phase); ++k) ring.advance();
             }
             return;
         }
+        ring.advance();
     }
 }
 

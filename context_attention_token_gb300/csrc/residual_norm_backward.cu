@@ -4,8 +4,8 @@
 // registers (which is why a thread of long rows has 16 columns here and up to 40 forward); parts meet in the workspace
 // and are added in a fixed order.
 //
-// 131071 x 2560 bf16 with both norms, a document's gate and dropout takes 921 us (4.4 TB/s, 0.64 of a copy): some 58
-// instructions a column at 15 warps an SM bound it. 20011 x 1132 float32 with a token's gate takes 132 us (5.5 TB/s).
+// 131071 x 2560 bf16 with both norms, a document's gate and dropout takes 948 us (4.2 TB/s, 0.63 of a copy): some 58
+// instructions a column at 15 warps an SM bound it. 20011 x 1132 float32 with a token's gate takes 140 us (5.2 TB/s).
 #include "residual_norm.cuh"
 
 namespace cpt {
@@ -56,7 +56,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<
     // the generator needs no data: it runs while the sums are on their way
     if (A::drop(p)) bits(rnd);
     float s[3] = {sum_of(q[0]), sum_of(q[1]), sum_of(q[2])};
-    if (pre || post) sum(s);
+    if ((pre || post) && sum(s)) return;
     if (A::gate(p) == kGateDocument) enter();
     const float r2 = pre ? rsqrt_mean(p, s[0]) : 0.0f, r1 = post ? rsqrt_mean(p, s[2]) : 1.0f;
     // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
@@ -272,7 +272,10 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
             [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; }, []() {},
             [&](int k) { return r.t[4][k]; },
             [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits); },
-            [&](auto &v) { lanes_sum(v, p.group); },
+            [&](auto &v) {
+                lanes_sum(v, p.group);
+                return false;
+            },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.y, at + k * p.group, v); },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.n, at + k * p.group, v); },
             [&](int k, bool there, uint4 v) { store_unit_if(real && there, p.dgate, at + k * p.group, v); });
@@ -368,9 +371,8 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         return row >= 0 && in_bounds(row < p.rows) ? row : -1;
     };
     auto row_of = [&](int32_t, int32_t row) { return static_cast<int64_t>(row); };
-    walk(ring, sum, count, p.tensors, row_bytes, base, index_of, row_of, [&](int32_t i, auto after) {
-        const int32_t row = ring.index[ring.slot];
-        if (row < 0) {   // an index that a check refused
+    walk(ring, sum, count, p.tensors, row_bytes, p.stall, base, index_of, row_of, [&](int32_t i, int32_t row, auto after) {
+        if (row < 0) {   // an index that a check refused, or a wait that has run out
             sum.stop = team.any(sum.ask);
             after();
             return;
@@ -400,6 +402,7 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
                 sum(v);
                 if (waiting) after();
                 waiting = false;
+                return sum.stop;
             },
             [&](int k, bool there, uint4 v) { store_unit_if(there, p.y + at, k * p.group, v); },
             [&](int k, bool there, uint4 v) { store_unit_if(there, p.n + at, k * p.group, v); },

@@ -595,10 +595,12 @@ CPT_API cpt_status cpt_epoch_status(const cpt_epoch *ep, int32_t owner, void *st
  * report). The bulk-copy kernels of the row gather, the gradient return and
  * the slot reduce move data through shared memory, each copy completing on
  * an mbarrier; the attention kernels hand tiles from warp to warp on such
- * barriers too. Every wait on one gives up after about a second or 2^24 polls
+ * barriers too, and the residual norms fetch long rows on them. Every wait on one gives up after about a second or 2^24 polls
  * (one wait of the attention kernel after more, with more than 2^25 tokens).
  * A wait that gives up is counted here, its warp (in the attention kernels its
- * CTA) stops, and the outputs it had not reached are left unwritten. A non-zero
+ * CTA, in the residual norms the threads that share its rows) stops, and the
+ * outputs it had not reached are left unwritten (a sum over tokens lacks
+ * theirs). A non-zero
  * count means some output of an earlier call is not valid.
  *  count  host, receives the count.
  *  reset  non-zero: set the count back to zero after reading it.
@@ -629,7 +631,8 @@ CPT_API int32_t cpt_bounds_checked(void);
 CPT_API cpt_status cpt_bounds_violations(uint32_t *count, int32_t reset);
 
 /* Test switch for the failure path of the bulk-copy kernels of the row gather,
- * the gradient return and the slot reduce (the pages have no
+ * the gradient return, the slot reduce and the residual norms (those: of calls
+ * made while it is on, on any device; the pages have no
  * counterpart). While on, every bulk-copy mbarrier of later launches on the
  * current device announces 16 bytes more than its copies deliver. Every
  * copy still completes, and nothing faults, but each wait runs out of its
