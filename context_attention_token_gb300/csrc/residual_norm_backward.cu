@@ -537,13 +537,21 @@ cudaError_t launch_backward(const ResidualParams &p, const Shape &s, int f, unsi
 
 int64_t residual_backward_workspace(int64_t T, int64_t row_elems, int dtype, int device)
 {
-    // enough for any options: those that read and ask for least have the most CTAs
-    const Shape s = shape_of(row_units(row_elems, dtype), dtype, true, 1);
-    const int64_t groups = s.threads / s.group;
-    int64_t most = static_cast<int64_t>(sm_count(device)) * s.ctas_per_sm * groups;
-    if (most > T) most = T;
-    const int64_t ctas = (most + groups - 1) / groups;
-    return (2 * ctas + 2 * ctas * groups) * row_elems * 4;
+    // enough for any options, so the largest of the shapes that a call can have: more tensors leave room for fewer teams, but
+    // for fewer weights too, so neither end is the largest by itself. (A document's gate is read outside the ring: four tensors.)
+    int64_t most = 0;
+    for (int tensors = 1; tensors <= 5; ++tensors) {
+        for (const bool by_document : {false, true}) {
+            if (by_document && tensors == 5) continue;
+            // (f: the most CTAs an SM)
+            const Shape s = shape_of(row_units(row_elems, dtype), dtype, true, tensors, by_document, 2);
+            int64_t per_group, ctas;
+            deal(T, s, device, per_group, ctas);
+            const int64_t rows = 2 * ctas + (by_document ? 2 * ctas * (s.threads / s.group) : 0);
+            if (rows > most) most = rows;
+        }
+    }
+    return most * row_elems * 4;
 }
 
 cudaError_t launch_residual_norm_backward(ResidualParams p, int dtype, void *workspace, int device, cudaStream_t stream)
