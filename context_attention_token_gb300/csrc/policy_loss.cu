@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
     const int rank = S == 1 ? 0 : static_cast<int>(blockIdx.x % S), lane = threadIdx.x & 31;
     const int64_t first = static_cast<int64_t>(blockIdx.x / S) * p.docs;
     const int64_t last = min(first + p.docs, static_cast<int64_t>(p.n_docs));
+    if constexpr (S > 1) cluster_begun();
 
     for (int64_t d = first + rank * (kThreads / 32) + (threadIdx.x >> 5); d < last; d += S * (kThreads / 32)) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
     }
 
     int turn = 0;
+    if constexpr (S > 1) cluster_wait_begun();
     for (int64_t d = first; d < last; ++d) {
         const int64_t lo = p.cu[d], hi = p.cu[d + 1];
         if (hi - lo <= kWarpTokens) continue;

@@ -198,6 +198,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logprob_kernel(const __grid
         if (threadIdx.x == 0 && part == 0) put_none(p, t);
         return;
     }
+    if (p.split > 1) cluster_begun();
     const uint4 *from = reinterpret_cast<const uint4 *>(p.logits) + row * p.units;
     float wanted = 0.0f;
     if (threadIdx.x == 0 && part == 0) wanted = logit<BF16>(from, target);
@@ -212,6 +213,7 @@ __global__ void __launch_bounds__(kRowThreads) token_logprob_kernel(const __grid
     if (p.split > 1) {
         namespace cg = cooperative_groups;
         cg::cluster_group cluster = cg::this_cluster();
+        cluster_wait_begun();
         if (threadIdx.x == 0) *cluster.map_shared_rank(&parts[part], 0) = sum;
         cluster.sync();
         if (part != 0) return;

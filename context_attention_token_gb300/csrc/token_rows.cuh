@@ -212,6 +212,11 @@ struct Team {
     }
 };
 
+// Shared memory of another CTA of the cluster may be written once that CTA has begun: every thread arrives at its own start
+// and waits for all before the first such write, with its loads in between.
+__device__ __forceinline__ void cluster_begun() { asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait_begun() { asm volatile("barrier.cluster.wait;" ::: "memory"); }
+
 // Sums over a team, in a fixed order. There are two places for the warps' sums; one is written again only after every
 // thread has passed the barrier of the other, so one barrier a sum is enough.
 template <int TURN>   // floats of a place: 1, 2, 4 or 8 for a warp's 1, 2, up to 4 or up to 8 values
