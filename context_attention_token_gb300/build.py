@@ -24,7 +24,7 @@ INCLUDE = os.path.join(ROOT, "include")
 SOURCES = ["cpt_api.cu", "index_map.cu", "gather.cu", "grad_return.cu", "slot_reduce.cu", "ceiling.cu",
            "rotary.cu", "attention.cu", "attention_backward.cu", "dropout.cu", "residual_norm.cu",
            "residual_norm_backward.cu", "token_logprob.cu", "policy_loss.cu"]
-HEADERS = ["cpt_internal.h", "cpt_device.cuh", "attention_common.cuh", "tcgen05.cuh", "token_rows.cuh",
+HEADERS = ["cpt_internal.h", "cpt_device.cuh", "attention_common.cuh", "pairs.cuh", "tcgen05.cuh", "token_rows.cuh",
            "residual_norm.cuh"]
 
 # The two builds of the library: the product, and the same sources with

@@ -12,6 +12,7 @@
 #include <cuda.h>
 
 #include "cpt_device.cuh"
+#include "pairs.cuh"
 
 namespace cpt {
 

@@ -4,6 +4,7 @@
 
 #include "cpt_device.cuh"
 #include "cpt_internal.h"
+#include "pairs.cuh"
 
 namespace cpt {
 
