@@ -164,6 +164,16 @@ def test_widest_float32_rows(cpt, cuda_device, units):
     c.check_backward(c.backward())
 
 
+# beyond 1920 units the rows and the weights no longer fit beside each other; several rows for every team
+@pytest.mark.parametrize("units", [1025, 1920, 1921, 2048])
+@pytest.mark.parametrize("gate,p", [(1, 0.0), (1, 0.2), (2, 0.0)])
+def test_widest_float32_rows_of_every_gate(cpt, cuda_device, units, gate, p):
+    b = Batch(cpt, 3, 2, [330, 141, 7], 1)
+    c = Case(cpt, b, units * 4, F32, gate=gate, p=p, seed=units)
+    c.check_forward(*c.forward())
+    c.check_backward(c.backward())
+
+
 # many groups, documents inside one, over two, over many, ending at their borders
 @pytest.mark.parametrize("kind,P,lens", [
     (1, 1, [20000]), (3, 4, [3000] * 5 + [1] * 500 + [0] * 40 + [9999]), (0, 2, [4] * 4000 + [4000]), (1, 8, [8] * 5000),
