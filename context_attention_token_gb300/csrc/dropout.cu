@@ -6,7 +6,8 @@
 // 16-byte unit of bf16.
 //
 // HBM bounds it: every row is read and written once. A CTA takes a tile of neighbouring units, four of every
-// thread in flight.
+// thread in flight. 131071 x 2048 bf16 (padded) takes 172 us, 6.25 TB/s, 0.92 of a copy; with a loop over the grid 181, with a
+// key schedule for every unit 195.
 #include "cpt_internal.h"
 #include "token_rows.cuh"
 

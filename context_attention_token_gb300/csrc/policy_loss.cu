@@ -10,6 +10,7 @@
 //
 // The gradient's weight needs the number of tokens that count. So the gradients wait for it in registers (in dlogp, where a
 // thread has more than kTokens), and a document's sums stay within a warp, a CTA or a cluster, so that one launch does.
+// Latency bounds it: 512 tokens take 9 us, most of it the call's, 262139 tokens 10.7, where the bytes would take 0.5.
 #include "cpt_internal.h"
 #include "token_rows.cuh"
 
