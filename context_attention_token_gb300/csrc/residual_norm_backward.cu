@@ -20,11 +20,12 @@ struct Sums {
 };
 
 // One token of the gradient; dy to gate give the data of a unit of its row (0 past the row's end). `enter` is called before
-// the gate is asked for.
+// the gate is asked for. Where `real` is false there is no token: its data are zeros, and it adds nothing to any sum (a
+// statistic of zeros, which is infinite without an eps, is not used).
 template <bool BF16, int U, int F, class W1, class W2, class DY, class DN, class Y, class H, class Enter, class G, class Bits,
           class Sum, class PutX, class PutH, class PutG>
-__device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<U> &has, W1 w1, W2 w2, Sums<BF16, U> &acc,
-                                             DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum, PutX put_x,
+__device__ __forceinline__ void backward_row(const ResidualParams &p, bool real, const Has<U> &has, W1 w1, W2 w2,
+                                             Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum, PutX put_x,
                                              PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
@@ -58,7 +59,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, const Has<
     float s[3] = {sum_of(q[0]), sum_of(q[1]), sum_of(q[2])};
     if ((pre || post) && sum(s)) return;
     if (A::gate(p) == kGateDocument) enter();
-    const float r2 = pre ? rsqrt_mean(p, s[0]) : 0.0f, r1 = post ? rsqrt_mean(p, s[2]) : 1.0f;
+    const float r2 = pre && real ? rsqrt_mean(p, s[0]) : 0.0f, r1 = !post ? 1.0f : real ? rsqrt_mean(p, s[2]) : 0.0f;
     // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
     const F2 back2 = twice(pre ? -__fmul_rn(__fmul_rn(r2, r2), __fmul_rn(__fmul_rn(s[1], r2), p.per_column)) : 0.0f);
     F2 e[U][N], t = twice(0.0f);
@@ -268,7 +269,7 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
         }
         const int64_t at = r.row * p.units + lane;
         backward_row<BF16, U, F>(
-            p, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; }, [&](int k) { return r.t[1][k]; },
+            p, real, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; }, [&](int k) { return r.t[1][k]; },
             [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; }, []() {},
             [&](int k) { return r.t[4][k]; },
             [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits); },
@@ -382,7 +383,7 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         const uint4 *data = ring.row() + lane;
         bool waiting = true;
         backward_row<BF16, U, F>(
-            p, has, w1, w2, acc, [&](int k) { return p.x != nullptr ? data[k * p.group] : make_uint4(0, 0, 0, 0); },
+            p, true, has, w1, w2, acc, [&](int k) { return p.x != nullptr ? data[k * p.group] : make_uint4(0, 0, 0, 0); },
             [&](int k) { return data[at_dn + k * p.group]; }, [&](int k) { return data[at_y + k * p.group]; },
             [&](int k) { return data[at_h + k * p.group]; },
             [&]() {
