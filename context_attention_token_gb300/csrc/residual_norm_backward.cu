@@ -8,6 +8,8 @@
 // instructions a column at 15 warps an SM bound it. 20011 x 1132 float32 with a token's gate takes 139 us (5.2 TB/s).
 #include "residual_norm.cuh"
 
+#include <math_constants.h>
+
 namespace cpt {
 
 namespace {
@@ -91,6 +93,9 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
 #pragma unroll
                 for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1));
             }
+            // What was dropped has no gradient and adds nothing to a sum, whatever it is multiplied by. (A row whose squares have a
+            // finite sum holds nothing that 0 would not take.)
+            if (A::drop(p) && (!post || !(s[2] < CUDART_INF_F))) keep_or_zero<N>(p.rule, rnd[k], hn);
         }
         const bool by_document = A::gate(p) == kGateDocument;
         if (A::gate(p) != 0) {
@@ -102,6 +107,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
                     acc.gate[k][i] = fma2(d[i], hn[i], acc.gate[k][i]);
                     d[i] = mul2(d[i], g[i]);
                 }
+                if (A::drop(p)) keep_or_zero<N>(p.rule, rnd[k], d);
             } else {
                 F2 z[N];
 #pragma unroll
@@ -109,7 +115,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
                     z[i] = mul2(d[i], post ? mul2(hn[i], w[i]) : hn[i]);
                     d[i] = mul2(d[i], g[i]);
                 }
-                if (A::drop(p)) {   // what was dropped has no gradient, whatever it is multiplied by
+                if (A::drop(p)) {
                     keep_or_zero<N>(p.rule, rnd[k], z);
                     keep_or_zero<N>(p.rule, rnd[k], d);
                 }
@@ -168,7 +174,8 @@ __device__ __forceinline__ void leave_document(const ResidualParams &p, const Do
             w1(k, w);
 #pragma unroll
             for (int i = 0; i < E / 2; ++i) {
-                acc.post[k][i] = fma2(z[i], g[i], acc.post[k][i]);
+                const float2 sums = both(z[i]), gates = both(g[i]);   // no sum, no part: an infinite gate of dropped columns
+                acc.post[k][i] = fma2(z[i], pair_of(sums.x == 0.0f ? 0.0f : gates.x, sums.y == 0.0f ? 0.0f : gates.y), acc.post[k][i]);
                 z[i] = mul2(z[i], w[i]);
             }
         }
