@@ -15,6 +15,7 @@
 #include "token_rows.cuh"
 
 #include <cooperative_groups.h>
+#include <math_constants.h>
 
 #include <cstring>
 
@@ -39,7 +40,7 @@ __device__ __forceinline__ void exact_difference(float a, float b, float &d, flo
     if (!(fabsf(rest) < 3.0e38f)) rest = 0.0f;   // infinities and NaN are in d
 }
 
-// exp(x) - 1 - x
+// exp(x) - 1 - x; infinite at both infinities
 __device__ __forceinline__ float exp_less_line(float x)
 {
     if (fabsf(x) < 0.5f) {
@@ -51,7 +52,8 @@ __device__ __forceinline__ float exp_less_line(float x)
         s = __fmaf_rn(x, s, 0.5f);
         return __fmul_rn(__fmul_rn(x, x), s);
     }
-    return __fsub_rn(expm1f(x), x);
+    const float y = expm1f(x);
+    return y == CUDART_INF_F ? y : __fsub_rn(y, x);
 }
 
 // A sum of any number of terms, with what its roundings left out.

@@ -1,0 +1,34 @@
+"""The clipped policy loss where a term is infinite, or beyond binary32, and what it is multiplied by is 0."""
+import pytest
+import torch
+
+from test_gpu_policy_loss import Case
+from token_rows_ref import Batch
+
+pytestmark = pytest.mark.gpu
+
+# documents of a warp, of a CTA, and of a cluster, with gradients in registers and without
+LENS = [5, 90, 1, 0, 777, 4000, 9000, 17000]
+
+
+@pytest.mark.parametrize("lens", [LENS[:5], LENS])
+@pytest.mark.parametrize("side", ["logp", "ref"])
+def test_infinite_kl(cpt, cuda_device, lens, side):
+    """A token that the policy or the reference gives no weight at all (a logarithm of -inf): the KL term and the loss are
+    infinite. The gradient 1 - exp(e) is -inf at e = inf and 1 at -inf."""
+    b = Batch(cpt, 3, 2, lens, 1)
+    c = Case(cpt, b, weights=False)
+    first = torch.tensor([sum(lens[:d]) for d in range(b.n) if lens[d]], device="cuda")
+    c.mask[first] = True
+    _, want = [t.clone() for t in c.run()]
+    (c.logp if side == "logp" else c.ref)[first] = float("-inf")
+    terms, dlogp = c.run()
+    some = torch.tensor(lens, device="cuda") > 0
+    assert (terms[some, :2] == float("inf")).all() and (terms[~some] == 0).all()
+    others = torch.ones(b.T, dtype=torch.bool, device="cuda")
+    others[first] = False
+    assert torch.equal(dlogp[others], want[others])
+    if side == "logp":
+        assert (dlogp[first] == float("-inf")).all()
+    else:
+        assert torch.isfinite(dlogp[first]).all()
