@@ -40,8 +40,8 @@ __device__ __forceinline__ void exact_difference(float a, float b, float &d, flo
     if (!(fabsf(rest) < 3.0e38f)) rest = 0.0f;   // infinities and NaN are in d
 }
 
-// exp(x) - 1 - x; infinite at both infinities
-__device__ __forceinline__ float exp_less_line(float x)
+// exp(x) - 1 - x from y = exp(x) - 1; infinite at both infinities
+__device__ __forceinline__ float exp_less_line(float x, float y)
 {
     if (fabsf(x) < 0.5f) {
         float s = __fmaf_rn(x, 1.0f / 40320, 1.0f / 5040);
@@ -52,7 +52,6 @@ __device__ __forceinline__ float exp_less_line(float x)
         s = __fmaf_rn(x, s, 0.5f);
         return __fmul_rn(__fmul_rn(x, x), s);
     }
-    const float y = expm1f(x);
     return y == CUDART_INF_F ? y : __fsub_rn(y, x);
 }
 
@@ -108,16 +107,17 @@ __device__ __forceinline__ void add_tokens(const PolicyParams &p, int64_t t, int
         ++f.count;
         g[k] = held ? 0.0f : ar;
         if (p.ref != nullptr) {
-            const float e = __fsub_rn(ref[k], logp[k]);
-            f.kl.add(exp_less_line(e));
-            g[k] = __fmaf_rn(-p.kl, expm1f(e), g[k]);
+            const float e = __fsub_rn(ref[k], logp[k]), y = expm1f(e);
+            f.kl.add(exp_less_line(e, y));
+            g[k] = __fmaf_rn(-p.kl, p.kl != 0.0f ? y : 0.0f, g[k]);   // with 0 the KL is only reported, infinite or not
         }
     }
 }
 
 __device__ __forceinline__ float4 terms_of(const PolicyParams &p, float loss, float kl, float held, float n, float share)
 {
-    return make_float4(__fmul_rn(__fmaf_rn(p.kl, kl, loss), share), __fmul_rn(kl, share), __fmul_rn(held, share), n);
+    const float all = p.kl != 0.0f ? __fmaf_rn(p.kl, kl, loss) : loss;
+    return make_float4(__fmul_rn(all, share), __fmul_rn(kl, share), __fmul_rn(held, share), n);
 }
 
 // A cluster of S CTAs takes p.docs neighbouring documents: the short ones a warp each, then the others one after the

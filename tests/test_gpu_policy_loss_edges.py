@@ -32,3 +32,25 @@ def test_infinite_kl(cpt, cuda_device, lens, side):
         assert (dlogp[first] == float("-inf")).all()
     else:
         assert torch.isfinite(dlogp[first]).all()
+
+
+@pytest.mark.parametrize("gap", [100.0, -1e30, float("inf"), float("nan")])
+@pytest.mark.parametrize("lens", [LENS[:5], LENS])
+def test_a_kl_that_is_only_reported(cpt, cuda_device, lens, gap):
+    """With kl_coef 0 the loss and its gradient are those without a reference, however large the KL."""
+    b = Batch(cpt, 3, 2, lens, 1)
+    c = Case(cpt, b, kl=0.0)
+    first = torch.tensor([sum(lens[:d]) for d in range(b.n) if lens[d]], device="cuda")
+    c.mask[first] = True
+    c.ref[first] = c.logp[first] + gap
+    terms, dlogp = c.run()
+    plain, want = c.run(logp_ref=None)
+    assert torch.isfinite(want).all() and torch.equal(dlogp, want)
+    assert torch.equal(terms[:, [0, 2, 3]], plain[:, [0, 2, 3]])
+    some = torch.tensor(lens, device="cuda") > 0
+    kl = terms[some, 1]
+    if gap == -1e30:
+        assert (kl > 1e25).all() and torch.isfinite(kl).all()     # exp(e) - e - 1 is -e
+    else:
+        assert torch.isnan(kl).all() if gap != gap else (kl == float("inf")).all()
+    assert (terms[~some] == 0).all()
