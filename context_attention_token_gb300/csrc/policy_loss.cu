@@ -100,7 +100,7 @@ __device__ __forceinline__ void add_tokens(const PolicyParams &p, int64_t t, int
         const bool above = __fadd_rn(__fsub_rn(u, p.high_hi), __fsub_rn(rest, p.high_lo)) > 0.0f;
         const bool below = __fadd_rn(__fsub_rn(u, p.low_hi), __fsub_rn(rest, p.low_lo)) < 0.0f;
         const bool held = (above && A > 0.0f) || (below && A < 0.0f);
-        const float r = expf(u);
+        const float r = expf(A == 0.0f && u > 0.0f ? 0.0f : u);   // of no advantage, not 0 times a ratio beyond binary32
         const float ar = __fmul_rn(-A, __fmul_rn(r, __fadd_rn(1.0f, rest)));
         f.loss.add(held ? __fmul_rn(-A, above ? p.above : p.below) : ar);
         f.held += held;

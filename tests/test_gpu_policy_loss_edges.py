@@ -54,3 +54,19 @@ def test_a_kl_that_is_only_reported(cpt, cuda_device, lens, gap):
     else:
         assert torch.isnan(kl).all() if gap != gap else (kl == float("inf")).all()
     assert (terms[~some] == 0).all()
+
+
+@pytest.mark.parametrize("gap", [100.0, 1e30, float("inf")])
+@pytest.mark.parametrize("lens", [LENS[:5], LENS])
+@pytest.mark.parametrize("ref", [False, True])
+def test_no_advantage(cpt, cuda_device, lens, gap, ref):
+    """An advantage of 0 leaves nothing of a ratio, however large."""
+    b = Batch(cpt, 3, 2, lens, 1)
+    c = Case(cpt, b, ref=ref, mask=False)
+    c.adv[:] = 0.0
+    c.logp = torch.where(torch.arange(b.T, device="cuda") % 3 == 0, -1.0, c.logp)
+    c.ref = c.logp.clone() if ref else None        # no KL either
+    c.old = torch.where(torch.arange(b.T, device="cuda") % 3 == 0, c.logp - gap, c.old)
+    terms, dlogp = c.run()
+    assert (terms[:, :3] == 0).all() and (dlogp == 0).all()
+    assert torch.equal(terms[:, 3], torch.tensor(lens, device="cuda", dtype=torch.float32))
