@@ -114,6 +114,13 @@ __device__ __forceinline__ void add_tokens(const PolicyParams &p, int64_t t, int
     }
 }
 
+// A token's gradient times its document's weight. A gradient of 0 (a masked or held token) stays 0, and a weight of 0 leaves nothing
+// of an infinite one.
+__device__ __forceinline__ float weighted(float g, float weight)
+{
+    return g == 0.0f || (weight == 0.0f && fabsf(g) == CUDART_INF_F) ? 0.0f : __fmul_rn(g, weight);
+}
+
 __device__ __forceinline__ float4 terms_of(const PolicyParams &p, float loss, float kl, float held, float n, float share)
 {
     const float all = p.kl != 0.0f ? __fmaf_rn(p.kl, kl, loss) : loss;
@@ -147,7 +154,7 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
         const float share = __fdiv_rn(1.0f, fmaxf(v[3], 1.0f)), weight = __fmul_rn(own, share);
 #pragma unroll
         for (int k = 0; k < kWarpTokens / 32; ++k)
-            if (lo + lane + k * 32 < hi) p.dlogp[lo + lane + k * 32] = __fmul_rn(g[k], weight);
+            if (lo + lane + k * 32 < hi) p.dlogp[lo + lane + k * 32] = weighted(g[k], weight);
         if (lane == 0) p.terms[d] = terms_of(p, v[0], v[1], v[2], v[3], share);
     }
 
@@ -195,10 +202,10 @@ __global__ void __launch_bounds__(kThreads) policy_loss_kernel(const __grid_cons
         if (held_back) {
 #pragma unroll
             for (int k = 0; k < kTokens; ++k)
-                if (t + k * step < hi) p.dlogp[t + k * step] = __fmul_rn(g[k], weight);
+                if (t + k * step < hi) p.dlogp[t + k * step] = weighted(g[k], weight);
         } else {
 #pragma unroll 4
-            for (int64_t at = t; at < hi; at += step) p.dlogp[at] = __fmul_rn(p.dlogp[at], weight);
+            for (int64_t at = t; at < hi; at += step) p.dlogp[at] = weighted(p.dlogp[at], weight);
         }
         if (rank == 0 && threadIdx.x == 0) p.terms[d] = terms_of(p, v[0], v[1], v[2], n, share);
     }

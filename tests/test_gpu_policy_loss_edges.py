@@ -70,3 +70,32 @@ def test_no_advantage(cpt, cuda_device, lens, gap, ref):
     terms, dlogp = c.run()
     assert (terms[:, :3] == 0).all() and (dlogp == 0).all()
     assert torch.equal(terms[:, 3], torch.tensor(lens, device="cuda", dtype=torch.float32))
+
+
+@pytest.mark.parametrize("lens", [LENS[:5], LENS])
+def test_weights_of_nothing(cpt, cuda_device, lens):
+    """A document without a token that counts may have any advantage and weight; one of weight 0 has no gradient, though its
+    loss is infinite. Tokens that do not count have none, whatever their document's weight."""
+    b = Batch(cpt, 3, 2, lens, 1)
+    c = Case(cpt, b)
+    doc = b.doc
+    nothing, out = doc % 3 == 0, doc % 3 == 1
+    c.mask &= ~nothing
+    keep, (_, want) = c.weights.clone(), [t.clone() for t in c.run()]
+    docs = torch.arange(b.n, device="cuda")
+    for value in (float("nan"), float("inf")):
+        c.adv[docs % 3 == 0] = value
+        c.weights[docs % 3 == 0] = value
+        terms, dlogp = c.run()
+        assert (terms[docs % 3 == 0] == 0).all() and torch.equal(dlogp, want)
+    c.weights = torch.where(docs % 3 == 1, 0.0, keep)
+    c.adv[docs % 3 == 1] = -1.0
+    first = torch.tensor([sum(lens[:d]) for d in range(b.n) if lens[d] and d % 3 == 1], device="cuda")
+    c.mask[first] = True
+    c.old[first] = c.logp[first] - 100.0
+    terms, dlogp = c.run()
+    assert (terms[doc[first], 0] == float("inf")).all()
+    assert (dlogp[out] == 0).all() and torch.equal(dlogp[~out], want[~out])
+    c.weights[docs % 3 == 1] = float("inf")
+    _, dlogp = c.run()
+    assert (dlogp[~c.mask] == 0).all()
