@@ -1630,8 +1630,8 @@ cpt_status check_logits(int64_t vocab, int64_t vocab_padded, cpt_dtype dtype, cp
     if ((st = check_row(vocab_padded, dtype, dtype, units))) return st;
     if (vocab < 1 || vocab > vocab_padded)
         return fail(CPT_ERR_INVALID_ARG, "vocab %lld outside 1..%lld", (long long)vocab, (long long)vocab_padded);
-    if (!std::isfinite(scale) || !(scale > 0.0f))
-        return fail(CPT_ERR_INVALID_ARG, "scale is not a finite positive number");
+    // (above it, scale / log 2 is infinite in binary32, and 0 times that no weight of 1)
+    if (!(scale > 0.0f && scale <= 2e38f)) return fail(CPT_ERR_INVALID_ARG, "scale is not a positive number of at most 2e38");
     return CPT_OK;
 }
 

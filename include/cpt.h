@@ -925,7 +925,7 @@ CPT_API cpt_status cpt_residual_norm_backward(const cpt_plan *plan, const void *
  *           from vocab on are not used.
  *  targets  device int32[T], raw global order. A target outside 0..vocab-1 is none:
  *           the row is not read and logp and stats are 0.
- *  scale    finite, positive: one over the temperature.
+ *  scale    positive, at most 2e38: one over the temperature.
  *  logp     device float32[T], raw global order.
  *  stats    device float32[T][2], 8-byte aligned: m and l, for the gradient. The
  *           logarithm of the row's sum is scale * m + l.
