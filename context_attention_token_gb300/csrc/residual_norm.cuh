@@ -342,7 +342,8 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensor
     if (first)
         for (int c = 0; c < ring.stages; ++c) issue();
     for (Int i = 0; i < count; ++i) {
-        const bool come = mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+        // a warp's lanes go on together, whichever of them saw the copy come: full-warp shuffles and votes follow
+        const bool come = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&ring.full[ring.slot], ring.phase));
         if (!come) sum.ask = true;
         work(i, come ? ring.index[ring.slot] : kUnknown, [&]() {
             if (several && first && i > 0) issue();   // into the place of the row before
