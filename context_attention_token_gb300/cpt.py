@@ -828,16 +828,32 @@ def _floats(t, count: int, what: str) -> int:
     return _ptr(t)
 
 
+def _row_weights(t, width: int, what: str) -> int:
+    """The pointer of an optional row of float32 weights, one for every element of the rows."""
+    if t is not None and t.numel() != width:
+        raise ValueError(f"{what} must hold {width} float32 values, not {t.numel()}")
+    return _floats(t, width, what)
+
+
+def _check_gate(plan: Plan, t, width: int, order: int, per_document: bool, what: str):
+    """A gate or its gradient: rows like h's, or one for every document (flat, too)."""
+    rows = plan.n_docs if per_document else _row_count(plan, order)
+    if t.numel() == rows * width and (t.dim() == 1 or (per_document and t.shape[0] == rows)):
+        return
+    if per_document or _row_width(plan, order, t) != width:
+        raise ValueError(f"{what} must hold {rows} rows of {width} elements, not {tuple(t.shape)}")
+
+
 def _residual_options(plan: Plan, width: int, dtype, order: int, post_weight, gate, gate_per_document, scale, p, rng,
                       site, pre_weight, eps):
     gate_ptr, kind = 0, CPT_GATE_NONE
     if gate is not None:
-        rows = plan.n_docs if gate_per_document else _row_count(plan, order)
-        if gate.dtype != dtype or gate.numel() < rows * width:
-            raise ValueError(f"gate must hold {rows} rows of {width} elements of the tensors' dtype")
+        if gate.dtype != dtype:
+            raise ValueError("gate must be of the tensors' dtype")
+        _check_gate(plan, gate, width, order, gate_per_document, "gate")
         gate_ptr, kind = _there(gate), CPT_GATE_DOCUMENT if gate_per_document else CPT_GATE_TOKEN
-    return _Residual(_floats(post_weight, width, "post_weight"), _floats(pre_weight, width, "pre_weight"), gate_ptr, kind,
-                     scale, eps, p, _rng_ptr(rng, p), site & 0xFFFFFFFF)
+    return _Residual(_row_weights(post_weight, width, "post_weight"), _row_weights(pre_weight, width, "pre_weight"), gate_ptr,
+                     kind, scale, eps, p, _rng_ptr(rng, p), site & 0xFFFFFFFF)
 
 
 def cpt_residual_norm(plan: Plan, x: torch.Tensor, h, y, n, *, post_weight=None, gate=None,
@@ -867,11 +883,12 @@ def cpt_residual_norm_backward(plan: Plan, h, y, dy, dn, dx: torch.Tensor, dh, *
     width = _rows_of(plan, order, dx, (h, y, dy, dn, dh), "h, y, dy, dn, dx and dh")
     o = _residual_options(plan, width, dx.dtype, order, post_weight, gate, gate_per_document, scale, p, rng, site,
                           pre_weight, eps)
-    dpost, dpre = _floats(dpost_weight, width, "dpost_weight"), _floats(dpre_weight, width, "dpre_weight")
+    dpost, dpre = _row_weights(dpost_weight, width, "dpost_weight"), _row_weights(dpre_weight, width, "dpre_weight")
     if dgate is not None:
-        rows, kind = (plan.n_docs, torch.float32) if gate_per_document else (_row_count(plan, order), dx.dtype)
-        if dgate.dtype != kind or dgate.numel() < rows * width:
-            raise ValueError(f"dgate must hold {rows} rows of {width} values of {kind}")
+        kind = torch.float32 if gate_per_document else dx.dtype
+        if dgate.dtype != kind:
+            raise ValueError(f"dgate must be of {kind}")
+        _check_gate(plan, dgate, width, order, gate_per_document, "dgate")
     if workspace is None:
         if stream is not None:
             raise ValueError("give a workspace with a stream: torch allocates on its current stream only")
@@ -883,12 +900,24 @@ def cpt_residual_norm_backward(plan: Plan, h, y, dy, dn, dx: torch.Tensor, dh, *
                                            _stream(stream)))
 
 
-def _logits_shape(plan: Plan, logits, vocab, order, targets, per_token):
+def _check_logits(t, rows: int, width: int, what: str):
+    """The rows and no others, or a longer table of rows."""
+    if t.dim() == 0 or t.shape[-1] != width or (t.numel() != rows * width and (t.dim() != 2 or t.shape[0] < rows)):
+        raise ValueError(f"{what} of shape {tuple(t.shape)} do not hold {rows} rows of {width}")
+
+
+def _check_columns(t, columns: int, what: str):
+    """A buffer of so many values a row, flat or of that shape."""
+    if t.dim() > 1 and t.shape[-1] != columns:
+        raise ValueError(f"{what} must hold {columns} values a row, not {tuple(t.shape)}")
+
+
+def _logits_shape(plan: Plan, logits, vocab, order, targets, stats, per_token):
     """(vocab, vocab_padded) of rows of logits, every buffer large enough."""
     rows, T = _row_count(plan, order), plan.total_tokens
     width = logits.shape[-1] if logits.dim() > 0 else 0
-    if logits.numel() < rows * width:
-        raise ValueError(f"the logits hold {logits.numel()} elements but the call touches {rows} rows of {width}")
+    _check_logits(logits, rows, width, "logits")
+    _check_columns(stats, 2, "stats")
     if targets.dtype != torch.int32 or targets.numel() < T:
         raise ValueError(f"targets must hold {T} int32 values")
     for t, count, what in per_token:
@@ -906,7 +935,7 @@ def cpt_token_logprob(plan: Plan, logits: torch.Tensor, targets: torch.Tensor, l
                       order: int = CPT_ORDER_LOCAL, stream=None):
     """logp[g] = log of the probability that token g's logits give to targets[g] (int32, global order; negative:
     none), over the first `vocab` columns (all, if None); stats [T, 2] for the gradient."""
-    v, width = _logits_shape(plan, logits, vocab, order, targets, ((logp, 1, "logp"), (stats, 2, "stats")))
+    v, width = _logits_shape(plan, logits, vocab, order, targets, stats, ((logp, 1, "logp"), (stats, 2, "stats")))
     _check(_lib.cpt_token_logprob(plan.handle, _ptr(logits), _ptr(targets), _ptr(logp), _ptr(stats), v, width,
                                   _dtype_code(logits), order, scale, _stream(stream)))
 
@@ -915,9 +944,10 @@ def cpt_token_logprob_backward(plan: Plan, logits: torch.Tensor, targets: torch.
                                dlogp: torch.Tensor, dlogits: torch.Tensor, *, vocab: int | None = None,
                                scale: float = 1.0, order: int = CPT_ORDER_LOCAL, stream=None):
     """dlogits (may be logits) of cpt_token_logprob from the gradient of logp."""
-    v, width = _logits_shape(plan, logits, vocab, order, targets, ((stats, 2, "stats"), (dlogp, 1, "dlogp")))
-    if dlogits.dtype != logits.dtype or dlogits.numel() < _row_count(plan, order) * width:
+    v, width = _logits_shape(plan, logits, vocab, order, targets, stats, ((stats, 2, "stats"), (dlogp, 1, "dlogp")))
+    if dlogits.dtype != logits.dtype:
         raise ValueError("dlogits must be like logits")
+    _check_logits(dlogits, _row_count(plan, order), width, "dlogits")
     _check(_lib.cpt_token_logprob_backward(plan.handle, _ptr(logits), _ptr(targets), _ptr(stats), _ptr(dlogp),
                                            _ptr(dlogits), v, width, _dtype_code(logits), order, scale,
                                            _stream(stream)))
@@ -931,6 +961,7 @@ def cpt_policy_loss(plan: Plan, logp: torch.Tensor, logp_old: torch.Tensor, adva
     T, n = plan.total_tokens, plan.n_docs
     if mask is not None and (mask.dtype not in (torch.bool, torch.uint8) or mask.numel() < T):
         raise ValueError(f"mask must hold {T} values of bool or uint8")
+    _check_columns(terms, 4, "terms")
     _check(_lib.cpt_policy_loss(plan.handle, _floats(logp, T, "logp"), _floats(logp_old, T, "logp_old"),
                                 _floats(logp_ref, T, "logp_ref"), _ptr(mask), _floats(advantages, n, "advantages"),
                                 _floats(weights, n, "weights"), clip_low, clip_high, kl_coef,
