@@ -49,3 +49,14 @@ def cuda_device():
         pytest.fail("the gpu-marked tests need a CUDA device")
     torch.cuda.set_device(0)
     return torch.device("cuda", 0)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def no_wait_ran_out():
+    """After every file's tests: no wait inside a kernel has run out (tests that make one run out set the count back)."""
+    yield
+    binding, torch = sys.modules.get("context_attention_token_gb300.cpt"), sys.modules.get("torch")
+    if binding is None or torch is None or not torch.cuda.is_initialized():
+        return
+    torch.cuda.synchronize()
+    assert binding.cpt_kernel_wait_timeouts() == 0, "a wait inside a kernel ran out"
