@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kForwardThreads) residual_norm_long_kernel(con
     const int tensor = lane & 31;
     const uint8_t *base = tensor == 0 ? p.x : tensor == 1 && A::block(p.h != nullptr) ? p.h : p.gate;
     uint8_t *y = p.y, *n = p.n;
-    walk(ring, sum, count, p.tensors, row_bytes, p.stall, base, token_of, row_of, [&](int64_t i, int32_t token, auto after) {
+    walk<kApart>(ring, sum, count, p.tensors, row_bytes, p.stall, base, token_of, row_of, [&](int64_t i, int32_t token, auto after) {
         const bool real = token >= 0;
         const uint4 *data = ring.row() + lane;
         const int64_t at = (begin + i) * row_bytes + lane * 16;   // of this thread's first unit, in bytes

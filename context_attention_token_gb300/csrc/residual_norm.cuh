@@ -287,7 +287,7 @@ struct Ring {
     uint32_t phase = 0;
 
     // the current row of tensor 0
-    __device__ __forceinline__ const uint4 *row() const { return reinterpret_cast<const uint4 *>(smem + slot * stage_bytes); }
+    __device__ __forceinline__ uint4 *row() const { return reinterpret_cast<uint4 *>(smem + slot * stage_bytes); }
     // What no copy writes: the ends of the places, behind the rows.
     __device__ __forceinline__ void zero_ends(const Team &team, int tensors, uint32_t row_bytes)
     {
@@ -308,11 +308,19 @@ static __device__ unsigned int g_wait_timeouts;   // of this translation unit
 
 constexpr int32_t kUnknown = -2;   // a row's index for a thread whose wait has run out: it uses and stores nothing of the row
 
+// How a warp's lanes come to the same index, kUnknown where one lane's wait has run out, whatever the others saw. Needed where
+// `work` parts by the index around full-warp shuffles, as the gradient's does: a lane would wait for ever for one that went the
+// other way. The forward call's parts by it in stores only, and a vote costs the forward kernel that looks at its
+// parameters 3 to 5 %. The gradient's kernels of their own are best with a vote (131072 x 2048 bf16, both norms, dropout: 557 us, 581 with
+// the minimum), the shared one with the minimum, which is uniform (131072 x 2560 bf16, a post norm and dropout: 1188 us, 1423 with a vote).
+enum Together { kApart, kVote, kMinimum };
+
 // Runs `work(i, index, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
 // first barrier, where every thread is done with the row before; `sum` votes there whether a wait has run
-// out, and then nothing that depends on other threads' data may be stored. (Int: 64 bits forward, where 32 make the compiler's schedule 4 % slower; 32 in the gradient, which is short of
-// registers.) index_of(i) looks the i-th row up (-1: it is not read), row_of(i, index) is its place in this lane's tensor, `base`.
-template <class Int, class Sum, class Index, class RowOf, class Work>
+// out, and then nothing that depends on other threads' data may be stored. (Int: 64 bits forward, where 32 make the compiler's
+// schedule 4 % slower; 32 in the gradient, which is short of registers.) index_of(i) looks the i-th row up (-1: it is not read),
+// row_of(i, index) is its place in this lane's tensor, `base`.
+template <Together TOGETHER, class Int, class Sum, class Index, class RowOf, class Work>
 __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensors, uint32_t row_bytes, uint32_t stall,
                                      const uint8_t *base, Index index_of, RowOf row_of, Work work)
 {
@@ -342,10 +350,12 @@ __device__ __forceinline__ void walk(Ring &ring, Sum &sum, Int count, int tensor
     if (first)
         for (int c = 0; c < ring.stages; ++c) issue();
     for (Int i = 0; i < count; ++i) {
-        // a warp's lanes go on together, whichever of them saw the copy come: full-warp shuffles and votes follow
-        const bool come = __all_sync(0xFFFFFFFFu, mbar_wait_bounded(&ring.full[ring.slot], ring.phase));
+        bool come = mbar_wait_bounded(&ring.full[ring.slot], ring.phase);
+        if (TOGETHER == kVote) come = __all_sync(0xFFFFFFFFu, come);
         if (!come) sum.ask = true;
-        work(i, come ? ring.index[ring.slot] : kUnknown, [&]() {
+        int32_t at = come ? ring.index[ring.slot] : kUnknown;
+        if (TOGETHER == kMinimum) at = __reduce_min_sync(0xFFFFFFFFu, at);
+        work(i, at, [&]() {
             if (several && first && i > 0) issue();   // into the place of the row before
         });
         if (!several) {

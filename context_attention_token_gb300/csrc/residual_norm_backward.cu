@@ -379,7 +379,7 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         return row >= 0 && in_bounds(row < p.rows) ? row : -1;
     };
     auto row_of = [&](int32_t, int32_t row) { return static_cast<int64_t>(row); };
-    walk(ring, sum, count, p.tensors, row_bytes, p.stall, base, index_of, row_of, [&](int32_t i, int32_t row, auto after) {
+    walk<F >= 0 ? kVote : kMinimum>(ring, sum, count, p.tensors, row_bytes, p.stall, base, index_of, row_of, [&](int32_t i, int32_t row, auto after) {
         if (row < 0) {   // an index that a check refused, or a wait that has run out
             sum.stop = team.any(sum.ask);
             after();

@@ -25,7 +25,7 @@ PROGRAM = r"""
 constexpr int kThreads = 64, kCount = 12;
 struct Warp {
     std::barrier<> meet{32};
-    bool all = true, votes[32];
+    int32_t values[32];
 };
 struct Place { uint32_t a, b, c, d; };
 typedef Place uint4;
@@ -43,12 +43,20 @@ static void __syncwarp() { warps[self / 32].meet.arrive_and_wait(); }
 static bool __all_sync(uint32_t, bool v)
 {
     Warp &w = warps[self / 32];
-    w.votes[self % 32] = v;
+    w.values[self % 32] = v;
     w.meet.arrive_and_wait();
-    bool all = true;
-    for (bool x : w.votes) all = all && x;
+    for (int32_t x : w.values) v = v && x;
     w.meet.arrive_and_wait();
-    return all;
+    return v;
+}
+static int32_t __reduce_min_sync(uint32_t, int32_t v)
+{
+    Warp &w = warps[self / 32];
+    w.values[self % 32] = v;
+    w.meet.arrive_and_wait();
+    for (int32_t x : w.values) v = x < v ? x : v;
+    w.meet.arrive_and_wait();
+    return v;
 }
 static unsigned atomicAdd(unsigned *p, unsigned v) { return __atomic_fetch_add(p, v, __ATOMIC_SEQ_CST); }
 
@@ -106,7 +114,7 @@ int main(int argc, char **argv)
             self = t;
             Sum sum = {Team{t, kThreads, 1}};
             Ring ring = {smem, full, index, stages, 16, 16};
-            walk(ring, sum, kCount, 1, 16u, 0u, base, [](int i) { return i < kCount ? i : -1; }, [](int i, int32_t) { return i; },
+            walk<TOGETHER>(ring, sum, kCount, 1, 16u, 0u, base, [](int i) { return i < kCount ? i : -1; }, [](int i, int32_t) { return i; },
                  [&](int i, int32_t row, auto after) {
                      seen[t][i] = row;
                      sum.stop = sum.team.any(sum.ask);
@@ -131,8 +139,8 @@ int main(int argc, char **argv)
 """
 
 
-@pytest.fixture(scope="module")
-def program():
+@pytest.fixture(scope="module", params=["kVote", "kMinimum"])
+def program(request):
     if shutil.which("g++") is None:
         pytest.skip("needs g++")
     with open(os.path.join(ROOT, "context_attention_token_gb300", "csrc", "residual_norm.cuh")) as f:
@@ -144,7 +152,7 @@ def program():
     src, exe = os.path.join(work, "walk.cpp"), os.path.join(work, "walk")
     with open(src, "w") as f:
         f.write(PROGRAM.replace("//RING", ring + walk))
-    subprocess.run(["g++", "-std=c++20", "-O1", "-pthread", src, "-o", exe], check=True)
+    subprocess.run(["g++", "-std=c++20", "-O1", "-pthread", f"-DTOGETHER={request.param}", src, "-o", exe], check=True)
     return exe
 
 
