@@ -21,18 +21,19 @@ struct Sums {
     F2 post[U][Unit<BF16>::E / 2], pre[U][Unit<BF16>::E / 2], gate[U][Unit<BF16>::E / 2];
 };
 
-// One token of the gradient; dy to gate give the data of a unit of its row (0 past the row's end). `enter` is called before
-// the gate is asked for. Where `real` is false there is no token: its data are zeros, and it adds nothing to any sum (a
-// statistic of zeros, which is infinite without an eps, is not used).
-template <bool BF16, int U, int F, class W1, class W2, class DY, class DN, class Y, class H, class Enter, class G, class Bits,
-          class Sum, class PutX, class PutH, class PutG>
+// One token of the gradient; dy to gate give the data of a unit of its row (0 past the row's end), set_h changes that of h.
+// `enter` is called before the gate is asked for. Where `real` is false there is no token: its data are zeros, and it adds
+// nothing to any sum (a statistic of zeros, which is infinite without an eps, is not used).
+template <bool LONG, bool BF16, int U, int F, class W1, class W2, class DY, class DN, class Y, class H, class SetH, class Enter, class G,
+          class Bits, class Sum, class PutX, class PutH, class PutG>
 __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real, const Has<U> &has, W1 w1, W2 w2,
-                                             Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, Enter enter, G gate, Bits bits, Sum sum, PutX put_x,
-                                             PutH put_h, PutG put_gate)
+                                             Sums<BF16, U> &acc, DY dy, DN dn, Y y, H h, SetH set_h, Enter enter, G gate, Bits bits,
+                                             Sum sum, PutX put_x, PutH put_h, PutG put_gate)
 {
     typedef UnitPairs<BF16> V;
     typedef Asked<F> A;
     constexpr int N = V::N;
+    constexpr bool IN_PLACE = LONG && F >= 0 && (F & 1);
     const bool post = A::post(p), pre = A::pre(p);
     uint32_t rnd[U][N];
     F2 q[3] = {twice(0.0f), twice(0.0f), twice(0.0f)};   // y^2, dn w2 y, h^2
@@ -62,6 +63,18 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
     if ((pre || post) && sum(s)) return;
     if (A::gate(p) == kGateDocument) enter();
     const float r2 = pre && real ? rsqrt_mean(p, s[0]) : 0.0f, r1 = !post ? 1.0f : real ? rsqrt_mean(p, s[2]) : 0.0f;
+    // What was dropped has no gradient and adds nothing to a sum, whatever it is multiplied by: h is 0 there. Behind a norm only a row
+    // whose squares have no finite sum holds what 0 would not take; such a row is changed where it stands, if it stands in
+    // shared memory.
+    if (IN_PLACE && A::drop(p) && !(s[2] < CUDART_INF_F)) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            F2 a[N];
+            V::unpack(h(k), a);
+            keep_or_zero<N>(p.rule, rnd[k], a);
+            set_h(k, V::pack(a));
+        }
+    }
     // dY = dy + r2 dn w2 - y r2^2 mean(dn w2 yn), yn = y r2
     const F2 back2 = twice(pre ? -__fmul_rn(__fmul_rn(r2, r2), __fmul_rn(__fmul_rn(s[1], r2), p.per_column)) : 0.0f);
     F2 e[U][N], t = twice(0.0f);
@@ -93,9 +106,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
 #pragma unroll
                 for (int i = 0; i < N; ++i) hn[i] = mul2(hn[i], twice(r1));
             }
-            // What was dropped has no gradient and adds nothing to a sum, whatever it is multiplied by. (A row whose squares have a
-            // finite sum holds nothing that 0 would not take.)
-            if (A::drop(p) && (!post || !(s[2] < CUDART_INF_F))) keep_or_zero<N>(p.rule, rnd[k], hn);
+            if (!IN_PLACE && A::drop(p)) keep_or_zero<N>(p.rule, rnd[k], hn);
         }
         const bool by_document = A::gate(p) == kGateDocument;
         if (A::gate(p) != 0) {
@@ -275,9 +286,10 @@ __global__ void __launch_bounds__(kShortThreads, short_ctas(U, F)) residual_norm
                 if (has.at[k]) r.t[4][k] = reinterpret_cast<const uint4 *>(p.gate)[static_cast<int64_t>(doc.at) * p.units + lane + k * p.group];
         }
         const int64_t at = r.row * p.units + lane;
-        backward_row<BF16, U, F>(
+        backward_row<false, BF16, U, F>(
             p, real, has, HeldWeights<BF16, U>{w1}, HeldWeights<BF16, U>{w2}, acc, [&](int k) { return r.t[0][k]; }, [&](int k) { return r.t[1][k]; },
-            [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; }, []() {},
+            [&](int k) { return r.t[2][k]; }, [&](int k) { return r.t[3][k]; },
+            [](int, uint4) {}, []() {},
             [&](int k) { return r.t[4][k]; },
             [&](uint32_t(&bits)[U][E / 2]) { short_bits<BF16, U>(p, key, static_cast<uint32_t>(t), lane, bits); },
             [&](auto &v) {
@@ -387,12 +399,16 @@ __global__ void __launch_bounds__(kBackwardThreads) residual_norm_backward_long_
         }
         const int32_t t = begin + i;
         const int64_t at = static_cast<int64_t>(row) * row_bytes + lane * 16;
-        const uint4 *data = ring.row() + lane;
+        uint4 *data = ring.row() + lane;   // a thread's units are its own
         bool waiting = true;
-        backward_row<BF16, U, F>(
+        backward_row<true, BF16, U, F>(
             p, true, has, w1, w2, acc, [&](int k) { return p.x != nullptr ? data[k * p.group] : make_uint4(0, 0, 0, 0); },
             [&](int k) { return data[at_dn + k * p.group]; }, [&](int k) { return data[at_y + k * p.group]; },
             [&](int k) { return data[at_h + k * p.group]; },
+            [&](int k, uint4 v) {
+                data[at_h + k * p.group] = v;
+                fence_proxy_async_smem();   // a copy writes here next
+            },
             [&]() {
                 if (t < doc.hi) return;
                 if (doc.hi >= 0) leave_document<BF16, U, F>(p, doc, which, begin, end, has, lane, w1, acc);
