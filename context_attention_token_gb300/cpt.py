@@ -963,7 +963,7 @@ def cpt_policy_loss(plan: Plan, logp: torch.Tensor, logp_old: torch.Tensor, adva
         raise ValueError(f"mask must hold {T} values of bool or uint8")
     _check_columns(terms, 4, "terms")
     _check(_lib.cpt_policy_loss(plan.handle, _floats(logp, T, "logp"), _floats(logp_old, T, "logp_old"),
-                                _floats(logp_ref, T, "logp_ref"), _ptr(mask), _floats(advantages, n, "advantages"),
+                                _floats(logp_ref, T, "logp_ref") or _there(logp_ref), _ptr(mask), _floats(advantages, n, "advantages"),
                                 _floats(weights, n, "weights"), clip_low, clip_high, kl_coef,
                                 _floats(terms, 4 * n, "terms"), _floats(dlogp, T, "dlogp"), _stream(stream)))
 

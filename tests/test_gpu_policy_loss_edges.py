@@ -99,3 +99,13 @@ def test_weights_of_nothing(cpt, cuda_device, lens):
     c.weights[docs % 3 == 1] = float("inf")
     _, dlogp = c.run()
     assert (dlogp[~c.mask] == 0).all()
+
+
+@pytest.mark.parametrize("kl", [0.0, 0.1])
+@pytest.mark.parametrize("lens", [[], [0], [0, 0, 0]])
+def test_empty_batches_with_everything(cpt, cuda_device, lens, kl):
+    """Documents without a token have a loss of 0, a reference and a mask given or not."""
+    b = Batch(cpt, 3, 2, lens, 1)
+    c = Case(cpt, b, kl=kl)
+    terms, dlogp = c.run()
+    assert (terms == 0).all() and dlogp.numel() == 0
