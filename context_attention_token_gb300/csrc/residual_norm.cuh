@@ -71,7 +71,9 @@ inline Shape shape_of(int units, int dtype, bool gradient, int tensors, bool by_
         return s;
     }
     const int eights = dtype == kBf16 ? units : (units + 1) / 2;   // groups of eight columns
-    const int wide = gradient || eights <= 128 ? 2 : eights <= 192 ? 3 : 5;   // of a thread
+    // (of a thread; 2560 columns are 64 threads of 5 exactly, 2048 and 4096 leave a fifth of them idle: 131072 x 4096 bf16 takes 1.35 times
+    // its bytes' time, 2048 columns 1.12, 2560 1.10)
+    const int wide = gradient || eights <= 128 ? 2 : eights <= 192 ? 3 : 5;
     s.per_thread = dtype == kBf16 ? wide : 2 * wide;
     s.group = ((eights + wide - 1) / wide + 31) / 32 * 32;
     // one CTA an SM, of as many teams as registers, barriers and shared memory allow (a row each at least)
@@ -413,10 +415,12 @@ inline int asked(const ResidualParams &p, bool block)
     return block ? (p.post != nullptr) + 2 * (p.pre != nullptr) + 4 * (p.rule.rng != nullptr) + 8 * p.gate_kind : 34;
 }
 
-// The kernel of its own for what is asked most: both norms, with any gate (long rows only); the pre norm alone, without one;
-// each with and without dropout; the first norm of a model. The others share one that looks at its parameters.
-// (262144 x 2560 bf16 with both norms and dropout: 866 us with its own kernel, 1183 with the shared one; gradient of 131071 x 2560
-// bf16, a document's gate too, 946 and 1865; of 20011 x 1132 float32 with a token's gate 139 and 221.)
+// Kernels of their own for both norms, with any gate (long rows only); for the pre norm alone, without one; each with and
+// without dropout; for the first norm of a model. The others (a gate without a post norm, no pre norm, short rows with a
+// gate) share one that looks at its parameters and spills.
+// (262144 x 2560 bf16 with both norms and dropout: 866 us with its own kernel, 1184 with the shared one; gradient of 131071 x 2560
+// bf16, a document's gate too, 915 and 1707; of 20011 x 1132 float32 with a token's gate 138 and 208. What has none: the pre norm
+// with a document's gate and dropout, 262144 x 2560 bf16, takes 1269 us where its bytes take 791, its gradient of 131072 rows 1239 for 593.)
 template <bool GATES, class Launch>
 cudaError_t with_asked(int f, Launch launch)
 {

@@ -179,7 +179,10 @@ constexpr int kRowUnroll = 8;
 constexpr int kShortUnroll = 4;
 constexpr int kMostSplit = 4;      // CTAs of a long row
 constexpr int kShortThreads = 256;
-constexpr int kShortUnits = 512;   // of rows that a part of a warp reads
+// Of rows that a part of a warp reads. No border that was measured: 8192 rows of 257 units take 18 us in parts of a warp, of
+// 513 units 47 (float32) and 66 (bf16) and of 1024 bf16 68 in CTAs most of whose loads are empty. From some 4000 units on
+// CTAs come within a fifth of HBM's rate.
+constexpr int kShortUnits = 512;
 
 // Long rows: p.split CTAs of a cluster a token, each a part of the row; their pairs are joined in the
 // first one's shared memory.
@@ -364,7 +367,8 @@ cudaError_t launch_token_logprob(LogprobParams p, int dtype, cudaStream_t stream
     }
     // few tokens: a row's columns over the CTAs of a cluster, two CTAs an SM at most (64 rows of 157184 bf16 take 14.7
     // us with one CTA a row, 10.2 with two, four or eight).
-    // 256 threads read 8191 such rows in 360 us, 512 in 381, 1024 in 501.
+    // 256 threads read 8191 such rows in 360 us, 512 in 381, 1024 in 501. (By all tokens, as those that have a target are
+    // not known here: 60 of 8192 take 31 us.)
     const int64_t room = 2 * static_cast<int64_t>(sm_count(-1));
     p.split = 1;
     while (p.split < kMostSplit && p.T * p.split * 2 <= room && units >= p.split * 2 * kRowThreads) p.split *= 2;

@@ -599,8 +599,8 @@ CPT_API cpt_status cpt_epoch_status(const cpt_epoch *ep, int32_t owner, void *st
  * (one wait of the attention kernel after more, with more than 2^25 tokens).
  * A wait that gives up is counted here, its warp (in the attention kernels its
  * CTA, in the residual norms the threads that share its rows) stops, and the
- * outputs it had not reached are left unwritten (a sum over tokens lacks
- * theirs). A non-zero
+ * outputs it had not reached are left unwritten (a sum over tokens is not
+ * valid). A non-zero
  * count means some output of an earlier call is not valid.
  *  count  host, receives the count.
  *  reset  non-zero: set the count back to zero after reading it.
@@ -829,7 +829,7 @@ CPT_API cpt_status cpt_attention_backward(const cpt_plan *plan, const void *q, c
  * With a probability p the element is kept when its bits are below
  * kept = floor((1 - p) * 2^16 + 1/2), and then multiplied by 2^16 / kept, so the
  * expectation is exact for the probability that 16 bits can hold. What is dropped is 0,
- * whatever it was, infinities and NaN included. */
+ * whatever it was, infinities and NaN included, and has no part in any gradient. */
 
 /* dst = dropout of src, row by row; also the gradient, with the same rng and site.
  *  src, dst   device [rows][row_elems], both in `order`. dst may be src; else
@@ -876,7 +876,8 @@ typedef struct cpt_residual {
  *  n      device, the next block's input; NULL exactly when pre_weight is.
  *  row_elems  at most CPT_RESIDUAL_MAX_ROW, a multiple of 16 bytes. x, h, y, n and
  *         gate are of one dtype.
- *  Arithmetic is binary32; y and n are rounded once each, n from the y before its
+ *  Arithmetic is binary32 (a row whose squares pass its range has a norm of 0; one of zeros, with
+ *  an eps of 0, is NaN); y and n are rounded once each, n from the y before its
  *  rounding. Padding rows of LOCAL are written as zeros and not used.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_UNSUPPORTED (row_elems), CPT_ERR_DEVICE,
  *  CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS, CPT_ERR_CUDA. */
@@ -964,6 +965,9 @@ CPT_API cpt_status cpt_token_logprob_backward(const cpt_plan *plan, const void *
  *  terms      device float32[n_docs][4]: L_d, the mean KL term, the share of tokens
  *             whose ratio is held by the clip, the number of tokens that count. 16-byte aligned.
  *  On which side of a border a ratio lies is settled without rounding logp - logp_old.
+ *  What binary32 cannot hold is infinite (an exp from 88.8 on; the KL of a logarithm of -inf is), but an
+ *  advantage, a kl_coef or a weight of 0 takes all of what it multiplies, and tokens without a mask have
+ *  a dlogp of 0 whatever their document's advantage and weight are.
  *  Sums are binary32 in a fixed order.
  *  Errors: CPT_ERR_INVALID_ARG, CPT_ERR_DEVICE, CPT_ERR_ALIGNMENT, CPT_ERR_ALIAS,
  *  CPT_ERR_CUDA. */
