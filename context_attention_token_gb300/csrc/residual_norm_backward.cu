@@ -154,6 +154,7 @@ __device__ __forceinline__ void backward_row(const ResidualParams &p, bool real,
     for (int k = 0; k < U; ++k) {
         F2 hn[N];
         V::unpack(h(k), hn);
+        if (!IN_PLACE && A::drop(p) && !(s[2] < CUDART_INF_F)) keep_or_zero<N>(p.rule, rnd[k], hn);
 #pragma unroll
         for (int i = 0; i < N; ++i) hn[i] = fma2(hn[i], back1, mul2(e[k][i], twice(r1)));
         put_h(k, has.at[k], V::pack(hn));

@@ -104,3 +104,19 @@ def test_gates_of_dropped_columns_behind_a_norm(cpt, cuda_device, C, dtype, valu
     c.gate = keep
     c.check_forward(y, n)
     c.check_backward(t)
+
+
+@pytest.mark.parametrize("C,dtype", DROPPED)
+@pytest.mark.parametrize("pre", [False, True])
+@pytest.mark.parametrize("gate", [0, 1, 2])
+def test_gradient_of_a_dropped_infinity(cpt, cuda_device, C, dtype, pre, gate):
+    """Behind a norm an infinite element of h makes its row's branch and its gradient 0, its own gradient too where it is dropped."""
+    b = Batch(cpt, 3, 2, [50, 31, 7], 1)
+    c = base.Case(cpt, b, C, dtype, post=True, pre=pre, gate=gate, p=0.5, seed=4)
+    h = b.pick(c.h)
+    at = c.drop() == 0
+    at[::2] = False
+    h[at] = -float("inf")
+    b.flat(c.h)[b.real] = h.to(dtype)
+    dh = b.flat(c.backward()["dh"])[b.real]
+    assert torch.isfinite(dh).all() and (dh[1::2] == 0).all() and (dh[::2] != 0).any(1).all()
