@@ -314,7 +314,8 @@ constexpr int32_t kUnknown = -2;   // a row's index for a thread whose wait has 
 // `work` parts by the index around full-warp shuffles, as the gradient's does: a lane would wait for ever for one that went the
 // other way. The forward call's parts by it in stores only, and a vote costs the forward kernel that looks at its
 // parameters 3 to 5 %. The gradient's kernels of their own are best with a vote (131072 x 2048 bf16, both norms, dropout: 557 us, 581 with
-// the minimum), the shared one with the minimum, which is uniform (131072 x 2560 bf16, a post norm and dropout: 1188 us, 1423 with a vote).
+// the minimum), the shared one with the minimum, which is uniform (131072 x 2560 bf16, a post norm and dropout: 1188 us, 1423 with a
+// vote; both before the dh of dropped infinities was looked after, which takes 50 more).
 enum Together { kApart, kVote, kMinimum };
 
 // Runs `work(i, index, after)` for i = 0 .. count - 1 with the i-th row's data in the ring. It has to call after() once behind its
